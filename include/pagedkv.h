@@ -56,7 +56,11 @@ typedef enum {
     PK_ERR_NOMEM = 9          /* host allocation failed                                 */
 } pk_status;
 
-typedef enum { PK_F32 = 0, PK_BF16 = 1 } pk_dtype;
+/* PK_E4M3 names an 8-bit cache (see "8-bit cache" below): the entry points
+ * with _e4m3 in their name take it, and the host helpers
+ * pk_paged_attention_resolve_partition, pk_paged_attention_workspace_size and
+ * pk_attention_plan; every other call refuses it (PK_ERR_UNSUPPORTED). */
+typedef enum { PK_F32 = 0, PK_BF16 = 1, PK_E4M3 = 2 } pk_dtype;
 
 /* Attention kernel choice. AUTO picks the tensor-core kernel for bf16 when it
  * is compiled for the shape and the CUDA-core kernel otherwise. */
@@ -70,7 +74,9 @@ enum {
     PK_DEVERR_PAIR = 3,        /* copy_blocks pair outside [0, num_blocks)             */
     PK_DEVERR_CONTEXT = 4,     /* context_lens entry < 1 or beyond the table / bound   */
     PK_DEVERR_TIMEOUT = 5,     /* a pipeline wait gave up (never expected)             */
-    PK_DEVERR_ORDER = 6        /* seq_order entry outside [0, num_seqs)                */
+    PK_DEVERR_ORDER = 6,       /* seq_order entry outside [0, num_seqs)                */
+    PK_DEVERR_POSITION = 7,    /* positions entry outside [0, max_position)            */
+    PK_DEVERR_OFFSETS = 8      /* q_offsets entry that is no range of the query rows   */
 };
 
 /* Geometry of one layer's KV pool. */
@@ -391,6 +397,151 @@ int32_t pk_paged_attention_resolve_partition(int32_t num_seqs, int32_t num_q_hea
 size_t pk_paged_attention_workspace_size(int32_t num_seqs, int32_t num_q_heads,
                                          int32_t max_context_len, int32_t partition_size,
                                          const pk_cache_desc *desc);
+
+/* ------------------------------------------------------------------------ */
+/* New tokens of a model's layer: norm, rotation and cache write            */
+/* ------------------------------------------------------------------------ */
+/* Per-head RMS norm of queries and keys, rotary positions and the cache write
+ * of new tokens in one pass. For token i and each query or key head x (d
+ * values):
+ *     y = x * (mean(x^2) + eps)^(-1/2) * weight         (skipped without weights)
+ *     (a, b) -> (a c - b s, b c + a s) for each pair of the first rotary_dim
+ * elements of y, with c, s the pair's cosine and sine at positions[i]; the
+ * other elements stay. Computed in fp32, each result rounded once. The queries
+ * go to q_out, the keys to k_out and, with a slot mapping, to their slots as in
+ * pk_reshape_and_cache, and the values to their slots unchanged.
+ *   q_out         [T, Hq, d]; k_out [T, Hk, d], optional when slots are given.
+ *                 q_out may be q, and k_out k, where the input is contiguous;
+ *                 other overlaps are not allowed.
+ *   q, k, v       token i's heads at i * q_stride (k_stride, v_stride) elements,
+ *                 [heads, d] contiguous: views of one packed projection serve.
+ *                 Strides in elements, multiples of 16 bytes.
+ *   q_weight, k_weight  [d], dtype of q; both or neither.
+ *   cos_sin       fp32 [max_position, rotary_dim]: rotary_dim / 2 cosines, then
+ *                 as many sines, per position.
+ *   positions     int64 [T]. One outside [0, max_position) is recorded
+ *                 (PK_DEVERR_POSITION) and its token is skipped.
+ *   rotary_dim    multiple of 16, 0 (no rotation; cos_sin and positions are not
+ *                 read) to d.
+ *   interleaved   0: pair j is (j, j + rotary_dim / 2); else (2j, 2j + 1).
+ *   slot_mapping  int64 [T], or NULL: no cache write (v, k_cache and v_cache are
+ *                 not used). Negative slots are skipped; out-of-range slots are
+ *                 skipped and recorded (PK_DEVERR_SLOT).
+ *   desc          dtype (PK_F32 or PK_BF16) of all but cos_sin; d a multiple of
+ *                 16, at most 256. */
+pk_status pk_qk_norm_rope_and_cache(
+    void *q_out, void *k_out, const void *q, const void *k, const void *v, int64_t q_stride,
+    int64_t k_stride, int64_t v_stride, const void *q_weight, const void *k_weight, float eps,
+    const float *cos_sin, const int64_t *positions, int32_t max_position, int32_t rotary_dim,
+    int32_t interleaved, const int64_t *slot_mapping, int32_t num_tokens, int32_t num_q_heads,
+    void *k_cache, void *v_cache, const pk_cache_desc *desc, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* 8-bit cache                                                              */
+/* ------------------------------------------------------------------------ */
+/* A pool of half the bytes: k_cache and v_cache hold e4m3 codes in the pool
+ * layout [N, B, Hk, d], and kv_exp, uint8 [N, Hk, B, 2], one power of two per
+ * token, KV head and side (K, then V):
+ *     value = code * 2^(kv_exp - 127),  kv_exp - 127 = e in [-100, 120]
+ * e is the smallest integer >= -100 with 448 * 2^e >= the row's largest finite
+ * magnitude (0 for a row of zeros), each code the e4m3 number nearest to
+ * x * 2^-e (ties to even). Infinities and NaN become the NaN code. Values are
+ * exact in bf16, and writing them again gives the same values. The descriptor's
+ * dtype is PK_E4M3, d a multiple of 16 and at most 256; kv_exp is 16-byte
+ * aligned. */
+
+/* As pk_reshape_and_cache into an 8-bit cache. k, v: src_dtype (PK_F32 or
+ * PK_BF16), token i's [Hk, d] at i * k_stride (v_stride) elements, strides
+ * multiples of 16 bytes. */
+pk_status pk_reshape_and_cache_e4m3(const void *k, const void *v, pk_dtype src_dtype,
+                                    int64_t k_stride, int64_t v_stride,
+                                    const int64_t *slot_mapping, int32_t num_tokens, void *k_cache,
+                                    void *v_cache, uint8_t *kv_exp, const pk_cache_desc *desc,
+                                    void *stream);
+
+/* Reads tokens back: k_out[i], v_out[i] ([T, Hk, d], out_dtype PK_F32 or
+ * PK_BF16) = the values at slot_mapping[i]. Rows of negative slots stay as they
+ * were; out-of-range slots likewise, and are recorded (PK_DEVERR_SLOT). */
+pk_status pk_gather_cache_e4m3(void *k_out, void *v_out, pk_dtype out_dtype,
+                               const int64_t *slot_mapping, int32_t num_tokens, const void *k_cache,
+                               const void *v_cache, const uint8_t *kv_exp,
+                               const pk_cache_desc *desc, void *stream);
+
+/* pk_copy_blocks of an 8-bit cache: the codes and the exponents of each block. */
+pk_status pk_copy_blocks_e4m3(void *k_cache, void *v_cache, uint8_t *kv_exp,
+                              const int64_t *src_dst_pairs, int32_t num_pairs,
+                              const pk_cache_desc *desc, void *stream);
+
+/* Decode attention over an 8-bit cache: pk_paged_attention_decode on its
+ * values, with q and out of io_dtype (PK_F32 or PK_BF16). Arguments, clamping
+ * and recorded events as there and in pk_paged_attention_decode_items;
+ * work_items may be NULL (then num_items is 0 and the (sequence, partition)
+ * grid runs). head_dim 64 or 128, B 8, 16 or 32, Hq / Hk at most 8. */
+pk_status pk_paged_attention_decode_e4m3(
+    void *out, const void *q, pk_dtype io_dtype, const void *k_cache, const void *v_cache,
+    const uint8_t *kv_exp, const int32_t *block_tables, const int32_t *context_lens, float scale,
+    int32_t num_seqs, int32_t num_q_heads, int32_t max_blocks_per_seq, int32_t max_context_len,
+    int32_t partition_size, const int32_t *work_items, int32_t num_items, void *workspace,
+    size_t workspace_bytes, const pk_cache_desc *desc, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Attention of drafted tokens                                              */
+/* ------------------------------------------------------------------------ */
+/* Verification of drafted tokens (speculative decoding): each sequence s has
+ * n = q_offsets[s + 1] - q_offsets[s] drafted tokens, 0 <= n <= max_draft_len,
+ * which are the last n of its context; their K/V are in the cache already. With
+ * base = context_lens[s] - n, draft i of the sequence attends to every token
+ * t < base and to the draft at base + j where bit j of tree_mask[q_offsets[s] +
+ * i] is set (bits n and up are ignored). Without masks the drafts are a chain:
+ * draft i sees drafts 0 .. i. A draft that sees nothing gets zeros; what a
+ * token that it does not see holds, NaN included, does not reach it.
+ *   out, q        [num_q_tokens, Hq, d], dtype of the pool; sequence s's rows
+ *                 are q_offsets[s] .. q_offsets[s + 1] - 1, and rows of no
+ *                 sequence are neither read nor written.
+ *   q_offsets     int32 [S + 1], ascending. An entry that is no range of the
+ *                 rows, or longer than max_draft_len, is recorded
+ *                 (PK_DEVERR_OFFSETS) and its sequence is skipped.
+ *   context_lens  int32 [S], drafts included: n <= length <= min(max_context_len,
+ *                 max_blocks_per_seq * B), clamped and recorded otherwise
+ *                 (PK_DEVERR_CONTEXT; a length below n gives zero rows). Not
+ *                 read where n is 0.
+ *   tree_mask     uint64 [num_q_tokens], or NULL (see pk_tree_masks).
+ *   max_draft_len at most PK_MAX_DRAFT (sizes the grid).
+ *   partition_size, work_items  0 and NULL: each context whole; otherwise
+ *                 pk_tree_plan's (work_items NULL: the grid of every partition).
+ *   workspace     pk_tree_workspace_size bytes when the contexts are split.
+ * dtype PK_F32 or PK_BF16, head_dim 64 or 128, Hq / Hk at most 8. */
+#define PK_MAX_DRAFT 64
+pk_status pk_paged_attention_tree(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                  const int32_t *block_tables, const int32_t *context_lens,
+                                  const int32_t *q_offsets, const uint64_t *tree_mask, float scale,
+                                  int32_t num_seqs, int32_t num_q_tokens, int32_t max_draft_len,
+                                  int32_t num_q_heads, int32_t max_blocks_per_seq,
+                                  int32_t max_context_len, int32_t partition_size,
+                                  const int32_t *work_items, int32_t num_items, void *workspace,
+                                  size_t workspace_bytes, const pk_cache_desc *desc, void *stream);
+
+/* Host helper: masks_out[i] = the drafts that draft i sees in the tree of
+ * parents (parents[i] in [-1, i); -1: a child of the last committed token):
+ * itself and its ancestors. depths_out (optional) receives the depths, so that
+ * draft i's position is base + depths_out[i]. */
+pk_status pk_tree_masks(const int32_t *parents, int32_t num_drafts, uint64_t *masks_out,
+                        int32_t *depths_out);
+
+/* Host planner for pk_paged_attention_tree, as pk_attention_plan: the
+ * partition size (-1: chosen from the lengths; > 0, a multiple of B, or 0: as
+ * given) and the work list of host context_lens. */
+pk_status pk_tree_plan(const int32_t *context_lens, int32_t num_seqs, int32_t max_draft_len,
+                       int32_t num_q_heads, int32_t partition_size, const pk_cache_desc *desc,
+                       int32_t *partition_out, int32_t *items_out, int32_t cap,
+                       int32_t *num_items_out);
+
+/* Workspace bytes of pk_paged_attention_tree for num_q_tokens rows: fp32
+ * partials [num_q_tokens, Hq, P, d + 2] with P = ceil(max_context_len /
+ * partition_size) when that is above 1, else 0. Needs no clearing; calls whose
+ * work overlaps on the GPU must not share it. Host only. */
+size_t pk_tree_workspace_size(int32_t num_q_tokens, int32_t num_q_heads, int32_t max_context_len,
+                              int32_t partition_size, const pk_cache_desc *desc);
 
 /* A pure read stream over `bytes` (a multiple of 16; device memory, 16-byte
  * aligned): every 16-byte vector is loaded once and the loads are folded so

@@ -10,7 +10,15 @@ The functions carry the C ABI's names (``include/pagedkv.h``):
 * :func:`pk_paged_attention_decode` -- attention through the block tables,
   with optional split-K partitions merged by log-sum-exp;
 * :class:`BlockManager` -- the host block manager (free list, refcounts,
-  fork, copy-on-write, block tables, slot mappings).
+  fork, copy-on-write, block tables, slot mappings);
+* :func:`pk_qk_norm_rope_and_cache` -- per-head norm of queries and keys,
+  rotary positions and the cache write in one pass;
+* :func:`pk_reshape_and_cache_e4m3`, :func:`pk_gather_cache_e4m3`,
+  :func:`pk_copy_blocks_e4m3`, :func:`pk_paged_attention_decode_e4m3` -- an
+  8-bit cache: write, read back, block copies, decode attention;
+* :func:`pk_paged_attention_tree` -- attention of drafted tokens (a tree or a
+  chain) over the cached context, with :func:`pk_tree_masks` and
+  :func:`pk_tree_plan`.
 
 PyTorch provides device memory and streams: the device entry points take
 CUDA tensors and enqueue on the current stream unless one is given.
@@ -30,16 +38,21 @@ __all__ = [
     "pk_reshape_and_cache", "pk_reshape_and_cache_append", "pk_copy_blocks", "pk_paged_attention_decode",
     "pk_paged_attention_workspace_size", "pk_paged_attention_resolve_partition",
     "pk_get_device_error", "pk_status_string", "BlockManager",
-    "PK_F32", "PK_BF16", "IMPLS", "DEVERR_NAMES",
+    "pk_qk_norm_rope_and_cache", "pk_reshape_and_cache_e4m3", "pk_gather_cache_e4m3", "pk_copy_blocks_e4m3",
+    "pk_paged_attention_decode_e4m3", "pk_paged_attention_tree", "pk_tree_masks", "pk_tree_plan",
+    "pk_tree_workspace_size",
+    "PK_F32", "PK_BF16", "PK_E4M3", "PK_MAX_DRAFT", "IMPLS", "DEVERR_NAMES",
 ]
 
 PK_OK, PK_ERR_INVALID_ARG, PK_ERR_UNSUPPORTED, PK_ERR_OUT_OF_BLOCKS = 0, 1, 2, 3
 PK_ERR_UNKNOWN_SEQ, PK_ERR_SEQ_EXISTS, PK_ERR_CUDA, PK_ERR_WORKSPACE = 4, 5, 6, 7
 PK_ERR_INVARIANT, PK_ERR_NOMEM = 8, 9
-PK_F32, PK_BF16 = 0, 1
+PK_F32, PK_BF16, PK_E4M3 = 0, 1, 2
+PK_MAX_DRAFT = 64  # drafted tokens per sequence of pk_paged_attention_tree
 IMPLS = {"auto": 0, "simt": 1, "mma": 2}
 PK_STATIC_WORKSPACE_BYTES = 64 << 20  # the static split-K scratch of pk_paged_attention_decode_static
-DEVERR_NAMES = {0: "none", 1: "slot", 2: "block_id", 3: "pair", 4: "context", 5: "timeout", 6: "order"}
+DEVERR_NAMES = {0: "none", 1: "slot", 2: "block_id", 3: "pair", 4: "context", 5: "timeout", 6: "order",
+                7: "position", 8: "offsets"}
 
 # Every symbol include/pagedkv.h declares.
 EXPORTED = (
@@ -58,6 +71,9 @@ EXPORTED = (
     "pk_swap_blocks", "pk_bm_set_swap_space", "pk_bm_swap_out", "pk_bm_swap_in", "pk_bm_is_swapped",
     "pk_bm_host_free", "pk_bm_add_seq_cached", "pk_bm_commit", "pk_bm_cache_match", "pk_bm_cache_stats",
     "pk_bm_is_cached", "pk_bm_free_blocks", "pk_sim_num_steps", "pk_sim_run",
+    "pk_qk_norm_rope_and_cache", "pk_reshape_and_cache_e4m3", "pk_gather_cache_e4m3", "pk_copy_blocks_e4m3",
+    "pk_paged_attention_decode_e4m3", "pk_paged_attention_tree", "pk_tree_masks", "pk_tree_plan",
+    "pk_tree_workspace_size",
 )
 PK_POLICY = {"max_reservation": 0, "exact_contiguous": 1, "paged": 2}
 PK_SIM_RULE = {"drop": 0, "stall": 1}
@@ -178,6 +194,18 @@ def lib() -> ctypes.CDLL:
         "pk_decode_step_launch": (i32, [i32, i32, f32, i32, P, P, D, ctypes.POINTER(StepBuffers), P]),
         "pk_decode_step_graph_count": (i32, [ctypes.POINTER(StepBuffers)]),
         "pk_decode_step_release": (None, [ctypes.POINTER(StepBuffers)]),
+        "pk_qk_norm_rope_and_cache": (i32, [P, P, P, P, P, i64, i64, i64, P, P, f32, P, P, i32, i32, i32, P, i32,
+                                            i32, P, P, D, P]),
+        "pk_reshape_and_cache_e4m3": (i32, [P, P, i32, i64, i64, P, i32, P, P, P, D, P]),
+        "pk_gather_cache_e4m3": (i32, [P, P, i32, P, i32, P, P, P, D, P]),
+        "pk_copy_blocks_e4m3": (i32, [P, P, P, P, i32, D, P]),
+        "pk_paged_attention_decode_e4m3": (i32, [P, P, i32, P, P, P, P, P, f32, i32, i32, i32, i32, i32, P, i32,
+                                                 P, sz, D, P]),
+        "pk_paged_attention_tree": (i32, [P, P, P, P, P, P, P, P, f32, i32, i32, i32, i32, i32, i32, i32, P, i32,
+                                          P, sz, D, P]),
+        "pk_tree_masks": (i32, [P, i32, P, P]),
+        "pk_tree_plan": (i32, [P, i32, i32, i32, i32, D, P, P, i32, P]),
+        "pk_tree_workspace_size": (sz, [i32, i32, i32, i32, D]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(L, name)
@@ -210,6 +238,8 @@ def _dtype_code(t) -> int:
         return PK_F32
     if t.dtype == torch.bfloat16:
         return PK_BF16
+    if t.dtype == torch.float8_e4m3fn:
+        return PK_E4M3
     raise TypeError(f"unsupported dtype {t.dtype}: libpagedkv takes float32 or bfloat16")
 
 
@@ -502,6 +532,266 @@ def pk_swap_blocks(k_cache, v_cache, k_host, v_host, pairs, direction: int, stre
                                 ctypes.c_void_p(k_host.data_ptr()), ctypes.c_void_p(v_host.data_ptr()),
                                 int(k_host.shape[0]), ctypes.c_void_p(pairs.data_ptr()), n, int(direction),
                                 ctypes.byref(desc), _stream(stream)), "pk_swap_blocks")
+
+
+# -- new tokens of a layer, 8-bit caches, drafted tokens ----------------------
+class _on_device:
+    """The tensors' device current for the call's launches, and a stream of it:
+    the given one, else that device's current stream."""
+
+    def __init__(self, stream, *tensors):
+        torch = _torch()
+        dev = tensors[0].device
+        for t in tensors[1:]:
+            if t is not None and t.device != dev:
+                raise ValueError("all tensors must be on one device")
+        if stream is not None and stream.device != dev:
+            raise ValueError("the stream is not on the tensors' device")
+        self.stream = ctypes.c_void_p((torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream)
+        self._guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def _heads(t, name, tokens, heads, d):
+    """Pointer and token stride of ``[tokens, heads, d]`` whose heads are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (libpagedkv has no CPU path)")
+    if tuple(t.shape) != (tokens, heads, d):
+        raise ValueError(f"{name} must be [{tokens}, {heads}, {d}]")
+    if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"the heads of {name} must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), (int(t.stride(0)) if tokens > 1 else heads * d)
+
+
+def pk_qk_norm_rope_and_cache(q_out, k_out, q, k, v, cos_sin, positions, q_weight=None, k_weight=None,
+                              eps: float = 1e-6, interleaved: bool = False, slot_mapping=None, k_cache=None,
+                              v_cache=None, stream=None):
+    """Per-head RMS norm of ``q [T, Hq, d]`` and ``k [T, Hk, d]`` (skipped
+    without weights ``[d]``), the rotation by ``cos_sin`` (fp32 ``[max_position,
+    rotary_dim]``: cosines, then sines; None: no rotation) at ``positions``
+    (int64 ``[T]``), and with ``slot_mapping`` (int64 ``[T]``) the write of the
+    new keys and of ``v`` into the caches. Results go to ``q_out`` and ``k_out``
+    (the latter optional with a slot mapping). ``q``, ``k`` and ``v`` may be views
+    of one packed projection: only each token's heads have to be contiguous."""
+    torch = _torch()
+    T, Hq, d = (int(x) for x in q.shape)
+    Hk = int(k.shape[1])
+    given = [t is not None for t in (slot_mapping, k_cache, v_cache)]
+    if any(given) != all(given):
+        raise ValueError("slot_mapping, k_cache and v_cache go together")
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight go together")
+    if all(given):
+        desc = cache_desc(k_cache)
+        if (desc.num_kv_heads, desc.head_dim) != (Hk, d) or v_cache.shape != k_cache.shape:
+            raise ValueError("the caches must be [num_blocks, block_size, num_kv_heads, head_dim]")
+        if v is None or tuple(slot_mapping.shape) != (T,):
+            raise ValueError("v is required and slot_mapping must be [num_tokens]")
+    else:
+        desc = CacheDesc(0, 0, Hk, d, _dtype_code(q))
+        v = None
+        if k_out is None:
+            raise ValueError("k_out is required without a cache")
+    for t in (q_out, k_out, k, v, q_weight, k_weight, k_cache, v_cache):
+        if t is not None and t.dtype != q.dtype:
+            raise TypeError("queries, keys, values, weights and caches must share one dtype")
+    for t, shape, name in ((q_out, (T, Hq, d), "q_out"), (k_out, (T, Hk, d), "k_out"), (q_weight, (d,), "q_weight"),
+                           (k_weight, (d,), "k_weight")):
+        if t is not None and tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {list(shape)}")
+    rot = max_pos = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or positions is None or tuple(positions.shape) != (T,):
+            raise ValueError("cos_sin must be [max_position, rotary_dim] and positions [num_tokens]")
+        max_pos, rot = (int(x) for x in cos_sin.shape)
+    opt = lambda t, name, dt=None: None if t is None else _dev(t, name, dt)
+    qp, qs = _heads(q, "q", T, Hq, d)
+    kp, ks = _heads(k, "k", T, Hk, d)
+    vp, vs = (None, 0) if v is None else _heads(v, "v", T, Hk, d)
+    with _on_device(stream, q, q_out, k_out, k, v, cos_sin, positions if rot else None, q_weight, k_weight,
+                    slot_mapping, k_cache, v_cache) as st:
+        _check(lib().pk_qk_norm_rope_and_cache(
+            _dev(q_out, "q_out"), opt(k_out, "k_out"), qp, kp, vp, qs, ks, vs, opt(q_weight, "q_weight"),
+            opt(k_weight, "k_weight"), float(eps), opt(cos_sin, "cos_sin", torch.float32),
+            _dev(positions, "positions", torch.int64) if rot else None, max_pos, rot, int(bool(interleaved)),
+            opt(slot_mapping, "slot_mapping", torch.int64), T, Hq, opt(k_cache, "k_cache"), opt(v_cache, "v_cache"),
+            ctypes.byref(desc), st), "pk_qk_norm_rope_and_cache")
+
+
+def _e4m3_cache(k_cache, v_cache, kv_exp) -> CacheDesc:
+    torch = _torch()
+    desc = cache_desc(k_cache)
+    if k_cache.dtype != torch.float8_e4m3fn or v_cache.dtype != k_cache.dtype:
+        raise TypeError("k_cache and v_cache must be torch.float8_e4m3fn")
+    if v_cache.shape != k_cache.shape or \
+            tuple(kv_exp.shape) != (desc.num_blocks, desc.num_kv_heads, desc.block_size, 2):
+        raise ValueError("kv_exp must be [num_blocks, num_kv_heads, block_size, 2] of the caches' shape")
+    return desc
+
+
+def pk_reshape_and_cache_e4m3(k, v, slot_mapping, k_cache, v_cache, kv_exp, stream=None):
+    """Writes token i's K/V (fp32 or bf16 ``[T, Hk, d]``, each token's heads
+    contiguous) into slot ``slot_mapping[i]`` (int64) of an 8-bit cache: e4m3
+    codes in ``k_cache``/``v_cache`` (``torch.float8_e4m3fn``) and exponents in
+    ``kv_exp`` (uint8 ``[N, Hk, B, 2]``); value = code * 2^(kv_exp - 127)."""
+    torch = _torch()
+    desc = _e4m3_cache(k_cache, v_cache, kv_exp)
+    T = int(k.shape[0])
+    if v.dtype != k.dtype or k.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("k and v must both be float32 or bfloat16")
+    if tuple(slot_mapping.shape) != (T,):
+        raise ValueError("slot_mapping must be [num_tokens]")
+    kp, ks = _heads(k, "k", T, desc.num_kv_heads, desc.head_dim)
+    vp, vs = _heads(v, "v", T, desc.num_kv_heads, desc.head_dim)
+    with _on_device(stream, k_cache, v_cache, kv_exp, k, v, slot_mapping) as st:
+        _check(lib().pk_reshape_and_cache_e4m3(
+            kp, vp, _dtype_code(k), ks, vs, _dev(slot_mapping, "slot_mapping", torch.int64), T,
+            _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(kv_exp, "kv_exp", torch.uint8),
+            ctypes.byref(desc), st), "pk_reshape_and_cache_e4m3")
+
+
+def pk_gather_cache_e4m3(k_out, v_out, slot_mapping, k_cache, v_cache, kv_exp, stream=None):
+    """Reads the tokens at ``slot_mapping`` back from an 8-bit cache into
+    ``k_out`` and ``v_out`` (fp32 or bf16 ``[T, Hk, d]``); rows of negative
+    slots stay as they were."""
+    torch = _torch()
+    desc = _e4m3_cache(k_cache, v_cache, kv_exp)
+    T = int(slot_mapping.shape[0])
+    if tuple(k_out.shape) != (T, desc.num_kv_heads, desc.head_dim) or v_out.shape != k_out.shape:
+        raise ValueError("k_out and v_out must be [num_tokens, num_kv_heads, head_dim]")
+    if v_out.dtype != k_out.dtype or k_out.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("k_out and v_out must both be float32 or bfloat16")
+    with _on_device(stream, k_cache, v_cache, kv_exp, k_out, v_out, slot_mapping) as st:
+        _check(lib().pk_gather_cache_e4m3(
+            _dev(k_out, "k_out"), _dev(v_out, "v_out"), _dtype_code(k_out),
+            _dev(slot_mapping, "slot_mapping", torch.int64), T, _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
+            _dev(kv_exp, "kv_exp", torch.uint8), ctypes.byref(desc), st), "pk_gather_cache_e4m3")
+
+
+def pk_copy_blocks_e4m3(k_cache, v_cache, kv_exp, src_dst_pairs, stream=None):
+    """:func:`pk_copy_blocks` of an 8-bit cache (codes and exponents)."""
+    torch = _torch()
+    desc = _e4m3_cache(k_cache, v_cache, kv_exp)
+    n = int(src_dst_pairs.shape[0]) if src_dst_pairs.numel() else 0
+    if n and tuple(src_dst_pairs.shape) != (n, 2):
+        raise ValueError("src_dst_pairs must be [num_pairs, 2]")
+    if n == 0:
+        return
+    with _on_device(stream, k_cache, v_cache, kv_exp, src_dst_pairs) as st:
+        _check(lib().pk_copy_blocks_e4m3(
+            _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(kv_exp, "kv_exp", torch.uint8),
+            _dev(src_dst_pairs, "src_dst_pairs", torch.int64), n, ctypes.byref(desc), st), "pk_copy_blocks_e4m3")
+
+
+def _attention_args(out, q, block_tables, context_lens, num_seqs, d, work_items, workspace):
+    """The checks and optional pointers that the two attentions below share."""
+    torch = _torch()
+    if q.dim() != 3 or int(q.shape[2]) != d or out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out and q must be [rows, num_q_heads, head_dim] of one dtype")
+    if block_tables.dim() != 2 or int(block_tables.shape[0]) != num_seqs or tuple(context_lens.shape) != (num_seqs,):
+        raise ValueError("block_tables must be [num_seqs, max_blocks] and context_lens [num_seqs]")
+    items, n_items, ws, ws_bytes = None, 0, None, 0
+    if work_items is not None:
+        if work_items.dim() != 2 or int(work_items.shape[1]) != 2:
+            raise ValueError("work_items must be [n, 2]")
+        items, n_items = _dev(work_items, "work_items", torch.int32), int(work_items.shape[0])
+    if workspace is not None:
+        ws, ws_bytes = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    return items, n_items, ws, ws_bytes
+
+
+def pk_paged_attention_decode_e4m3(out, q, k_cache, v_cache, kv_exp, block_tables, context_lens, scale: float,
+                                   max_context_len: int, partition_size: int = -1, workspace=None,
+                                   work_items=None, stream=None):
+    """:func:`pk_paged_attention_decode` over an 8-bit cache; ``q`` and ``out``
+    ``[S, Hq, d]`` are fp32 or bf16. ``partition_size``, ``workspace`` and
+    ``work_items`` as there (:func:`pk_attention_plan` and
+    :func:`pk_paged_attention_workspace_size` take the 8-bit cache's descriptor)."""
+    torch = _torch()
+    desc = _e4m3_cache(k_cache, v_cache, kv_exp)
+    if q.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("q and out must be float32 or bfloat16")
+    S = int(q.shape[0])
+    items, n_items, ws, ws_bytes = _attention_args(out, q, block_tables, context_lens, S, desc.head_dim, work_items,
+                                                   workspace)
+    with _on_device(stream, k_cache, v_cache, kv_exp, out, q, block_tables, context_lens, work_items,
+                    workspace) as st:
+        _check(lib().pk_paged_attention_decode_e4m3(
+            _dev(out, "out"), _dev(q, "q"), _dtype_code(q), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
+            _dev(kv_exp, "kv_exp", torch.uint8), _dev(block_tables, "block_tables", torch.int32),
+            _dev(context_lens, "context_lens", torch.int32), float(scale), S, int(q.shape[1]),
+            int(block_tables.shape[1]), int(max_context_len), int(partition_size), items, n_items, ws, ws_bytes,
+            ctypes.byref(desc), st), "pk_paged_attention_decode_e4m3")
+
+
+def pk_paged_attention_tree(out, q, k_cache, v_cache, block_tables, context_lens, q_offsets, scale: float,
+                            max_draft_len: int, max_context_len: int, tree_mask=None, partition_size: int = 0,
+                            workspace=None, work_items=None, stream=None):
+    """Attention of drafted tokens over the cached context (see the header):
+    rows ``q_offsets[s] .. q_offsets[s + 1]`` (int32 ``[S + 1]``) of ``q`` and
+    ``out`` ``[rows, Hq, d]`` are sequence s's drafts, the last tokens of its
+    ``context_lens[s]``. ``tree_mask`` int64 or uint64 ``[rows]``: bit j of a
+    row's word lets it see draft j of its sequence (None: a chain; see
+    :func:`pk_tree_masks`). ``partition_size`` and ``work_items`` from
+    :func:`pk_tree_plan`, ``workspace`` of :func:`pk_tree_workspace_size` bytes
+    when the contexts are split."""
+    torch = _torch()
+    desc = cache_desc(k_cache)
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or q.dtype != k_cache.dtype:
+        raise ValueError("q, k_cache and v_cache must share one dtype, the caches one shape")
+    S = int(block_tables.shape[0])
+    items, n_items, ws, ws_bytes = _attention_args(out, q, block_tables, context_lens, S, desc.head_dim, work_items,
+                                                   workspace)
+    if tuple(q_offsets.shape) != (S + 1,):
+        raise ValueError("q_offsets must be [num_seqs + 1]")
+    mask = None
+    if tree_mask is not None:
+        if tree_mask.dtype not in (torch.int64, torch.uint64) or tuple(tree_mask.shape) != (int(q.shape[0]),):
+            raise ValueError("tree_mask must be int64 or uint64 [rows]")
+        mask = _dev(tree_mask, "tree_mask")
+    with _on_device(stream, k_cache, v_cache, out, q, block_tables, context_lens, q_offsets, tree_mask, work_items,
+                    workspace) as st:
+        _check(lib().pk_paged_attention_tree(
+            _dev(out, "out"), _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
+            _dev(block_tables, "block_tables", torch.int32), _dev(context_lens, "context_lens", torch.int32),
+            _dev(q_offsets, "q_offsets", torch.int32), mask, float(scale), S, int(q.shape[0]), int(max_draft_len),
+            int(q.shape[1]), int(block_tables.shape[1]), int(max_context_len), int(partition_size), items, n_items,
+            ws, ws_bytes, ctypes.byref(desc), st), "pk_paged_attention_tree")
+
+
+def pk_tree_masks(parents) -> Tuple[np.ndarray, np.ndarray]:
+    """Host helper: ``(masks int64 [n], depths int32 [n])`` of the tree whose
+    draft i is a child of draft ``parents[i]`` (-1: of the last committed token)."""
+    par = np.ascontiguousarray(parents, dtype=np.int32)
+    masks, depths = np.zeros(max(len(par), 1), np.int64), np.zeros(max(len(par), 1), np.int32)
+    _check(lib().pk_tree_masks(_np_ptr(par), len(par), _np_ptr(masks), _np_ptr(depths)), "pk_tree_masks")
+    return masks[: len(par)], depths[: len(par)]
+
+
+def pk_tree_plan(context_lens, max_draft_len: int, num_q_heads: int, desc: CacheDesc, partition_size: int = -1):
+    """Host planner: ``(partition, items int32 [n, 2])`` of
+    :func:`pk_paged_attention_tree` for the host context lengths."""
+    lens = np.ascontiguousarray(context_lens, dtype=np.int32)
+    part, n = ctypes.c_int32(0), ctypes.c_int32(0)
+    args = (_np_ptr(lens), len(lens), int(max_draft_len), int(num_q_heads), int(partition_size), ctypes.byref(desc),
+            ctypes.byref(part))
+    lib().pk_tree_plan(*args, None, 0, ctypes.byref(n))
+    out = np.empty((max(n.value, 1), 2), np.int32)
+    _check(lib().pk_tree_plan(*args, _np_ptr(out), n.value, ctypes.byref(n)), "pk_tree_plan")
+    return int(part.value), out[: n.value]
+
+
+def pk_tree_workspace_size(num_q_tokens, num_q_heads, max_context_len, partition_size, desc) -> int:
+    return int(lib().pk_tree_workspace_size(int(num_q_tokens), int(num_q_heads), int(max_context_len),
+                                            int(partition_size), ctypes.byref(desc)))
 
 
 def pk_get_device_error(stream=None) -> Tuple[int, int]:

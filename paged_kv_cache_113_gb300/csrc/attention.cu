@@ -73,6 +73,10 @@ extern "C" pk_status pkx_reshape_and_cache_advance(const void *k, const void *v,
                                                    const int32_t *lens_in, int32_t *lens_out,
                                                    void *stream);
 
+// CTAs of the 8-bit cache's attention kernel resident on one SM
+// (attention_e4m3.cu).
+extern "C" int pkx_e4m3_resident_ctas(int head_dim, int block_size);
+
 namespace {
 
 __device__ int g_attn_error;
@@ -1473,6 +1477,7 @@ int simt_resident_ctas() {
 }
 
 int resident_ctas(const pk_cache_desc &d, int group) {
+  if (d.dtype == PK_E4M3) return pkx_e4m3_resident_ctas(d.head_dim, d.block_size);
   if (mma_supported(d, group)) {
     const bool d128 = d.head_dim == 128;
     switch (d.block_size) {
@@ -1523,12 +1528,13 @@ pk_status launch_lse_merge_d(const AttnParams &p, int D, cudaStream_t s) {
   return D == 128 ? launch_lse_merge<128>(p, s) : launch_lse_merge<64>(p, s);
 }
 
+// `e4m3`: the host helpers plan for 8-bit caches too.
 pk_status check_common(const pk_cache_desc *desc, int32_t num_seqs, int32_t num_q_heads,
-                       int32_t max_context_len) {
+                       int32_t max_context_len, bool e4m3 = false) {
   if (!desc || desc->num_blocks <= 0 || desc->block_size <= 0 || desc->num_kv_heads <= 0 ||
       desc->head_dim <= 0 || num_seqs < 0 || num_q_heads <= 0 || max_context_len <= 0)
     return PK_ERR_INVALID_ARG;
-  if (elem_size(desc->dtype) == 0) return PK_ERR_UNSUPPORTED;
+  if (elem_size(desc->dtype) == 0 && !(e4m3 && desc->dtype == PK_E4M3)) return PK_ERR_UNSUPPORTED;
   if (num_q_heads % desc->num_kv_heads != 0) return PK_ERR_INVALID_ARG;
   if (num_q_heads / desc->num_kv_heads > kMaxGroup) return PK_ERR_UNSUPPORTED;
   if (desc->head_dim != 64 && desc->head_dim != 128) return PK_ERR_UNSUPPORTED;
@@ -1601,7 +1607,7 @@ extern "C" {
 int32_t pk_paged_attention_resolve_partition(int32_t num_seqs, int32_t num_q_heads,
                                              int32_t max_context_len, int32_t partition_size,
                                              const pk_cache_desc *desc) {
-  if (check_common(desc, num_seqs, num_q_heads, max_context_len) != PK_OK) return -1;
+  if (check_common(desc, num_seqs, num_q_heads, max_context_len, true) != PK_OK) return -1;
   const int32_t B = desc->block_size;
   if (partition_size > 0) return partition_size % B == 0 ? partition_size : -1;
   if (partition_size == 0) return 0;
@@ -1616,7 +1622,7 @@ int32_t pk_paged_attention_resolve_partition(int32_t num_seqs, int32_t num_q_hea
   const int64_t units = int64_t(num_seqs) * desc->num_kv_heads;
   const int64_t slots =
       int64_t(sm_count()) * resident_ctas(*desc, num_q_heads / desc->num_kv_heads);
-  if (units >= slots || max_context_len <= 512) return 0;
+  if (units == 0 || units >= slots || max_context_len <= 512) return 0;
   const int64_t P = slots / units;
   if (P < 2) return 0;
   int64_t part = (max_context_len + P - 1) / P;
@@ -1835,7 +1841,7 @@ pk_status pk_attention_plan(const int32_t *context_lens, int32_t num_seqs, int32
     max_ctx = std::max(max_ctx, c);
     total += c;
   }
-  pk_status st = check_common(desc, num_seqs, num_q_heads, max_ctx);
+  pk_status st = check_common(desc, num_seqs, num_q_heads, max_ctx, true);
   if (st != PK_OK) return st;
   const int32_t B = desc->block_size;
   int32_t part = 0;

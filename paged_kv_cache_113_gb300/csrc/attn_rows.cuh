@@ -1,0 +1,421 @@
+// Shared by the attention kernels over 8-bit caches and over drafted tokens:
+// the launch parameters, a sequence's place in the batch, the CUDA-core
+// kernel for fp32 and for shapes the tensor-core kernels are not compiled
+// for, and the log-sum-exp merge of split rows.
+//
+// A sequence s has n_s query tokens (1 without q_offsets), the last n_s of its
+// context. With base = ctx - n_s, query i of it sees every token t < base and
+// the token base + j where bit j of its mask is set (a chain without masks:
+// j <= i). Per KV head the sequence is n_s * G rows of query, row r being token
+// r / G, query head kvh * G + r % G.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "pagedkv.h"
+#include "pk_device.cuh"
+
+namespace pk {
+namespace {
+
+// The device error word of the including translation unit.
+__device__ int g_rows_error;
+
+struct RowsParams {
+  void *out;                  // [num_rows, Hq, D]
+  const void *q;              // [num_rows, Hq, D]
+  const void *k_cache, *v_cache;  // [N, B, Hk, D]
+  const uint8_t *kv_exp;      // [N, Hk, B, 2] (8-bit caches)
+  const int32_t *tables;      // [S, max_blocks]
+  const int32_t *ctx_lens;    // [S]
+  const int32_t *q_offsets;   // [S + 1], or null: row s is sequence s's only query
+  const uint64_t *tree_mask;  // [num_rows], or null: a chain
+  float *ws_acc, *ws_m, *ws_l;  // split-K partials [num_rows, Hq, P, D], [.., P], [.., P]
+  const int32_t *items;       // [num_items][2] (sequence, partition), or null
+  float scale_log2;           // scale * log2(e)
+  int32_t num_seqs, num_rows, max_draft, num_q_heads, num_kv_heads, group;
+  int32_t block_size, max_blocks, num_blocks;
+  int32_t partition, num_partitions, num_items;
+  int32_t row_tiles;          // CTAs that share a (sequence, KV head)'s rows
+};
+
+struct SeqRows {
+  int q0, n;     // query rows q0 .. q0 + n - 1 (n = 0: nothing to do)
+  int ctx;       // context length (0: the rows are zero)
+  int np;        // partitions with tokens
+};
+
+// Sequence s's rows and length, checked; bad entries are recorded when asked.
+__device__ __forceinline__ SeqRows seq_rows(const RowsParams &p, int s, bool record) {
+  SeqRows r{s, 1, 0, 0};
+  if (p.q_offsets) {
+    const int a = __ldg(p.q_offsets + s), b = __ldg(p.q_offsets + s + 1);
+    if (a < 0 || b < a || b > p.num_rows || b - a > p.max_draft) {
+      if (record) record_error(&g_rows_error, PK_DEVERR_OFFSETS, s);
+      r.n = 0;
+      return r;
+    }
+    r.q0 = a;
+    r.n = b - a;
+    if (r.n == 0) return r;
+  }
+  int c = __ldg(p.ctx_lens + s);
+  const int cap = int(min(int64_t(p.max_blocks) * p.block_size,
+                          int64_t(p.num_partitions) * p.partition));
+  if (c < r.n || c > cap) {
+    if (record) record_error(&g_rows_error, PK_DEVERR_CONTEXT, s);
+    c = c < r.n || cap < r.n ? 0 : cap;
+  }
+  r.ctx = c;
+  r.np = int((int64_t(c) + p.partition - 1) / p.partition);
+  return r;
+}
+
+// The (sequence, partition) of work y: an item of the list, or the grid's.
+__device__ __forceinline__ bool work_item(const RowsParams &p, int y, int z, bool record,
+                                          int &s, int &part) {
+  s = y;
+  part = z;
+  if (!p.items) return true;
+  s = __ldg(p.items + 2 * y);
+  part = __ldg(p.items + 2 * y + 1);
+  if (s < 0 || s >= p.num_seqs || part < 0 || part >= p.num_partitions) {
+    if (record) record_error(&g_rows_error, PK_DEVERR_ORDER, y);
+    return false;
+  }
+  return true;
+}
+
+// Which drafted tokens row q0 + i of a sequence of n sees, one bit each.
+__device__ __forceinline__ uint64_t draft_mask(const RowsParams &p, int q0, int i, int n) {
+  const uint64_t all = n >= 64 ? ~0ull : (1ull << n) - 1;
+  if (p.tree_mask) return __ldg(reinterpret_cast<const unsigned long long *>(p.tree_mask) + q0 + i) & all;
+  return i >= 63 ? all : ((2ull << i) - 1) & all;
+}
+
+// Which of the 64 tokens t0 .. t0 + 63 a row sees: those before base, and the
+// drafted ones of its mask (bits past the last draft are clear).
+__device__ __forceinline__ uint64_t see64(uint64_t mask, int base, int t0) {
+  const int cut = base - t0;  // tokens of these that everyone sees
+  if (cut >= 64) return ~0ull;
+  if (cut <= -64) return 0;
+  if (cut >= 0) return (mask << cut) | ((1ull << cut) - 1);
+  return mask >> -cut;
+}
+
+// Tile element types of the pools: four values of a row as fp32.
+struct E4M3 {
+  uint8_t x;
+};
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+  const uint2 v = *reinterpret_cast<const uint2 *>(p);
+  return make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
+}
+__device__ __forceinline__ float4 load4(const E4M3 *p) {
+  const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+  const float2 a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(uint16_t(w & 0xffff), __NV_E4M3)));
+  const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(uint16_t(w >> 16), __NV_E4M3)));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// ---------------------------------------------------------------------------
+// CUDA-core kernel. One CTA of 8 warps per (KV head, tile of 8 * RPW rows,
+// sequence, partition); 32 tokens of K and V at a time are widened into shared
+// memory. Scores: a lane owns a token and goes over the warp's RPW rows, whose
+// queries broadcast. Values: a lane owns D / 32 columns.
+// ---------------------------------------------------------------------------
+template <int D, int RPW>
+struct RowsShape {
+  static constexpr int NW = 8, TT = 32, R = NW * RPW;
+  static constexpr int KS = D + 4;  // padded: lanes read their rows without bank conflicts
+  static constexpr int FLOATS = TT * KS + TT * D + R * D + NW * RPW * TT;
+  static constexpr int SMEM_BYTES = FLOATS * 4;
+};
+
+template <typename Pool, typename IO, int D, int RPW>
+__global__ void __launch_bounds__(256) attn_rows_kernel(RowsParams p) {
+  using S = RowsShape<D, RPW>;
+  constexpr int EPL = D / 32;
+  extern __shared__ __align__(16) float smem[];
+  launch_dependents();  // the merge may be scheduled as this grid drains
+  float *ks = smem, *vs = ks + S::TT * S::KS, *qs = vs + S::TT * D, *ps = qs + S::R * D;
+  const int kvh = blockIdx.x / p.row_tiles, tile = blockIdx.x % p.row_tiles;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool record = blockIdx.x == 0 && threadIdx.x == 0;
+  int s, part;
+  if (!work_item(p, blockIdx.y, blockIdx.z, record, s, part)) return;
+  const SeqRows sr = seq_rows(p, s, record && part == 0);
+  const int G = p.group, r0 = tile * S::R, rows = min(S::R, sr.n * G - r0);
+  if (rows <= 0) return;
+  auto q_row = [&](int r) {  // element offset of row r0 + r in q and out
+    return (size_t(sr.q0 + (r0 + r) / G) * p.num_q_heads + kvh * G + (r0 + r) % G) * D;
+  };
+  if (sr.ctx == 0) {
+    if (part == 0)
+      for (int i = threadIdx.x; i < rows * D; i += 256)
+        store_elem(static_cast<IO *>(p.out) + q_row(i / D) + i % D, 0.0f);
+    return;
+  }
+  if (part >= sr.np) return;
+  const int start = part * p.partition;
+  const int end = min(sr.ctx, start + p.partition), base = sr.ctx - sr.n;
+  for (int i = threadIdx.x; i < S::R * D; i += 256)
+    qs[i] = i / D < rows ? load_elem(static_cast<const IO *>(p.q) + q_row(i / D) + i % D) * p.scale_log2
+                         : 0.0f;
+  float m[RPW], l[RPW], acc[RPW][EPL];
+  uint64_t mask[RPW];
+#pragma unroll
+  for (int r = 0; r < RPW; ++r) {
+    const int row = warp * RPW + r;
+    m[r] = -INFINITY;
+    l[r] = 0.0f;
+    mask[r] = row < rows ? draft_mask(p, sr.q0, (r0 + row) / G, sr.n) : 0;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) acc[r][e] = 0.0f;
+  }
+  const int32_t *trow = p.tables + size_t(s) * p.max_blocks;
+  const int B = p.block_size;
+  for (int t0 = start; t0 < end; t0 += S::TT) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < S::TT * (D / 4); i += 256) {
+      const int j = i / (D / 4), c = (i % (D / 4)) * 4, t = t0 + j;
+      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
+      if (t < end) {
+        const int phys = __ldg(trow + t / B);
+        if (phys < 0 || phys >= p.num_blocks) {
+          record_error(&g_rows_error, PK_DEVERR_BLOCK_ID, s);
+        } else {
+          const size_t row = ((size_t(phys) * B + t % B) * p.num_kv_heads + kvh) * D + c;
+          a = load4(static_cast<const Pool *>(p.k_cache) + row);
+          b = load4(static_cast<const Pool *>(p.v_cache) + row);
+          if (sizeof(Pool) == 1) {
+            const uint16_t e = *reinterpret_cast<const uint16_t *>(
+                p.kv_exp + ((size_t(phys) * p.num_kv_heads + kvh) * B + t % B) * 2);
+            const float ka = __uint_as_float(uint32_t(e & 0xff) << 23);
+            const float va = __uint_as_float(uint32_t(e >> 8) << 23);
+            a.x *= ka, a.y *= ka, a.z *= ka, a.w *= ka;
+            b.x *= va, b.y *= va, b.z *= va, b.w *= va;
+          }
+        }
+      }
+      *reinterpret_cast<float4 *>(ks + j * S::KS + c) = a;
+      *reinterpret_cast<float4 *>(vs + j * D + c) = b;
+    }
+    __syncthreads();
+    if (warp * RPW >= rows) continue;
+    float x[RPW];
+#pragma unroll
+    for (int r = 0; r < RPW; ++r) x[r] = 0.0f;
+    for (int c = 0; c < D; c += 4) {
+      const float4 k = *reinterpret_cast<const float4 *>(ks + lane * S::KS + c);
+#pragma unroll
+      for (int r = 0; r < RPW; ++r) {
+        const float4 q = *reinterpret_cast<const float4 *>(qs + (warp * RPW + r) * D + c);
+        x[r] = fmaf(k.x, q.x, fmaf(k.y, q.y, fmaf(k.z, q.z, fmaf(k.w, q.w, x[r]))));
+      }
+    }
+    float *pw = ps + warp * RPW * S::TT;
+#pragma unroll
+    for (int r = 0; r < RPW; ++r) {
+      const int t = t0 + lane;
+      const bool see = t < end && (t < base || ((mask[r] >> (t - base)) & 1));
+      if (!see) x[r] = -INFINITY;
+      float mx = x[r];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float mn = fmaxf(m[r], mx);
+      const float ref = mn == -INFINITY ? 0.0f : mn;  // nothing seen so far: every weight is 0
+      const float corr = exp2f(m[r] - ref), w = exp2f(x[r] - ref);
+      l[r] = fmaf(l[r], corr, w);
+      m[r] = mn;
+      pw[r * S::TT + lane] = w;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) acc[r][e] *= corr;
+    }
+    __syncwarp();
+    for (int j = 0; j < S::TT; ++j) {
+      float v[EPL];
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) v[e] = vs[j * D + lane * EPL + e];
+#pragma unroll
+      for (int r = 0; r < RPW; ++r) {
+        const float w = pw[r * S::TT + j];
+        if (w != 0.0f)  // a token of no weight adds nothing, whatever its value holds
+#pragma unroll
+          for (int e = 0; e < EPL; ++e) acc[r][e] = fmaf(w, v[e], acc[r][e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < RPW; ++r) {
+    const int row = warp * RPW + r;
+    float sum = l[r];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (row >= rows) continue;
+    const size_t at = q_row(row);
+    if (sr.np == 1) {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e)
+        store_elem(static_cast<IO *>(p.out) + at + lane * EPL + e, acc[r][e] * inv);
+    } else {
+      const size_t slot = at / D * p.num_partitions + part;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) p.ws_acc[slot * D + lane * EPL + e] = acc[r][e];
+      if (lane == 0) {
+        p.ws_m[slot] = m[r];
+        p.ws_l[slot] = sum;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Merge of split rows: M = max_q m_q, out = sum_q acc_q 2^(m_q - M) /
+// sum_q l_q 2^(m_q - M). One warp per row; grid.y = sequence, so that a row
+// needs no search for its sequence.
+// ---------------------------------------------------------------------------
+template <typename IO, int D>
+__global__ void __launch_bounds__(256) rows_merge_kernel(RowsParams p) {
+  constexpr int EPL = D / 32;
+  const int s = blockIdx.y, lane = threadIdx.x & 31;
+  const SeqRows sr = seq_rows(p, s, false);
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5);  // token * Hq + head
+  wait_prerequisites();
+  if (row >= sr.n * p.num_q_heads || sr.np <= 1) return;
+  const size_t at = size_t(sr.q0) * p.num_q_heads + row;
+  const float *mr = p.ws_m + at * p.num_partitions, *lr = p.ws_l + at * p.num_partitions;
+  const float *ar = p.ws_acc + at * p.num_partitions * D + lane * EPL;
+  float M = -INFINITY;
+  for (int q = lane; q < sr.np; q += 32) M = fmaxf(M, __ldcg(mr + q));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float ref = M == -INFINITY ? 0.0f : M;
+  float L = 0.0f, acc[EPL] = {};
+  for (int q = 0; q < sr.np; ++q) {
+    const float w = exp2f(__ldcg(mr + q) - ref);
+    if (w == 0.0f) continue;
+    L = fmaf(__ldcg(lr + q), w, L);
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) acc[e] = fmaf(__ldcg(ar + size_t(q) * D + e), w, acc[e]);
+  }
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+  for (int e = 0; e < EPL; ++e)
+    store_elem(static_cast<IO *>(p.out) + at * D + lane * EPL + e, acc[e] * inv);
+}
+
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Host: the checks and parameters that both attentions share, from the call's
+// arguments. `part` is the resolved partition size (0: no split).
+inline pk_status rows_params(RowsParams &p, void *out, const void *q, const void *k_cache,
+                             const void *v_cache, const int32_t *block_tables,
+                             const int32_t *context_lens, float scale, int32_t num_seqs,
+                             int32_t num_rows, int32_t max_draft, int32_t num_q_heads,
+                             int32_t max_blocks_per_seq, int32_t max_context_len, int32_t part,
+                             const int32_t *items, int32_t num_items, void *workspace,
+                             size_t workspace_bytes, const pk_cache_desc &d) {
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || max_blocks_per_seq <= 0)
+    return PK_ERR_INVALID_ARG;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
+    return PK_ERR_INVALID_ARG;
+  if (!(scale == scale)) return PK_ERR_INVALID_ARG;
+  if (int64_t(max_blocks_per_seq) * d.block_size > INT32_MAX) return PK_ERR_UNSUPPORTED;
+  const int64_t P = part > 0 ? (int64_t(max_context_len) + part - 1) / part : 1;
+  if (num_seqs > 65535 || P > 65535) return PK_ERR_UNSUPPORTED;
+  if (items ? (num_items <= 0 || num_items > 65535) : num_items != 0) return PK_ERR_UNSUPPORTED;
+  p.out = out;
+  p.q = q;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.tables = block_tables;
+  p.ctx_lens = context_lens;
+  p.items = items;
+  p.num_items = num_items;
+  p.scale_log2 = float(double(scale) * 1.4426950408889634);
+  p.num_seqs = num_seqs;
+  p.num_rows = num_rows;
+  p.max_draft = max_draft;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = d.num_kv_heads;
+  p.group = num_q_heads / d.num_kv_heads;
+  p.block_size = d.block_size;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = d.num_blocks;
+  p.partition = P > 1 ? part : max_blocks_per_seq * d.block_size;
+  p.num_partitions = int32_t(P);
+  p.row_tiles = 1;
+  if (workspace && !aligned16(workspace)) return PK_ERR_WORKSPACE;
+  if (P > 1) {
+    const size_t slots = size_t(num_rows) * num_q_heads * size_t(P);
+    if (!workspace || workspace_bytes < slots * (size_t(d.head_dim) + 2) * sizeof(float))
+      return PK_ERR_WORKSPACE;
+    p.ws_acc = static_cast<float *>(workspace);
+    p.ws_m = p.ws_acc + slots * d.head_dim;
+    p.ws_l = p.ws_m + slots;
+  }
+  return PK_OK;
+}
+
+inline dim3 rows_grid(const RowsParams &p) {
+  return dim3(unsigned(p.num_kv_heads * p.row_tiles), unsigned(p.items ? p.num_items : p.num_seqs),
+              unsigned(p.items ? 1 : p.num_partitions));
+}
+
+// Opts a kernel into its dynamic shared memory, once per device (the attribute
+// belongs to the device that is current).
+template <typename Kernel>
+bool smem_ready(Kernel kern, int bytes, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return false;
+  if (dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
+
+// Launches the CUDA-core kernel with 8 * RPW rows per CTA.
+template <typename Pool, typename IO, int D, int RPW>
+pk_status launch_rows(RowsParams p, cudaStream_t stream) {
+  using S = RowsShape<D, RPW>;
+  auto kern = attn_rows_kernel<Pool, IO, D, RPW>;
+  static std::atomic<uint64_t> ready{0};
+  if (!smem_ready(kern, S::SMEM_BYTES, ready)) return PK_ERR_CUDA;
+  p.row_tiles = (p.max_draft * p.group + S::R - 1) / S::R;
+  kern<<<rows_grid(p), 256, S::SMEM_BYTES, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? PK_OK : PK_ERR_CUDA;
+}
+
+// The merge, as the attention's programmatic dependent (an ordinary launch
+// where that is refused).
+template <typename IO, int D>
+pk_status launch_rows_merge(const RowsParams &p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned((int64_t(p.max_draft) * p.num_q_heads + 7) / 8), unsigned(p.num_seqs));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, rows_merge_kernel<IO, D>, p) == cudaSuccess) return PK_OK;
+  cudaGetLastError();
+  rows_merge_kernel<IO, D><<<cfg.gridDim, cfg.blockDim, 0, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? PK_OK : PK_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace pk

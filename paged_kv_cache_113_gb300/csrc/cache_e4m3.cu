@@ -1,0 +1,297 @@
+// The 8-bit cache: new tokens' K/V quantised as they are written
+// (pk_reshape_and_cache_e4m3), read back (pk_gather_cache_e4m3), and the
+// copy-on-write block copy (pk_copy_blocks_e4m3).
+//
+// A row is one token's K or V of one KV head, d values. It is held as d e4m3
+// codes and one power of two:
+//     e = the smallest integer >= -100 with 448 * 2^e >= max |x|   (finite x)
+//     code = e4m3(x * 2^-e), nearest even;      value = code * 2^e
+// and kv_exp holds e + 127. A power of two loses no precision against a scale
+// of max / 448 (e4m3 is a floating format: at most one step of its 2^15 range
+// is given up), the product x * 2^-e is exact, so each code is one rounding of
+// its input whatever computes it, every value is exact in bf16, and values that
+// are written again stay what they are.
+//
+// Pure data movement bounds all three kernels.
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "pagedkv.h"
+#include "pk_device.cuh"
+
+namespace {
+
+__device__ int g_cache_e4m3_error;
+
+struct RowParams {
+  const void *k, *v;           // [T, Hk, d] rows of token i at i * stride elements
+  int64_t k_stride, v_stride;
+  void *k_out, *v_out;         // read back: [T, Hk, d]
+  const int64_t *slots;        // [T]
+  uint8_t *k_cache, *v_cache;  // [N, B, Hk, d]
+  uint8_t *kv_exp;             // [N, Hk, B, 2]
+  int64_t num_slots;
+  int32_t num_tokens, hk, d, block_size;
+};
+
+// LANES lanes of 16 elements hold one row; a token's rows are its Hk keys,
+// then its Hk values.
+template <int LANES>
+__device__ __forceinline__ bool row_of(const RowParams &p, int64_t &tok, int &h, bool &is_v,
+                                       int &e0, int64_t &slot) {
+  const int64_t unit = int64_t(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
+  tok = unit / (2 * p.hk);
+  const int j = int(unit % (2 * p.hk));
+  is_v = j >= p.hk;
+  h = is_v ? j - p.hk : j;
+  e0 = (threadIdx.x % LANES) * 16;
+  slot = -1;
+  if (tok >= p.num_tokens) return false;
+  slot = __ldg(p.slots + tok);
+  if (slot >= p.num_slots) {
+    if (e0 == 0 && j == 0) pk::record_error(&g_cache_e4m3_error, PK_DEVERR_SLOT, tok);
+    slot = -1;
+  }
+  return slot >= 0 && e0 < p.d;
+}
+
+__device__ __forceinline__ uint8_t *exp_of(const RowParams &p, int64_t slot, int h, bool is_v) {
+  const int64_t block = slot / p.block_size, at = slot % p.block_size;
+  return p.kv_exp + ((block * p.hk + h) * p.block_size + at) * 2 + (is_v ? 1 : 0);
+}
+
+template <typename T, int LANES>
+__global__ void __launch_bounds__(256) quantize_kernel(RowParams p) {
+  int64_t tok, slot;
+  int h, e0;
+  bool is_v;
+  const bool on = row_of<LANES>(p, tok, h, is_v, e0, slot);
+  float x[2][8] = {};
+  if (on) {
+    const T *src = static_cast<const T *>(is_v ? p.v : p.k) + tok * (is_v ? p.v_stride : p.k_stride) +
+                   int64_t(h) * p.d + e0;
+    pk::load8(src, x[0]);
+    pk::load8(src + 8, x[1]);
+  }
+  // The largest finite magnitude as its bits (their order is the values').
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t b = __float_as_uint(x[i >> 3][i & 7]) & 0x7fffffffu;
+    top = max(top, b < 0x7f800000u ? b : 0u);
+  }
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (!on) return;
+  // With top = f * 2^E, 1 <= f < 2: e = E - 8 where f <= 1.75 = 448 / 256, else
+  // E - 7. Adding 0x1fffff carries into the exponent exactly where f > 1.75.
+  int e = int((top + 0x1fffffu) >> 23) - 127 - 8;
+  e = top == 0 ? 0 : max(e, -100);
+  const float s = __uint_as_float(uint32_t(127 - e) << 23);  // 2^-e: e is in [-100, 120]
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t c = 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int at = 4 * i + 2 * j;
+      float a = x[at >> 3][at & 7], b = x[(at + 1) >> 3][(at + 1) & 7];
+      // Infinities become the NaN code too: the conversion would saturate them.
+      a = fabsf(a) <= 3.402823466e38f ? a * s : __uint_as_float(0x7fc00000u);
+      b = fabsf(b) <= 3.402823466e38f ? b * s : __uint_as_float(0x7fc00000u);
+      c |= uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3)) << (16 * j);
+    }
+    w[i] = c;
+  }
+  *reinterpret_cast<uint4 *>((is_v ? p.v_cache : p.k_cache) + (slot * p.hk + h) * p.d + e0) =
+      make_uint4(w[0], w[1], w[2], w[3]);
+  if (e0 == 0) *exp_of(p, slot, h, is_v) = uint8_t(e + 127);
+}
+
+template <typename T, int LANES>
+__global__ void __launch_bounds__(256) gather_kernel(RowParams p) {
+  int64_t tok, slot;
+  int h, e0;
+  bool is_v;
+  if (!row_of<LANES>(p, tok, h, is_v, e0, slot)) return;
+  const uint4 c = __ldg(reinterpret_cast<const uint4 *>((is_v ? p.v_cache : p.k_cache) +
+                                                        (slot * p.hk + h) * p.d + e0));
+  const float s = __uint_as_float(uint32_t(__ldg(exp_of(p, slot, h, is_v))) << 23);
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  T *dst = static_cast<T *>(is_v ? p.v_out : p.k_out) + (tok * p.hk + h) * p.d + e0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t pair = w[2 * i + j / 2] >> (16 * (j & 1));
+      const float2 f = __half22float2(
+          __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(pair & 0xffffu), __NV_E4M3)));
+      x[2 * j] = f.x * s;
+      x[2 * j + 1] = f.y * s;
+    }
+    pk::store8(dst + 8 * i, x);
+  }
+}
+
+// grid.x = pair, grid.y = 0 K codes / 1 V codes / 2 exponents, grid.z = chunk
+// of 16-byte vectors (bytes where the exponents of a block are no multiple).
+__global__ void __launch_bounds__(256) copy_blocks_e4m3_kernel(
+    uint8_t *k_cache, uint8_t *v_cache, uint8_t *kv_exp, const int64_t *__restrict__ pairs,
+    int32_t num_blocks, int64_t code_bytes, int64_t exp_bytes) {
+  const int64_t src = pairs[2 * blockIdx.x], dst = pairs[2 * blockIdx.x + 1];
+  if (src < 0 || src >= num_blocks || dst < 0 || dst >= num_blocks) {
+    if (threadIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+      pk::record_error(&g_cache_e4m3_error, PK_DEVERR_PAIR, blockIdx.x);
+    return;
+  }
+  const int64_t n = blockIdx.y == 2 ? exp_bytes : code_bytes;
+  uint8_t *pool = blockIdx.y == 0 ? k_cache : (blockIdx.y == 1 ? v_cache : kv_exp);
+  const uint8_t *from = pool + src * n;
+  uint8_t *to = pool + dst * n;
+  const int64_t i = int64_t(blockIdx.z) * 256 + threadIdx.x;
+  if (n % 16 == 0) {
+    if (i < n / 16) reinterpret_cast<uint4 *>(to)[i] = reinterpret_cast<const uint4 *>(from)[i];
+  } else {
+    for (int64_t j = 16 * i; j < min(n, 16 * i + 16); ++j) to[j] = from[j];
+  }
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+pk_status check_desc_e4m3(const pk_cache_desc *d) {
+  if (!d || d->num_blocks <= 0 || d->block_size <= 0 || d->num_kv_heads <= 0 || d->head_dim <= 0)
+    return PK_ERR_INVALID_ARG;
+  if (d->dtype != PK_E4M3) return PK_ERR_UNSUPPORTED;
+  if (d->head_dim % 16 != 0 || d->head_dim > 256) return PK_ERR_UNSUPPORTED;
+  if (int64_t(d->num_kv_heads) * d->head_dim > INT32_MAX ||
+      int64_t(d->num_blocks) * d->block_size > INT32_MAX)
+    return PK_ERR_UNSUPPORTED;
+  return PK_OK;
+}
+
+// Calls f with the lanes of a row (4, 8 or 16 of 16 elements) and its grid.
+template <typename F>
+pk_status by_lanes(const RowParams &p, F f) {
+  const int64_t units = int64_t(p.num_tokens) * 2 * p.hk;
+  auto go = [&](auto c) {
+    constexpr int L = decltype(c)::value;
+    const int64_t ctas = (units + 256 / L - 1) / (256 / L);
+    if (ctas > INT32_MAX) return PK_ERR_UNSUPPORTED;
+    f(c, unsigned(ctas));
+    return cudaGetLastError() == cudaSuccess ? PK_OK : PK_ERR_CUDA;
+  };
+  if (p.d <= 64) return go(std::integral_constant<int, 4>());
+  if (p.d <= 128) return go(std::integral_constant<int, 8>());
+  return go(std::integral_constant<int, 16>());
+}
+
+}  // namespace
+
+extern "C" int pkx_take_cache_e4m3_error(cudaStream_t stream) {
+  return pk::take_error_word(g_cache_e4m3_error, stream);
+}
+
+extern "C" {
+
+pk_status pk_reshape_and_cache_e4m3(const void *k, const void *v, pk_dtype src_dtype,
+                                    int64_t k_stride, int64_t v_stride,
+                                    const int64_t *slot_mapping, int32_t num_tokens, void *k_cache,
+                                    void *v_cache, uint8_t *kv_exp, const pk_cache_desc *desc,
+                                    void *stream) {
+  pk_status st = check_desc_e4m3(desc);
+  if (st != PK_OK) return st;
+  if (num_tokens < 0) return PK_ERR_INVALID_ARG;
+  if (src_dtype != PK_F32 && src_dtype != PK_BF16) return PK_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return PK_OK;
+  if (!k || !v || !slot_mapping || !k_cache || !v_cache || !kv_exp) return PK_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned16(kv_exp))
+    return PK_ERR_INVALID_ARG;
+  const int64_t row = int64_t(desc->num_kv_heads) * desc->head_dim;
+  const int64_t esz = src_dtype == PK_F32 ? 4 : 2;
+  if (k_stride < row || v_stride < row || k_stride * esz % 16 != 0 || v_stride * esz % 16 != 0)
+    return PK_ERR_INVALID_ARG;
+  RowParams p{};
+  p.k = k;
+  p.v = v;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.slots = slot_mapping;
+  p.k_cache = static_cast<uint8_t *>(k_cache);
+  p.v_cache = static_cast<uint8_t *>(v_cache);
+  p.kv_exp = kv_exp;
+  p.num_slots = int64_t(desc->num_blocks) * desc->block_size;
+  p.num_tokens = num_tokens;
+  p.hk = desc->num_kv_heads;
+  p.d = desc->head_dim;
+  p.block_size = desc->block_size;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return by_lanes(p, [&](auto c, unsigned ctas) {
+    constexpr int L = decltype(c)::value;
+    if (src_dtype == PK_F32)
+      quantize_kernel<float, L><<<ctas, 256, 0, s>>>(p);
+    else
+      quantize_kernel<__nv_bfloat16, L><<<ctas, 256, 0, s>>>(p);
+  });
+}
+
+pk_status pk_gather_cache_e4m3(void *k_out, void *v_out, pk_dtype out_dtype,
+                               const int64_t *slot_mapping, int32_t num_tokens, const void *k_cache,
+                               const void *v_cache, const uint8_t *kv_exp,
+                               const pk_cache_desc *desc, void *stream) {
+  pk_status st = check_desc_e4m3(desc);
+  if (st != PK_OK) return st;
+  if (num_tokens < 0) return PK_ERR_INVALID_ARG;
+  if (out_dtype != PK_F32 && out_dtype != PK_BF16) return PK_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return PK_OK;
+  if (!k_out || !v_out || !slot_mapping || !k_cache || !v_cache || !kv_exp) return PK_ERR_INVALID_ARG;
+  if (!aligned16(k_out) || !aligned16(v_out) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned16(kv_exp))
+    return PK_ERR_INVALID_ARG;
+  RowParams p{};
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.slots = slot_mapping;
+  p.k_cache = static_cast<uint8_t *>(const_cast<void *>(k_cache));
+  p.v_cache = static_cast<uint8_t *>(const_cast<void *>(v_cache));
+  p.kv_exp = const_cast<uint8_t *>(kv_exp);
+  p.num_slots = int64_t(desc->num_blocks) * desc->block_size;
+  p.num_tokens = num_tokens;
+  p.hk = desc->num_kv_heads;
+  p.d = desc->head_dim;
+  p.block_size = desc->block_size;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return by_lanes(p, [&](auto c, unsigned ctas) {
+    constexpr int L = decltype(c)::value;
+    if (out_dtype == PK_F32)
+      gather_kernel<float, L><<<ctas, 256, 0, s>>>(p);
+    else
+      gather_kernel<__nv_bfloat16, L><<<ctas, 256, 0, s>>>(p);
+  });
+}
+
+pk_status pk_copy_blocks_e4m3(void *k_cache, void *v_cache, uint8_t *kv_exp,
+                              const int64_t *src_dst_pairs, int32_t num_pairs,
+                              const pk_cache_desc *desc, void *stream) {
+  pk_status st = check_desc_e4m3(desc);
+  if (st != PK_OK) return st;
+  if (num_pairs < 0) return PK_ERR_INVALID_ARG;
+  if (num_pairs == 0) return PK_OK;
+  if (!k_cache || !v_cache || !kv_exp || !src_dst_pairs) return PK_ERR_INVALID_ARG;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(kv_exp)) return PK_ERR_INVALID_ARG;
+  const int64_t tokens = int64_t(desc->block_size) * desc->num_kv_heads;
+  const int64_t code_bytes = tokens * desc->head_dim, exp_bytes = tokens * 2;
+  const int64_t chunks = (code_bytes / 16 + 255) / 256;
+  if (chunks > 65535) return PK_ERR_UNSUPPORTED;
+  copy_blocks_e4m3_kernel<<<dim3(unsigned(num_pairs), 3, unsigned(chunks)), 256, 0,
+                            static_cast<cudaStream_t>(stream)>>>(
+      static_cast<uint8_t *>(k_cache), static_cast<uint8_t *>(v_cache), kv_exp, src_dst_pairs,
+      desc->num_blocks, code_bytes, exp_bytes);
+  return cudaGetLastError() == cudaSuccess ? PK_OK : PK_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -10,6 +10,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "pagedkv.h"
 #include "pk_device.cuh"
 
@@ -181,6 +183,10 @@ extern "C" int pkx_take_cache_ops_error(cudaStream_t stream) {
 }
 
 extern "C" int pkx_take_attention_error(cudaStream_t stream);
+extern "C" int pkx_take_qk_norm_rope_error(cudaStream_t stream);
+extern "C" int pkx_take_cache_e4m3_error(cudaStream_t stream);
+extern "C" int pkx_take_attention_e4m3_error(cudaStream_t stream);
+extern "C" int pkx_take_tree_attention_error(cudaStream_t stream);
 
 extern "C" {
 
@@ -330,10 +336,15 @@ pk_status pk_swap_blocks(void *k_cache, void *v_cache, void *k_host, void *v_hos
 pk_status pk_get_device_error(int32_t *code_out, void *stream) {
   if (!code_out) return PK_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int a = pkx_take_cache_ops_error(s);
-  const int b = pkx_take_attention_error(s);
-  if (a < 0 || b < 0) return PK_ERR_CUDA;
-  *code_out = a != 0 ? a : b;
+  int first = 0;
+  for (auto take : {pkx_take_cache_ops_error, pkx_take_attention_error, pkx_take_qk_norm_rope_error,
+                    pkx_take_cache_e4m3_error, pkx_take_attention_e4m3_error,
+                    pkx_take_tree_attention_error}) {
+    const int code = take(s);
+    if (code < 0) return PK_ERR_CUDA;
+    if (first == 0) first = code;
+  }
+  *code_out = first;
   return PK_OK;
 }
 
