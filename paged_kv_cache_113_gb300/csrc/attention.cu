@@ -48,7 +48,6 @@
 // planner (pk_attention_plan, pk_attention_work_items) and the launch-order
 // helper.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -61,6 +60,7 @@
 
 #include "pagedkv.h"
 #include "pk_device.cuh"
+#include "pk_tma_host.h"
 
 // The resident-table scatter of cache_ops.cu with separate input and output
 // lengths (library-internal).
@@ -1256,24 +1256,10 @@ int64_t elem_size(pk_dtype t) { return t == PK_F32 ? 4 : (t == PK_BF16 ? 2 : 0);
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  });
-  return fn;
-}
-
 // A [N*B, Hk, D] bf16 view of one pool; each load is a box of B token rows of
 // one head and 64 elements (128 bytes), swizzled 128B in shared memory.
 bool encode_pool_map_uncached(CUtensorMap *map, const void *pool, const pk_cache_desc &d) {
-  auto enc = tensor_map_encoder();
+  auto enc = pk::tensor_map_encoder();
   if (!enc) return false;
   const cuuint64_t dims[3] = {cuuint64_t(d.head_dim), cuuint64_t(d.num_kv_heads),
                               cuuint64_t(d.num_blocks) * cuuint64_t(d.block_size)};

@@ -1,33 +1,442 @@
 // Decode attention over the 8-bit cache (pk_paged_attention_decode_e4m3).
 //
-// With K_t = 2^ek_t kc_t and V_t = 2^ev_t vc_t (e4m3 codes kc, vc):
-//     x_t = scale * 2^ek_t <q, kc_t>
-//     out = sum_t 2^(x_t - m) 2^ev_t vc_t / sum_t 2^(x_t - m)     (x in log2)
-// Bound by memory: a token and KV head cost 2 (d + 1) bytes, half of bf16.
+// With K_t = 2^ek_t kc_t and V_t = 2^ev_t vc_t (e4m3 codes kc, vc), x in log2:
+//     x_t = scale log2(e) 2^ek_t <q, kc_t>
+//     out = sum_t 2^(x_t + ev_t) vc_t / sum_t 2^x_t
+// Bound by memory: a token and KV head cost 2 (d + 1) bytes, half of bf16, for
+// 4 G d operations.
+//
+// One CTA per (KV head, sequence, partition) or work item, 4 consumer warps and
+// a producer warp, as the bf16 kernel: the producer streams each block's codes
+// with TMA tensor loads and its exponents with one bulk copy (a block and head's
+// K and V exponents are contiguous) into a ring of 64-token stages. Consumers
+// widen codes to fp16, where e4m3 is exact, in registers and multiply on the
+// tensor cores (m16n8k16, tokens as M, the group's heads as N); the exponents
+// never touch the codes. K's scale the finished scores. V's join the softmax's
+// exponent: the weight of a token is 2^(x_t + ev_t - m) with m the running
+// maximum of x_t + ev_t, less 10, so that fp16 weights lie in (0, 2^10] and keep
+// their 11 bits down to 2^-24 of the largest; the denominator's terms 2^(x_t -
+// m) stay fp32 and cannot overflow as ev >= -100.
+//
+// Precision: a query head is scaled by the power of two that brings its largest
+// value into [2^14, 2^15), so bf16 queries are exact in fp16 (down to 2^-32 of
+// the largest); bf16 results take weights of one fp16 (2^-11 relative, against
+// 2^-8 of the result's own rounding). fp32 queries and weights are fp16 pairs,
+// hi + lo, good to 2^-22, at twice the tensor work.
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "attn_rows.cuh"
 #include "pagedkv.h"
+#include "pk_tma_host.h"
 
-using namespace pk;
+namespace pk {
 
 extern "C" int pkx_take_attention_e4m3_error(cudaStream_t stream) {
   return take_error_word(g_rows_error, stream);
 }
 
-extern "C" int pkx_e4m3_resident_ctas(int, int) { return 3; }
-
 namespace {
 
+constexpr int kWarps = 4;             // consumer warps, 16 tokens each per stage
+constexpr int kTps = 16 * kWarps;     // tokens per stage
+constexpr float kHeadroom = 10.0f;    // log2 of the largest fp16 weight
+
+template <int D, int BS>
+struct Shape {
+  static constexpr int STAGES = 4;
+  static constexpr int BPS = kTps / BS;         // blocks per stage
+  static constexpr int KV_BYTES = kTps * D;     // the stage's K, and its V
+  static constexpr int STAGE_BYTES = 2 * KV_BYTES;
+  static constexpr int EXP_BYTES = kTps * 2;
+  static constexpr int KC = D / 32;             // 32-byte steps of a row
+  static constexpr int OUT_STRIDE = D + 4;      // padded row of the warps' merge
+  static constexpr int MERGE_BYTES = kWarps * 8 * (OUT_STRIDE + 2) * 4;
+  static constexpr int RING_BYTES = STAGES * (STAGE_BYTES + EXP_BYTES);
+  static constexpr int SMEM_BYTES =
+      1024 + 16 * STAGES + (RING_BYTES > MERGE_BYTES ? RING_BYTES : MERGE_BYTES);
+  static_assert(32 % BPS == 0, "a stage's blocks lie in one chunk of 32 table entries");
+};
+
+// Byte offset of 16-byte chunk c of row r in a TMA tile of D-byte rows (128- or
+// 64-byte swizzle).
+template <int D>
+__device__ __forceinline__ int swizzled(int r, int c) {
+  return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// Whether the codes of row r of a tile are all zeros.
+template <int D>
+__device__ __forceinline__ bool zero_row(uint32_t base, int r) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) {
+    uint32_t x, y, z, w;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x), "=r"(y), "=r"(z), "=r"(w)
+                 : "r"(base + r * D + c * 16));
+    any |= x | y | z | w;
+  }
+  return (any & 0x7f7f7f7fu) == 0;
+}
+
+// 2^e as a float, e in [-126, 127].
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
+
+template <typename IO, int D, int BS>
+__global__ void __launch_bounds__((kWarps + 1) * 32, 3)
+    attn_e4m3_kernel(RowsParams p, const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap) {
+  using S = Shape<D, BS>;
+  constexpr int STAGES = S::STAGES, KC = S::KC;
+  constexpr int QW = sizeof(IO) == 4 ? 2 : 1;   // fp16 parts of a query and of a weight
+  launch_dependents();  // the merge may be scheduled as this grid drains
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t stages = (raw + 1023u) & ~1023u;
+  const uint32_t exps = stages + STAGES * S::STAGE_BYTES;
+  __shared__ __align__(8) uint64_t bars[2 * STAGES];
+  auto full_bar = [&](int i) { return smem_addr(bars + i); };
+  auto empty_bar = [&](int i) { return smem_addr(bars + STAGES + i); };
+
+  const int kvh = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool record = kvh == 0 && threadIdx.x == 0;
+  int s, part;
+  if (!work_item(p, blockIdx.y, gridDim.z - 1 - blockIdx.z, record, s, part)) return;
+  const SeqRows sr = seq_rows(p, s, record && part == 0);
+  const int G = p.group;
+  const size_t row0 = size_t(s) * p.num_q_heads + kvh * G;  // the group's first row of q and out
+  if (sr.ctx == 0) {  // invalid length (recorded): a zero row, nothing to merge
+    if (part == 0)
+      for (int i = threadIdx.x; i < G * D; i += blockDim.x)
+        store_elem(static_cast<IO *>(p.out) + row0 * D + i, 0.0f);
+    return;
+  }
+  if (part >= sr.np) return;
+  const int start = part * p.partition, end = min(sr.ctx, start + p.partition);
+  const int nst = (end - start + kTps - 1) / kTps;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(full_bar(i), 1);
+      mbar_init(empty_bar(i), kWarps);
+    }
+    fence_barrier_init();
+  }
+  __syncthreads();
+
+  if (warp == kWarps) {
+    // ---------------- producer warp ----------------
+    if (lane == 0) {
+      prefetch_tensormap(&kmap);
+      prefetch_tensormap(&vmap);
+    }
+    // Table entries are read ahead in chunks of 32, one per lane, one chunk in
+    // reserve, so that no stage waits on a dependent load.
+    const int32_t *trow = p.tables + size_t(s) * p.max_blocks + start / BS;
+    const int nb = (end - start + BS - 1) / BS;
+    int cur = lane < nb ? __ldg(trow + lane) : 0;
+    int nxt = 32 + lane < nb ? __ldg(trow + 32 + lane) : 0;
+    int chunk = 0, issued = 0;
+    for (int st = 0; st < nst; ++st) {
+      const int slot = st % STAGES, b0 = st * S::BPS;
+      if (b0 >= 32 * (chunk + 1)) {
+        ++chunk;
+        cur = nxt;
+        const int j = 32 * (chunk + 1) + lane;
+        nxt = j < nb ? __ldg(trow + j) : 0;
+      }
+      int phys = __shfl_sync(0xffffffffu, cur, (b0 & 31) + min(lane, S::BPS - 1));
+      if (st >= STAGES && !mbar_wait(empty_bar(slot), ((st / STAGES) - 1) & 1)) {
+        if (lane == 0) record_error(&g_rows_error, PK_DEVERR_TIMEOUT, s);
+        break;
+      }
+      const int nblk = min(S::BPS, nb - b0);
+      if (lane == 0) mbar_arrive_expect_tx(full_bar(slot), uint32_t(nblk * BS * (2 * D + 2)));
+      __syncwarp();
+      if (lane < nblk) {
+        if (phys < 0 || phys >= p.num_blocks) {
+          record_error(&g_rows_error, PK_DEVERR_BLOCK_ID, s);
+          phys = 0;  // stay in bounds and keep the byte count; the result is flagged
+        }
+        const uint32_t dst = stages + slot * S::STAGE_BYTES + lane * BS * D;
+        tma_load_3d(dst, &kmap, full_bar(slot), 0, kvh, phys * BS);
+        tma_load_3d(dst + S::KV_BYTES, &vmap, full_bar(slot), 0, kvh, phys * BS);
+        bulk_load(exps + slot * S::EXP_BYTES + lane * BS * 2,
+                  p.kv_exp + (size_t(phys) * p.num_kv_heads + kvh) * BS * 2, BS * 2, full_bar(slot));
+      }
+      issued = st + 1;
+    }
+    // Let every issued copy land before the warp leaves.
+    if (lane == 0)
+      for (int st = max(0, issued - STAGES); st < issued; ++st)
+        mbar_wait(full_bar(st % STAGES), (st / STAGES) & 1);
+    return;
+  }
+
+  // ---------------- consumer warps ----------------
+  // C fragments: a lane holds tokens rw and rw + 8 (or d rows), heads 2 qd and
+  // 2 qd + 1. A key row's 32-byte step comes as four bytes 4 qd .. 4 qd + 3 per
+  // lane and 16-byte chunk; the product's k index follows that order, and so
+  // does the query operand.
+  const int qd = lane & 3, rw = lane >> 2;
+  const int mi = lane >> 3, r8 = lane & 7;
+  uint32_t qb[QW][KC][4];
+  float sl0, sl1;  // scale log2(e) and the query scaling undone, heads 2 qd and 2 qd + 1
+  {
+    float qv[KC][8];
+    uint32_t top = 0;
+    const IO *qrow = static_cast<const IO *>(p.q) + (row0 + min(rw, G - 1)) * D;
+#pragma unroll
+    for (int c = 0; c < KC; ++c)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 x = load4(qrow + 32 * c + 16 * h + 4 * qd);
+        qv[c][4 * h] = x.x, qv[c][4 * h + 1] = x.y, qv[c][4 * h + 2] = x.z, qv[c][4 * h + 3] = x.w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t b = __float_as_uint(qv[c][4 * h + i]) & 0x7fffffffu;
+          top = max(top, b < 0x7f800000u ? b : 0u);
+        }
+      }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int up = min(126, 14 - (int(top >> 23) - 127));  // >= -113
+    const float f = pow2(up);
+    const float sl = p.scale_log2 * pow2(-up);
+    sl0 = __shfl_sync(0xffffffffu, sl, 8 * qd);
+    sl1 = __shfl_sync(0xffffffffu, sl, 8 * qd + 4);
+#pragma unroll
+    for (int c = 0; c < KC; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = rw < G ? qv[c][2 * i] * f : 0.0f, b = rw < G ? qv[c][2 * i + 1] * f : 0.0f;
+        qb[0][c][i] = pack_f16x2(a, b);
+        if (QW == 2) {
+          const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&qb[0][c][i]));
+          qb[QW - 1][c][i] = pack_f16x2(a - hi.x, b - hi.y);
+        }
+      }
+  }
+  float o[KC][2][4];  // [32-column step][even, odd column]
+#pragma unroll
+  for (int c = 0; c < KC; ++c)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) o[c][h][0] = o[c][h][1] = o[c][h][2] = o[c][h][3] = 0.0f;
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+  const int t0 = warp * 16;
+
+  for (int st = 0; st < nst; ++st) {
+    const int slot = st % STAGES;
+    if (!mbar_wait(full_bar(slot), (st / STAGES) & 1)) {
+      if (lane == 0) record_error(&g_rows_error, PK_DEVERR_TIMEOUT, s);
+      break;
+    }
+    const uint32_t kbase = stages + slot * S::STAGE_BYTES, vbase = kbase + S::KV_BYTES;
+    const int nvalid = end - (start + st * kTps + t0);
+    if (nvalid > 0) {
+      if (nvalid < 16) {
+        // Rows past the end may hold anything: zero values, so that a zero
+        // weight never meets a NaN.
+        for (int i = lane; i < (16 - nvalid) * (D / 16); i += 32) {
+          const uint32_t a = vbase + (t0 + nvalid + i / (D / 16)) * D + (i % (D / 16)) * 16;
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+        }
+        __syncwarp();
+      }
+      uint32_t e0, e1;  // exponents of tokens rw, rw + 8: K in the low byte, V above
+      {
+        const uint32_t a = exps + slot * S::EXP_BYTES + (t0 + rw) * 2;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=r"(e0) : "r"(a));
+        asm volatile("ld.shared.u16 %0, [%1];" : "=r"(e1) : "r"(a + 16));
+      }
+      // S^T = K_tile Q^T; low 16 bits and high 16 bits of a lane's four bytes
+      // are the two k halves of one product.
+      float sa[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        uint32_t r[4];
+        ldmatrix_x4(kbase + swizzled<D>(t0 + (mi & 1) * 8 + r8, 2 * c + (mi >> 1)), r[0], r[1], r[2], r[3]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t a0 = e4m3x2_to_f16x2(r[2 * h]), a2 = e4m3x2_to_f16x2(r[2 * h] >> 16);
+          const uint32_t a1 = e4m3x2_to_f16x2(r[2 * h + 1]), a3 = e4m3x2_to_f16x2(r[2 * h + 1] >> 16);
+#pragma unroll
+          for (int w = 0; w < QW; ++w)
+            mma_f16_16816(sa[h], a0, a1, a2, a3, qb[w][c][2 * h], qb[w][c][2 * h + 1]);
+        }
+      }
+      const float k0 = __uint_as_float((e0 & 0xffu) << 23), k1 = __uint_as_float((e1 & 0xffu) << 23);
+      // A row of zeros is written with exponent 0, which says nothing of its
+      // neighbours: it counts as the smallest, or it would push the weights of
+      // far smaller values out of fp16's range.
+      int ev0 = int(e0 >> 8) - 127, ev1 = int(e1 >> 8) - 127;
+      if (__any_sync(0xffffffffu, ev0 == 0 || ev1 == 0)) {
+        if (zero_row<D>(vbase, t0 + rw)) ev0 = -100;
+        if (zero_row<D>(vbase, t0 + rw + 8)) ev1 = -100;
+      }
+      const float v0 = float(ev0), v1 = float(ev1);
+      float x0 = (sa[0][0] + sa[1][0]) * sl0 * k0, x1 = (sa[0][1] + sa[1][1]) * sl1 * k0;
+      float x2 = (sa[0][2] + sa[1][2]) * sl0 * k1, x3 = (sa[0][3] + sa[1][3]) * sl1 * k1;
+      if (rw >= nvalid) x0 = x1 = -INFINITY;
+      if (rw + 8 >= nvalid) x2 = x3 = -INFINITY;
+      float z0 = fmaxf(x0 + v0, x2 + v1), z1 = fmaxf(x1 + v0, x3 + v1);
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        z0 = fmaxf(z0, __shfl_xor_sync(0xffffffffu, z0, off));
+        z1 = fmaxf(z1, __shfl_xor_sync(0xffffffffu, z1, off));
+      }
+      const float n0 = fmaxf(m0, z0 - kHeadroom), n1 = fmaxf(m1, z1 - kHeadroom);
+      const float c0 = exp2_ftz(m0 - n0), c1 = exp2_ftz(m1 - n1);
+      m0 = n0;
+      m1 = n1;
+      const float y0 = x0 - n0, y1 = x1 - n1, y2 = x2 - n0, y3 = x3 - n1;
+      l0 = fmaf(l0, c0, exp2_ftz(y0) + exp2_ftz(y2));
+      l1 = fmaf(l1, c1, exp2_ftz(y1) + exp2_ftz(y3));
+      const float p0 = exp2_ftz(y0 + v0), p1 = exp2_ftz(y1 + v0);
+      const float p2 = exp2_ftz(y2 + v1), p3 = exp2_ftz(y3 + v1);
+      uint32_t b[QW][2];  // P^T as the B operand: the C fragments transposed
+      {
+        const uint32_t w0 = pack_f16x2(p0, p1), w1 = pack_f16x2(p2, p3);
+        b[0][0] = movmatrix_trans(w0);
+        b[0][1] = movmatrix_trans(w1);
+        if (QW == 2) {
+          const float2 h0 = __half22float2(*reinterpret_cast<const __half2 *>(&w0));
+          const float2 h1 = __half22float2(*reinterpret_cast<const __half2 *>(&w1));
+          b[QW - 1][0] = movmatrix_trans(pack_f16x2(p0 - h0.x, p1 - h0.y));
+          b[QW - 1][1] = movmatrix_trans(pack_f16x2(p2 - h1.x, p3 - h1.y));
+        }
+      }
+      if (__any_sync(0xffffffffu, c0 != 1.0f || c1 != 1.0f)) {
+#pragma unroll
+        for (int c = 0; c < KC; ++c)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            o[c][h][0] *= c0;
+            o[c][h][1] *= c1;
+            o[c][h][2] *= c0;
+            o[c][h][3] *= c1;
+          }
+      }
+      // O^T += V^T P^T. A transposed load pairs two columns of one token; the
+      // byte permutation pairs two tokens of one column instead, even columns
+      // low and odd ones high.
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        uint32_t r[4];
+        ldmatrix_x4_trans(vbase + swizzled<D>(t0 + (mi >> 1) * 8 + r8, 2 * c + (mi & 1)), r[0], r[1], r[2], r[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = __byte_perm(r[i], 0, 0x3120);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t a0 = e4m3x2_to_f16x2(r[0] >> (16 * h)), a1 = e4m3x2_to_f16x2(r[1] >> (16 * h));
+          const uint32_t a2 = e4m3x2_to_f16x2(r[2] >> (16 * h)), a3 = e4m3x2_to_f16x2(r[3] >> (16 * h));
+#pragma unroll
+          for (int w = 0; w < QW; ++w) mma_f16_16816(o[c][h], a0, a1, a2, a3, b[w][0], b[w][1]);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty_bar(slot));
+  }
+
+  // The denominators of a warp's 16 tokens lie in the 8 lanes of a quad index.
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) {
+    l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+  }
+  // Merge the consumer warps' states in shared memory (the ring is free: every
+  // copy has landed and been consumed).
+  named_barrier(1, kWarps * 32);
+  float *sm_o = reinterpret_cast<float *>(smem_raw + (stages - raw));
+  float *sm_m = sm_o + kWarps * 8 * S::OUT_STRIDE, *sm_l = sm_m + kWarps * 8;
+#pragma unroll
+  for (int c = 0; c < KC; ++c)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float *base = sm_o + (warp * 8 + 2 * qd) * S::OUT_STRIDE + 32 * c + 2 * rw + h;
+      base[0] = o[c][h][0];
+      base[S::OUT_STRIDE] = o[c][h][1];
+      base[16] = o[c][h][2];
+      base[S::OUT_STRIDE + 16] = o[c][h][3];
+    }
+  if (rw == 0) {
+    sm_m[warp * 8 + 2 * qd] = m0;
+    sm_m[warp * 8 + 2 * qd + 1] = m1;
+    sm_l[warp * 8 + 2 * qd] = l0;
+    sm_l[warp * 8 + 2 * qd + 1] = l1;
+  }
+  named_barrier(1, kWarps * 32);
+  for (int i = threadIdx.x; i < G * D; i += kWarps * 32) {
+    const int g = i / D, col = i % D;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w * 8 + g]);
+    float L = 0.0f, O = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = exp2_ftz(sm_m[w * 8 + g] - M);  // 0 for a warp that saw no token
+      L = fmaf(sm_l[w * 8 + g], f, L);
+      O = fmaf(sm_o[(w * 8 + g) * S::OUT_STRIDE + col], f, O);
+    }
+    if (sr.np == 1) {
+      store_elem(static_cast<IO *>(p.out) + (row0 + g) * D + col, O / L);
+    } else {
+      const size_t slot = (row0 + g) * p.num_partitions + part;
+      p.ws_acc[slot * D + col] = O;
+      if (col == 0) {
+        p.ws_m[slot] = M;
+        p.ws_l[slot] = L;
+      }
+    }
+  }
+}
+
+// The codes of a pool, [N * B, Hk, D] bytes; a load is one head's rows of a block.
+template <int D>
+bool encode_codes(CUtensorMap *map, const void *pool, const pk_cache_desc &d) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(d.num_kv_heads),
+                              cuuint64_t(d.num_blocks) * cuuint64_t(d.block_size)};
+  const cuuint64_t strides[2] = {cuuint64_t(D), cuuint64_t(D) * cuuint64_t(d.num_kv_heads)};
+  const cuuint32_t box[3] = {D, 1, cuuint32_t(d.block_size)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(pool), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE,
+             D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename IO, int D, int BS>
+pk_status launch(const RowsParams &p, const pk_cache_desc &d, cudaStream_t stream) {
+  using S = Shape<D, BS>;
+  CUtensorMap kmap, vmap;
+  if (!encode_codes<D>(&kmap, p.k_cache, d) || !encode_codes<D>(&vmap, p.v_cache, d)) return PK_ERR_CUDA;
+  auto kern = attn_e4m3_kernel<IO, D, BS>;
+  static std::atomic<uint64_t> ready{0};
+  if (!smem_ready(kern, S::SMEM_BYTES, ready)) return PK_ERR_CUDA;
+  kern<<<rows_grid(p), (kWarps + 1) * 32, S::SMEM_BYTES, stream>>>(p, kmap, vmap);
+  return cudaGetLastError() == cudaSuccess ? PK_OK : PK_ERR_CUDA;
+}
+
 template <typename IO, int D>
-pk_status run(const RowsParams &p, cudaStream_t stream) {
-  pk_status st = launch_rows<E4M3, IO, D, 1>(p, stream);
+pk_status run(const RowsParams &p, const pk_cache_desc &d, cudaStream_t stream) {
+  const pk_status st = d.block_size == 8    ? launch<IO, D, 8>(p, d, stream)
+                       : d.block_size == 16 ? launch<IO, D, 16>(p, d, stream)
+                                            : launch<IO, D, 32>(p, d, stream);
   if (st != PK_OK || p.num_partitions == 1) return st;
   return launch_rows_merge<IO, D>(p, stream);
 }
 
 }  // namespace
+
+// The launch bounds ask for 3, and the shared memory allows them (head_dim 128:
+// 3 x 67 KB); the planner fills that many.
+extern "C" int pkx_e4m3_resident_ctas(int, int) { return 3; }
 
 extern "C" pk_status pk_paged_attention_decode_e4m3(
     void *out, const void *q, pk_dtype io_dtype, const void *k_cache, const void *v_cache,
@@ -52,6 +461,9 @@ extern "C" pk_status pk_paged_attention_decode_e4m3(
   if (st != PK_OK) return st;
   p.kv_exp = kv_exp;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (io_dtype == PK_F32) return desc->head_dim == 128 ? run<float, 128>(p, s) : run<float, 64>(p, s);
-  return desc->head_dim == 128 ? run<__nv_bfloat16, 128>(p, s) : run<__nv_bfloat16, 64>(p, s);
+  if (io_dtype == PK_F32) return desc->head_dim == 128 ? run<float, 128>(p, *desc, s) : run<float, 64>(p, *desc, s);
+  return desc->head_dim == 128 ? run<__nv_bfloat16, 128>(p, *desc, s)
+                               : run<__nv_bfloat16, 64>(p, *desc, s);
 }
+
+}  // namespace pk

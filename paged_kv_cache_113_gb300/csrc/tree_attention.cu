@@ -8,7 +8,7 @@
 #include "attn_rows.cuh"
 #include "pagedkv.h"
 
-using namespace pk;
+namespace pk {
 
 extern "C" int pkx_take_tree_attention_error(cudaStream_t stream) {
   return take_error_word(g_rows_error, stream);
@@ -141,3 +141,5 @@ pk_status pk_paged_attention_tree(void *out, const void *q, const void *k_cache,
 }
 
 }  // extern "C"
+
+}  // namespace pk
