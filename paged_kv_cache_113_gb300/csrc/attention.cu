@@ -1256,22 +1256,6 @@ int64_t elem_size(pk_dtype t) { return t == PK_F32 ? 4 : (t == PK_BF16 ? 2 : 0);
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// A [N*B, Hk, D] bf16 view of one pool; each load is a box of B token rows of
-// one head and 64 elements (128 bytes), swizzled 128B in shared memory.
-bool encode_pool_map_uncached(CUtensorMap *map, const void *pool, const pk_cache_desc &d) {
-  auto enc = pk::tensor_map_encoder();
-  if (!enc) return false;
-  const cuuint64_t dims[3] = {cuuint64_t(d.head_dim), cuuint64_t(d.num_kv_heads),
-                              cuuint64_t(d.num_blocks) * cuuint64_t(d.block_size)};
-  const cuuint64_t strides[2] = {cuuint64_t(d.head_dim) * 2,
-                                 cuuint64_t(d.num_kv_heads) * cuuint64_t(d.head_dim) * 2};
-  const cuuint32_t box[3] = {64, 1, cuuint32_t(d.block_size)};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(pool), dims, strides,
-             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Opts the tensor-core kernel into its dynamic shared memory (once).
 // The pool's tensor map (boxes of 64 columns x 1 head x one block), encoded
 // once per (pool address, geometry): a decode loop launches on the same two
@@ -1300,7 +1284,7 @@ bool encode_pool_map(CUtensorMap *map, const void *pool, const pk_cache_desc &d)
         return true;
       }
   }
-  if (!encode_pool_map_uncached(map, pool, d)) return false;
+  if (!pk::encode_bf16_pool(map, pool, d)) return false;
   std::lock_guard<std::mutex> lock(mu);
   Entry &e = cache[next];
   e.pool = pool;
