@@ -70,17 +70,22 @@ __global__ void __launch_bounds__(kThreads, 2)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t q_sm = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t k_sm = q_sm + S::Q_BYTES, v_sm = k_sm + STAGES * S::KV_BYTES;
-  __shared__ __align__(8) uint64_t bars[6 + 4 * STAGES];
+  __shared__ __align__(8) uint64_t bars[7 + 4 * STAGES];
   __shared__ uint32_t tmem_slot;
   __shared__ int poisoned;
   auto bar = [&](int i) { return smem_addr(bars + i); };
-  const uint32_t q_ready = bar(0), o_done = bar(1);
-  auto s_full = [&](int i) { return bar(2 + i); };
-  auto p_full = [&](int i) { return bar(4 + i); };
-  auto k_full = [&](int i) { return bar(6 + i); };
-  auto k_empty = [&](int i) { return bar(6 + STAGES + i); };
-  auto v_full = [&](int i) { return bar(6 + 2 * STAGES + i); };
-  auto v_empty = [&](int i) { return bar(6 + 3 * STAGES + i); };
+  // Every wait names a phase of which the one before has ended for certain and
+  // the one after cannot: a wait by parity tells neighbouring phases apart, not
+  // more. So the products' ends alternate between two barriers: when tile j's
+  // scores are there, product j - 2 has ended, but j - 1 may not have.
+  const uint32_t q_ready = bar(0);
+  auto s_full = [&](int i) { return bar(1 + i); };
+  auto p_full = [&](int i) { return bar(3 + i); };
+  auto o_done = [&](int i) { return bar(5 + i); };  // product i, i + 2, ... has ended
+  auto k_full = [&](int i) { return bar(7 + i); };
+  auto k_empty = [&](int i) { return bar(7 + STAGES + i); };
+  auto v_full = [&](int i) { return bar(7 + 2 * STAGES + i); };
+  auto v_empty = [&](int i) { return bar(7 + 3 * STAGES + i); };
 
   const int kvh = blockIdx.x / p.row_tiles, tile = blockIdx.x % p.row_tiles;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -108,8 +113,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   if (threadIdx.x == 0) {
     mbar_init(q_ready, 128);
-    mbar_init(o_done, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(o_done(i), 1);
       mbar_init(s_full(i), 1);
       mbar_init(p_full(i), active);
     }
@@ -204,13 +209,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                       smem_desc(v_sm + slot * S::KV_BYTES + ks * 2048, S::KV_SLAB, 1024), O_DESC,
                       j > 0 || part > 0 || ks > 0);
         tc_commit(v_empty(slot));
-        tc_commit(o_done);
+        tc_commit(o_done(j & 1));
         issued = j + 1;
       };
       for (int j = 0; j < nt && ok; ++j) {
         const int slot = j % STAGES;
         // The score tile holds the weights of tile j - 2 until their product ends.
-        ok = mbar_wait(k_full(slot), (j / STAGES) & 1) && (j < 2 || mbar_wait(o_done, j & 1));
+        ok = mbar_wait(k_full(slot), (j / STAGES) & 1) && (j < 2 || mbar_wait(o_done(j & 1), ((j >> 1) - 1) & 1));
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
@@ -225,17 +230,21 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (ok) pv(nt - 1);
       if (!ok) timeout();
       // Nothing of the tensor cores' is under way when tensor memory is freed.
-      if (issued > 0) mbar_wait(o_done, (issued - 1) & 1);
+      for (int j = max(0, issued - 2); j < issued; ++j) mbar_wait(o_done(j & 1), (j >> 1) & 1);
     }
     __syncwarp();
   } else {
     // ---------------- softmax: a thread is a row ----------------
     const int r = threadIdx.x;
+    // A negative scale turns the queries' signs, so that scores order as the
+    // products do.
+    const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
     for (int i = r; i < kRows * (D / 8); i += 128) {
       const int row = i / (D / 8), c = i % (D / 8);
       uint4 x = make_uint4(0, 0, 0, 0);
       if (row < rows)
         x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + q_row(row) + c * 8));
+      x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
       const uint32_t a = q_sm + (c >> 3) * S::Q_SLAB + row * 128 + (((c & 7) ^ (row & 7)) << 4);
       asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
                    : "memory");
@@ -245,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp < active) {
       const uint32_t lane_base = uint32_t(warp * 32) << 16;
       const uint64_t mask = r < rows ? draft_mask(p, sr.q0, (r0 + r) / G, sr.n) : 0;
-      const float sl = p.scale_log2;
+      const float sl = fabsf(p.scale_log2);
       float ref = -INFINITY, l = 0.0f;  // the exponent's reference (scaled scores), the sum
       bool ok = true;
       // A wait of the whole warp (which converges on it): tensor memory is
@@ -297,10 +306,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         tmem_wait_load(x[0]);
         tmem_wait_load(x[1]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[h][i] = __float_as_uint(__uint_as_float(x[h][i]) * sl);
         if (careful) {
           const uint64_t see = see64(mask, base, t0);
 #pragma unroll
@@ -313,17 +318,22 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
         float mx = -INFINITY;
+        {
+          float part[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(x[h][i]));
+          for (int i = 0; i < 32; ++i)
+            part[i & 3] = max3(part[i & 3], __uint_as_float(x[i >> 4][2 * (i & 15)]),
+                               __uint_as_float(x[i >> 4][2 * (i & 15) + 1]));
+          mx = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])) * sl;
+        }
         const bool move = mx > ref + kSlack;
         if (__any_sync(0xffffffffu, move)) {
           const float f = move ? exp2_ftz(ref - mx) : 1.0f;
           if (move) ref = mx;
+          const uint64_t f2 = pack2(f, f);
           l *= f;
           if (j > 0) {
-            if (!(ok = wait(o_done, (j - 1) & 1))) break;
+            if (!(ok = wait(o_done((j - 1) & 1), ((j - 1) >> 1) & 1))) break;
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
@@ -331,24 +341,39 @@ __global__ void __launch_bounds__(kThreads, 2)
               tmem_load32(t_o + lane_base + 32 * c, o);
               tmem_wait_load(o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              for (int i = 0; i < 16; ++i) {
+                float a, b;
+                unpack2(mul2(pack2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), f2), a, b);
+                o[2 * i] = __float_as_uint(a);
+                o[2 * i + 1] = __float_as_uint(b);
+              }
               tmem_store32(t_o + lane_base + 32 * c, o);
             }
           }
         }
         const float m = ref == -INFINITY ? 0.0f : ref;  // nothing seen so far: every weight is 0
-        float sum0 = 0.0f, sum1 = 0.0f;
+        const uint64_t sl2 = pack2(sl, sl), m2 = pack2(-m, -m), minus = pack2(-1.0f, -1.0f);
+        uint64_t sum2 = 0;
         uint32_t hi[32], lo[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const float a = exp2_ftz(__uint_as_float(x[i >> 4][2 * (i & 15)]) - m);
-          const float b = exp2_ftz(__uint_as_float(x[i >> 4][2 * (i & 15) + 1]) - m);
-          sum0 += a;
-          sum1 += b;
+          float a, b;
+          unpack2(fma2(pack2(__uint_as_float(x[i >> 4][2 * (i & 15)]), __uint_as_float(x[i >> 4][2 * (i & 15) + 1])),
+                       sl2, m2),
+                  a, b);
+          a = exp2_ftz(a);
+          b = exp2_ftz(b);
+          const uint64_t ab = pack2(a, b);
+          sum2 = add2(sum2, ab);
           hi[i] = pack_bf16x2(a, b);
-          lo[i] = pack_bf16x2(a - bf16_lo(hi[i]), b - bf16_hi(hi[i]));
+          unpack2(fma2(pack2(bf16_lo(hi[i]), bf16_hi(hi[i])), minus, ab), a, b);
+          lo[i] = pack_bf16x2(a, b);
         }
-        l += sum0 + sum1;
+        {
+          float a, b;
+          unpack2(sum2, a, b);
+          l += a + b;
+        }
         tmem_store32(t_s(j & 1) + lane_base, hi);
         tmem_store32(t_s(j & 1) + lane_base + 32, lo);
         tmem_wait_store();
@@ -356,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full(j & 1));
       }
-      ok = ok && wait(o_done, (nt - 1) & 1);
+      ok = ok && wait(o_done((nt - 1) & 1), ((nt - 1) >> 1) & 1);
       tc_fence_after();
       named_barrier(1, active * 32);  // every warp's part of `poisoned` is in
       if (ok) {

@@ -644,3 +644,25 @@ def test_streams_and_graph_replay():
     vals = [plain.decode_values(codes_of(c), np.moveaxis(ex.cpu().numpy()[..., i], 1, 2)) for i, c in enumerate((k8, v8))]
     want, terms = plain.tree_attention(f64(qd), *vals, tables, lens + 20, 0.09)
     check_attention(f64(o2), want, terms, d, dt, RHO_E4M3[dt])
+
+
+def test_tree_attention_repeats_bit_for_bit():
+    """The same call many times, on one to a few tiles per partition and few
+    rows, gives the same bits: nothing depends on when a product ends."""
+    hq, hk, d, B = 8, 1, 128, 16
+    rng = np.random.default_rng(944)
+    counts = np.array([3, 1, 12, 40], np.int32)
+    lens = np.array([131, 190, 260, 330], np.int32)
+    tables, k, v, ofs, masks, q, mt = tree_case(rng, counts, lens, B, hq, hk, d, torch.bfloat16, "any")
+    for part in (0, 64, 128, 192):
+        ws = torch.empty(max(16, pk.pk_tree_workspace_size(len(q), hq, 330, part, pk.cache_desc(k))),
+                         dtype=torch.uint8, device=DEV)
+        first = None
+        for _ in range(60):
+            out = torch.full_like(q, 5.0)
+            pk.pk_paged_attention_tree(out, q, k, v, i32(tables), i32(lens), i32(ofs), d ** -0.5, 40, 330,
+                                       tree_mask=mt, partition_size=part, workspace=ws)
+            if first is None:
+                first = out
+                check_tree(out, q, k, v, tables, lens, d ** -0.5, ofs, masks, d, torch.bfloat16)
+            assert torch.equal(out, first)
