@@ -26,7 +26,9 @@
 // 2^-9 on every output).
 // 256 columns of tensor memory (two 64-column score tiles, 128 for O) and 97 KB
 // of shared memory let two CTAs share an SM: one's softmax overlaps the
-// other's products.
+// other's products. The CTAs stay: each goes over its share of the (128 rows,
+// partition) units, and the producer runs into the next unit while the softmax
+// warps finish the last, so that short contexts keep memory busy too.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -48,83 +50,83 @@ constexpr int kRows = 128;          // query rows of a CTA
 constexpr int kTile = 64;           // tokens of a tile
 constexpr int kThreads = 192;       // 4 softmax warps, the producer, the product warp
 constexpr uint32_t kTmemCols = 256;
+constexpr uint32_t kNegateA = 1u << 13;  // of an instruction descriptor
 constexpr float kSlack = 8.0f;      // log2 of how far a maximum may outgrow the reference
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess &&
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0)
+    return n;
+  cudaGetLastError();  // clear a failed query on a machine without a GPU
+  return 152;
+}
 
 template <int D, int BS>
 struct TreeShape {
   static constexpr int SLABS = D / 64;               // 128-byte column slabs
   static constexpr int Q_SLAB = kRows * 128, KV_SLAB = kTile * 128;
   static constexpr int Q_BYTES = SLABS * Q_SLAB, KV_BYTES = SLABS * KV_SLAB;
-  static constexpr int STAGES = 2;                   // of the K ring and of the V ring
   static constexpr int BPT = kTile / BS;             // blocks per tile
-  static constexpr int SMEM_BYTES = 1024 + Q_BYTES + 2 * STAGES * KV_BYTES;
+  static constexpr int SMEM_BYTES = 1024 + Q_BYTES + 4 * KV_BYTES;  // Q, two K and two V tiles
+};
+
+// A unit of work: 128 rows of one (sequence, KV head) over one partition.
+struct Unit {
+  int s, kvh, part;
+  int q0, n, ctx, np;  // as SeqRows
+  int r0, rows;        // its rows
+  int start, end, nt;  // its tokens, its tiles (0: the rows are zero); s < 0: no more units
 };
 
 template <int D, int BS>
 __global__ void __launch_bounds__(kThreads, 2)
     attn_tree_kernel(RowsParams p, const __grid_constant__ CUtensorMap kmap,
-                     const __grid_constant__ CUtensorMap vmap) {
+                     const __grid_constant__ CUtensorMap vmap, int num_units) {
   using S = TreeShape<D, BS>;
-  constexpr int STAGES = S::STAGES;
   launch_dependents();  // the merge may be scheduled as this grid drains
   extern __shared__ uint8_t smem_raw[];
   const uint32_t q_sm = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const uint32_t k_sm = q_sm + S::Q_BYTES, v_sm = k_sm + STAGES * S::KV_BYTES;
-  __shared__ __align__(8) uint64_t bars[7 + 4 * STAGES];
+  const uint32_t k_sm = q_sm + S::Q_BYTES, v_sm = k_sm + 2 * S::KV_BYTES;
+  __shared__ __align__(8) uint64_t bars[20];
+  __shared__ Unit units[2];
   __shared__ uint32_t tmem_slot;
-  __shared__ int poisoned;
+  __shared__ int poisoned[2];
   auto bar = [&](int i) { return smem_addr(bars + i); };
-  // Every wait names a phase of which the one before has ended for certain and
-  // the one after cannot: a wait by parity tells neighbouring phases apart, not
-  // more. So the products' ends alternate between two barriers: when tile j's
-  // scores are there, product j - 2 has ended, but j - 1 may not have.
-  const uint32_t q_ready = bar(0);
-  auto s_full = [&](int i) { return bar(1 + i); };
-  auto p_full = [&](int i) { return bar(3 + i); };
-  auto o_done = [&](int i) { return bar(5 + i); };  // product i, i + 2, ... has ended
-  auto k_full = [&](int i) { return bar(7 + i); };
-  auto k_empty = [&](int i) { return bar(7 + STAGES + i); };
-  auto v_full = [&](int i) { return bar(7 + 2 * STAGES + i); };
-  auto v_empty = [&](int i) { return bar(7 + 3 * STAGES + i); };
+  // Tiles t and units i are counted over the whole life of the CTA; what there
+  // are two of alternates. Every wait names a phase of which the one before has
+  // ended for certain and the one after cannot have: a wait by parity tells
+  // neighbouring phases apart, not more. So the products' ends alternate too:
+  // when tile t's scores are there, product t - 2 has ended, t - 1 may not have.
+  const uint32_t q_ready = bar(0), u_done = bar(1);
+  auto s_full = [&](int t) { return bar(2 + (t & 1)); };
+  auto p_full = [&](int t) { return bar(4 + (t & 1)); };
+  auto o_done = [&](int t) { return bar(6 + (t & 1)); };
+  auto k_full = [&](int t) { return bar(8 + (t & 1)); };
+  auto k_empty = [&](int t) { return bar(10 + (t & 1)); };
+  auto v_full = [&](int t) { return bar(12 + (t & 1)); };
+  auto v_empty = [&](int t) { return bar(14 + (t & 1)); };
+  auto u_full = [&](int i) { return bar(16 + (i & 1)); };
+  auto u_empty = [&](int i) { return bar(18 + (i & 1)); };
+  auto phase = [](int t) { return uint32_t(t >> 1) & 1u; };
 
-  const int kvh = blockIdx.x / p.row_tiles, tile = blockIdx.x % p.row_tiles;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool record = blockIdx.x == 0 && threadIdx.x == 0;
-  int s, part;
-  if (!work_item(p, blockIdx.y, gridDim.z - 1 - blockIdx.z, record, s, part)) return;
-  const SeqRows sr = seq_rows(p, s, record && part == 0);
-  const int G = p.group, r0 = tile * kRows, rows = min(kRows, sr.n * G - r0);
-  if (rows <= 0) return;
-  auto q_row = [&](int r) {  // element offset of row r0 + r in q and out
-    return (size_t(sr.q0 + (r0 + r) / G) * p.num_q_heads + kvh * G + (r0 + r) % G) * D;
-  };
-  if (sr.ctx == 0) {  // invalid length (recorded): zero rows
-    if (part == 0)
-      for (int i = threadIdx.x; i < rows * (D / 8); i += kThreads)
-        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + q_row(i / (D / 8)) +
-                                   (i % (D / 8)) * 8) = make_uint4(0, 0, 0, 0);
-    return;
-  }
-  if (part >= sr.np) return;
-  const int start = part * p.partition, end = min(sr.ctx, start + p.partition);
-  const int base = sr.ctx - sr.n;
-  const int nt = (end - start + kTile - 1) / kTile;
-  const int active = (rows + 31) / 32;  // softmax warps with rows
-
+  const int G = p.group;
   if (threadIdx.x == 0) {
     mbar_init(q_ready, 128);
+    mbar_init(u_done, 4);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(o_done(i), 1);
       mbar_init(s_full(i), 1);
-      mbar_init(p_full(i), active);
-    }
-    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(p_full(i), 4);
+      mbar_init(o_done(i), 1);
       mbar_init(k_full(i), 1);
       mbar_init(k_empty(i), 1);
       mbar_init(v_full(i), 1);
       mbar_init(v_empty(i), 1);
+      mbar_init(u_full(i), 1);
+      mbar_init(u_empty(i), 5);  // the softmax warps and the product thread
+      poisoned[i] = 0;
     }
-    poisoned = 0;
     fence_barrier_init();
   }
   if (warp == 5) tmem_alloc(smem_addr(&tmem_slot), kTmemCols);
@@ -132,9 +134,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  const uint32_t t_o = tmem + 128;                       // O: columns 128 .. 128 + D
-  auto t_s = [&](int i) { return tmem + 64u * i; };      // S_i, then P_i: hi 32 columns, lo 32
-  auto timeout = [&] { record_error(&g_rows_error, PK_DEVERR_TIMEOUT, s); };
+  const uint32_t t_o = tmem + 128;                             // O: columns 128 .. 128 + D
+  auto t_s = [&](int t) { return tmem + 64u * uint32_t(t & 1); };  // S_t, then P_t: hi 32 columns, lo 32
+  auto timeout = [&] { record_error(&g_rows_error, PK_DEVERR_TIMEOUT, blockIdx.x); };
 
   if (warp == 4) {
     // ---------------- producer ----------------
@@ -142,148 +144,236 @@ __global__ void __launch_bounds__(kThreads, 2)
       prefetch_tensormap(&kmap);
       prefetch_tensormap(&vmap);
     }
-    const int32_t *trow = p.tables + size_t(s) * p.max_blocks + start / BS;
-    const int nb = (end - start + BS - 1) / BS;
+    // The first unit with work at or after u in this CTA's share.
+    auto find = [&](int &u, Unit &c) {
+      const int X = p.num_kv_heads * p.row_tiles, Y = p.items ? p.num_items : p.num_seqs;
+      for (; u < num_units; u += gridDim.x) {
+        const int x = u % X, y = (u / X) % Y, z = u / X / Y;
+        const bool record = x == 0 && lane == 0;
+        if (!work_item(p, y, p.num_partitions - 1 - z, record, c.s, c.part)) continue;
+        const SeqRows sr = seq_rows(p, c.s, record && c.part == 0);
+        c.kvh = x / p.row_tiles;
+        c.r0 = x % p.row_tiles * kRows;
+        c.rows = min(kRows, sr.n * G - c.r0);
+        if (c.rows <= 0 || (sr.ctx == 0 ? c.part != 0 : c.part >= sr.np)) continue;
+        c.q0 = sr.q0, c.n = sr.n, c.ctx = sr.ctx, c.np = sr.np;
+        c.start = c.part * p.partition;
+        c.end = min(sr.ctx, c.start + p.partition);
+        c.nt = (c.end - c.start + kTile - 1) / kTile;
+        return;
+      }
+      c.s = -1;
+      c.nt = 0;
+    };
     const int mine = min(lane, S::BPT - 1);
-    auto entry = [&](int j) { return j * S::BPT + mine < nb ? __ldg(trow + j * S::BPT + mine) : 0; };
-    // One tile's K (or V) blocks into its ring's slot.
-    auto load = [&](const CUtensorMap *map, uint32_t ring, uint32_t full, int j, int phys) {
-      const int nblk = min(S::BPT, nb - j * S::BPT);
+    auto entry = [&](const Unit &c, int j) {
+      const int b = j * S::BPT + mine;
+      return c.start / BS + b < (c.end + BS - 1) / BS
+                 ? __ldg(p.tables + size_t(c.s) * p.max_blocks + c.start / BS + b)
+                 : 0;
+    };
+    // Tile j of a unit, the CTA's tile t: its K (or V) blocks into their slot.
+    auto load = [&](const CUtensorMap *map, uint32_t ring, uint32_t full, const Unit &c, int j, int t, int phys) {
+      const int nblk = min(S::BPT, (c.end - c.start + BS - 1) / BS - j * S::BPT);
       if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(nblk * S::SLABS * BS * 128));
       __syncwarp();
       if (lane < nblk) {
         if (phys < 0 || phys >= p.num_blocks) {
-          record_error(&g_rows_error, PK_DEVERR_BLOCK_ID, s);
+          record_error(&g_rows_error, PK_DEVERR_BLOCK_ID, c.s);
           phys = 0;  // stay in bounds and keep the byte count; the result is flagged
         }
-        const uint32_t dst = ring + (j % STAGES) * S::KV_BYTES + lane * BS * 128;
+        const uint32_t dst = ring + uint32_t(t & 1) * S::KV_BYTES + lane * BS * 128;
 #pragma unroll
         for (int h = 0; h < S::SLABS; ++h)
-          tma_load_3d(dst + h * S::KV_SLAB, map, full, h * 64, kvh, phys * BS);
+          tma_load_3d(dst + h * S::KV_SLAB, map, full, h * 64, c.kvh, phys * BS);
       }
     };
-    // K runs one tile ahead of V: its slots come free earlier.
-    int cur = entry(0), nxt = entry(1);
-    int kdone = 0, vdone = 0;
-    load(&kmap, k_sm, k_full(0), 0, cur);
-    kdone = 1;
-    for (int j = 0; j < nt; ++j) {
-      const int after = entry(j + 2);
-      if (j + 1 < nt) {
-        const int i = j + 1;
-        if (i >= STAGES && !mbar_wait(k_empty(i % STAGES), ((i / STAGES) - 1) & 1)) {
-          if (lane == 0) timeout();
-          break;
+    Unit cur, nxt;
+    int u = blockIdx.x, kt = 0, vt = 0;  // K and V tiles loaded so far
+    bool ok = true;
+    auto load_k = [&](const Unit &c, int j, int phys) {
+      ok = ok && (kt < 2 || mbar_wait(k_empty(kt), phase(kt - 2)));
+      if (!ok) return;
+      load(&kmap, k_sm, k_full(kt), c, j, kt, phys);
+      ++kt;
+    };
+    find(u, cur);
+    for (int i = 0; ok; ++i) {
+      ok = i < 2 || mbar_wait(u_empty(i), phase(i - 2));
+      if (!ok) break;
+      if (lane == 0) {
+        units[i & 1] = cur;
+        mbar_arrive(u_full(i));
+      }
+      if (cur.s < 0) break;
+      u += gridDim.x;
+      if (cur.nt == 0) {
+        find(u, nxt);
+      } else {
+        // K runs one tile ahead of V, whose slots come free later; the next unit
+        // is looked up while this one's first tiles are under way.
+        int e0 = entry(cur, 0), e1 = entry(cur, 1);
+        load_k(cur, 0, e0);
+        for (int j = 0; j < cur.nt && ok; ++j) {
+          const int e2 = entry(cur, j + 2);
+          if (j + 1 < cur.nt) load_k(cur, j + 1, e1);
+          ok = ok && (vt < 2 || mbar_wait(v_empty(vt), phase(vt - 2)));
+          if (!ok) break;
+          load(&vmap, v_sm, v_full(vt), cur, j, vt, e0);
+          ++vt;
+          e0 = e1;
+          e1 = e2;
+          if (j == 0) find(u, nxt);
         }
-        load(&kmap, k_sm, k_full(i % STAGES), i, nxt);
-        kdone = i + 1;
       }
-      if (j >= STAGES && !mbar_wait(v_empty(j % STAGES), ((j / STAGES) - 1) & 1)) {
-        if (lane == 0) timeout();
-        break;
-      }
-      load(&vmap, v_sm, v_full(j % STAGES), j, cur);
-      vdone = j + 1;
       cur = nxt;
-      nxt = after;
     }
+    if (!ok && lane == 0) timeout();
     // Let every issued copy land before the warp leaves.
-    for (int j = max(0, kdone - STAGES); j < kdone; ++j) mbar_wait(k_full(j % STAGES), (j / STAGES) & 1);
-    for (int j = max(0, vdone - STAGES); j < vdone; ++j) mbar_wait(v_full(j % STAGES), (j / STAGES) & 1);
+    for (int t = max(0, kt - 2); t < kt; ++t) mbar_wait(k_full(t), phase(t));
+    for (int t = max(0, vt - 2); t < vt; ++t) mbar_wait(v_full(t), phase(t));
   } else if (warp == 5) {
     // ---------------- products ----------------
     if (lane == 0) {
-      constexpr uint32_t S_DESC = mma_desc(kRows, kTile, false), O_DESC = mma_desc(kRows, D, true);
-      bool ok = mbar_wait(q_ready, 0);
-      int issued = 0;  // P V products
-      auto pv = [&](int j) {
-        const int slot = j % STAGES;
-        ok = ok && mbar_wait(p_full(j & 1), (j >> 1) & 1) && mbar_wait(v_full(slot), (j / STAGES) & 1);
+      // A negative scale negates the queries, so that scores order as their
+      // exponents do.
+      const uint32_t s_desc = mma_desc(kRows, kTile, false) | (p.scale_log2 < 0.0f ? kNegateA : 0u);
+      constexpr uint32_t O_DESC = mma_desc(kRows, D, true);
+      bool ok = true;
+      int t = 0, issued = 0, qi = 0;  // tiles, P V products, units with tiles
+      auto pv = [&](int w, bool first) {
+        ok = ok && mbar_wait(p_full(w), phase(w)) && mbar_wait(v_full(w), phase(w));
         if (!ok) return;
         tc_fence_after();
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
           for (int ks = 0; ks < kTile / 16; ++ks)
-            tc_mma_ts(t_o, t_s(j & 1) + 32 * part + 8 * ks,
-                      smem_desc(v_sm + slot * S::KV_BYTES + ks * 2048, S::KV_SLAB, 1024), O_DESC,
-                      j > 0 || part > 0 || ks > 0);
-        tc_commit(v_empty(slot));
-        tc_commit(o_done(j & 1));
-        issued = j + 1;
+            tc_mma_ts(t_o, t_s(w) + 32 * half + 8 * ks,
+                      smem_desc(v_sm + uint32_t(w & 1) * S::KV_BYTES + ks * 2048, S::KV_SLAB, 1024), O_DESC,
+                      !first || half > 0 || ks > 0);
+        tc_commit(v_empty(w));
+        tc_commit(o_done(w));
+        issued = w + 1;
       };
-      for (int j = 0; j < nt && ok; ++j) {
-        const int slot = j % STAGES;
-        // The score tile holds the weights of tile j - 2 until their product ends.
-        ok = mbar_wait(k_full(slot), (j / STAGES) & 1) && (j < 2 || mbar_wait(o_done(j & 1), ((j >> 1) - 1) & 1));
+      for (int i = 0; ok; ++i) {
+        ok = mbar_wait(u_full(i), phase(i));
         if (!ok) break;
-        tc_fence_after();
+        const int nt = units[i & 1].nt;
+        const bool last = units[i & 1].s < 0;
+        mbar_arrive(u_empty(i));
+        if (last) break;
+        if (nt == 0) continue;
+        ok = mbar_wait(q_ready, qi & 1);
+        ++qi;
+        for (int j = 0; j < nt && ok; ++j, ++t) {
+          // The score tile holds the weights of tile t - 2 until their product ends.
+          ok = mbar_wait(k_full(t), phase(t)) && (t < 2 || mbar_wait(o_done(t), phase(t - 2)));
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          tc_mma_ss(t_s(j & 1), smem_desc(q_sm + (ks / 4) * S::Q_SLAB + (ks % 4) * 32, 16, 1024),
-                    smem_desc(k_sm + slot * S::KV_BYTES + (ks / 4) * S::KV_SLAB + (ks % 4) * 32, 16, 1024),
-                    S_DESC, ks > 0);
-        tc_commit(k_empty(slot));
-        tc_commit(s_full(j & 1));
-        if (j > 0) pv(j - 1);
+          for (int ks = 0; ks < D / 16; ++ks)
+            tc_mma_ss(t_s(t), smem_desc(q_sm + (ks / 4) * S::Q_SLAB + (ks % 4) * 32, 16, 1024),
+                      smem_desc(k_sm + uint32_t(t & 1) * S::KV_BYTES + (ks / 4) * S::KV_SLAB + (ks % 4) * 32, 16, 1024),
+                      s_desc, ks > 0);
+          tc_commit(k_empty(t));
+          tc_commit(s_full(t));
+          if (j > 0) pv(t - 1, j == 1);
+        }
+        if (ok) pv(t - 1, nt == 1);
       }
-      if (ok) pv(nt - 1);
       if (!ok) timeout();
       // Nothing of the tensor cores' is under way when tensor memory is freed.
-      for (int j = max(0, issued - 2); j < issued; ++j) mbar_wait(o_done(j & 1), (j >> 1) & 1);
+      for (int w = max(0, issued - 2); w < issued; ++w) mbar_wait(o_done(w), phase(w));
     }
     __syncwarp();
   } else {
     // ---------------- softmax: a thread is a row ----------------
     const int r = threadIdx.x;
-    // A negative scale turns the queries' signs, so that scores order as the
-    // products do.
-    const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
-    for (int i = r; i < kRows * (D / 8); i += 128) {
-      const int row = i / (D / 8), c = i % (D / 8);
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (row < rows)
-        x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + q_row(row) + c * 8));
-      x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
-      const uint32_t a = q_sm + (c >> 3) * S::Q_SLAB + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
-                   : "memory");
-    }
-    fence_proxy_async();
-    mbar_arrive(q_ready);
-    if (warp < active) {
-      const uint32_t lane_base = uint32_t(warp * 32) << 16;
-      const uint64_t mask = r < rows ? draft_mask(p, sr.q0, (r0 + r) / G, sr.n) : 0;
-      const float sl = fabsf(p.scale_log2);
-      float ref = -INFINITY, l = 0.0f;  // the exponent's reference (scaled scores), the sum
-      bool ok = true;
-      // A wait of the whole warp (which converges on it): tensor memory is
-      // accessed by whole warps.
-      auto wait = [&](uint32_t b, uint32_t parity) {
-        const bool done = __all_sync(0xffffffffu, mbar_wait(b, parity));
-        if (!done && lane == 0) timeout();
-        return done;
+    const uint32_t lane_base = uint32_t(warp * 32) << 16;
+    const float sl = fabsf(p.scale_log2);
+    // A wait of the whole warp (which converges on it): tensor memory is
+    // accessed by whole warps.
+    bool ok = true;
+    auto wait = [&](uint32_t b, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, mbar_wait(b, parity));
+      return ok;
+    };
+    auto q_row = [&](int q0, int row, int kvh) {  // element offset of a row of q and out
+      return (size_t(q0 + row / G) * p.num_q_heads + kvh * G + row % G) * D;
+    };
+    // A unit's queries into shared memory, rows past the last as zeros.
+    auto load_q = [&](const Unit &c) {
+      for (int i = r; i < kRows * (D / 8); i += 128) {
+        const int row = i / (D / 8), ch = i % (D / 8);
+        const __nv_bfloat16 *src =
+            static_cast<const __nv_bfloat16 *>(p.q) + q_row(c.q0, c.r0 + min(row, c.rows - 1), c.kvh) + ch * 8;
+        cp_async16(q_sm + (ch >> 3) * S::Q_SLAB + row * 128 + (((ch & 7) ^ (row & 7)) << 4), src,
+                   row < c.rows ? 16 : 0);
+      }
+    };
+    auto q_landed = [&] {
+      cp_async_wait();
+      fence_proxy_async();
+      mbar_arrive(q_ready);
+    };
+    bool loaded = false;  // the unit's queries were loaded under the one before
+    for (int i = 0, t = 0, qi = 0; wait(u_full(i), phase(i)); ++i) {
+      const Unit &c = units[i & 1];  // read where it is needed: registers are short
+      auto release = [&] {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(u_empty(i));
       };
-      const int lim = min(base, end);  // tokens before it are seen by every row
-      for (int j = 0; j < nt; ++j) {
+      if (c.s < 0) break;
+      if (c.nt == 0) {  // invalid length (recorded): zero rows
+        if (r < c.rows)
+          for (int e = 0; e < D; e += 8)
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + q_row(c.q0, c.r0 + r, c.kvh) + e) =
+                make_uint4(0, 0, 0, 0);
+        release();
+        continue;
+      }
+      if (!loaded) {
+        load_q(c);
+        q_landed();
+      }
+      loaded = false;
+      const bool busy = warp * 32 < c.rows;  // this warp has rows
+      const int nt = c.nt, start = c.start;
+      const int lim = min(c.ctx - c.n, c.end);  // tokens before it are seen by every row
+      // The drafts that this thread's row sees.
+      auto row_mask = [&] { return r < c.rows ? draft_mask(p, c.q0, (c.r0 + r) / G, c.n) : 0; };
+      float ref = -INFINITY, l = 0.0f;  // the exponent's reference (scaled scores), the sum
+      for (int j = 0; j < nt; ++j, ++t) {
         const int t0 = start + j * kTile;
         const bool careful = t0 + kTile > lim;
-        if (!(ok = wait(s_full(j & 1), (j >> 1) & 1))) break;
+        if (!wait(s_full(t), phase(t))) break;
         tc_fence_after();
         uint32_t x[2][32];
-        tmem_load32(t_s(j & 1) + lane_base, x[0]);
-        tmem_load32(t_s(j & 1) + lane_base + 32, x[1]);
+        if (busy) {
+          tmem_load32(t_s(t) + lane_base, x[0]);
+          tmem_load32(t_s(t) + lane_base + 32, x[1]);
+        }
+        if (j == nt - 1) {
+          // The unit's last scores are there, so its queries are done with: the
+          // next unit's come in under this tile's softmax.
+          if (!wait(u_full(i + 1), phase(i + 1))) break;
+          if (units[(i + 1) & 1].nt > 0) {
+            load_q(units[(i + 1) & 1]);
+            loaded = true;
+          }
+        }
         if (careful) {
           // Drafts, or the partition's end: what a row does not see is masked, the
           // values past the end are zeroed, and so is what is not finite in the
           // drafts' values, which would reach rows that do not see it (0 * NaN);
           // the rows that do see it get it at the end.
-          if (!(ok = wait(v_full(j % STAGES), (j / STAGES) & 1))) break;
-          const uint32_t vb = v_sm + (j % STAGES) * S::KV_BYTES;
-          const int first = max(0, lim - t0), valid = min(kTile, end - t0);
-          for (int i = first * (D / 8) + int(threadIdx.x); i < kTile * (D / 8); i += active * 32) {
-            const int row = i / (D / 8), c = i % (D / 8);
-            const uint32_t a = vb + (c >> 3) * S::KV_SLAB + row * 128 + (c & 7) * 16;
+          if (!wait(v_full(t), phase(t))) break;
+          const uint32_t vb = v_sm + uint32_t(t & 1) * S::KV_BYTES;
+          const int first = max(0, lim - t0), valid = min(kTile, c.end - t0);
+          for (int k = first * (D / 8) + r; k < kTile * (D / 8); k += 128) {
+            const int row = k / (D / 8), ch = k % (D / 8);
+            const uint32_t a = vb + (ch >> 3) * S::KV_SLAB + row * 128 + (ch & 7) * 16;
             uint32_t w[4] = {0, 0, 0, 0};
             bool dirty = row >= valid;
             if (!dirty) {
@@ -295,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u, dirty = true;
                 if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu, dirty = true;
               }
-              if (dirty) poisoned = 1;
+              if (dirty) poisoned[qi & 1] = 1;
             }
             if (dirty)
               asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w[0]), "r"(w[1]), "r"(w[2]),
@@ -303,137 +393,157 @@ __global__ void __launch_bounds__(kThreads, 2)
                            : "memory");
           }
           fence_proxy_async();
-        }
-        tmem_wait_load(x[0]);
-        tmem_wait_load(x[1]);
-        if (careful) {
-          const uint64_t see = see64(mask, base, t0);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t w = uint32_t(see >> (32 * h));
-            const int live = end - t0 - 32 * h;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((w >> i) & 1) || i >= live) x[h][i] = 0xff800000u;  // -inf
-          }
-        }
-        float mx = -INFINITY;
-        {
-          float part[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            part[i & 3] = max3(part[i & 3], __uint_as_float(x[i >> 4][2 * (i & 15)]),
-                               __uint_as_float(x[i >> 4][2 * (i & 15) + 1]));
-          mx = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])) * sl;
-        }
-        const bool move = mx > ref + kSlack;
-        if (__any_sync(0xffffffffu, move)) {
-          const float f = move ? exp2_ftz(ref - mx) : 1.0f;
-          if (move) ref = mx;
-          const uint64_t f2 = pack2(f, f);
-          l *= f;
-          if (j > 0) {
-            if (!(ok = wait(o_done((j - 1) & 1), ((j - 1) >> 1) & 1))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_load32(t_o + lane_base + 32 * c, o);
-              tmem_wait_load(o);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float a, b;
-                unpack2(mul2(pack2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), f2), a, b);
-                o[2 * i] = __float_as_uint(a);
-                o[2 * i + 1] = __float_as_uint(b);
-              }
-              tmem_store32(t_o + lane_base + 32 * c, o);
-            }
-          }
-        }
-        const float m = ref == -INFINITY ? 0.0f : ref;  // nothing seen so far: every weight is 0
-        const uint64_t sl2 = pack2(sl, sl), m2 = pack2(-m, -m), minus = pack2(-1.0f, -1.0f);
-        uint64_t sum2 = 0;
-        uint32_t hi[32], lo[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float a, b;
-          unpack2(fma2(pack2(__uint_as_float(x[i >> 4][2 * (i & 15)]), __uint_as_float(x[i >> 4][2 * (i & 15) + 1])),
-                       sl2, m2),
-                  a, b);
-          a = exp2_ftz(a);
-          b = exp2_ftz(b);
-          const uint64_t ab = pack2(a, b);
-          sum2 = add2(sum2, ab);
-          hi[i] = pack_bf16x2(a, b);
-          unpack2(fma2(pack2(bf16_lo(hi[i]), bf16_hi(hi[i])), minus, ab), a, b);
-          lo[i] = pack_bf16x2(a, b);
-        }
-        {
-          float a, b;
-          unpack2(sum2, a, b);
-          l += a + b;
-        }
-        tmem_store32(t_s(j & 1) + lane_base, hi);
-        tmem_store32(t_s(j & 1) + lane_base + 32, lo);
-        tmem_wait_store();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(j & 1));
-      }
-      ok = ok && wait(o_done((nt - 1) & 1), ((nt - 1) >> 1) & 1);
-      tc_fence_after();
-      named_barrier(1, active * 32);  // every warp's part of `poisoned` is in
-      if (ok) {
-        const bool split = sr.np > 1;
-        const float inv = split ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
-        const size_t at = r < rows ? q_row(r) : 0;
-        const size_t slot = at / D * p.num_partitions + part;
-        const bool fix = poisoned;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_load32(t_o + lane_base + 32 * c, o);
-          tmem_wait_load(o);
-          if (fix && r < rows) {
-            for (int t = max(base, start); t < end; ++t) {
-              if (!((mask >> (t - base)) & 1)) continue;
-              const int phys = __ldg(p.tables + size_t(s) * p.max_blocks + t / BS);
-              if (phys < 0 || phys >= p.num_blocks) continue;
-              const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.v_cache) +
-                                       ((size_t(phys) * BS + t % BS) * p.num_kv_heads + kvh) * D + 32 * c;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float y = __bfloat162float(v[i]);
-                if (!(fabsf(y) <= 3.402823466e38f)) o[i] = __float_as_uint(__uint_as_float(o[i]) + y);
-              }
-            }
-          }
-          if (split && r < rows) {
-            float4 *dst = reinterpret_cast<float4 *>(p.ws_acc + slot * D + 32 * c);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                   __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
-          } else if (r < rows) {
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at + 32 * c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
           __syncwarp();
         }
-        if (split && r < rows) {
-          p.ws_m[slot] = ref;
-          p.ws_l[slot] = l;
+        if (busy) {
+          tmem_wait_load(x[0]);
+          tmem_wait_load(x[1]);
+          if (careful) {
+            const uint64_t see = see64(row_mask(), c.ctx - c.n, t0);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t w = uint32_t(see >> (32 * h));
+              const int live = c.end - t0 - 32 * h;
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!((w >> k) & 1) || k >= live) x[h][k] = 0xff800000u;  // -inf
+            }
+          }
+          float mx;
+          {
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              top[k & 3] = max3(top[k & 3], __uint_as_float(x[k >> 4][2 * (k & 15)]),
+                                __uint_as_float(x[k >> 4][2 * (k & 15) + 1]));
+            mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+            mx = mx == -INFINITY ? mx : mx * sl;
+          }
+          const bool move = mx > ref + kSlack;
+          if (__any_sync(0xffffffffu, move)) {
+            const float f = move ? exp2_ftz(ref - mx) : 1.0f;
+            if (move) ref = mx;
+            l *= f;
+            if (j > 0) {
+              if (!wait(o_done(t - 1), phase(t - 1))) break;
+              tc_fence_after();
+              const uint64_t f2 = pack2(f, f);
+#pragma unroll
+              for (int ch = 0; ch < D / 32; ++ch) {
+                uint32_t o[32];
+                tmem_load32(t_o + lane_base + 32 * ch, o);
+                tmem_wait_load(o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  float a, b;
+                  unpack2(mul2(pack2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])), f2), a, b);
+                  o[2 * k] = __float_as_uint(a);
+                  o[2 * k + 1] = __float_as_uint(b);
+                }
+                tmem_store32(t_o + lane_base + 32 * ch, o);
+              }
+            }
+          }
+          const float m = ref == -INFINITY ? 0.0f : ref;  // nothing seen so far: every weight is 0
+          const uint64_t sl2 = pack2(sl, sl), m2 = pack2(-m, -m), minus = pack2(-1.0f, -1.0f);
+          uint64_t sum2 = 0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float a, b;
+              unpack2(fma2(pack2(__uint_as_float(x[h][2 * k]), __uint_as_float(x[h][2 * k + 1])), sl2, m2), a, b);
+              a = exp2_ftz(a);
+              b = exp2_ftz(b);
+              const uint64_t ab = pack2(a, b);
+              sum2 = add2(sum2, ab);
+              hi[k] = pack_bf16x2(a, b);
+              unpack2(fma2(pack2(bf16_lo(hi[k]), bf16_hi(hi[k])), minus, ab), a, b);
+              lo[k] = pack_bf16x2(a, b);
+            }
+            tmem_store16(t_s(t) + lane_base + 16 * h, hi);
+            tmem_store16(t_s(t) + lane_base + 32 + 16 * h, lo);
+          }
+          {
+            float a, b;
+            unpack2(sum2, a, b);
+            l += a + b;
+          }
+          tmem_wait_store();
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(t));
       }
+      if (!ok) break;
+      if (loaded) q_landed();
+      // Every warp is past the tiles: what they found of `poisoned` is in, and
+      // the other flag, last read in the unit before, is free.
+      if (lane == 0) mbar_arrive(u_done);
+      if (!wait(u_done, qi & 1)) break;
+      const bool fix = poisoned[qi & 1] != 0;
+      if (r == 0) poisoned[(qi + 1) & 1] = 0;
+      ++qi;
+      if (!busy) {
+        release();
+        continue;
+      }
+      if (!wait(o_done(t - 1), phase(t - 1))) break;
+      tc_fence_after();
+      const bool mine = r < c.rows;
+      const size_t at = mine ? q_row(c.q0, c.r0 + r, c.kvh) : 0;
+      const bool split = c.np > 1;
+      const float inv = split ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+      const size_t slot = at / D * p.num_partitions + c.part;
+#pragma unroll
+      for (int ch = 0; ch < D / 32; ++ch) {
+        uint32_t o[32];
+        tmem_load32(t_o + lane_base + 32 * ch, o);
+        tmem_wait_load(o);
+        if (fix && mine) {
+          const uint64_t mask = row_mask();
+          const int base = c.ctx - c.n;
+          for (int k = max(base, c.start); k < c.end; ++k) {
+            if (!((mask >> (k - base)) & 1)) continue;
+            const int phys = __ldg(p.tables + size_t(c.s) * p.max_blocks + k / BS);
+            if (phys < 0 || phys >= p.num_blocks) continue;
+            const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.v_cache) +
+                                     ((size_t(phys) * BS + k % BS) * p.num_kv_heads + c.kvh) * D + 32 * ch;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float y = __bfloat162float(v[e]);
+              if (!(fabsf(y) <= 3.402823466e38f)) o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
+            }
+          }
+        }
+        if (mine && split) {
+          float4 *dst = reinterpret_cast<float4 *>(p.ws_acc + slot * D + 32 * ch);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                 __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+        } else if (mine) {
+          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at + 32 * ch);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+            dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        __syncwarp();
+      }
+      if (mine && split) {
+        p.ws_m[slot] = ref;
+        p.ws_l[slot] = l;
+      }
+      release();
+      tc_fence_before();  // O may be overwritten once the next unit's weights are there
     }
+    if (!ok && lane == 0) timeout();
   }
   tc_fence_before();
   __syncthreads();
@@ -452,7 +562,11 @@ pk_status launch_tree(RowsParams p, const pk_cache_desc &d, cudaStream_t stream)
   static std::atomic<uint64_t> ready{0};
   if (!smem_ready(kern, S::SMEM_BYTES, ready)) return PK_ERR_CUDA;
   p.row_tiles = (p.max_draft * p.group + kRows - 1) / kRows;
-  kern<<<rows_grid(p), kThreads, S::SMEM_BYTES, stream>>>(p, kmap, vmap);
+  const dim3 g = rows_grid(p);
+  const int64_t units = int64_t(g.x) * g.y * g.z;
+  if (units > INT32_MAX / 2) return PK_ERR_UNSUPPORTED;
+  const int ctas = int(std::min<int64_t>(units, 2 * sm_count()));
+  kern<<<ctas, kThreads, S::SMEM_BYTES, stream>>>(p, kmap, vmap, int(units));
   return cudaGetLastError() == cudaSuccess ? PK_OK : PK_ERR_CUDA;
 }
 
@@ -488,15 +602,6 @@ pk_status check_tree(const pk_cache_desc *d, int32_t num_q_heads, int32_t max_co
     return PK_ERR_UNSUPPORTED;
   if (int64_t(d->num_blocks) * d->block_size > INT32_MAX) return PK_ERR_UNSUPPORTED;
   return PK_OK;
-}
-
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) == cudaSuccess &&
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0)
-    return n;
-  cudaGetLastError();  // clear a failed query on a machine without a GPU
-  return 152;
 }
 
 }  // namespace
