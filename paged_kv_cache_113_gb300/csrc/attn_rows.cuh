@@ -281,33 +281,76 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(RowsParams p) {
 
 // ---------------------------------------------------------------------------
 // Merge of split rows: M = max_q m_q, out = sum_q acc_q 2^(m_q - M) /
-// sum_q l_q 2^(m_q - M). One warp per row; grid.y = sequence, so that a row
-// needs no search for its sequence.
+// sum_q l_q 2^(m_q - M). A row (grid.y = sequence, so that it needs no search
+// for its sequence) gets wpr warps, enough that a warp merges at most eight
+// partials, all loaded at once; the row's first warp joins the warps' states.
 // ---------------------------------------------------------------------------
 template <typename IO, int D>
-__global__ void __launch_bounds__(256) rows_merge_kernel(RowsParams p) {
-  constexpr int EPL = D / 32;
-  const int s = blockIdx.y, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(256) rows_merge_kernel(RowsParams p, int wpr) {
+  constexpr int EPL = D / 32, U = 8;
+  __shared__ float sm_acc[8][D], sm_m[8], sm_l[8];
+  const int s = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const SeqRows sr = seq_rows(p, s, false);
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5);  // token * Hq + head
+  const int row = blockIdx.x * (8 / wpr) + warp / wpr, sub = warp % wpr;  // row: token * Hq + head
   wait_prerequisites();
-  if (row >= sr.n * p.num_q_heads || sr.np <= 1) return;
+  const bool live = row < sr.n * p.num_q_heads && sr.np > 1;
   const size_t at = size_t(sr.q0) * p.num_q_heads + row;
-  const float *mr = p.ws_m + at * p.num_partitions, *lr = p.ws_l + at * p.num_partitions;
-  const float *ar = p.ws_acc + at * p.num_partitions * D + lane * EPL;
-  float M = -INFINITY;
-  for (int q = lane; q < sr.np; q += 32) M = fmaxf(M, __ldcg(mr + q));
+  const int chunk = (sr.np + wpr - 1) / wpr;
+  const int q_end = live ? min(sr.np, (sub + 1) * chunk) : 0;
+  float M = -INFINITY, L = 0.0f, acc[EPL] = {};
+  for (int q0 = sub * chunk; q0 < q_end; q0 += U) {
+    float m[U], l[U], x[U][EPL];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float ref = M == -INFINITY ? 0.0f : M;
-  float L = 0.0f, acc[EPL] = {};
-  for (int q = 0; q < sr.np; ++q) {
-    const float w = exp2f(__ldcg(mr + q) - ref);
-    if (w == 0.0f) continue;
-    L = fmaf(__ldcg(lr + q), w, L);
+    for (int u = 0; u < U; ++u) {
+      const size_t q = at * p.num_partitions + min(q0 + u, q_end - 1);
+      m[u] = q0 + u < q_end ? __ldcg(p.ws_m + q) : -INFINITY;
+      l[u] = __ldcg(p.ws_l + q);
+      const float *src = p.ws_acc + q * D + lane * EPL;
+      if (EPL == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
+        x[u][0] = v.x, x[u][1] = v.y, x[u][EPL - 2] = v.z, x[u][EPL - 1] = v.w;
+      } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
+        x[u][0] = v.x, x[u][1] = v.y;
+      }
+    }
+    float top = M;
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) acc[e] = fmaf(__ldcg(ar + size_t(q) * D + e), w, acc[e]);
+    for (int u = 0; u < U; ++u) top = fmaxf(top, m[u]);
+    const float ref = top == -INFINITY ? 0.0f : top, f = exp2f(M - ref);
+    M = top;
+    L *= f;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) acc[e] = f == 0.0f ? 0.0f : acc[e] * f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float w = exp2f(m[u] - ref);
+      if (w == 0.0f) continue;  // nothing of this partition counts, whatever it holds
+      L = fmaf(l[u], w, L);
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) acc[e] = fmaf(x[u][e], w, acc[e]);
+    }
   }
+  if (wpr > 1) {
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) sm_acc[warp][lane * EPL + e] = acc[e];
+    if (lane == 0) sm_m[warp] = M, sm_l[warp] = L;
+    __syncthreads();
+    if (sub != 0) return;
+    for (int w = 1; w < wpr; ++w) M = fmaxf(M, sm_m[warp + w]);
+    const float ref = M == -INFINITY ? 0.0f : M;
+    L = 0.0f;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) acc[e] = 0.0f;
+    for (int w = 0; w < wpr; ++w) {
+      const float f = exp2f(sm_m[warp + w] - ref);
+      if (f == 0.0f) continue;
+      L = fmaf(sm_l[warp + w], f, L);
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) acc[e] = fmaf(sm_acc[warp + w][lane * EPL + e], f, acc[e]);
+    }
+  }
+  if (!live) return;
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
   for (int e = 0; e < EPL; ++e)
@@ -402,8 +445,11 @@ pk_status launch_rows(RowsParams p, cudaStream_t stream) {
 // where that is refused).
 template <typename IO, int D>
 pk_status launch_rows_merge(const RowsParams &p, cudaStream_t stream) {
+  int wpr = 1;
+  while (wpr < 8 && wpr * 8 < p.num_partitions) wpr *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((int64_t(p.max_draft) * p.num_q_heads + 7) / 8), unsigned(p.num_seqs));
+  cfg.gridDim = dim3(unsigned((int64_t(p.max_draft) * p.num_q_heads + 8 / wpr - 1) / (8 / wpr)),
+                     unsigned(p.num_seqs));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -411,9 +457,9 @@ pk_status launch_rows_merge(const RowsParams &p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, rows_merge_kernel<IO, D>, p) == cudaSuccess) return PK_OK;
+  if (cudaLaunchKernelEx(&cfg, rows_merge_kernel<IO, D>, p, wpr) == cudaSuccess) return PK_OK;
   cudaGetLastError();
-  rows_merge_kernel<IO, D><<<cfg.gridDim, cfg.blockDim, 0, stream>>>(p);
+  rows_merge_kernel<IO, D><<<cfg.gridDim, cfg.blockDim, 0, stream>>>(p, wpr);
   return cudaGetLastError() == cudaSuccess ? PK_OK : PK_ERR_CUDA;
 }
 

@@ -31,7 +31,10 @@
 // warps finish the last, so that short contexts keep memory busy too.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
+
+#include <cmath>
 
 #include "attn_rows.cuh"
 #include "pagedkv.h"
@@ -50,6 +53,10 @@ constexpr int kRows = 128;          // query rows of a CTA
 constexpr int kTile = 64;           // tokens of a tile
 constexpr int kThreads = 192;       // 4 softmax warps, the producer, the product warp
 constexpr uint32_t kTmemCols = 256;
+// Units known ahead. The producer's look-ahead is three tiles, so three units
+// at most, and it is two tiles ahead of the softmax: eight places never leave
+// it waiting for a unit whose tiles it has yet to load.
+constexpr int kUnits = 8;
 constexpr uint32_t kNegateA = 1u << 13;  // of an instruction descriptor
 constexpr float kSlack = 8.0f;      // log2 of how far a maximum may outgrow the reference
 
@@ -76,7 +83,7 @@ struct Unit {
   int s, kvh, part;
   int q0, n, ctx, np;  // as SeqRows
   int r0, rows;        // its rows
-  int start, end, nt;  // its tokens, its tiles (0: the rows are zero); s < 0: no more units
+  int start, end, nt;  // its tokens and tiles; s < 0: no more units
 };
 
 template <int D, int BS>
@@ -88,13 +95,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t q_sm = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t k_sm = q_sm + S::Q_BYTES, v_sm = k_sm + 2 * S::KV_BYTES;
-  __shared__ __align__(8) uint64_t bars[20];
-  __shared__ Unit units[2];
+  __shared__ __align__(8) uint64_t bars[16 + 2 * kUnits];
+  __shared__ Unit units[kUnits];
   __shared__ uint32_t tmem_slot;
   __shared__ int poisoned[2];
   auto bar = [&](int i) { return smem_addr(bars + i); };
-  // Tiles t and units i are counted over the whole life of the CTA; what there
-  // are two of alternates. Every wait names a phase of which the one before has
+  // Tiles t and units i are counted over the whole life of the CTA; of what a
+  // tile uses there are two, which alternate. Every wait names a phase of which the one before has
   // ended for certain and the one after cannot have: a wait by parity tells
   // neighbouring phases apart, not more. So the products' ends alternate too:
   // when tile t's scores are there, product t - 2 has ended, t - 1 may not have.
@@ -106,8 +113,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   auto k_empty = [&](int t) { return bar(10 + (t & 1)); };
   auto v_full = [&](int t) { return bar(12 + (t & 1)); };
   auto v_empty = [&](int t) { return bar(14 + (t & 1)); };
-  auto u_full = [&](int i) { return bar(16 + (i & 1)); };
-  auto u_empty = [&](int i) { return bar(18 + (i & 1)); };
+  auto u_full = [&](int i) { return bar(16 + i % kUnits); };
+  auto u_empty = [&](int i) { return bar(16 + kUnits + i % kUnits); };
+  auto u_phase = [](int i) { return uint32_t(i / kUnits) & 1u; };
   auto phase = [](int t) { return uint32_t(t >> 1) & 1u; };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -123,9 +131,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(k_empty(i), 1);
       mbar_init(v_full(i), 1);
       mbar_init(v_empty(i), 1);
-      mbar_init(u_full(i), 1);
-      mbar_init(u_empty(i), 5);  // the softmax warps and the product thread
       poisoned[i] = 0;
+    }
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(u_full(i), 1);
+      mbar_init(u_empty(i), 6);  // the softmax warps, the product thread, the producer
     }
     fence_barrier_init();
   }
@@ -136,6 +146,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t tmem = tmem_slot;
   const uint32_t t_o = tmem + 128;                             // O: columns 128 .. 128 + D
   auto t_s = [&](int t) { return tmem + 64u * uint32_t(t & 1); };  // S_t, then P_t: hi 32 columns, lo 32
+  auto q_row = [&](int q0, int row, int kvh) {  // element offset of a row of q and out
+    return (size_t(q0 + row / G) * p.num_q_heads + kvh * G + row % G) * D;
+  };
   auto timeout = [&] { record_error(&g_rows_error, PK_DEVERR_TIMEOUT, blockIdx.x); };
 
   if (warp == 4) {
@@ -144,89 +157,121 @@ __global__ void __launch_bounds__(kThreads, 2)
       prefetch_tensormap(&kmap);
       prefetch_tensormap(&vmap);
     }
-    // The first unit with work at or after u in this CTA's share.
-    auto find = [&](int &u, Unit &c) {
-      const int X = p.num_kv_heads * p.row_tiles, Y = p.items ? p.num_items : p.num_seqs;
-      for (; u < num_units; u += gridDim.x) {
-        const int x = u % X, y = (u / X) % Y, z = u / X / Y;
-        const bool record = x == 0 && lane == 0;
-        if (!work_item(p, y, p.num_partitions - 1 - z, record, c.s, c.part)) continue;
-        const SeqRows sr = seq_rows(p, c.s, record && c.part == 0);
-        c.kvh = x / p.row_tiles;
-        c.r0 = x % p.row_tiles * kRows;
-        c.rows = min(kRows, sr.n * G - c.r0);
-        if (c.rows <= 0 || (sr.ctx == 0 ? c.part != 0 : c.part >= sr.np)) continue;
-        c.q0 = sr.q0, c.n = sr.n, c.ctx = sr.ctx, c.np = sr.np;
-        c.start = c.part * p.partition;
-        c.end = min(sr.ctx, c.start + p.partition);
-        c.nt = (c.end - c.start + kTile - 1) / kTile;
-        return;
+    // 32 units of this CTA's share are looked up at a time, one per lane, and
+    // those with work published in order; `left` are the lanes not yet taken.
+    const int X = p.num_kv_heads * p.row_tiles, Y = p.items ? p.num_items : p.num_seqs;
+    Unit look;
+    uint32_t left = 0;
+    int next_u = blockIdx.x, published = 0;
+    auto look_up = [&](int u) {
+      const int x = u % X, y = (u / X) % Y, z = u / X / Y;
+      if (!work_item(p, y, p.num_partitions - 1 - z, x == 0, look.s, look.part)) return false;
+      const SeqRows sr = seq_rows(p, look.s, x == 0 && look.part == 0);
+      look.kvh = x / p.row_tiles;
+      look.r0 = x % p.row_tiles * kRows;
+      look.rows = min(kRows, sr.n * G - look.r0);
+      if (look.rows <= 0) return false;
+      if (sr.ctx == 0) {  // invalid length (recorded): zero rows
+        for (int i = 0; look.part == 0 && i < look.rows * (D / 8); ++i)
+          *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
+                                     q_row(sr.q0, look.r0 + i / (D / 8), look.kvh) + i % (D / 8) * 8) =
+              make_uint4(0, 0, 0, 0);
+        return false;
       }
-      c.s = -1;
-      c.nt = 0;
+      if (look.part >= sr.np) return false;
+      look.q0 = sr.q0, look.n = sr.n, look.ctx = sr.ctx, look.np = sr.np;
+      look.start = look.part * p.partition;
+      look.end = min(sr.ctx, look.start + p.partition);
+      look.nt = (look.end - look.start + kTile - 1) / kTile;
+      return true;
     };
-    const int mine = min(lane, S::BPT - 1);
-    auto entry = [&](const Unit &c, int j) {
-      const int b = j * S::BPT + mine;
-      return c.start / BS + b < (c.end + BS - 1) / BS
-                 ? __ldg(p.tables + size_t(c.s) * p.max_blocks + c.start / BS + b)
-                 : 0;
-    };
-    // Tile j of a unit, the CTA's tile t: its K (or V) blocks into their slot.
-    auto load = [&](const CUtensorMap *map, uint32_t ring, uint32_t full, const Unit &c, int j, int t, int phys) {
-      const int nblk = min(S::BPT, (c.end - c.start + BS - 1) / BS - j * S::BPT);
-      if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(nblk * S::SLABS * BS * 128));
+    bool ok = true;
+    // Publishes the CTA's next unit (s < 0 after the last) and returns it; null
+    // when its place does not come free in time.
+    auto publish = [&]() -> const Unit * {
+      while (left == 0 && next_u < num_units) {
+        const int64_t u = next_u + int64_t(lane) * gridDim.x;
+        left = __ballot_sync(0xffffffffu, u < num_units && look_up(int(u)));
+        next_u = int(min(int64_t(num_units), next_u + 32 * int64_t(gridDim.x)));
+      }
+      const int i = published;
+      ok = ok && (i < kUnits || mbar_wait(u_empty(i), uint32_t((i - kUnits) / kUnits) & 1u));
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return nullptr;
+      Unit *to = units + i % kUnits;
+      if (left == 0) {
+        if (lane == 0) to->s = -1;
+      } else if (lane == __ffs(left) - 1) {
+        *to = look;
+      }
+      left &= left - 1;
       __syncwarp();
-      if (lane < nblk) {
-        if (phys < 0 || phys >= p.num_blocks) {
-          record_error(&g_rows_error, PK_DEVERR_BLOCK_ID, c.s);
-          phys = 0;  // stay in bounds and keep the byte count; the result is flagged
+      if (lane == 0) mbar_arrive(u_full(i));
+      ++published;
+      return to;
+    };
+    // A tile to load: the lane's block of it, read from the table ahead of time.
+    struct Tile {
+      int phys, nblk, kvh, s;  // nblk 0: no more tiles
+    };
+    const Unit *at = nullptr;  // the unit that `next` is in, and the tile there
+    int at_j = 0, at_nt = 0;
+    auto next = [&] {
+      Tile tl{0, 0, 0, 0};
+      if (at && ++at_j == at_nt) at = nullptr;
+      if (!at) {
+        const Unit *c = publish();
+        if (c && c->s >= 0) at = c, at_j = 0, at_nt = c->nt;
+      }
+      if (at) {
+        const int nb = (at->end - at->start + BS - 1) / BS;
+        tl.nblk = min(S::BPT, nb - at_j * S::BPT);
+        tl.kvh = at->kvh;
+        tl.s = at->s;
+        if (lane < tl.nblk)
+          tl.phys = __ldg(p.tables + size_t(at->s) * p.max_blocks + at->start / BS + at_j * S::BPT + lane);
+        if (at_j == at_nt - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(u_empty(published - 1));  // done with the unit's entry
+        }
+      }
+      return tl;
+    };
+    // Tile t's K (or V) blocks into their slot.
+    auto load = [&](const CUtensorMap *map, uint32_t ring, uint32_t full, int t, Tile tl) {
+      if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(tl.nblk * S::SLABS * BS * 128));
+      __syncwarp();
+      if (lane < tl.nblk) {
+        if (tl.phys < 0 || tl.phys >= p.num_blocks) {
+          record_error(&g_rows_error, PK_DEVERR_BLOCK_ID, tl.s);
+          tl.phys = 0;  // stay in bounds and keep the byte count; the result is flagged
         }
         const uint32_t dst = ring + uint32_t(t & 1) * S::KV_BYTES + lane * BS * 128;
 #pragma unroll
         for (int h = 0; h < S::SLABS; ++h)
-          tma_load_3d(dst + h * S::KV_SLAB, map, full, h * 64, c.kvh, phys * BS);
+          tma_load_3d(dst + h * S::KV_SLAB, map, full, h * 64, tl.kvh, tl.phys * BS);
       }
     };
-    Unit cur, nxt;
-    int u = blockIdx.x, kt = 0, vt = 0;  // K and V tiles loaded so far
-    bool ok = true;
-    auto load_k = [&](const Unit &c, int j, int phys) {
-      ok = ok && (kt < 2 || mbar_wait(k_empty(kt), phase(kt - 2)));
-      if (!ok) return;
-      load(&kmap, k_sm, k_full(kt), c, j, kt, phys);
-      ++kt;
-    };
-    find(u, cur);
-    for (int i = 0; ok; ++i) {
-      ok = i < 2 || mbar_wait(u_empty(i), phase(i - 2));
-      if (!ok) break;
-      if (lane == 0) {
-        units[i & 1] = cur;
-        mbar_arrive(u_full(i));
+    // K runs one tile ahead of V, whose slots come free later, and the block
+    // table two tiles ahead, across units.
+    int kt = 0, vt = 0;  // K and V tiles loaded so far
+    Tile a{0, 0, 0, 0}, b = a;
+    for (bool more = true; ok && (more || a.nblk || b.nblk);) {
+      Tile c{0, 0, 0, 0};
+      if (more) c = next();
+      more = more && c.nblk;
+      if (b.nblk) {
+        if (!(ok = ok && (kt < 2 || mbar_wait(k_empty(kt), phase(kt - 2))))) break;
+        load(&kmap, k_sm, k_full(kt), kt, b);
+        ++kt;
       }
-      if (cur.s < 0) break;
-      u += gridDim.x;
-      if (cur.nt == 0) {
-        find(u, nxt);
-      } else {
-        // K runs one tile ahead of V, whose slots come free later; the next unit
-        // is looked up while this one's first tiles are under way.
-        int e0 = entry(cur, 0), e1 = entry(cur, 1);
-        load_k(cur, 0, e0);
-        for (int j = 0; j < cur.nt && ok; ++j) {
-          const int e2 = entry(cur, j + 2);
-          if (j + 1 < cur.nt) load_k(cur, j + 1, e1);
-          ok = ok && (vt < 2 || mbar_wait(v_empty(vt), phase(vt - 2)));
-          if (!ok) break;
-          load(&vmap, v_sm, v_full(vt), cur, j, vt, e0);
-          ++vt;
-          e0 = e1;
-          e1 = e2;
-          if (j == 0) find(u, nxt);
-        }
+      if (a.nblk) {
+        if (!(ok = ok && (vt < 2 || mbar_wait(v_empty(vt), phase(vt - 2))))) break;
+        load(&vmap, v_sm, v_full(vt), vt, a);
+        ++vt;
       }
-      cur = nxt;
+      a = b;
+      b = c;
     }
     if (!ok && lane == 0) timeout();
     // Let every issued copy land before the warp leaves.
@@ -240,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint32_t s_desc = mma_desc(kRows, kTile, false) | (p.scale_log2 < 0.0f ? kNegateA : 0u);
       constexpr uint32_t O_DESC = mma_desc(kRows, D, true);
       bool ok = true;
-      int t = 0, issued = 0, qi = 0;  // tiles, P V products, units with tiles
+      int t = 0, issued = 0;  // tiles, P V products
       auto pv = [&](int w, bool first) {
         ok = ok && mbar_wait(p_full(w), phase(w)) && mbar_wait(v_full(w), phase(w));
         if (!ok) return;
@@ -257,15 +302,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         issued = w + 1;
       };
       for (int i = 0; ok; ++i) {
-        ok = mbar_wait(u_full(i), phase(i));
+        ok = mbar_wait(u_full(i), u_phase(i));
         if (!ok) break;
-        const int nt = units[i & 1].nt;
-        const bool last = units[i & 1].s < 0;
+        const int nt = units[i % kUnits].nt;
+        const bool last = units[i % kUnits].s < 0;
         mbar_arrive(u_empty(i));
         if (last) break;
-        if (nt == 0) continue;
-        ok = mbar_wait(q_ready, qi & 1);
-        ++qi;
+        ok = mbar_wait(q_ready, i & 1);
         for (int j = 0; j < nt && ok; ++j, ++t) {
           // The score tile holds the weights of tile t - 2 until their product ends.
           ok = mbar_wait(k_full(t), phase(t)) && (t < 2 || mbar_wait(o_done(t), phase(t - 2)));
@@ -299,9 +342,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       ok = __all_sync(0xffffffffu, mbar_wait(b, parity));
       return ok;
     };
-    auto q_row = [&](int q0, int row, int kvh) {  // element offset of a row of q and out
-      return (size_t(q0 + row / G) * p.num_q_heads + kvh * G + row % G) * D;
-    };
     // A unit's queries into shared memory, rows past the last as zeros.
     auto load_q = [&](const Unit &c) {
       for (int i = r; i < kRows * (D / 8); i += 128) {
@@ -318,21 +358,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_arrive(q_ready);
     };
     bool loaded = false;  // the unit's queries were loaded under the one before
-    for (int i = 0, t = 0, qi = 0; wait(u_full(i), phase(i)); ++i) {
-      const Unit &c = units[i & 1];  // read where it is needed: registers are short
+    for (int i = 0, t = 0; wait(u_full(i), u_phase(i)); ++i) {
+      const Unit &c = units[i % kUnits];  // read where it is needed: registers are short
       auto release = [&] {
         __syncwarp();
         if (lane == 0) mbar_arrive(u_empty(i));
       };
       if (c.s < 0) break;
-      if (c.nt == 0) {  // invalid length (recorded): zero rows
-        if (r < c.rows)
-          for (int e = 0; e < D; e += 8)
-            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + q_row(c.q0, c.r0 + r, c.kvh) + e) =
-                make_uint4(0, 0, 0, 0);
-        release();
-        continue;
-      }
       if (!loaded) {
         load_q(c);
         q_landed();
@@ -357,11 +389,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (j == nt - 1) {
           // The unit's last scores are there, so its queries are done with: the
           // next unit's come in under this tile's softmax.
-          if (!wait(u_full(i + 1), phase(i + 1))) break;
-          if (units[(i + 1) & 1].nt > 0) {
-            load_q(units[(i + 1) & 1]);
-            loaded = true;
-          }
+          if (!wait(u_full(i + 1), u_phase(i + 1))) break;
+          loaded = units[(i + 1) % kUnits].s >= 0;
+          if (loaded) load_q(units[(i + 1) % kUnits]);
         }
         if (careful) {
           // Drafts, or the partition's end: what a row does not see is masked, the
@@ -385,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u, dirty = true;
                 if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu, dirty = true;
               }
-              if (dirty) poisoned[qi & 1] = 1;
+              if (dirty) poisoned[i & 1] = 1;
             }
             if (dirty)
               asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w[0]), "r"(w[1]), "r"(w[2]),
@@ -428,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               if (!wait(o_done(t - 1), phase(t - 1))) break;
               tc_fence_after();
               const uint64_t f2 = pack2(f, f);
-#pragma unroll
+#pragma unroll 1
               for (int ch = 0; ch < D / 32; ++ch) {
                 uint32_t o[32];
                 tmem_load32(t_o + lane_base + 32 * ch, o);
@@ -481,10 +511,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       // Every warp is past the tiles: what they found of `poisoned` is in, and
       // the other flag, last read in the unit before, is free.
       if (lane == 0) mbar_arrive(u_done);
-      if (!wait(u_done, qi & 1)) break;
-      const bool fix = poisoned[qi & 1] != 0;
-      if (r == 0) poisoned[(qi + 1) & 1] = 0;
-      ++qi;
+      if (!wait(u_done, i & 1)) break;
+      const bool fix = poisoned[i & 1] != 0;
+      if (r == 0) poisoned[(i + 1) & 1] = 0;
       if (!busy) {
         release();
         continue;
@@ -496,27 +525,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       const bool split = c.np > 1;
       const float inv = split ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
       const size_t slot = at / D * p.num_partitions + c.part;
-#pragma unroll
+#pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
         uint32_t o[32];
         tmem_load32(t_o + lane_base + 32 * ch, o);
         tmem_wait_load(o);
-        if (fix && mine) {
-          const uint64_t mask = row_mask();
-          const int base = c.ctx - c.n;
-          for (int k = max(base, c.start); k < c.end; ++k) {
-            if (!((mask >> (k - base)) & 1)) continue;
-            const int phys = __ldg(p.tables + size_t(c.s) * p.max_blocks + k / BS);
-            if (phys < 0 || phys >= p.num_blocks) continue;
-            const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.v_cache) +
-                                     ((size_t(phys) * BS + k % BS) * p.num_kv_heads + c.kvh) * D + 32 * ch;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float y = __bfloat162float(v[e]);
-              if (!(fabsf(y) <= 3.402823466e38f)) o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
-            }
-          }
-        }
         if (mine && split) {
           float4 *dst = reinterpret_cast<float4 *>(p.ws_acc + slot * D + 32 * ch);
 #pragma unroll
@@ -539,6 +552,26 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (mine && split) {
         p.ws_m[slot] = ref;
         p.ws_l[slot] = l;
+      }
+      if (fix && mine) {  // what is not finite in the values of the drafts that the row sees
+        const uint64_t mask = row_mask();
+        const int base = c.ctx - c.n;
+        for (int k = max(base, c.start); k < c.end; ++k) {
+          const int phys = __ldg(p.tables + size_t(c.s) * p.max_blocks + k / BS);
+          if (!((mask >> (k - base)) & 1) || phys < 0 || phys >= p.num_blocks) continue;
+          const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.v_cache) +
+                                   ((size_t(phys) * BS + k % BS) * p.num_kv_heads + c.kvh) * D;
+          for (int e = 0; e < D; ++e) {
+            const float y = __bfloat162float(v[e]);
+            if (fabsf(y) <= 3.402823466e38f) continue;
+            if (split) {
+              p.ws_acc[slot * D + e] += y;
+            } else {
+              __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + at + e;
+              *dst = __float2bfloat16_rn(__bfloat162float(*dst) + y);
+            }
+          }
+        }
       }
       release();
       tc_fence_before();  // O may be overwritten once the next unit's weights are there
@@ -604,6 +637,43 @@ pk_status check_tree(const pk_cache_desc *d, int32_t num_q_heads, int32_t max_co
   return PK_OK;
 }
 
+// The partition size that the planner chooses (0: none). The kernel's CTAs each
+// take every slots-th of the units (128 rows of a sequence and KV head, over one
+// partition), so with c partitions of the longest context a launch lasts about
+//     rounds(c) * longest / c tokens,  rounds = ceil(units(c) / slots)
+// for contexts of similar length, and total / slots + half a partition for
+// ragged ones. Each partition adds a partial row of d + 2 floats, written and
+// read once, per query row: about merge tokens' worth of a CTA's time (22 ns a
+// token where two CTAs share an SM's memory bandwidth, 6 TB/s of partials).
+int32_t tree_partition(const int32_t *context_lens, int32_t num_seqs, int64_t total, int32_t longest,
+                       int32_t max_draft_len, int32_t num_q_heads, const pk_cache_desc &d) {
+  if (longest <= 1024) return 0;
+  const int64_t rows = int64_t(max_draft_len) * (num_q_heads / d.num_kv_heads);
+  const int64_t per_item = d.num_kv_heads * ((rows + kRows - 1) / kRows);
+  const double slots = 2.0 * sm_count();
+  const bool even = total * 4 >= int64_t(longest) * num_seqs * 3;
+  const double merge = double(num_seqs) * max_draft_len * num_q_heads * (d.head_dim + 2) * 8 / 6e12 / 22e-9;
+  int32_t best = 0;
+  double least = 0;
+  for (int c = 1; c <= 32; ++c) {
+    int64_t n = (int64_t(longest) + c - 1) / c;
+    n = (n + kTile - 1) / kTile * kTile;
+    n = (n + d.block_size - 1) / d.block_size * d.block_size;
+    if (c > 1 && n < 512) break;
+    int64_t items = 0;
+    for (int32_t s = 0; s < num_seqs; ++s) items += (std::max<int64_t>(context_lens[s], 1) + n - 1) / n;
+    const double rounds = std::ceil(double(items * per_item) / slots);
+    double cost = even ? rounds * double(n)
+                       : std::max(double(n), double(total * per_item) / slots + 0.5 * double(n));
+    if (c > 1) cost += merge * c;
+    if (c == 1 || cost < 0.97 * least) {
+      least = cost;
+      best = c == 1 ? 0 : int32_t(n);
+    }
+  }
+  return best;
+}
+
 }  // namespace
 
 extern "C" {
@@ -652,17 +722,7 @@ pk_status pk_tree_plan(const int32_t *context_lens, int32_t num_seqs, int32_t ma
   if (st != PK_OK) return st;
   int32_t part = partition_size > 0 && partition_size < longest ? partition_size : 0;
   if (partition_size == -1) {
-    const int64_t rows = int64_t(max_draft_len) * (num_q_heads / desc->num_kv_heads);
-    const int64_t units = desc->num_kv_heads * ((rows + 127) / 128);
-    const int64_t slots = int64_t(sm_count()) * 2;
-    const int64_t W = std::max<int64_t>(1, (total * units + slots - 1) / slots);
-    if (longest > 2 * W && longest > 1024) {
-      const int64_t k = std::max<int64_t>(1, longest / W);
-      int64_t n = (longest + k - 1) / k;
-      n = std::max<int64_t>(512, (n + 63) / 64 * 64);
-      n = (n + desc->block_size - 1) / desc->block_size * desc->block_size;
-      part = n < longest ? int32_t(n) : 0;
-    }
+    part = tree_partition(context_lens, num_seqs, total, longest, max_draft_len, num_q_heads, *desc);
   }
   *partition_out = part;
   return pk_attention_work_items(context_lens, num_seqs, part, items_out, cap, num_items_out);
