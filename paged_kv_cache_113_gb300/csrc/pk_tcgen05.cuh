@@ -44,6 +44,13 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint
          uint64_t((stride >> 4) & 0x3FFF) << 32 | 1ull << 46 | 2ull << 61;
 }
 
+// One lane of a converged warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+  return yes != 0;
+}
+
 // Instruction descriptor: bf16 operands, fp32 accumulator, M x N; B MN-major or
 // K-major (A is K-major).
 constexpr uint32_t mma_desc(int m, int n, bool b_mn) {

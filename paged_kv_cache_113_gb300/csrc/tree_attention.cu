@@ -279,56 +279,64 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int t = max(0, vt - 2); t < vt; ++t) mbar_wait(v_full(t), phase(t));
   } else if (warp == 5) {
     // ---------------- products ----------------
-    if (lane == 0) {
-      // A negative scale negates the queries, so that scores order as their
-      // exponents do.
-      const uint32_t s_desc = mma_desc(kRows, kTile, false) | (p.scale_log2 < 0.0f ? kNegateA : 0u);
-      constexpr uint32_t O_DESC = mma_desc(kRows, D, true);
-      bool ok = true;
-      int t = 0, issued = 0;  // tiles, P V products
-      auto pv = [&](int w, bool first) {
-        ok = ok && mbar_wait(p_full(w), phase(w)) && mbar_wait(v_full(w), phase(w));
-        if (!ok) return;
-        tc_fence_after();
+    // The whole warp goes over the tiles, so that descriptors and addresses are
+    // uniform values, and one elected lane issues: with the loop in one lane the
+    // issue alone took longer than the products.
+    // A negative scale negates the queries, so that scores order as their
+    // exponents do.
+    const uint32_t s_desc = mma_desc(kRows, kTile, false) | (p.scale_log2 < 0.0f ? kNegateA : 0u);
+    constexpr uint32_t O_DESC = mma_desc(kRows, D, true);
+    const uint64_t q_d = smem_desc(q_sm, 16, 1024), k_d = smem_desc(k_sm, 16, 1024);
+    const uint64_t v_d = smem_desc(v_sm, S::KV_SLAB, 1024);
+    constexpr uint64_t NEXT = S::KV_BYTES / 16;  // a descriptor's address counts 16 bytes
+    bool ok = true;
+    auto wait = [&](uint32_t b, uint32_t parity) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(b, parity));
+      return ok;
+    };
+    int t = 0, issued = 0;  // tiles, P V products
+    auto pv = [&](int w, bool first) {
+      if (!wait(p_full(w), phase(w)) || !wait(v_full(w), phase(w))) return;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t d = v_d + (w & 1 ? NEXT : 0);
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
           for (int ks = 0; ks < kTile / 16; ++ks)
-            tc_mma_ts(t_o, t_s(w) + 32 * half + 8 * ks,
-                      smem_desc(v_sm + uint32_t(w & 1) * S::KV_BYTES + ks * 2048, S::KV_SLAB, 1024), O_DESC,
-                      !first || half > 0 || ks > 0);
+            tc_mma_ts(t_o, t_s(w) + 32 * half + 8 * ks, d + ks * 128, O_DESC, !first || half > 0 || ks > 0);
         tc_commit(v_empty(w));
         tc_commit(o_done(w));
-        issued = w + 1;
-      };
-      for (int i = 0; ok; ++i) {
-        ok = mbar_wait(u_full(i), u_phase(i));
-        if (!ok) break;
-        const int nt = units[i % kUnits].nt;
-        const bool last = units[i % kUnits].s < 0;
-        mbar_arrive(u_empty(i));
-        if (last) break;
-        ok = mbar_wait(q_ready, i & 1);
-        for (int j = 0; j < nt && ok; ++j, ++t) {
-          // The score tile holds the weights of tile t - 2 until their product ends.
-          ok = mbar_wait(k_full(t), phase(t)) && (t < 2 || mbar_wait(o_done(t), phase(t - 2)));
-          if (!ok) break;
-          tc_fence_after();
+      }
+      issued = w + 1;
+    };
+    for (int i = 0; wait(u_full(i), u_phase(i)); ++i) {
+      const int nt = units[i % kUnits].nt;
+      const bool last = units[i % kUnits].s < 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(u_empty(i));
+      if (last || !wait(q_ready, i & 1)) break;
+      for (int j = 0; j < nt; ++j, ++t) {
+        // The score tile holds the weights of tile t - 2 until their product ends.
+        if (!wait(k_full(t), phase(t)) || (t >= 2 && !wait(o_done(t), phase(t - 2)))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t d = k_d + (t & 1 ? NEXT : 0);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
-            tc_mma_ss(t_s(t), smem_desc(q_sm + (ks / 4) * S::Q_SLAB + (ks % 4) * 32, 16, 1024),
-                      smem_desc(k_sm + uint32_t(t & 1) * S::KV_BYTES + (ks / 4) * S::KV_SLAB + (ks % 4) * 32, 16, 1024),
-                      s_desc, ks > 0);
+            tc_mma_ss(t_s(t), q_d + (ks / 4) * (S::Q_SLAB / 16) + (ks % 4) * 2,
+                      d + (ks / 4) * (S::KV_SLAB / 16) + (ks % 4) * 2, s_desc, ks > 0);
           tc_commit(k_empty(t));
           tc_commit(s_full(t));
-          if (j > 0) pv(t - 1, j == 1);
         }
-        if (ok) pv(t - 1, nt == 1);
+        if (j > 0) pv(t - 1, j == 1);
       }
-      if (!ok) timeout();
-      // Nothing of the tensor cores' is under way when tensor memory is freed.
-      for (int w = max(0, issued - 2); w < issued; ++w) mbar_wait(o_done(w), phase(w));
+      if (ok) pv(t - 1, nt == 1);
+      if (!ok) break;
     }
+    if (!ok && lane == 0) timeout();
+    // Nothing of the tensor cores' is under way when tensor memory is freed.
+    for (int w = max(0, issued - 2); w < issued; ++w) mbar_wait(o_done(w), phase(w));
     __syncwarp();
   } else {
     // ---------------- softmax: a thread is a row ----------------
