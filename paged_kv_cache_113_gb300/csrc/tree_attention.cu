@@ -11,10 +11,9 @@
 // CTA holds 128 rows, one lane of tensor memory each, and goes over its keys in
 // tiles of 64 tokens:
 //   producer warp   TMA loads of each block's K and V into two rings;
-//   product warp    one thread issues S_j = Q K_j^T (128 x 64) and, once the
-//                   weights are there, O += P_j V_j, P_j read from tensor
-//                   memory; S_{j+1} is issued before P_j V_j, so that it runs
-//                   under the softmax of tile j;
+//   score warp      S_j = Q K_j^T (128 x 64), two tiles' worth ahead of
+//   value warp      O += P_j V_j, P_j read from tensor memory, so that products
+//                   run under the softmax of the tile between;
 //   softmax warps   a thread owns a row: reads its 64 scores, masks them,
 //                   keeps the running maximum and sum, and writes the weights
 //                   over the scores.
@@ -51,7 +50,10 @@ namespace {
 
 constexpr int kRows = 128;          // query rows of a CTA
 constexpr int kTile = 64;           // tokens of a tile
-constexpr int kThreads = 192;       // 4 softmax warps, the producer, the product warp
+constexpr int kThreads = 256;       // 4 softmax warps, the producer, two product warps, one idle
+// Registers: 256 threads of 128 at launch, of which the softmax warps' four take
+// 176 each and the other four leave themselves 80 (176 + 80 = 2 x 128).
+constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
 constexpr uint32_t kTmemCols = 256;
 // Units known ahead. The producer's look-ahead is three tiles, so three units
 // at most, and it is two tiles ahead of the softmax: eight places never leave
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(u_full(i), 1);
-      mbar_init(u_empty(i), 6);  // the softmax warps, the product thread, the producer
+      mbar_init(u_empty(i), 7);  // every warp
     }
     fence_barrier_init();
   }
@@ -146,6 +148,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t tmem = tmem_slot;
   const uint32_t t_o = tmem + 128;                             // O: columns 128 .. 128 + D
   auto t_s = [&](int t) { return tmem + 64u * uint32_t(t & 1); };  // S_t, then P_t: hi 32 columns, lo 32
+  // A wait of the whole warp, which converges on it (tensor memory is accessed
+  // by whole warps); once one has failed, so do all.
+  auto warp_wait = [](uint32_t b, uint32_t parity, bool &ok) {
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(b, parity));
+    return ok;
+  };
   auto q_row = [&](int q0, int row, int kvh) {  // element offset of a row of q and out
     return (size_t(q0 + row / G) * p.num_q_heads + kvh * G + row % G) * D;
   };
@@ -153,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   if (warp == 4) {
     // ---------------- producer ----------------
+    setmaxnreg_dec<kOtherRegs>();
     if (lane == 0) {
       prefetch_tensormap(&kmap);
       prefetch_tensormap(&vmap);
@@ -278,50 +287,31 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int t = max(0, kt - 2); t < kt; ++t) mbar_wait(k_full(t), phase(t));
     for (int t = max(0, vt - 2); t < vt; ++t) mbar_wait(v_full(t), phase(t));
   } else if (warp == 5) {
-    // ---------------- products ----------------
+    // ---------------- scores ----------------
+    setmaxnreg_dec<kOtherRegs>();
     // The whole warp goes over the tiles, so that descriptors and addresses are
-    // uniform values, and one elected lane issues: with the loop in one lane the
-    // issue alone took longer than the products.
+    // uniform values, and one elected lane issues. Scores and values have a warp
+    // each: a wait on a barrier costs some 200 cycles even when its phase has
+    // ended, and in one warp the waits and issues of both took longer than the
+    // products. Every order between the two is by barrier.
     // A negative scale negates the queries, so that scores order as their
     // exponents do.
     const uint32_t s_desc = mma_desc(kRows, kTile, false) | (p.scale_log2 < 0.0f ? kNegateA : 0u);
-    constexpr uint32_t O_DESC = mma_desc(kRows, D, true);
     const uint64_t q_d = smem_desc(q_sm, 16, 1024), k_d = smem_desc(k_sm, 16, 1024);
-    const uint64_t v_d = smem_desc(v_sm, S::KV_SLAB, 1024);
-    constexpr uint64_t NEXT = S::KV_BYTES / 16;  // a descriptor's address counts 16 bytes
     bool ok = true;
-    auto wait = [&](uint32_t b, uint32_t parity) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(b, parity));
-      return ok;
-    };
-    int t = 0, issued = 0;  // tiles, P V products
-    auto pv = [&](int w, bool first) {
-      if (!wait(p_full(w), phase(w)) || !wait(v_full(w), phase(w))) return;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t d = v_d + (w & 1 ? NEXT : 0);
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks)
-            tc_mma_ts(t_o, t_s(w) + 32 * half + 8 * ks, d + ks * 128, O_DESC, !first || half > 0 || ks > 0);
-        tc_commit(v_empty(w));
-        tc_commit(o_done(w));
-      }
-      issued = w + 1;
-    };
-    for (int i = 0; wait(u_full(i), u_phase(i)); ++i) {
+    int t = 0;
+    for (int i = 0; warp_wait(u_full(i), u_phase(i), ok); ++i) {
       const int nt = units[i % kUnits].nt;
       const bool last = units[i % kUnits].s < 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(u_empty(i));
-      if (last || !wait(q_ready, i & 1)) break;
+      if (last || !warp_wait(q_ready, i & 1, ok)) break;
       for (int j = 0; j < nt; ++j, ++t) {
         // The score tile holds the weights of tile t - 2 until their product ends.
-        if (!wait(k_full(t), phase(t)) || (t >= 2 && !wait(o_done(t), phase(t - 2)))) break;
+        if (!warp_wait(k_full(t), phase(t), ok) || (t >= 2 && !warp_wait(o_done(t), phase(t - 2), ok))) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t d = k_d + (t & 1 ? NEXT : 0);
+          const uint64_t d = k_d + (t & 1 ? S::KV_BYTES / 16 : 0);  // a descriptor's address counts 16 bytes
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
             tc_mma_ss(t_s(t), q_d + (ks / 4) * (S::Q_SLAB / 16) + (ks % 4) * 2,
@@ -329,27 +319,53 @@ __global__ void __launch_bounds__(kThreads, 2)
           tc_commit(k_empty(t));
           tc_commit(s_full(t));
         }
-        if (j > 0) pv(t - 1, j == 1);
       }
-      if (ok) pv(t - 1, nt == 1);
       if (!ok) break;
     }
     if (!ok && lane == 0) timeout();
-    // Nothing of the tensor cores' is under way when tensor memory is freed.
-    for (int w = max(0, issued - 2); w < issued; ++w) mbar_wait(o_done(w), phase(w));
+    // Nothing of this warp's products is under way when tensor memory is freed.
+    for (int w = max(0, t - 2); w < t; ++w) mbar_wait(s_full(w), phase(w));
     __syncwarp();
-  } else {
+  } else if (warp == 6) {
+    // ---------------- weights times values ----------------
+    setmaxnreg_dec<kOtherRegs>();
+    constexpr uint32_t O_DESC = mma_desc(kRows, D, true);
+    const uint64_t v_d = smem_desc(v_sm, S::KV_SLAB, 1024);
+    bool ok = true;
+    int t = 0;
+    for (int i = 0; warp_wait(u_full(i), u_phase(i), ok); ++i) {
+      const int nt = units[i % kUnits].nt;
+      const bool last = units[i % kUnits].s < 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(u_empty(i));
+      if (last) break;
+      for (int j = 0; j < nt; ++j, ++t) {
+        if (!warp_wait(v_full(t), phase(t), ok) || !warp_wait(p_full(t), phase(t), ok)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t d = v_d + (t & 1 ? S::KV_BYTES / 16 : 0);
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int ks = 0; ks < kTile / 16; ++ks)
+              tc_mma_ts(t_o, t_s(t) + 32 * half + 8 * ks, d + ks * 128, O_DESC, j > 0 || half > 0 || ks > 0);
+          tc_commit(v_empty(t));
+          tc_commit(o_done(t));
+        }
+      }
+      if (!ok) break;
+    }
+    if (!ok && lane == 0) timeout();
+    for (int w = max(0, t - 2); w < t; ++w) mbar_wait(o_done(w), phase(w));
+    __syncwarp();
+  } else if (warp < 4) {
     // ---------------- softmax: a thread is a row ----------------
+    setmaxnreg_inc<kSoftmaxRegs>();
     const int r = threadIdx.x;
     const uint32_t lane_base = uint32_t(warp * 32) << 16;
     const float sl = fabsf(p.scale_log2);
-    // A wait of the whole warp (which converges on it): tensor memory is
-    // accessed by whole warps.
     bool ok = true;
-    auto wait = [&](uint32_t b, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, mbar_wait(b, parity));
-      return ok;
-    };
+    auto wait = [&](uint32_t b, uint32_t parity) { return warp_wait(b, parity, ok); };
     // A unit's queries into shared memory, rows past the last as zeros.
     auto load_q = [&](const Unit &c) {
       for (int i = r; i < kRows * (D / 8); i += 128) {
@@ -585,6 +601,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       tc_fence_before();  // O may be overwritten once the next unit's weights are there
     }
     if (!ok && lane == 0) timeout();
+  } else {
+    setmaxnreg_dec<kOtherRegs>();
   }
   tc_fence_before();
   __syncthreads();
