@@ -50,6 +50,7 @@ namespace {
 
 constexpr int kRows = 128;          // query rows of a CTA
 constexpr int kTile = 64;           // tokens of a tile
+constexpr int kPair = 2 * kTile;    // tokens whose scores are computed at once
 constexpr int kThreads = 256;       // 4 softmax warps, the producer, two product warps, one idle
 // Registers: 256 threads of 128 at launch, of which the softmax warps' four take
 // 176 each and the other four leave themselves 80 (176 + 80 = 2 x 128).
@@ -74,10 +75,10 @@ int sm_count() {
 template <int D, int BS>
 struct TreeShape {
   static constexpr int SLABS = D / 64;               // 128-byte column slabs
-  static constexpr int Q_SLAB = kRows * 128, KV_SLAB = kTile * 128;
-  static constexpr int Q_BYTES = SLABS * Q_SLAB, KV_BYTES = SLABS * KV_SLAB;
-  static constexpr int BPT = kTile / BS;             // blocks per tile
-  static constexpr int SMEM_BYTES = 1024 + Q_BYTES + 4 * KV_BYTES;  // Q, two K and two V tiles
+  static constexpr int Q_SLAB = kRows * 128, K_SLAB = kPair * 128, V_SLAB = kTile * 128;
+  static constexpr int Q_BYTES = SLABS * Q_SLAB, K_BYTES = SLABS * K_SLAB, V_BYTES = SLABS * V_SLAB;
+  static constexpr int BPT = kTile / BS, BPP = kPair / BS;  // blocks per tile, per pair
+  static constexpr int SMEM_BYTES = 1024 + Q_BYTES + K_BYTES + 2 * V_BYTES;
 };
 
 // A unit of work: 128 rows of one (sequence, KV head) over one partition.
@@ -85,7 +86,7 @@ struct Unit {
   int s, kvh, part;
   int q0, n, ctx, np;  // as SeqRows
   int r0, rows;        // its rows
-  int start, end, nt;  // its tokens and tiles; s < 0: no more units
+  int start, end, nt;  // its tokens and tiles (the last pair may be half); s < 0: no more units
 };
 
 template <int D, int BS>
@@ -96,44 +97,39 @@ __global__ void __launch_bounds__(kThreads, 2)
   launch_dependents();  // the merge may be scheduled as this grid drains
   extern __shared__ uint8_t smem_raw[];
   const uint32_t q_sm = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const uint32_t k_sm = q_sm + S::Q_BYTES, v_sm = k_sm + 2 * S::KV_BYTES;
-  __shared__ __align__(8) uint64_t bars[16 + 2 * kUnits];
+  const uint32_t k_sm = q_sm + S::Q_BYTES, v_sm = k_sm + S::K_BYTES;
+  __shared__ __align__(8) uint64_t bars[12 + 2 * kUnits];
   __shared__ Unit units[kUnits];
   __shared__ uint32_t tmem_slot;
   __shared__ int poisoned[2];
   auto bar = [&](int i) { return smem_addr(bars + i); };
-  // Tiles t and units i are counted over the whole life of the CTA; of what a
-  // tile uses there are two, which alternate. Every wait names a phase of which the one before has
-  // ended for certain and the one after cannot have: a wait by parity tells
-  // neighbouring phases apart, not more. So the products' ends alternate too:
-  // when tile t's scores are there, product t - 2 has ended, t - 1 may not have.
+  // Units i, pairs g and, as the last pair of a unit may be half, second halves f
+  // are counted over the whole life of the CTA; a barrier's phase is the count of
+  // what uses it. Every wait names a phase of which the one before has ended for
+  // certain and the one after cannot have: a wait by parity tells neighbouring
+  // phases apart, not more.
   const uint32_t q_ready = bar(0), u_done = bar(1);
-  auto s_full = [&](int t) { return bar(2 + (t & 1)); };
-  auto p_full = [&](int t) { return bar(4 + (t & 1)); };
-  auto o_done = [&](int t) { return bar(6 + (t & 1)); };
-  auto k_full = [&](int t) { return bar(8 + (t & 1)); };
-  auto k_empty = [&](int t) { return bar(10 + (t & 1)); };
-  auto v_full = [&](int t) { return bar(12 + (t & 1)); };
-  auto v_empty = [&](int t) { return bar(14 + (t & 1)); };
-  auto u_full = [&](int i) { return bar(16 + i % kUnits); };
-  auto u_empty = [&](int i) { return bar(16 + kUnits + i % kUnits); };
+  const uint32_t k_full = bar(2), k_empty = bar(3), s_full = bar(4);  // by pair
+  auto p_full = [&](int h) { return bar(5 + h); };                     // by half
+  auto o_done = [&](int h) { return bar(7 + h); };
+  auto v_full = [&](int h) { return bar(9 + h); };
+  auto u_full = [&](int i) { return bar(12 + i % kUnits); };
+  auto u_empty = [&](int i) { return bar(12 + kUnits + i % kUnits); };
   auto u_phase = [](int i) { return uint32_t(i / kUnits) & 1u; };
-  auto phase = [](int t) { return uint32_t(t >> 1) & 1u; };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.group;
   if (threadIdx.x == 0) {
     mbar_init(q_ready, 128);
     mbar_init(u_done, 4);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(s_full(i), 1);
-      mbar_init(p_full(i), 4);
-      mbar_init(o_done(i), 1);
-      mbar_init(k_full(i), 1);
-      mbar_init(k_empty(i), 1);
-      mbar_init(v_full(i), 1);
-      mbar_init(v_empty(i), 1);
-      poisoned[i] = 0;
+    mbar_init(k_full, 1);
+    mbar_init(k_empty, 1);
+    mbar_init(s_full, 1);
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(p_full(h), 4);
+      mbar_init(o_done(h), 1);
+      mbar_init(v_full(h), 1);
+      poisoned[h] = 0;
     }
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(u_full(i), 1);
@@ -147,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const uint32_t t_o = tmem + 128;                             // O: columns 128 .. 128 + D
-  auto t_s = [&](int t) { return tmem + 64u * uint32_t(t & 1); };  // S_t, then P_t: hi 32 columns, lo 32
+  auto t_s = [&](int h) { return tmem + 64u * h; };  // a half's scores, then its weights: hi 32 columns, lo 32
   // A wait of the whole warp, which converges on it (tensor memory is accessed
   // by whole warps); once one has failed, so do all.
   auto warp_wait = [](uint32_t b, uint32_t parity, bool &ok) {
@@ -219,73 +215,80 @@ __global__ void __launch_bounds__(kThreads, 2)
       ++published;
       return to;
     };
-    // A tile to load: the lane's block of it, read from the table ahead of time.
-    struct Tile {
-      int phys, nblk, kvh, s;  // nblk 0: no more tiles
+    // A pair of tiles to load: the lane's block of it, read from the table ahead
+    // of time.
+    struct Pair {
+      int phys, nblk, kvh, s;  // nblk 0: no more
     };
-    const Unit *at = nullptr;  // the unit that `next` is in, and the tile there
-    int at_j = 0, at_nt = 0;
+    const Unit *at = nullptr;  // the unit that `next` is in, and its pairs so far
+    int at_g = 0, at_n = 0;
     auto next = [&] {
-      Tile tl{0, 0, 0, 0};
-      if (at && ++at_j == at_nt) at = nullptr;
+      Pair x{0, 0, 0, 0};
+      if (at && ++at_g == at_n) at = nullptr;
       if (!at) {
         const Unit *c = publish();
-        if (c && c->s >= 0) at = c, at_j = 0, at_nt = c->nt;
+        if (c && c->s >= 0) at = c, at_g = 0, at_n = (c->nt + 1) / 2;
       }
       if (at) {
         const int nb = (at->end - at->start + BS - 1) / BS;
-        tl.nblk = min(S::BPT, nb - at_j * S::BPT);
-        tl.kvh = at->kvh;
-        tl.s = at->s;
-        if (lane < tl.nblk)
-          tl.phys = __ldg(p.tables + size_t(at->s) * p.max_blocks + at->start / BS + at_j * S::BPT + lane);
-        if (at_j == at_nt - 1) {
+        x.nblk = min(S::BPP, nb - at_g * S::BPP);
+        x.kvh = at->kvh;
+        x.s = at->s;
+        if (lane < x.nblk)
+          x.phys = __ldg(p.tables + size_t(at->s) * p.max_blocks + at->start / BS + at_g * S::BPP + lane);
+        if (x.phys < 0 || x.phys >= p.num_blocks) {
+          record_error(&g_rows_error, PK_DEVERR_BLOCK_ID, at->s);
+          x.phys = 0;  // stay in bounds and keep the byte count; the result is flagged
+        }
+        if (at_g == at_n - 1) {
           __syncwarp();
           if (lane == 0) mbar_arrive(u_empty(published - 1));  // done with the unit's entry
         }
       }
-      return tl;
+      return x;
     };
-    // Tile t's K (or V) blocks into their slot.
-    auto load = [&](const CUtensorMap *map, uint32_t ring, uint32_t full, int t, Tile tl) {
-      if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(tl.nblk * S::SLABS * BS * 128));
+    // The blocks [b0, b0 + n) of a pair into dst, their rows' slabs `slab` apart.
+    auto load = [&](const CUtensorMap *map, uint32_t dst, int slab, uint32_t full, const Pair &x, int b0, int n) {
+      if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(n * S::SLABS * BS * 128));
       __syncwarp();
-      if (lane < tl.nblk) {
-        if (tl.phys < 0 || tl.phys >= p.num_blocks) {
-          record_error(&g_rows_error, PK_DEVERR_BLOCK_ID, tl.s);
-          tl.phys = 0;  // stay in bounds and keep the byte count; the result is flagged
-        }
-        const uint32_t dst = ring + uint32_t(t & 1) * S::KV_BYTES + lane * BS * 128;
+      if (lane >= b0 && lane < b0 + n) {
 #pragma unroll
         for (int h = 0; h < S::SLABS; ++h)
-          tma_load_3d(dst + h * S::KV_SLAB, map, full, h * 64, tl.kvh, tl.phys * BS);
+          tma_load_3d(dst + h * slab + (lane - b0) * BS * 128, map, full, h * 64, x.kvh, x.phys * BS);
       }
     };
-    // K runs one tile ahead of V, whose slots come free later, and the block
-    // table two tiles ahead, across units.
-    int kt = 0, vt = 0;  // K and V tiles loaded so far
-    Tile a{0, 0, 0, 0}, b = a;
+    // A pair's K goes when the scores of the one before are done, its V tiles when
+    // the products before have ended; the block table is read two pairs ahead,
+    // across units.
+    int g = 0, f = 0;  // pairs whose V, and second halves whose V, are loaded
+    Pair a{0, 0, 0, 0}, b = a;
     for (bool more = true; ok && (more || a.nblk || b.nblk);) {
-      Tile c{0, 0, 0, 0};
+      Pair c{0, 0, 0, 0};
       if (more) c = next();
       more = more && c.nblk;
-      if (b.nblk) {
-        if (!(ok = ok && (kt < 2 || mbar_wait(k_empty(kt), phase(kt - 2))))) break;
-        load(&kmap, k_sm, k_full(kt), kt, b);
-        ++kt;
-      }
       if (a.nblk) {
-        if (!(ok = ok && (vt < 2 || mbar_wait(v_empty(vt), phase(vt - 2))))) break;
-        load(&vmap, v_sm, v_full(vt), vt, a);
-        ++vt;
+        // o_done(0) of pair g - 1 is its phase g - 1.
+        if (!(ok = ok && (g < 1 || mbar_wait(o_done(0), (g - 1) & 1)))) break;
+        load(&vmap, v_sm, S::V_SLAB, v_full(0), a, 0, min(a.nblk, S::BPT));
+        if (a.nblk > S::BPT) {
+          if (!(ok = f < 1 || mbar_wait(o_done(1), (f - 1) & 1))) break;
+          load(&vmap, v_sm + S::V_BYTES, S::V_SLAB, v_full(1), a, S::BPT, a.nblk - S::BPT);
+          ++f;
+        }
+        ++g;
+      }
+      if (b.nblk) {
+        // Pair g's K: the scores of pair g - 1 are done.
+        if (!(ok = ok && (g < 1 || mbar_wait(k_empty, (g - 1) & 1)))) break;
+        load(&kmap, k_sm, S::K_SLAB, k_full, b, 0, b.nblk);
       }
       a = b;
       b = c;
     }
     if (!ok && lane == 0) timeout();
     // Let every issued copy land before the warp leaves.
-    for (int t = max(0, kt - 2); t < kt; ++t) mbar_wait(k_full(t), phase(t));
-    for (int t = max(0, vt - 2); t < vt; ++t) mbar_wait(v_full(t), phase(t));
+    if (g > 0) mbar_wait(k_full, (g - 1) & 1), mbar_wait(v_full(0), (g - 1) & 1);
+    if (f > 0) mbar_wait(v_full(1), (f - 1) & 1);
   } else if (warp == 5) {
     // ---------------- scores ----------------
     setmaxnreg_dec<kOtherRegs>();
@@ -296,67 +299,75 @@ __global__ void __launch_bounds__(kThreads, 2)
     // products. Every order between the two is by barrier.
     // A negative scale negates the queries, so that scores order as their
     // exponents do.
-    const uint32_t s_desc = mma_desc(kRows, kTile, false) | (p.scale_log2 < 0.0f ? kNegateA : 0u);
+    const uint32_t s_desc = mma_desc(kRows, kPair, false) | (p.scale_log2 < 0.0f ? kNegateA : 0u);
     const uint64_t q_d = smem_desc(q_sm, 16, 1024), k_d = smem_desc(k_sm, 16, 1024);
     bool ok = true;
-    int t = 0;
+    int g = 0, f = 0;
+    bool whole = false;  // the pair before had a second half
     for (int i = 0; warp_wait(u_full(i), u_phase(i), ok); ++i) {
       const int nt = units[i % kUnits].nt;
       const bool last = units[i % kUnits].s < 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(u_empty(i));
       if (last || !warp_wait(q_ready, i & 1, ok)) break;
-      for (int j = 0; j < nt; ++j, ++t) {
-        // The score tile holds the weights of tile t - 2 until their product ends.
-        if (!warp_wait(k_full(t), phase(t), ok) || (t >= 2 && !warp_wait(o_done(t), phase(t - 2), ok))) break;
+      for (int j = 0; j < nt; j += 2, ++g) {
+        // The score columns hold the weights of the pair before until its last
+        // product ends (products end in order).
+        if (!warp_wait(k_full, g & 1, ok)) break;
+        if (g > 0 && !(whole ? warp_wait(o_done(1), (f - 1) & 1, ok) : warp_wait(o_done(0), (g - 1) & 1, ok))) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t d = k_d + (t & 1 ? S::KV_BYTES / 16 : 0);  // a descriptor's address counts 16 bytes
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            tc_mma_ss(t_s(t), q_d + (ks / 4) * (S::Q_SLAB / 16) + (ks % 4) * 2,
-                      d + (ks / 4) * (S::KV_SLAB / 16) + (ks % 4) * 2, s_desc, ks > 0);
-          tc_commit(k_empty(t));
-          tc_commit(s_full(t));
+          for (int ks = 0; ks < D / 16; ++ks)  // a descriptor's address counts 16 bytes
+            tc_mma_ss(tmem, q_d + (ks / 4) * (S::Q_SLAB / 16) + (ks % 4) * 2,
+                      k_d + (ks / 4) * (S::K_SLAB / 16) + (ks % 4) * 2, s_desc, ks > 0);
+          tc_commit(k_empty);
+          tc_commit(s_full);
         }
+        whole = j + 1 < nt;
+        f += whole;
       }
       if (!ok) break;
     }
     if (!ok && lane == 0) timeout();
     // Nothing of this warp's products is under way when tensor memory is freed.
-    for (int w = max(0, t - 2); w < t; ++w) mbar_wait(s_full(w), phase(w));
+    if (g > 0) mbar_wait(s_full, (g - 1) & 1);
     __syncwarp();
   } else if (warp == 6) {
     // ---------------- weights times values ----------------
     setmaxnreg_dec<kOtherRegs>();
     constexpr uint32_t O_DESC = mma_desc(kRows, D, true);
-    const uint64_t v_d = smem_desc(v_sm, S::KV_SLAB, 1024);
+    const uint64_t v_d = smem_desc(v_sm, S::V_SLAB, 1024);
     bool ok = true;
-    int t = 0;
+    int g = 0, f = 0;
     for (int i = 0; warp_wait(u_full(i), u_phase(i), ok); ++i) {
       const int nt = units[i % kUnits].nt;
       const bool last = units[i % kUnits].s < 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(u_empty(i));
       if (last) break;
-      for (int j = 0; j < nt; ++j, ++t) {
-        if (!warp_wait(v_full(t), phase(t), ok) || !warp_wait(p_full(t), phase(t), ok)) break;
+      for (int j = 0; j < nt; ++j) {
+        const int h = j & 1;
+        const uint32_t phase = uint32_t(h ? f : g) & 1u;
+        if (!warp_wait(v_full(h), phase, ok) || !warp_wait(p_full(h), phase, ok)) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t d = v_d + (t & 1 ? S::KV_BYTES / 16 : 0);
+          const uint64_t d = v_d + (h ? S::V_BYTES / 16 : 0);
 #pragma unroll
           for (int half = 0; half < 2; ++half)
 #pragma unroll
             for (int ks = 0; ks < kTile / 16; ++ks)
-              tc_mma_ts(t_o, t_s(t) + 32 * half + 8 * ks, d + ks * 128, O_DESC, j > 0 || half > 0 || ks > 0);
-          tc_commit(v_empty(t));
-          tc_commit(o_done(t));
+              tc_mma_ts(t_o, t_s(h) + 32 * half + 8 * ks, d + ks * 128, O_DESC, j > 0 || half > 0 || ks > 0);
+          tc_commit(o_done(h));  // and the V tile is free
         }
+        f += h;
+        g += h || j + 1 == nt;
       }
       if (!ok) break;
     }
     if (!ok && lane == 0) timeout();
-    for (int w = max(0, t - 2); w < t; ++w) mbar_wait(o_done(w), phase(w));
+    if (g > 0) mbar_wait(o_done(0), (g - 1) & 1);
+    if (f > 0) mbar_wait(o_done(1), (f - 1) & 1);
     __syncwarp();
   } else if (warp < 4) {
     // ---------------- softmax: a thread is a row ----------------
@@ -382,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_arrive(q_ready);
     };
     bool loaded = false;  // the unit's queries were loaded under the one before
-    for (int i = 0, t = 0; wait(u_full(i), u_phase(i)); ++i) {
+    for (int i = 0, g = 0, f = 0; wait(u_full(i), u_phase(i)); ++i) {
       const Unit &c = units[i % kUnits];  // read where it is needed: registers are short
       auto release = [&] {
         __syncwarp();
@@ -400,15 +411,16 @@ __global__ void __launch_bounds__(kThreads, 2)
       // The drafts that this thread's row sees.
       auto row_mask = [&] { return r < c.rows ? draft_mask(p, c.q0, (c.r0 + r) / G, c.n) : 0; };
       float ref = -INFINITY, l = 0.0f;  // the exponent's reference (scaled scores), the sum
-      for (int j = 0; j < nt; ++j, ++t) {
-        const int t0 = start + j * kTile;
+      for (int j = 0; j < nt; ++j) {
+        const int t0 = start + j * kTile, h = j & 1;
+        const uint32_t phase = uint32_t(h ? f : g) & 1u;
         const bool careful = t0 + kTile > lim;
-        if (!wait(s_full(t), phase(t))) break;
+        if (h == 0 && !wait(s_full, g & 1)) break;
         tc_fence_after();
         uint32_t x[2][32];
         if (busy) {
-          tmem_load32(t_s(t) + lane_base, x[0]);
-          tmem_load32(t_s(t) + lane_base + 32, x[1]);
+          tmem_load32(t_s(h) + lane_base, x[0]);
+          tmem_load32(t_s(h) + lane_base + 32, x[1]);
         }
         if (j == nt - 1) {
           // The unit's last scores are there, so its queries are done with: the
@@ -422,12 +434,12 @@ __global__ void __launch_bounds__(kThreads, 2)
           // values past the end are zeroed, and so is what is not finite in the
           // drafts' values, which would reach rows that do not see it (0 * NaN);
           // the rows that do see it get it at the end.
-          if (!wait(v_full(t), phase(t))) break;
-          const uint32_t vb = v_sm + uint32_t(t & 1) * S::KV_BYTES;
+          if (!wait(v_full(h), phase)) break;
+          const uint32_t vb = v_sm + (h ? S::V_BYTES : 0);
           const int first = max(0, lim - t0), valid = min(kTile, c.end - t0);
           for (int k = first * (D / 8) + r; k < kTile * (D / 8); k += 128) {
             const int row = k / (D / 8), ch = k % (D / 8);
-            const uint32_t a = vb + (ch >> 3) * S::KV_SLAB + row * 128 + (ch & 7) * 16;
+            const uint32_t a = vb + (ch >> 3) * S::V_SLAB + row * 128 + (ch & 7) * 16;
             uint32_t w[4] = {0, 0, 0, 0};
             bool dirty = row >= valid;
             if (!dirty) {
@@ -455,12 +467,12 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (careful) {
             const uint64_t see = see64(row_mask(), c.ctx - c.n, t0);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t w = uint32_t(see >> (32 * h));
-              const int live = c.end - t0 - 32 * h;
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t w = uint32_t(see >> (32 * e));
+              const int live = c.end - t0 - 32 * e;
 #pragma unroll
               for (int k = 0; k < 32; ++k)
-                if (!((w >> k) & 1) || k >= live) x[h][k] = 0xff800000u;  // -inf
+                if (!((w >> k) & 1) || k >= live) x[e][k] = 0xff800000u;  // -inf
             }
           }
           float mx;
@@ -479,7 +491,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (move) ref = mx;
             l *= f;
             if (j > 0) {
-              if (!wait(o_done(t - 1), phase(t - 1))) break;
+              // The scores of a pair come after the products of the one before.
+              if (h == 1 && !wait(o_done(0), g & 1)) break;
               tc_fence_after();
               const uint64_t f2 = pack2(f, f);
 #pragma unroll 1
@@ -502,12 +515,12 @@ __global__ void __launch_bounds__(kThreads, 2)
           const uint64_t sl2 = pack2(sl, sl), m2 = pack2(-m, -m), minus = pack2(-1.0f, -1.0f);
           uint64_t sum2 = 0;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int e = 0; e < 2; ++e) {
             uint32_t hi[16], lo[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               float a, b;
-              unpack2(fma2(pack2(__uint_as_float(x[h][2 * k]), __uint_as_float(x[h][2 * k + 1])), sl2, m2), a, b);
+              unpack2(fma2(pack2(__uint_as_float(x[e][2 * k]), __uint_as_float(x[e][2 * k + 1])), sl2, m2), a, b);
               a = exp2_ftz(a);
               b = exp2_ftz(b);
               const uint64_t ab = pack2(a, b);
@@ -516,8 +529,8 @@ __global__ void __launch_bounds__(kThreads, 2)
               unpack2(fma2(pack2(bf16_lo(hi[k]), bf16_hi(hi[k])), minus, ab), a, b);
               lo[k] = pack_bf16x2(a, b);
             }
-            tmem_store16(t_s(t) + lane_base + 16 * h, hi);
-            tmem_store16(t_s(t) + lane_base + 32 + 16 * h, lo);
+            tmem_store16(t_s(h) + lane_base + 16 * e, hi);
+            tmem_store16(t_s(h) + lane_base + 32 + 16 * e, lo);
           }
           {
             float a, b;
@@ -528,7 +541,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(t));
+        if (lane == 0) mbar_arrive(p_full(h));
+        f += h;
+        g += h || j + 1 == nt;
       }
       if (!ok) break;
       if (loaded) q_landed();
@@ -542,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         release();
         continue;
       }
-      if (!wait(o_done(t - 1), phase(t - 1))) break;
+      if (!(nt & 1 ? wait(o_done(0), (g - 1) & 1) : wait(o_done(1), (f - 1) & 1))) break;
       tc_fence_after();
       const bool mine = r < c.rows;
       const size_t at = mine ? q_row(c.q0, c.r0 + r, c.kvh) : 0;
