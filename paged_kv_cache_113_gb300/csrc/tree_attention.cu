@@ -30,10 +30,10 @@
 // warps finish the last, so that short contexts keep memory busy too.
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <math.h>
 #include <stdint.h>
 
-#include <cmath>
+#include <new>
+#include <vector>
 
 #include "attn_rows.cuh"
 #include "pagedkv.h"
@@ -78,7 +78,8 @@ struct TreeShape {
   static constexpr int Q_SLAB = kRows * 128, K_SLAB = kPair * 128, V_SLAB = kTile * 128;
   static constexpr int Q_BYTES = SLABS * Q_SLAB, K_BYTES = SLABS * K_SLAB, V_BYTES = SLABS * V_SLAB;
   static constexpr int BPT = kTile / BS, BPP = kPair / BS;  // blocks per tile, per pair
-  static constexpr int SMEM_BYTES = 1024 + Q_BYTES + K_BYTES + 2 * V_BYTES;
+  static constexpr int STAGE_BYTES = 2048;  // per softmax warp: 64 bytes of each of its rows, on their way out
+  static constexpr int SMEM_BYTES = 1024 + Q_BYTES + K_BYTES + 2 * V_BYTES + 4 * STAGE_BYTES;
 };
 
 // A unit of work: 128 rows of one (sequence, KV head) over one partition.
@@ -564,34 +565,57 @@ __global__ void __launch_bounds__(kThreads, 2)
       const bool split = c.np > 1;
       const float inv = split ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
       const size_t slot = at / D * p.num_partitions + c.part;
+      // A lane has a row, but rows are 64 bytes or more apart in memory: 64 bytes of
+      // each go through shared memory, so that four lanes write a row's together.
+      const uint32_t stage = v_sm + 2 * S::V_BYTES + warp * S::STAGE_BYTES;
+      const size_t to = split ? slot * D * 4 : at * 2;  // byte offset of the row
+      auto put = [&](const uint32_t (&w)[16], int byte) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 64 +
+                                                                       ((e ^ ((lane >> 1) & 3)) << 4)),
+                       "r"(w[4 * e]), "r"(w[4 * e + 1]), "r"(w[4 * e + 2]), "r"(w[4 * e + 3])
+                       : "memory");
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = 8 * e + lane / 4, ch = lane & 3;
+          const size_t dst = __shfl_sync(0xffffffffu, to, row);
+          uint4 v;
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                       : "r"(stage + row * 64 + ((ch ^ ((row >> 1) & 3)) << 4)));
+          if (warp * 32 + row < c.rows)
+            *reinterpret_cast<uint4 *>((split ? reinterpret_cast<char *>(p.ws_acc) : static_cast<char *>(p.out)) +
+                                       dst + byte + ch * 16) = v;
+        }
+        __syncwarp();
+      };
 #pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
         uint32_t o[32];
         tmem_load32(t_o + lane_base + 32 * ch, o);
         tmem_wait_load(o);
-        if (mine && split) {
-          float4 *dst = reinterpret_cast<float4 *>(p.ws_acc + slot * D + 32 * ch);
+        uint32_t w[16];
+        if (split) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                 __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
-        } else if (mine) {
-          uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at + 32 * ch);
+          for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
-            dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int e = 0; e < 16; ++e) w[e] = o[16 * h + e];
+            put(w, 128 * ch + 64 * h);
           }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            w[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+          put(w, 64 * ch);
         }
-        __syncwarp();
       }
       if (mine && split) {
         p.ws_m[slot] = ref;
         p.ws_l[slot] = l;
       }
+      __syncwarp();
       if (fix && mine) {  // what is not finite in the values of the drafts that the row sees
         const uint64_t mask = row_mask();
         const int base = c.ctx - c.n;
@@ -680,20 +704,18 @@ pk_status check_tree(const pk_cache_desc *d, int32_t num_q_heads, int32_t max_co
 
 // The partition size that the planner chooses (0: none). The kernel's CTAs each
 // take every slots-th of the units (128 rows of a sequence and KV head, over one
-// partition), so with c partitions of the longest context a launch lasts about
-//     rounds(c) * longest / c tokens,  rounds = ceil(units(c) / slots)
-// for contexts of similar length, and total / slots + half a partition for
-// ragged ones. Each partition adds a partial row of d + 2 floats, written and
-// read once, per query row: about merge tokens' worth of a CTA's time (22 ns a
-// token where two CTAs share an SM's memory bandwidth, 6 TB/s of partials).
-int32_t tree_partition(const int32_t *context_lens, int32_t num_seqs, int64_t total, int32_t longest,
+// partition), longest first, so a launch lasts as long as the first CTA's: the
+// units 0, slots, 2 slots, ... of the list. Each partition of a context that is
+// split adds a partial row of d + 2 floats per query row, written and read once:
+// 6 TB/s, against 22 ns for a token of a CTA where two share an SM's bandwidth.
+int32_t tree_partition(const int32_t *context_lens, int32_t num_seqs, int32_t longest,
                        int32_t max_draft_len, int32_t num_q_heads, const pk_cache_desc &d) {
   if (longest <= 1024) return 0;
   const int64_t rows = int64_t(max_draft_len) * (num_q_heads / d.num_kv_heads);
   const int64_t per_item = d.num_kv_heads * ((rows + kRows - 1) / kRows);
-  const double slots = 2.0 * sm_count();
-  const bool even = total * 4 >= int64_t(longest) * num_seqs * 3;
-  const double merge = double(num_seqs) * max_draft_len * num_q_heads * (d.head_dim + 2) * 8 / 6e12 / 22e-9;
+  const int64_t slots = 2 * sm_count();
+  const double merge = double(max_draft_len) * num_q_heads * (d.head_dim + 2) * 8 / 6e12 / 22e-9;
+  std::vector<int32_t> count;  // items by tiles
   int32_t best = 0;
   double least = 0;
   for (int c = 1; c <= 32; ++c) {
@@ -701,12 +723,20 @@ int32_t tree_partition(const int32_t *context_lens, int32_t num_seqs, int64_t to
     n = (n + kTile - 1) / kTile * kTile;
     n = (n + d.block_size - 1) / d.block_size * d.block_size;
     if (c > 1 && n < 512) break;
-    int64_t items = 0;
-    for (int32_t s = 0; s < num_seqs; ++s) items += (std::max<int64_t>(context_lens[s], 1) + n - 1) / n;
-    const double rounds = std::ceil(double(items * per_item) / slots);
-    double cost = even ? rounds * double(n)
-                       : std::max(double(n), double(total * per_item) / slots + 0.5 * double(n));
-    if (c > 1) cost += merge * c;
+    count.assign(size_t(n / kTile + 2), 0);
+    double partials = 0;
+    for (int32_t s = 0; s < num_seqs; ++s) {
+      const int64_t len = std::max(context_lens[s], 1), whole = len / n;
+      count[size_t((n + kTile - 1) / kTile)] += int32_t(whole);
+      if (len % n) ++count[size_t((len % n + kTile - 1) / kTile)];
+      if (len > n) partials += double(whole + (len % n != 0));
+    }
+    double cost = merge * partials;
+    int64_t seen = 0, take = 0;  // units passed, the first CTA's next
+    for (size_t tiles = count.size(); tiles-- > 0;) {
+      seen += count[tiles] * per_item;
+      for (; take < seen; take += slots) cost += double(tiles * kTile) + 64.0;  // 64: a unit's own cost
+    }
     if (c == 1 || cost < 0.97 * least) {
       least = cost;
       best = c == 1 ? 0 : int32_t(n);
@@ -754,16 +784,16 @@ pk_status pk_tree_plan(const int32_t *context_lens, int32_t num_seqs, int32_t ma
   *partition_out = 0;
   *num_items_out = 0;
   int32_t longest = 1;
-  int64_t total = 0;
-  for (int32_t s = 0; s < num_seqs; ++s) {
-    longest = std::max(longest, context_lens[s]);
-    total += std::max(context_lens[s], 1);
-  }
+  for (int32_t s = 0; s < num_seqs; ++s) longest = std::max(longest, context_lens[s]);
   const pk_status st = check_tree(desc, num_q_heads, longest, std::max(partition_size, 0));
   if (st != PK_OK) return st;
   int32_t part = partition_size > 0 && partition_size < longest ? partition_size : 0;
   if (partition_size == -1) {
-    part = tree_partition(context_lens, num_seqs, total, longest, max_draft_len, num_q_heads, *desc);
+    try {
+      part = tree_partition(context_lens, num_seqs, longest, max_draft_len, num_q_heads, *desc);
+    } catch (const std::bad_alloc &) {
+      return PK_ERR_NOMEM;
+    }
   }
   *partition_out = part;
   return pk_attention_work_items(context_lens, num_seqs, part, items_out, cap, num_items_out);
