@@ -51,15 +51,14 @@ namespace {
 constexpr int kRows = 128;          // query rows of a CTA
 constexpr int kTile = 64;           // tokens of a tile
 constexpr int kPair = 2 * kTile;    // tokens whose scores are computed at once
-constexpr int kThreads = 256;       // 4 softmax warps, the producer, two product warps, one idle
+constexpr int kThreads = 256;       // 4 softmax warps, the producer, two product warps, the units'
 // Registers: 256 threads of 128 at launch, of which the softmax warps' four take
 // 176 each and the other four leave themselves 80 (176 + 80 = 2 x 128).
 constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
 constexpr uint32_t kTmemCols = 256;
-// Units known ahead. The producer's look-ahead is three tiles, so three units
-// at most, and it is two tiles ahead of the softmax: eight places never leave
-// it waiting for a unit whose tiles it has yet to load.
-constexpr int kUnits = 8;
+// Units known at a time: the softmax may be one behind the producer, which asks
+// for one more.
+constexpr int kUnits = 4;
 constexpr uint32_t kNegateA = 1u << 13;  // of an instruction descriptor
 constexpr float kSlack = 8.0f;      // log2 of how far a maximum may outgrow the reference
 
@@ -93,13 +92,14 @@ struct Unit {
 template <int D, int BS>
 __global__ void __launch_bounds__(kThreads, 2)
     attn_tree_kernel(RowsParams p, const __grid_constant__ CUtensorMap kmap,
-                     const __grid_constant__ CUtensorMap vmap, int num_units) {
+                     const __grid_constant__ CUtensorMap vmap) {
   using S = TreeShape<D, BS>;
   launch_dependents();  // the merge may be scheduled as this grid drains
   extern __shared__ uint8_t smem_raw[];
   const uint32_t q_sm = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t k_sm = q_sm + S::Q_BYTES, v_sm = k_sm + S::K_BYTES;
-  __shared__ __align__(8) uint64_t bars[12 + 2 * kUnits];
+  __shared__ __align__(8) uint64_t bars[14 + 2 * kUnits];
+  __shared__ uint4 answer;
   __shared__ Unit units[kUnits];
   __shared__ uint32_t tmem_slot;
   __shared__ int poisoned[2];
@@ -114,8 +114,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   auto p_full = [&](int h) { return bar(5 + h); };                     // by half
   auto o_done = [&](int h) { return bar(7 + h); };
   auto v_full = [&](int h) { return bar(9 + h); };
-  auto u_full = [&](int i) { return bar(12 + i % kUnits); };
-  auto u_empty = [&](int i) { return bar(12 + kUnits + i % kUnits); };
+  const uint32_t u_want = bar(11), u_answer = bar(12);
+  auto u_full = [&](int i) { return bar(14 + i % kUnits); };
+  auto u_empty = [&](int i) { return bar(14 + kUnits + i % kUnits); };
   auto u_phase = [](int i) { return uint32_t(i / kUnits) & 1u; };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -123,6 +124,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (threadIdx.x == 0) {
     mbar_init(q_ready, 128);
     mbar_init(u_done, 4);
+    mbar_init(u_want, 1);
+    mbar_init(u_answer, 1);
     mbar_init(k_full, 1);
     mbar_init(k_empty, 1);
     mbar_init(s_full, 1);
@@ -134,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(u_full(i), 1);
-      mbar_init(u_empty(i), 7);  // every warp
+      mbar_init(u_empty(i), 7);  // every warp but the one that fills them
     }
     fence_barrier_init();
   }
@@ -163,88 +166,40 @@ __global__ void __launch_bounds__(kThreads, 2)
       prefetch_tensormap(&kmap);
       prefetch_tensormap(&vmap);
     }
-    // 32 units of this CTA's share are looked up at a time, one per lane, and
-    // those with work published in order; `left` are the lanes not yet taken.
-    const int X = p.num_kv_heads * p.row_tiles, Y = p.items ? p.num_items : p.num_seqs;
-    Unit look;
-    uint32_t left = 0;
-    int next_u = blockIdx.x, published = 0;
-    auto look_up = [&](int u) {
-      const int x = u % X, y = (u / X) % Y, z = u / X / Y;
-      if (!work_item(p, y, p.num_partitions - 1 - z, x == 0, look.s, look.part)) return false;
-      const SeqRows sr = seq_rows(p, look.s, x == 0 && look.part == 0);
-      look.kvh = x / p.row_tiles;
-      look.r0 = x % p.row_tiles * kRows;
-      look.rows = min(kRows, sr.n * G - look.r0);
-      if (look.rows <= 0) return false;
-      if (sr.ctx == 0) {  // invalid length (recorded): zero rows
-        for (int i = 0; look.part == 0 && i < look.rows * (D / 8); ++i)
-          *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
-                                     q_row(sr.q0, look.r0 + i / (D / 8), look.kvh) + i % (D / 8) * 8) =
-              make_uint4(0, 0, 0, 0);
-        return false;
-      }
-      if (look.part >= sr.np) return false;
-      look.q0 = sr.q0, look.n = sr.n, look.ctx = sr.ctx, look.np = sr.np;
-      look.start = look.part * p.partition;
-      look.end = min(sr.ctx, look.start + p.partition);
-      look.nt = (look.end - look.start + kTile - 1) / kTile;
-      return true;
-    };
-    bool ok = true;
-    // Publishes the CTA's next unit (s < 0 after the last) and returns it; null
-    // when its place does not come free in time.
-    auto publish = [&]() -> const Unit * {
-      while (left == 0 && next_u < num_units) {
-        const int64_t u = next_u + int64_t(lane) * gridDim.x;
-        left = __ballot_sync(0xffffffffu, u < num_units && look_up(int(u)));
-        next_u = int(min(int64_t(num_units), next_u + 32 * int64_t(gridDim.x)));
-      }
-      const int i = published;
-      ok = ok && (i < kUnits || mbar_wait(u_empty(i), uint32_t((i - kUnits) / kUnits) & 1u));
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return nullptr;
-      Unit *to = units + i % kUnits;
-      if (left == 0) {
-        if (lane == 0) to->s = -1;
-      } else if (lane == __ffs(left) - 1) {
-        *to = look;
-      }
-      left &= left - 1;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(u_full(i));
-      ++published;
-      return to;
-    };
     // A pair of tiles to load: the lane's block of it, read from the table ahead
     // of time.
     struct Pair {
       int phys, nblk, kvh, s;  // nblk 0: no more
     };
-    const Unit *at = nullptr;  // the unit that `next` is in, and its pairs so far
-    int at_g = 0, at_n = 0;
+    const Unit *at = nullptr;  // the unit that `next` is in, its pairs so far, its number
+    int at_g = 0, at_n = 0, at_i = -1;
+    bool ok = true;
     auto next = [&] {
       Pair x{0, 0, 0, 0};
       if (at && ++at_g == at_n) at = nullptr;
       if (!at) {
-        const Unit *c = publish();
-        if (c && c->s >= 0) at = c, at_g = 0, at_n = (c->nt + 1) / 2;
+        ++at_i;
+        if (!warp_wait(u_full(at_i), u_phase(at_i), ok)) return x;
+        const Unit *c = units + at_i % kUnits;
+        if (c->s < 0) return x;
+        at = c, at_g = 0, at_n = (c->nt + 1) / 2;
       }
-      if (at) {
-        const int nb = (at->end - at->start + BS - 1) / BS;
-        x.nblk = min(S::BPP, nb - at_g * S::BPP);
-        x.kvh = at->kvh;
-        x.s = at->s;
-        if (lane < x.nblk)
-          x.phys = __ldg(p.tables + size_t(at->s) * p.max_blocks + at->start / BS + at_g * S::BPP + lane);
-        if (x.phys < 0 || x.phys >= p.num_blocks) {
-          record_error(&g_rows_error, PK_DEVERR_BLOCK_ID, at->s);
-          x.phys = 0;  // stay in bounds and keep the byte count; the result is flagged
-        }
-        if (at_g == at_n - 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(u_empty(published - 1));  // done with the unit's entry
-        }
+      // The unit after this one is asked for two pairs before the end: early enough
+      // to be here in time, late enough to go to the CTA that is free first.
+      if (at_g == max(0, at_n - 2) && lane == 0) mbar_arrive(u_want);
+      const int nb = (at->end - at->start + BS - 1) / BS;
+      x.nblk = min(S::BPP, nb - at_g * S::BPP);
+      x.kvh = at->kvh;
+      x.s = at->s;
+      if (lane < x.nblk)
+        x.phys = __ldg(p.tables + size_t(at->s) * p.max_blocks + at->start / BS + at_g * S::BPP + lane);
+      if (x.phys < 0 || x.phys >= p.num_blocks) {
+        record_error(&g_rows_error, PK_DEVERR_BLOCK_ID, at->s);
+        x.phys = 0;  // stay in bounds and keep the byte count; the result is flagged
+      }
+      if (at_g == at_n - 1) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(u_empty(at_i));  // done with the unit's entry
       }
       return x;
     };
@@ -259,17 +214,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     };
     // A pair's K goes when the scores of the one before are done, its V tiles when
-    // the products before have ended; the block table is read two pairs ahead,
-    // across units.
+    // the products before have ended; the block table is read ahead of both.
     int g = 0, f = 0;  // pairs whose V, and second halves whose V, are loaded
-    Pair a{0, 0, 0, 0}, b = a;
-    for (bool more = true; ok && (more || a.nblk || b.nblk);) {
-      Pair c{0, 0, 0, 0};
-      if (more) c = next();
-      more = more && c.nblk;
+    Pair a{0, 0, 0, 0}, b = next();
+    while (ok && (a.nblk || b.nblk)) {
       if (a.nblk) {
         // o_done(0) of pair g - 1 is its phase g - 1.
-        if (!(ok = ok && (g < 1 || mbar_wait(o_done(0), (g - 1) & 1)))) break;
+        if (!(ok = g < 1 || mbar_wait(o_done(0), (g - 1) & 1))) break;
         load(&vmap, v_sm, S::V_SLAB, v_full(0), a, 0, min(a.nblk, S::BPT));
         if (a.nblk > S::BPT) {
           if (!(ok = f < 1 || mbar_wait(o_done(1), (f - 1) & 1))) break;
@@ -280,11 +231,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       if (b.nblk) {
         // Pair g's K: the scores of pair g - 1 are done.
-        if (!(ok = ok && (g < 1 || mbar_wait(k_empty, (g - 1) & 1)))) break;
+        if (!(ok = g < 1 || mbar_wait(k_empty, (g - 1) & 1))) break;
         load(&kmap, k_sm, S::K_SLAB, k_full, b, 0, b.nblk);
       }
       a = b;
-      b = c;
+      b = a.nblk ? next() : Pair{0, 0, 0, 0};
     }
     if (!ok && lane == 0) timeout();
     // Let every issued copy land before the warp leaves.
@@ -425,9 +376,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         if (j == nt - 1) {
           // The unit's last scores are there, so its queries are done with: the
-          // next unit's come in under this tile's softmax.
-          if (!wait(u_full(i + 1), u_phase(i + 1))) break;
-          loaded = units[(i + 1) % kUnits].s >= 0;
+          // next unit's, if it is known already, come in under this tile's softmax.
+          loaded = __all_sync(0xffffffffu, mbar_test(u_full(i + 1), u_phase(i + 1))) &&
+                   units[(i + 1) % kUnits].s >= 0;
           if (loaded) load_q(units[(i + 1) % kUnits]);
         }
         if (careful) {
@@ -641,7 +592,58 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (!ok && lane == 0) timeout();
   } else {
+    // ---------------- units ----------------
+    // The grid has a CTA per unit, longest first; those that find no room are
+    // taken over, one at a time, by whichever CTA needs work next.
     setmaxnreg_dec<kOtherRegs>();
+    const int X = p.num_kv_heads * p.row_tiles, Y = p.items ? p.num_items : p.num_seqs;
+    bool ok = true;
+    int published = 0;
+    auto publish = [&](const Unit &c) {
+      const int i = published;
+      if (i >= kUnits && !warp_wait(u_empty(i), u_phase(i - kUnits), ok)) return;
+      if (lane == 0) {
+        units[i % kUnits] = c;
+        mbar_arrive(u_full(i));
+      }
+      ++published;
+    };
+    for (int u = blockIdx.x, asked = 0; u >= 0;) {
+      const int x = u % X, y = (u / X) % Y, z = u / X / Y;
+      Unit c;
+      if (work_item(p, y, p.num_partitions - 1 - z, x == 0 && lane == 0, c.s, c.part)) {
+        const SeqRows sr = seq_rows(p, c.s, x == 0 && lane == 0 && c.part == 0);
+        c.kvh = x / p.row_tiles;
+        c.r0 = x % p.row_tiles * kRows;
+        c.rows = min(kRows, sr.n * G - c.r0);
+        if (c.rows > 0 && sr.ctx == 0) {  // invalid length (recorded): zero rows
+          for (int k = lane; c.part == 0 && k < c.rows * (D / 8); k += 32)
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
+                                       q_row(sr.q0, c.r0 + k / (D / 8), c.kvh) + k % (D / 8) * 8) =
+                make_uint4(0, 0, 0, 0);
+        } else if (c.rows > 0 && c.part < sr.np) {
+          c.q0 = sr.q0, c.n = sr.n, c.ctx = sr.ctx, c.np = sr.np;
+          c.start = c.part * p.partition;
+          c.end = min(sr.ctx, c.start + p.partition);
+          c.nt = (c.end - c.start + kTile - 1) / kTile;
+          publish(c);
+          if (!ok || !warp_wait(u_want, (published - 1) & 1, ok)) break;
+        }
+      }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(u_answer, 16);
+        try_cancel(smem_addr(&answer), u_answer);
+      }
+      if (!warp_wait(u_answer, asked & 1, ok)) break;
+      ++asked;
+      u = cancelled_cta(smem_addr(&answer));
+      fence_proxy_async();  // the answer has been read before the next one is asked for
+      __syncwarp();
+    }
+    Unit end;
+    end.s = -1;
+    if (ok) publish(end);
+    if (!ok && lane == 0) timeout();
   }
   tc_fence_before();
   __syncthreads();
@@ -662,9 +664,8 @@ pk_status launch_tree(RowsParams p, const pk_cache_desc &d, cudaStream_t stream)
   p.row_tiles = (p.max_draft * p.group + kRows - 1) / kRows;
   const dim3 g = rows_grid(p);
   const int64_t units = int64_t(g.x) * g.y * g.z;
-  if (units > INT32_MAX / 2) return PK_ERR_UNSUPPORTED;
-  const int ctas = int(std::min<int64_t>(units, 2 * sm_count()));
-  kern<<<ctas, kThreads, S::SMEM_BYTES, stream>>>(p, kmap, vmap, int(units));
+  if (units > INT32_MAX) return PK_ERR_UNSUPPORTED;
+  kern<<<unsigned(units), kThreads, S::SMEM_BYTES, stream>>>(p, kmap, vmap);
   return cudaGetLastError() == cudaSuccess ? PK_OK : PK_ERR_CUDA;
 }
 
@@ -702,12 +703,14 @@ pk_status check_tree(const pk_cache_desc *d, int32_t num_q_heads, int32_t max_co
   return PK_OK;
 }
 
-// The partition size that the planner chooses (0: none). The kernel's CTAs each
-// take every slots-th of the units (128 rows of a sequence and KV head, over one
-// partition), longest first, so a launch lasts as long as the first CTA's: the
-// units 0, slots, 2 slots, ... of the list. Each partition of a context that is
-// split adds a partial row of d + 2 floats per query row, written and read once:
-// 6 TB/s, against 22 ns for a token of a CTA where two share an SM's bandwidth.
+// The partition size that the planner chooses (0: none). The units (128 rows of a
+// sequence and KV head, over one partition) go longest first to the CTA that is
+// free first, so a launch lasts about as long as its longest unit or as the mean
+// share of a CTA, whichever is more, plus what the last round leaves idle (of the
+// shortest units' length). Each partition of a context that is split adds a
+// partial row of d + 2 floats per query row, written and read once: 6 TB/s,
+// against 22 ns for a token of a CTA where two share an SM's bandwidth; a unit
+// costs about 128 tokens more than its own.
 int32_t tree_partition(const int32_t *context_lens, int32_t num_seqs, int32_t longest,
                        int32_t max_draft_len, int32_t num_q_heads, const pk_cache_desc &d) {
   if (longest <= 1024) return 0;
@@ -731,12 +734,18 @@ int32_t tree_partition(const int32_t *context_lens, int32_t num_seqs, int32_t lo
       if (len % n) ++count[size_t((len % n + kTile - 1) / kTile)];
       if (len > n) partials += double(whole + (len % n != 0));
     }
-    double cost = merge * partials;
-    int64_t seen = 0, take = 0;  // units passed, the first CTA's next
-    for (size_t tiles = count.size(); tiles-- > 0;) {
-      seen += count[tiles] * per_item;
-      for (; take < seen; take += slots) cost += double(tiles * kTile) + 64.0;  // 64: a unit's own cost
+    int64_t units = 0, tail = 0;
+    double work = 0;
+    size_t top = 0;
+    for (size_t tiles = 0; tiles < count.size(); ++tiles) {
+      if (!count[tiles]) continue;
+      if (units < slots) tail = int64_t(tiles) * kTile;  // the length that the last `slots` units reach
+      units += count[tiles] * per_item;
+      work += double(count[tiles] * per_item) * (double(tiles) * kTile + 128);
+      top = tiles;
     }
+    const double idle = double((slots - units % slots) % slots) / double(slots) * double(tail);
+    const double cost = merge * partials + std::max(double(top * kTile), work / double(slots) + idle);
     if (c == 1 || cost < 0.97 * least) {
       least = cost;
       best = c == 1 ? 0 : int32_t(n);
