@@ -535,40 +535,58 @@ def pk_swap_blocks(k_cache, v_cache, k_host, v_host, pairs, direction: int, stre
 
 
 # -- new tokens of a layer, 8-bit caches, drafted tokens ----------------------
-class _on_device:
-    """The tensors' device current for the call's launches, and a stream of it:
-    the given one, else that device's current stream."""
-
-    def __init__(self, stream, *tensors):
-        torch = _torch()
-        dev = tensors[0].device
-        for t in tensors[1:]:
-            if t is not None and t.device != dev:
-                raise ValueError("all tensors must be on one device")
-        if stream is not None and stream.device != dev:
-            raise ValueError("the stream is not on the tensors' device")
-        self.stream = ctypes.c_void_p((torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream)
-        self._guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+# These calls are short on the GPU, so the checks are kept cheap: device indices
+# as ints, raw pointers and stream handles.
+def _at(t, name, dev, dtype=None) -> int:
+    """The address of a contiguous tensor on CUDA device ``dev``."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on device {dev}, with the call's other tensors "
+                         "(libpagedkv has no CPU path)")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return t.data_ptr()
 
 
-def _heads(t, name, tokens, heads, d):
-    """Pointer and token stride of ``[tokens, heads, d]`` whose heads are contiguous."""
-    if not t.is_cuda:
+def _cuda_device(t, name) -> int:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor (libpagedkv has no CPU path)")
-    if tuple(t.shape) != (tokens, heads, d):
+    return dev
+
+
+def _heads(t, name, dev, tokens, heads, d):
+    """Pointer and token stride of ``[tokens, heads, d]`` whose heads are contiguous."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on device {dev}, with the call's other tensors "
+                         "(libpagedkv has no CPU path)")
+    if t.shape != (tokens, heads, d):
         raise ValueError(f"{name} must be [{tokens}, {heads}, {d}]")
-    if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d):
+    step, head, elem = t.stride()
+    if (d > 1 and elem != 1) or (heads > 1 and head != d):
         raise ValueError(f"the heads of {name} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), (int(t.stride(0)) if tokens > 1 else heads * d)
+    return t.data_ptr(), (step if tokens > 1 else heads * d)
+
+
+def _launch(name, dev, stream, *args):
+    """The library's call with the tensors' device current, on the given stream
+    or that device's current one."""
+    torch = _torch()
+    if stream is None:
+        st = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
+        raise ValueError("the stream is not on the tensors' device")
+    else:
+        st = stream.cuda_stream
+    fn = getattr(lib(), name)
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, st)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, st)
+    if status != PK_OK:
+        raise PagedKVError(status, name)
 
 
 def pk_qk_norm_rope_and_cache(q_out, k_out, q, k, v, cos_sin, positions, q_weight=None, k_weight=None,
@@ -582,59 +600,62 @@ def pk_qk_norm_rope_and_cache(q_out, k_out, q, k, v, cos_sin, positions, q_weigh
     (the latter optional with a slot mapping). ``q``, ``k`` and ``v`` may be views
     of one packed projection: only each token's heads have to be contiguous."""
     torch = _torch()
-    T, Hq, d = (int(x) for x in q.shape)
-    Hk = int(k.shape[1])
-    given = [t is not None for t in (slot_mapping, k_cache, v_cache)]
-    if any(given) != all(given):
+    dev, dt = _cuda_device(q, "q"), q.dtype
+    T, Hq, d = q.shape
+    Hk = k.shape[1]
+    cache = slot_mapping is not None
+    if (k_cache is not None) != cache or (v_cache is not None) != cache:
         raise ValueError("slot_mapping, k_cache and v_cache go together")
     if (q_weight is None) != (k_weight is None):
         raise ValueError("q_weight and k_weight go together")
-    if all(given):
+    qp, qs = _heads(q, "q", dev, T, Hq, d)
+    kp, ks = _heads(k, "k", dev, T, Hk, d)
+    vp, vs, slots, kc, vc, ko, qw, kw, cs, pos, rot, max_pos = None, 0, None, None, None, None, None, None, None, \
+        None, 0, 0
+    if cache:
         desc = cache_desc(k_cache)
-        if (desc.num_kv_heads, desc.head_dim) != (Hk, d) or v_cache.shape != k_cache.shape:
+        if desc.num_kv_heads != Hk or desc.head_dim != d or v_cache.shape != k_cache.shape:
             raise ValueError("the caches must be [num_blocks, block_size, num_kv_heads, head_dim]")
-        if v is None or tuple(slot_mapping.shape) != (T,):
+        if v is None or slot_mapping.shape != (T,):
             raise ValueError("v is required and slot_mapping must be [num_tokens]")
+        if v.dtype != dt:
+            raise TypeError("queries, keys, values, weights and caches must share one dtype")
+        vp, vs = _heads(v, "v", dev, T, Hk, d)
+        slots = _at(slot_mapping, "slot_mapping", dev, torch.int64)
+        kc, vc = _at(k_cache, "k_cache", dev, dt), _at(v_cache, "v_cache", dev, dt)
     else:
         desc = CacheDesc(0, 0, Hk, d, _dtype_code(q))
-        v = None
         if k_out is None:
             raise ValueError("k_out is required without a cache")
-    for t in (q_out, k_out, k, v, q_weight, k_weight, k_cache, v_cache):
-        if t is not None and t.dtype != q.dtype:
-            raise TypeError("queries, keys, values, weights and caches must share one dtype")
-    for t, shape, name in ((q_out, (T, Hq, d), "q_out"), (k_out, (T, Hk, d), "k_out"), (q_weight, (d,), "q_weight"),
-                           (k_weight, (d,), "k_weight")):
-        if t is not None and tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be {list(shape)}")
-    rot = max_pos = 0
+    if k.dtype != dt:
+        raise TypeError("queries, keys, values, weights and caches must share one dtype")
+    if q_out.shape != (T, Hq, d) or (k_out is not None and k_out.shape != (T, Hk, d)):
+        raise ValueError("q_out and k_out must have the shapes of q and k")
+    if k_out is not None:
+        ko = _at(k_out, "k_out", dev, dt)
+    if q_weight is not None:
+        if q_weight.shape != (d,) or k_weight.shape != (d,):
+            raise ValueError("q_weight and k_weight must be [head_dim]")
+        qw, kw = _at(q_weight, "q_weight", dev, dt), _at(k_weight, "k_weight", dev, dt)
     if cos_sin is not None:
-        if cos_sin.dim() != 2 or positions is None or tuple(positions.shape) != (T,):
+        if cos_sin.dim() != 2 or positions is None or positions.shape != (T,):
             raise ValueError("cos_sin must be [max_position, rotary_dim] and positions [num_tokens]")
-        max_pos, rot = (int(x) for x in cos_sin.shape)
-    opt = lambda t, name, dt=None: None if t is None else _dev(t, name, dt)
-    qp, qs = _heads(q, "q", T, Hq, d)
-    kp, ks = _heads(k, "k", T, Hk, d)
-    vp, vs = (None, 0) if v is None else _heads(v, "v", T, Hk, d)
-    with _on_device(stream, q, q_out, k_out, k, v, cos_sin, positions if rot else None, q_weight, k_weight,
-                    slot_mapping, k_cache, v_cache) as st:
-        _check(lib().pk_qk_norm_rope_and_cache(
-            _dev(q_out, "q_out"), opt(k_out, "k_out"), qp, kp, vp, qs, ks, vs, opt(q_weight, "q_weight"),
-            opt(k_weight, "k_weight"), float(eps), opt(cos_sin, "cos_sin", torch.float32),
-            _dev(positions, "positions", torch.int64) if rot else None, max_pos, rot, int(bool(interleaved)),
-            opt(slot_mapping, "slot_mapping", torch.int64), T, Hq, opt(k_cache, "k_cache"), opt(v_cache, "v_cache"),
-            ctypes.byref(desc), st), "pk_qk_norm_rope_and_cache")
+        max_pos, rot = cos_sin.shape
+        cs, pos = _at(cos_sin, "cos_sin", dev, torch.float32), _at(positions, "positions", dev, torch.int64)
+    _launch("pk_qk_norm_rope_and_cache", dev, stream, _at(q_out, "q_out", dev, dt), ko, qp, kp, vp, qs, ks, vs, qw, kw,
+            float(eps), cs, pos, max_pos, rot, 1 if interleaved else 0, slots, T, Hq, kc, vc, ctypes.byref(desc))
 
 
-def _e4m3_cache(k_cache, v_cache, kv_exp) -> CacheDesc:
+def _e4m3_cache(k_cache, v_cache, kv_exp):
+    """Descriptor and addresses of an 8-bit cache, and its device."""
     torch = _torch()
-    desc = cache_desc(k_cache)
     if k_cache.dtype != torch.float8_e4m3fn or v_cache.dtype != k_cache.dtype:
         raise TypeError("k_cache and v_cache must be torch.float8_e4m3fn")
-    if v_cache.shape != k_cache.shape or \
-            tuple(kv_exp.shape) != (desc.num_blocks, desc.num_kv_heads, desc.block_size, 2):
+    desc = cache_desc(k_cache)
+    if v_cache.shape != k_cache.shape or kv_exp.shape != (desc.num_blocks, desc.num_kv_heads, desc.block_size, 2):
         raise ValueError("kv_exp must be [num_blocks, num_kv_heads, block_size, 2] of the caches' shape")
-    return desc
+    dev = _cuda_device(k_cache, "k_cache")
+    return desc, dev, _at(k_cache, "k_cache", dev), _at(v_cache, "v_cache", dev), _at(kv_exp, "kv_exp", dev, torch.uint8)
 
 
 def pk_reshape_and_cache_e4m3(k, v, slot_mapping, k_cache, v_cache, kv_exp, stream=None):
@@ -643,19 +664,16 @@ def pk_reshape_and_cache_e4m3(k, v, slot_mapping, k_cache, v_cache, kv_exp, stre
     codes in ``k_cache``/``v_cache`` (``torch.float8_e4m3fn``) and exponents in
     ``kv_exp`` (uint8 ``[N, Hk, B, 2]``); value = code * 2^(kv_exp - 127)."""
     torch = _torch()
-    desc = _e4m3_cache(k_cache, v_cache, kv_exp)
-    T = int(k.shape[0])
-    if v.dtype != k.dtype or k.dtype not in (torch.float32, torch.bfloat16):
+    desc, dev, kc, vc, ex = _e4m3_cache(k_cache, v_cache, kv_exp)
+    T = k.shape[0]
+    if v.dtype != k.dtype or (k.dtype != torch.bfloat16 and k.dtype != torch.float32):
         raise TypeError("k and v must both be float32 or bfloat16")
-    if tuple(slot_mapping.shape) != (T,):
+    if slot_mapping.shape != (T,):
         raise ValueError("slot_mapping must be [num_tokens]")
-    kp, ks = _heads(k, "k", T, desc.num_kv_heads, desc.head_dim)
-    vp, vs = _heads(v, "v", T, desc.num_kv_heads, desc.head_dim)
-    with _on_device(stream, k_cache, v_cache, kv_exp, k, v, slot_mapping) as st:
-        _check(lib().pk_reshape_and_cache_e4m3(
-            kp, vp, _dtype_code(k), ks, vs, _dev(slot_mapping, "slot_mapping", torch.int64), T,
-            _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(kv_exp, "kv_exp", torch.uint8),
-            ctypes.byref(desc), st), "pk_reshape_and_cache_e4m3")
+    kp, ks = _heads(k, "k", dev, T, desc.num_kv_heads, desc.head_dim)
+    vp, vs = _heads(v, "v", dev, T, desc.num_kv_heads, desc.head_dim)
+    _launch("pk_reshape_and_cache_e4m3", dev, stream, kp, vp, _dtype_code(k), ks, vs,
+            _at(slot_mapping, "slot_mapping", dev, torch.int64), T, kc, vc, ex, ctypes.byref(desc))
 
 
 def pk_gather_cache_e4m3(k_out, v_out, slot_mapping, k_cache, v_cache, kv_exp, stream=None):
@@ -663,49 +681,46 @@ def pk_gather_cache_e4m3(k_out, v_out, slot_mapping, k_cache, v_cache, kv_exp, s
     ``k_out`` and ``v_out`` (fp32 or bf16 ``[T, Hk, d]``); rows of negative
     slots stay as they were."""
     torch = _torch()
-    desc = _e4m3_cache(k_cache, v_cache, kv_exp)
-    T = int(slot_mapping.shape[0])
-    if tuple(k_out.shape) != (T, desc.num_kv_heads, desc.head_dim) or v_out.shape != k_out.shape:
+    desc, dev, kc, vc, ex = _e4m3_cache(k_cache, v_cache, kv_exp)
+    T = slot_mapping.shape[0]
+    if k_out.shape != (T, desc.num_kv_heads, desc.head_dim) or v_out.shape != k_out.shape:
         raise ValueError("k_out and v_out must be [num_tokens, num_kv_heads, head_dim]")
-    if v_out.dtype != k_out.dtype or k_out.dtype not in (torch.float32, torch.bfloat16):
+    if k_out.dtype != torch.bfloat16 and k_out.dtype != torch.float32:
         raise TypeError("k_out and v_out must both be float32 or bfloat16")
-    with _on_device(stream, k_cache, v_cache, kv_exp, k_out, v_out, slot_mapping) as st:
-        _check(lib().pk_gather_cache_e4m3(
-            _dev(k_out, "k_out"), _dev(v_out, "v_out"), _dtype_code(k_out),
-            _dev(slot_mapping, "slot_mapping", torch.int64), T, _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
-            _dev(kv_exp, "kv_exp", torch.uint8), ctypes.byref(desc), st), "pk_gather_cache_e4m3")
+    _launch("pk_gather_cache_e4m3", dev, stream, _at(k_out, "k_out", dev), _at(v_out, "v_out", dev, k_out.dtype),
+            _dtype_code(k_out), _at(slot_mapping, "slot_mapping", dev, torch.int64), T, kc, vc, ex,
+            ctypes.byref(desc))
 
 
 def pk_copy_blocks_e4m3(k_cache, v_cache, kv_exp, src_dst_pairs, stream=None):
     """:func:`pk_copy_blocks` of an 8-bit cache (codes and exponents)."""
-    torch = _torch()
-    desc = _e4m3_cache(k_cache, v_cache, kv_exp)
-    n = int(src_dst_pairs.shape[0]) if src_dst_pairs.numel() else 0
-    if n and tuple(src_dst_pairs.shape) != (n, 2):
+    desc, dev, kc, vc, ex = _e4m3_cache(k_cache, v_cache, kv_exp)
+    n = src_dst_pairs.shape[0] if src_dst_pairs.numel() else 0
+    if n and src_dst_pairs.shape != (n, 2):
         raise ValueError("src_dst_pairs must be [num_pairs, 2]")
-    if n == 0:
-        return
-    with _on_device(stream, k_cache, v_cache, kv_exp, src_dst_pairs) as st:
-        _check(lib().pk_copy_blocks_e4m3(
-            _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(kv_exp, "kv_exp", torch.uint8),
-            _dev(src_dst_pairs, "src_dst_pairs", torch.int64), n, ctypes.byref(desc), st), "pk_copy_blocks_e4m3")
+    if n:
+        _launch("pk_copy_blocks_e4m3", dev, stream, kc, vc, ex,
+                _at(src_dst_pairs, "src_dst_pairs", dev, _torch().int64), n, ctypes.byref(desc))
 
 
-def _attention_args(out, q, block_tables, context_lens, num_seqs, d, work_items, workspace):
-    """The checks and optional pointers that the two attentions below share."""
-    torch = _torch()
-    if q.dim() != 3 or int(q.shape[2]) != d or out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("out and q must be [rows, num_q_heads, head_dim] of one dtype")
-    if block_tables.dim() != 2 or int(block_tables.shape[0]) != num_seqs or tuple(context_lens.shape) != (num_seqs,):
+def _attention_args(dev, out, q, block_tables, context_lens, num_seqs, d, work_items, workspace):
+    """Checked addresses of what the two attentions below share: (out, q),
+    (block_tables, context_lens) and (work_items, count, workspace, bytes)."""
+    i32 = _torch().int32
+    if q.dim() != 3 or q.shape[2] != d or out.shape != q.shape:
+        raise ValueError("out and q must be [rows, num_q_heads, head_dim]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != num_seqs or context_lens.shape != (num_seqs,):
         raise ValueError("block_tables must be [num_seqs, max_blocks] and context_lens [num_seqs]")
     items, n_items, ws, ws_bytes = None, 0, None, 0
     if work_items is not None:
-        if work_items.dim() != 2 or int(work_items.shape[1]) != 2:
+        if work_items.dim() != 2 or work_items.shape[1] != 2:
             raise ValueError("work_items must be [n, 2]")
-        items, n_items = _dev(work_items, "work_items", torch.int32), int(work_items.shape[0])
+        items, n_items = _at(work_items, "work_items", dev, i32), work_items.shape[0]
     if workspace is not None:
-        ws, ws_bytes = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
-    return items, n_items, ws, ws_bytes
+        ws, ws_bytes = _at(workspace, "workspace", dev), workspace.numel() * workspace.element_size()
+    return ((_at(out, "out", dev, q.dtype), _at(q, "q", dev)),
+            (_at(block_tables, "block_tables", dev, i32), _at(context_lens, "context_lens", dev, i32)),
+            (items, n_items, ws, ws_bytes))
 
 
 def pk_paged_attention_decode_e4m3(out, q, k_cache, v_cache, kv_exp, block_tables, context_lens, scale: float,
@@ -716,20 +731,13 @@ def pk_paged_attention_decode_e4m3(out, q, k_cache, v_cache, kv_exp, block_table
     ``work_items`` as there (:func:`pk_attention_plan` and
     :func:`pk_paged_attention_workspace_size` take the 8-bit cache's descriptor)."""
     torch = _torch()
-    desc = _e4m3_cache(k_cache, v_cache, kv_exp)
-    if q.dtype not in (torch.float32, torch.bfloat16):
+    desc, dev, kc, vc, ex = _e4m3_cache(k_cache, v_cache, kv_exp)
+    if q.dtype != torch.bfloat16 and q.dtype != torch.float32:
         raise TypeError("q and out must be float32 or bfloat16")
-    S = int(q.shape[0])
-    items, n_items, ws, ws_bytes = _attention_args(out, q, block_tables, context_lens, S, desc.head_dim, work_items,
-                                                   workspace)
-    with _on_device(stream, k_cache, v_cache, kv_exp, out, q, block_tables, context_lens, work_items,
-                    workspace) as st:
-        _check(lib().pk_paged_attention_decode_e4m3(
-            _dev(out, "out"), _dev(q, "q"), _dtype_code(q), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
-            _dev(kv_exp, "kv_exp", torch.uint8), _dev(block_tables, "block_tables", torch.int32),
-            _dev(context_lens, "context_lens", torch.int32), float(scale), S, int(q.shape[1]),
-            int(block_tables.shape[1]), int(max_context_len), int(partition_size), items, n_items, ws, ws_bytes,
-            ctypes.byref(desc), st), "pk_paged_attention_decode_e4m3")
+    S = q.shape[0]
+    rows, seqs, split = _attention_args(dev, out, q, block_tables, context_lens, S, desc.head_dim, work_items, workspace)
+    _launch("pk_paged_attention_decode_e4m3", dev, stream, *rows, _dtype_code(q), kc, vc, ex, *seqs, float(scale),
+            S, q.shape[1], block_tables.shape[1], int(max_context_len), int(partition_size), *split, ctypes.byref(desc))
 
 
 def pk_paged_attention_tree(out, q, k_cache, v_cache, block_tables, context_lens, q_offsets, scale: float,
@@ -744,27 +752,23 @@ def pk_paged_attention_tree(out, q, k_cache, v_cache, block_tables, context_lens
     :func:`pk_tree_plan`, ``workspace`` of :func:`pk_tree_workspace_size` bytes
     when the contexts are split."""
     torch = _torch()
+    dev = _cuda_device(q, "q")
     desc = cache_desc(k_cache)
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or q.dtype != k_cache.dtype:
-        raise ValueError("q, k_cache and v_cache must share one dtype, the caches one shape")
-    S = int(block_tables.shape[0])
-    items, n_items, ws, ws_bytes = _attention_args(out, q, block_tables, context_lens, S, desc.head_dim, work_items,
-                                                   workspace)
-    if tuple(q_offsets.shape) != (S + 1,):
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have one shape")
+    S = block_tables.shape[0]
+    rows, seqs, split = _attention_args(dev, out, q, block_tables, context_lens, S, desc.head_dim, work_items, workspace)
+    if q_offsets.shape != (S + 1,):
         raise ValueError("q_offsets must be [num_seqs + 1]")
     mask = None
     if tree_mask is not None:
-        if tree_mask.dtype not in (torch.int64, torch.uint64) or tuple(tree_mask.shape) != (int(q.shape[0]),):
+        if (tree_mask.dtype != torch.int64 and tree_mask.dtype != torch.uint64) or tree_mask.shape != (q.shape[0],):
             raise ValueError("tree_mask must be int64 or uint64 [rows]")
-        mask = _dev(tree_mask, "tree_mask")
-    with _on_device(stream, k_cache, v_cache, out, q, block_tables, context_lens, q_offsets, tree_mask, work_items,
-                    workspace) as st:
-        _check(lib().pk_paged_attention_tree(
-            _dev(out, "out"), _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
-            _dev(block_tables, "block_tables", torch.int32), _dev(context_lens, "context_lens", torch.int32),
-            _dev(q_offsets, "q_offsets", torch.int32), mask, float(scale), S, int(q.shape[0]), int(max_draft_len),
-            int(q.shape[1]), int(block_tables.shape[1]), int(max_context_len), int(partition_size), items, n_items,
-            ws, ws_bytes, ctypes.byref(desc), st), "pk_paged_attention_tree")
+        mask = _at(tree_mask, "tree_mask", dev)
+    _launch("pk_paged_attention_tree", dev, stream, *rows, _at(k_cache, "k_cache", dev, q.dtype),
+            _at(v_cache, "v_cache", dev, q.dtype), *seqs, _at(q_offsets, "q_offsets", dev, torch.int32), mask,
+            float(scale), S, q.shape[0], int(max_draft_len), q.shape[1], block_tables.shape[1], int(max_context_len),
+            int(partition_size), *split, ctypes.byref(desc))
 
 
 def pk_tree_masks(parents) -> Tuple[np.ndarray, np.ndarray]:

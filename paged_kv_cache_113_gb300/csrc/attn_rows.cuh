@@ -114,10 +114,9 @@ __device__ __forceinline__ uint64_t see64(uint64_t mask, int base, int t0) {
 struct E4M3 {
   uint8_t x;
 };
-__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-  const uint2 v = *reinterpret_cast<const uint2 *>(p);
-  return make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
+template <typename T>
+__device__ __forceinline__ float4 load4(const T *p) {
+  return widen4(raw4(p));
 }
 __device__ __forceinline__ float4 load4(const E4M3 *p) {
   const uint32_t w = *reinterpret_cast<const uint32_t *>(p);

@@ -37,45 +37,34 @@ struct RowParams {
   int32_t num_tokens, hk, d, block_size;
 };
 
-// LANES lanes of 16 elements hold one row; a token's rows are its Hk keys,
-// then its Hk values.
-template <int LANES>
-__device__ __forceinline__ bool row_of(const RowParams &p, int64_t &tok, int &h, bool &is_v,
-                                       int &e0, int64_t &slot) {
-  const int64_t unit = int64_t(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
-  tok = unit / (2 * p.hk);
-  const int j = int(unit % (2 * p.hk));
-  is_v = j >= p.hk;
-  h = is_v ? j - p.hk : j;
-  e0 = (threadIdx.x % LANES) * 16;
-  slot = -1;
-  if (tok >= p.num_tokens) return false;
-  slot = __ldg(p.slots + tok);
-  if (slot >= p.num_slots) {
-    if (e0 == 0 && j == 0) pk::record_error(&g_cache_e4m3_error, PK_DEVERR_SLOT, tok);
-    slot = -1;
-  }
-  return slot >= 0 && e0 < p.d;
-}
-
-__device__ __forceinline__ uint8_t *exp_of(const RowParams &p, int64_t slot, int h, bool is_v) {
-  const int64_t block = slot / p.block_size, at = slot % p.block_size;
-  return p.kv_exp + ((block * p.hk + h) * p.block_size + at) * 2 + (is_v ? 1 : 0);
-}
-
-template <typename T, int LANES>
-__global__ void __launch_bounds__(256) quantize_kernel(RowParams p) {
-  int64_t tok, slot;
+// LANES lanes of 16 elements hold a head's row of K and its row of V, both of
+// which are loaded before either is converted.
+struct Place {
+  int64_t tok, slot, exp;  // exp: index of the pair of exponents
   int h, e0;
-  bool is_v;
-  const bool on = row_of<LANES>(p, tok, h, is_v, e0, slot);
-  float x[2][8] = {};
-  if (on) {
-    const T *src = static_cast<const T *>(is_v ? p.v : p.k) + tok * (is_v ? p.v_stride : p.k_stride) +
-                   int64_t(h) * p.d + e0;
-    pk::load8(src, x[0]);
-    pk::load8(src + 8, x[1]);
+};
+
+template <int LANES>
+__device__ __forceinline__ bool place_of(const RowParams &p, Place &at) {
+  const int64_t unit = int64_t(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
+  at.tok = unit / p.hk;
+  at.h = int(unit % p.hk);
+  at.e0 = (threadIdx.x % LANES) * 16;
+  if (at.tok >= p.num_tokens) return false;
+  at.slot = __ldg(p.slots + at.tok);
+  if (at.slot >= p.num_slots) {
+    if (at.e0 == 0 && at.h == 0) pk::record_error(&g_cache_e4m3_error, PK_DEVERR_SLOT, at.tok);
+    return false;
   }
+  if (at.slot < 0) return false;
+  const int64_t block = int32_t(at.slot) / p.block_size;  // slots fit 32 bits
+  at.exp = (block * p.hk + at.h) * p.block_size + (at.slot - block * p.block_size);
+  return at.e0 < p.d;
+}
+
+// The exponent e of a row of which a lane holds 16 values.
+template <int LANES>
+__device__ __forceinline__ int row_exponent(const float (&x)[2][8]) {
   // The largest finite magnitude as its bits (their order is the values').
   uint32_t top = 0;
 #pragma unroll
@@ -85,16 +74,17 @@ __global__ void __launch_bounds__(256) quantize_kernel(RowParams p) {
   }
 #pragma unroll
   for (int o = LANES / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (!on) return;
   // With top = f * 2^E, 1 <= f < 2: e = E - 8 where f <= 1.75 = 448 / 256, else
   // E - 7. Adding 0x1fffff carries into the exponent exactly where f > 1.75.
-  int e = int((top + 0x1fffffu) >> 23) - 127 - 8;
-  e = top == 0 ? 0 : max(e, -100);
+  return top == 0 ? 0 : max(int((top + 0x1fffffu) >> 23) - 127 - 8, -100);
+}
+
+__device__ __forceinline__ uint4 codes_of(const float (&x)[2][8], int e) {
   const float s = __uint_as_float(uint32_t(127 - e) << 23);  // 2^-e: e is in [-100, 120]
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t c = 0;
+    w[i] = 0;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int at = 4 * i + 2 * j;
@@ -102,26 +92,38 @@ __global__ void __launch_bounds__(256) quantize_kernel(RowParams p) {
       // Infinities become the NaN code too: the conversion would saturate them.
       a = fabsf(a) <= 3.402823466e38f ? a * s : __uint_as_float(0x7fc00000u);
       b = fabsf(b) <= 3.402823466e38f ? b * s : __uint_as_float(0x7fc00000u);
-      c |= uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3)) << (16 * j);
+      w[i] |= uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3)) << (16 * j);
     }
-    w[i] = c;
   }
-  *reinterpret_cast<uint4 *>((is_v ? p.v_cache : p.k_cache) + (slot * p.hk + h) * p.d + e0) =
-      make_uint4(w[0], w[1], w[2], w[3]);
-  if (e0 == 0) *exp_of(p, slot, h, is_v) = uint8_t(e + 127);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <typename T, int LANES>
-__global__ void __launch_bounds__(256) gather_kernel(RowParams p) {
-  int64_t tok, slot;
-  int h, e0;
-  bool is_v;
-  if (!row_of<LANES>(p, tok, h, is_v, e0, slot)) return;
-  const uint4 c = __ldg(reinterpret_cast<const uint4 *>((is_v ? p.v_cache : p.k_cache) +
-                                                        (slot * p.hk + h) * p.d + e0));
-  const float s = __uint_as_float(uint32_t(__ldg(exp_of(p, slot, h, is_v))) << 23);
+__global__ void __launch_bounds__(256) quantize_kernel(RowParams p) {
+  Place at;
+  const bool on = place_of<LANES>(p, at);
+  float k[2][8] = {}, v[2][8] = {};
+  if (on) {
+    const T *ks = static_cast<const T *>(p.k) + at.tok * p.k_stride + int64_t(at.h) * p.d + at.e0;
+    const T *vs = static_cast<const T *>(p.v) + at.tok * p.v_stride + int64_t(at.h) * p.d + at.e0;
+    pk::load8(ks, k[0]);
+    pk::load8(ks + 8, k[1]);
+    pk::load8(vs, v[0]);
+    pk::load8(vs + 8, v[1]);
+  }
+  const int ke = row_exponent<LANES>(k), ve = row_exponent<LANES>(v);
+  if (!on) return;
+  const int64_t to = (at.slot * p.hk + at.h) * p.d + at.e0;
+  *reinterpret_cast<uint4 *>(p.k_cache + to) = codes_of(k, ke);
+  *reinterpret_cast<uint4 *>(p.v_cache + to) = codes_of(v, ve);
+  if (at.e0 == 0)
+    *reinterpret_cast<uint16_t *>(p.kv_exp + at.exp * 2) = uint16_t((ke + 127) | (ve + 127) << 8);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_values(T *dst, const uint4 &c, uint32_t exp) {
+  const float s = __uint_as_float(exp << 23);
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  T *dst = static_cast<T *>(is_v ? p.v_out : p.k_out) + (tok * p.hk + h) * p.d + e0;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     float x[8];
@@ -135,6 +137,18 @@ __global__ void __launch_bounds__(256) gather_kernel(RowParams p) {
     }
     pk::store8(dst + 8 * i, x);
   }
+}
+
+template <typename T, int LANES>
+__global__ void __launch_bounds__(256) gather_kernel(RowParams p) {
+  Place at;
+  if (!place_of<LANES>(p, at)) return;
+  const int64_t from = (at.slot * p.hk + at.h) * p.d + at.e0, to = (at.tok * p.hk + at.h) * p.d + at.e0;
+  const uint4 k = __ldg(reinterpret_cast<const uint4 *>(p.k_cache + from));
+  const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p.v_cache + from));
+  const uint32_t e = __ldg(reinterpret_cast<const uint16_t *>(p.kv_exp + at.exp * 2));
+  store_values(static_cast<T *>(p.k_out) + to, k, e & 0xffu);
+  store_values(static_cast<T *>(p.v_out) + to, v, e >> 8);
 }
 
 // grid.x = pair, grid.y = 0 K codes / 1 V codes / 2 exponents, grid.z = chunk
@@ -176,7 +190,7 @@ pk_status check_desc_e4m3(const pk_cache_desc *d) {
 // Calls f with the lanes of a row (4, 8 or 16 of 16 elements) and its grid.
 template <typename F>
 pk_status by_lanes(const RowParams &p, F f) {
-  const int64_t units = int64_t(p.num_tokens) * 2 * p.hk;
+  const int64_t units = int64_t(p.num_tokens) * p.hk;
   auto go = [&](auto c) {
     constexpr int L = decltype(c)::value;
     const int64_t ctas = (units + 256 / L - 1) / (256 / L);

@@ -328,6 +328,18 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
                                              pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
 }
 
+// Four consecutive elements as they are stored, and as fp32 values.
+__device__ __forceinline__ float4 raw4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ uint2 raw4(const __nv_bfloat16 *p) { return *reinterpret_cast<const uint2 *>(p); }
+__device__ __forceinline__ float4 widen4(const float4 &v) { return v; }
+__device__ __forceinline__ float4 widen4(const uint2 &v) {
+  return make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
+}
+__device__ __forceinline__ void store4(float *p, const float4 &v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float4 &v) {
+  *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
 // Host: the value of a translation unit's device error word, which is cleared
 // (-1 when a call fails). Synchronises the stream.
 template <typename Word>

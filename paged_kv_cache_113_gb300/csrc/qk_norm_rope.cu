@@ -35,114 +35,132 @@ struct RopeParams {
   int64_t num_slots;
   float eps;
   int32_t num_tokens, hq, hk, d, rot, max_position, interleaved;
+  float inv_d;
+  uint32_t warps;               // warps of a token
   int32_t heads;                // heads of a token that have work: Hq + Hk (+ Hk values)
 };
 
-// A head is LANES lanes of eight elements each (LANES a power of two; lanes
-// past the head's end carry zeros). Rotated pairs that lie in other lanes are
-// exchanged with shuffles: rotary_dim / 2 is a multiple of eight, so a pair's
-// two halves sit at the same place of two lanes.
-template <typename T, int LANES>
+#ifndef PK_RU
+#define PK_RU 4
+#endif
+// Rounds per warp: 4 from this many heads on, else 1.
+constexpr int64_t kManyHeads = 16384;
+
+// A head is d / 8 of LANES lanes (a power of two), each with two chunks of four
+// elements that hold whole pairs, so that the rotation stays in the lane: with
+// halves apart, chunks 4 l and rotary_dim / 2 + 4 l; with neighbouring pairs, and
+// past the rotated elements, two chunks side by side. Either way the lane's four
+// cosines and sines are those from 4 l on. A warp holds 32 / LANES heads of one
+// token at a time and does U such rounds, all loaded before the first is
+// computed; the token's cosines and sines are loaded once.
+template <typename T, int LANES, int U>
 __global__ void __launch_bounds__(256) qk_norm_rope_kernel(RopeParams p) {
-  const int64_t unit = int64_t(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
-  const int lane = threadIdx.x % LANES, e0 = lane * 8;
-  const int64_t tok = unit / p.heads;
-  const int head = int(unit % p.heads);
-  bool live = tok < p.num_tokens;
-  int64_t pos = 0, slot = -1;
-  if (live && p.rot) {
-    pos = __ldg(p.positions + tok);
-    if (pos < 0 || pos >= p.max_position) {
-      if (lane == 0 && head == 0) pk::record_error(&g_qk_norm_rope_error, PK_DEVERR_POSITION, tok);
-      live = false;
-    }
+  constexpr int HPW = 32 / LANES;  // heads of a round
+  using Raw = decltype(pk::raw4(static_cast<const T *>(nullptr)));
+  const uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5), warps = p.warps;
+  const uint32_t t = unit / warps;
+  if (t >= uint32_t(p.num_tokens)) return;
+  const int64_t tok = t;
+  const int lane = threadIdx.x % LANES;
+  const int first = int(unit - t * warps) * HPW * U + (threadIdx.x & 31) / LANES;
+  const int64_t pos = p.rot ? __ldg(p.positions + tok) : 0;
+  int64_t slot = p.slots ? __ldg(p.slots + tok) : -1;
+  const bool in = lane * 8 < p.d, turn = lane * 8 < p.rot;
+  const bool apart = turn && !p.interleaved;
+  const int ea = apart ? 4 * lane : 8 * lane, eb = apart ? p.rot / 2 + 4 * lane : 8 * lane + 4;
+  Raw ra[U], rb[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int head = first + u * HPW;
+    ra[u] = rb[u] = Raw{};
+    if (!in || head >= p.heads) continue;
+    const bool is_q = head < p.hq, is_k = head < p.hq + p.hk;
+    const T *src = static_cast<const T *>(is_q ? p.q : (is_k ? p.k : p.v)) +
+                   tok * (is_q ? p.q_stride : (is_k ? p.k_stride : p.v_stride)) +
+                   (is_q ? head : (is_k ? head - p.hq : head - p.hq - p.hk)) * p.d;
+    ra[u] = pk::raw4(src + ea);
+    rb[u] = pk::raw4(src + eb);
   }
-  const bool is_q = head < p.hq, is_k = !is_q && head < p.hq + p.hk;
-  const int h = is_q ? head : (is_k ? head - p.hq : head - p.hq - p.hk);
-  if (live && !is_q && p.slots) {
-    slot = __ldg(p.slots + tok);
-    if (slot >= p.num_slots) {
-      if (lane == 0 && is_k && h == 0)
-        pk::record_error(&g_qk_norm_rope_error, PK_DEVERR_SLOT, tok);
-      slot = -1;
-    }
-  }
-  const bool on = live && e0 < p.d;
-  const T *src = static_cast<const T *>(is_q ? p.q : (is_k ? p.k : p.v)) +
-                 tok * (is_q ? p.q_stride : (is_k ? p.k_stride : p.v_stride)) + int64_t(h) * p.d + e0;
-  float x[8] = {};
-  if (on) pk::load8(src, x);
-  // Every lane of the warp takes part in the shuffles, whatever its head is.
-  float ss = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const void *w = is_q ? p.q_weight : (is_k ? p.k_weight : nullptr);
-  if (w && on) {
-    const float r = 1.0f / sqrtf(ss / float(p.d) + p.eps);
-    float g[8];
-    pk::load8(static_cast<const T *>(w) + e0, g);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * g[i];
-  }
-  const int half = p.rot / 2;
-  const bool turn = on && (is_q || is_k) && e0 < p.rot;
-  if (p.interleaved) {
-    if (turn) {
-      const float *cs = p.cos_sin + pos * p.rot + e0 / 2;
-      const float4 c = __ldg(reinterpret_cast<const float4 *>(cs));
-      const float4 s = __ldg(reinterpret_cast<const float4 *>(cs + half));
-      const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = a * cc[i] - b * sn[i];
-        x[2 * i + 1] = b * cc[i] + a * sn[i];
-      }
-    }
-  } else {
-    const bool upper = e0 >= half;
-    const int other = e0 < p.rot ? (upper ? lane - half / 8 : lane + half / 8) : lane;
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], other, LANES);
-    if (turn) {
-      const float *cs = p.cos_sin + pos * p.rot + (upper ? e0 - half : e0);
-      float c[8], s[8];
-      pk::load8(cs, c);
-      pk::load8(cs + half, s);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * c[i] + (upper ? y[i] : -y[i]) * s[i];
-    }
-  }
-  if (!on) return;
-  const int64_t row = (tok * (is_q ? p.hq : p.hk) + h) * p.d + e0;
-  if (is_q) {
-    pk::store8(static_cast<T *>(p.q_out) + row, x);
+  if (p.rot && (pos < 0 || pos >= p.max_position)) {  // the whole token: recorded and skipped
+    if ((threadIdx.x & 31) == 0 && first == 0)
+      pk::record_error(&g_qk_norm_rope_error, PK_DEVERR_POSITION, tok);
     return;
   }
-  if (is_k && p.k_out) pk::store8(static_cast<T *>(p.k_out) + row, x);
-  if (slot >= 0)  // a value reaches here as it was loaded: the round trip through fp32 is exact
-    pk::store8(static_cast<T *>(is_k ? p.k_cache : p.v_cache) + (slot * p.hk + h) * p.d + e0, x);
+  if (slot >= p.num_slots) {
+    if ((threadIdx.x & 31) == 0 && first == 0)
+      pk::record_error(&g_qk_norm_rope_error, PK_DEVERR_SLOT, tok);
+    slot = -1;
+  }
+  float4 c, s;
+  if (turn) {
+    const float *cs = p.cos_sin + pos * p.rot + 4 * lane;
+    c = __ldg(reinterpret_cast<const float4 *>(cs));
+    s = __ldg(reinterpret_cast<const float4 *>(cs + p.rot / 2));
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int head = first + u * HPW;
+    const bool is_q = head < p.hq, is_k = !is_q && head < p.hq + p.hk, on = in && head < p.heads;
+    float4 a = pk::widen4(ra[u]), b = pk::widen4(rb[u]);
+    if (p.q_weight) {  // every lane of the warp takes part in the shuffles
+      float ss = a.x * a.x + a.y * a.y + a.z * a.z + a.w * a.w;
+      ss += b.x * b.x + b.y * b.y + b.z * b.z + b.w * b.w;
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (on && (is_q || is_k)) {
+        const float r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
+        const T *w = static_cast<const T *>(is_q ? p.q_weight : p.k_weight);
+        const float4 ga = pk::widen4(pk::raw4(w + ea)), gb = pk::widen4(pk::raw4(w + eb));
+        a.x *= r * ga.x, a.y *= r * ga.y, a.z *= r * ga.z, a.w *= r * ga.w;
+        b.x *= r * gb.x, b.y *= r * gb.y, b.z *= r * gb.z, b.w *= r * gb.w;
+      }
+    }
+    if (!on) continue;
+    if (turn && (is_q || is_k)) {
+      const float4 x = a, y = b;
+      if (apart) {
+        a = make_float4(x.x * c.x - y.x * s.x, x.y * c.y - y.y * s.y, x.z * c.z - y.z * s.z, x.w * c.w - y.w * s.w);
+        b = make_float4(y.x * c.x + x.x * s.x, y.y * c.y + x.y * s.y, y.z * c.z + x.z * s.z, y.w * c.w + x.w * s.w);
+      } else {
+        a = make_float4(x.x * c.x - x.y * s.x, x.y * c.x + x.x * s.x, x.z * c.y - x.w * s.y, x.w * c.y + x.z * s.y);
+        b = make_float4(y.x * c.z - y.y * s.z, y.y * c.z + y.x * s.z, y.z * c.w - y.w * s.w, y.w * c.w + y.z * s.w);
+      }
+    }
+    auto put = [&](T *to) {
+      pk::store4(to + ea, a);
+      pk::store4(to + eb, b);
+    };
+    if (is_q) {
+      put(static_cast<T *>(p.q_out) + (tok * p.hq + head) * p.d);
+      continue;
+    }
+    const int h = is_k ? head - p.hq : head - p.hq - p.hk;
+    if (is_k && p.k_out) put(static_cast<T *>(p.k_out) + (tok * p.hk + h) * p.d);
+    if (slot >= 0)  // a value reaches here as it was loaded: the round trip through fp32 is exact
+      put(static_cast<T *>(is_k ? p.k_cache : p.v_cache) + (slot * p.hk + h) * p.d);
+  }
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 template <typename T>
-pk_status launch(const RopeParams &p, cudaStream_t stream) {
-  const int lanes = p.d / 8;
-  auto go = [&](auto lanes_c) {
-    constexpr int L = decltype(lanes_c)::value;
-    const int64_t units = int64_t(p.num_tokens) * p.heads;
-    const int64_t ctas = (units + 256 / L - 1) / (256 / L);
-    if (ctas > INT32_MAX) return PK_ERR_UNSUPPORTED;
-    qk_norm_rope_kernel<T, L><<<unsigned(ctas), 256, 0, stream>>>(p);
+pk_status launch(RopeParams p, cudaStream_t stream) {
+  auto go = [&](auto lanes_c, auto rounds_c) {
+    constexpr int L = decltype(lanes_c)::value, U = decltype(rounds_c)::value;
+    p.warps = (p.heads + 32 / L * U - 1) / (32 / L * U);
+    const int64_t units = int64_t(p.num_tokens) * p.warps;
+    if (units > INT32_MAX) return PK_ERR_UNSUPPORTED;
+    qk_norm_rope_kernel<T, L, U><<<unsigned((units + 7) / 8), 256, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? PK_OK : PK_ERR_CUDA;
   };
-  if (lanes <= 8) return go(std::integral_constant<int, 8>());
-  if (lanes <= 16) return go(std::integral_constant<int, 16>());
-  return go(std::integral_constant<int, 32>());
+  using std::integral_constant;
+  auto by_lanes = [&](auto rounds_c) {
+    if (p.d <= 64) return go(integral_constant<int, 8>(), rounds_c);
+    if (p.d <= 128) return go(integral_constant<int, 16>(), rounds_c);
+    return go(integral_constant<int, 32>(), rounds_c);
+  };
+  return int64_t(p.num_tokens) * p.heads >= kManyHeads ? by_lanes(integral_constant<int, PK_RU>())
+                                                       : by_lanes(integral_constant<int, 1>());
 }
 
 }  // namespace
@@ -209,6 +227,7 @@ extern "C" pk_status pk_qk_norm_rope_and_cache(
   p.d = d;
   p.rot = rotary_dim;
   p.max_position = max_position;
+  p.inv_d = 1.0f / float(d);
   p.interleaved = interleaved ? 1 : 0;
   p.heads = num_q_heads + hk + (cache ? hk : 0);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
