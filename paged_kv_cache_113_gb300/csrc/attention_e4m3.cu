@@ -39,24 +39,36 @@ extern "C" int pkx_take_attention_e4m3_error(cudaStream_t stream) {
 
 namespace {
 
-constexpr int kWarps = 4;             // consumer warps, 16 tokens each per stage
-constexpr int kTps = 16 * kWarps;     // tokens per stage
+constexpr int kWarps = 4;             // consumer warps
+constexpr int kThreads = (kWarps + 1) * 32;  // and the producer
+constexpr int kUnits = 4;             // units known at a time
+constexpr int kAhead = 4;             // stages of a unit left when the next is asked for
 constexpr float kHeadroom = 10.0f;    // log2 of the largest fp16 weight
 
-template <int D, int BS>
+template <typename IO, int D, int BS>
 struct Shape {
-  static constexpr int STAGES = 4;
-  static constexpr int BPS = kTps / BS;         // blocks per stage
-  static constexpr int KV_BYTES = kTps * D;     // the stage's K, and its V
+  static constexpr int STAGES = 3;
+  static constexpr int TILES = 128 / D;         // 16-token tiles of a warp in a stage: 16 KB of codes
+  static constexpr int TPS = 16 * kWarps * TILES;  // tokens per stage
+  static constexpr int BPS = TPS / BS;          // blocks per stage
+  static constexpr int KV_BYTES = TPS * D;      // the stage's K, and its V
   static constexpr int STAGE_BYTES = 2 * KV_BYTES;
-  static constexpr int EXP_BYTES = kTps * 2;
+  static constexpr int EXP_BYTES = TPS * 2;
+  static constexpr int EXP_LANES = TPS / 8;     // lanes that copy 16 bytes of exponents each
   static constexpr int KC = D / 32;             // 32-byte steps of a row
+  static constexpr int Q_ROW = D * int(sizeof(IO)) + 16;  // padded against bank conflicts
+  static constexpr int Q_BYTES = 8 * Q_ROW;     // a group's queries
   static constexpr int OUT_STRIDE = D + 4;      // padded row of the warps' merge
   static constexpr int MERGE_BYTES = kWarps * 8 * (OUT_STRIDE + 2) * 4;
-  static constexpr int RING_BYTES = STAGES * (STAGE_BYTES + EXP_BYTES);
   static constexpr int SMEM_BYTES =
-      1024 + 16 * STAGES + (RING_BYTES > MERGE_BYTES ? RING_BYTES : MERGE_BYTES);
+      1024 + STAGES * (STAGE_BYTES + EXP_BYTES) + 2 * Q_BYTES + MERGE_BYTES;
   static_assert(32 % BPS == 0, "a stage's blocks lie in one chunk of 32 table entries");
+};
+
+// A unit of work: a sequence and KV head's queries over one partition.
+struct Unit {
+  int s, kvh, part, np;
+  int start, end, nst;  // its tokens and stages; s < 0: no more units
 };
 
 // Byte offset of 16-byte chunk c of row r in a TMA tile of D-byte rows (128- or
@@ -85,10 +97,10 @@ __device__ __forceinline__ bool zero_row(uint32_t base, int r) {
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 
 template <typename IO, int D, int BS>
-__global__ void __launch_bounds__((kWarps + 1) * 32, 3)
+__global__ void __launch_bounds__(kThreads, 3)
     attn_e4m3_kernel(RowsParams p, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
-  using S = Shape<D, BS>;
+  using S = Shape<IO, D, BS>;
   constexpr int STAGES = S::STAGES, KC = S::KC;
   constexpr int QW = sizeof(IO) == 4 ? 2 : 1;   // fp16 parts of a query and of a weight
   launch_dependents();  // the merge may be scheduled as this grid drains
@@ -96,111 +108,222 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t stages = (raw + 1023u) & ~1023u;
   const uint32_t exps = stages + STAGES * S::STAGE_BYTES;
-  __shared__ __align__(8) uint64_t bars[2 * STAGES];
-  auto full_bar = [&](int i) { return smem_addr(bars + i); };
-  auto empty_bar = [&](int i) { return smem_addr(bars + STAGES + i); };
+  const uint32_t q_sm = exps + STAGES * S::EXP_BYTES;
+  __shared__ __align__(8) uint64_t bars[2 * STAGES + 7 + 2 * kUnits];
+  __shared__ uint4 answer;
+  __shared__ Unit units[kUnits];
+  auto bar = [&](int i) { return smem_addr(bars + i); };
+  // Units i and stages t are counted over the whole life of the CTA.
+  auto full_bar = [&](int t) { return bar(t % STAGES); };
+  auto empty_bar = [&](int t) { return bar(STAGES + t % STAGES); };
+  auto q_full = [&](int i) { return bar(2 * STAGES + (i & 1)); };
+  auto q_empty = [&](int i) { return bar(2 * STAGES + 2 + (i & 1)); };
+  const uint32_t m_full = bar(2 * STAGES + 4), m_empty = bar(2 * STAGES + 5);  // the warps' merge
+  const uint32_t u_answer = bar(2 * STAGES + 6);
+  auto u_full = [&](int i) { return bar(2 * STAGES + 7 + i % kUnits); };
+  auto u_empty = [&](int i) { return bar(2 * STAGES + 7 + kUnits + i % kUnits); };
+  auto t_phase = [](int t) { return uint32_t(t / STAGES) & 1u; };
+  auto u_phase = [](int i) { return uint32_t(i / kUnits) & 1u; };
+  // A wait of the whole warp, which converges on it; once one has failed, so do all.
+  auto warp_wait = [](uint32_t b, uint32_t parity, bool &ok) {
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(b, parity));
+    return ok;
+  };
+  auto timeout = [&] { record_error(&g_rows_error, PK_DEVERR_TIMEOUT, blockIdx.x); };
 
-  const int kvh = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool record = kvh == 0 && threadIdx.x == 0;
-  int s, part;
-  if (!work_item(p, blockIdx.y, gridDim.z - 1 - blockIdx.z, record, s, part)) return;
-  const SeqRows sr = seq_rows(p, s, record && part == 0);
   const int G = p.group;
-  const size_t row0 = size_t(s) * p.num_q_heads + kvh * G;  // the group's first row of q and out
-  if (sr.ctx == 0) {  // invalid length (recorded): a zero row, nothing to merge
-    if (part == 0)
-      for (int i = threadIdx.x; i < G * D; i += blockDim.x)
-        store_elem(static_cast<IO *>(p.out) + row0 * D + i, 0.0f);
-    return;
-  }
-  if (part >= sr.np) return;
-  const int start = part * p.partition, end = min(sr.ctx, start + p.partition);
-  const int nst = (end - start + kTps - 1) / kTps;
-
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(full_bar(i), 1);
+      mbar_init(full_bar(i), 1 + S::EXP_LANES);
       mbar_init(empty_bar(i), kWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full(i), 1);
+      mbar_init(q_empty(i), kWarps);
+    }
+    mbar_init(m_full, kWarps);
+    mbar_init(m_empty, kWarps);
+    mbar_init(u_answer, 1);
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(u_full(i), 1);
+      mbar_init(u_empty(i), kWarps);
     }
     fence_barrier_init();
   }
   __syncthreads();
 
   if (warp == kWarps) {
-    // ---------------- producer warp ----------------
+    // ---------------- producer ----------------
+    // The grid has a CTA per unit, longest first; those that find no room are
+    // taken over, one at a time, by whichever CTA needs work next. The next unit is
+    // asked for kAhead stages before the end of this one (early enough to be here
+    // in time, late enough to go to the CTA that is free first) and looked up a
+    // step a stage, so that no stage waits on the steps' dependent loads.
     if (lane == 0) {
       prefetch_tensormap(&kmap);
       prefetch_tensormap(&vmap);
     }
-    // Table entries are read ahead in chunks of 32, one per lane, one chunk in
-    // reserve, so that no stage waits on a dependent load.
-    const int32_t *trow = p.tables + size_t(s) * p.max_blocks + start / BS;
-    const int nb = (end - start + BS - 1) / BS;
-    int cur = lane < nb ? __ldg(trow + lane) : 0;
-    int nxt = 32 + lane < nb ? __ldg(trow + 32 + lane) : 0;
-    int chunk = 0, issued = 0;
-    for (int st = 0; st < nst; ++st) {
-      const int slot = st % STAGES, b0 = st * S::BPS;
-      if (b0 >= 32 * (chunk + 1)) {
-        ++chunk;
-        cur = nxt;
-        const int j = 32 * (chunk + 1) + lane;
-        nxt = j < nb ? __ldg(trow + j) : 0;
+    const int X = p.num_kv_heads, Y = p.items ? p.num_items : p.num_seqs;
+    bool ok = true;
+    int asked = 0;
+    auto ask = [&] {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(u_answer, 16);
+        try_cancel(smem_addr(&answer), u_answer);
       }
-      int phys = __shfl_sync(0xffffffffu, cur, (b0 & 31) + min(lane, S::BPS - 1));
-      if (st >= STAGES && !mbar_wait(empty_bar(slot), ((st / STAGES) - 1) & 1)) {
-        if (lane == 0) record_error(&g_rows_error, PK_DEVERR_TIMEOUT, s);
-        break;
-      }
-      const int nblk = min(S::BPS, nb - b0);
-      if (lane == 0) mbar_arrive_expect_tx(full_bar(slot), uint32_t(nblk * BS * (2 * D + 2)));
+    };
+    auto answered = [&] {  // the unit's number, or -1: none is left
+      if (!warp_wait(u_answer, asked & 1, ok)) return -1;
+      ++asked;
+      const int u = cancelled_cta(smem_addr(&answer));
+      fence_proxy_async();  // the answer has been read before the next one is asked for
       __syncwarp();
-      if (lane < nblk) {
-        if (phys < 0 || phys >= p.num_blocks) {
-          record_error(&g_rows_error, PK_DEVERR_BLOCK_ID, s);
+      return u;
+    };
+    // Unit u's sequence and partition, and with those its tokens: false where it
+    // has no work (a zero row for an invalid length, which is recorded).
+    auto item_of = [&](int u, int &s, int &part) {
+      const int x = u % X, y = (u / X) % Y, z = u / X / Y;
+      return work_item(p, y, p.num_partitions - 1 - z, x == 0 && lane == 0, s, part);
+    };
+    auto unit_of = [&](int u, int s, int part, Unit &c) {
+      const int x = u % X;
+      const SeqRows sr = seq_rows(p, s, x == 0 && lane == 0 && part == 0);
+      if (sr.ctx == 0)
+        for (int k = lane; part == 0 && k < G * D; k += 32)
+          store_elem(static_cast<IO *>(p.out) + (size_t(s) * p.num_q_heads + x * G) * D + k, 0.0f);
+      if (part >= sr.np) return false;  // no partition has tokens where ctx is 0
+      c.s = s, c.kvh = x, c.part = part, c.np = sr.np;
+      c.start = part * p.partition;
+      c.end = min(sr.ctx, c.start + p.partition);
+      c.nst = (c.end - c.start + S::TPS - 1) / S::TPS;
+      return true;
+    };
+    Unit c;  // the unit at hand
+    int u = blockIdx.x, s = 0, part = 0;
+    bool have = item_of(u, s, part) && unit_of(u, s, part, c);
+    int t = 0, i = 0;
+    for (; ok; ++i) {
+      while (!have && u >= 0 && ok) {  // units without work
+        ask();
+        u = answered();
+        have = u >= 0 && item_of(u, s, part) && unit_of(u, s, part, c);
+      }
+      if (!ok || (i >= kUnits && !warp_wait(u_empty(i), u_phase(i - kUnits), ok))) break;
+      if (lane == 0) {
+        if (have)
+          units[i % kUnits] = c;
+        else
+          units[i % kUnits].s = -1;
+        mbar_arrive(u_full(i));
+      }
+      if (!have) break;
+      // Table entries are read ahead in chunks of 32, one per lane, one chunk in
+      // reserve, so that no stage waits on a dependent load.
+      const int32_t *trow = p.tables + size_t(c.s) * p.max_blocks + c.start / BS;
+      const int nb = (c.end - c.start + BS - 1) / BS;
+      int cur = lane < nb ? __ldg(trow + lane) : 0;
+      int nxt = 32 + lane < nb ? __ldg(trow + 32 + lane) : 0;
+      int chunk = 0;
+      if (i >= 2 && !warp_wait(q_empty(i), uint32_t((i >> 1) - 1) & 1u, ok)) break;
+      if (lane == 0) mbar_arrive_expect_tx(q_full(i), uint32_t(G * D * sizeof(IO)));
+      __syncwarp();
+      if (lane < G)
+        bulk_load(q_sm + (i & 1) * S::Q_BYTES + lane * S::Q_ROW,
+                  static_cast<const IO *>(p.q) + (size_t(c.s) * p.num_q_heads + c.kvh * G + lane) * D,
+                  D * sizeof(IO), q_full(i));
+      int step = 0;  // of the next unit's look-up
+      bool item = false;
+      for (int st = 0; st < c.nst; ++st, ++t) {
+        if (c.nst - st <= kAhead) {
+          if (step == 0)
+            ask();
+          else if (step == 1)
+            u = answered(), item = u >= 0 && item_of(u, s, part);
+          ++step;
+        }
+        const int b0 = st * S::BPS;
+        if (b0 >= 32 * (chunk + 1)) {
+          ++chunk;
+          cur = nxt;
+          const int j = 32 * (chunk + 1) + lane;
+          nxt = j < nb ? __ldg(trow + j) : 0;
+        }
+        int phys = __shfl_sync(0xffffffffu, cur, (b0 & 31) + min(lane, S::BPS - 1));
+        if (t >= STAGES && !warp_wait(empty_bar(t), t_phase(t - STAGES), ok)) break;
+        const int nblk = min(S::BPS, nb - b0);
+        if (lane == 0) mbar_arrive_expect_tx(full_bar(t), uint32_t(nblk * BS * 2 * D));
+        if (lane < nblk && (phys < 0 || phys >= p.num_blocks)) {
+          record_error(&g_rows_error, PK_DEVERR_BLOCK_ID, c.s);
           phys = 0;  // stay in bounds and keep the byte count; the result is flagged
         }
-        const uint32_t dst = stages + slot * S::STAGE_BYTES + lane * BS * D;
-        tma_load_3d(dst, &kmap, full_bar(slot), 0, kvh, phys * BS);
-        tma_load_3d(dst + S::KV_BYTES, &vmap, full_bar(slot), 0, kvh, phys * BS);
-        bulk_load(exps + slot * S::EXP_BYTES + lane * BS * 2,
-                  p.kv_exp + (size_t(phys) * p.num_kv_heads + kvh) * BS * 2, BS * 2, full_bar(slot));
+        // The exponents, eight tokens' 16 bytes a lane: through the load unit, as
+        // small blocks already give TMA a request per kilobyte.
+        const int eb = __shfl_sync(0xffffffffu, phys, lane * 8 / BS % 32);
+        if (lane < S::EXP_LANES) {
+          if (lane * 8 / BS < nblk)
+            cp_async16(exps + (t % STAGES) * S::EXP_BYTES + lane * 16,
+                       p.kv_exp + ((size_t(eb) * p.num_kv_heads + c.kvh) * BS + lane * 8 % BS) * 2, 16);
+          cp_async_arrive(full_bar(t));
+        }
+        if (lane < nblk) {
+          const uint32_t dst = stages + (t % STAGES) * S::STAGE_BYTES + lane * BS * D;
+          tma_load_3d(dst, &kmap, full_bar(t), 0, c.kvh, phys * BS);
+          tma_load_3d(dst + S::KV_BYTES, &vmap, full_bar(t), 0, c.kvh, phys * BS);
+        }
       }
-      issued = st + 1;
+      if (!ok) break;
+      if (step < 2) u = answered(), item = u >= 0 && item_of(u, s, part);
+      have = item && unit_of(u, s, part, c);
     }
+    if (!ok && lane == 0) timeout();
     // Let every issued copy land before the warp leaves.
-    if (lane == 0)
-      for (int st = max(0, issued - STAGES); st < issued; ++st)
-        mbar_wait(full_bar(st % STAGES), (st / STAGES) & 1);
+    for (int k = max(0, t - STAGES); k < t; ++k) mbar_wait(full_bar(k), t_phase(k));
+    for (int k = max(0, i - 2); k < i; ++k) mbar_wait(q_full(k), uint32_t(k >> 1) & 1u);
     return;
   }
 
   // ---------------- consumer warps ----------------
-  // C fragments: a lane holds tokens rw and rw + 8 (or d rows), heads 2 qd and
-  // 2 qd + 1. A key row's 32-byte step comes as four bytes 4 qd .. 4 qd + 3 per
+  // C fragments: a lane holds rows rw and rw + 8, heads 2 qd and 2 qd + 1. Rows of
+  // the scores are tokens in the order in which a lane gets four consecutive
+  // tokens of a value column: rows 2 q, 2 q + 1, 8 + 2 q, 9 + 2 q are tokens 4 q
+  // to 4 q + 3. A key row's 32-byte step comes as four bytes 4 qd .. 4 qd + 3 per
   // lane and 16-byte chunk; the product's k index follows that order, and so
   // does the query operand.
   const int qd = lane & 3, rw = lane >> 2;
   const int mi = lane >> 3, r8 = lane & 7;
+  auto token_of = [](int row) { return 4 * ((row & 7) >> 1) + 2 * (row >> 3) + (row & 1); };
+  const int tok0 = token_of(rw);  // of row rw; that of row rw + 8 is two later
+  float *sm_o = reinterpret_cast<float *>(smem_raw + (q_sm + 2 * S::Q_BYTES - raw));
+  float *sm_m = sm_o + kWarps * 8 * S::OUT_STRIDE, *sm_l = sm_m + kWarps * 8;
+  bool ok = true;
+  for (int i = 0, t = 0; warp_wait(u_full(i), u_phase(i), ok); ++i) {
+  const Unit c = units[i % kUnits];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(u_empty(i));
+  if (c.s < 0 || !warp_wait(q_full(i), uint32_t(i >> 1) & 1u, ok)) break;
   uint32_t qb[QW][KC][4];
   float sl0, sl1;  // scale log2(e) and the query scaling undone, heads 2 qd and 2 qd + 1
   {
     float qv[KC][8];
     uint32_t top = 0;
-    const IO *qrow = static_cast<const IO *>(p.q) + (row0 + min(rw, G - 1)) * D;
+    const IO *qrow = reinterpret_cast<const IO *>(smem_raw + (q_sm - raw) + (i & 1) * S::Q_BYTES +
+                                                  min(rw, G - 1) * S::Q_ROW);
 #pragma unroll
-    for (int c = 0; c < KC; ++c)
+    for (int k = 0; k < KC; ++k)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float4 x = load4(qrow + 32 * c + 16 * h + 4 * qd);
-        qv[c][4 * h] = x.x, qv[c][4 * h + 1] = x.y, qv[c][4 * h + 2] = x.z, qv[c][4 * h + 3] = x.w;
+        const float4 x = load4(qrow + 32 * k + 16 * h + 4 * qd);
+        qv[k][4 * h] = x.x, qv[k][4 * h + 1] = x.y, qv[k][4 * h + 2] = x.z, qv[k][4 * h + 3] = x.w;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t b = __float_as_uint(qv[c][4 * h + i]) & 0x7fffffffu;
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t b = __float_as_uint(qv[k][4 * h + e]) & 0x7fffffffu;
           top = max(top, b < 0x7f800000u ? b : 0u);
         }
       }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_empty(i));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const int up = min(126, 14 - (int(top >> 23) - 127));  // >= -113
@@ -209,34 +332,32 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
     sl0 = __shfl_sync(0xffffffffu, sl, 8 * qd);
     sl1 = __shfl_sync(0xffffffffu, sl, 8 * qd + 4);
 #pragma unroll
-    for (int c = 0; c < KC; ++c)
+    for (int k = 0; k < KC; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = rw < G ? qv[c][2 * i] * f : 0.0f, b = rw < G ? qv[c][2 * i + 1] * f : 0.0f;
-        qb[0][c][i] = pack_f16x2(a, b);
+      for (int e = 0; e < 4; ++e) {
+        const float a = rw < G ? qv[k][2 * e] * f : 0.0f, b = rw < G ? qv[k][2 * e + 1] * f : 0.0f;
+        qb[0][k][e] = pack_f16x2(a, b);
         if (QW == 2) {
-          const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&qb[0][c][i]));
-          qb[QW - 1][c][i] = pack_f16x2(a - hi.x, b - hi.y);
+          const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&qb[0][k][e]));
+          qb[QW - 1][k][e] = pack_f16x2(a - hi.x, b - hi.y);
         }
       }
   }
-  float o[KC][2][4];  // [32-column step][even, odd column]
+  float o[KC][2][4];  // [32-column step][16-column half]
 #pragma unroll
-  for (int c = 0; c < KC; ++c)
+  for (int k = 0; k < KC; ++k)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) o[c][h][0] = o[c][h][1] = o[c][h][2] = o[c][h][3] = 0.0f;
+    for (int h = 0; h < 2; ++h) o[k][h][0] = o[k][h][1] = o[k][h][2] = o[k][h][3] = 0.0f;
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-  const int t0 = warp * 16;
-
-  for (int st = 0; st < nst; ++st) {
-    const int slot = st % STAGES;
-    if (!mbar_wait(full_bar(slot), (st / STAGES) & 1)) {
-      if (lane == 0) record_error(&g_rows_error, PK_DEVERR_TIMEOUT, s);
-      break;
-    }
+  for (int st = 0; st < c.nst; ++st, ++t) {
+    const int slot = t % STAGES;
+    if (!warp_wait(full_bar(t), t_phase(t), ok)) break;
     const uint32_t kbase = stages + slot * S::STAGE_BYTES, vbase = kbase + S::KV_BYTES;
-    const int nvalid = end - (start + st * kTps + t0);
-    if (nvalid > 0) {
+#pragma unroll 1
+    for (int tile = 0; tile < S::TILES; ++tile) {
+      const int t0 = (tile * kWarps + warp) * 16;
+      const int nvalid = c.end - (c.start + st * S::TPS + t0);
+      if (nvalid <= 0) break;
       if (nvalid < 16) {
         // Rows past the end may hold anything: zero values, so that a zero
         // weight never meets a NaN.
@@ -246,26 +367,27 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
         }
         __syncwarp();
       }
-      uint32_t e0, e1;  // exponents of tokens rw, rw + 8: K in the low byte, V above
+      uint32_t e0, e1;  // exponents of the lane's tokens: K in the low byte, V above
       {
-        const uint32_t a = exps + slot * S::EXP_BYTES + (t0 + rw) * 2;
+        const uint32_t a = exps + slot * S::EXP_BYTES + (t0 + tok0) * 2;
         asm volatile("ld.shared.u16 %0, [%1];" : "=r"(e0) : "r"(a));
-        asm volatile("ld.shared.u16 %0, [%1];" : "=r"(e1) : "r"(a + 16));
+        asm volatile("ld.shared.u16 %0, [%1];" : "=r"(e1) : "r"(a + 4));
       }
       // S^T = K_tile Q^T; low 16 bits and high 16 bits of a lane's four bytes
       // are the two k halves of one product.
       float sa[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
-      for (int c = 0; c < KC; ++c) {
+      for (int k = 0; k < KC; ++k) {
         uint32_t r[4];
-        ldmatrix_x4(kbase + swizzled<D>(t0 + (mi & 1) * 8 + r8, 2 * c + (mi >> 1)), r[0], r[1], r[2], r[3]);
+        ldmatrix_x4(kbase + swizzled<D>(t0 + token_of((mi & 1) * 8 + r8), 2 * k + (mi >> 1)), r[0], r[1], r[2], r[3]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t a0 = e4m3x2_to_f16x2(r[2 * h]), a2 = e4m3x2_to_f16x2(r[2 * h] >> 16);
-          const uint32_t a1 = e4m3x2_to_f16x2(r[2 * h + 1]), a3 = e4m3x2_to_f16x2(r[2 * h + 1] >> 16);
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16x4(r[2 * h], a0, a2);
+          e4m3x4_to_f16x4(r[2 * h + 1], a1, a3);
 #pragma unroll
           for (int w = 0; w < QW; ++w)
-            mma_f16_16816(sa[h], a0, a1, a2, a3, qb[w][c][2 * h], qb[w][c][2 * h + 1]);
+            mma_f16_16816(sa[h], a0, a1, a2, a3, qb[w][k][2 * h], qb[w][k][2 * h + 1]);
         }
       }
       const float k0 = __uint_as_float((e0 & 0xffu) << 23), k1 = __uint_as_float((e1 & 0xffu) << 23);
@@ -274,14 +396,14 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
       // far smaller values out of fp16's range.
       int ev0 = int(e0 >> 8) - 127, ev1 = int(e1 >> 8) - 127;
       if (__any_sync(0xffffffffu, ev0 == 0 || ev1 == 0)) {
-        if (zero_row<D>(vbase, t0 + rw)) ev0 = -100;
-        if (zero_row<D>(vbase, t0 + rw + 8)) ev1 = -100;
+        if (zero_row<D>(vbase, t0 + tok0)) ev0 = -100;
+        if (zero_row<D>(vbase, t0 + tok0 + 2)) ev1 = -100;
       }
       const float v0 = float(ev0), v1 = float(ev1);
       float x0 = (sa[0][0] + sa[1][0]) * sl0 * k0, x1 = (sa[0][1] + sa[1][1]) * sl1 * k0;
       float x2 = (sa[0][2] + sa[1][2]) * sl0 * k1, x3 = (sa[0][3] + sa[1][3]) * sl1 * k1;
-      if (rw >= nvalid) x0 = x1 = -INFINITY;
-      if (rw + 8 >= nvalid) x2 = x3 = -INFINITY;
+      if (tok0 >= nvalid) x0 = x1 = -INFINITY;
+      if (tok0 + 2 >= nvalid) x2 = x3 = -INFINITY;
       float z0 = fmaxf(x0 + v0, x2 + v1), z1 = fmaxf(x1 + v0, x3 + v1);
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {
@@ -311,35 +433,33 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
       }
       if (__any_sync(0xffffffffu, c0 != 1.0f || c1 != 1.0f)) {
 #pragma unroll
-        for (int c = 0; c < KC; ++c)
+        for (int k = 0; k < KC; ++k)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            o[c][h][0] *= c0;
-            o[c][h][1] *= c1;
-            o[c][h][2] *= c0;
-            o[c][h][3] *= c1;
+            o[k][h][0] *= c0;
+            o[k][h][1] *= c1;
+            o[k][h][2] *= c0;
+            o[k][h][3] *= c1;
           }
       }
-      // O^T += V^T P^T. A transposed load pairs two columns of one token; the
-      // byte permutation pairs two tokens of one column instead, even columns
-      // low and odd ones high.
+      // O^T += V^T P^T: a transposed load gives a lane four tokens of a column, the
+      // ones that its rows of the scores belong to.
 #pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        uint32_t r[4];
-        ldmatrix_x4_trans(vbase + swizzled<D>(t0 + (mi >> 1) * 8 + r8, 2 * c + (mi & 1)), r[0], r[1], r[2], r[3]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = __byte_perm(r[i], 0, 0x3120);
+      for (int k = 0; k < KC; ++k) {
+        uint32_t r[4];  // columns 32 k + rw, + 8 of both 16-column halves
+        ldmatrix_b8_x2_trans(vbase + swizzled<D>(t0 + (lane & 15), 2 * k + (lane >> 4)), r[0], r[1], r[2], r[3]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t a0 = e4m3x2_to_f16x2(r[0] >> (16 * h)), a1 = e4m3x2_to_f16x2(r[1] >> (16 * h));
-          const uint32_t a2 = e4m3x2_to_f16x2(r[2] >> (16 * h)), a3 = e4m3x2_to_f16x2(r[3] >> (16 * h));
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16x4(r[2 * h], a0, a2);
+          e4m3x4_to_f16x4(r[2 * h + 1], a1, a3);
 #pragma unroll
-          for (int w = 0; w < QW; ++w) mma_f16_16816(o[c][h], a0, a1, a2, a3, b[w][0], b[w][1]);
+          for (int w = 0; w < QW; ++w) mma_f16_16816(o[k][h], a0, a1, a2, a3, b[w][0], b[w][1]);
         }
       }
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(empty_bar(slot));
+    if (lane == 0) mbar_arrive(empty_bar(t));
   }
 
   // The denominators of a warp's 16 tokens lie in the 8 lanes of a quad index.
@@ -348,20 +468,19 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
     l0 += __shfl_xor_sync(0xffffffffu, l0, off);
     l1 += __shfl_xor_sync(0xffffffffu, l1, off);
   }
-  // Merge the consumer warps' states in shared memory (the ring is free: every
-  // copy has landed and been consumed).
-  named_barrier(1, kWarps * 32);
-  float *sm_o = reinterpret_cast<float *>(smem_raw + (stages - raw));
-  float *sm_m = sm_o + kWarps * 8 * S::OUT_STRIDE, *sm_l = sm_m + kWarps * 8;
+  if (!ok) break;
+  // Merge the consumer warps' states in shared memory, once all have read the
+  // unit's before.
+  if (i > 0 && !warp_wait(m_empty, uint32_t(i - 1) & 1u, ok)) break;
 #pragma unroll
-  for (int c = 0; c < KC; ++c)
+  for (int k = 0; k < KC; ++k)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float *base = sm_o + (warp * 8 + 2 * qd) * S::OUT_STRIDE + 32 * c + 2 * rw + h;
-      base[0] = o[c][h][0];
-      base[S::OUT_STRIDE] = o[c][h][1];
-      base[16] = o[c][h][2];
-      base[S::OUT_STRIDE + 16] = o[c][h][3];
+      float *base = sm_o + (warp * 8 + 2 * qd) * S::OUT_STRIDE + 32 * k + 16 * h + rw;
+      base[0] = o[k][h][0];
+      base[S::OUT_STRIDE] = o[k][h][1];
+      base[8] = o[k][h][2];
+      base[S::OUT_STRIDE + 8] = o[k][h][3];
     }
   if (rw == 0) {
     sm_m[warp * 8 + 2 * qd] = m0;
@@ -369,9 +488,12 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
     sm_l[warp * 8 + 2 * qd] = l0;
     sm_l[warp * 8 + 2 * qd + 1] = l1;
   }
-  named_barrier(1, kWarps * 32);
-  for (int i = threadIdx.x; i < G * D; i += kWarps * 32) {
-    const int g = i / D, col = i % D;
+  __syncwarp();
+  if (lane == 0) mbar_arrive(m_full);
+  if (!warp_wait(m_full, uint32_t(i) & 1u, ok)) break;
+  const size_t row0 = size_t(c.s) * p.num_q_heads + c.kvh * G;  // the group's first row of out
+  for (int k = threadIdx.x; k < G * D; k += kWarps * 32) {
+    const int g = k / D, col = k % D;
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w * 8 + g]);
@@ -382,10 +504,10 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
       L = fmaf(sm_l[w * 8 + g], f, L);
       O = fmaf(sm_o[(w * 8 + g) * S::OUT_STRIDE + col], f, O);
     }
-    if (sr.np == 1) {
+    if (c.np == 1) {
       store_elem(static_cast<IO *>(p.out) + (row0 + g) * D + col, O / L);
     } else {
-      const size_t slot = (row0 + g) * p.num_partitions + part;
+      const size_t slot = (row0 + g) * p.num_partitions + c.part;
       p.ws_acc[slot * D + col] = O;
       if (col == 0) {
         p.ws_m[slot] = M;
@@ -393,6 +515,10 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
       }
     }
   }
+  __syncwarp();
+  if (lane == 0) mbar_arrive(m_empty);
+  }
+  if (!ok && lane == 0) timeout();
 }
 
 // The codes of a pool, [N * B, Hk, D] bytes; a load is one head's rows of a block.
@@ -413,13 +539,16 @@ bool encode_codes(CUtensorMap *map, const void *pool, const pk_cache_desc &d) {
 
 template <typename IO, int D, int BS>
 pk_status launch(const RowsParams &p, const pk_cache_desc &d, cudaStream_t stream) {
-  using S = Shape<D, BS>;
+  using S = Shape<IO, D, BS>;
   CUtensorMap kmap, vmap;
   if (!encode_codes<D>(&kmap, p.k_cache, d) || !encode_codes<D>(&vmap, p.v_cache, d)) return PK_ERR_CUDA;
   auto kern = attn_e4m3_kernel<IO, D, BS>;
   static std::atomic<uint64_t> ready{0};
   if (!smem_ready(kern, S::SMEM_BYTES, ready)) return PK_ERR_CUDA;
-  kern<<<rows_grid(p), (kWarps + 1) * 32, S::SMEM_BYTES, stream>>>(p, kmap, vmap);
+  const dim3 g = rows_grid(p);
+  const int64_t units = int64_t(g.x) * g.y * g.z;
+  if (units > INT32_MAX) return PK_ERR_UNSUPPORTED;
+  kern<<<unsigned(units), kThreads, S::SMEM_BYTES, stream>>>(p, kmap, vmap);
   return cudaGetLastError() == cudaSuccess ? PK_OK : PK_ERR_CUDA;
 }
 

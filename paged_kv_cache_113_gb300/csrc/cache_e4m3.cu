@@ -46,9 +46,10 @@ struct Place {
 
 template <int LANES>
 __device__ __forceinline__ bool place_of(const RowParams &p, Place &at) {
-  const int64_t unit = int64_t(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
-  at.tok = unit / p.hk;
-  at.h = int(unit % p.hk);
+  const uint32_t unit = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
+  const uint32_t t = unit / uint32_t(p.hk);
+  at.tok = t;
+  at.h = int(unit - t * p.hk);
   at.e0 = (threadIdx.x % LANES) * 16;
   if (at.tok >= p.num_tokens) return false;
   at.slot = __ldg(p.slots + at.tok);
@@ -194,7 +195,7 @@ pk_status by_lanes(const RowParams &p, F f) {
   auto go = [&](auto c) {
     constexpr int L = decltype(c)::value;
     const int64_t ctas = (units + 256 / L - 1) / (256 / L);
-    if (ctas > INT32_MAX) return PK_ERR_UNSUPPORTED;
+    if (units > INT32_MAX) return PK_ERR_UNSUPPORTED;
     f(c, unsigned(ctas));
     return cudaGetLastError() == cudaSuccess ? PK_OK : PK_ERR_CUDA;
   };

@@ -116,6 +116,10 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int by
                "l"(__cvta_generic_to_global(src)), "r"(bytes)
                : "memory");
 }
+// cp_async_arrive: an arrival on the mbarrier (one that it counts) once they have.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Orders this thread's earlier generic-proxy memory writes before later
@@ -202,6 +206,18 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t &r0, u
                : "memory");
 }
 
+// Two 16x16 matrices of bytes, transposed: lanes 0 - 15 give the first one's row
+// addresses, 16 - 31 the second's. r0 holds bytes 4 (lane % 4) .. + 3 of row
+// lane / 4 of the first transposed matrix, r1 of row 8 + lane / 4; r2, r3 the
+// second's.
+__device__ __forceinline__ void ldmatrix_b8_x2_trans(uint32_t addr, uint32_t &r0, uint32_t &r1,
+                                                     uint32_t &r2, uint32_t &r3) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr)
+               : "memory");
+}
+
 // Transposes an 8x8 matrix of 16-bit values held one row pair per thread.
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t y;
@@ -230,15 +246,14 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Two e4m3 codes (low 16 bits of x, low code first) as an fp16x2 word: exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
-  uint32_t y;
-  asm("{\n\t.reg .b16 h;\n\t"
-      "cvt.u16.u32 h, %1;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, h;\n\t}"
-      : "=r"(y)
+// Four e4m3 codes as two fp16x2 words, the low two codes first: exact.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t x, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
       : "r"(x));
-  return y;
 }
 
 // Two floats to an fp16x2 word (lo in the low half), round to nearest even.

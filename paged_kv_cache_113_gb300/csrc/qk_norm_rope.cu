@@ -40,9 +40,6 @@ struct RopeParams {
   int32_t heads;                // heads of a token that have work: Hq + Hk (+ Hk values)
 };
 
-#ifndef PK_RU
-#define PK_RU 4
-#endif
 // Rounds per warp: 4 from this many heads on, else 1.
 constexpr int64_t kManyHeads = 16384;
 
@@ -159,7 +156,7 @@ pk_status launch(RopeParams p, cudaStream_t stream) {
     if (p.d <= 128) return go(integral_constant<int, 16>(), rounds_c);
     return go(integral_constant<int, 32>(), rounds_c);
   };
-  return int64_t(p.num_tokens) * p.heads >= kManyHeads ? by_lanes(integral_constant<int, PK_RU>())
+  return int64_t(p.num_tokens) * p.heads >= kManyHeads ? by_lanes(integral_constant<int, 4>())
                                                        : by_lanes(integral_constant<int, 1>());
 }
 
