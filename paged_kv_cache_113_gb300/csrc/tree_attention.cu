@@ -326,7 +326,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     setmaxnreg_inc<kSoftmaxRegs>();
     const int r = threadIdx.x;
     const uint32_t lane_base = uint32_t(warp * 32) << 16;
-    const float sl = fabsf(p.scale_log2);
+    // At least the smallest normal number: a scale of 0 must not turn the -inf of
+    // what is masked into NaN.
+    const float sl = fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);
     bool ok = true;
     auto wait = [&](uint32_t b, uint32_t parity) { return warp_wait(b, parity, ok); };
     // A unit's queries into shared memory, rows past the last as zeros.

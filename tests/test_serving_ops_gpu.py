@@ -666,3 +666,158 @@ def test_tree_attention_repeats_bit_for_bit():
                 first = out
                 check_tree(out, q, k, v, tables, lens, d ** -0.5, ofs, masks, d, torch.bfloat16)
             assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30, 4.0])
+def test_scales_of_any_sign(scale):
+    """Zero weighs every seen token alike; a negative scale reverses the order."""
+    hq, hk, d, B = 4, 2, 128, 16
+    rng = np.random.default_rng(55)
+    counts, lens = np.array([5, 3], np.int32), np.array([70, 150], np.int32)
+    for dt in (torch.bfloat16, torch.float32):
+        tables, k, v, ofs, masks, q, mt = tree_case(rng, counts, lens, B, hq, hk, d, dt, "any")
+        out = torch.full_like(q, 5.0)
+        pk.pk_paged_attention_tree(out, q, k, v, i32(tables), i32(lens), i32(ofs), scale, 5, 150, tree_mask=mt)
+        n = int(ofs[-1])
+        want, (wv, mag, cnt) = plain.tree_attention(f64(q), f64(k), f64(v), tables, lens, scale, ofs, masks)
+        check_attention(f64(out)[:n], want[:n], (wv[:n], np.abs(mag[:n]), cnt[:n]), d, dt, RHO_TREE[dt])
+        tables, N = tables_for(rng, lens, B)
+        kc, vc, ex, vals = fill_e4m3(rng, tables, lens, N, B, hk, d)
+        q = rand(rng, (2, hq, d), dt)
+        out = torch.empty_like(q)
+        pk.pk_paged_attention_decode_e4m3(out, q, kc, vc, ex, i32(tables), i32(lens), scale, 150, partition_size=0)
+        want, (wv, mag, cnt) = plain.tree_attention(f64(q), *vals, tables, lens, scale)
+        check_attention(f64(out), want, (wv, np.abs(mag), cnt), d, dt, RHO_E4M3[dt])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_more_units_than_fit_and_sequences_without_work(dtype):
+    """Hundreds of units for the persistent kernels, among them sequences without
+    drafts, of invalid length and of one token; with a grid of partitions of which
+    most are empty."""
+    dt, hq, hk, d, B, S = DTYPES[dtype], 16, 16, 64, 16, 90
+    rng = np.random.default_rng(66)
+    lens = rng.integers(1, 90, S).astype(np.int32)
+    lens[::9] = 1
+    counts = np.minimum(rng.integers(0, 4, S), lens).astype(np.int32)
+    counts[5::7] = 0
+    tables, k, v, ofs, masks, q, mt = tree_case(rng, counts, lens, B, hq, hk, d, dt, "tree")
+    want, terms = plain.tree_attention(f64(q), f64(k), f64(v), tables, lens, 0.125, ofs, masks)
+    n = int(ofs[-1])
+    for part in (0, 16):
+        out = torch.full_like(q, 5.0)
+        ws = torch.empty(max(16, pk.pk_tree_workspace_size(len(q), hq, 90, part, pk.cache_desc(k))), dtype=torch.uint8,
+                         device=DEV)
+        pk.pk_paged_attention_tree(out, q, k, v, i32(tables), i32(lens), i32(ofs), 0.125, 3, 90, tree_mask=mt,
+                                   partition_size=part, workspace=ws)
+        check_attention(f64(out)[:n], want[:n], tuple(t[:n] for t in terms), d, dt, RHO_TREE[dt])
+        assert (out[n:] == 5.0).all()
+    # every other sequence shorter than its drafts: zero rows, the others as before
+    short = lens.copy()
+    bad = (np.arange(S) % 2 == 0) & (counts > 0)
+    short[bad] = counts[bad] - 1
+    out = torch.full_like(q, 5.0)
+    pk.pk_paged_attention_tree(out, q, k, v, i32(tables), i32(short), i32(ofs), 0.125, 3, 90, tree_mask=mt)
+    assert pk.pk_get_device_error()[0] == 4
+    row_bad = np.repeat(bad, counts)
+    got = f64(out)[:n]
+    assert (got[row_bad] == 0).all()
+    check_attention(got, want[:n], tuple(t[:n] for t in terms), d, dt, RHO_TREE[dt], ~row_bad)
+
+    kc, vc, ex, vals = fill_e4m3(rng, tables, lens, int(k.shape[0]), B, hk, d)
+    q = rand(rng, (S, hq, d), dt)
+    want, terms = plain.tree_attention(f64(q), *vals, tables, lens, 0.125)
+    for part, bad in ((0, False), (16, False), (0, True)):
+        use = lens.copy()
+        if bad:
+            use[::2] = 0
+        out = torch.full_like(q, 5.0)
+        ws = torch.empty(max(16, pk.pk_paged_attention_workspace_size(S, hq, 90, part, pk.cache_desc(kc))),
+                         dtype=torch.uint8, device=DEV)
+        pk.pk_paged_attention_decode_e4m3(out, q, kc, vc, ex, i32(tables), i32(use), 0.125, 90, partition_size=part,
+                                          workspace=ws)
+        if bad:
+            assert pk.pk_get_device_error()[0] == 4 and (out[::2] == 0).all()
+        live = np.ones(S, bool)
+        live[::2] = not bad
+        check_attention(f64(out), want, terms, d, dt, RHO_E4M3[dt], live)
+
+
+def test_offsets_past_32_bits():
+    """Blocks at the end of pools of more than 2^31 elements, and 2^32 bytes."""
+    hq, hk, d, B = 4, 2, 128, 16
+    rng = np.random.default_rng(88)
+    N = (2 ** 31) // (B * hk * d) + 64
+    lens, counts = np.array([40, 20], np.int32), np.array([3, 1], np.int32)
+    tables = np.full((2, 3), -1, np.int32)
+    tables[0, :3], tables[1, :2] = [N - 1, N - 7, 3], [N - 2, N - 20]
+    use = np.unique(tables[tables >= 0])
+    small = np.searchsorted(use, tables).astype(np.int32)          # the same blocks, packed
+    kc = torch.empty((N, B, hk, d), dtype=torch.bfloat16, device=DEV)
+    vc = torch.empty_like(kc)
+    blocks = i64(use)
+    kc[blocks], vc[blocks] = rand(rng, (len(use), B, hk, d), torch.bfloat16), rand(rng, (len(use), B, hk, d), torch.bfloat16)
+    q, ofs = rand(rng, (4, hq, d), torch.bfloat16), [0, 3, 4]
+    # new tokens through the fused write, at slots of the last blocks
+    qkv = rand(rng, (4, hq + 2 * hk, d), torch.bfloat16)
+    slots = np.array([(N - 1) * B + 15, (N - 7) * B + 3, (N - 2) * B, (N - 20) * B + 1])
+    qo = torch.empty((4, hq, d), dtype=torch.bfloat16, device=DEV)
+    pk.pk_qk_norm_rope_and_cache(qo, None, qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:], None, None,
+                                 slot_mapping=i64(slots), k_cache=kc, v_cache=vc)
+    for s, row in zip(slots, qkv[:, hq:]):
+        assert torch.equal(kc[int(s) // B, int(s) % B], row[:hk]) and torch.equal(vc[int(s) // B, int(s) % B], row[hk:])
+    out = torch.full_like(q, 5.0)
+    pk.pk_paged_attention_tree(out, q, kc, vc, i32(tables), i32(lens), i32(ofs), 0.09, 3, 40)
+    want, terms = plain.tree_attention(f64(q), f64(kc[blocks]), f64(vc[blocks]), small, lens, 0.09, ofs, None)
+    check_attention(f64(out), want, terms, d, torch.bfloat16, RHO_TREE[torch.bfloat16])
+    del kc, vc
+    torch.cuda.empty_cache()
+    k8 = torch.empty((N, B, hk, d), dtype=torch.float8_e4m3fn, device=DEV)
+    v8 = torch.empty_like(k8)
+    ex = torch.empty((N, hk, B, 2), dtype=torch.uint8, device=DEV)
+    every = (use[:, None].astype(np.int64) * B + np.arange(B)).reshape(-1)
+    k, v = rand(rng, (len(every), hk, d)), rand(rng, (len(every), hk, d))
+    pk.pk_reshape_and_cache_e4m3(k, v, i64(every), k8, v8, ex)
+    k2, v2 = torch.empty_like(k), torch.empty_like(v)
+    pk.pk_gather_cache_e4m3(k2, v2, i64(every), k8, v8, ex)
+    assert (k2 - k).abs().max() <= k.abs().max() * 2.0 ** -4 and (v2 - v).abs().max() <= v.abs().max() * 2.0 ** -4
+    q = rand(rng, (2, hq, d))
+    out = torch.empty_like(q)
+    pk.pk_paged_attention_decode_e4m3(out, q, k8, v8, ex, i32(tables), i32(lens), 0.09, 40, partition_size=0)
+    want, terms = plain.tree_attention(f64(q), f64(k2).reshape(-1, B, hk, d), f64(v2).reshape(-1, B, hk, d), small, lens, 0.09)
+    check_attention(f64(out), want, terms, d, torch.float32, RHO_E4M3[torch.float32])
+
+
+def test_two_streams_at_once():
+    """Overlapping calls of the attentions on two streams, with a workspace each."""
+    hq, hk, d, B, S = 8, 2, 128, 16, 40
+    rng = np.random.default_rng(99)
+    lens = rng.integers(40, 900, S).astype(np.int32)
+    counts = rng.integers(1, 9, S).astype(np.int32)
+    tables, k, v, ofs, masks, q, mt = tree_case(rng, counts, lens, B, hq, hk, d, torch.bfloat16, "tree", pad=0)
+    kc, vc, ex, _ = fill_e4m3(rng, tables, lens, int(k.shape[0]), B, hk, d)
+    qd = rand(rng, (S, hq, d), torch.bfloat16)
+    tb, ln, of = i32(tables), i32(lens), i32(ofs)
+
+    def call(stream=None):
+        outs = [torch.zeros_like(q), torch.zeros_like(qd)]
+        ws = [torch.empty(pk.pk_tree_workspace_size(len(q), hq, 900, 128, pk.cache_desc(k)), dtype=torch.uint8, device=DEV),
+              torch.empty(pk.pk_paged_attention_workspace_size(S, hq, 900, 128, pk.cache_desc(kc)), dtype=torch.uint8,
+                          device=DEV)]
+        torch.cuda.synchronize()
+        return outs, ws, lambda: (
+            pk.pk_paged_attention_tree(outs[0], q, k, v, tb, ln, of, 0.09, 8, 900, tree_mask=mt, partition_size=128,
+                                       workspace=ws[0], stream=stream),
+            pk.pk_paged_attention_decode_e4m3(outs[1], qd, kc, vc, ex, tb, ln, 0.09, 900, partition_size=128,
+                                              workspace=ws[1], stream=stream))
+
+    ref, _, f = call()
+    f()
+    torch.cuda.synchronize()
+    sides = [call(torch.cuda.Stream()) for _ in range(3)]
+    for _ in range(20):
+        for _, _, f in sides:
+            f()
+    torch.cuda.synchronize()
+    for outs, _, _ in sides:
+        assert torch.equal(outs[0], ref[0]) and torch.equal(outs[1], ref[1])
