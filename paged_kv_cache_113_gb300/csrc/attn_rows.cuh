@@ -1,7 +1,6 @@
 // Shared by the attention kernels over 8-bit caches and over drafted tokens:
-// the launch parameters, a sequence's place in the batch, the CUDA-core
-// kernel for fp32 and for shapes the tensor-core kernels are not compiled
-// for, and the log-sum-exp merge of split rows.
+// the launch parameters, a sequence's place in the batch, and the log-sum-exp
+// merge of split rows.
 //
 // A sequence s has n_s query tokens (1 without q_offsets), the last n_s of its
 // context. With base = ctx - n_s, query i of it sees every token t < base and
@@ -11,7 +10,6 @@
 #pragma once
 
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -110,174 +108,11 @@ __device__ __forceinline__ uint64_t see64(uint64_t mask, int base, int t0) {
   return mask >> -cut;
 }
 
-// Tile element types of the pools: four values of a row as fp32.
-struct E4M3 {
-  uint8_t x;
-};
+// Four consecutive elements as fp32 values.
 template <typename T>
 __device__ __forceinline__ float4 load4(const T *p) {
   return widen4(raw4(p));
 }
-__device__ __forceinline__ float4 load4(const E4M3 *p) {
-  const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
-  const float2 a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(uint16_t(w & 0xffff), __NV_E4M3)));
-  const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(uint16_t(w >> 16), __NV_E4M3)));
-  return make_float4(a.x, a.y, b.x, b.y);
-}
-
-// ---------------------------------------------------------------------------
-// CUDA-core kernel. One CTA of 8 warps per (KV head, tile of 8 * RPW rows,
-// sequence, partition); 32 tokens of K and V at a time are widened into shared
-// memory. Scores: a lane owns a token and goes over the warp's RPW rows, whose
-// queries broadcast. Values: a lane owns D / 32 columns.
-// ---------------------------------------------------------------------------
-template <int D, int RPW>
-struct RowsShape {
-  static constexpr int NW = 8, TT = 32, R = NW * RPW;
-  static constexpr int KS = D + 4;  // padded: lanes read their rows without bank conflicts
-  static constexpr int FLOATS = TT * KS + TT * D + R * D + NW * RPW * TT;
-  static constexpr int SMEM_BYTES = FLOATS * 4;
-};
-
-template <typename Pool, typename IO, int D, int RPW>
-__global__ void __launch_bounds__(256) attn_rows_kernel(RowsParams p) {
-  using S = RowsShape<D, RPW>;
-  constexpr int EPL = D / 32;
-  extern __shared__ __align__(16) float smem[];
-  launch_dependents();  // the merge may be scheduled as this grid drains
-  float *ks = smem, *vs = ks + S::TT * S::KS, *qs = vs + S::TT * D, *ps = qs + S::R * D;
-  const int kvh = blockIdx.x / p.row_tiles, tile = blockIdx.x % p.row_tiles;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool record = blockIdx.x == 0 && threadIdx.x == 0;
-  int s, part;
-  if (!work_item(p, blockIdx.y, blockIdx.z, record, s, part)) return;
-  const SeqRows sr = seq_rows(p, s, record && part == 0);
-  const int G = p.group, r0 = tile * S::R, rows = min(S::R, sr.n * G - r0);
-  if (rows <= 0) return;
-  auto q_row = [&](int r) {  // element offset of row r0 + r in q and out
-    return (size_t(sr.q0 + (r0 + r) / G) * p.num_q_heads + kvh * G + (r0 + r) % G) * D;
-  };
-  if (sr.ctx == 0) {
-    if (part == 0)
-      for (int i = threadIdx.x; i < rows * D; i += 256)
-        store_elem(static_cast<IO *>(p.out) + q_row(i / D) + i % D, 0.0f);
-    return;
-  }
-  if (part >= sr.np) return;
-  const int start = part * p.partition;
-  const int end = min(sr.ctx, start + p.partition), base = sr.ctx - sr.n;
-  for (int i = threadIdx.x; i < S::R * D; i += 256)
-    qs[i] = i / D < rows ? load_elem(static_cast<const IO *>(p.q) + q_row(i / D) + i % D) * p.scale_log2
-                         : 0.0f;
-  float m[RPW], l[RPW], acc[RPW][EPL];
-  uint64_t mask[RPW];
-#pragma unroll
-  for (int r = 0; r < RPW; ++r) {
-    const int row = warp * RPW + r;
-    m[r] = -INFINITY;
-    l[r] = 0.0f;
-    mask[r] = row < rows ? draft_mask(p, sr.q0, (r0 + row) / G, sr.n) : 0;
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) acc[r][e] = 0.0f;
-  }
-  const int32_t *trow = p.tables + size_t(s) * p.max_blocks;
-  const int B = p.block_size;
-  for (int t0 = start; t0 < end; t0 += S::TT) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < S::TT * (D / 4); i += 256) {
-      const int j = i / (D / 4), c = (i % (D / 4)) * 4, t = t0 + j;
-      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
-      if (t < end) {
-        const int phys = __ldg(trow + t / B);
-        if (phys < 0 || phys >= p.num_blocks) {
-          record_error(&g_rows_error, PK_DEVERR_BLOCK_ID, s);
-        } else {
-          const size_t row = ((size_t(phys) * B + t % B) * p.num_kv_heads + kvh) * D + c;
-          a = load4(static_cast<const Pool *>(p.k_cache) + row);
-          b = load4(static_cast<const Pool *>(p.v_cache) + row);
-          if (sizeof(Pool) == 1) {
-            const uint16_t e = *reinterpret_cast<const uint16_t *>(
-                p.kv_exp + ((size_t(phys) * p.num_kv_heads + kvh) * B + t % B) * 2);
-            const float ka = __uint_as_float(uint32_t(e & 0xff) << 23);
-            const float va = __uint_as_float(uint32_t(e >> 8) << 23);
-            a.x *= ka, a.y *= ka, a.z *= ka, a.w *= ka;
-            b.x *= va, b.y *= va, b.z *= va, b.w *= va;
-          }
-        }
-      }
-      *reinterpret_cast<float4 *>(ks + j * S::KS + c) = a;
-      *reinterpret_cast<float4 *>(vs + j * D + c) = b;
-    }
-    __syncthreads();
-    if (warp * RPW >= rows) continue;
-    float x[RPW];
-#pragma unroll
-    for (int r = 0; r < RPW; ++r) x[r] = 0.0f;
-    for (int c = 0; c < D; c += 4) {
-      const float4 k = *reinterpret_cast<const float4 *>(ks + lane * S::KS + c);
-#pragma unroll
-      for (int r = 0; r < RPW; ++r) {
-        const float4 q = *reinterpret_cast<const float4 *>(qs + (warp * RPW + r) * D + c);
-        x[r] = fmaf(k.x, q.x, fmaf(k.y, q.y, fmaf(k.z, q.z, fmaf(k.w, q.w, x[r]))));
-      }
-    }
-    float *pw = ps + warp * RPW * S::TT;
-#pragma unroll
-    for (int r = 0; r < RPW; ++r) {
-      const int t = t0 + lane;
-      const bool see = t < end && (t < base || ((mask[r] >> (t - base)) & 1));
-      if (!see) x[r] = -INFINITY;
-      float mx = x[r];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float mn = fmaxf(m[r], mx);
-      const float ref = mn == -INFINITY ? 0.0f : mn;  // nothing seen so far: every weight is 0
-      const float corr = exp2f(m[r] - ref), w = exp2f(x[r] - ref);
-      l[r] = fmaf(l[r], corr, w);
-      m[r] = mn;
-      pw[r * S::TT + lane] = w;
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) acc[r][e] *= corr;
-    }
-    __syncwarp();
-    for (int j = 0; j < S::TT; ++j) {
-      float v[EPL];
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) v[e] = vs[j * D + lane * EPL + e];
-#pragma unroll
-      for (int r = 0; r < RPW; ++r) {
-        const float w = pw[r * S::TT + j];
-        if (w != 0.0f)  // a token of no weight adds nothing, whatever its value holds
-#pragma unroll
-          for (int e = 0; e < EPL; ++e) acc[r][e] = fmaf(w, v[e], acc[r][e]);
-      }
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < RPW; ++r) {
-    const int row = warp * RPW + r;
-    float sum = l[r];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (row >= rows) continue;
-    const size_t at = q_row(row);
-    if (sr.np == 1) {
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-      for (int e = 0; e < EPL; ++e)
-        store_elem(static_cast<IO *>(p.out) + at + lane * EPL + e, acc[r][e] * inv);
-    } else {
-      const size_t slot = at / D * p.num_partitions + part;
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) p.ws_acc[slot * D + lane * EPL + e] = acc[r][e];
-      if (lane == 0) {
-        p.ws_m[slot] = m[r];
-        p.ws_l[slot] = sum;
-      }
-    }
-  }
-}
-
 // ---------------------------------------------------------------------------
 // Merge of split rows: M = max_q m_q, out = sum_q acc_q 2^(m_q - M) /
 // sum_q l_q 2^(m_q - M). A row (grid.y = sequence, so that it needs no search
@@ -426,18 +261,6 @@ bool smem_ready(Kernel kern, int bytes, std::atomic<uint64_t> &done) {
     return false;
   if (dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
   return true;
-}
-
-// Launches the CUDA-core kernel with 8 * RPW rows per CTA.
-template <typename Pool, typename IO, int D, int RPW>
-pk_status launch_rows(RowsParams p, cudaStream_t stream) {
-  using S = RowsShape<D, RPW>;
-  auto kern = attn_rows_kernel<Pool, IO, D, RPW>;
-  static std::atomic<uint64_t> ready{0};
-  if (!smem_ready(kern, S::SMEM_BYTES, ready)) return PK_ERR_CUDA;
-  p.row_tiles = (p.max_draft * p.group + S::R - 1) / S::R;
-  kern<<<rows_grid(p), 256, S::SMEM_BYTES, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PK_OK : PK_ERR_CUDA;
 }
 
 // The merge, as the attention's programmatic dependent (an ordinary launch
