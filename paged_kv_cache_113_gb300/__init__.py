@@ -569,17 +569,22 @@ def _heads(t, name, dev, tokens, heads, d):
     return t.data_ptr(), (step if tokens > 1 else heads * d)
 
 
-def _launch(name, dev, stream, *args):
+_FUNCTIONS: dict = {}  # loaded entry points by name
+_DESCS: dict = {}      # pool descriptors by shape and dtype: (descriptor, its reference, shape of kv_exp)
+
+
+def _launch(torch, name, dev, stream, *args):
     """The library's call with the tensors' device current, on the given stream
     or that device's current one."""
-    torch = _torch()
+    fn = _FUNCTIONS.get(name)
+    if fn is None:
+        fn = _FUNCTIONS[name] = getattr(lib(), name)
     if stream is None:
         st = torch._C._cuda_getCurrentRawStream(dev)
     elif stream.device.index != dev:
         raise ValueError("the stream is not on the tensors' device")
     else:
         st = stream.cuda_stream
-    fn = getattr(lib(), name)
     if torch._C._cuda_getDevice() == dev:
         status = fn(*args, st)
     else:
@@ -587,6 +592,19 @@ def _launch(name, dev, stream, *args):
             status = fn(*args, st)
     if status != PK_OK:
         raise PagedKVError(status, name)
+
+
+def _desc_of(cache):
+    """:func:`cache_desc` of a pool, kept for its shape and dtype."""
+    key = (cache.shape, cache.dtype)
+    found = _DESCS.get(key)
+    if found is None:
+        if len(_DESCS) >= 256:
+            _DESCS.clear()
+        desc = cache_desc(cache)
+        exps = (desc.num_blocks, desc.num_kv_heads, desc.block_size, 2)
+        found = _DESCS[key] = (desc, ctypes.byref(desc), exps)
+    return found
 
 
 def pk_qk_norm_rope_and_cache(q_out, k_out, q, k, v, cos_sin, positions, q_weight=None, k_weight=None,
@@ -613,8 +631,8 @@ def pk_qk_norm_rope_and_cache(q_out, k_out, q, k, v, cos_sin, positions, q_weigh
     vp, vs, slots, kc, vc, ko, qw, kw, cs, pos, rot, max_pos = None, 0, None, None, None, None, None, None, None, \
         None, 0, 0
     if cache:
-        desc = cache_desc(k_cache)
-        if desc.num_kv_heads != Hk or desc.head_dim != d or v_cache.shape != k_cache.shape:
+        ref = _desc_of(k_cache)[1]
+        if k_cache.shape[2:] != (Hk, d) or v_cache.shape != k_cache.shape:
             raise ValueError("the caches must be [num_blocks, block_size, num_kv_heads, head_dim]")
         if v is None or slot_mapping.shape != (T,):
             raise ValueError("v is required and slot_mapping must be [num_tokens]")
@@ -624,7 +642,7 @@ def pk_qk_norm_rope_and_cache(q_out, k_out, q, k, v, cos_sin, positions, q_weigh
         slots = _at(slot_mapping, "slot_mapping", dev, torch.int64)
         kc, vc = _at(k_cache, "k_cache", dev, dt), _at(v_cache, "v_cache", dev, dt)
     else:
-        desc = CacheDesc(0, 0, Hk, d, _dtype_code(q))
+        ref = ctypes.byref(CacheDesc(0, 0, Hk, d, _dtype_code(q)))
         if k_out is None:
             raise ValueError("k_out is required without a cache")
     if k.dtype != dt:
@@ -642,20 +660,29 @@ def pk_qk_norm_rope_and_cache(q_out, k_out, q, k, v, cos_sin, positions, q_weigh
             raise ValueError("cos_sin must be [max_position, rotary_dim] and positions [num_tokens]")
         max_pos, rot = cos_sin.shape
         cs, pos = _at(cos_sin, "cos_sin", dev, torch.float32), _at(positions, "positions", dev, torch.int64)
-    _launch("pk_qk_norm_rope_and_cache", dev, stream, _at(q_out, "q_out", dev, dt), ko, qp, kp, vp, qs, ks, vs, qw, kw,
-            float(eps), cs, pos, max_pos, rot, 1 if interleaved else 0, slots, T, Hq, kc, vc, ctypes.byref(desc))
+    _launch(torch, "pk_qk_norm_rope_and_cache", dev, stream, _at(q_out, "q_out", dev, dt), ko, qp, kp, vp, qs, ks, vs, qw, kw,
+            float(eps), cs, pos, max_pos, rot, 1 if interleaved else 0, slots, T, Hq, kc, vc, ref)
 
 
-def _e4m3_cache(k_cache, v_cache, kv_exp):
-    """Descriptor and addresses of an 8-bit cache, and its device."""
-    torch = _torch()
-    if k_cache.dtype != torch.float8_e4m3fn or v_cache.dtype != k_cache.dtype:
+def _e4m3_cache(torch, k_cache, v_cache, kv_exp):
+    """Reference of the descriptor of an 8-bit cache, its device, Hk, d and the
+    addresses of its three tensors."""
+    if k_cache.dtype != torch.float8_e4m3fn or v_cache.dtype != torch.float8_e4m3fn:
         raise TypeError("k_cache and v_cache must be torch.float8_e4m3fn")
-    desc = cache_desc(k_cache)
-    if v_cache.shape != k_cache.shape or kv_exp.shape != (desc.num_blocks, desc.num_kv_heads, desc.block_size, 2):
+    desc, ref, exps = _desc_of(k_cache)
+    if v_cache.shape != k_cache.shape or kv_exp.shape != exps:
         raise ValueError("kv_exp must be [num_blocks, num_kv_heads, block_size, 2] of the caches' shape")
     dev = _cuda_device(k_cache, "k_cache")
-    return desc, dev, _at(k_cache, "k_cache", dev), _at(v_cache, "v_cache", dev), _at(kv_exp, "kv_exp", dev, torch.uint8)
+    return (ref, dev, exps[1], desc.head_dim, _at(k_cache, "k_cache", dev), _at(v_cache, "v_cache", dev),
+            _at(kv_exp, "kv_exp", dev, torch.uint8))
+
+
+def _io_code(torch, t, what) -> int:
+    if t.dtype == torch.bfloat16:
+        return PK_BF16
+    if t.dtype == torch.float32:
+        return PK_F32
+    raise TypeError(f"{what} must be float32 or bfloat16")
 
 
 def pk_reshape_and_cache_e4m3(k, v, slot_mapping, k_cache, v_cache, kv_exp, stream=None):
@@ -664,16 +691,16 @@ def pk_reshape_and_cache_e4m3(k, v, slot_mapping, k_cache, v_cache, kv_exp, stre
     codes in ``k_cache``/``v_cache`` (``torch.float8_e4m3fn``) and exponents in
     ``kv_exp`` (uint8 ``[N, Hk, B, 2]``); value = code * 2^(kv_exp - 127)."""
     torch = _torch()
-    desc, dev, kc, vc, ex = _e4m3_cache(k_cache, v_cache, kv_exp)
+    ref, dev, Hk, d, kc, vc, ex = _e4m3_cache(torch, k_cache, v_cache, kv_exp)
     T = k.shape[0]
-    if v.dtype != k.dtype or (k.dtype != torch.bfloat16 and k.dtype != torch.float32):
+    if v.dtype != k.dtype:
         raise TypeError("k and v must both be float32 or bfloat16")
     if slot_mapping.shape != (T,):
         raise ValueError("slot_mapping must be [num_tokens]")
-    kp, ks = _heads(k, "k", dev, T, desc.num_kv_heads, desc.head_dim)
-    vp, vs = _heads(v, "v", dev, T, desc.num_kv_heads, desc.head_dim)
-    _launch("pk_reshape_and_cache_e4m3", dev, stream, kp, vp, _dtype_code(k), ks, vs,
-            _at(slot_mapping, "slot_mapping", dev, torch.int64), T, kc, vc, ex, ctypes.byref(desc))
+    kp, ks = _heads(k, "k", dev, T, Hk, d)
+    vp, vs = _heads(v, "v", dev, T, Hk, d)
+    _launch(torch, "pk_reshape_and_cache_e4m3", dev, stream, kp, vp, _io_code(torch, k, "k and v"), ks, vs,
+            _at(slot_mapping, "slot_mapping", dev, torch.int64), T, kc, vc, ex, ref)
 
 
 def pk_gather_cache_e4m3(k_out, v_out, slot_mapping, k_cache, v_cache, kv_exp, stream=None):
@@ -681,33 +708,32 @@ def pk_gather_cache_e4m3(k_out, v_out, slot_mapping, k_cache, v_cache, kv_exp, s
     ``k_out`` and ``v_out`` (fp32 or bf16 ``[T, Hk, d]``); rows of negative
     slots stay as they were."""
     torch = _torch()
-    desc, dev, kc, vc, ex = _e4m3_cache(k_cache, v_cache, kv_exp)
+    ref, dev, Hk, d, kc, vc, ex = _e4m3_cache(torch, k_cache, v_cache, kv_exp)
     T = slot_mapping.shape[0]
-    if k_out.shape != (T, desc.num_kv_heads, desc.head_dim) or v_out.shape != k_out.shape:
+    if k_out.shape != (T, Hk, d) or v_out.shape != k_out.shape:
         raise ValueError("k_out and v_out must be [num_tokens, num_kv_heads, head_dim]")
-    if k_out.dtype != torch.bfloat16 and k_out.dtype != torch.float32:
-        raise TypeError("k_out and v_out must both be float32 or bfloat16")
-    _launch("pk_gather_cache_e4m3", dev, stream, _at(k_out, "k_out", dev), _at(v_out, "v_out", dev, k_out.dtype),
-            _dtype_code(k_out), _at(slot_mapping, "slot_mapping", dev, torch.int64), T, kc, vc, ex,
-            ctypes.byref(desc))
+    _launch(torch, "pk_gather_cache_e4m3", dev, stream, _at(k_out, "k_out", dev), _at(v_out, "v_out", dev, k_out.dtype),
+            _io_code(torch, k_out, "k_out and v_out"), _at(slot_mapping, "slot_mapping", dev, torch.int64), T, kc, vc,
+            ex, ref)
 
 
 def pk_copy_blocks_e4m3(k_cache, v_cache, kv_exp, src_dst_pairs, stream=None):
     """:func:`pk_copy_blocks` of an 8-bit cache (codes and exponents)."""
-    desc, dev, kc, vc, ex = _e4m3_cache(k_cache, v_cache, kv_exp)
+    torch = _torch()
+    ref, dev, _, _, kc, vc, ex = _e4m3_cache(torch, k_cache, v_cache, kv_exp)
     n = src_dst_pairs.shape[0] if src_dst_pairs.numel() else 0
     if n and src_dst_pairs.shape != (n, 2):
         raise ValueError("src_dst_pairs must be [num_pairs, 2]")
     if n:
-        _launch("pk_copy_blocks_e4m3", dev, stream, kc, vc, ex,
-                _at(src_dst_pairs, "src_dst_pairs", dev, _torch().int64), n, ctypes.byref(desc))
+        _launch(torch, "pk_copy_blocks_e4m3", dev, stream, kc, vc, ex,
+                _at(src_dst_pairs, "src_dst_pairs", dev, torch.int64), n, ref)
 
 
-def _attention_args(dev, out, q, block_tables, context_lens, num_seqs, d, work_items, workspace):
+def _attention_args(i32, dev, out, q, block_tables, context_lens, num_seqs, d, work_items, workspace):
     """Checked addresses of what the two attentions below share: (out, q),
     (block_tables, context_lens) and (work_items, count, workspace, bytes)."""
-    i32 = _torch().int32
-    if q.dim() != 3 or q.shape[2] != d or out.shape != q.shape:
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != d or out.shape != shape:
         raise ValueError("out and q must be [rows, num_q_heads, head_dim]")
     if block_tables.dim() != 2 or block_tables.shape[0] != num_seqs or context_lens.shape != (num_seqs,):
         raise ValueError("block_tables must be [num_seqs, max_blocks] and context_lens [num_seqs]")
@@ -717,7 +743,7 @@ def _attention_args(dev, out, q, block_tables, context_lens, num_seqs, d, work_i
             raise ValueError("work_items must be [n, 2]")
         items, n_items = _at(work_items, "work_items", dev, i32), work_items.shape[0]
     if workspace is not None:
-        ws, ws_bytes = _at(workspace, "workspace", dev), workspace.numel() * workspace.element_size()
+        ws, ws_bytes = _at(workspace, "workspace", dev), workspace.nbytes
     return ((_at(out, "out", dev, q.dtype), _at(q, "q", dev)),
             (_at(block_tables, "block_tables", dev, i32), _at(context_lens, "context_lens", dev, i32)),
             (items, n_items, ws, ws_bytes))
@@ -731,13 +757,12 @@ def pk_paged_attention_decode_e4m3(out, q, k_cache, v_cache, kv_exp, block_table
     ``work_items`` as there (:func:`pk_attention_plan` and
     :func:`pk_paged_attention_workspace_size` take the 8-bit cache's descriptor)."""
     torch = _torch()
-    desc, dev, kc, vc, ex = _e4m3_cache(k_cache, v_cache, kv_exp)
-    if q.dtype != torch.bfloat16 and q.dtype != torch.float32:
-        raise TypeError("q and out must be float32 or bfloat16")
+    ref, dev, _, d, kc, vc, ex = _e4m3_cache(torch, k_cache, v_cache, kv_exp)
     S = q.shape[0]
-    rows, seqs, split = _attention_args(dev, out, q, block_tables, context_lens, S, desc.head_dim, work_items, workspace)
-    _launch("pk_paged_attention_decode_e4m3", dev, stream, *rows, _dtype_code(q), kc, vc, ex, *seqs, float(scale),
-            S, q.shape[1], block_tables.shape[1], int(max_context_len), int(partition_size), *split, ctypes.byref(desc))
+    rows, seqs, split = _attention_args(torch.int32, dev, out, q, block_tables, context_lens, S, d, work_items, workspace)
+    _launch(torch, "pk_paged_attention_decode_e4m3", dev, stream, *rows, _io_code(torch, q, "q and out"), kc, vc, ex,
+            *seqs, float(scale), S, q.shape[1], block_tables.shape[1], int(max_context_len), int(partition_size), *split,
+            ref)
 
 
 def pk_paged_attention_tree(out, q, k_cache, v_cache, block_tables, context_lens, q_offsets, scale: float,
@@ -752,23 +777,24 @@ def pk_paged_attention_tree(out, q, k_cache, v_cache, block_tables, context_lens
     :func:`pk_tree_plan`, ``workspace`` of :func:`pk_tree_workspace_size` bytes
     when the contexts are split."""
     torch = _torch()
-    dev = _cuda_device(q, "q")
-    desc = cache_desc(k_cache)
+    dev, dt = _cuda_device(q, "q"), q.dtype
+    desc, ref, _ = _desc_of(k_cache)
     if v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache must have one shape")
-    S = block_tables.shape[0]
-    rows, seqs, split = _attention_args(dev, out, q, block_tables, context_lens, S, desc.head_dim, work_items, workspace)
+    S, R = block_tables.shape[0], q.shape[0]
+    rows, seqs, split = _attention_args(torch.int32, dev, out, q, block_tables, context_lens, S, desc.head_dim,
+                                        work_items, workspace)
     if q_offsets.shape != (S + 1,):
         raise ValueError("q_offsets must be [num_seqs + 1]")
     mask = None
     if tree_mask is not None:
-        if (tree_mask.dtype != torch.int64 and tree_mask.dtype != torch.uint64) or tree_mask.shape != (q.shape[0],):
+        if (tree_mask.dtype != torch.int64 and tree_mask.dtype != torch.uint64) or tree_mask.shape != (R,):
             raise ValueError("tree_mask must be int64 or uint64 [rows]")
         mask = _at(tree_mask, "tree_mask", dev)
-    _launch("pk_paged_attention_tree", dev, stream, *rows, _at(k_cache, "k_cache", dev, q.dtype),
-            _at(v_cache, "v_cache", dev, q.dtype), *seqs, _at(q_offsets, "q_offsets", dev, torch.int32), mask,
-            float(scale), S, q.shape[0], int(max_draft_len), q.shape[1], block_tables.shape[1], int(max_context_len),
-            int(partition_size), *split, ctypes.byref(desc))
+    _launch(torch, "pk_paged_attention_tree", dev, stream, *rows, _at(k_cache, "k_cache", dev, dt),
+            _at(v_cache, "v_cache", dev, dt), *seqs, _at(q_offsets, "q_offsets", dev, torch.int32), mask, float(scale),
+            S, R, int(max_draft_len), q.shape[1], block_tables.shape[1], int(max_context_len), int(partition_size),
+            *split, ref)
 
 
 def pk_tree_masks(parents) -> Tuple[np.ndarray, np.ndarray]:
