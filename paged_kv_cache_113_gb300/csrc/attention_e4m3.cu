@@ -165,9 +165,10 @@ __global__ void __launch_bounds__(kThreads, 3)
       prefetch_tensormap(&vmap);
     }
     const int X = p.num_kv_heads, Y = p.items ? p.num_items : p.num_seqs;
-    bool ok = true;
+    bool ok = true, open = false;  // open: an answer is under way
     int asked = 0;
     auto ask = [&] {
+      open = true;
       if (lane == 0) {
         mbar_arrive_expect_tx(u_answer, 16);
         try_cancel(smem_addr(&answer), u_answer);
@@ -176,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     auto answered = [&] {  // the unit's number, or -1: none is left
       if (!warp_wait(u_answer, asked & 1, ok)) return -1;
       ++asked;
+      open = false;
       const int u = cancelled_cta(smem_addr(&answer));
       fence_proxy_async();  // the answer has been read before the next one is asked for
       __syncwarp();
@@ -278,7 +280,8 @@ __global__ void __launch_bounds__(kThreads, 3)
       have = item && unit_of(u, s, part, c);
     }
     if (!ok && lane == 0) timeout();
-    // Let every issued copy land before the warp leaves.
+    // Let every issued copy, and an answer, land before the warp leaves.
+    if (open) mbar_wait(u_answer, asked & 1);
     for (int k = max(0, t - STAGES); k < t; ++k) mbar_wait(full_bar(k), t_phase(k));
     for (int k = max(0, i - 2); k < i; ++k) mbar_wait(q_full(k), uint32_t(k >> 1) & 1u);
     return;
@@ -299,224 +302,226 @@ __global__ void __launch_bounds__(kThreads, 3)
   float *sm_m = sm_o + kWarps * 8 * S::OUT_STRIDE, *sm_l = sm_m + kWarps * 8;
   bool ok = true;
   for (int i = 0, t = 0; warp_wait(u_full(i), u_phase(i), ok); ++i) {
-  const Unit c = units[i % kUnits];
-  __syncwarp();
-  if (lane == 0) mbar_arrive(u_empty(i));
-  if (c.s < 0 || !warp_wait(q_full(i), uint32_t(i >> 1) & 1u, ok)) break;
-  uint32_t qb[QW][KC][4];
-  float sl0, sl1;  // scale log2(e) and the query scaling undone, heads 2 qd and 2 qd + 1
-  {
-    float qv[KC][8];
-    uint32_t top = 0;
-    const IO *qrow = reinterpret_cast<const IO *>(smem_raw + (q_sm - raw) + (i & 1) * S::Q_BYTES +
-                                                  min(rw, G - 1) * S::Q_ROW);
+    const Unit c = units[i % kUnits];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(u_empty(i));
+    if (c.s < 0 || !warp_wait(q_full(i), uint32_t(i >> 1) & 1u, ok)) break;
+    uint32_t qb[QW][KC][4];
+    float sl0, sl1;  // scale log2(e) and the query scaling undone, heads 2 qd and 2 qd + 1
+    {
+      float qv[KC][8];
+      uint32_t top = 0;
+      const IO *qrow = reinterpret_cast<const IO *>(smem_raw + (q_sm - raw) + (i & 1) * S::Q_BYTES +
+                                                    min(rw, G - 1) * S::Q_ROW);
+#pragma unroll
+      for (int k = 0; k < KC; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 x = load4(qrow + 32 * k + 16 * h + 4 * qd);
+          qv[k][4 * h] = x.x, qv[k][4 * h + 1] = x.y, qv[k][4 * h + 2] = x.z, qv[k][4 * h + 3] = x.w;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t b = __float_as_uint(qv[k][4 * h + e]) & 0x7fffffffu;
+            top = max(top, b < 0x7f800000u ? b : 0u);
+          }
+        }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_empty(i));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int up = min(126, 14 - (int(top >> 23) - 127));  // >= -113
+      const float f = pow2(up);
+      const float sl = p.scale_log2 * pow2(-up);
+      sl0 = __shfl_sync(0xffffffffu, sl, 8 * qd);
+      sl1 = __shfl_sync(0xffffffffu, sl, 8 * qd + 4);
+#pragma unroll
+      for (int k = 0; k < KC; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float a = rw < G ? qv[k][2 * e] * f : 0.0f, b = rw < G ? qv[k][2 * e + 1] * f : 0.0f;
+          qb[0][k][e] = pack_f16x2(a, b);
+          if (QW == 2) {
+            const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&qb[0][k][e]));
+            qb[QW - 1][k][e] = pack_f16x2(a - hi.x, b - hi.y);
+          }
+        }
+    }
+    float o[KC][2][4];  // [32-column step][16-column half]
+#pragma unroll
+    for (int k = 0; k < KC; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) o[k][h][0] = o[k][h][1] = o[k][h][2] = o[k][h][3] = 0.0f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+    for (int st = 0; st < c.nst; ++st, ++t) {
+      const int slot = t % STAGES;
+      if (!warp_wait(full_bar(t), t_phase(t), ok)) break;
+      const uint32_t kbase = stages + slot * S::STAGE_BYTES, vbase = kbase + S::KV_BYTES;
+#pragma unroll 1
+      for (int tile = 0; tile < S::TILES; ++tile) {
+        const int t0 = (tile * kWarps + warp) * 16;
+        const int nvalid = c.end - (c.start + st * S::TPS + t0);
+        if (nvalid <= 0) break;
+        if (nvalid < 16) {
+          // Rows past the end may hold anything: zero values, so that a zero
+          // weight never meets a NaN.
+          for (int i = lane; i < (16 - nvalid) * (D / 16); i += 32) {
+            const uint32_t a = vbase + (t0 + nvalid + i / (D / 16)) * D + (i % (D / 16)) * 16;
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+          }
+          fence_proxy_async();  // a later unit's copies go to the same rows
+          __syncwarp();
+        }
+        uint32_t e0, e1;  // exponents of the lane's tokens: K in the low byte, V above
+        {
+          const uint32_t a = exps + slot * S::EXP_BYTES + (t0 + tok0) * 2;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=r"(e0) : "r"(a));
+          asm volatile("ld.shared.u16 %0, [%1];" : "=r"(e1) : "r"(a + 4));
+        }
+        // S^T = K_tile Q^T; low 16 bits and high 16 bits of a lane's four bytes
+        // are the two k halves of one product.
+        float sa[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+        for (int k = 0; k < KC; ++k) {
+          uint32_t r[4];
+          ldmatrix_x4(kbase + swizzled<D>(t0 + token_of((mi & 1) * 8 + r8), 2 * k + (mi >> 1)), r[0],
+                      r[1], r[2], r[3]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16x4(r[2 * h], a0, a2);
+            e4m3x4_to_f16x4(r[2 * h + 1], a1, a3);
+#pragma unroll
+            for (int w = 0; w < QW; ++w)
+              mma_f16_16816(sa[h], a0, a1, a2, a3, qb[w][k][2 * h], qb[w][k][2 * h + 1]);
+          }
+        }
+        const float k0 = __uint_as_float((e0 & 0xffu) << 23), k1 = __uint_as_float((e1 & 0xffu) << 23);
+        // A row of zeros is written with exponent 0, which says nothing of its
+        // neighbours: it counts as the smallest, or it would push the weights of
+        // far smaller values out of fp16's range.
+        int ev0 = int(e0 >> 8) - 127, ev1 = int(e1 >> 8) - 127;
+        if (__any_sync(0xffffffffu, ev0 == 0 || ev1 == 0)) {
+          if (zero_row<D>(vbase, t0 + tok0)) ev0 = -100;
+          if (zero_row<D>(vbase, t0 + tok0 + 2)) ev1 = -100;
+        }
+        const float v0 = float(ev0), v1 = float(ev1);
+        float x0 = (sa[0][0] + sa[1][0]) * sl0 * k0, x1 = (sa[0][1] + sa[1][1]) * sl1 * k0;
+        float x2 = (sa[0][2] + sa[1][2]) * sl0 * k1, x3 = (sa[0][3] + sa[1][3]) * sl1 * k1;
+        if (tok0 >= nvalid) x0 = x1 = -INFINITY;
+        if (tok0 + 2 >= nvalid) x2 = x3 = -INFINITY;
+        float z0 = fmaxf(x0 + v0, x2 + v1), z1 = fmaxf(x1 + v0, x3 + v1);
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          z0 = fmaxf(z0, __shfl_xor_sync(0xffffffffu, z0, off));
+          z1 = fmaxf(z1, __shfl_xor_sync(0xffffffffu, z1, off));
+        }
+        const float n0 = fmaxf(m0, z0 - kHeadroom), n1 = fmaxf(m1, z1 - kHeadroom);
+        const float c0 = exp2_ftz(m0 - n0), c1 = exp2_ftz(m1 - n1);
+        m0 = n0;
+        m1 = n1;
+        const float y0 = x0 - n0, y1 = x1 - n1, y2 = x2 - n0, y3 = x3 - n1;
+        l0 = fmaf(l0, c0, exp2_ftz(y0) + exp2_ftz(y2));
+        l1 = fmaf(l1, c1, exp2_ftz(y1) + exp2_ftz(y3));
+        const float p0 = exp2_ftz(y0 + v0), p1 = exp2_ftz(y1 + v0);
+        const float p2 = exp2_ftz(y2 + v1), p3 = exp2_ftz(y3 + v1);
+        uint32_t b[QW][2];  // P^T as the B operand: the C fragments transposed
+        {
+          const uint32_t w0 = pack_f16x2(p0, p1), w1 = pack_f16x2(p2, p3);
+          b[0][0] = movmatrix_trans(w0);
+          b[0][1] = movmatrix_trans(w1);
+          if (QW == 2) {
+            const float2 h0 = __half22float2(*reinterpret_cast<const __half2 *>(&w0));
+            const float2 h1 = __half22float2(*reinterpret_cast<const __half2 *>(&w1));
+            b[QW - 1][0] = movmatrix_trans(pack_f16x2(p0 - h0.x, p1 - h0.y));
+            b[QW - 1][1] = movmatrix_trans(pack_f16x2(p2 - h1.x, p3 - h1.y));
+          }
+        }
+        if (__any_sync(0xffffffffu, c0 != 1.0f || c1 != 1.0f)) {
+#pragma unroll
+          for (int k = 0; k < KC; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              o[k][h][0] *= c0;
+              o[k][h][1] *= c1;
+              o[k][h][2] *= c0;
+              o[k][h][3] *= c1;
+            }
+        }
+        // O^T += V^T P^T: a transposed load gives a lane four tokens of a column, the
+        // ones that its rows of the scores belong to.
+#pragma unroll
+        for (int k = 0; k < KC; ++k) {
+          uint32_t r[4];  // columns 32 k + rw, + 8 of both 16-column halves
+          ldmatrix_b8_x2_trans(vbase + swizzled<D>(t0 + (lane & 15), 2 * k + (lane >> 4)), r[0], r[1], r[2], r[3]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16x4(r[2 * h], a0, a2);
+            e4m3x4_to_f16x4(r[2 * h + 1], a1, a3);
+#pragma unroll
+            for (int w = 0; w < QW; ++w) mma_f16_16816(o[k][h], a0, a1, a2, a3, b[w][0], b[w][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty_bar(t));
+    }
+
+    // The denominators of a warp's 16 tokens lie in the 8 lanes of a quad index.
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+    }
+    if (!ok) break;
+    // Merge the consumer warps' states in shared memory, once all have read the
+    // unit's before.
+    if (i > 0 && !warp_wait(m_empty, uint32_t(i - 1) & 1u, ok)) break;
 #pragma unroll
     for (int k = 0; k < KC; ++k)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float4 x = load4(qrow + 32 * k + 16 * h + 4 * qd);
-        qv[k][4 * h] = x.x, qv[k][4 * h + 1] = x.y, qv[k][4 * h + 2] = x.z, qv[k][4 * h + 3] = x.w;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t b = __float_as_uint(qv[k][4 * h + e]) & 0x7fffffffu;
-          top = max(top, b < 0x7f800000u ? b : 0u);
-        }
+        float *base = sm_o + (warp * 8 + 2 * qd) * S::OUT_STRIDE + 32 * k + 16 * h + rw;
+        base[0] = o[k][h][0];
+        base[S::OUT_STRIDE] = o[k][h][1];
+        base[8] = o[k][h][2];
+        base[S::OUT_STRIDE + 8] = o[k][h][3];
       }
+    if (rw == 0) {
+      sm_m[warp * 8 + 2 * qd] = m0;
+      sm_m[warp * 8 + 2 * qd + 1] = m1;
+      sm_l[warp * 8 + 2 * qd] = l0;
+      sm_l[warp * 8 + 2 * qd + 1] = l1;
+    }
     __syncwarp();
-    if (lane == 0) mbar_arrive(q_empty(i));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const int up = min(126, 14 - (int(top >> 23) - 127));  // >= -113
-    const float f = pow2(up);
-    const float sl = p.scale_log2 * pow2(-up);
-    sl0 = __shfl_sync(0xffffffffu, sl, 8 * qd);
-    sl1 = __shfl_sync(0xffffffffu, sl, 8 * qd + 4);
+    if (lane == 0) mbar_arrive(m_full);
+    if (!warp_wait(m_full, uint32_t(i) & 1u, ok)) break;
+    const size_t row0 = size_t(c.s) * p.num_q_heads + c.kvh * G;  // the group's first row of out
+    for (int k = threadIdx.x; k < G * D; k += kWarps * 32) {
+      const int g = k / D, col = k % D;
+      float M = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < KC; ++k)
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w * 8 + g]);
+      float L = 0.0f, O = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float a = rw < G ? qv[k][2 * e] * f : 0.0f, b = rw < G ? qv[k][2 * e + 1] * f : 0.0f;
-        qb[0][k][e] = pack_f16x2(a, b);
-        if (QW == 2) {
-          const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&qb[0][k][e]));
-          qb[QW - 1][k][e] = pack_f16x2(a - hi.x, b - hi.y);
-        }
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = exp2_ftz(sm_m[w * 8 + g] - M);  // 0 for a warp that saw no token
+        L = fmaf(sm_l[w * 8 + g], f, L);
+        O = fmaf(sm_o[(w * 8 + g) * S::OUT_STRIDE + col], f, O);
       }
-  }
-  float o[KC][2][4];  // [32-column step][16-column half]
-#pragma unroll
-  for (int k = 0; k < KC; ++k)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) o[k][h][0] = o[k][h][1] = o[k][h][2] = o[k][h][3] = 0.0f;
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-  for (int st = 0; st < c.nst; ++st, ++t) {
-    const int slot = t % STAGES;
-    if (!warp_wait(full_bar(t), t_phase(t), ok)) break;
-    const uint32_t kbase = stages + slot * S::STAGE_BYTES, vbase = kbase + S::KV_BYTES;
-#pragma unroll 1
-    for (int tile = 0; tile < S::TILES; ++tile) {
-      const int t0 = (tile * kWarps + warp) * 16;
-      const int nvalid = c.end - (c.start + st * S::TPS + t0);
-      if (nvalid <= 0) break;
-      if (nvalid < 16) {
-        // Rows past the end may hold anything: zero values, so that a zero
-        // weight never meets a NaN.
-        for (int i = lane; i < (16 - nvalid) * (D / 16); i += 32) {
-          const uint32_t a = vbase + (t0 + nvalid + i / (D / 16)) * D + (i % (D / 16)) * 16;
-          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
-        }
-        __syncwarp();
-      }
-      uint32_t e0, e1;  // exponents of the lane's tokens: K in the low byte, V above
-      {
-        const uint32_t a = exps + slot * S::EXP_BYTES + (t0 + tok0) * 2;
-        asm volatile("ld.shared.u16 %0, [%1];" : "=r"(e0) : "r"(a));
-        asm volatile("ld.shared.u16 %0, [%1];" : "=r"(e1) : "r"(a + 4));
-      }
-      // S^T = K_tile Q^T; low 16 bits and high 16 bits of a lane's four bytes
-      // are the two k halves of one product.
-      float sa[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-#pragma unroll
-      for (int k = 0; k < KC; ++k) {
-        uint32_t r[4];
-        ldmatrix_x4(kbase + swizzled<D>(t0 + token_of((mi & 1) * 8 + r8), 2 * k + (mi >> 1)), r[0], r[1], r[2], r[3]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t a0, a1, a2, a3;
-          e4m3x4_to_f16x4(r[2 * h], a0, a2);
-          e4m3x4_to_f16x4(r[2 * h + 1], a1, a3);
-#pragma unroll
-          for (int w = 0; w < QW; ++w)
-            mma_f16_16816(sa[h], a0, a1, a2, a3, qb[w][k][2 * h], qb[w][k][2 * h + 1]);
-        }
-      }
-      const float k0 = __uint_as_float((e0 & 0xffu) << 23), k1 = __uint_as_float((e1 & 0xffu) << 23);
-      // A row of zeros is written with exponent 0, which says nothing of its
-      // neighbours: it counts as the smallest, or it would push the weights of
-      // far smaller values out of fp16's range.
-      int ev0 = int(e0 >> 8) - 127, ev1 = int(e1 >> 8) - 127;
-      if (__any_sync(0xffffffffu, ev0 == 0 || ev1 == 0)) {
-        if (zero_row<D>(vbase, t0 + tok0)) ev0 = -100;
-        if (zero_row<D>(vbase, t0 + tok0 + 2)) ev1 = -100;
-      }
-      const float v0 = float(ev0), v1 = float(ev1);
-      float x0 = (sa[0][0] + sa[1][0]) * sl0 * k0, x1 = (sa[0][1] + sa[1][1]) * sl1 * k0;
-      float x2 = (sa[0][2] + sa[1][2]) * sl0 * k1, x3 = (sa[0][3] + sa[1][3]) * sl1 * k1;
-      if (tok0 >= nvalid) x0 = x1 = -INFINITY;
-      if (tok0 + 2 >= nvalid) x2 = x3 = -INFINITY;
-      float z0 = fmaxf(x0 + v0, x2 + v1), z1 = fmaxf(x1 + v0, x3 + v1);
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) {
-        z0 = fmaxf(z0, __shfl_xor_sync(0xffffffffu, z0, off));
-        z1 = fmaxf(z1, __shfl_xor_sync(0xffffffffu, z1, off));
-      }
-      const float n0 = fmaxf(m0, z0 - kHeadroom), n1 = fmaxf(m1, z1 - kHeadroom);
-      const float c0 = exp2_ftz(m0 - n0), c1 = exp2_ftz(m1 - n1);
-      m0 = n0;
-      m1 = n1;
-      const float y0 = x0 - n0, y1 = x1 - n1, y2 = x2 - n0, y3 = x3 - n1;
-      l0 = fmaf(l0, c0, exp2_ftz(y0) + exp2_ftz(y2));
-      l1 = fmaf(l1, c1, exp2_ftz(y1) + exp2_ftz(y3));
-      const float p0 = exp2_ftz(y0 + v0), p1 = exp2_ftz(y1 + v0);
-      const float p2 = exp2_ftz(y2 + v1), p3 = exp2_ftz(y3 + v1);
-      uint32_t b[QW][2];  // P^T as the B operand: the C fragments transposed
-      {
-        const uint32_t w0 = pack_f16x2(p0, p1), w1 = pack_f16x2(p2, p3);
-        b[0][0] = movmatrix_trans(w0);
-        b[0][1] = movmatrix_trans(w1);
-        if (QW == 2) {
-          const float2 h0 = __half22float2(*reinterpret_cast<const __half2 *>(&w0));
-          const float2 h1 = __half22float2(*reinterpret_cast<const __half2 *>(&w1));
-          b[QW - 1][0] = movmatrix_trans(pack_f16x2(p0 - h0.x, p1 - h0.y));
-          b[QW - 1][1] = movmatrix_trans(pack_f16x2(p2 - h1.x, p3 - h1.y));
-        }
-      }
-      if (__any_sync(0xffffffffu, c0 != 1.0f || c1 != 1.0f)) {
-#pragma unroll
-        for (int k = 0; k < KC; ++k)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            o[k][h][0] *= c0;
-            o[k][h][1] *= c1;
-            o[k][h][2] *= c0;
-            o[k][h][3] *= c1;
-          }
-      }
-      // O^T += V^T P^T: a transposed load gives a lane four tokens of a column, the
-      // ones that its rows of the scores belong to.
-#pragma unroll
-      for (int k = 0; k < KC; ++k) {
-        uint32_t r[4];  // columns 32 k + rw, + 8 of both 16-column halves
-        ldmatrix_b8_x2_trans(vbase + swizzled<D>(t0 + (lane & 15), 2 * k + (lane >> 4)), r[0], r[1], r[2], r[3]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t a0, a1, a2, a3;
-          e4m3x4_to_f16x4(r[2 * h], a0, a2);
-          e4m3x4_to_f16x4(r[2 * h + 1], a1, a3);
-#pragma unroll
-          for (int w = 0; w < QW; ++w) mma_f16_16816(o[k][h], a0, a1, a2, a3, b[w][0], b[w][1]);
+      if (c.np == 1) {
+        store_elem(static_cast<IO *>(p.out) + (row0 + g) * D + col, O / L);
+      } else {
+        const size_t slot = (row0 + g) * p.num_partitions + c.part;
+        p.ws_acc[slot * D + col] = O;
+        if (col == 0) {
+          p.ws_m[slot] = M;
+          p.ws_l[slot] = L;
         }
       }
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(empty_bar(t));
-  }
-
-  // The denominators of a warp's 16 tokens lie in the 8 lanes of a quad index.
-#pragma unroll
-  for (int off = 4; off < 32; off <<= 1) {
-    l0 += __shfl_xor_sync(0xffffffffu, l0, off);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, off);
-  }
-  if (!ok) break;
-  // Merge the consumer warps' states in shared memory, once all have read the
-  // unit's before.
-  if (i > 0 && !warp_wait(m_empty, uint32_t(i - 1) & 1u, ok)) break;
-#pragma unroll
-  for (int k = 0; k < KC; ++k)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float *base = sm_o + (warp * 8 + 2 * qd) * S::OUT_STRIDE + 32 * k + 16 * h + rw;
-      base[0] = o[k][h][0];
-      base[S::OUT_STRIDE] = o[k][h][1];
-      base[8] = o[k][h][2];
-      base[S::OUT_STRIDE + 8] = o[k][h][3];
-    }
-  if (rw == 0) {
-    sm_m[warp * 8 + 2 * qd] = m0;
-    sm_m[warp * 8 + 2 * qd + 1] = m1;
-    sm_l[warp * 8 + 2 * qd] = l0;
-    sm_l[warp * 8 + 2 * qd + 1] = l1;
-  }
-  __syncwarp();
-  if (lane == 0) mbar_arrive(m_full);
-  if (!warp_wait(m_full, uint32_t(i) & 1u, ok)) break;
-  const size_t row0 = size_t(c.s) * p.num_q_heads + c.kvh * G;  // the group's first row of out
-  for (int k = threadIdx.x; k < G * D; k += kWarps * 32) {
-    const int g = k / D, col = k % D;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w * 8 + g]);
-    float L = 0.0f, O = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = exp2_ftz(sm_m[w * 8 + g] - M);  // 0 for a warp that saw no token
-      L = fmaf(sm_l[w * 8 + g], f, L);
-      O = fmaf(sm_o[(w * 8 + g) * S::OUT_STRIDE + col], f, O);
-    }
-    if (c.np == 1) {
-      store_elem(static_cast<IO *>(p.out) + (row0 + g) * D + col, O / L);
-    } else {
-      const size_t slot = (row0 + g) * p.num_partitions + c.part;
-      p.ws_acc[slot * D + col] = O;
-      if (col == 0) {
-        p.ws_m[slot] = M;
-        p.ws_l[slot] = L;
-      }
-    }
-  }
-  __syncwarp();
-  if (lane == 0) mbar_arrive(m_empty);
+    if (lane == 0) mbar_arrive(m_empty);
   }
   if (!ok && lane == 0) timeout();
 }

@@ -847,7 +847,8 @@ __global__ void __launch_bounds__(128, 2) attn_split_kernel(RowsParams p) {
         uint32_t b[2][NP];
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
-          const uint2 w = *reinterpret_cast<const uint2 *>(q_sm + (k * R + 8 * n + rw) * S::Q_PITCH + 32 * c + 8 * qd);
+          const uint2 w = *reinterpret_cast<const uint2 *>(q_sm + (k * R + 8 * n + rw) * S::Q_PITCH +
+                                                           32 * c + 8 * qd);
           b[0][k] = w.x, b[1][k] = w.y;
         }
         mma_parts(x[n], a, b);

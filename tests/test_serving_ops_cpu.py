@@ -150,7 +150,8 @@ def test_norm_rope_refusals(L, ptr):
                 dict(cs=ptr(7) + 4), dict(kc=ptr(10) + 2), dict(qo=ptr(2), qs=1024), dict(ko=ptr(3), ks=512),
                 dict(desc=(0, 16, 2, 128, 1)), dict(desc=(64, 16, 0, 128, 1))):
         assert call(**bad) == BAD, bad
-    for uns in (dict(desc=(64, 16, 2, 128, pk.PK_E4M3)), dict(desc=(64, 16, 2, 120, 1)), dict(desc=(64, 16, 2, 272, 1))):
+    for uns in (dict(desc=(64, 16, 2, 128, pk.PK_E4M3)), dict(desc=(64, 16, 2, 120, 1)),
+                dict(desc=(64, 16, 2, 272, 1))):
         assert call(**uns) == UNS, uns
 
 

@@ -54,6 +54,12 @@ def codes_of(t):
     return t.view(torch.uint8).cpu().numpy()
 
 
+def values_of(kc, vc, ex):
+    """The fp64 values of an 8-bit pool's keys and values."""
+    e = np.moveaxis(ex.cpu().numpy(), 1, 2)
+    return [plain.decode_values(codes_of(c), e[..., i]) for i, c in enumerate((kc, vc))]
+
+
 def rand(rng, shape, dtype=torch.float32):
     return torch.from_numpy(rng.standard_normal(shape).astype(np.float32)).to(DEV).to(dtype)
 
@@ -285,9 +291,10 @@ def fill_e4m3(rng, tables, lens, N, B, Hk, d, spread=0, exp=127):
         k, v = rand(rng, (n, Hk, d)), rand(rng, (n, Hk, d))
         if spread:
             k = k * torch.exp2(torch.from_numpy(rng.integers(-2, 3, (n, Hk, 1)).astype(np.float32)).to(DEV))
-            v = v * torch.exp2(torch.from_numpy(rng.integers(-spread, spread + 1, (n, Hk, 1)).astype(np.float32)).to(DEV))
+            step = rng.integers(-spread, spread + 1, (n, Hk, 1)).astype(np.float32)
+            v = v * torch.exp2(torch.from_numpy(step).to(DEV))
         pk.pk_reshape_and_cache_e4m3(k, v, i64(slots), kc, vc, ex)
-    vals = [plain.decode_values(codes_of(c), np.moveaxis(ex.cpu().numpy()[..., i], 1, 2)) for i, c in enumerate((kc, vc))]
+    vals = values_of(kc, vc, ex)
     return kc, vc, ex, vals
 
 
@@ -337,7 +344,7 @@ def test_decode_e4m3_exponents(dtype, shift):
     first = int(tables[0][0])
     vc.view(torch.uint8)[first, 3], ex[first, :, 3, 1] = 0, 127
     kc.view(torch.uint8)[first, 5], ex[first, :, 5, 0] = 0, 127
-    vals = [plain.decode_values(codes_of(c), np.moveaxis(ex.cpu().numpy()[..., i], 1, 2)) for i, c in enumerate((kc, vc))]
+    vals = values_of(kc, vc, ex)
     q = rand(rng, (3, hq, d), dt)
     want, terms = plain.tree_attention(f64(q), *vals, tables, lens, d ** -0.5)
     for part in (0, 64):
@@ -406,7 +413,8 @@ def tree_case(rng, counts, lens, B, hq, hk, d, dt, kind, pad=3):
     v = k.clone()
     for s, n in enumerate(lens):
         slots = tables[s][np.arange(n) // B].astype(np.int64) * B + np.arange(n) % B
-        k.view(-1, hk, d)[slots], v.view(-1, hk, d)[slots] = rand(rng, (int(n), hk, d), dt), rand(rng, (int(n), hk, d), dt)
+        for t in (k, v):
+            t.view(-1, hk, d)[slots] = rand(rng, (int(n), hk, d), dt)
     ofs = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
     masks = None
     if kind != "chain":
@@ -577,7 +585,7 @@ def test_verification_step(dtype):
     kn, vn = rand(rng, (4, hk, d), dt), rand(rng, (4, hk, d), dt)
     pk.pk_reshape_and_cache_e4m3(kn, vn, i64(slots), k8, v8, ex)
     tables, lens = bm.export_tables(range(4), 8)
-    vals = [plain.decode_values(codes_of(c), np.moveaxis(ex.cpu().numpy()[..., i], 1, 2)) for i, c in enumerate((k8, v8))]
+    vals = values_of(k8, v8, ex)
     for s, n in enumerate(lens):   # every token of every context has been written
         p = np.arange(n)
         assert np.isfinite(vals[0][tables[s][p // B], p % B]).all()
@@ -641,7 +649,7 @@ def test_streams_and_graph_replay():
     got = snap()
     step()
     assert all(torch.equal(a, b) for a, b in zip(got, snap()))
-    vals = [plain.decode_values(codes_of(c), np.moveaxis(ex.cpu().numpy()[..., i], 1, 2)) for i, c in enumerate((k8, v8))]
+    vals = values_of(k8, v8, ex)
     want, terms = plain.tree_attention(f64(qd), *vals, tables, lens + 20, 0.09)
     check_attention(f64(o2), want, terms, d, dt, RHO_E4M3[dt])
 
