@@ -6,17 +6,35 @@
 // Bound by memory: a token and KV head cost 2 (d + 1) bytes, half of bf16, for
 // 4 G d operations.
 //
-// One CTA per (KV head, sequence, partition) or work item, 4 consumer warps and
-// a producer warp, as the bf16 kernel: the producer streams each block's codes
-// with TMA tensor loads and its exponents with one bulk copy (a block and head's
-// K and V exponents are contiguous) into a ring of 64-token stages. Consumers
-// widen codes to fp16, where e4m3 is exact, in registers and multiply on the
-// tensor cores (m16n8k16, tokens as M, the group's heads as N); the exponents
-// never touch the codes. K's scale the finished scores. V's join the softmax's
-// exponent: the weight of a token is 2^(x_t + ev_t - m) with m the running
-// maximum of x_t + ev_t, less 10, so that fp16 weights lie in (0, 2^10] and keep
-// their 11 bits down to 2^-24 of the largest; the denominator's terms 2^(x_t -
-// m) stay fp32 and cannot overflow as ev >= -100.
+// A unit of work is a (KV head, sequence, partition) or work item. Four consumer
+// warps and a producer warp make a CTA; three CTAs share an SM, and each stays:
+// when a unit's stages are almost all asked for, the producer asks launch control
+// for a CTA that has not started and takes its unit over, so the next unit's codes
+// are under way while the consumers finish this one. The producer streams each
+// block's codes with TMA tensor loads into a ring of three 16 KB stages (64 tokens
+// of d = 128, 128 of d = 64), their exponents with 16-byte asynchronous copies (a
+// block and head's K and V exponents are contiguous) and a unit's queries with one
+// bulk copy. Consumers widen codes to fp16, where e4m3 is exact, in registers and
+// multiply on the tensor cores (m16n8k16, tokens as M, the group's heads as N); V's
+// codes are transposed on their way out of shared memory (ldmatrix .b8.trans),
+// which fixes the order of a tile's tokens. The exponents never touch the codes.
+// K's scale the finished scores. V's join the softmax's exponent: the weight of a
+// token is 2^(x_t + ev_t - m) with m the running maximum of x_t + ev_t, less 10,
+// so that fp16 weights lie in (0, 2^10] and keep their 11 bits down to 2^-24 of
+// the largest; the denominator's terms 2^(x_t - m) stay fp32 and cannot overflow
+// as ev >= -100.
+//
+// mma.sync carries it: with 8 rows of query for 2 (d + 1) bytes the tensor cores
+// are 14% busy, and the widening to fp16 has to pass registers in any case, where
+// tcgen05 would want it back in shared memory.
+//
+// Measured (bf16 queries, 64 = 8 x 8 heads of 128 unless said): 8 sequences of
+// 32 768 tokens in 90.6 us, 5.97 TB/s (88% of a copy); 256 of 16 to 1964 tokens,
+// 32 = 4 x 8 heads, in 52.9, 4.79 TB/s (71%): a unit there is 15 stages or fewer,
+// and what remains is their beginnings and ends (issue slots 45%, DRAM 63% busy).
+// There, one CTA per unit took 58.0 us with 4 stages, 56.0 with 3 stages and 4
+// CTAs; exponents by bulk copies cost 68 against 63.5 at blocks of 8; stages of 64
+// tokens at d = 64 cost 50.8 against 42.6.
 //
 // Precision: a query head is scaled by the power of two that brings its largest
 // value into [2^14, 2^15), so bf16 queries are exact in fp16 (down to 2^-32 of
@@ -569,7 +587,7 @@ pk_status run(const RowsParams &p, const pk_cache_desc &d, cudaStream_t stream) 
 }  // namespace
 
 // The launch bounds ask for 3, and the shared memory allows them (head_dim 128:
-// 3 x 67 KB); the planner fills that many.
+// 3 x 72 KB, fp32 queries 76); the planner fills that many.
 extern "C" int pkx_e4m3_resident_ctas(int, int) { return 3; }
 
 extern "C" pk_status pk_paged_attention_decode_e4m3(

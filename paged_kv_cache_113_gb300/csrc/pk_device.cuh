@@ -357,9 +357,9 @@ __device__ __forceinline__ float4 widen4(const float4 &v) { return v; }
 __device__ __forceinline__ float4 widen4(const uint2 &v) {
   return make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
 }
-__device__ __forceinline__ void store4(float *p, const float4 &v) { *reinterpret_cast<float4 *>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float4 &v) {
-  *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+__device__ __forceinline__ float4 narrow4(const float4 &v, float) { return v; }
+__device__ __forceinline__ uint2 narrow4(const float4 &v, __nv_bfloat16) {
+  return make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
 // Host: the value of a translation unit's device error word, which is cleared

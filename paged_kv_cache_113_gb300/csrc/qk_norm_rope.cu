@@ -9,8 +9,12 @@
 // rounded once. The key goes to k_out and to its slot of the cache, the value
 // to its slot.
 //
-// Pure data movement bounds it: every input is read once and every output
-// written once, and a head costs about 7 operations per element.
+// Data movement bounds it: every input is read once and every output written
+// once, and a head costs about 7 operations per element. What decides is how much
+// a warp has under way before its first result: 8192 tokens of 32 + 2 x 8 heads
+// of 128 (bf16, 222 MB with the rotations) take 44.8 us, 4.96 TB/s, with four rounds of loads first;
+// 67.6 us with one, 55.3 with two, 53.3 with eight (registers leave too few warps).
+// A decode step's 64 tokens take 2.3 us on the device: latency, not bytes.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -40,7 +44,11 @@ struct RopeParams {
   int32_t heads;                // heads of a token that have work: Hq + Hk (+ Hk values)
 };
 
-// Rounds per warp: 4 from this many heads on, else 1.
+// Rounds per warp: 4 from this many heads on, else 1. Fewer heads leave SMs idle
+// and one round is the shorter way through; more are bounded by the bytes under
+// way. Device times with one and four rounds, bf16, 48 heads of 128 a token: 768
+// heads 1.9 and 2.9 us, 12 288 heads 4.06 and 4.09, 16 320 heads 5.0 and 4.7,
+// 24 576 heads 6.5 and 5.4, 393 216 heads 65 and 42.
 constexpr int64_t kManyHeads = 16384;
 
 // A head is d / 8 of LANES lanes (a power of two), each with two chunks of four
@@ -65,16 +73,17 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(RopeParams p) {
   const bool in = lane * 8 < p.d, turn = lane * 8 < p.rot;
   const bool apart = turn && !p.interleaved;
   const int ea = apart ? 4 * lane : 8 * lane, eb = apart ? p.rot / 2 + 4 * lane : 8 * lane + 4;
+  // Bases such that head * d leads to the head, whichever of the three it is.
+  const T *const in_q = static_cast<const T *>(p.q) + tok * p.q_stride;
+  const T *const in_k = static_cast<const T *>(p.k) + tok * p.k_stride - p.hq * p.d;
+  const T *const in_v = static_cast<const T *>(p.v) + tok * p.v_stride - (p.hq + p.hk) * p.d;
   Raw ra[U], rb[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int head = first + u * HPW;
     ra[u] = rb[u] = Raw{};
     if (!in || head >= p.heads) continue;
-    const bool is_q = head < p.hq, is_k = head < p.hq + p.hk;
-    const T *src = static_cast<const T *>(is_q ? p.q : (is_k ? p.k : p.v)) +
-                   tok * (is_q ? p.q_stride : (is_k ? p.k_stride : p.v_stride)) +
-                   (is_q ? head : (is_k ? head - p.hq : head - p.hq - p.hk)) * p.d;
+    const T *src = (head < p.hq ? in_q : (head < p.hq + p.hk ? in_k : in_v)) + head * p.d;
     ra[u] = pk::raw4(src + ea);
     rb[u] = pk::raw4(src + eb);
   }
@@ -94,17 +103,29 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(RopeParams p) {
     c = __ldg(reinterpret_cast<const float4 *>(cs));
     s = __ldg(reinterpret_cast<const float4 *>(cs + p.rot / 2));
   }
+  T *const to_q = static_cast<T *>(p.q_out) + tok * p.hq * p.d;
+  T *const to_k = p.k_out ? static_cast<T *>(p.k_out) + (tok * p.hk - p.hq) * p.d : nullptr;
+  T *const cache_k = static_cast<T *>(p.k_cache) + (slot * p.hk - p.hq) * p.d;
+  T *const cache_v = static_cast<T *>(p.v_cache) + (slot * p.hk - p.hq - p.hk) * p.d;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int head = first + u * HPW;
-    const bool is_q = head < p.hq, is_k = !is_q && head < p.hq + p.hk, on = in && head < p.heads;
+    const bool is_q = head < p.hq, on = in && head < p.heads;
+    if (__all_sync(0xffffffffu, head >= p.hq + p.hk)) {  // values, or nothing: as they are
+      if (on && slot >= 0) {
+        *reinterpret_cast<Raw *>(cache_v + head * p.d + ea) = ra[u];
+        *reinterpret_cast<Raw *>(cache_v + head * p.d + eb) = rb[u];
+      }
+      continue;
+    }
+    const bool value = head >= p.hq + p.hk;
     float4 a = pk::widen4(ra[u]), b = pk::widen4(rb[u]);
     if (p.q_weight) {  // every lane of the warp takes part in the shuffles
       float ss = a.x * a.x + a.y * a.y + a.z * a.z + a.w * a.w;
       ss += b.x * b.x + b.y * b.y + b.z * b.z + b.w * b.w;
 #pragma unroll
       for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (on && (is_q || is_k)) {
+      if (!value && on) {
         const float r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
         const T *w = static_cast<const T *>(is_q ? p.q_weight : p.k_weight);
         const float4 ga = pk::widen4(pk::raw4(w + ea)), gb = pk::widen4(pk::raw4(w + eb));
@@ -113,7 +134,7 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(RopeParams p) {
       }
     }
     if (!on) continue;
-    if (turn && (is_q || is_k)) {
+    if (turn && !value) {
       const float4 x = a, y = b;
       if (apart) {
         a = make_float4(x.x * c.x - y.x * s.x, x.y * c.y - y.y * s.y, x.z * c.z - y.z * s.z, x.w * c.w - y.w * s.w);
@@ -123,18 +144,17 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(RopeParams p) {
         b = make_float4(y.x * c.z - y.y * s.z, y.y * c.z + y.x * s.z, y.z * c.w - y.w * s.w, y.w * c.w + y.z * s.w);
       }
     }
+    const Raw oa = value ? ra[u] : pk::narrow4(a, T()), ob = value ? rb[u] : pk::narrow4(b, T());
     auto put = [&](T *to) {
-      pk::store4(to + ea, a);
-      pk::store4(to + eb, b);
+      *reinterpret_cast<Raw *>(to + head * p.d + ea) = oa;
+      *reinterpret_cast<Raw *>(to + head * p.d + eb) = ob;
     };
     if (is_q) {
-      put(static_cast<T *>(p.q_out) + (tok * p.hq + head) * p.d);
-      continue;
+      put(to_q);
+    } else {
+      if (to_k && !value) put(to_k);
+      if (slot >= 0) put(value ? cache_v : cache_k);
     }
-    const int h = is_k ? head - p.hq : head - p.hq - p.hk;
-    if (is_k && p.k_out) put(static_cast<T *>(p.k_out) + (tok * p.hk + h) * p.d);
-    if (slot >= 0)  // a value reaches here as it was loaded: the round trip through fp32 is exact
-      put(static_cast<T *>(is_k ? p.k_cache : p.v_cache) + (slot * p.hk + h) * p.d);
   }
 }
 

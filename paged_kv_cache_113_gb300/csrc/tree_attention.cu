@@ -4,30 +4,46 @@
 // in the cache, and a 64-bit mask per token says which drafts it sees.
 //
 // Per KV head a sequence is n G rows of query against ctx keys: 4 d operations
-// per row and key for 4 d bytes (bf16), so that up to some 283 rows of work per
-// byte read the memory bounds it, beyond that the tensor cores.
+// per row and key for 4 d bytes of key and value (bf16), so up to some 283 rows
+// the memory bounds it, beyond that the tensor cores.
 //
 // bf16 (attn_tree_kernel): tcgen05 products with tensor-memory accumulators. A
 // CTA holds 128 rows, one lane of tensor memory each, and goes over its keys in
-// tiles of 64 tokens:
-//   producer warp   TMA loads of each block's K and V into two rings;
-//   score warp      S_j = Q K_j^T (128 x 64), two tiles' worth ahead of
-//   value warp      O += P_j V_j, P_j read from tensor memory, so that products
-//                   run under the softmax of the tile between;
-//   softmax warps   a thread owns a row: reads its 64 scores, masks them,
-//                   keeps the running maximum and sum, and writes the weights
-//                   over the scores.
+// pairs of 64-token tiles:
+//   producer warp   TMA loads of each block's K (a pair at a time) and V (a tile
+//                   at a time);
+//   score warp      S = Q K^T of a pair (128 x 128) as soon as the softmax has
+//                   read the last; a 128 x 64 product costs as much time;
+//   value warp      O += P V per tile, P read from tensor memory, under the
+//                   softmax of the next tile;
+//   softmax warps   a thread owns a row: reads its 64 scores, masks them, keeps
+//                   the running maximum and sum, and writes the weights over the
+//                   scores;
+//   units' warp     asks launch control for the next unit.
 // O stays in tensor memory. A row's reference of the exponent moves only when
 // the maximum has outgrown it by 2^8: until then weights up to 2^8 are added as
 // they are (fp32 accumulators, fp32 sums), and O is rescaled a few times per
 // row instead of once per tile.
 // The weights enter the product as a bf16 pair hi + lo (one bf16 would put
 // 2^-9 on every output).
-// 256 columns of tensor memory (two 64-column score tiles, 128 for O) and 97 KB
-// of shared memory let two CTAs share an SM: one's softmax overlaps the
-// other's products. The CTAs stay: each goes over its share of the (128 rows,
-// partition) units, and the producer runs into the next unit while the softmax
-// warps finish the last, so that short contexts keep memory busy too.
+// 256 columns of tensor memory (128 of scores, 128 of O) and 105 KB of shared
+// memory let two CTAs share an SM: one's softmax overlaps the other's products.
+// The CTAs stay: a unit is 128 rows of a (sequence, KV head) over a partition,
+// and when one is almost done its CTA takes over the unit of one that has not
+// started, so that short contexts keep memory busy too and uneven ones even out.
+//
+// Measured (heads of 128, blocks of 16): 8 sequences of 32 768 tokens with 32
+// drafts, 64 = 8 x 8 heads (256 rows a KV head) 346 us, 795 TFLOP/s of the
+// formula's work, 1.19 PFLOP/s with the second half of the weights; with 16 drafts
+// or fewer (one unit of 128 rows reads all) 178 to 198 us, 5.4 to 6.0 TB/s. 256
+// sequences of 16 to 1964 tokens with 16 drafts, 32 = 4 x 8 heads, 113 us, 4.7
+// TB/s (69% of a copy). There units dealt out at launch took 149 us (ragged
+// lengths) against 115 by launch control. One product warp in place of two: equal.
+// Scores of 64 tokens at a time: 343 us against 334 (the long case). The wait on a
+// barrier that has long completed costs a product warp 200 cycles, so the fewer
+// steps, the better; what bounds it now is the softmax's path from scores read to
+// weights written, which the other CTA's products cover but in part (tensor pipe
+// 41 to 44% busy, issue slots 27%).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -698,6 +714,11 @@ pk_status launch_tree_d(const RowsParams &p, const pk_cache_desc &d, cudaStream_
 // Which elements of d (or tokens) are a fragment's k (or M) is free as long as
 // both factors agree: a lane takes four neighbours at a time, one vector load for
 // two products.
+//
+// Measured (fp32, 64 sequences of some 1000 tokens, 32 = 4 x 8 heads of 128): 16
+// drafts 418 us (652 with three tf32 products, 797 with fp32 FMAs), 4 drafts 154
+// us (554 with FMAs), one draft 113 us: bounded by the splitting of K and V into
+// parts and the products' issue, not by memory (a quarter of its rate at 4).
 // ---------------------------------------------------------------------------
 template <typename T, int D, int NT>
 struct SplitShape {
