@@ -660,8 +660,8 @@ def pk_qk_norm_rope_and_cache(q_out, k_out, q, k, v, cos_sin, positions, q_weigh
             raise ValueError("cos_sin must be [max_position, rotary_dim] and positions [num_tokens]")
         max_pos, rot = cos_sin.shape
         cs, pos = _at(cos_sin, "cos_sin", dev, torch.float32), _at(positions, "positions", dev, torch.int64)
-    _launch(torch, "pk_qk_norm_rope_and_cache", dev, stream, _at(q_out, "q_out", dev, dt), ko, qp, kp, vp, qs, ks, vs, qw,
-            kw, float(eps), cs, pos, max_pos, rot, 1 if interleaved else 0, slots, T, Hq, kc, vc, ref)
+    _launch(torch, "pk_qk_norm_rope_and_cache", dev, stream, _at(q_out, "q_out", dev, dt), ko, qp, kp, vp, qs, ks, vs,
+            qw, kw, float(eps), cs, pos, max_pos, rot, 1 if interleaved else 0, slots, T, Hq, kc, vc, ref)
 
 
 def _e4m3_cache(torch, k_cache, v_cache, kv_exp):

@@ -29,9 +29,10 @@
 // tcgen05 would want it back in shared memory.
 //
 // Measured (bf16 queries, 64 = 8 x 8 heads of 128 unless said): 8 sequences of
-// 32 768 tokens in 90.6 us, 5.97 TB/s (88% of a copy); 256 of 16 to 1964 tokens,
-// 32 = 4 x 8 heads, in 52.9, 4.79 TB/s (71%): a unit there is 15 stages or fewer,
-// and what remains is their beginnings and ends (issue slots 45%, DRAM 63% busy).
+// 32 768 tokens in 90.6 us, 5.97 TB/s (88% of a copy); 256 of some 500 (33 to
+// 4608) tokens, 32 = 4 x 8 heads, in 53 to 54, 4.7 to 4.8 TB/s (70%): a unit there
+// is eight stages on average, and what remains is beginnings and ends (issue slots
+// 41%, DRAM 63% busy).
 // There, one CTA per unit took 58.0 us with 4 stages, 56.0 with 3 stages and 4
 // CTAs; exponents by bulk copies cost 68 against 63.5 at blocks of 8; stages of 64
 // tokens at d = 64 cost 50.8 against 42.6.

@@ -325,22 +325,8 @@ __device__ __forceinline__ float load_elem(const __nv_bfloat16 *p) { return __bf
 __device__ __forceinline__ void store_elem(float *p, float x) { *p = x; }
 __device__ __forceinline__ void store_elem(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
-// Eight consecutive elements (16-byte aligned) of either storage type as fp32
-// values, and back (rounded to nearest even).
-__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4 *>(p);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16_lo(w[i]);
-    x[2 * i + 1] = bf16_hi(w[i]);
-  }
-}
+// Eight fp32 values to consecutive elements (16-byte aligned) of either storage
+// type, rounded to nearest even.
 __device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
   reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
   reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);

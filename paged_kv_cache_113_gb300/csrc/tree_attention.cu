@@ -36,14 +36,14 @@
 // drafts, 64 = 8 x 8 heads (256 rows a KV head) 346 us, 795 TFLOP/s of the
 // formula's work, 1.19 PFLOP/s with the second half of the weights; with 16 drafts
 // or fewer (one unit of 128 rows reads all) 178 to 198 us, 5.4 to 6.0 TB/s. 256
-// sequences of 16 to 1964 tokens with 16 drafts, 32 = 4 x 8 heads, 113 us, 4.7
-// TB/s (69% of a copy). There units dealt out at launch took 149 us (ragged
-// lengths) against 115 by launch control. One product warp in place of two: equal.
+// sequences of some 500 (64 to 4608) tokens with 16 drafts, 32 = 4 x 8 heads, 113
+// to 122 us, 4.4 to 4.7 TB/s (64 to 69% of a copy). There units dealt out at launch
+// took 149 us against 115 by launch control. One product warp in place of two: equal.
 // Scores of 64 tokens at a time: 343 us against 334 (the long case). The wait on a
 // barrier that has long completed costs a product warp 200 cycles, so the fewer
 // steps, the better; what bounds it now is the softmax's path from scores read to
 // weights written, which the other CTA's products cover but in part (tensor pipe
-// 41 to 44% busy, issue slots 27%).
+// 38 to 44% busy, issue slots 25 to 30%).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -617,7 +617,8 @@ def test_streams_and_graph_replay():
     ws2 = torch.empty(pk.pk_paged_attention_workspace_size(S, hq, 220, 64, desc8), dtype=torch.uint8, device=DEV)
 
     def step(stream=None):
-        pk.pk_qk_norm_rope_and_cache(qo, ko, q, k, v, cs, pos, slot_mapping=slots, k_cache=kc, v_cache=vc, stream=stream)
+        pk.pk_qk_norm_rope_and_cache(qo, ko, q, k, v, cs, pos, slot_mapping=slots, k_cache=kc, v_cache=vc,
+                                     stream=stream)
         pk.pk_reshape_and_cache_e4m3(ko, v, slots, k8, v8, ex, stream=stream)
         pk.pk_paged_attention_tree(o1, qo, kc, vc, tb, ln, of, 0.09, 7, 220, partition_size=64, workspace=ws1,
                                    stream=stream)
@@ -764,7 +765,8 @@ def test_offsets_past_32_bits():
     kc = torch.empty((N, B, hk, d), dtype=torch.bfloat16, device=DEV)
     vc = torch.empty_like(kc)
     blocks = i64(use)
-    kc[blocks], vc[blocks] = rand(rng, (len(use), B, hk, d), torch.bfloat16), rand(rng, (len(use), B, hk, d), torch.bfloat16)
+    kc[blocks] = rand(rng, (len(use), B, hk, d), torch.bfloat16)
+    vc[blocks] = rand(rng, (len(use), B, hk, d), torch.bfloat16)
     q, ofs = rand(rng, (4, hq, d), torch.bfloat16), [0, 3, 4]
     # new tokens through the fused write, at slots of the last blocks
     qkv = rand(rng, (4, hq + 2 * hk, d), torch.bfloat16)
@@ -792,7 +794,8 @@ def test_offsets_past_32_bits():
     q = rand(rng, (2, hq, d))
     out = torch.empty_like(q)
     pk.pk_paged_attention_decode_e4m3(out, q, k8, v8, ex, i32(tables), i32(lens), 0.09, 40, partition_size=0)
-    want, terms = plain.tree_attention(f64(q), f64(k2).reshape(-1, B, hk, d), f64(v2).reshape(-1, B, hk, d), small, lens, 0.09)
+    want, terms = plain.tree_attention(f64(q), f64(k2).reshape(-1, B, hk, d), f64(v2).reshape(-1, B, hk, d), small,
+                                       lens, 0.09)
     check_attention(f64(out), want, terms, d, torch.float32, RHO_E4M3[torch.float32])
 
 
@@ -809,7 +812,8 @@ def test_two_streams_at_once():
 
     def call(stream=None):
         outs = [torch.zeros_like(q), torch.zeros_like(qd)]
-        ws = [torch.empty(pk.pk_tree_workspace_size(len(q), hq, 900, 128, pk.cache_desc(k)), dtype=torch.uint8, device=DEV),
+        ws = [torch.empty(pk.pk_tree_workspace_size(len(q), hq, 900, 128, pk.cache_desc(k)), dtype=torch.uint8,
+                          device=DEV),
               torch.empty(pk.pk_paged_attention_workspace_size(S, hq, 900, 128, pk.cache_desc(kc)), dtype=torch.uint8,
                           device=DEV)]
         torch.cuda.synchronize()
