@@ -426,7 +426,7 @@ size_t pk_paged_attention_workspace_size(int32_t num_seqs, int32_t num_q_heads,
  *   interleaved   0: pair j is (j, j + rotary_dim / 2); else (2j, 2j + 1).
  *   slot_mapping  int64 [T], or NULL: no cache write (v, k_cache and v_cache are
  *                 not used). Negative slots are skipped; out-of-range slots are
- *                 skipped and recorded (PK_DEVERR_SLOT).
+ *                 skipped and recorded (PK_DEVERR_SLOT); duplicates race.
  *   desc          dtype (PK_F32 or PK_BF16) of all but cos_sin; d a multiple of
  *                 16, at most 256. */
 pk_status pk_qk_norm_rope_and_cache(
@@ -452,7 +452,8 @@ pk_status pk_qk_norm_rope_and_cache(
 
 /* As pk_reshape_and_cache into an 8-bit cache. k, v: src_dtype (PK_F32 or
  * PK_BF16), token i's [Hk, d] at i * k_stride (v_stride) elements, strides
- * multiples of 16 bytes. */
+ * multiples of 16 bytes. Duplicate slots in one call race: such a slot's codes and
+ * exponents may then come from different tokens. */
 pk_status pk_reshape_and_cache_e4m3(const void *k, const void *v, pk_dtype src_dtype,
                                     int64_t k_stride, int64_t v_stride,
                                     const int64_t *slot_mapping, int32_t num_tokens, void *k_cache,

@@ -560,11 +560,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         __syncwarp();
       };
+      float odd = 0.0f;  // NaN once an element is not finite
 #pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
         uint32_t o[32];
         tmem_load32(t_o + lane_base + 32 * ch, o);
         tmem_wait_load(o);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) odd = fmaf(__uint_as_float(o[e]), 0.0f, odd);
         uint32_t w[16];
         if (split) {
 #pragma unroll
@@ -585,6 +588,42 @@ __global__ void __launch_bounds__(kThreads, 2)
         p.ws_l[slot] = l;
       }
       __syncwarp();
+      if (odd != 0.0f && mine && fabsf(l) <= 3.402823466e38f) {
+        // A context value that is not finite gave NaN, by the product with a weight's
+        // lower half: the sum of what is not finite in its place. Eight columns at a
+        // time.
+#pragma unroll 1
+        for (int ch = 0; ch < D / 8; ++ch) {
+          float *const acc = p.ws_acc + slot * D + ch * 8;
+          __nv_bfloat16 *const res = static_cast<__nv_bfloat16 *>(p.out) + at + ch * 8;
+          bool bad = false;
+          for (int e = 0; e < 8; ++e)
+            bad = bad || !(fabsf(split ? acc[e] : __bfloat162float(res[e])) <= 3.402823466e38f);
+          if (!bad) continue;
+          float sum[8] = {};
+#pragma unroll 4
+          for (int k = c.start; k < lim; ++k) {
+            const int phys = min(max(__ldg(p.tables + size_t(c.s) * p.max_blocks + k / BS), 0), p.num_blocks - 1);
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(
+                static_cast<const __nv_bfloat16 *>(p.v_cache) +
+                ((size_t(phys) * BS + k % BS) * p.num_kv_heads + c.kvh) * D + ch * 8));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float y = e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+              sum[e] += fabsf(y) <= 3.402823466e38f ? 0.0f : y;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (sum[e] == 0.0f) continue;
+            if (split)
+              acc[e] = sum[e];
+            else
+              res[e] = __float2bfloat16_rn(sum[e]);
+          }
+        }
+      }
       if (fix && mine) {  // what is not finite in the values of the drafts that the row sees
         const uint64_t mask = row_mask();
         const int base = c.ctx - c.n;
@@ -716,8 +755,8 @@ pk_status launch_tree_d(const RowsParams &p, const pk_cache_desc &d, cudaStream_
 // two products.
 //
 // Measured (fp32, 64 sequences of some 1000 tokens, 32 = 4 x 8 heads of 128): 16
-// drafts 418 us (652 with three tf32 products, 797 with fp32 FMAs), 4 drafts 154
-// us (554 with FMAs), one draft 113 us: bounded by the splitting of K and V into
+// drafts 404 us (652 with three tf32 products, 797 with fp32 FMAs), 4 drafts 148
+// us (554 with FMAs), one draft 109 us: bounded by the splitting of K and V into
 // parts and the products' issue, not by memory (a quarter of its rate at 4).
 // ---------------------------------------------------------------------------
 template <typename T, int D, int NT>
@@ -737,17 +776,16 @@ struct SplitShape {
   static constexpr int SMEM_BYTES = KV_BYTES + PARTS * R * Q_PITCH + 4 * WARP_P;
 };
 
-// N bf16 parts of a pair of fp32 values, largest first. `key`: an infinite key
-// keeps its infinite score (inf - inf has no place in the next part).
+// N bf16 parts of a pair of fp32 values, largest first (what is not finite
+// becomes NaN if N > 1: inf - inf).
 template <int N>
-__device__ __forceinline__ void bf16_parts(float x, float y, uint32_t (&w)[N], bool key) {
+__device__ __forceinline__ void bf16_parts(float x, float y, uint32_t (&w)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     w[i] = pack_bf16x2(x, y);
     if (i + 1 == N) break;
-    const float a = bf16_lo(w[i]), b = bf16_hi(w[i]);
-    x = key && !(fabsf(a) <= 3.402823466e38f) ? 0.0f : x - a;
-    y = key && !(fabsf(b) <= 3.402823466e38f) ? 0.0f : y - b;
+    x -= bf16_lo(w[i]);
+    y -= bf16_hi(w[i]);
   }
 }
 
@@ -832,7 +870,7 @@ __global__ void __launch_bounds__(128, 2) attn_split_kernel(RowsParams p) {
     const T *src = static_cast<const T *>(p.q) + q_row(min(r, rows - 1)) + c;
     const float f = r >= rows ? 0.0f : (NP > 1 ? p.scale_log2 : 1.0f);  // bf16 queries stay as they are
     uint32_t w[NP];
-    bf16_parts(r < rows ? load_elem(src) * f : 0.0f, r < rows ? load_elem(src + 1) * f : 0.0f, w, false);
+    bf16_parts(r < rows ? load_elem(src) * f : 0.0f, r < rows ? load_elem(src + 1) * f : 0.0f, w);
 #pragma unroll
     for (int k = 0; k < NP; ++k) *reinterpret_cast<uint32_t *>(q_sm + (k * R + r) * S::Q_PITCH + c * 2) = w[k];
   }
@@ -859,10 +897,10 @@ __global__ void __launch_bounds__(128, 2) attn_split_kernel(RowsParams p) {
       uint32_t a[4][NP];
       const float4 k0 = load4(reinterpret_cast<const T *>(kw + rw * S::K_PITCH) + 16 * c + 4 * qd);
       const float4 k1 = load4(reinterpret_cast<const T *>(kw + (rw + 8) * S::K_PITCH) + 16 * c + 4 * qd);
-      bf16_parts(k0.x, k0.y, a[0], true);
-      bf16_parts(k1.x, k1.y, a[1], true);
-      bf16_parts(k0.z, k0.w, a[2], true);
-      bf16_parts(k1.z, k1.w, a[3], true);
+      bf16_parts(k0.x, k0.y, a[0]);
+      bf16_parts(k1.x, k1.y, a[1]);
+      bf16_parts(k0.z, k0.w, a[2]);
+      bf16_parts(k1.z, k1.w, a[3]);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         uint32_t b[2][NP];
@@ -873,6 +911,35 @@ __global__ void __launch_bounds__(128, 2) attn_split_kernel(RowsParams p) {
           b[0][k] = w.x, b[1][k] = w.y;
         }
         mma_parts(x[n], a, b);
+      }
+    }
+    if (NP > 1) {
+      // A key value that is not finite made its scores NaN, as its second part is
+      // inf - inf: those are summed again without parts, as -inf is a score too.
+      float odd = 0.0f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) odd = fmaf(x[n][e], 0.0f, odd);
+      if (__any_sync(0xffffffffu, odd != 0.0f)) {
+        uint32_t which = 0;
+#pragma unroll
+        for (int i = 0; i < 4 * NT; ++i)
+          if (x[i / 4][i % 4] != x[i / 4][i % 4]) which |= 1u << i, x[i / 4][i % 4] = 0.0f;
+#pragma unroll 1
+        for (int j = 0; which && j < D; ++j)
+#pragma unroll
+          for (int i = 0; i < 4 * NT; ++i) {
+            if (!((which >> i) & 1)) continue;
+            float f = 0.0f;
+#pragma unroll
+            for (int k = NP - 1; k >= 0; --k)
+              f += load_elem(reinterpret_cast<const __nv_bfloat16 *>(
+                                 q_sm + (k * R + 8 * (i / 4) + 2 * qd + (i & 1)) * S::Q_PITCH) + j);
+            x[i / 4][i % 4] =
+                fmaf(load_elem(reinterpret_cast<const T *>(kw + (rw + 8 * (i % 4 / 2)) * S::K_PITCH) + j), f,
+                     x[i / 4][i % 4]);
+          }
       }
     }
     __syncwarp();
@@ -939,8 +1006,8 @@ __global__ void __launch_bounds__(128, 2) attn_split_kernel(RowsParams p) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const float *w = pw + (8 * n + rw) * (S::P_PITCH / 4) + qd;
-      bf16_parts(w[0], w[4], b[n][0], false);
-      bf16_parts(w[8], w[12], b[n][1], false);
+      bf16_parts(w[0], w[4], b[n][0]);
+      bf16_parts(w[8], w[12], b[n][1]);
     }
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
@@ -953,10 +1020,10 @@ __global__ void __launch_bounds__(128, 2) attn_split_kernel(RowsParams p) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         uint32_t a[4][NP];
-        bf16_parts(v[0][2 * e], v[1][2 * e], a[0], false);
-        bf16_parts(v[0][2 * e + 1], v[1][2 * e + 1], a[1], false);
-        bf16_parts(v[2][2 * e], v[3][2 * e], a[2], false);
-        bf16_parts(v[2][2 * e + 1], v[3][2 * e + 1], a[3], false);
+        bf16_parts(v[0][2 * e], v[1][2 * e], a[0]);
+        bf16_parts(v[0][2 * e + 1], v[1][2 * e + 1], a[1]);
+        bf16_parts(v[2][2 * e], v[3][2 * e], a[2]);
+        bf16_parts(v[2][2 * e + 1], v[3][2 * e + 1], a[3]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) mma_parts(o[2 * c + e][n], a, b[n]);
       }
@@ -1003,6 +1070,19 @@ __global__ void __launch_bounds__(128, 2) attn_split_kernel(RowsParams p) {
       if (f == 0.0f) continue;
       L = fmaf(sm_l[w * R + r], f, L);
       O = fmaf(sm_o[(w * R + r) * S::O_PITCH + c], f, O);
+    }
+    // A context value that is not finite gave NaN, by the product with a part of a
+    // weight that is 0 or negative: the sum of what is not finite in its place.
+    if (!(fabsf(O) <= 3.402823466e38f) && fabsf(L) <= 3.402823466e38f) {
+      float odd = 0.0f;
+#pragma unroll 4
+      for (int t = start; t < lim; ++t) {
+        const int phys = min(max(__ldg(trow + t / p.block_size), 0), p.num_blocks - 1);
+        const float y = load_elem(static_cast<const T *>(p.v_cache) +
+                                  ((size_t(phys) * p.block_size + t % p.block_size) * p.num_kv_heads + kvh) * D + c);
+        odd += fabsf(y) <= 3.402823466e38f ? 0.0f : y;
+      }
+      if (odd != 0.0f) O = odd;
     }
     if (poisoned)  // what is not finite in the values of the drafts that the row sees
       for (int t = max(base, start); t < end; ++t) {

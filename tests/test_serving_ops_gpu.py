@@ -494,6 +494,47 @@ def test_tree_hidden_tokens_do_not_reach_a_row(dtype):
                         assert (hit == val).all()
 
 
+@pytest.mark.parametrize("dtype,B", [("f32", 16), ("bf16", 16), ("bf16", 5)])
+def test_tree_infinities_that_a_row_sees(dtype, B):
+    """Infinite context keys are scores of +-inf, infinite values reach the rows as they are."""
+    dt, hq, hk, d = DTYPES[dtype], 4, 2, 128
+    rng = np.random.default_rng(14)
+    counts, lens = [7, 3], np.array([150, 40], np.int32)
+    tables, k, v, ofs, masks, q, mt = tree_case(rng, counts, lens, B, hq, hk, d, dt, "tree")
+    kf, vf = k.clone(), v.clone()                  # finite twins, for the bounds
+
+    def at(s, pos):
+        return int(tables[s][pos // B]), pos % B
+
+    inf, n = float("inf"), int(ofs[-1])
+    k[at(0, 70)][1, 5] = -inf                      # -inf for positive query elements, +inf for the others
+    k[at(1, 3)][0, 40] = inf
+    q[0, 2, 5] = 0.75                              # exact in few bits
+    for s, pos, col, val in ((0, 3, 7, inf), (0, 100, 8, -inf), (0, 64, 9, float("nan")), (0, 1, 10, inf),
+                             (0, 140, 10, -inf), (1, 20, 127, -inf), (0, 130, 11, inf), (0, 131, 11, inf)):
+        v[at(s, pos)][1, col] = val
+    scale = d ** -0.5
+    with np.errstate(invalid="ignore"):
+        want, _ = plain.tree_attention(f64(q), f64(k), f64(v), tables, lens, scale, ofs, masks)
+    _, terms = plain.tree_attention(f64(q), f64(kf), f64(vf), tables, lens, scale, ofs, masks)
+    live = np.isfinite(want[:n])
+    assert live.any(axis=-1).any() and np.isinf(want[:n]).any() and np.isnan(want[:n]).all(axis=-1).any()
+    top = np.nanmax(np.abs(f64(vf)))
+    for part in (0, -(-64 // B) * B):
+        out = torch.full_like(q, 5.0)
+        ws = torch.empty(max(16, pk.pk_tree_workspace_size(len(q), hq, 200, part, pk.cache_desc(k))),
+                         dtype=torch.uint8, device=DEV)
+        pk.pk_paged_attention_tree(out, q, k, v, i32(tables), i32(lens), i32(ofs), scale, 64, 200, tree_mask=mt,
+                                   partition_size=part, workspace=ws)
+        got = f64(out)[:n]
+        assert np.array_equal(np.isnan(got), np.isnan(want[:n]))
+        odd = np.isinf(want[:n])
+        assert np.array_equal(odd, np.isinf(got)) and (got[odd] == want[:n][odd]).all()
+        # The finite elements; a weighted mean of values is at most the largest.
+        wv, mag, cnt = (np.full_like(want[:n], top), terms[1][:n], terms[2][:n])
+        check_attention(np.where(live, got, 0.0), np.where(live, want[:n], 0.0), (wv, mag, cnt), d, dt, RHO_TREE[dt])
+
+
 def test_tree_bad_inputs_are_recorded():
     hq, hk, d, B = 4, 2, 64, 16
     rng = np.random.default_rng(13)
