@@ -19,23 +19,25 @@
 // codes are transposed on their way out of shared memory (ldmatrix .b8.trans),
 // which fixes the order of a tile's tokens. The exponents never touch the codes.
 // K's scale the finished scores. V's join the softmax's exponent: the weight of a
-// token is 2^(x_t + ev_t - m) with m the running maximum of x_t + ev_t, less 10,
-// so that fp16 weights lie in (0, 2^10] and keep their 11 bits down to 2^-24 of
-// the largest; the denominator's terms 2^(x_t - m) stay fp32 and cannot overflow
-// as ev >= -100.
+// token is 2^(x_t + ev_t - m) with m the largest x_t + ev_t so far, less 10, moved
+// only when a weight would pass 2^15: fp16 weights keep their 11 bits down to 2^-24
+// of the largest, and most tiles need neither the warp's maximum nor a rescaling.
+// The denominator's terms 2^(x_t - m) stay fp32 and cannot overflow as ev >= -100.
 //
 // mma.sync carries it: with 8 rows of query for 2 (d + 1) bytes the tensor cores
 // are 14% busy, and the widening to fp16 has to pass registers in any case, where
 // tcgen05 would want it back in shared memory.
 //
 // Measured (bf16 queries, 64 = 8 x 8 heads of 128 unless said): 8 sequences of
-// 32 768 tokens in 90.6 us, 5.97 TB/s (88% of a copy); 256 of some 500 (33 to
-// 4608) tokens, 32 = 4 x 8 heads, in 53 to 54, 4.7 to 4.8 TB/s (70%): a unit there
-// is eight stages on average, and what remains is beginnings and ends (issue slots
-// 41%, DRAM 63% busy).
-// There, one CTA per unit took 58.0 us with 4 stages, 56.0 with 3 stages and 4
-// CTAs; exponents by bulk copies cost 68 against 63.5 at blocks of 8; stages of 64
-// tokens at d = 64 cost 50.8 against 42.6.
+// 32 768 tokens in 89 to 90 us, 6.05 TB/s (89% of a copy); 256 of some 500 (33 to
+// 4608) tokens, 32 = 4 x 8 heads, in 50 to 52, 4.9 to 5.1 TB/s (74%): there the
+// first stage is full 4.8 us after the launch (items, lengths and tables, then
+// codes, each from cold memory), and the last CTAs end 7 us apart. A stage costs
+// the producer 620 cycles of issue for its eight tensor loads, of 2100 to 2400;
+// before the next unit was looked up without a wait it cost 590 more, 53 to 57 us.
+// One CTA per unit took 58.0 us with 4 stages, 56.0 with 3 stages and 4 CTAs;
+// exponents by bulk copies 68 against 63.5 at blocks of 8; stages of 64 tokens at
+// d = 64 50.8 against 42.6.
 //
 // Precision: a query head is scaled by the power of two that brings its largest
 // value into [2^14, 2^15), so bf16 queries are exact in fp16 (down to 2^-32 of
@@ -61,8 +63,9 @@ namespace {
 constexpr int kWarps = 4;             // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;  // and the producer
 constexpr int kUnits = 4;             // units known at a time
-constexpr int kAhead = 4;             // stages of a unit left when the next is asked for
-constexpr float kHeadroom = 10.0f;    // log2 of the largest fp16 weight
+constexpr int kAhead = 5;             // stages of a unit left when the next is asked for
+// log2 of the largest fp16 weight when the reference is set, and at most.
+constexpr float kHeadroom = 10.0f, kSlack = 15.0f;
 
 template <typename IO, int D, int BS>
 struct Shape {
@@ -176,9 +179,9 @@ __global__ void __launch_bounds__(kThreads, 3)
     // ---------------- producer ----------------
     // The grid has a CTA per unit, longest first; those that find no room are
     // taken over, one at a time, by whichever CTA needs work next. The next unit is
-    // asked for kAhead stages before the end of this one (early enough to be here
-    // in time, late enough to go to the CTA that is free first) and looked up a
-    // step a stage, so that no stage waits on the steps' dependent loads.
+    // asked for kAhead stages before the end of this one: early enough to be here in
+    // time, late enough to go to the CTA that is free first (4, 5, 6 and 8 stages:
+    // 52, 50, 50.3 and 53 us for the 256 short sequences).
     if (lane == 0) {
       prefetch_tensormap(&kmap);
       prefetch_tensormap(&vmap);
@@ -194,76 +197,121 @@ __global__ void __launch_bounds__(kThreads, 3)
       }
     };
     auto answered = [&] {  // the unit's number, or -1: none is left
-      if (!warp_wait(u_answer, asked & 1, ok)) return -1;
       ++asked;
       open = false;
       const int u = cancelled_cta(smem_addr(&answer));
-      fence_proxy_async();  // the answer has been read before the next one is asked for
+      fence_answer_read();
       __syncwarp();
       return u;
     };
-    // Unit u's sequence and partition, and with those its tokens: false where it
-    // has no work (a zero row for an invalid length, which is recorded).
-    auto item_of = [&](int u, int &s, int &part) {
-      const int x = u % X, y = (u / X) % Y, z = u / X / Y;
-      return work_item(p, y, p.num_partitions - 1 - z, x == 0 && lane == 0, s, part);
+    // Whether a barrier's phase has ended; with `wait`, after a wait for it.
+    auto ended = [&](uint32_t b, uint32_t parity, bool wait) {
+      return wait ? warp_wait(b, parity, ok) : bool(__all_sync(0xffffffffu, mbar_test(b, parity)));
     };
-    auto unit_of = [&](int u, int s, int part, Unit &c) {
-      const int x = u % X;
-      const SeqRows sr = seq_rows(p, s, x == 0 && lane == 0 && part == 0);
-      if (sr.ctx == 0)
-        for (int k = lane; part == 0 && k < G * D; k += 32)
-          store_elem(static_cast<IO *>(p.out) + (size_t(s) * p.num_q_heads + x * G) * D + k, 0.0f);
-      if (part >= sr.np) return false;  // no partition has tokens where ctx is 0
-      c.s = s, c.kvh = x, c.part = part, c.np = sr.np;
-      c.start = part * p.partition;
-      c.end = min(sr.ctx, c.start + p.partition);
-      c.nst = (c.end - c.start + S::TPS - 1) / S::TPS;
-      return true;
+    // The next unit u becomes known, and its queries come, in five steps, a stage or
+    // more apart; a step whose barrier is not there yet is left to the next stage.
+    // What a step needs from memory is loaded after the one before it, by every
+    // stage alike (from somewhere harmless when nothing is needed), so that no
+    // branch has a load of its own to wait for.
+    int step = 1, u = blockIdx.x;
+    const int32_t *at0 = p.ctx_lens, *at1 = p.ctx_lens;
+    int got0 = 0, got1 = 0;
+    Unit next;
+    int first = 0;                 // its first 32 table entries, a lane's one
+    bool have = false;             // it is known and has work
+    int loaded = 0;                // units whose queries are under way
+    int x = 0, y = 0, z = 0;       // u's place: KV head, work, partition of the grid
+    auto advance = [&](bool wait) {
+      const bool record = x == 0 && lane == 0;
+      switch (step++) {
+        case 0:
+          ask();
+          break;
+        case 1:
+          if (open) {  // else the first unit, the CTA's own
+            if (!ended(u_answer, asked & 1, wait)) {
+              --step;
+              break;
+            }
+            u = answered();
+          }
+          x = u % X, y = u / X % Y, z = u / X / Y;
+          if (u >= 0 && p.items) at0 = p.items + 2 * y + (lane & 1);
+          break;
+        case 2: {
+          next.s = p.items ? __shfl_sync(0xffffffffu, got0, 0) : y;
+          next.part = p.items ? __shfl_sync(0xffffffffu, got0, 1) : p.num_partitions - 1 - z;
+          have = u >= 0 && checked_item(p, y, next.s, next.part, record);
+          if (!have) break;
+          next.start = next.part * p.partition;
+          at0 = p.tables + size_t(next.s) * p.max_blocks + min(next.start / BS + lane, p.max_blocks - 1);
+          at1 = p.ctx_lens + next.s;
+          break;
+        }
+        case 3: {
+          if (!have) break;
+          const int ctx = checked_context(p, next.s, 1, got1, record && next.part == 0);
+          if (ctx == 0)  // invalid (recorded): a zero row
+            for (int k = lane; next.part == 0 && k < G * D; k += 32)
+              store_elem(static_cast<IO *>(p.out) + (size_t(next.s) * p.num_q_heads + x * G) * D + k, 0.0f);
+          next.kvh = x;
+          next.np = partitions_of(p, ctx);
+          have = next.part < next.np;
+          if (!have) break;
+          next.end = min(ctx, next.start + p.partition);
+          next.nst = (next.end - next.start + S::TPS - 1) / S::TPS;
+          first = got0;
+          break;
+        }
+        case 4: {
+          if (!have) break;
+          const int k = loaded;
+          if (k >= 2 && !ended(q_empty(k), uint32_t((k >> 1) - 1) & 1u, wait)) {
+            --step;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(q_full(k), uint32_t(G * D * sizeof(IO)));
+          __syncwarp();
+          if (lane < G)
+            bulk_load(q_sm + (k & 1) * S::Q_BYTES + lane * S::Q_ROW,
+                      static_cast<const IO *>(p.q) + (size_t(next.s) * p.num_q_heads + x * G + lane) * D,
+                      D * sizeof(IO), q_full(k));
+          ++loaded;
+        }
+      }
     };
-    Unit c;  // the unit at hand
-    int u = blockIdx.x, s = 0, part = 0;
-    bool have = item_of(u, s, part) && unit_of(u, s, part, c);
+    auto fetch = [&] {
+      got0 = __ldg(at0);
+      got1 = __ldg(at1);
+    };
     int t = 0, i = 0;
     for (; ok; ++i) {
-      while (!have && u >= 0 && ok) {  // units without work
-        ask();
-        u = answered();
-        have = u >= 0 && item_of(u, s, part) && unit_of(u, s, part, c);
+      while (ok && (step < 5 || (!have && u >= 0))) {
+        if (step == 5) step = 0;  // a unit without work
+        advance(true);
+        fetch();
       }
       if (!ok || (i >= kUnits && !warp_wait(u_empty(i), u_phase(i - kUnits), ok))) break;
       if (lane == 0) {
         if (have)
-          units[i % kUnits] = c;
+          units[i % kUnits] = next;
         else
           units[i % kUnits].s = -1;
         mbar_arrive(u_full(i));
       }
       if (!have) break;
+      const Unit c = next;
       // Table entries are read ahead in chunks of 32, one per lane, one chunk in
       // reserve, so that no stage waits on a dependent load.
       const int32_t *trow = p.tables + size_t(c.s) * p.max_blocks + c.start / BS;
       const int nb = (c.end - c.start + BS - 1) / BS;
-      int cur = lane < nb ? __ldg(trow + lane) : 0;
-      int nxt = 32 + lane < nb ? __ldg(trow + 32 + lane) : 0;
+      int cur = first, nxt = 32 + lane < nb ? __ldg(trow + 32 + lane) : 0;
       int chunk = 0;
-      if (i >= 2 && !warp_wait(q_empty(i), uint32_t((i >> 1) - 1) & 1u, ok)) break;
-      if (lane == 0) mbar_arrive_expect_tx(q_full(i), uint32_t(G * D * sizeof(IO)));
-      __syncwarp();
-      if (lane < G)
-        bulk_load(q_sm + (i & 1) * S::Q_BYTES + lane * S::Q_ROW,
-                  static_cast<const IO *>(p.q) + (size_t(c.s) * p.num_q_heads + c.kvh * G + lane) * D,
-                  D * sizeof(IO), q_full(i));
-      int step = 0;  // of the next unit's look-up
-      bool item = false;
+      step = 0;
+      have = false;
       for (int st = 0; st < c.nst; ++st, ++t) {
-        if (c.nst - st <= kAhead) {
-          if (step == 0)
-            ask();
-          else if (step == 1)
-            u = answered(), item = u >= 0 && item_of(u, s, part);
-          ++step;
-        }
+        if (c.nst - st <= kAhead && step < 5) advance(false);
+        fetch();
         const int b0 = st * S::BPS;
         if (b0 >= 32 * (chunk + 1)) {
           ++chunk;
@@ -294,15 +342,12 @@ __global__ void __launch_bounds__(kThreads, 3)
           tma_load_3d(dst + S::KV_BYTES, &vmap, full_bar(t), 0, c.kvh, phys * BS);
         }
       }
-      if (!ok) break;
-      if (step < 2) u = answered(), item = u >= 0 && item_of(u, s, part);
-      have = item && unit_of(u, s, part, c);
     }
     if (!ok && lane == 0) timeout();
     // Let every issued copy, and an answer, land before the warp leaves.
     if (open) mbar_wait(u_answer, asked & 1);
     for (int k = max(0, t - STAGES); k < t; ++k) mbar_wait(full_bar(k), t_phase(k));
-    for (int k = max(0, i - 2); k < i; ++k) mbar_wait(q_full(k), uint32_t(k >> 1) & 1u);
+    for (int k = max(0, loaded - 2); k < loaded; ++k) mbar_wait(q_full(k), uint32_t(k >> 1) & 1u);
     return;
   }
 
@@ -429,18 +474,32 @@ __global__ void __launch_bounds__(kThreads, 3)
         if (tok0 >= nvalid) x0 = x1 = -INFINITY;
         if (tok0 + 2 >= nvalid) x2 = x3 = -INFINITY;
         float z0 = fmaxf(x0 + v0, x2 + v1), z1 = fmaxf(x1 + v0, x3 + v1);
+        // The reference moves only when a weight would pass fp16's range.
+        if (__any_sync(0xffffffffu, z0 > m0 + kSlack || z1 > m1 + kSlack)) {
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          z0 = fmaxf(z0, __shfl_xor_sync(0xffffffffu, z0, off));
-          z1 = fmaxf(z1, __shfl_xor_sync(0xffffffffu, z1, off));
+          for (int off = 4; off < 32; off <<= 1) {
+            z0 = fmaxf(z0, __shfl_xor_sync(0xffffffffu, z0, off));
+            z1 = fmaxf(z1, __shfl_xor_sync(0xffffffffu, z1, off));
+          }
+          const float n0 = fmaxf(m0, z0 - kHeadroom), n1 = fmaxf(m1, z1 - kHeadroom);
+          const float c0 = exp2_ftz(m0 - n0), c1 = exp2_ftz(m1 - n1);
+          m0 = n0;
+          m1 = n1;
+          l0 *= c0;
+          l1 *= c1;
+#pragma unroll
+          for (int k = 0; k < KC; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              o[k][h][0] *= c0;
+              o[k][h][1] *= c1;
+              o[k][h][2] *= c0;
+              o[k][h][3] *= c1;
+            }
         }
-        const float n0 = fmaxf(m0, z0 - kHeadroom), n1 = fmaxf(m1, z1 - kHeadroom);
-        const float c0 = exp2_ftz(m0 - n0), c1 = exp2_ftz(m1 - n1);
-        m0 = n0;
-        m1 = n1;
-        const float y0 = x0 - n0, y1 = x1 - n1, y2 = x2 - n0, y3 = x3 - n1;
-        l0 = fmaf(l0, c0, exp2_ftz(y0) + exp2_ftz(y2));
-        l1 = fmaf(l1, c1, exp2_ftz(y1) + exp2_ftz(y3));
+        const float y0 = x0 - m0, y1 = x1 - m1, y2 = x2 - m0, y3 = x3 - m1;
+        l0 += exp2_ftz(y0) + exp2_ftz(y2);
+        l1 += exp2_ftz(y1) + exp2_ftz(y3);
         const float p0 = exp2_ftz(y0 + v0), p1 = exp2_ftz(y1 + v0);
         const float p2 = exp2_ftz(y2 + v1), p3 = exp2_ftz(y3 + v1);
         uint32_t b[QW][2];  // P^T as the B operand: the C fragments transposed
@@ -454,17 +513,6 @@ __global__ void __launch_bounds__(kThreads, 3)
             b[QW - 1][0] = movmatrix_trans(pack_f16x2(p0 - h0.x, p1 - h0.y));
             b[QW - 1][1] = movmatrix_trans(pack_f16x2(p2 - h1.x, p3 - h1.y));
           }
-        }
-        if (__any_sync(0xffffffffu, c0 != 1.0f || c1 != 1.0f)) {
-#pragma unroll
-          for (int k = 0; k < KC; ++k)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              o[k][h][0] *= c0;
-              o[k][h][1] *= c1;
-              o[k][h][2] *= c0;
-              o[k][h][3] *= c1;
-            }
         }
         // O^T += V^T P^T: a transposed load gives a lane four tokens of a column, the
         // ones that its rows of the scores belong to.
@@ -516,23 +564,26 @@ __global__ void __launch_bounds__(kThreads, 3)
     if (lane == 0) mbar_arrive(m_full);
     if (!warp_wait(m_full, uint32_t(i) & 1u, ok)) break;
     const size_t row0 = size_t(c.s) * p.num_q_heads + c.kvh * G;  // the group's first row of out
-    for (int k = threadIdx.x; k < G * D; k += kWarps * 32) {
+    for (int k = threadIdx.x * 4; k < G * D; k += kWarps * 128) {  // four columns each
       const int g = k / D, col = k % D;
       float M = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w * 8 + g]);
-      float L = 0.0f, O = 0.0f;
+      float L = 0.0f;
+      float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float f = exp2_ftz(sm_m[w * 8 + g] - M);  // 0 for a warp that saw no token
+        const float4 v = *reinterpret_cast<const float4 *>(sm_o + (w * 8 + g) * S::OUT_STRIDE + col);
         L = fmaf(sm_l[w * 8 + g], f, L);
-        O = fmaf(sm_o[(w * 8 + g) * S::OUT_STRIDE + col], f, O);
+        O.x = fmaf(v.x, f, O.x), O.y = fmaf(v.y, f, O.y), O.z = fmaf(v.z, f, O.z), O.w = fmaf(v.w, f, O.w);
       }
       if (c.np == 1) {
-        store_elem(static_cast<IO *>(p.out) + (row0 + g) * D + col, O / L);
+        IO *to = static_cast<IO *>(p.out) + (row0 + g) * D + col;
+        *reinterpret_cast<decltype(raw4(to)) *>(to) = narrow4(make_float4(O.x / L, O.y / L, O.z / L, O.w / L), IO());
       } else {
         const size_t slot = (row0 + g) * p.num_partitions + c.part;
-        p.ws_acc[slot * D + col] = O;
+        *reinterpret_cast<float4 *>(p.ws_acc + slot * D + col) = O;
         if (col == 0) {
           p.ws_m[slot] = M;
           p.ws_l[slot] = L;

@@ -50,6 +50,21 @@ struct SeqRows {
   int np;        // partitions with tokens
 };
 
+// Sequence s's context length c, n of its tokens being queries: clamped to the
+// table and the partitions, 0 where c is below n; either is recorded when asked.
+__device__ __forceinline__ int checked_context(const RowsParams &p, int s, int n, int c, bool record) {
+  const int cap = int(min(int64_t(p.max_blocks) * p.block_size,
+                          int64_t(p.num_partitions) * p.partition));
+  if (c >= n && c <= cap) return c;
+  if (record) record_error(&g_rows_error, PK_DEVERR_CONTEXT, s);
+  return c < n || cap < n ? 0 : cap;
+}
+
+// Partitions with tokens of a context of c.
+__device__ __forceinline__ int partitions_of(const RowsParams &p, int c) {
+  return int((int64_t(c) + p.partition - 1) / p.partition);
+}
+
 // Sequence s's rows and length, checked; bad entries are recorded when asked.
 __device__ __forceinline__ SeqRows seq_rows(const RowsParams &p, int s, bool record) {
   SeqRows r{s, 1, 0, 0};
@@ -64,31 +79,22 @@ __device__ __forceinline__ SeqRows seq_rows(const RowsParams &p, int s, bool rec
     r.n = b - a;
     if (r.n == 0) return r;
   }
-  int c = __ldg(p.ctx_lens + s);
-  const int cap = int(min(int64_t(p.max_blocks) * p.block_size,
-                          int64_t(p.num_partitions) * p.partition));
-  if (c < r.n || c > cap) {
-    if (record) record_error(&g_rows_error, PK_DEVERR_CONTEXT, s);
-    c = c < r.n || cap < r.n ? 0 : cap;
-  }
-  r.ctx = c;
-  r.np = int((int64_t(c) + p.partition - 1) / p.partition);
+  r.ctx = checked_context(p, s, r.n, __ldg(p.ctx_lens + s), record);
+  r.np = partitions_of(p, r.ctx);
   return r;
 }
 
 // The (sequence, partition) of work y: an item of the list, or the grid's.
+__device__ __forceinline__ bool checked_item(const RowsParams &p, int y, int s, int part, bool record) {
+  if (s >= 0 && s < p.num_seqs && part >= 0 && part < p.num_partitions) return true;
+  if (record) record_error(&g_rows_error, PK_DEVERR_ORDER, y);
+  return false;
+}
 __device__ __forceinline__ bool work_item(const RowsParams &p, int y, int z, bool record,
                                           int &s, int &part) {
-  s = y;
-  part = z;
-  if (!p.items) return true;
-  s = __ldg(p.items + 2 * y);
-  part = __ldg(p.items + 2 * y + 1);
-  if (s < 0 || s >= p.num_seqs || part < 0 || part >= p.num_partitions) {
-    if (record) record_error(&g_rows_error, PK_DEVERR_ORDER, y);
-    return false;
-  }
-  return true;
+  s = p.items ? __ldg(p.items + 2 * y) : y;
+  part = p.items ? __ldg(p.items + 2 * y + 1) : z;
+  return checked_item(p, y, s, part, record);
 }
 
 // Which drafted tokens row q0 + i of a sequence of n sees, one bit each.

@@ -162,6 +162,12 @@ __device__ __forceinline__ void try_cancel(uint32_t answer, uint32_t bar) {
       "r"(bar)
       : "memory");
 }
+// Orders this thread's read of an answer before the next answer, which comes
+// through the async proxy. fence_proxy_async would also wait for the thread's
+// copies under way.
+__device__ __forceinline__ void fence_answer_read() {
+  asm volatile("fence.proxy.async::generic.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
 // The first CTA's x in the answer, or -1: none was left (and none may be asked for).
 __device__ __forceinline__ int cancelled_cta(uint32_t answer) {
   uint32_t yes, x;

@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!warp_wait(u_answer, asked & 1, ok)) break;
       ++asked;
       u = cancelled_cta(smem_addr(&answer));
-      fence_proxy_async();  // the answer has been read before the next one is asked for
+      fence_answer_read();
       __syncwarp();
     }
     Unit end;
