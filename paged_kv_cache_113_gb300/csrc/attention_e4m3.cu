@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 3)
             const uint32_t a = vbase + (t0 + nvalid + i / (D / 16)) * D + (i % (D / 16)) * 16;
             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
           }
-          fence_proxy_async();  // a later unit's copies go to the same rows
+          fence_proxy_async_shared();  // a later unit's copies go to the same rows
           __syncwarp();
         }
         uint32_t e0, e1;  // exponents of the lane's tokens: K in the low byte, V above

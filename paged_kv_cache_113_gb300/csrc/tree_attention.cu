@@ -33,17 +33,18 @@
 // started, so that short contexts keep memory busy too and uneven ones even out.
 //
 // Measured (heads of 128, blocks of 16): 8 sequences of 32 768 tokens with 32
-// drafts, 64 = 8 x 8 heads (256 rows a KV head) 346 us, 795 TFLOP/s of the
-// formula's work, 1.19 PFLOP/s with the second half of the weights; with 16 drafts
-// or fewer (one unit of 128 rows reads all) 178 to 198 us, 5.4 to 6.0 TB/s. 256
-// sequences of some 500 (64 to 4608) tokens with 16 drafts, 32 = 4 x 8 heads, 113
-// to 122 us, 4.4 to 4.7 TB/s (64 to 69% of a copy). There units dealt out at launch
-// took 149 us against 115 by launch control. One product warp in place of two: equal.
-// Scores of 64 tokens at a time: 343 us against 334 (the long case). The wait on a
-// barrier that has long completed costs a product warp 200 cycles, so the fewer
-// steps, the better; what bounds it now is the softmax's path from scores read to
-// weights written, which the other CTA's products cover but in part (tensor pipe
-// 38 to 44% busy, issue slots 25 to 30%).
+// drafts, 64 = 8 x 8 heads (256 rows a KV head) 340 us, 805 TFLOP/s of the
+// formula's work, 1.2 PFLOP/s with the second half of the weights; with 1 to 16
+// drafts (one unit of 128 rows reads all) 173 to 193 us, 5.6 to 6.2 TB/s. 256
+// sequences of some 500 (64 to 4608) tokens with 16 drafts, 32 = 4 x 8 heads, 98 to
+// 101 us, 5.3 TB/s (78% of a copy). There units dealt out at launch took 149 us
+// against 115 by launch control; then 100 by shortening what a unit's end costs its
+// softmax warps (a timeline: 2700 cycles to ask for the next unit's queries, 1700 to
+// look for values that are not finite, and fences that waited for the last unit's
+// stores). One product warp in place of two: equal. Scores of 64 tokens at a time:
+// 343 us against 334 (the long case). What bounds it now: long, the chain of a pair,
+// 5200 cycles of which each softmax is 1330 and each wait for scores 970, with two
+// CTAs to overlap (tensor pipe 44% busy); short, beginnings and ends of units.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -347,19 +348,25 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float sl = fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);
     bool ok = true;
     auto wait = [&](uint32_t b, uint32_t parity) { return warp_wait(b, parity, ok); };
-    // A unit's queries into shared memory, rows past the last as zeros.
+    // A unit's queries into shared memory. Rows past its last keep what was there:
+    // no row's result depends on another's query.
+    const uint32_t inv_g = (65536 + G - 1) / G;  // x / G = x inv_g >> 16 for x < 512
     auto load_q = [&](const Unit &c) {
-      for (int i = r; i < kRows * (D / 8); i += 128) {
-        const int row = i / (D / 8), ch = i % (D / 8);
-        const __nv_bfloat16 *src =
-            static_cast<const __nv_bfloat16 *>(p.q) + q_row(c.q0, c.r0 + min(row, c.rows - 1), c.kvh) + ch * 8;
-        cp_async16(q_sm + (ch >> 3) * S::Q_SLAB + row * 128 + (((ch & 7) ^ (row & 7)) << 4), src,
-                   row < c.rows ? 16 : 0);
+      constexpr int CH = D / 8, STEP = 128 / CH;  // chunks of a row, rows at once
+      const int ch = r % CH;
+      const __nv_bfloat16 *src =
+          static_cast<const __nv_bfloat16 *>(p.q) + (size_t(c.q0) * p.num_q_heads + c.kvh * G) * D + ch * 8;
+      const uint32_t dst = q_sm + (ch >> 3) * S::Q_SLAB;
+#pragma unroll 4
+      for (int row = r / CH; row < c.rows; row += STEP) {
+        const uint32_t x = c.r0 + row, tok = x * inv_g >> 16;
+        cp_async16(dst + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                   src + size_t(tok * (p.num_q_heads - G) + x) * D, 16);
       }
     };
     auto q_landed = [&] {
       cp_async_wait();
-      fence_proxy_async();
+      fence_proxy_async_shared();
       mbar_arrive(q_ready);
     };
     bool loaded = false;  // the unit's queries were loaded under the one before
@@ -376,10 +383,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       loaded = false;
       const bool busy = warp * 32 < c.rows;  // this warp has rows
+      const int unit = i;
       const int nt = c.nt, start = c.start;
       const int lim = min(c.ctx - c.n, c.end);  // tokens before it are seen by every row
-      // The drafts that this thread's row sees.
-      auto row_mask = [&] { return r < c.rows ? draft_mask(p, c.q0, (c.r0 + r) / G, c.n) : 0; };
+      // The drafts that this thread's row sees, loaded ahead of the tiles that need it.
+      const uint64_t mask = r < c.rows ? draft_mask(p, c.q0, (c.r0 + r) / G, c.n) : 0;
       float ref = -INFINITY, l = 0.0f;  // the exponent's reference (scaled scores), the sum
       for (int j = 0; j < nt; ++j) {
         const int t0 = start + j * kTile, h = j & 1;
@@ -392,13 +400,6 @@ __global__ void __launch_bounds__(kThreads, 2)
           tmem_load32(t_s(h) + lane_base, x[0]);
           tmem_load32(t_s(h) + lane_base + 32, x[1]);
         }
-        if (j == nt - 1) {
-          // The unit's last scores are there, so its queries are done with: the
-          // next unit's, if it is known already, come in under this tile's softmax.
-          loaded = __all_sync(0xffffffffu, mbar_test(u_full(i + 1), u_phase(i + 1))) &&
-                   units[(i + 1) % kUnits].s >= 0;
-          if (loaded) load_q(units[(i + 1) % kUnits]);
-        }
         if (careful) {
           // Drafts, or the partition's end: what a row does not see is masked, the
           // values past the end are zeroed, and so is what is not finite in the
@@ -407,42 +408,72 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (!wait(v_full(h), phase)) break;
           const uint32_t vb = v_sm + (h ? S::V_BYTES : 0);
           const int first = max(0, lim - t0), valid = min(kTile, c.end - t0);
-          for (int k = first * (D / 8) + r; k < kTile * (D / 8); k += 128) {
-            const int row = k / (D / 8), ch = k % (D / 8);
-            const uint32_t a = vb + (ch >> 3) * S::V_SLAB + row * 128 + (ch & 7) * 16;
-            uint32_t w[4] = {0, 0, 0, 0};
-            bool dirty = row >= valid;
-            if (!dirty) {
-              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                           : "r"(a));
+          // Four rows' chunks of 16 bytes at once; they are looked at word by word only
+          // if a carry into a half's sign shows an exponent of all ones.
+          constexpr int STEP = 128 / (D / 8);  // rows that the threads cover at once
+          const uint32_t a = vb + (r % (D / 8) >> 3) * S::V_SLAB + r / (D / 8) * 128 + (r & 7) * 16;
+          bool wrote = valid < kTile;
+#pragma unroll 1
+          for (int k0 = first / (4 * STEP) * (4 * STEP); k0 < kTile; k0 += 4 * STEP) {
+            uint32_t w[4][4], odd = 0;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u, dirty = true;
-                if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu, dirty = true;
-              }
-              if (dirty) poisoned[i & 1] = 1;
+            for (int i = 0; i < 4; ++i) {
+              const int row = k0 + i * STEP + r / (D / 8);
+              w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0;
+              if (row >= first && row < valid)
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                             : "r"(a + (k0 + i * STEP) * 128));
             }
-            if (dirty)
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                           "r"(w[3])
-                           : "memory");
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (k0 + i * STEP + r / (D / 8) >= valid)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a + (k0 + i * STEP) * 128), "r"(0)
+                             : "memory");
+#pragma unroll
+              for (int e = 0; e < 4; ++e) odd |= (w[i][e] & 0x7f807f80u) + 0x00800080u;
+            }
+            if (odd & 0x80008000u) {
+              poisoned[unit & 1] = 1;
+              wrote = true;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if ((w[i][e] & 0x7f80u) == 0x7f80u) w[i][e] &= 0xffff0000u;
+                  if ((w[i][e] & 0x7f800000u) == 0x7f800000u) w[i][e] &= 0xffffu;
+                }
+                const int row = k0 + i * STEP + r / (D / 8);
+                if (row >= first && row < valid)
+                  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a + (k0 + i * STEP) * 128),
+                               "r"(w[i][0]), "r"(w[i][1]), "r"(w[i][2]), "r"(w[i][3])
+                               : "memory");
+              }
+            }
           }
-          fence_proxy_async();
+          if (__any_sync(0xffffffffu, wrote)) fence_proxy_async_shared();
           __syncwarp();
+        }
+        if (j == nt - 1) {
+          // The unit's last scores are there, so its queries are done with: the
+          // next unit's, if it is known already, come in under this tile's softmax
+          // (after the fence above, which would wait for them).
+          loaded = __all_sync(0xffffffffu, mbar_test(u_full(i + 1), u_phase(i + 1))) &&
+                   units[(i + 1) % kUnits].s >= 0;
+          if (loaded) load_q(units[(i + 1) % kUnits]);
         }
         if (busy) {
           tmem_wait_load(x[0]);
           tmem_wait_load(x[1]);
           if (careful) {
-            const uint64_t see = see64(row_mask(), c.ctx - c.n, t0);
+            const int live = c.end - t0;  // more than 0
+            const uint64_t see = see64(mask, c.ctx - c.n, t0) & (live < 64 ? (1ull << live) - 1 : ~0ull);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const uint32_t w = uint32_t(see >> (32 * e));
-              const int live = c.end - t0 - 32 * e;
 #pragma unroll
               for (int k = 0; k < 32; ++k)
-                if (!((w >> k) & 1) || k >= live) x[e][k] = 0xff800000u;  // -inf
+                if (!(w & (1u << k))) x[e][k] = 0xff800000u;  // -inf
             }
           }
           float mx;
@@ -538,6 +569,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       // each go through shared memory, so that four lanes write a row's together.
       const uint32_t stage = v_sm + 2 * S::V_BYTES + warp * S::STAGE_BYTES;
       const size_t to = split ? slot * D * 4 : at * 2;  // byte offset of the row
+      size_t dst[4];  // where the lane's quarters of rows go
+#pragma unroll
+      for (int e = 0; e < 4; ++e) dst[e] = __shfl_sync(0xffffffffu, to, 8 * e + lane / 4) + (lane & 3) * 16;
+      char *const base = split ? reinterpret_cast<char *>(p.ws_acc) : static_cast<char *>(p.out);
       auto put = [&](const uint32_t (&w)[16], int byte) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -546,18 +581,17 @@ __global__ void __launch_bounds__(kThreads, 2)
                        "r"(w[4 * e]), "r"(w[4 * e + 1]), "r"(w[4 * e + 2]), "r"(w[4 * e + 3])
                        : "memory");
         __syncwarp();
+        uint4 v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int row = 8 * e + lane / 4, ch = lane & 3;
-          const size_t dst = __shfl_sync(0xffffffffu, to, row);
-          uint4 v;
+          const int row = 8 * e + lane / 4;
           asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                       : "r"(stage + row * 64 + ((ch ^ ((row >> 1) & 3)) << 4)));
-          if (warp * 32 + row < c.rows)
-            *reinterpret_cast<uint4 *>((split ? reinterpret_cast<char *>(p.ws_acc) : static_cast<char *>(p.out)) +
-                                       dst + byte + ch * 16) = v;
+                       : "=r"(v[e].x), "=r"(v[e].y), "=r"(v[e].z), "=r"(v[e].w)
+                       : "r"(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4)));
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (warp * 32 + 8 * e + lane / 4 < c.rows) *reinterpret_cast<uint4 *>(base + dst[e] + byte) = v[e];
         __syncwarp();
       };
       float odd = 0.0f;  // NaN once an element is not finite
@@ -625,7 +659,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       if (fix && mine) {  // what is not finite in the values of the drafts that the row sees
-        const uint64_t mask = row_mask();
         const int base = c.ctx - c.n;
         for (int k = max(base, c.start); k < c.end; ++k) {
           const int phys = __ldg(p.tables + size_t(c.s) * p.max_blocks + k / BS);
