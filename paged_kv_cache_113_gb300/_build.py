@@ -23,7 +23,8 @@ LIB_PATH = os.path.join(PKG, "libpagedkv.so")
 SOURCES = ["attention.cu", "attention_e4m3.cu", "tree_attention.cu", "cache_ops.cu", "cache_e4m3.cu",
            "qk_norm_rope.cu", "block_manager.cpp", "decode_step.cpp", "allocator_sim.cpp"]
 HEADERS = [os.path.join(CSRC, "pk_device.cuh"), os.path.join(CSRC, "attn_rows.cuh"),
-           os.path.join(CSRC, "pk_tma_host.h"), os.path.join(CSRC, "pk_tcgen05.cuh"), os.path.join(INCLUDE, "pagedkv.h")]
+           os.path.join(CSRC, "pk_tma_host.h"), os.path.join(CSRC, "pk_tcgen05.cuh"),
+           os.path.join(INCLUDE, "pagedkv.h")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 _lock = threading.Lock()

@@ -12,8 +12,8 @@
 // pairs of 64-token tiles:
 //   producer warp   TMA loads of each block's K (a pair at a time) and V (a tile
 //                   at a time);
-//   score warp      S = Q K^T of a pair (128 x 128) as soon as the softmax has
-//                   read the last; a 128 x 64 product costs as much time;
+//   score warp      S = Q K^T of a pair (128 x 128) as soon as the last pair's
+//                   products have ended; a 128 x 64 product costs as much time;
 //   value warp      O += P V per tile, P read from tensor memory, under the
 //                   softmax of the next tile;
 //   softmax warps   a thread owns a row: reads its 64 scores, masks them, keeps
@@ -767,7 +767,7 @@ pk_status launch_tree_d(const RowsParams &p, const pk_cache_desc &d, cudaStream_
 }
 
 // ---------------------------------------------------------------------------
-// fp32 pools, and bf16 ones of other block sizes (attn_split_kernel).
+// fp32 pools, bf16 ones of other block sizes, and few rows of bf16 (attn_split_kernel).
 //
 // Products on the tensor cores (mma.sync m16n8k16 bf16): each fp32 factor is the
 // sum of three bf16 parts, x = x0 + x1 + x2 to 2^-25, and of the nine partial
@@ -1149,8 +1149,15 @@ pk_status launch_split(RowsParams p, cudaStream_t stream) {
   return cudaGetLastError() == cudaSuccess ? PK_OK : PK_ERR_CUDA;
 }
 
-bool tcgen05_path(const pk_cache_desc &d) {
-  return d.dtype == PK_BF16 && (d.block_size == 8 || d.block_size == 16 || d.block_size == 32);
+// Whether `rows` rows of a (sequence, KV head) go to attn_tree_kernel. Up to eight
+// rows of 64 values are too little for its 128 lanes and its chain of a pair, and
+// attn_split_kernel, with more CTAs an SM, reads faster (us, tcgen05 and split):
+// 256 x 500 tokens, 4 x 8 heads, one draft 76 and 62, two 76 and 66, four (16 rows)
+// 76 and 91; 8 x 32 768 tokens 118 and 103, 118 and 105, 119 and 115. With rows of
+// 128 values it does not: 99 and 117, 172 and 234 with one draft.
+bool tcgen05_path(const pk_cache_desc &d, int64_t rows) {
+  return d.dtype == PK_BF16 && (d.block_size == 8 || d.block_size == 16 || d.block_size == 32) &&
+         (d.head_dim == 128 || rows > 8);
 }
 // Rows per CTA of attn_split_kernel: the fewest that hold a sequence's, at most 32.
 int split_rows(int rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : 32); }
@@ -1158,7 +1165,7 @@ int split_rows(int rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : 32); }
 template <typename T, int D>
 pk_status run(const RowsParams &p, const pk_cache_desc &d, cudaStream_t stream) {
   pk_status st = PK_ERR_UNSUPPORTED;
-  if (sizeof(T) == 2 && tcgen05_path(d)) {
+  if (sizeof(T) == 2 && tcgen05_path(d, p.max_draft * p.group)) {
     st = launch_tree_d<D>(p, d, stream);
   } else {
     switch (split_rows(p.max_draft * p.group)) {
@@ -1197,7 +1204,7 @@ int32_t tree_partition(const int32_t *context_lens, int32_t num_seqs, int32_t lo
                        int32_t max_draft_len, int32_t num_q_heads, const pk_cache_desc &d) {
   if (longest <= 1024) return 0;
   const int64_t rows = int64_t(max_draft_len) * (num_q_heads / d.num_kv_heads);
-  const int unit_rows = tcgen05_path(d) ? kRows : split_rows(int(rows));
+  const int unit_rows = tcgen05_path(d, rows) ? kRows : split_rows(int(rows));
   const int64_t per_item = d.num_kv_heads * ((rows + unit_rows - 1) / unit_rows);
   const int64_t slots = 2 * sm_count();
   const double merge = double(max_draft_len) * num_q_heads * (d.head_dim + 2) * 8 / 6e12 / 22e-9;

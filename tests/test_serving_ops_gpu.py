@@ -302,7 +302,8 @@ RHO_E4M3 = {torch.bfloat16: 2.0 ** -11, torch.float32: 2.0 ** -20}
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("hq,hk,d,B", [(8, 8, 64, 16), (8, 1, 128, 16), (6, 2, 128, 8), (4, 1, 64, 32), (10, 2, 128, 32),
+@pytest.mark.parametrize("hq,hk,d,B", [(8, 8, 64, 16), (8, 1, 128, 16), (6, 2, 128, 8), (4, 1, 64, 32),
+                                       (10, 2, 128, 32),
                                        (7, 1, 64, 8), (8, 8, 128, 16)])
 def test_decode_e4m3(dtype, hq, hk, d, B):
     dt = DTYPES[dtype]
@@ -460,6 +461,28 @@ def test_tree_attention(dtype, hq, hk, d, B, kind):
         pk.pk_paged_attention_tree(out, q, k, v, i32(tables), i32(lens), i32(ofs), scale, 64, 200, tree_mask=mt,
                                    partition_size=part, workspace=ws, work_items=items)
         check_tree(out, q, k, v, tables, lens, scale, ofs, masks, d, dt)
+
+
+@pytest.mark.parametrize("hq,hk,d,B,drafts", [(8, 8, 64, 16, 8), (4, 1, 64, 8, 2), (6, 2, 64, 32, 2), (2, 2, 64, 16, 9),
+                                              (8, 1, 128, 16, 1), (4, 4, 128, 8, 8)])
+def test_tree_few_rows(hq, hk, d, B, drafts):
+    """bf16, one to nine rows of a KV head, on both sides of the rule that picks the kernel."""
+    rng = np.random.default_rng(hq + 10 * d + drafts)
+    counts = rng.integers(0, drafts + 1, 9).astype(np.int32)
+    counts[3] = drafts
+    lens = np.maximum(counts, [1, 700, 64, 130, 9, 65, 1031, 16, 17]).astype(np.int32)
+    tables, k, v, ofs, masks, q, mt = tree_case(rng, counts, lens, B, hq, hk, d, torch.bfloat16, "any")
+    desc = pk.cache_desc(k)
+    for part in (0, 256, -1):
+        part, it = pk.pk_tree_plan(lens, drafts, hq, desc, part)
+        out = torch.full_like(q, 5.0)
+        ws = torch.full((max(16, pk.pk_tree_workspace_size(len(q), hq, 1031, part, desc)),), 255, dtype=torch.uint8,
+                        device=DEV)
+        pk.pk_paged_attention_tree(out, q, k, v, i32(tables), i32(lens), i32(ofs), d ** -0.5, drafts, 1031,
+                                   tree_mask=mt, partition_size=part, workspace=ws,
+                                   work_items=torch.from_numpy(it).to(DEV))
+        check_tree(out, q, k, v, tables, lens, d ** -0.5, ofs, masks, d, torch.bfloat16)
+    assert pk.pk_get_device_error() == (0, 0)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
