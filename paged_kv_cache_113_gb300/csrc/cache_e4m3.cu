@@ -12,13 +12,16 @@
 // its input whatever computes it, every value is exact in bf16, and values that
 // are written again stay what they are.
 //
-// Data movement bounds all three kernels. A lane takes 16 elements of K and the
-// same 16 of V, loads both before it converts either (a row's magnitude is a
-// maximum over the bits, two bf16 at a time) and stores 16 codes at once. 16 000
-// tokens of 8 heads of 128 (bf16) are written in 18.6 us, 5.3 TB/s; widening each
-// value to fp32 first and testing it for infinity took 23.9, bounded by
-// instructions. 32 768 such tokens are read back in 37.4 us, 5.4 TB/s. Up to some
-// hundred tokens a call is bounded by its launch.
+// Data movement bounds all three kernels. A row of K and the same row of V are
+// loaded before either is converted. Written, a lane has 16 elements of each: the
+// row's magnitude is a maximum over the bits, two bf16 at a time, and 16 codes are
+// stored at once. 16 000 tokens of 8 heads of 128 (bf16) take 18.6 us, 5.3 TB/s, and
+// 32 768 take 31.4, 6.4 TB/s; widening each value first and testing it for infinity
+// took 23.9 for the former, bounded by instructions, and eight elements a lane 22.5.
+// Read back, a lane has the elements of 16 bytes of the result, of two rows, so that
+// a warp's stores are whole lines: 32 768 such tokens take 34.8 us, 5.8 TB/s, as fp32
+// 56; 16 codes a lane took 37.4 and 74, one row a lane 38.5 and 64, four 36.9 and 56.
+// Up to some hundred tokens a call is bounded by its launch.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -43,20 +46,19 @@ struct RowParams {
   int32_t num_tokens, hk, d, block_size;
 };
 
-// LANES lanes of 16 elements hold a head's row of K and its row of V, both of
+// LANES lanes of E elements hold a head's row of K and its row of V, both of
 // which are loaded before either is converted.
 struct Place {
   int64_t tok, slot, exp;  // exp: index of the pair of exponents
   int h, e0;
 };
 
-template <int LANES>
-__device__ __forceinline__ bool place_of(const RowParams &p, Place &at) {
-  const uint32_t unit = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
+template <int LANES, int E>
+__device__ __forceinline__ bool place_of(const RowParams &p, uint32_t unit, Place &at) {
   const uint32_t t = unit / uint32_t(p.hk);
   at.tok = t;
   at.h = int(unit - t * p.hk);
-  at.e0 = (threadIdx.x % LANES) * 16;
+  at.e0 = (threadIdx.x % LANES) * E;
   if (at.tok >= p.num_tokens) return false;
   at.slot = __ldg(p.slots + at.tok);
   if (at.slot >= p.num_slots) {
@@ -162,7 +164,7 @@ __device__ __forceinline__ int quantize16(const Row &row, uint4 &codes) {
 template <typename T, int LANES>
 __global__ void __launch_bounds__(256) quantize_kernel(RowParams p) {
   Place at;
-  const bool on = place_of<LANES>(p, at);
+  const bool on = place_of<LANES, 16>(p, blockIdx.x * (256 / LANES) + threadIdx.x / LANES, at);
   typename Row16Of<T>::Type k{}, v{};
   if (on) {
     k.load(static_cast<const T *>(p.k) + at.tok * p.k_stride + int64_t(at.h) * p.d + at.e0);
@@ -178,35 +180,51 @@ __global__ void __launch_bounds__(256) quantize_kernel(RowParams p) {
     *reinterpret_cast<uint16_t *>(p.kv_exp + at.exp * 2) = uint16_t((ke + 127) | (ve + 127) << 8);
 }
 
-template <typename T>
-__device__ __forceinline__ void store_values(T *dst, const uint4 &c, uint32_t exp) {
+// Two codes as fp32 values.
+__device__ __forceinline__ float2 values_of(uint32_t pair, float s) {
+  const float2 f =
+      __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(pair & 0xffffu), __NV_E4M3)));
+  return make_float2(f.x * s, f.y * s);
+}
+__device__ __forceinline__ void store_values(float *dst, uint32_t c, uint32_t exp) {
   const float s = __uint_as_float(exp << 23);
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    float x[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t pair = w[2 * i + j / 2] >> (16 * (j & 1));
-      const float2 f = __half22float2(
-          __half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(pair & 0xffffu), __NV_E4M3)));
-      x[2 * j] = f.x * s;
-      x[2 * j + 1] = f.y * s;
-    }
-    pk::store8(dst + 8 * i, x);
-  }
+  const float2 a = values_of(c, s), b = values_of(c >> 16, s);
+  *reinterpret_cast<float4 *>(dst) = make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void store_values(__nv_bfloat16 *dst, const uint2 &c, uint32_t exp) {
+  const float s = __uint_as_float(exp << 23);
+  const float2 x[4] = {values_of(c.x, s), values_of(c.x >> 16, s), values_of(c.y, s), values_of(c.y >> 16, s)};
+  *reinterpret_cast<uint4 *>(dst) = make_uint4(pk::pack_bf16x2(x[0].x, x[0].y), pk::pack_bf16x2(x[1].x, x[1].y),
+                                               pk::pack_bf16x2(x[2].x, x[2].y), pk::pack_bf16x2(x[3].x, x[3].y));
 }
 
+constexpr int kGatherRows = 2;  // of a lane, all loaded before the first is stored
+
+// A lane writes 16 bytes of a row, so that a warp's stores are whole lines.
 template <typename T, int LANES>
 __global__ void __launch_bounds__(256) gather_kernel(RowParams p) {
-  Place at;
-  if (!place_of<LANES>(p, at)) return;
-  const int64_t from = (at.slot * p.hk + at.h) * p.d + at.e0, to = (at.tok * p.hk + at.h) * p.d + at.e0;
-  const uint4 k = __ldg(reinterpret_cast<const uint4 *>(p.k_cache + from));
-  const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p.v_cache + from));
-  const uint32_t e = __ldg(reinterpret_cast<const uint16_t *>(p.kv_exp + at.exp * 2));
-  store_values(static_cast<T *>(p.k_out) + to, k, e & 0xffu);
-  store_values(static_cast<T *>(p.v_out) + to, v, e >> 8);
+  constexpr int E = 16 / int(sizeof(T)), U = kGatherRows;
+  using Codes = typename std::conditional<E == 4, uint32_t, uint2>::type;
+  Place at[U];
+  bool on[U];
+  Codes k[U], v[U];
+  uint32_t e[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    on[u] = place_of<LANES, E>(p, (blockIdx.x * U + u) * (256 / LANES) + threadIdx.x / LANES, at[u]);
+    if (!on[u]) continue;
+    const int64_t from = (at[u].slot * p.hk + at[u].h) * p.d + at[u].e0;
+    k[u] = __ldg(reinterpret_cast<const Codes *>(p.k_cache + from));
+    v[u] = __ldg(reinterpret_cast<const Codes *>(p.v_cache + from));
+    e[u] = __ldg(reinterpret_cast<const uint16_t *>(p.kv_exp + at[u].exp * 2));
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (!on[u]) continue;
+    const int64_t to = (at[u].tok * p.hk + at[u].h) * p.d + at[u].e0;
+    store_values(static_cast<T *>(p.k_out) + to, k[u], e[u] & 0xffu);
+    store_values(static_cast<T *>(p.v_out) + to, v[u], e[u] >> 8);
+  }
 }
 
 // grid.x = pair, grid.y = 0 K codes / 1 V codes / 2 exponents, grid.z = chunk
@@ -245,20 +263,21 @@ pk_status check_desc_e4m3(const pk_cache_desc *d) {
   return PK_OK;
 }
 
-// Calls f with the lanes of a row (4, 8 or 16 of 16 elements) and its grid.
-template <typename F>
-pk_status by_lanes(const RowParams &p, F f) {
+// Calls f with the lanes that a row takes at E elements each, and with the grid for
+// `rows` rows a lane.
+template <int E, typename F>
+pk_status by_lanes(const RowParams &p, int rows, F f) {
   const int64_t units = int64_t(p.num_tokens) * p.hk;
   auto go = [&](auto c) {
     constexpr int L = decltype(c)::value;
-    const int64_t ctas = (units + 256 / L - 1) / (256 / L);
+    const int64_t per = 256 / L * rows, ctas = (units + per - 1) / per;
     if (units > INT32_MAX) return PK_ERR_UNSUPPORTED;
     f(c, unsigned(ctas));
     return cudaGetLastError() == cudaSuccess ? PK_OK : PK_ERR_CUDA;
   };
-  if (p.d <= 64) return go(std::integral_constant<int, 4>());
-  if (p.d <= 128) return go(std::integral_constant<int, 8>());
-  return go(std::integral_constant<int, 16>());
+  if (p.d <= 64) return go(std::integral_constant<int, 64 / E>());
+  if (p.d <= 128) return go(std::integral_constant<int, 128 / E>());
+  return go(std::integral_constant<int, 256 / E>());
 }
 
 }  // namespace
@@ -302,7 +321,7 @@ pk_status pk_reshape_and_cache_e4m3(const void *k, const void *v, pk_dtype src_d
   p.d = desc->head_dim;
   p.block_size = desc->block_size;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return by_lanes(p, [&](auto c, unsigned ctas) {
+  return by_lanes<16>(p, 1, [&](auto c, unsigned ctas) {
     constexpr int L = decltype(c)::value;
     if (src_dtype == PK_F32)
       quantize_kernel<float, L><<<ctas, 256, 0, s>>>(p);
@@ -337,12 +356,12 @@ pk_status pk_gather_cache_e4m3(void *k_out, void *v_out, pk_dtype out_dtype,
   p.d = desc->head_dim;
   p.block_size = desc->block_size;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return by_lanes(p, [&](auto c, unsigned ctas) {
-    constexpr int L = decltype(c)::value;
-    if (out_dtype == PK_F32)
-      gather_kernel<float, L><<<ctas, 256, 0, s>>>(p);
-    else
-      gather_kernel<__nv_bfloat16, L><<<ctas, 256, 0, s>>>(p);
+  if (out_dtype == PK_F32)
+    return by_lanes<4>(p, kGatherRows, [&](auto c, unsigned ctas) {
+      gather_kernel<float, decltype(c)::value><<<ctas, 256, 0, s>>>(p);
+    });
+  return by_lanes<8>(p, kGatherRows, [&](auto c, unsigned ctas) {
+    gather_kernel<__nv_bfloat16, decltype(c)::value><<<ctas, 256, 0, s>>>(p);
   });
 }
 

@@ -337,17 +337,6 @@ __device__ __forceinline__ float load_elem(const __nv_bfloat16 *p) { return __bf
 __device__ __forceinline__ void store_elem(float *p, float x) { *p = x; }
 __device__ __forceinline__ void store_elem(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
-// Eight fp32 values to consecutive elements (16-byte aligned) of either storage
-// type, rounded to nearest even.
-__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
-  reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
-  *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                             pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-}
-
 // Four consecutive elements as they are stored, and as fp32 values.
 __device__ __forceinline__ float4 raw4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 __device__ __forceinline__ uint2 raw4(const __nv_bfloat16 *p) { return *reinterpret_cast<const uint2 *>(p); }
