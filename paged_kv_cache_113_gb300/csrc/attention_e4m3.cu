@@ -525,8 +525,17 @@ __global__ void __launch_bounds__(kThreads, 3)
             uint32_t a0, a1, a2, a3;
             e4m3x4_to_f16x4(r[2 * h], a0, a2);
             e4m3x4_to_f16x4(r[2 * h + 1], a1, a3);
+            if (QW == 1) {
+              mma_f16_16816(o[k][h], a0, a1, a2, a3, b[0][0], b[0][1]);
+            } else {
+              // The tensor cores cut their fp32 sums off, always toward zero (2 10^-5 after
+              // 32 768 tokens): fp32 results add a tile's sum with a rounding.
+              float t4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int w = 0; w < QW; ++w) mma_f16_16816(o[k][h], a0, a1, a2, a3, b[w][0], b[w][1]);
+              for (int w = QW - 1; w >= 0; --w) mma_f16_16816(t4, a0, a1, a2, a3, b[w][0], b[w][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[k][h][e] += t4[e];
+            }
           }
         }
       }

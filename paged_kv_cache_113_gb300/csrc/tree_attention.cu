@@ -788,9 +788,10 @@ pk_status launch_tree_d(const RowsParams &p, const pk_cache_desc &d, cudaStream_
 // two products.
 //
 // Measured (fp32, 64 sequences of some 1000 tokens, 32 = 4 x 8 heads of 128): 16
-// drafts 404 us (652 with three tf32 products, 797 with fp32 FMAs), 4 drafts 148
+// drafts 431 us (404 with sums left to the tensor cores, whose error grew to 5 10^-5
+// at 32 768 tokens; 652 with three tf32 products, 797 with fp32 FMAs), 4 drafts 151
 // us (554 with FMAs), one draft 109 us: bounded by the splitting of K and V into
-// parts and the products' issue, not by memory (a quarter of its rate at 4).
+// parts and the products' issue, not by memory (half of its rate at 4 drafts).
 // ---------------------------------------------------------------------------
 template <typename T, int D, int NT>
 struct SplitShape {
@@ -822,16 +823,24 @@ __device__ __forceinline__ void bf16_parts(float x, float y, uint32_t (&w)[N]) {
   }
 }
 
-// D += A B over the parts of both, smallest products first.
+// D += A B over the parts of both, smallest products first. The tensor cores cut
+// their fp32 sums off instead of rounding them, always toward zero: over thousands of
+// tokens 10^-5 would be missing. So fp32 products are summed from zero, and the sum
+// is added to D with a rounding.
 template <int NA, int NB>
 __device__ __forceinline__ void mma_parts(float (&d)[4], const uint32_t (&a)[4][NA], const uint32_t (&b)[2][NB]) {
   constexpr int LAST = NA > NB ? NA : NB;
+  constexpr bool APART = NA > 1;
+  float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int order = LAST - 1; order >= 0; --order)
 #pragma unroll
     for (int i = 0; i <= order; ++i)
       if (i < NA && order - i < NB)
-        mma_bf16_16816(d, a[0][i], a[1][i], a[2][i], a[3][i], b[0][order - i], b[1][order - i]);
+        mma_bf16_16816(APART ? t : d, a[0][i], a[1][i], a[2][i], a[3][i], b[0][order - i], b[1][order - i]);
+  if (APART)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] += t[e];
 }
 
 template <typename T, int D, int NT>
@@ -925,7 +934,7 @@ __global__ void __launch_bounds__(128, 2) attn_split_kernel(RowsParams p) {
     float x[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.0f;
-#pragma unroll
+#pragma unroll 2  // all eight at once cost registers: 525 us for 431
     for (int c = 0; c < D / 16; ++c) {
       uint32_t a[4][NP];
       const float4 k0 = load4(reinterpret_cast<const T *>(kw + rw * S::K_PITCH) + 16 * c + 4 * qd);

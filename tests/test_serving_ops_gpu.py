@@ -816,6 +816,36 @@ def test_more_units_than_fit_and_sequences_without_work(dtype):
         check_attention(f64(out), want, terms, d, dt, RHO_E4M3[dt], live)
 
 
+def test_fp32_sums_have_no_bias():
+    """Long unsplit contexts, fp32: rounding errors have no side, so that their mean over thousands of
+    elements stays below 2^-20 of the values. (Each element is some 10^-6 off at most, in either
+    direction: 140 roundings of 2^-24 a warp, and those of the scores. Sums that are cut off toward
+    zero lose 10^-5.)"""
+    hq, hk, d, B, ctx = 8, 2, 128, 16, 9000
+    rng = np.random.default_rng(31)
+    lens = np.array([ctx, ctx - 7], np.int32)
+    tables, N = tables_for(rng, lens, B)
+    for kind in ("e4m3", "tree"):
+        k, v = rand(rng, (N, B, hk, d)), rand(rng, (N, B, hk, d))
+        v += 1.0                                     # sums that only grow
+        ofs = np.array([0, 12, 24], np.int32) if kind == "tree" else None
+        q = rand(rng, (24 if kind == "tree" else 2, hq, d))
+        out = torch.empty_like(q)
+        if kind == "e4m3":
+            kc, vc, ex = e4m3_pool(N, B, hk, d, 0, 127)
+            every = torch.arange(N * B, device=DEV)
+            pk.pk_reshape_and_cache_e4m3(k.view(-1, hk, d), v.view(-1, hk, d), every, kc, vc, ex)
+            pk.pk_gather_cache_e4m3(k.view(-1, hk, d), v.view(-1, hk, d), every, kc, vc, ex)
+            pk.pk_paged_attention_decode_e4m3(out, q, kc, vc, ex, i32(tables), i32(lens), d ** -0.5, ctx,
+                                              partition_size=0)
+        else:
+            pk.pk_paged_attention_tree(out, q, k, v, i32(tables), i32(lens), i32(ofs), d ** -0.5, 12, ctx)
+        want, _ = plain.tree_attention(f64(q), f64(k), f64(v), tables, lens, d ** -0.5, ofs)
+        got = f64(out)
+        assert abs((got * want).sum() / (want * want).sum() - 1.0) < 2.0 ** -20, kind
+    assert pk.pk_get_device_error() == (0, 0)
+
+
 def test_offsets_past_32_bits():
     """Blocks at the end of pools of more than 2^31 elements, and 2^32 bytes."""
     hq, hk, d, B = 4, 2, 128, 16
