@@ -119,6 +119,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ uint4 answer;
   __shared__ Unit units[kUnits];
   __shared__ uint32_t tmem_slot;
+  // The last unit, plus one, of either parity whose drafts' values were not all finite.
+  // Nothing is cleared: a unit's mark is written by its own softmax warps and read once
+  // all four are past its tiles (u_done), and the next unit but one, which writes the
+  // same word, is begun only after all four have read it.
   __shared__ int poisoned[2];
   auto bar = [&](int i) { return smem_addr(bars + i); };
   // Units i, pairs g and, as the last pair of a unit may be half, second halves f
@@ -434,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               for (int e = 0; e < 4; ++e) odd |= (w[i][e] & 0x7f807f80u) + 0x00800080u;
             }
             if (odd & 0x80008000u) {
-              poisoned[unit & 1] = 1;
+              poisoned[unit & 1] = unit + 1;
               wrote = true;
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
@@ -548,12 +552,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       if (!ok) break;
       if (loaded) q_landed();
-      // Every warp is past the tiles: what they found of `poisoned` is in, and
-      // the other flag, last read in the unit before, is free.
+      // Every warp is past the tiles: their marks are in.
       if (lane == 0) mbar_arrive(u_done);
       if (!wait(u_done, i & 1)) break;
-      const bool fix = poisoned[i & 1] != 0;
-      if (r == 0) poisoned[(i + 1) & 1] = 0;
+      const bool fix = poisoned[i & 1] == i + 1;
       if (!busy) {
         release();
         continue;
