@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         const size_t slot = (row0 + g) * p.num_partitions + c.part;
         *reinterpret_cast<float4 *>(p.ws_acc + slot * D + col) = O;
         if (col == 0) {
-          p.ws_m[slot] = M;
+          p.ws_m[slot] = merge_max(M, L);
           p.ws_l[slot] = L;
         }
       }

@@ -114,6 +114,14 @@ __device__ __forceinline__ uint64_t see64(uint64_t mask, int base, int t0) {
   return mask >> -cut;
 }
 
+// The m of a state as it is kept for a merge: maxima leave NaN out, sums do not.
+__device__ __forceinline__ float merge_max(float m, float l) { return l == l ? m : l; }
+
+// sum + x f for a state's factor f; with f 0 only what is not finite counts.
+__device__ __forceinline__ float merge_add(float sum, float x, float f) {
+  return f != 0.0f ? fmaf(x, f, sum) : (fabsf(x) <= 3.402823466e38f ? sum : sum + x);
+}
+
 // Four consecutive elements as fp32 values.
 template <typename T>
 __device__ __forceinline__ float4 load4(const T *p) {
@@ -121,7 +129,9 @@ __device__ __forceinline__ float4 load4(const T *p) {
 }
 // ---------------------------------------------------------------------------
 // Merge of split rows: M = max_q m_q, out = sum_q acc_q 2^(m_q - M) /
-// sum_q l_q 2^(m_q - M). A row (grid.y = sequence, so that it needs no search
+// sum_q l_q 2^(m_q - M). What is not finite survives it: a state whose sum is NaN
+// (a NaN score, which no maximum shows) has NaN for its m, so that its factor is
+// NaN, and an infinite or NaN acc counts even where its factor is 0. A row (grid.y = sequence, so that it needs no search
 // for its sequence) gets wpr warps, enough that a warp merges at most eight
 // partials, all loaded at once; the row's first warp joins the warps' states.
 // ---------------------------------------------------------------------------
@@ -159,22 +169,22 @@ __global__ void __launch_bounds__(256) rows_merge_kernel(RowsParams p, int wpr) 
     for (int u = 0; u < U; ++u) top = fmaxf(top, m[u]);
     const float ref = top == -INFINITY ? 0.0f : top, f = exp2f(M - ref);
     M = top;
-    L *= f;
+    L *= f;  // NaN stays
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) acc[e] = f == 0.0f ? 0.0f : acc[e] * f;
+    for (int e = 0; e < EPL; ++e) acc[e] = merge_add(0.0f, acc[e], f);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      if (q0 + u >= q_end) break;
       const float w = exp2f(m[u] - ref);
-      if (w == 0.0f) continue;  // nothing of this partition counts, whatever it holds
       L = fmaf(l[u], w, L);
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) acc[e] = fmaf(x[u][e], w, acc[e]);
+      for (int e = 0; e < EPL; ++e) acc[e] = merge_add(acc[e], x[u][e], w);
     }
   }
   if (wpr > 1) {
 #pragma unroll
     for (int e = 0; e < EPL; ++e) sm_acc[warp][lane * EPL + e] = acc[e];
-    if (lane == 0) sm_m[warp] = M, sm_l[warp] = L;
+    if (lane == 0) sm_m[warp] = merge_max(M, L), sm_l[warp] = L;
     __syncthreads();
     if (sub != 0) return;
     for (int w = 1; w < wpr; ++w) M = fmaxf(M, sm_m[warp + w]);
@@ -184,10 +194,9 @@ __global__ void __launch_bounds__(256) rows_merge_kernel(RowsParams p, int wpr) 
     for (int e = 0; e < EPL; ++e) acc[e] = 0.0f;
     for (int w = 0; w < wpr; ++w) {
       const float f = exp2f(sm_m[warp + w] - ref);
-      if (f == 0.0f) continue;
       L = fmaf(sm_l[warp + w], f, L);
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) acc[e] = fmaf(sm_acc[warp + w][lane * EPL + e], f, acc[e]);
+      for (int e = 0; e < EPL; ++e) acc[e] = merge_add(acc[e], sm_acc[warp + w][lane * EPL + e], f);
     }
   }
   if (!live) return;

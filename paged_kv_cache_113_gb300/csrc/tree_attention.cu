@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       if (mine && split) {
-        p.ws_m[slot] = ref;
+        p.ws_m[slot] = merge_max(ref, l);
         p.ws_l[slot] = l;
       }
       __syncwarp();
@@ -1098,7 +1098,7 @@ __global__ void __launch_bounds__(128, 2) attn_split_kernel(RowsParams p) {
       *reinterpret_cast<float2 *>(to + S::O_PITCH) = make_float2(o[k][n][1], o[k][n][3]);
     }
     if (rw == 0) {
-      sm_m[r] = m[n][0], sm_m[r + 1] = m[n][1];
+      sm_m[r] = merge_max(m[n][0], l[n][0]), sm_m[r + 1] = merge_max(m[n][1], l[n][1]);
       sm_l[r] = l[n][0], sm_l[r + 1] = l[n][1];
     }
   }
@@ -1113,9 +1113,8 @@ __global__ void __launch_bounds__(128, 2) attn_split_kernel(RowsParams p) {
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       const float f = exp2f(sm_m[w * R + r] - ref);  // 0 for a warp that saw no token
-      if (f == 0.0f) continue;
       L = fmaf(sm_l[w * R + r], f, L);
-      O = fmaf(sm_o[(w * R + r) * S::O_PITCH + c], f, O);
+      O = merge_add(O, sm_o[(w * R + r) * S::O_PITCH + c], f);
     }
     // A context value that is not finite gave NaN, by the product with a part of a
     // weight that is 0 or negative: the sum of what is not finite in its place.
@@ -1142,7 +1141,7 @@ __global__ void __launch_bounds__(128, 2) attn_split_kernel(RowsParams p) {
       const size_t to = q_row(r) / D * p.num_partitions + part;
       p.ws_acc[to * D + c] = O;
       if (c == 0) {
-        p.ws_m[to] = M;
+        p.ws_m[to] = merge_max(M, L);
         p.ws_l[to] = L;
       }
     } else {

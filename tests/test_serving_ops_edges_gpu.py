@@ -5,7 +5,9 @@ import numpy as np
 import pytest
 
 import paged_kv_cache_113_gb300 as pk
-from test_serving_ops_gpu import DEV, f64, i32, rand, tables_for
+from oracle import serving_ops as plain
+from test_serving_ops_gpu import (DEV, DTYPES, RHO_E4M3, RHO_TREE, check_attention, f64, fill_e4m3, i32, rand,
+                                  tables_for, tree_case, values_of)
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -35,6 +37,26 @@ def tree_call(q, k, v, tables, lens, ofs, drafts, longest, part=0, items=None, m
     return out
 
 
+def decode_call(q, kc, vc, ex, tables, lens, longest, part=0, items=None, scale=None):
+    """pk_paged_attention_decode_e4m3 with a poisoned workspace."""
+    out = torch.full_like(q, 5.0)
+    size = pk.pk_paged_attention_workspace_size(len(q), q.shape[1], longest, part, pk.cache_desc(kc))
+    ws = torch.full((max(16, size),), 255, dtype=torch.uint8, device=DEV)
+    pk.pk_paged_attention_decode_e4m3(out, q, kc, vc, ex, tables, lens, q.shape[2] ** -0.5 if scale is None else scale,
+                                      longest, partition_size=part, workspace=ws, work_items=items)
+    return out
+
+
+def check_like(got, want, terms, top, d, dtype, rho):
+    """NaN and infinities where ``want`` has them; the rest within the bound, a weighted mean of
+    values being at most the largest, ``top``."""
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    odd, live = np.isinf(want), np.isfinite(want)
+    assert np.array_equal(odd, np.isinf(got)) and (got[odd] == want[odd]).all()
+    wv, mag, cnt = np.full_like(want, top), np.abs(terms[1]), terms[2]
+    check_attention(np.where(live, got, 0.0), np.where(live, want, 0.0), (wv, mag, cnt), d, dtype, rho)
+
+
 def test_infinite_drafts_of_alternating_units():
     """Some 1600 units of one or two tiles, several to a CTA one after another, half of them with an
     infinite value in their first or last draft: the rows that see it are infinite in that column, and
@@ -60,3 +82,95 @@ def test_infinite_drafts_of_alternating_units():
             want[ofs[s] + at:ofs[s + 1], h, col] = val
     for _ in range(100):
         assert np.array_equal(f64(tree_call(q, k, v, *args)), want)
+
+
+# (dtype, heads, head_dim, block): drafts on tcgen05 (the first), and on the kernel of fp32 pools, of
+# other block sizes and of few rows of 64 values
+TREE_KERNELS = [("bf16", 8, 2, 128, 16), ("f32", 8, 2, 128, 16), ("bf16", 4, 2, 128, 5), ("bf16", 4, 2, 64, 16)]
+
+
+@pytest.mark.parametrize("dtype,hq,hk,d,B", TREE_KERNELS)
+@pytest.mark.parametrize("what", ["query", "key", "value"])
+def test_tree_nan_that_a_row_sees(dtype, hq, hk, d, B, what):
+    """A NaN query makes its row and head NaN and no other. A NaN key makes NaN what sees it, and a
+    NaN or infinite value its column, also where they are alone in a warp's share of the context or in
+    a partition, or have a weight that is 0 in 32 bits. Whole, split, and planned."""
+    dt, p64 = DTYPES[dtype], -(-64 // B) * B
+    rng = np.random.default_rng(17 + d + B)
+    lens = np.array([17, p64 + 1, 2 * p64 + 1, 9, 700, 130], np.int32)
+    counts = np.array([1, 2, 2, 1, 2, 0], np.int32)
+    tables, k, v, ofs, masks, q, mt = tree_case(rng, counts, lens, B, hq, hk, d, dt, "chain")
+    n, scale = int(ofs[-1]), d ** -0.5
+
+    def at(s, pos):
+        return int(tables[s][pos // B]), pos % B
+
+    # Sequence 4: some scores of its second half are above those of its first by hundreds, so that the
+    # first half's weights are 0 in 32 bits.
+    k[at(4, 600)] = k[at(4, 600)] * 0 + 30.0
+    q[int(ofs[4]):int(ofs[5])] = q[int(ofs[4]):int(ofs[5])].abs() + 1.0
+    kf, vf, qf = k.clone(), v.clone(), q.clone()
+    if what == "query":
+        q[0, 1], q[int(ofs[2]), hq - 1], q[int(ofs[4]) + 1, 0, 3] = float("nan"), float("nan"), float("nan")
+    elif what == "key":
+        k[at(0, 16)][1] = float("nan")               # a draft, alone in a warp's 16 tokens
+        k[at(1, p64)][0, 3] = float("nan")           # a draft, alone in the last partition
+        k[at(2, 2 * p64 - 1)][0] = float("nan")      # the last draft but one: alone in nothing, seen by both rows
+        k[at(3, 0)][1] = float("nan")                # context, with the draft in one tile
+    else:
+        for s, pos, col, val in ((0, 16, 2, "nan"), (1, p64, 5, "inf"), (2, 2 * p64, 6, "-inf"), (3, 0, 7, "nan"),
+                                 (4, 3, 8, "inf"), (4, 70, 9, "nan"), (4, 200, 10, "-inf"), (4, 16, 11, "inf")):
+            v[at(s, pos)][1, col] = float(val)
+    with np.errstate(invalid="ignore"):
+        want, _ = plain.tree_attention(f64(q), f64(k), f64(v), tables, lens, scale, ofs, masks)
+    _, terms = plain.tree_attention(f64(qf), f64(kf), f64(vf), tables, lens, scale, ofs, masks)
+    terms, top = tuple(t[:n] for t in terms), np.nanmax(np.abs(f64(vf)))
+    assert not np.isfinite(want[:n]).all() and np.isfinite(want[:n]).any()
+    for part, planned in ((0, False), (p64, False), (p64, True), (-1, True), (2 * p64, True)):
+        items = None
+        if planned:
+            part, it = pk.pk_tree_plan(lens, 2, hq, pk.cache_desc(k), part)
+            items = torch.from_numpy(it).to(DEV)
+        got = f64(tree_call(q, k, v, i32(tables), i32(lens), i32(ofs), 2, 700, part, items))
+        check_like(got[:n], want[:n], terms, top, d, dt, RHO_TREE[dt])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("what", ["query", "key", "value"])
+def test_decode_e4m3_nan(dtype, what):
+    """As above over the 8-bit cache, where infinities are the NaN code too."""
+    dt, hq, hk, d, B = DTYPES[dtype], 8, 2, 128, 16
+    rng = np.random.default_rng(18)
+    lens = np.array([1, 17, 65, 129, 700, 700, 64], np.int32)
+    S = len(lens)
+    tables, N = tables_for(rng, lens, B)
+    kc, vc, ex, (kv, vv) = fill_e4m3(rng, tables, lens, N, B, hk, d)
+    q = rand(rng, (S, hq, d), dt)
+    q[4] = q[4].abs() + 1.0
+    qf = q.clone()
+    first = int(tables[4][600 // B])
+    kc.view(torch.uint8)[first, 600 % B], ex[first, :, 600 % B, 0] = 0x78, 127   # keys of 256: scores of thousands
+    finite = values_of(kc, vc, ex)
+
+    def nan(codes, s, pos, h, col):
+        codes.view(torch.uint8)[int(tables[s][pos // B]), pos % B, h, col] = 0x7F
+
+    if what == "query":
+        q[0, 1], q[2, 7], q[5, 0, 3] = float("nan"), float("nan"), float("nan")
+    elif what == "key":
+        nan(kc, 0, 0, 0, 5), nan(kc, 1, 16, 1, 6), nan(kc, 2, 64, 0, 7), nan(kc, 3, 128, 1, 8), nan(kc, 5, 3, 0, 9)
+    else:
+        nan(vc, 0, 0, 0, 5), nan(vc, 1, 16, 1, 6), nan(vc, 2, 64, 0, 7), nan(vc, 3, 128, 1, 8)
+        nan(vc, 4, 3, 0, 9), nan(vc, 4, 100, 1, 10), nan(vc, 5, 699, 1, 11)
+    with np.errstate(invalid="ignore"):
+        want, _ = plain.tree_attention(f64(q), *values_of(kc, vc, ex), tables, lens, d ** -0.5)
+    _, terms = plain.tree_attention(f64(qf), *finite, tables, lens, d ** -0.5)
+    top = np.nanmax(np.abs(finite[1]))
+    assert np.isnan(want).any() and np.isfinite(want).any()
+    for part, planned in ((0, False), (64, False), (64, True), (-1, True), (128, True)):
+        items = None
+        if planned:
+            part, it = pk.pk_attention_plan(lens, hq, pk.cache_desc(kc), part)
+            items = torch.from_numpy(it).to(DEV)
+        got = f64(decode_call(q, kc, vc, ex, i32(tables), i32(lens), 700, part, items))
+        check_like(got, want, terms, top, d, dt, RHO_E4M3[dt])
