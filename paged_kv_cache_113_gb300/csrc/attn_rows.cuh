@@ -117,6 +117,12 @@ __device__ __forceinline__ uint64_t see64(uint64_t mask, int base, int t0) {
 // The m of a state as it is kept for a merge: maxima leave NaN out, sums do not.
 __device__ __forceinline__ float merge_max(float m, float l) { return l == l ? m : l; }
 
+// What a row's accumulator is divided by. A sum of 0 is a row that sees nothing (its
+// result is 0), or one that sees scores of -inf alone (NaN).
+__device__ __forceinline__ float denominator(float l, bool sees) {
+  return l != 0.0f ? l : (sees ? __uint_as_float(0x7fc00000u) : INFINITY);
+}
+
 // sum + x f for a state's factor f; with f 0 only what is not finite counts.
 __device__ __forceinline__ float merge_add(float sum, float x, float f) {
   return f != 0.0f ? fmaf(x, f, sum) : (fabsf(x) <= 3.402823466e38f ? sum : sum + x);
@@ -200,7 +206,7 @@ __global__ void __launch_bounds__(256) rows_merge_kernel(RowsParams p, int wpr) 
     }
   }
   if (!live) return;
-  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  const float inv = 1.0f / denominator(L, sr.ctx > sr.n || draft_mask(p, sr.q0, row / p.num_q_heads, sr.n) != 0);
 #pragma unroll
   for (int e = 0; e < EPL; ++e)
     store_elem(static_cast<IO *>(p.out) + at * D + lane * EPL + e, acc[e] * inv);

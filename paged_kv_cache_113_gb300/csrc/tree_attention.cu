@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const bool mine = r < c.rows;
       const size_t at = mine ? q_row(c.q0, c.r0 + r, c.kvh) : 0;
       const bool split = c.np > 1;
-      const float inv = split ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+      const float inv = split ? 1.0f : 1.0f / denominator(l, c.ctx > c.n || mask != 0);
       const size_t slot = at / D * p.num_partitions + c.part;
       // A lane has a row, but rows are 64 bytes or more apart in memory: 64 bytes of
       // each go through shared memory, so that four lanes write a row's together.
@@ -1145,7 +1145,7 @@ __global__ void __launch_bounds__(128, 2) attn_split_kernel(RowsParams p) {
         p.ws_l[to] = L;
       }
     } else {
-      store_elem(static_cast<T *>(p.out) + q_row(r) + c, L == 0.0f ? 0.0f : O / L);
+      store_elem(static_cast<T *>(p.out) + q_row(r) + c, O / denominator(L, base > 0 || masks[r] != 0));
     }
   }
 }

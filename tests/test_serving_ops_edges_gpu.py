@@ -174,3 +174,29 @@ def test_decode_e4m3_nan(dtype, what):
             items = torch.from_numpy(it).to(DEV)
         got = f64(decode_call(q, kc, vc, ex, i32(tables), i32(lens), 700, part, items))
         check_like(got, want, terms, top, d, dt, RHO_E4M3[dt])
+
+
+@pytest.mark.parametrize("dtype,hq,hk,d,B", TREE_KERNELS)
+def test_tree_rows_whose_scores_are_all_minus_infinity(dtype, hq, hk, d, B):
+    """exp(-inf - -inf) is NaN in the formula; a row that sees nothing stays 0, and a row of one more
+    token has that token's value."""
+    dt = DTYPES[dtype]
+    rng = np.random.default_rng(19)
+    lens, counts = np.array([4, 3, 90], np.int32), np.array([4, 2, 2], np.int32)
+    tables, k, v, ofs, _, q, _ = tree_case(rng, counts, lens, B, hq, hk, d, dt, "chain", pad=0)
+    q = q.abs() + 0.5
+    masks = [0b0, 0b1, 0b11, 0b100, 0, 1, 0, 3]       # per sequence: 4, 2, 2 drafts
+    for s, pos in ((0, 0), (0, 1), (1, 0), (1, 1)):
+        k[int(tables[s][pos // B]), pos % B] = -float("inf")
+    for pos in range(88):                             # the whole context of the last sequence
+        k[int(tables[2][pos // B]), pos % B, 1] = -float("inf")
+    with np.errstate(invalid="ignore"):
+        want, _ = plain.tree_attention(f64(q), f64(k), f64(v), tables, lens, d ** -0.5, ofs, masks)
+    assert np.isnan(want[[1, 2, 4, 5]]).all() and (want[0] == 0).all() and np.isfinite(want[[3, 7]]).all()
+    assert np.isnan(want[6, hq // hk:]).all()
+    words = torch.tensor(masks, dtype=torch.int64, device=DEV)
+    p32 = -(-32 // B) * B
+    for part in (0, p32):
+        got = f64(tree_call(q, k, v, i32(tables), i32(lens), i32(ofs), 4, 90, part, masks=words))
+        assert np.array_equal(np.isnan(got), np.isnan(want)) and (got[0] == 0).all()
+        assert np.array_equal(got[3], want[3])        # one token, exact
