@@ -159,6 +159,8 @@ __global__ void __launch_bounds__(256) rows_merge_kernel(RowsParams p, int wpr) 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const size_t q = at * p.num_partitions + min(q0 + u, q_end - 1);
+      // Past the end the last one again, at a factor of 0: what is not finite in it
+      // counts already.
       m[u] = q0 + u < q_end ? __ldcg(p.ws_m + q) : -INFINITY;
       l[u] = __ldcg(p.ws_l + q);
       const float *src = p.ws_acc + q * D + lane * EPL;
@@ -180,7 +182,6 @@ __global__ void __launch_bounds__(256) rows_merge_kernel(RowsParams p, int wpr) 
     for (int e = 0; e < EPL; ++e) acc[e] = merge_add(0.0f, acc[e], f);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (q0 + u >= q_end) break;
       const float w = exp2f(m[u] - ref);
       L = fmaf(l[u], w, L);
 #pragma unroll
