@@ -332,6 +332,13 @@ __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w 
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 // Element load / store for the two storage types.
+// The same, no further than the largest finite bf16 (infinities too; NaN stays).
+__device__ __forceinline__ uint32_t pack_bf16x2_finite(float lo, float hi) {
+  uint32_t y;
+  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+  return y;
+}
+
 __device__ __forceinline__ float load_elem(const float *p) { return *p; }
 __device__ __forceinline__ float load_elem(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void store_elem(float *p, float x) { *p = x; }

@@ -814,13 +814,15 @@ struct SplitShape {
   static constexpr int SMEM_BYTES = KV_BYTES + PARTS * R * Q_PITCH + 4 * WARP_P;
 };
 
-// N bf16 parts of a pair of fp32 values, largest first (what is not finite
-// becomes NaN if N > 1: inf - inf).
+// N bf16 parts of a pair of fp32 values, largest first. What is not finite becomes
+// NaN if N > 1 (inf - inf); what is finite has finite parts: of three, the first is at
+// most the largest bf16 (fp32's largest values would round to infinity, and their NaN
+// would reach rows that do not see them).
 template <int N>
 __device__ __forceinline__ void bf16_parts(float x, float y, uint32_t (&w)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    w[i] = pack_bf16x2(x, y);
+    w[i] = N == 3 && i == 0 ? pack_bf16x2_finite(x, y) : pack_bf16x2(x, y);
     if (i + 1 == N) break;
     x -= bf16_lo(w[i]);
     y -= bf16_hi(w[i]);

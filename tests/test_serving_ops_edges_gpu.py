@@ -200,3 +200,28 @@ def test_tree_rows_whose_scores_are_all_minus_infinity(dtype, hq, hk, d, B):
         got = f64(tree_call(q, k, v, i32(tables), i32(lens), i32(ofs), 4, 90, part, masks=words))
         assert np.array_equal(np.isnan(got), np.isnan(want)) and (got[0] == 0).all()
         assert np.array_equal(got[3], want[3])        # one token, exact
+
+
+@pytest.mark.parametrize("drafts", [2, 9, 20])
+def test_tree_largest_finite_fp32_values(drafts):
+    """fp32's largest numbers round to infinity in bf16: they must not reach the rows that do not see
+    them, and act as finite ones in those that do."""
+    hq, hk, d, B = 2, 1, 128, 16
+    rng = np.random.default_rng(20)
+    lens, counts = np.array([drafts + 21, 40], np.int32), np.array([drafts, 1], np.int32)
+    tables, k, v, ofs, _, q, _ = tree_case(rng, counts, lens, B, hq, hk, d, torch.float32, "chain", pad=0)
+    top = torch.finfo(torch.float32).max
+    last = int(tables[0][(lens[0] - 1) // B]), int(lens[0] - 1) % B
+    n = int(ofs[-1])
+    for side in (k, v):
+        was = side[last].clone()
+        for val in (top, -top):
+            side[last] = val
+            got = f64(tree_call(q, k, v, i32(tables), i32(lens), i32(ofs), drafts, int(lens[0])))
+            with np.errstate(over="ignore"):
+                want, terms = plain.tree_attention(f64(q), f64(k), f64(v), tables, lens, d ** -0.5, ofs, None)
+            live = np.ones((n, hq), bool)
+            if side is k:                      # its own row's scores pass 32 bits
+                live[drafts - 1] = False
+            check_attention(got, want, terms, d, torch.float32, RHO_TREE[torch.float32], live)
+        side[last] = was
