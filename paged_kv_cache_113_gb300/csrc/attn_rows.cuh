@@ -41,6 +41,7 @@ struct RowsParams {
   int32_t num_seqs, num_rows, max_draft, num_q_heads, num_kv_heads, group;
   int32_t block_size, max_blocks, num_blocks;
   int32_t partition, num_partitions, num_items;
+  int32_t max_context;        // the longest context that the call allows and a table holds
   int32_t row_tiles;          // CTAs that share a (sequence, KV head)'s rows
 };
 
@@ -50,11 +51,10 @@ struct SeqRows {
   int np;        // partitions with tokens
 };
 
-// Sequence s's context length c, n of its tokens being queries: clamped to the
-// table and the partitions, 0 where c is below n; either is recorded when asked.
+// Sequence s's context length c, n of its tokens being queries: clamped to
+// max_context, 0 where c is below n; either is recorded when asked.
 __device__ __forceinline__ int checked_context(const RowsParams &p, int s, int n, int c, bool record) {
-  const int cap = int(min(int64_t(p.max_blocks) * p.block_size,
-                          int64_t(p.num_partitions) * p.partition));
+  const int cap = p.max_context;
   if (c >= n && c <= cap) return c;
   if (record) record_error(&g_rows_error, PK_DEVERR_CONTEXT, s);
   return c < n || cap < n ? 0 : cap;
@@ -253,6 +253,7 @@ inline pk_status rows_params(RowsParams &p, void *out, const void *q, const void
   p.num_blocks = d.num_blocks;
   p.partition = P > 1 ? part : max_blocks_per_seq * d.block_size;
   p.num_partitions = int32_t(P);
+  p.max_context = std::min(max_context_len, max_blocks_per_seq * d.block_size);
   p.row_tiles = 1;
   if (workspace && !aligned16(workspace)) return PK_ERR_WORKSPACE;
   if (P > 1) {

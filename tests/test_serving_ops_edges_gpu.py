@@ -217,7 +217,7 @@ def test_tree_largest_finite_fp32_values(drafts):
         was = side[last].clone()
         for val in (top, -top):
             side[last] = val
-            got = f64(tree_call(q, k, v, i32(tables), i32(lens), i32(ofs), drafts, int(lens[0])))
+            got = f64(tree_call(q, k, v, i32(tables), i32(lens), i32(ofs), drafts, int(lens.max())))
             with np.errstate(over="ignore"):
                 want, terms = plain.tree_attention(f64(q), f64(k), f64(v), tables, lens, d ** -0.5, ofs, None)
             live = np.ones((n, hq), bool)
@@ -225,3 +225,27 @@ def test_tree_largest_finite_fp32_values(drafts):
                 live[drafts - 1] = False
             check_attention(got, want, terms, d, torch.float32, RHO_TREE[torch.float32], live)
         side[last] = was
+
+
+def test_lengths_above_the_bound_are_clamped_to_it():
+    """A length that the table holds but the call's max_context_len does not is recorded and cut to
+    it, whether the call splits or not."""
+    hq, hk, d, B, most = 4, 2, 128, 16, 100
+    rng = np.random.default_rng(23)
+    lens, counts = np.array([60, 140], np.int32), np.array([2, 3], np.int32)
+    cut = np.minimum(lens, most)
+    for dt in DTYPES.values():
+        tables, k, v, ofs, _, q, _ = tree_case(rng, counts, lens, B, hq, hk, d, dt, "chain", pad=0)
+        n = int(ofs[-1])
+        want, terms = plain.tree_attention(f64(q), f64(k), f64(v), tables, cut, d ** -0.5, ofs, None)
+        for part in (0, 64):
+            out = tree_call(q, k, v, i32(tables), i32(lens), i32(ofs), 3, most, part)
+            assert pk.pk_get_device_error() == (4, 1)
+            check_attention(f64(out)[:n], want[:n], tuple(t[:n] for t in terms), d, dt, RHO_TREE[dt])
+        kc, vc, ex, vals = fill_e4m3(rng, tables, lens, int(k.shape[0]), B, hk, d)
+        q = rand(rng, (2, hq, d), dt)
+        want, terms = plain.tree_attention(f64(q), *vals, tables, cut, d ** -0.5)
+        for part in (0, 64):
+            out = decode_call(q, kc, vc, ex, i32(tables), i32(lens), most, part)
+            assert pk.pk_get_device_error() == (4, 1)
+            check_attention(f64(out), want, terms, d, dt, RHO_E4M3[dt])
