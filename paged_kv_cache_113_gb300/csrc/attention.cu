@@ -1559,18 +1559,7 @@ extern "C" void pkx_attn_params_rebind(void *params, const void *const from[4],
   if (p->out == from[3]) p->out = const_cast<void *>(to[3]);
 }
 
-extern "C" int pkx_take_attention_error(cudaStream_t stream) {
-  int code = 0;
-  const int zero = 0;
-  if (cudaMemcpyFromSymbolAsync(&code, g_attn_error, sizeof(int), 0, cudaMemcpyDeviceToHost,
-                                stream) != cudaSuccess)
-    return -1;
-  if (cudaMemcpyToSymbolAsync(g_attn_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice,
-                              stream) != cudaSuccess)
-    return -1;
-  if (cudaStreamSynchronize(stream) != cudaSuccess) return -1;
-  return code;
-}
+extern "C" int *pkx_attention_error_word() { return pk::error_word(g_attn_error); }
 
 extern "C" {
 

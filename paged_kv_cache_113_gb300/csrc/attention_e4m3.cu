@@ -54,9 +54,7 @@
 
 namespace pk {
 
-extern "C" int pkx_take_attention_e4m3_error(cudaStream_t stream) {
-  return take_error_word(g_rows_error, stream);
-}
+extern "C" int *pkx_attention_e4m3_error_word() { return error_word(g_rows_error); }
 
 namespace {
 

@@ -282,9 +282,7 @@ pk_status by_lanes(const RowParams &p, int rows, F f) {
 
 }  // namespace
 
-extern "C" int pkx_take_cache_e4m3_error(cudaStream_t stream) {
-  return pk::take_error_word(g_cache_e4m3_error, stream);
-}
+extern "C" int *pkx_cache_e4m3_error_word() { return pk::error_word(g_cache_e4m3_error); }
 
 extern "C" {
 

@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <initializer_list>
 
 #include "pagedkv.h"
@@ -157,6 +158,25 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 int64_t elem_size(pk_dtype t) { return t == PK_F32 ? 4 : (t == PK_BF16 ? 2 : 0); }
 
+// The device error words of all files, in the order in which they are reported.
+constexpr int kErrorWords = 6;
+struct ErrorWords {
+  int *at[kErrorWords];
+};
+// What the last calls of pk_get_device_error found, one word a call in turn: calls
+// at once, of several threads, do not share one.
+constexpr int kTaken = 64;
+__device__ int g_taken[kTaken];
+
+// Reads and clears every word, all at once; the first that holds an event is the
+// result.
+__global__ void take_errors_kernel(ErrorWords words, int *taken) {
+  const int code = threadIdx.x < kErrorWords ? atomicExch(words.at[threadIdx.x], 0) : 0;
+  const uint32_t found = __ballot_sync(0xffffffffu, code != 0);
+  const int first = __shfl_sync(0xffffffffu, code, found ? __ffs(found) - 1 : 0);
+  if (threadIdx.x == 0) *taken = first;
+}
+
 pk_status check_desc(const pk_cache_desc *d) {
   if (!d || d->num_blocks <= 0 || d->block_size <= 0 || d->num_kv_heads <= 0 || d->head_dim <= 0)
     return PK_ERR_INVALID_ARG;
@@ -168,25 +188,11 @@ pk_status check_desc(const pk_cache_desc *d) {
 
 }  // namespace
 
-// Read-and-clear of this file's device error word (used by pk_get_device_error).
-extern "C" int pkx_take_cache_ops_error(cudaStream_t stream) {
-  int code = 0;
-  const int zero = 0;
-  if (cudaMemcpyFromSymbolAsync(&code, g_cache_ops_error, sizeof(int), 0,
-                                cudaMemcpyDeviceToHost, stream) != cudaSuccess)
-    return -1;
-  if (cudaMemcpyToSymbolAsync(g_cache_ops_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice,
-                              stream) != cudaSuccess)
-    return -1;
-  if (cudaStreamSynchronize(stream) != cudaSuccess) return -1;
-  return code;
-}
-
-extern "C" int pkx_take_attention_error(cudaStream_t stream);
-extern "C" int pkx_take_qk_norm_rope_error(cudaStream_t stream);
-extern "C" int pkx_take_cache_e4m3_error(cudaStream_t stream);
-extern "C" int pkx_take_attention_e4m3_error(cudaStream_t stream);
-extern "C" int pkx_take_tree_attention_error(cudaStream_t stream);
+extern "C" int *pkx_attention_error_word();
+extern "C" int *pkx_qk_norm_rope_error_word();
+extern "C" int *pkx_cache_e4m3_error_word();
+extern "C" int *pkx_attention_e4m3_error_word();
+extern "C" int *pkx_tree_attention_error_word();
 
 extern "C" {
 
@@ -336,15 +342,25 @@ pk_status pk_swap_blocks(void *k_cache, void *v_cache, void *k_host, void *v_hos
 pk_status pk_get_device_error(int32_t *code_out, void *stream) {
   if (!code_out) return PK_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int first = 0;
-  for (auto take : {pkx_take_cache_ops_error, pkx_take_attention_error, pkx_take_qk_norm_rope_error,
-                    pkx_take_cache_e4m3_error, pkx_take_attention_e4m3_error,
-                    pkx_take_tree_attention_error}) {
-    const int code = take(s);
-    if (code < 0) return PK_ERR_CUDA;
-    if (first == 0) first = code;
+  ErrorWords words;
+  int i = 0;
+  for (int *word : {pk::error_word(g_cache_ops_error), pkx_attention_error_word(), pkx_qk_norm_rope_error_word(),
+                    pkx_cache_e4m3_error_word(), pkx_attention_e4m3_error_word(),
+                    pkx_tree_attention_error_word()}) {
+    if (!word) return PK_ERR_CUDA;
+    words.at[i++] = word;
   }
-  *code_out = first;
+  int *taken = pk::error_word(g_taken);
+  if (!taken) return PK_ERR_CUDA;
+  static std::atomic<uint32_t> calls{0};
+  taken += calls.fetch_add(1, std::memory_order_relaxed) % kTaken;
+  take_errors_kernel<<<1, 32, 0, s>>>(words, taken);
+  int code = 0;
+  if (cudaGetLastError() != cudaSuccess ||
+      cudaMemcpyAsync(&code, taken, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return PK_ERR_CUDA;
+  *code_out = code;
   return PK_OK;
 }
 

@@ -13,8 +13,8 @@
 namespace pk {
 
 // ---------------------------------------------------------------------------
-// Device error word. One per translation unit; the host reads each through
-// the accessor that its .cu file exports. Only the first event is kept.
+// Device error word. One per translation unit, whose .cu file exports its
+// address; pk_get_device_error reads them all. Only the first event is kept.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void record_error(int *word, int kind, long long index) {
   const int code = (kind << 24) | int(index & 0xFFFFFF);
@@ -356,20 +356,12 @@ __device__ __forceinline__ uint2 narrow4(const float4 &v, __nv_bfloat16) {
   return make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
-// Host: the value of a translation unit's device error word, which is cleared
-// (-1 when a call fails). Synchronises the stream.
+// Host: the address of a translation unit's device error word on the current
+// device (null when the lookup fails).
 template <typename Word>
-inline int take_error_word(const Word &word, cudaStream_t stream) {
-  int code = 0;
-  const int zero = 0;
-  if (cudaMemcpyFromSymbolAsync(&code, word, sizeof(int), 0, cudaMemcpyDeviceToHost, stream) !=
-      cudaSuccess)
-    return -1;
-  if (cudaMemcpyToSymbolAsync(word, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, stream) !=
-      cudaSuccess)
-    return -1;
-  if (cudaStreamSynchronize(stream) != cudaSuccess) return -1;
-  return code;
+inline int *error_word(const Word &word) {
+  void *at = nullptr;
+  return cudaGetSymbolAddress(&at, word) == cudaSuccess ? static_cast<int *>(at) : nullptr;
 }
 
 }  // namespace pk

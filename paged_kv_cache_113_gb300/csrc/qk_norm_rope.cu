@@ -182,9 +182,7 @@ pk_status launch(RopeParams p, cudaStream_t stream) {
 
 }  // namespace
 
-extern "C" int pkx_take_qk_norm_rope_error(cudaStream_t stream) {
-  return pk::take_error_word(g_qk_norm_rope_error, stream);
-}
+extern "C" int *pkx_qk_norm_rope_error_word() { return pk::error_word(g_qk_norm_rope_error); }
 
 extern "C" pk_status pk_qk_norm_rope_and_cache(
     void *q_out, void *k_out, const void *q, const void *k, const void *v, int64_t q_stride,

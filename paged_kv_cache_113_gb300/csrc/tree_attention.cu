@@ -59,9 +59,7 @@
 
 namespace pk {
 
-extern "C" int pkx_take_tree_attention_error(cudaStream_t stream) {
-  return take_error_word(g_rows_error, stream);
-}
+extern "C" int *pkx_tree_attention_error_word() { return error_word(g_rows_error); }
 
 namespace {
 

@@ -1,6 +1,8 @@
 """Attention of drafted tokens and over the 8-bit cache where its parts meet: units
 that follow one another on a CTA, states that are merged, values that are not
 finite, long partitions. Bounds as in test_serving_ops_gpu."""
+import time
+
 import numpy as np
 import pytest
 
@@ -249,3 +251,39 @@ def test_lengths_above_the_bound_are_clamped_to_it():
             out = decode_call(q, kc, vc, ex, i32(tables), i32(lens), most, part)
             assert pk.pk_get_device_error() == (4, 1)
             check_attention(f64(out), want, terms, d, dt, RHO_E4M3[dt])
+
+
+def test_device_errors_are_read_at_once():
+    """Events of several operators: the first of the documented kinds in the library's order comes back,
+    all are cleared, and the read costs a few round trips to the device, however many operators there
+    are (six reads one after another took nine times one scalar's)."""
+    rng = np.random.default_rng(24)
+    q, k = rand(rng, (3, 2, 64)), rand(rng, (3, 1, 64))
+    cs = torch.ones((4, 64), device=DEV)
+    bad_pos = torch.tensor([0, 9, 1], device=DEV)
+    kc = torch.zeros((2, 16, 1, 64), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    ex = torch.zeros((2, 1, 16, 2), dtype=torch.uint8, device=DEV)
+    out = torch.zeros_like(k)
+    pool = torch.zeros((2, 16, 1, 64), device=DEV)
+    for only in (False, True):
+        pk.pk_paged_attention_tree(torch.empty_like(q), q, pool, pool, i32([[0]]), i32([3]), i32([0, 9]), 0.1, 4, 16)
+        pk.pk_gather_cache_e4m3(out, out.clone(), torch.tensor([0, 1, 99], device=DEV), kc, kc.clone(), ex)
+        if not only:
+            pk.pk_qk_norm_rope_and_cache(torch.empty_like(q), torch.empty_like(k), q, k, None, cs, bad_pos)
+        assert pk.pk_get_device_error() == ((1, 2) if only else (7, 1))
+        assert pk.pk_get_device_error() == (0, 0)
+
+    word = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def median(f):
+        times = []
+        for _ in range(60):
+            t = time.perf_counter()
+            f()
+            times.append(time.perf_counter() - t)
+        return sorted(times)[30]
+
+    median(pk.pk_get_device_error)
+    one, read = median(word.item), median(pk.pk_get_device_error)
+    print(f"a scalar {one * 1e6:.1f} us, the errors {read * 1e6:.1f} us")
+    assert read < 4 * one
