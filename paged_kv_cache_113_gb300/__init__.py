@@ -238,17 +238,20 @@ def _dtype_code(t) -> int:
         return PK_F32
     if t.dtype == torch.bfloat16:
         return PK_BF16
-    if t.dtype == torch.float8_e4m3fn:
-        return PK_E4M3
-    raise TypeError(f"unsupported dtype {t.dtype}: libpagedkv takes float32 or bfloat16")
+    raise TypeError(f"unsupported dtype {t.dtype}: this call of libpagedkv takes float32 or bfloat16")
 
 
-def cache_desc(k_cache) -> CacheDesc:
-    """The pool descriptor of a ``[num_blocks, B, Hk, d]`` cache tensor."""
+def _pool_desc(k_cache, dtype=None) -> CacheDesc:
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [num_blocks, block_size, num_kv_heads, head_dim]")
     N, B, Hk, d = k_cache.shape
-    return CacheDesc(int(N), int(B), int(Hk), int(d), _dtype_code(k_cache))
+    return CacheDesc(int(N), int(B), int(Hk), int(d), _dtype_code(k_cache) if dtype is None else dtype)
+
+
+def cache_desc(k_cache) -> CacheDesc:
+    """The pool descriptor of a ``[num_blocks, B, Hk, d]`` cache tensor (fp32 or
+    bf16; of an 8-bit cache's codes, float8_e4m3fn, for the calls that take one)."""
+    return _pool_desc(k_cache, PK_E4M3 if k_cache.dtype == _torch().float8_e4m3fn else None)
 
 
 def _dev(t, name, dtype=None):
@@ -272,7 +275,7 @@ def _stream(stream):
 def pk_reshape_and_cache(k, v, slot_mapping, k_cache, v_cache, stream=None):
     """Writes token i's K/V ``[T, Hk, d]`` into slot ``slot_mapping[i]`` (int64)."""
     torch = _torch()
-    desc = cache_desc(k_cache)
+    desc = _pool_desc(k_cache)
     T = int(k.shape[0])
     if tuple(k.shape) != (T, desc.num_kv_heads, desc.head_dim) or v.shape != k.shape:
         raise ValueError("k and v must be [num_tokens, num_kv_heads, head_dim]")
@@ -290,7 +293,7 @@ def pk_reshape_and_cache_append(k, v, slot_mapping, k_cache, v_cache, block_tabl
     next token goes to ``slot_mapping[i]``, ``block_tables[i][ctx/B]`` becomes
     ``slot/B`` and ``context_lens[i]`` grows by one (int32 CUDA tensors)."""
     torch = _torch()
-    desc = cache_desc(k_cache)
+    desc = _pool_desc(k_cache)
     T = int(k.shape[0])
     if slot_mapping.dtype != torch.int64 or block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
         raise TypeError("slot_mapping int64, block_tables and context_lens int32")
@@ -306,7 +309,7 @@ def pk_reshape_and_cache_append(k, v, slot_mapping, k_cache, v_cache, block_tabl
 def pk_copy_blocks(k_cache, v_cache, src_dst_pairs, stream=None):
     """Copies whole blocks ``src_dst_pairs[p] = (src, dst)`` (int64 ``[n, 2]``) in K and V."""
     torch = _torch()
-    desc = cache_desc(k_cache)
+    desc = _pool_desc(k_cache)
     n = int(src_dst_pairs.shape[0]) if src_dst_pairs.numel() else 0
     if n and tuple(src_dst_pairs.shape) != (n, 2):
         raise ValueError("src_dst_pairs must be [num_pairs, 2]")
@@ -376,7 +379,7 @@ def pk_paged_attention_decode(out, q, k_cache, v_cache, block_tables, context_le
     :func:`pk_attention_work_items`); replaces ``seq_order``.
     """
     torch = _torch()
-    desc = cache_desc(k_cache)
+    desc = _pool_desc(k_cache)
     S, Hq, d = (int(x) for x in q.shape)
     if out.shape != q.shape or out.dtype != q.dtype or q.dtype != k_cache.dtype:
         raise ValueError("out and q must be [num_seqs, num_q_heads, head_dim] of the cache dtype")
@@ -416,7 +419,7 @@ def pk_paged_attention_decode_append(out, q, k_new, v_new, slot_mapping, k_cache
     sequence i's last token; ``work_items`` int32 ``[n, 2]`` for the given
     (resolved) partition size."""
     torch = _torch()
-    desc = cache_desc(k_cache)
+    desc = _pool_desc(k_cache)
     S, Hq, d = (int(x) for x in q.shape)
     if out.shape != q.shape or tuple(k_new.shape) != (S, desc.num_kv_heads, d) or v_new.shape != k_new.shape:
         raise ValueError("shape mismatch")
@@ -440,7 +443,7 @@ def pk_paged_attention_decode_advance(out, q, k_new, v_new, slot_mapping, k_cach
     them plus one, ``block_tables`` is updated in place; ``max_context_len``
     and ``work_items`` are for the advanced lengths."""
     torch = _torch()
-    desc = cache_desc(k_cache)
+    desc = _pool_desc(k_cache)
     S, Hq, d = (int(x) for x in q.shape)
     if out.shape != q.shape or tuple(k_new.shape) != (S, desc.num_kv_heads, d) or v_new.shape != k_new.shape:
         raise ValueError("shape mismatch")
@@ -464,7 +467,7 @@ def pk_paged_attention_decode_static(out, q, k_cache, v_cache, block_tables, con
     (``PK_STATIC_WORKSPACE_BYTES``), shared by every call on a device, so
     calls whose work overlaps on the GPU race on it."""
     torch = _torch()
-    desc = cache_desc(k_cache)
+    desc = _pool_desc(k_cache)
     S, Hq, d = (int(x) for x in q.shape)
     if out.shape != q.shape or out.dtype != q.dtype or q.dtype != k_cache.dtype:
         raise ValueError("out and q must be [num_seqs, num_q_heads, head_dim] of the cache dtype")
@@ -493,7 +496,7 @@ def pk_cascade_attention_decode(out, q, k_cache, v_cache, block_tables, context_
     ``num_groups``, ``max_group_size``, ``max_prefix_len`` (see
     :meth:`BlockManager.prefix_groups`)."""
     torch = _torch()
-    desc = cache_desc(k_cache)
+    desc = _pool_desc(k_cache)
     S, Hq, d = (int(x) for x in q.shape)
     if out.shape != q.shape or out.dtype != q.dtype or q.dtype != k_cache.dtype:
         raise ValueError("out and q must be [num_seqs, num_q_heads, head_dim] of the cache dtype")
@@ -516,7 +519,7 @@ def pk_swap_blocks(k_cache, v_cache, k_host, v_host, pairs, direction: int, stre
     """Whole-block copies between the device pool and a pinned host pool
     ``[H, B, Hk, d]``: ``pairs`` int64 ``[n, 2]`` (CUDA or pinned CPU tensor)
     from pk_bm_swap_out (``PK_SWAP_OUT``) or pk_bm_swap_in (``PK_SWAP_IN``)."""
-    desc = cache_desc(k_cache)
+    desc = _pool_desc(k_cache)
     if k_host.is_cuda or not k_host.is_pinned() or not v_host.is_pinned():
         raise ValueError("k_host and v_host must be pinned host tensors")
     if tuple(k_host.shape[1:]) != tuple(k_cache.shape[1:]) or v_host.shape != k_host.shape:
@@ -1046,7 +1049,7 @@ class DecodeStepper:
                  zero_copy: bool = False):
         torch = _torch()
         self.bm, self.k_cache, self.v_cache = bm, k_cache, v_cache
-        self.desc = cache_desc(k_cache)
+        self.desc = _pool_desc(k_cache)
         self.ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
         S, Hk, d = len(self.ids), self.desc.num_kv_heads, self.desc.head_dim
         self.S, self.Hq, self.scale, self.maxb, self.partition = S, int(num_q_heads), float(scale), \
