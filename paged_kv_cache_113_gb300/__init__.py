@@ -576,19 +576,33 @@ _FUNCTIONS: dict = {}  # loaded entry points by name
 _DESCS: dict = {}      # pool descriptors by shape and dtype: (descriptor, its reference, shape of kv_exp)
 
 
+_RAW_STREAM = None     # device index -> handle of its current stream
+
+
+def _raw_stream(torch):
+    """PyTorch's own short way to a stream handle, which is not part of its
+    documented interface, or the documented one (a microsecond longer) where a
+    version has no such function."""
+    short = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return short if short is not None else lambda dev: torch.cuda.current_stream(dev).cuda_stream
+
+
 def _launch(torch, name, dev, stream, *args):
     """The library's call with the tensors' device current, on the given stream
     or that device's current one."""
+    global _RAW_STREAM
+    if _RAW_STREAM is None:
+        _RAW_STREAM = _raw_stream(torch)
     fn = _FUNCTIONS.get(name)
     if fn is None:
         fn = _FUNCTIONS[name] = getattr(lib(), name)
     if stream is None:
-        st = torch._C._cuda_getCurrentRawStream(dev)
+        st = _RAW_STREAM(dev)
     elif stream.device.index != dev:
         raise ValueError("the stream is not on the tensors' device")
     else:
         st = stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
+    if torch.cuda.current_device() == dev:
         status = fn(*args, st)
     else:
         with torch.cuda.device(dev):

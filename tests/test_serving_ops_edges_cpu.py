@@ -1,5 +1,6 @@
 """The 8-bit cache's dtype beside the calls that do not take it, on the CPU."""
 import ctypes
+from types import SimpleNamespace
 
 import numpy as np
 import pytest
@@ -66,3 +67,11 @@ def test_every_call_of_fp32_and_bf16_pools_refuses_8_bit_ones(L):
     ids = np.zeros(1, np.int64)
     assert L.pk_decode_step_prepare(bm._h, ids.ctypes.data, 1, 8, 4, 0, ref, ctypes.byref(steps)) == uns
     assert L.pk_decode_step_launch(1, 8, 0.1, 4, p, p, ref, ctypes.byref(steps), None) in (uns, pk.PK_ERR_INVALID_ARG)
+
+
+def test_stream_handles_without_the_short_way():
+    """A PyTorch without the undocumented lookup serves through the documented one."""
+    cuda = SimpleNamespace(current_stream=lambda dev: SimpleNamespace(cuda_stream=1000 + dev))
+    assert pk._raw_stream(SimpleNamespace(_C=SimpleNamespace(), cuda=cuda))(3) == 1003
+    short = SimpleNamespace(_cuda_getCurrentRawStream=lambda dev: 7 + dev)
+    assert pk._raw_stream(SimpleNamespace(_C=short, cuda=cuda))(3) == 10
