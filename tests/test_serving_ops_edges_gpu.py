@@ -287,3 +287,77 @@ def test_device_errors_are_read_at_once():
     one, read = median(word.item), median(pk.pk_get_device_error)
     print(f"a scalar {one * 1e6:.1f} us, the errors {read * 1e6:.1f} us")
     assert read < 4 * one
+
+
+def fast_attention(q, k, v, lens, scale, ofs=None):
+    """As plain.tree_attention over contexts that lie one after another, fp64 on the GPU: k, v
+    [sum of lens, Hk, d] on the GPU; a chain with ``ofs``."""
+    R, hq, d = q.shape
+    qd = q.double()
+    out, wv = torch.zeros((R, hq, d), dtype=torch.float64, device=DEV), torch.zeros((R, hq, d), dtype=torch.float64,
+                                                                                  device=DEV)
+    mag, cnt = torch.zeros((R, hq), dtype=torch.float64, device=DEV), torch.zeros((R, hq), dtype=torch.float64,
+                                                                                device=DEV)
+    at = 0
+    for s, n in enumerate(lens):
+        ks, vs = k[at:at + n].double(), v[at:at + n].double()
+        at += n
+        r0, r1 = (s, s + 1) if ofs is None else (ofs[s], ofs[s + 1])
+        for i in range(r0, r1):
+            m = n - (r1 - 1 - i)
+            for h in range(hq):
+                g = h // (hq // k.shape[1])
+                x = ks[:m, g] @ qd[i, h] * scale
+                w = torch.softmax(x, 0)
+                out[i, h], wv[i, h] = w @ vs[:m, g], w @ vs[:m, g].abs()
+                mag[i, h] = (ks[:m, g].abs() @ qd[i, h].abs()).max() * scale * plain.LOG2E
+                cnt[i, h] = m
+    return tuple(f64(t) for t in (out, wv, mag, cnt))
+
+
+def check_long(got, exact, terms, d, dtype, rel):
+    """Three bounds, the coarse one for every element. Each: the scores' D (see test_serving_ops_gpu),
+    and ``rel`` of the weighted magnitudes for all that weights and sums may lose if no two errors
+    cancel, beside the result's own rounding. fp32: the mean error over all elements, which roundings to
+    the nearest leave near 0 (2^-24 sqrt(n), of which independent rows cancel), is below 2^-19; sums
+    that are cut off toward zero lose 2^-15 at 32 768 tokens. bf16: an error of r crosses the border of
+    a rounding with a probability of at most 2 r 2^8, so that with r up to 2^-16 fewer than 2% of the
+    results differ from the exact one, rounded; weights of one fp16 cross it in 10%."""
+    wv, mag, _ = terms
+    half = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}[dtype]
+    bound = (4 * np.log(2) * (d + 8) * 2.0 ** -23 * mag[..., None] + rel) * wv + half * np.abs(exact)
+    assert np.isfinite(got).all() and (np.abs(got - exact) <= bound).all(), float((np.abs(got - exact) / bound).max())
+    if dtype == torch.float32:
+        assert abs(((got - exact) * exact).sum() / (exact * exact).sum()) < 2.0 ** -19
+    else:
+        assert (got != f64(torch.from_numpy(exact).to(torch.bfloat16))).mean() < 0.02
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d,B", [(128, 8), (128, 16), (64, 16)])
+def test_decode_e4m3_long(dtype, d, B):
+    """Long contexts element by element: hundreds of stages and table chunks, whole and planned. A warp
+    adds up to 2^9 tiles, and a lane 2^10 terms of the denominator, each with a rounding of 2^-24 of what
+    is there so far, half the total on average: 2^-16 and 2^-15; weights are good to 2^-22."""
+    dt, hq, hk = DTYPES[dtype], 8, 2
+    rng = np.random.default_rng(25 + d + B)
+    lens = np.array([8191, 32768 + 7, 4097], np.int32)
+    tables, N = tables_for(rng, lens, B)
+    kc, vc = (torch.zeros((N, B, hk, d), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn) for _ in range(2))
+    ex = torch.zeros((N, hk, B, 2), dtype=torch.uint8, device=DEV)
+    slots = torch.from_numpy(np.concatenate([tables[s][np.arange(n) // B].astype(np.int64) * B + np.arange(n) % B
+                                             for s, n in enumerate(lens)])).to(DEV)
+    k, v = rand(rng, (len(slots), hk, d)), rand(rng, (len(slots), hk, d))
+    if dt == torch.float32:
+        v += 1.0                                     # sums that only grow
+    pk.pk_reshape_and_cache_e4m3(k, v, slots, kc, vc, ex)
+    pk.pk_gather_cache_e4m3(k, v, slots, kc, vc, ex)
+    q = rand(rng, (3, hq, d), dt)
+    exact, *terms = fast_attention(q, k, v, lens, d ** -0.5)
+    for part, planned in ((0, False), (-1, True), (1024, True)):
+        items = None
+        if planned:
+            part, it = pk.pk_attention_plan(lens, hq, pk.cache_desc(kc), part)
+            items = torch.from_numpy(it).to(DEV)
+        out = decode_call(q, kc, vc, ex, i32(tables), i32(lens), int(lens.max()), part, items)
+        check_long(f64(out), exact, terms, d, dt, 2.0 ** -14)
