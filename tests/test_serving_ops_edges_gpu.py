@@ -315,22 +315,23 @@ def fast_attention(q, k, v, lens, scale, ofs=None):
     return tuple(f64(t) for t in (out, wv, mag, cnt))
 
 
-def check_long(got, exact, terms, d, dtype, rel):
+def check_long(got, exact, terms, d, dtype, rel, flips=0.02):
     """Three bounds, the coarse one for every element. Each: the scores' D (see test_serving_ops_gpu),
     and ``rel`` of the weighted magnitudes for all that weights and sums may lose if no two errors
     cancel, beside the result's own rounding. fp32: the mean error over all elements, which roundings to
     the nearest leave near 0 (2^-24 sqrt(n), of which independent rows cancel), is below 2^-19; sums
     that are cut off toward zero lose 2^-15 at 32 768 tokens. bf16: an error of r crosses the border of
     a rounding with a probability of at most 2 r 2^8, so that with r up to 2^-16 fewer than 2% of the
-    results differ from the exact one, rounded; weights of one fp16 cross it in 10%."""
+    results differ from the exact one, rounded; weights of one fp16 cross it in 10% (``flips`` None:
+    not asked)."""
     wv, mag, _ = terms
     half = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}[dtype]
     bound = (4 * np.log(2) * (d + 8) * 2.0 ** -23 * mag[..., None] + rel) * wv + half * np.abs(exact)
     assert np.isfinite(got).all() and (np.abs(got - exact) <= bound).all(), float((np.abs(got - exact) / bound).max())
     if dtype == torch.float32:
         assert abs(((got - exact) * exact).sum() / (exact * exact).sum()) < 2.0 ** -19
-    else:
-        assert (got != f64(torch.from_numpy(exact).to(torch.bfloat16))).mean() < 0.02
+    elif flips is not None:
+        assert (got != f64(torch.from_numpy(exact).to(torch.bfloat16))).mean() < flips
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -361,3 +362,58 @@ def test_decode_e4m3_long(dtype, d, B):
             items = torch.from_numpy(it).to(DEV)
         out = decode_call(q, kc, vc, ex, i32(tables), i32(lens), int(lens.max()), part, items)
         check_long(f64(out), exact, terms, d, dt, 2.0 ** -14)
+
+
+@pytest.mark.parametrize("dtype,hq,hk,d,B,drafts", [("bf16", 8, 2, 128, 8, 3), ("bf16", 8, 2, 128, 16, 40),
+                                                    ("bf16", 8, 2, 64, 16, 4), ("bf16", 4, 2, 64, 16, 3),
+                                                    ("f32", 8, 2, 128, 16, 3)])
+def test_tree_long(dtype, hq, hk, d, B, drafts):
+    """Long contexts element by element, on both kernels, one and two tiles of rows, whole and planned.
+    fp32 as over the 8-bit cache. bf16: weights good to 2^-17, and sums left to the tensor cores, which
+    cut each off by at most 2^-23 of what is there so far, half the total on average: eight products a
+    tile of 64 tokens, 4104 of them, 2^-12 at most. 2^-11 holds both."""
+    dt = DTYPES[dtype]
+    rng = np.random.default_rng(26 + d + drafts)
+    lens, counts = np.array([8191, 32768 + 7, 4097], np.int32), np.array([drafts, drafts - 1, 1], np.int32)
+    tables, N = tables_for(rng, lens, B)
+    kc, vc = torch.zeros((N, B, hk, d), dtype=dt, device=DEV), torch.zeros((N, B, hk, d), dtype=dt, device=DEV)
+    slots = torch.from_numpy(np.concatenate([tables[s][np.arange(n) // B].astype(np.int64) * B + np.arange(n) % B
+                                             for s, n in enumerate(lens)])).to(DEV)
+    k, v = rand(rng, (len(slots), hk, d), dt), rand(rng, (len(slots), hk, d), dt) + 1.0   # sums that only grow
+    kc.view(-1, hk, d)[slots], vc.view(-1, hk, d)[slots] = k, v
+    ofs = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    q = rand(rng, (int(ofs[-1]), hq, d), dt)
+    exact, *terms = fast_attention(q, k, v, lens, d ** -0.5, ofs)
+    for part, planned in ((0, False), (-1, True), (1024, True)):
+        items = None
+        if planned:
+            part, it = pk.pk_tree_plan(lens, drafts, hq, pk.cache_desc(kc), part)
+            items = torch.from_numpy(it).to(DEV)
+        out = tree_call(q, kc, vc, i32(tables), i32(lens), i32(ofs), drafts, int(lens.max()), part, items)
+        check_long(f64(out), exact, terms, d, dt, 2.0 ** (-14 if dt == torch.float32 else -11), None)
+
+
+@pytest.mark.parametrize("kind", ["decode", "tree", "few rows"])
+def test_fp32_rows_are_close_as_a_whole(kind):
+    """The bounds of single elements add every rounding up and let 10^-4 pass. Of a whole row the errors
+    are independent: d products of a score leave sqrt(d) 2^-24 of its magnitude (a few 10^-7 of a weight
+    at scores of a few units), the weights' errors average out over the tokens, and sums of n terms leave
+    sqrt(n) 2^-24: below 2^-18 of the row's norm, all told."""
+    dt, hq, hk, B = torch.float32, 8, 2, 16
+    d, drafts = (64, 2) if kind == "few rows" else (128, 9)
+    rng = np.random.default_rng(27 + d)
+    lens = np.array([300, 64, 17, 200, 1], np.int32)
+    if kind == "decode":
+        tables, N = tables_for(rng, lens, B)
+        kc, vc, ex, vals = fill_e4m3(rng, tables, lens, N, B, hk, d, spread=3)
+        q = rand(rng, (len(lens), hq, d))
+        want, _ = plain.tree_attention(f64(q), *vals, tables, lens, d ** -0.5)
+        runs = [decode_call(q, kc, vc, ex, i32(tables), i32(lens), 300, part) for part in (0, 64)]
+    else:
+        counts = np.minimum(drafts, lens).astype(np.int32)
+        tables, k, v, ofs, masks, q, mt = tree_case(rng, counts, lens, B, hq, hk, d, dt, "tree", pad=0)
+        want, _ = plain.tree_attention(f64(q), f64(k), f64(v), tables, lens, d ** -0.5, ofs, masks)
+        runs = [tree_call(q, k, v, i32(tables), i32(lens), i32(ofs), drafts, 300, part, masks=mt) for part in (0, 64)]
+    for out in runs:
+        off = np.linalg.norm(f64(out) - want, axis=-1) / np.linalg.norm(want, axis=-1)
+        assert off.max() < 2.0 ** -18, float(off.max())
