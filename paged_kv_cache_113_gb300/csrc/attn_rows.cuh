@@ -16,6 +16,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "pagedkv.h"
 #include "pk_device.cuh"
@@ -153,41 +154,58 @@ __global__ void __launch_bounds__(256) rows_merge_kernel(RowsParams p, int wpr) 
   const size_t at = size_t(sr.q0) * p.num_q_heads + row;
   const int chunk = (sr.np + wpr - 1) / wpr;
   const int q_end = live ? min(sr.np, (sub + 1) * chunk) : 0;
-  float M = -INFINITY, L = 0.0f, acc[EPL] = {};
-  for (int q0 = sub * chunk; q0 < q_end; q0 += U) {
-    float m[U], l[U], x[U][EPL];
+  float M, L, acc[EPL];
+  // Whether a result is not finite although its sum is: then the states are joined
+  // again with care for what a factor of 0 would hide (see merge_add), which costs
+  // registers and a fifth of the time in a loop that has it for every state.
+  auto odd = [&] {
+    float o = 0.0f;  // NaN once an element is not finite
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const size_t q = at * p.num_partitions + min(q0 + u, q_end - 1);
-      // Past the end the last one again, at a factor of 0: what is not finite in it
-      // counts already.
-      m[u] = q0 + u < q_end ? __ldcg(p.ws_m + q) : -INFINITY;
-      l[u] = __ldcg(p.ws_l + q);
-      const float *src = p.ws_acc + q * D + lane * EPL;
-      if (EPL == 4) {
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
-        x[u][0] = v.x, x[u][1] = v.y, x[u][EPL - 2] = v.z, x[u][EPL - 1] = v.w;
-      } else {
-        const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
-        x[u][0] = v.x, x[u][1] = v.y;
+    for (int e = 0; e < EPL; ++e) o = fmaf(acc[e], 0.0f, o);
+    return __any_sync(0xffffffffu, o != 0.0f) && fabsf(L) <= 3.402823466e38f;
+  };
+  auto partitions = [&](auto care) {
+    constexpr bool CARE = decltype(care)::value;
+    M = -INFINITY, L = 0.0f;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) acc[e] = 0.0f;
+    for (int q0 = sub * chunk; q0 < q_end; q0 += U) {
+      float m[U], l[U], x[U][EPL];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const size_t q = at * p.num_partitions + min(q0 + u, q_end - 1);
+        // Past the end the last one again, at a factor of 0: what is not finite in it
+        // counts already.
+        m[u] = q0 + u < q_end ? __ldcg(p.ws_m + q) : -INFINITY;
+        l[u] = __ldcg(p.ws_l + q);
+        const float *src = p.ws_acc + q * D + lane * EPL;
+        if (EPL == 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
+          x[u][0] = v.x, x[u][1] = v.y, x[u][EPL - 2] = v.z, x[u][EPL - 1] = v.w;
+        } else {
+          const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
+          x[u][0] = v.x, x[u][1] = v.y;
+        }
+      }
+      float top = M;
+#pragma unroll
+      for (int u = 0; u < U; ++u) top = fmaxf(top, m[u]);
+      const float ref = top == -INFINITY ? 0.0f : top, f = exp2f(M - ref);
+      M = top;
+      L *= f;  // NaN stays
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) acc[e] = CARE ? merge_add(0.0f, acc[e], f) : acc[e] * f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float w = exp2f(m[u] - ref);
+        L = fmaf(l[u], w, L);
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) acc[e] = CARE ? merge_add(acc[e], x[u][e], w) : fmaf(x[u][e], w, acc[e]);
       }
     }
-    float top = M;
-#pragma unroll
-    for (int u = 0; u < U; ++u) top = fmaxf(top, m[u]);
-    const float ref = top == -INFINITY ? 0.0f : top, f = exp2f(M - ref);
-    M = top;
-    L *= f;  // NaN stays
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) acc[e] = merge_add(0.0f, acc[e], f);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float w = exp2f(m[u] - ref);
-      L = fmaf(l[u], w, L);
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) acc[e] = merge_add(acc[e], x[u][e], w);
-    }
-  }
+  };
+  partitions(std::false_type());
+  if (odd()) partitions(std::true_type());
   if (wpr > 1) {
 #pragma unroll
     for (int e = 0; e < EPL; ++e) sm_acc[warp][lane * EPL + e] = acc[e];
@@ -196,15 +214,22 @@ __global__ void __launch_bounds__(256) rows_merge_kernel(RowsParams p, int wpr) 
     if (sub != 0) return;
     for (int w = 1; w < wpr; ++w) M = fmaxf(M, sm_m[warp + w]);
     const float ref = M == -INFINITY ? 0.0f : M;
-    L = 0.0f;
+    auto warps = [&](auto care) {
+      L = 0.0f;
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) acc[e] = 0.0f;
-    for (int w = 0; w < wpr; ++w) {
-      const float f = exp2f(sm_m[warp + w] - ref);
-      L = fmaf(sm_l[warp + w], f, L);
+      for (int e = 0; e < EPL; ++e) acc[e] = 0.0f;
+      for (int w = 0; w < wpr; ++w) {
+        const float f = exp2f(sm_m[warp + w] - ref);
+        L = fmaf(sm_l[warp + w], f, L);
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) acc[e] = merge_add(acc[e], sm_acc[warp + w][lane * EPL + e], f);
-    }
+        for (int e = 0; e < EPL; ++e) {
+          const float x = sm_acc[warp + w][lane * EPL + e];
+          acc[e] = decltype(care)::value ? merge_add(acc[e], x, f) : fmaf(x, f, acc[e]);
+        }
+      }
+    };
+    warps(std::false_type());
+    if (odd()) warps(std::true_type());
   }
   if (!live) return;
   const float inv = 1.0f / denominator(L, sr.ctx > sr.n || draft_mask(p, sr.q0, row / p.num_q_heads, sr.n) != 0);
