@@ -179,8 +179,222 @@ __global__ void __launch_bounds__(kThreads, 2)
   auto timeout = [&] { record_error(&g_rows_error, PK_DEVERR_TIMEOUT, blockIdx.x); };
 
   // Registers change hands by whole warpgroups: all four warps of one have to execute
-  // the same instruction, so each stands before the warps' ways part.
-  if (warp < 4) {
+  // the same instruction, so it stands before the roles of the second one part.
+  if (warp >= 4) {
+    setmaxnreg_dec<kOtherRegs>();
+    if (warp == 4) {
+      // ---------------- producer ----------------
+      if (lane == 0) {
+        prefetch_tensormap(&kmap);
+        prefetch_tensormap(&vmap);
+      }
+      // A pair of tiles to load: the lane's block of it, read from the table ahead
+      // of time.
+      struct Pair {
+        int phys, nblk, kvh, s;  // nblk 0: no more
+      };
+      const Unit *at = nullptr;  // the unit that `next` is in, its pairs so far, its number
+      int at_g = 0, at_n = 0, at_i = -1;
+      bool ok = true;
+      auto next = [&] {
+        Pair x{0, 0, 0, 0};
+        if (at && ++at_g == at_n) at = nullptr;
+        if (!at) {
+          ++at_i;
+          if (!warp_wait(u_full(at_i), u_phase(at_i), ok)) return x;
+          const Unit *c = units + at_i % kUnits;
+          if (c->s < 0) return x;
+          at = c, at_g = 0, at_n = (c->nt + 1) / 2;
+        }
+        // The unit after this one is asked for two pairs before the end: early enough
+        // to be here in time, late enough to go to the CTA that is free first.
+        if (at_g == max(0, at_n - 2) && lane == 0) mbar_arrive(u_want);
+        const int nb = (at->end - at->start + BS - 1) / BS;
+        x.nblk = min(S::BPP, nb - at_g * S::BPP);
+        x.kvh = at->kvh;
+        x.s = at->s;
+        if (lane < x.nblk)
+          x.phys = __ldg(p.tables + size_t(at->s) * p.max_blocks + at->start / BS + at_g * S::BPP + lane);
+        if (x.phys < 0 || x.phys >= p.num_blocks) {
+          record_error(&g_rows_error, PK_DEVERR_BLOCK_ID, at->s);
+          x.phys = 0;  // stay in bounds and keep the byte count; the result is flagged
+        }
+        if (at_g == at_n - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(u_empty(at_i));  // done with the unit's entry
+        }
+        return x;
+      };
+      // The blocks [b0, b0 + n) of a pair into dst, their rows' slabs `slab` apart.
+      auto load = [&](const CUtensorMap *map, uint32_t dst, int slab, uint32_t full, const Pair &x, int b0, int n) {
+        if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(n * S::SLABS * BS * 128));
+        __syncwarp();
+        if (lane >= b0 && lane < b0 + n) {
+#pragma unroll
+          for (int h = 0; h < S::SLABS; ++h)
+            tma_load_3d(dst + h * slab + (lane - b0) * BS * 128, map, full, h * 64, x.kvh, x.phys * BS);
+        }
+      };
+      // A pair's K goes when the scores of the one before are done, its V tiles when
+      // the products before have ended; the block table is read ahead of both.
+      int g = 0, f = 0;  // pairs whose V, and second halves whose V, are loaded
+      Pair a{0, 0, 0, 0}, b = next();
+      while (ok && (a.nblk || b.nblk)) {
+        if (a.nblk) {
+          // o_done(0) of pair g - 1 is its phase g - 1.
+          if (!(ok = g < 1 || mbar_wait(o_done(0), (g - 1) & 1))) break;
+          load(&vmap, v_sm, S::V_SLAB, v_full(0), a, 0, min(a.nblk, S::BPT));
+          if (a.nblk > S::BPT) {
+            if (!(ok = f < 1 || mbar_wait(o_done(1), (f - 1) & 1))) break;
+            load(&vmap, v_sm + S::V_BYTES, S::V_SLAB, v_full(1), a, S::BPT, a.nblk - S::BPT);
+            ++f;
+          }
+          ++g;
+        }
+        if (b.nblk) {
+          // Pair g's K: the scores of pair g - 1 are done.
+          if (!(ok = g < 1 || mbar_wait(k_empty, (g - 1) & 1))) break;
+          load(&kmap, k_sm, S::K_SLAB, k_full, b, 0, b.nblk);
+        }
+        a = b;
+        b = a.nblk ? next() : Pair{0, 0, 0, 0};
+      }
+      if (!ok && lane == 0) timeout();
+      // Let every issued copy land before the warp leaves.
+      if (g > 0) mbar_wait(k_full, (g - 1) & 1), mbar_wait(v_full(0), (g - 1) & 1);
+      if (f > 0) mbar_wait(v_full(1), (f - 1) & 1);
+    } else if (warp == 5) {
+      // ---------------- scores ----------------
+      // The whole warp goes over the tiles, so that descriptors and addresses are
+      // uniform values, and one elected lane issues. Scores and values have a warp
+      // each: a wait on a barrier costs some 200 cycles even when its phase has
+      // ended, and in one warp the waits and issues of both took longer than the
+      // products. Every order between the two is by barrier.
+      // A negative scale negates the queries, so that scores order as their
+      // exponents do.
+      const uint32_t s_desc = mma_desc(kRows, kPair, false) | (p.scale_log2 < 0.0f ? kNegateA : 0u);
+      const uint64_t q_d = smem_desc(q_sm, 16, 1024), k_d = smem_desc(k_sm, 16, 1024);
+      bool ok = true;
+      int g = 0, f = 0;
+      bool whole = false;  // the pair before had a second half
+      for (int i = 0; warp_wait(u_full(i), u_phase(i), ok); ++i) {
+        const int nt = units[i % kUnits].nt;
+        const bool last = units[i % kUnits].s < 0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(u_empty(i));
+        if (last || !warp_wait(q_ready, i & 1, ok)) break;
+        for (int j = 0; j < nt; j += 2, ++g) {
+          // The score columns hold the weights of the pair before until its last
+          // product ends (products end in order).
+          if (!warp_wait(k_full, g & 1, ok)) break;
+          if (g > 0 && !(whole ? warp_wait(o_done(1), (f - 1) & 1, ok) : warp_wait(o_done(0), (g - 1) & 1, ok))) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)  // a descriptor's address counts 16 bytes
+              tc_mma_ss(tmem, q_d + (ks / 4) * (S::Q_SLAB / 16) + (ks % 4) * 2,
+                        k_d + (ks / 4) * (S::K_SLAB / 16) + (ks % 4) * 2, s_desc, ks > 0);
+            tc_commit(k_empty);
+            tc_commit(s_full);
+          }
+          whole = j + 1 < nt;
+          f += whole;
+        }
+        if (!ok) break;
+      }
+      if (!ok && lane == 0) timeout();
+      // Nothing of this warp's products is under way when tensor memory is freed.
+      if (g > 0) mbar_wait(s_full, (g - 1) & 1);
+      __syncwarp();
+    } else if (warp == 6) {
+      // ---------------- weights times values ----------------
+      constexpr uint32_t O_DESC = mma_desc(kRows, D, true);
+      const uint64_t v_d = smem_desc(v_sm, S::V_SLAB, 1024);
+      bool ok = true;
+      int g = 0, f = 0;
+      for (int i = 0; warp_wait(u_full(i), u_phase(i), ok); ++i) {
+        const int nt = units[i % kUnits].nt;
+        const bool last = units[i % kUnits].s < 0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(u_empty(i));
+        if (last) break;
+        for (int j = 0; j < nt; ++j) {
+          const int h = j & 1;
+          const uint32_t phase = uint32_t(h ? f : g) & 1u;
+          if (!warp_wait(v_full(h), phase, ok) || !warp_wait(p_full(h), phase, ok)) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t d = v_d + (h ? S::V_BYTES / 16 : 0);
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+              for (int ks = 0; ks < kTile / 16; ++ks)
+                tc_mma_ts(t_o, t_s(h) + 32 * half + 8 * ks, d + ks * 128, O_DESC, j > 0 || half > 0 || ks > 0);
+            tc_commit(o_done(h));  // and the V tile is free
+          }
+          f += h;
+          g += h || j + 1 == nt;
+        }
+        if (!ok) break;
+      }
+      if (!ok && lane == 0) timeout();
+      if (g > 0) mbar_wait(o_done(0), (g - 1) & 1);
+      if (f > 0) mbar_wait(o_done(1), (f - 1) & 1);
+      __syncwarp();
+    } else {
+      // ---------------- units ----------------
+      // The grid has a CTA per unit, longest first; those that find no room are
+      // taken over, one at a time, by whichever CTA needs work next.
+      const int X = p.num_kv_heads * p.row_tiles, Y = p.items ? p.num_items : p.num_seqs;
+      bool ok = true;
+      int published = 0;
+      auto publish = [&](const Unit &c) {
+        const int i = published;
+        if (i >= kUnits && !warp_wait(u_empty(i), u_phase(i - kUnits), ok)) return;
+        if (lane == 0) {
+          units[i % kUnits] = c;
+          mbar_arrive(u_full(i));
+        }
+        ++published;
+      };
+      for (int u = blockIdx.x, asked = 0; u >= 0;) {
+        const int x = u % X, y = (u / X) % Y, z = u / X / Y;
+        Unit c;
+        if (work_item(p, y, p.num_partitions - 1 - z, x == 0 && lane == 0, c.s, c.part)) {
+          const SeqRows sr = seq_rows(p, c.s, x == 0 && lane == 0 && c.part == 0);
+          c.kvh = x / p.row_tiles;
+          c.r0 = x % p.row_tiles * kRows;
+          c.rows = min(kRows, sr.n * G - c.r0);
+          if (c.rows > 0 && sr.ctx == 0) {  // invalid length (recorded): zero rows
+            for (int k = lane; c.part == 0 && k < c.rows * (D / 8); k += 32)
+              *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
+                                         q_row(sr.q0, c.r0 + k / (D / 8), c.kvh) + k % (D / 8) * 8) =
+                  make_uint4(0, 0, 0, 0);
+          } else if (c.rows > 0 && c.part < sr.np) {
+            c.q0 = sr.q0, c.n = sr.n, c.ctx = sr.ctx, c.np = sr.np;
+            c.start = c.part * p.partition;
+            c.end = min(sr.ctx, c.start + p.partition);
+            c.nt = (c.end - c.start + kTile - 1) / kTile;
+            publish(c);
+            if (!ok || !warp_wait(u_want, (published - 1) & 1, ok)) break;
+          }
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(u_answer, 16);
+          try_cancel(smem_addr(&answer), u_answer);
+        }
+        if (!warp_wait(u_answer, asked & 1, ok)) break;
+        ++asked;
+        u = cancelled_cta(smem_addr(&answer));
+        fence_answer_read();
+        __syncwarp();
+      }
+      Unit end;
+      end.s = -1;
+      if (ok) publish(end);
+      if (!ok && lane == 0) timeout();
+    }
+  } else {
     // ---------------- softmax: a thread is a row ----------------
     setmaxnreg_inc<kSoftmaxRegs>();
     const int r = threadIdx.x;
@@ -520,221 +734,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       release();
       tc_fence_before();  // O may be overwritten once the next unit's weights are there
     }
-    if (!ok && lane == 0) timeout();
-  } else {
-    setmaxnreg_dec<kOtherRegs>();
-  }
-
-  if (warp == 4) {
-    // ---------------- producer ----------------
-    if (lane == 0) {
-      prefetch_tensormap(&kmap);
-      prefetch_tensormap(&vmap);
-    }
-    // A pair of tiles to load: the lane's block of it, read from the table ahead
-    // of time.
-    struct Pair {
-      int phys, nblk, kvh, s;  // nblk 0: no more
-    };
-    const Unit *at = nullptr;  // the unit that `next` is in, its pairs so far, its number
-    int at_g = 0, at_n = 0, at_i = -1;
-    bool ok = true;
-    auto next = [&] {
-      Pair x{0, 0, 0, 0};
-      if (at && ++at_g == at_n) at = nullptr;
-      if (!at) {
-        ++at_i;
-        if (!warp_wait(u_full(at_i), u_phase(at_i), ok)) return x;
-        const Unit *c = units + at_i % kUnits;
-        if (c->s < 0) return x;
-        at = c, at_g = 0, at_n = (c->nt + 1) / 2;
-      }
-      // The unit after this one is asked for two pairs before the end: early enough
-      // to be here in time, late enough to go to the CTA that is free first.
-      if (at_g == max(0, at_n - 2) && lane == 0) mbar_arrive(u_want);
-      const int nb = (at->end - at->start + BS - 1) / BS;
-      x.nblk = min(S::BPP, nb - at_g * S::BPP);
-      x.kvh = at->kvh;
-      x.s = at->s;
-      if (lane < x.nblk)
-        x.phys = __ldg(p.tables + size_t(at->s) * p.max_blocks + at->start / BS + at_g * S::BPP + lane);
-      if (x.phys < 0 || x.phys >= p.num_blocks) {
-        record_error(&g_rows_error, PK_DEVERR_BLOCK_ID, at->s);
-        x.phys = 0;  // stay in bounds and keep the byte count; the result is flagged
-      }
-      if (at_g == at_n - 1) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(u_empty(at_i));  // done with the unit's entry
-      }
-      return x;
-    };
-    // The blocks [b0, b0 + n) of a pair into dst, their rows' slabs `slab` apart.
-    auto load = [&](const CUtensorMap *map, uint32_t dst, int slab, uint32_t full, const Pair &x, int b0, int n) {
-      if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(n * S::SLABS * BS * 128));
-      __syncwarp();
-      if (lane >= b0 && lane < b0 + n) {
-#pragma unroll
-        for (int h = 0; h < S::SLABS; ++h)
-          tma_load_3d(dst + h * slab + (lane - b0) * BS * 128, map, full, h * 64, x.kvh, x.phys * BS);
-      }
-    };
-    // A pair's K goes when the scores of the one before are done, its V tiles when
-    // the products before have ended; the block table is read ahead of both.
-    int g = 0, f = 0;  // pairs whose V, and second halves whose V, are loaded
-    Pair a{0, 0, 0, 0}, b = next();
-    while (ok && (a.nblk || b.nblk)) {
-      if (a.nblk) {
-        // o_done(0) of pair g - 1 is its phase g - 1.
-        if (!(ok = g < 1 || mbar_wait(o_done(0), (g - 1) & 1))) break;
-        load(&vmap, v_sm, S::V_SLAB, v_full(0), a, 0, min(a.nblk, S::BPT));
-        if (a.nblk > S::BPT) {
-          if (!(ok = f < 1 || mbar_wait(o_done(1), (f - 1) & 1))) break;
-          load(&vmap, v_sm + S::V_BYTES, S::V_SLAB, v_full(1), a, S::BPT, a.nblk - S::BPT);
-          ++f;
-        }
-        ++g;
-      }
-      if (b.nblk) {
-        // Pair g's K: the scores of pair g - 1 are done.
-        if (!(ok = g < 1 || mbar_wait(k_empty, (g - 1) & 1))) break;
-        load(&kmap, k_sm, S::K_SLAB, k_full, b, 0, b.nblk);
-      }
-      a = b;
-      b = a.nblk ? next() : Pair{0, 0, 0, 0};
-    }
-    if (!ok && lane == 0) timeout();
-    // Let every issued copy land before the warp leaves.
-    if (g > 0) mbar_wait(k_full, (g - 1) & 1), mbar_wait(v_full(0), (g - 1) & 1);
-    if (f > 0) mbar_wait(v_full(1), (f - 1) & 1);
-  } else if (warp == 5) {
-    // ---------------- scores ----------------
-    // The whole warp goes over the tiles, so that descriptors and addresses are
-    // uniform values, and one elected lane issues. Scores and values have a warp
-    // each: a wait on a barrier costs some 200 cycles even when its phase has
-    // ended, and in one warp the waits and issues of both took longer than the
-    // products. Every order between the two is by barrier.
-    // A negative scale negates the queries, so that scores order as their
-    // exponents do.
-    const uint32_t s_desc = mma_desc(kRows, kPair, false) | (p.scale_log2 < 0.0f ? kNegateA : 0u);
-    const uint64_t q_d = smem_desc(q_sm, 16, 1024), k_d = smem_desc(k_sm, 16, 1024);
-    bool ok = true;
-    int g = 0, f = 0;
-    bool whole = false;  // the pair before had a second half
-    for (int i = 0; warp_wait(u_full(i), u_phase(i), ok); ++i) {
-      const int nt = units[i % kUnits].nt;
-      const bool last = units[i % kUnits].s < 0;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(u_empty(i));
-      if (last || !warp_wait(q_ready, i & 1, ok)) break;
-      for (int j = 0; j < nt; j += 2, ++g) {
-        // The score columns hold the weights of the pair before until its last
-        // product ends (products end in order).
-        if (!warp_wait(k_full, g & 1, ok)) break;
-        if (g > 0 && !(whole ? warp_wait(o_done(1), (f - 1) & 1, ok) : warp_wait(o_done(0), (g - 1) & 1, ok))) break;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)  // a descriptor's address counts 16 bytes
-            tc_mma_ss(tmem, q_d + (ks / 4) * (S::Q_SLAB / 16) + (ks % 4) * 2,
-                      k_d + (ks / 4) * (S::K_SLAB / 16) + (ks % 4) * 2, s_desc, ks > 0);
-          tc_commit(k_empty);
-          tc_commit(s_full);
-        }
-        whole = j + 1 < nt;
-        f += whole;
-      }
-      if (!ok) break;
-    }
-    if (!ok && lane == 0) timeout();
-    // Nothing of this warp's products is under way when tensor memory is freed.
-    if (g > 0) mbar_wait(s_full, (g - 1) & 1);
-    __syncwarp();
-  } else if (warp == 6) {
-    // ---------------- weights times values ----------------
-    constexpr uint32_t O_DESC = mma_desc(kRows, D, true);
-    const uint64_t v_d = smem_desc(v_sm, S::V_SLAB, 1024);
-    bool ok = true;
-    int g = 0, f = 0;
-    for (int i = 0; warp_wait(u_full(i), u_phase(i), ok); ++i) {
-      const int nt = units[i % kUnits].nt;
-      const bool last = units[i % kUnits].s < 0;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(u_empty(i));
-      if (last) break;
-      for (int j = 0; j < nt; ++j) {
-        const int h = j & 1;
-        const uint32_t phase = uint32_t(h ? f : g) & 1u;
-        if (!warp_wait(v_full(h), phase, ok) || !warp_wait(p_full(h), phase, ok)) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t d = v_d + (h ? S::V_BYTES / 16 : 0);
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int ks = 0; ks < kTile / 16; ++ks)
-              tc_mma_ts(t_o, t_s(h) + 32 * half + 8 * ks, d + ks * 128, O_DESC, j > 0 || half > 0 || ks > 0);
-          tc_commit(o_done(h));  // and the V tile is free
-        }
-        f += h;
-        g += h || j + 1 == nt;
-      }
-      if (!ok) break;
-    }
-    if (!ok && lane == 0) timeout();
-    if (g > 0) mbar_wait(o_done(0), (g - 1) & 1);
-    if (f > 0) mbar_wait(o_done(1), (f - 1) & 1);
-    __syncwarp();
-  } else if (warp == 7) {
-    // ---------------- units ----------------
-    // The grid has a CTA per unit, longest first; those that find no room are
-    // taken over, one at a time, by whichever CTA needs work next.
-    const int X = p.num_kv_heads * p.row_tiles, Y = p.items ? p.num_items : p.num_seqs;
-    bool ok = true;
-    int published = 0;
-    auto publish = [&](const Unit &c) {
-      const int i = published;
-      if (i >= kUnits && !warp_wait(u_empty(i), u_phase(i - kUnits), ok)) return;
-      if (lane == 0) {
-        units[i % kUnits] = c;
-        mbar_arrive(u_full(i));
-      }
-      ++published;
-    };
-    for (int u = blockIdx.x, asked = 0; u >= 0;) {
-      const int x = u % X, y = (u / X) % Y, z = u / X / Y;
-      Unit c;
-      if (work_item(p, y, p.num_partitions - 1 - z, x == 0 && lane == 0, c.s, c.part)) {
-        const SeqRows sr = seq_rows(p, c.s, x == 0 && lane == 0 && c.part == 0);
-        c.kvh = x / p.row_tiles;
-        c.r0 = x % p.row_tiles * kRows;
-        c.rows = min(kRows, sr.n * G - c.r0);
-        if (c.rows > 0 && sr.ctx == 0) {  // invalid length (recorded): zero rows
-          for (int k = lane; c.part == 0 && k < c.rows * (D / 8); k += 32)
-            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
-                                       q_row(sr.q0, c.r0 + k / (D / 8), c.kvh) + k % (D / 8) * 8) =
-                make_uint4(0, 0, 0, 0);
-        } else if (c.rows > 0 && c.part < sr.np) {
-          c.q0 = sr.q0, c.n = sr.n, c.ctx = sr.ctx, c.np = sr.np;
-          c.start = c.part * p.partition;
-          c.end = min(sr.ctx, c.start + p.partition);
-          c.nt = (c.end - c.start + kTile - 1) / kTile;
-          publish(c);
-          if (!ok || !warp_wait(u_want, (published - 1) & 1, ok)) break;
-        }
-      }
-      if (lane == 0) {
-        mbar_arrive_expect_tx(u_answer, 16);
-        try_cancel(smem_addr(&answer), u_answer);
-      }
-      if (!warp_wait(u_answer, asked & 1, ok)) break;
-      ++asked;
-      u = cancelled_cta(smem_addr(&answer));
-      fence_answer_read();
-      __syncwarp();
-    }
-    Unit end;
-    end.s = -1;
-    if (ok) publish(end);
     if (!ok && lane == 0) timeout();
   }
   tc_fence_before();
