@@ -446,7 +446,8 @@ pk_status pk_qk_norm_rope_and_cache(
  * e is the smallest integer >= -100 with 448 * 2^e >= the row's largest finite
  * magnitude (0 for a row of zeros), each code the e4m3 number nearest to
  * x * 2^-e (ties to even). Infinities and NaN become the NaN code. Values are
- * exact in bf16, and writing them again gives the same values. The descriptor's
+ * exact in bf16 (but for 2^128, to which magnitudes from 0.97 2^128 on round: it
+ * reads back as infinity), and writing them again gives the same values. The descriptor's
  * dtype is PK_E4M3, d a multiple of 16 and at most 256; kv_exp is 16-byte
  * aligned. */
 
@@ -477,7 +478,11 @@ pk_status pk_copy_blocks_e4m3(void *k_cache, void *v_cache, uint8_t *kv_exp,
  * values, with q and out of io_dtype (PK_F32 or PK_BF16). Arguments, clamping
  * and recorded events as there and in pk_paged_attention_decode_items;
  * work_items may be NULL (then num_items is 0 and the (sequence, partition)
- * grid runs). head_dim 64 or 128, B 8, 16 or 32, Hq / Hk at most 8. */
+ * grid runs). head_dim 64 or 128, B 8, 16 or 32, Hq / Hk at most 8.
+ * Precision: bf16 queries enter exactly (elements below 2^-32 of a head's
+ * largest lose bits), fp32 queries and the softmax weights with 22 bits; sums
+ * are fp32. A NaN that a query sees, in it or in the cache, makes its result NaN
+ * (a value's: that element). */
 pk_status pk_paged_attention_decode_e4m3(
     void *out, const void *q, pk_dtype io_dtype, const void *k_cache, const void *v_cache,
     const uint8_t *kv_exp, const int32_t *block_tables, const int32_t *context_lens, float scale,
@@ -495,7 +500,13 @@ pk_status pk_paged_attention_decode_e4m3(
  * t < base and to the draft at base + j where bit j of tree_mask[q_offsets[s] +
  * i] is set (bits n and up are ignored). Without masks the drafts are a chain:
  * draft i sees drafts 0 .. i. A draft that sees nothing gets zeros; what a
- * token that it does not see holds, NaN included, does not reach it.
+ * token that it does not see holds, NaN included, does not reach it. What it
+ * sees acts as in the formula: a NaN in the query or a seen key makes the row
+ * (a query head's) NaN, and so do scores of -inf alone; an infinite or NaN value
+ * reaches its element.
+ * Precision: of an fp32 pool, factors of 24 bits and fp32 sums; of a bf16 pool,
+ * weights of 16 bits, and sums that the tensor cores cut off toward zero, up to
+ * some 10^-4 after 32 768 tokens of one partition (results round to 2^-9).
  *   out, q        [num_q_tokens, Hq, d], dtype of the pool; sequence s's rows
  *                 are q_offsets[s] .. q_offsets[s + 1] - 1, and rows of no
  *                 sequence are neither read nor written.
@@ -509,7 +520,8 @@ pk_status pk_paged_attention_decode_e4m3(
  *   tree_mask     uint64 [num_q_tokens], or NULL (see pk_tree_masks).
  *   max_draft_len at most PK_MAX_DRAFT (sizes the grid).
  *   partition_size, work_items  0 and NULL: each context whole; otherwise
- *                 pk_tree_plan's (work_items NULL: the grid of every partition).
+ *                 pk_tree_plan's (work_items NULL: the grid of every partition),
+ *                 at most 65535 items.
  *   workspace     pk_tree_workspace_size bytes when the contexts are split.
  * dtype PK_F32 or PK_BF16, head_dim 64 or 128, Hq / Hk at most 8. */
 #define PK_MAX_DRAFT 64

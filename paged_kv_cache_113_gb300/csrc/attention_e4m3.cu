@@ -26,12 +26,12 @@
 // their sum overflows only past 2^13 tokens of which no value reaches 2^-90.
 //
 // mma.sync carries it: with 8 rows of query for 2 (d + 1) bytes the tensor cores
-// are 14% busy, and the widening to fp16 has to pass registers in any case, where
+// are 19 to 22% busy, and the widening to fp16 has to pass registers in any case, where
 // tcgen05 would want it back in shared memory.
 //
 // Measured (bf16 queries, 64 = 8 x 8 heads of 128 unless said): 8 sequences of
-// 32 768 tokens in 89 to 90 us, 6.05 TB/s (89% of a copy); 256 of some 500 (33 to
-// 4608) tokens, 32 = 4 x 8 heads, in 50 to 52, 4.9 to 5.1 TB/s (74%): there the
+// 32 768 tokens in 91 to 92 us, 5.9 TB/s (87% of a copy); 256 of some 500 (33 to
+// 4608) tokens, 32 = 4 x 8 heads, in 50 to 54, 4.7 to 5.1 TB/s (69 to 75%): there the
 // first stage is full 4.8 us after the launch (items, lengths and tables, then
 // codes, each from cold memory), and the last CTAs end 7 us apart. A stage costs
 // the producer 620 cycles of issue for its eight tensor loads, of 2100 to 2400;
@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(kThreads, 3)
     // taken over, one at a time, by whichever CTA needs work next. The next unit is
     // asked for kAhead stages before the end of this one: early enough to be here in
     // time, late enough to go to the CTA that is free first (4, 5, 6 and 8 stages:
-    // 52, 50, 50.3 and 53 us for the 256 short sequences).
+    // 52, 50, 50.3 and 53 us for 256 sequences of some 500 tokens; of lengths more
+    // uneven, of heads of 64, of blocks of 8 and for 8 x 32 768 tokens all within 1%).
     if (lane == 0) {
       prefetch_tensormap(&kmap);
       prefetch_tensormap(&vmap);

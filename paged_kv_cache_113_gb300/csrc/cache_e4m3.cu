@@ -21,6 +21,8 @@
 // Read back, a lane has the elements of 16 bytes of the result, of two rows, so that
 // a warp's stores are whole lines: 32 768 such tokens take 34.8 us, 5.8 TB/s, as fp32
 // 56; 16 codes a lane took 37.4 and 74, one row a lane 38.5 and 64, four 36.9 and 56.
+// Copied, 4096 pairs of blocks of 16 such tokens (270 MB moved) take 59 us, 4.6 TB/s:
+// a thread has one 16-byte vector; 64 pairs 7.4 us.
 // Up to some hundred tokens a call is bounded by its launch.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>

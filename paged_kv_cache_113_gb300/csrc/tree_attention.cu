@@ -37,7 +37,7 @@
 // formula's work, 1.2 PFLOP/s with the second half of the weights; with 1 to 16
 // drafts (one unit of 128 rows reads all) 173 to 193 us, 5.6 to 6.2 TB/s. 256
 // sequences of some 500 (64 to 4608) tokens with 16 drafts, 32 = 4 x 8 heads, 98 to
-// 101 us, 5.3 TB/s (78% of a copy). There units dealt out at launch took 149 us
+// 105 us, 5.1 to 5.3 TB/s (75 to 78% of a copy). There units dealt out at launch took 149 us
 // against 115 by launch control; then 100 by shortening what a unit's end costs its
 // softmax warps (a timeline: 2700 cycles to ask for the next unit's queries, 1700 to
 // look for values that are not finite, and fences that waited for the last unit's
@@ -791,7 +791,7 @@ pk_status launch_tree_d(const RowsParams &p, const pk_cache_desc &d, cudaStream_
 // Measured (fp32, 64 sequences of some 1000 tokens, 32 = 4 x 8 heads of 128): 16
 // drafts 431 us (404 with sums left to the tensor cores, whose error grew to 5 10^-5
 // at 32 768 tokens; 652 with three tf32 products, 797 with fp32 FMAs), 4 drafts 151
-// us (554 with FMAs), one draft 109 us: bounded by the splitting of K and V into
+// us (554 with FMAs), one draft 109 to 113 us: bounded by the splitting of K and V into
 // parts and the products' issue, not by memory (half of its rate at 4 drafts).
 // ---------------------------------------------------------------------------
 template <typename T, int D, int NT>
@@ -1164,8 +1164,11 @@ pk_status launch_split(RowsParams p, cudaStream_t stream) {
 // rows of 64 values are too little for its 128 lanes and its chain of a pair, and
 // attn_split_kernel, with more CTAs an SM, reads faster (us, tcgen05 and split):
 // 256 x 500 tokens, 4 x 8 heads, one draft 76 and 62, two 76 and 66, four (16 rows)
-// 76 and 91; 8 x 32 768 tokens 118 and 103, 118 and 105, 119 and 115. With rows of
-// 128 values it does not: 99 and 117, 172 and 234 with one draft.
+// 76 and 91; 8 x 32 768 tokens 118 and 103, 118 and 105, 119 and 115. Between, with a
+// query head per KV head: 256 x 510 tokens of very uneven lengths, 8 rows 80 and 84, 9
+// to 16 rows 81 and 93 to 96; 8 x 32 768 tokens, 8 rows 125 and 103, 9 to 16 rows 125
+// and 116 to 119. With rows of 128 values it does not: 99 and 117, 172 and 234 with one
+// draft.
 bool tcgen05_path(const pk_cache_desc &d, int64_t rows) {
   return d.dtype == PK_BF16 && (d.block_size == 8 || d.block_size == 16 || d.block_size == 32) &&
          (d.head_dim == 128 || rows > 8);
