@@ -76,7 +76,8 @@ enum {
     PK_DEVERR_TIMEOUT = 5,     /* a pipeline wait gave up (never expected)             */
     PK_DEVERR_ORDER = 6,       /* seq_order entry outside [0, num_seqs)                */
     PK_DEVERR_POSITION = 7,    /* positions entry outside [0, max_position)            */
-    PK_DEVERR_OFFSETS = 8      /* q_offsets entry that is no range of the query rows   */
+    PK_DEVERR_OFFSETS = 8,     /* q_offsets entry that is no range of the query rows   */
+    PK_DEVERR_DRAFT = 9        /* drafted token, parent or kept row out of range        */
 };
 
 /* Geometry of one layer's KV pool. */
@@ -556,6 +557,142 @@ pk_status pk_tree_plan(const int32_t *context_lens, int32_t num_seqs, int32_t ma
 size_t pk_tree_workspace_size(int32_t num_q_tokens, int32_t num_q_heads, int32_t max_context_len,
                               int32_t partition_size, const pk_cache_desc *desc);
 
+/* ------------------------------------------------------------------------ */
+/* Attention of new tokens with changed scores                              */
+/* ------------------------------------------------------------------------ */
+/* What is done to the scores of pk_paged_attention_extend, and what a row sees.
+ * Arrays are device memory. All zero: plain causal attention. */
+typedef struct {
+    float softcap;                /* c > 0: x becomes c tanh(x / c); 0: not capped       */
+    int32_t window;               /* w > 0: a row sees no token before position - w + 1  */
+    const float *slopes;          /* [Hq] or NULL: x -= slope |position - t|             */
+    const int32_t *prefix_lens;   /* [S] or NULL: every row sees the tokens before it    */
+    const int32_t *first_tokens;  /* [num_q_tokens] or NULL: the first token a row sees  */
+} pk_score_desc;
+
+/* Attention of each sequence's new tokens over its paged context, for prompts,
+ * chunks of prompts and single decoded tokens. Sequence s has n = q_offsets[s + 1] -
+ * q_offsets[s] new tokens, the last n of its context, whose K/V are in the cache
+ * already. Token i of them, at position pos = context_lens[s] - n + i, sees token t
+ * where lo <= t < hi:
+ *     hi = max(pos + 1, min(prefix_lens[s], context_lens[s]))
+ *     lo = max(0, pos - window + 1, first_tokens[row])
+ * (a prefix that is read both ways; a sliding window; packed documents, with
+ * first_tokens the beginning of the row's document) and, for query head h,
+ *     x_t = scale <q[row, h], K_t>;  x_t = c tanh(x_t / c);  x_t -= slopes[h] |pos - t|
+ *     out[row, h] = sum_t softmax(x)_t V_t.
+ * A row that sees nothing, or scores of -inf alone, gets zeros. What a row does not
+ * see, NaN included, does not reach it; a value that is not finite where it is seen
+ * makes its element not finite, a NaN query, key or score the row.
+ * Precision: of an fp32 pool, factors of 24 bits and fp32 sums; of a bf16 pool,
+ * weights of 16 bits (of 8 bits, divided by the sum of the same, where a sequence has
+ * more than 8 rows, new tokens times Hq / Hk), fp32 sums of the tensor cores.
+ *   out, q        [num_q_tokens, Hq, d], dtype of the pool; rows of no sequence are
+ *                 neither read nor written.
+ *   q_offsets     int32 [S + 1], ascending, or NULL: row s is sequence s's only new
+ *                 token (max_query_len 1). An entry that is no range of the rows, or
+ *                 longer than max_query_len, is recorded (PK_DEVERR_OFFSETS) and its
+ *                 sequence is skipped.
+ *   context_lens  int32 [S], new tokens included: n <= length <=
+ *                 min(max_context_len, max_blocks_per_seq * B), clamped and recorded
+ *                 otherwise (PK_DEVERR_CONTEXT; a length below n gives zero rows).
+ *   scores        NULL: plain causal attention. softcap finite and not negative.
+ *   partition_size, work_items  0 and NULL: each context whole; otherwise
+ *                 pk_extend_plan's for the same max_query_len (work_items NULL: all
+ *                 units and partitions). An item that is no unit of the call's is
+ *                 skipped and recorded (PK_DEVERR_ORDER).
+ *   workspace     pk_extend_workspace_size bytes when the contexts are split.
+ * dtype PK_F32 or PK_BF16, head_dim 64 or 128, Hq / Hk at most 8. Bad table entries
+ * are recorded (PK_DEVERR_BLOCK_ID). */
+pk_status pk_paged_attention_extend(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                    const int32_t *block_tables, const int32_t *context_lens,
+                                    const int32_t *q_offsets, float scale, const pk_score_desc *scores,
+                                    int32_t num_seqs, int32_t num_q_tokens, int32_t max_query_len,
+                                    int32_t num_q_heads, int32_t max_blocks_per_seq,
+                                    int32_t max_context_len, int32_t partition_size,
+                                    const int32_t *work_items, int32_t num_items, void *workspace,
+                                    size_t workspace_bytes, const pk_cache_desc *desc, void *stream);
+
+/* Host planner for pk_paged_attention_extend: the partition size (-1: chosen from the
+ * lengths; > 0, a multiple of B, or 0: as given) and the work list of host context_lens
+ * and query_lens (NULL: one new token each; none above max_query_len), longest first.
+ * window: the call's, or 0 (then units before it are listed and end at once). items_out
+ * has room for `cap` items of four int32: (sequence, first row, rows, partition);
+ * *num_items_out receives the count, PK_ERR_INVALID_ARG if it exceeds cap. */
+pk_status pk_extend_plan(const int32_t *context_lens, const int32_t *query_lens, int32_t num_seqs,
+                         int32_t max_query_len, int32_t num_q_heads, int32_t window,
+                         int32_t partition_size, const pk_cache_desc *desc, int32_t *partition_out,
+                         int32_t *items_out, int32_t cap, int32_t *num_items_out);
+
+/* Workspace bytes of pk_paged_attention_extend for num_q_tokens rows: fp32 partials
+ * [num_q_tokens, Hq, P, d + 2], P = ceil(max_context_len / partition_size); 0 without a
+ * split or on invalid arguments. Calls whose work overlaps on the GPU must not share
+ * one. Host only. */
+size_t pk_extend_workspace_size(int32_t num_q_tokens, int32_t num_q_heads, int32_t max_context_len,
+                                int32_t partition_size, const pk_cache_desc *desc);
+
+/* ------------------------------------------------------------------------ */
+/* Verification of drafted tokens                                           */
+/* ------------------------------------------------------------------------ */
+/* Which drafted tokens are kept, and the token after them, so that what is kept is
+ * distributed as the target's own samples are. Sequence s has the rows
+ * q_offsets[s] .. q_offsets[s + 1] - 1: its root (the last token known), then its
+ * drafts, each after its parent; target_probs[row] is the target's distribution of the
+ * token after that row's. From the root on, the children of the row reached are taken
+ * in order: child i, with token t, u = uniforms[i] and the row's probabilities p, is
+ * accepted (and becomes the row reached) where
+ *     u M < p(t)              M = 1 - the p of the children refused before it; a token
+ *                             refused before has p = 0          (drafts chosen greedily)
+ *     u draft_probs[i](t) < p(t)                  (a chain drawn from draft_probs)
+ * until none is. The next token is drawn from that row: from p without the refused
+ * tokens, or from max(p - draft_probs[i], 0) of the refused draft i, or from p if none
+ * was refused or those weights are all 0. It is the lowest k whose weights up to and
+ * including k are more than r times all of them, r = uniforms[the root's row]. Sums and
+ * products are exact to 2^-45; probabilities that are not positive and finite count
+ * as 0.
+ *   num_accepted  int32 [S], accepted drafts (without the root).
+ *   accepted      int32 [num_rows]: at q_offsets[s] + k the k-th row of the path,
+ *                 counted from the sequence's first (0 is the root), -1 behind it.
+ *   next_tokens   int64 [S]; -1 where the row has no weight at all, or the sequence no
+ *                 rows (then num_accepted is 0).
+ *   target_probs, draft_probs  rows of vocab values of probs_dtype (PK_F32, PK_BF16),
+ *                 target_stride and draft_stride elements apart; draft_probs NULL: drafts
+ *                 chosen greedily. The roots' rows of draft_probs are not read.
+ *   tokens        int64 [num_rows] (the roots' are not read); uniforms fp32 [num_rows] in
+ *                 [0, 1).
+ *   parents       int32 [num_rows], the parent's place in the sequence (0 is the root;
+ *                 less than the row's own; the roots' are not read), or NULL: a chain.
+ *                 Only a chain has draft_probs (PK_ERR_UNSUPPORTED otherwise).
+ *   max_rows      rows of a sequence, at most PK_MAX_DRAFT.
+ * A token outside the vocabulary or a bad parent is recorded (PK_DEVERR_DRAFT) and its
+ * draft refused unseen; a bad range of rows is recorded (PK_DEVERR_OFFSETS) and its
+ * sequence gets 0 and -1. vocab at most 2^24. */
+pk_status pk_verify_drafts(int32_t *num_accepted, int32_t *accepted, int64_t *next_tokens,
+                           const void *target_probs, int64_t target_stride, const void *draft_probs,
+                           int64_t draft_stride, pk_dtype probs_dtype, const int64_t *tokens,
+                           const float *uniforms, const int32_t *q_offsets, const int32_t *parents,
+                           int32_t num_seqs, int32_t num_rows, int32_t max_rows, int32_t vocab,
+                           void *stream);
+
+/* The cached K and V of what pk_verify_drafts kept, moved together: with the n rows of
+ * sequence s the last n tokens of its context and base = context_lens[s] - n, the token
+ * at base + accepted[q_offsets[s] + k] moves to base + k, for k = 0 .. num_accepted[s].
+ * context_lens_out[s] (NULL: not wanted; not context_lens itself) receives base +
+ * num_accepted[s] + 1, to which pk_bm_truncate cuts the host's sequence; what lies
+ * behind it is free to be overwritten. One call per layer's pools. The blocks that hold
+ * the n tokens must be the sequence's own (as they are after pk_bm_append_slots).
+ * accepted has to ascend within the sequence's rows, num_accepted[s] to lie in
+ * [0, n - 1] (PK_DEVERR_DRAFT otherwise), and the context to hold n tokens and fit the
+ * table (PK_DEVERR_CONTEXT); such a sequence keeps its cache and length. A sequence
+ * without rows keeps its length; a token whose block's table entry is bad (recorded,
+ * PK_DEVERR_BLOCK_ID) is not moved. dtype PK_F32 or PK_BF16. */
+pk_status pk_compact_drafts(void *k_cache, void *v_cache, const int32_t *block_tables,
+                            int32_t max_blocks_per_seq, const int32_t *context_lens,
+                            const int32_t *q_offsets, const int32_t *accepted,
+                            const int32_t *num_accepted, int32_t *context_lens_out, int32_t num_seqs,
+                            int32_t num_rows, int32_t max_rows, const pk_cache_desc *desc,
+                            void *stream);
+
 /* A pure read stream over `bytes` (a multiple of 16; device memory, 16-byte
  * aligned): every 16-byte vector is loaded once and the loads are folded so
  * none can be dropped; *sink (device) is left unchanged in practice. A
@@ -617,6 +754,14 @@ pk_status pk_bm_fork(pk_bm *bm, int64_t parent, int64_t child);
 /* Decrements every block of the table; blocks reaching zero return to the
  * free list. */
 pk_status pk_bm_free_seq(pk_bm *bm, int64_t seq_id);
+
+/* Cuts a sequence to its first new_len tokens (0 <= new_len <= its length; swapped
+ * sequences: PK_ERR_INVALID_ARG), as after drafts were refused: the blocks behind lose a
+ * reference each, last first, and those that no table names any more are free again
+ * (cached ones stay cached). A shared or cached tail block stays as it is: the next
+ * append copies it on write. Resident tables of a decode step that holds the sequence
+ * are out of step then, as after any other change of it (tables_resident). */
+pk_status pk_bm_truncate(pk_bm *bm, int64_t seq_id, int64_t new_len);
 
 pk_status pk_bm_seq_len(const pk_bm *bm, int64_t seq_id, int64_t *len_out);
 

@@ -18,7 +18,13 @@ The functions carry the C ABI's names (``include/pagedkv.h``):
   8-bit cache: write, read back, block copies, decode attention;
 * :func:`pk_paged_attention_tree` -- attention of drafted tokens (a tree or a
   chain) over the cached context, with :func:`pk_tree_masks` and
-  :func:`pk_tree_plan`.
+  :func:`pk_tree_plan`;
+* :func:`pk_paged_attention_extend` -- attention of new tokens (a prompt, a
+  chunk, one token) with capped or biased scores, a window, a prefix or
+  documents, with :func:`pk_extend_plan`;
+* :func:`pk_verify_drafts`, :func:`pk_compact_drafts` -- drafted tokens
+  accepted or refused by the target's probabilities, and the kept ones moved
+  together in the cache.
 
 PyTorch provides device memory and streams: the device entry points take
 CUDA tensors and enqueue on the current stream unless one is given.
@@ -40,7 +46,8 @@ __all__ = [
     "pk_get_device_error", "pk_status_string", "BlockManager",
     "pk_qk_norm_rope_and_cache", "pk_reshape_and_cache_e4m3", "pk_gather_cache_e4m3", "pk_copy_blocks_e4m3",
     "pk_paged_attention_decode_e4m3", "pk_paged_attention_tree", "pk_tree_masks", "pk_tree_plan",
-    "pk_tree_workspace_size",
+    "pk_tree_workspace_size", "pk_paged_attention_extend", "pk_extend_plan", "pk_extend_workspace_size",
+    "pk_verify_drafts", "pk_compact_drafts",
     "PK_F32", "PK_BF16", "PK_E4M3", "PK_MAX_DRAFT", "IMPLS", "DEVERR_NAMES",
 ]
 
@@ -52,7 +59,7 @@ PK_MAX_DRAFT = 64  # drafted tokens per sequence of pk_paged_attention_tree
 IMPLS = {"auto": 0, "simt": 1, "mma": 2}
 PK_STATIC_WORKSPACE_BYTES = 64 << 20  # the static split-K scratch of pk_paged_attention_decode_static
 DEVERR_NAMES = {0: "none", 1: "slot", 2: "block_id", 3: "pair", 4: "context", 5: "timeout", 6: "order",
-                7: "position", 8: "offsets"}
+                7: "position", 8: "offsets", 9: "draft"}
 
 # Every symbol include/pagedkv.h declares.
 EXPORTED = (
@@ -73,7 +80,8 @@ EXPORTED = (
     "pk_bm_is_cached", "pk_bm_free_blocks", "pk_sim_num_steps", "pk_sim_run",
     "pk_qk_norm_rope_and_cache", "pk_reshape_and_cache_e4m3", "pk_gather_cache_e4m3", "pk_copy_blocks_e4m3",
     "pk_paged_attention_decode_e4m3", "pk_paged_attention_tree", "pk_tree_masks", "pk_tree_plan",
-    "pk_tree_workspace_size",
+    "pk_tree_workspace_size", "pk_paged_attention_extend", "pk_extend_plan", "pk_extend_workspace_size",
+    "pk_verify_drafts", "pk_compact_drafts", "pk_bm_truncate",
 )
 PK_POLICY = {"max_reservation": 0, "exact_contiguous": 1, "paged": 2}
 PK_SIM_RULE = {"drop": 0, "stall": 1}
@@ -84,6 +92,11 @@ class CacheDesc(ctypes.Structure):
     _fields_ = [("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+
+
+class ScoreDesc(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("slopes", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p), ("first_tokens", ctypes.c_void_p)]
 
 
 class StepBuffers(ctypes.Structure):
@@ -206,6 +219,13 @@ def lib() -> ctypes.CDLL:
         "pk_tree_masks": (i32, [P, i32, P, P]),
         "pk_tree_plan": (i32, [P, i32, i32, i32, i32, D, P, P, i32, P]),
         "pk_tree_workspace_size": (sz, [i32, i32, i32, i32, D]),
+        "pk_paged_attention_extend": (i32, [P, P, P, P, P, P, P, f32, P, i32, i32, i32, i32, i32, i32, i32, P, i32,
+                                            P, sz, D, P]),
+        "pk_extend_plan": (i32, [P, P, i32, i32, i32, i32, i32, D, P, P, i32, P]),
+        "pk_extend_workspace_size": (sz, [i32, i32, i32, i32, D]),
+        "pk_verify_drafts": (i32, [P, P, P, P, i64, P, i64, i32, P, P, P, P, i32, i32, i32, i32, P]),
+        "pk_compact_drafts": (i32, [P, P, P, i32, P, P, P, P, P, i32, i32, i32, D, P]),
+        "pk_bm_truncate": (i32, [P, i64, i64]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(L, name)
@@ -746,7 +766,7 @@ def pk_copy_blocks_e4m3(k_cache, v_cache, kv_exp, src_dst_pairs, stream=None):
                 _at(src_dst_pairs, "src_dst_pairs", dev, torch.int64), n, ref)
 
 
-def _attention_args(i32, dev, out, q, block_tables, context_lens, num_seqs, d, work_items, workspace):
+def _attention_args(i32, dev, out, q, block_tables, context_lens, num_seqs, d, work_items, workspace, item_len=2):
     """Checked addresses of what the two attentions below share: (out, q),
     (block_tables, context_lens) and (work_items, count, workspace, bytes)."""
     shape = q.shape
@@ -756,8 +776,8 @@ def _attention_args(i32, dev, out, q, block_tables, context_lens, num_seqs, d, w
         raise ValueError("block_tables must be [num_seqs, max_blocks] and context_lens [num_seqs]")
     items, n_items, ws, ws_bytes = None, 0, None, 0
     if work_items is not None:
-        if work_items.dim() != 2 or work_items.shape[1] != 2:
-            raise ValueError("work_items must be [n, 2]")
+        if work_items.dim() != 2 or work_items.shape[1] != item_len:
+            raise ValueError(f"work_items must be [n, {item_len}]")
         items, n_items = _at(work_items, "work_items", dev, i32), work_items.shape[0]
     if workspace is not None:
         ws, ws_bytes = _at(workspace, "workspace", dev), workspace.nbytes
@@ -842,6 +862,139 @@ def pk_tree_workspace_size(num_q_tokens, num_q_heads, max_context_len, partition
                                             int(partition_size), ctypes.byref(desc)))
 
 
+def pk_paged_attention_extend(out, q, k_cache, v_cache, block_tables, context_lens, q_offsets, scale: float,
+                              max_query_len: int, max_context_len: int, softcap: float = 0.0, window: int = 0,
+                              slopes=None, prefix_lens=None, first_tokens=None, partition_size: int = 0,
+                              workspace=None, work_items=None, stream=None):
+    """Attention of each sequence's new tokens over its paged context (see the
+    header): rows ``q_offsets[s] .. q_offsets[s + 1]`` (int32 ``[S + 1]``; None: one
+    row each) of ``q`` and ``out`` ``[rows, Hq, d]`` are the last tokens of its
+    ``context_lens[s]``. Scores are capped by ``softcap``, biased by ``slopes`` (fp32
+    ``[Hq]``) times the distance, and limited by ``window``, ``prefix_lens`` (int32
+    ``[S]``, seen by every row) and ``first_tokens`` (int32 ``[rows]``, the first
+    token that a row sees). ``partition_size`` and ``work_items`` from
+    :func:`pk_extend_plan` for the same ``max_query_len``, ``workspace`` of
+    :func:`pk_extend_workspace_size` bytes when the contexts are split."""
+    torch = _torch()
+    i32 = torch.int32
+    dev, dt = _cuda_device(q, "q"), q.dtype
+    desc, ref, _ = _desc_of(k_cache)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have one shape")
+    S, R = block_tables.shape[0], q.shape[0]
+    rows, seqs, split = _attention_args(i32, dev, out, q, block_tables, context_lens, S, desc.head_dim, work_items,
+                                        workspace, 4)
+    offsets = None
+    if q_offsets is not None:
+        if q_offsets.shape != (S + 1,):
+            raise ValueError("q_offsets must be [num_seqs + 1]")
+        offsets = _at(q_offsets, "q_offsets", dev, i32)
+    scores = None
+    if softcap or window or slopes is not None or prefix_lens is not None or first_tokens is not None:
+        at = []
+        for t, name, n, kind in ((slopes, "slopes", q.shape[1], torch.float32), (prefix_lens, "prefix_lens", S, i32),
+                                 (first_tokens, "first_tokens", R, i32)):
+            if t is not None and t.shape != (n,):
+                raise ValueError(f"{name} must be [{n}]")
+            at.append(None if t is None else _at(t, name, dev, kind))
+        scores = ctypes.byref(ScoreDesc(float(softcap), int(window), *at))
+    _launch(torch, "pk_paged_attention_extend", dev, stream, *rows, _at(k_cache, "k_cache", dev, dt),
+            _at(v_cache, "v_cache", dev, dt), *seqs, offsets, float(scale), scores, S, R, int(max_query_len),
+            q.shape[1], block_tables.shape[1], int(max_context_len), int(partition_size), *split, ref)
+
+
+def pk_extend_plan(context_lens, query_lens, num_q_heads: int, desc: CacheDesc, partition_size: int = -1,
+                   window: int = 0, max_query_len: Optional[int] = None):
+    """Host planner: ``(partition, items int32 [n, 4])`` of
+    :func:`pk_paged_attention_extend` for host lengths (``query_lens`` None: one new
+    token each). ``max_query_len`` is the call's, by default the longest."""
+    lens = np.ascontiguousarray(context_lens, dtype=np.int32)
+    new = None if query_lens is None else np.ascontiguousarray(query_lens, dtype=np.int32)
+    if new is not None and new.shape != lens.shape:
+        raise ValueError("context_lens and query_lens must have one shape")
+    if max_query_len is None:
+        max_query_len = 1 if new is None else max(int(new.max(initial=1)), 1)
+    part, n = ctypes.c_int32(0), ctypes.c_int32(0)
+    args = (_np_ptr(lens), _np_ptr(new), len(lens), int(max_query_len), int(num_q_heads), int(window),
+            int(partition_size), ctypes.byref(desc), ctypes.byref(part))
+    lib().pk_extend_plan(*args, None, 0, ctypes.byref(n))
+    out = np.empty((max(n.value, 1), 4), np.int32)
+    _check(lib().pk_extend_plan(*args, _np_ptr(out), n.value, ctypes.byref(n)), "pk_extend_plan")
+    return int(part.value), out[: n.value]
+
+
+def pk_extend_workspace_size(num_q_tokens, num_q_heads, max_context_len, partition_size, desc) -> int:
+    return int(lib().pk_extend_workspace_size(int(num_q_tokens), int(num_q_heads), int(max_context_len),
+                                              int(partition_size), ctypes.byref(desc)))
+
+
+def pk_verify_drafts(num_accepted, accepted, next_tokens, target_probs, tokens, uniforms, q_offsets, max_rows: int,
+                     parents=None, draft_probs=None, stream=None):
+    """Which drafted tokens are kept, and the token after them (see the header).
+    Sequence s has rows ``q_offsets[s] .. q_offsets[s + 1]`` (int32 ``[S + 1]``), its
+    root and its drafts: ``tokens`` int64, ``uniforms`` fp32 and ``parents`` int32
+    ``[rows]`` (places in the sequence; None: a chain), ``target_probs`` and, of a
+    chain that was drawn from them, ``draft_probs`` ``[rows, vocab]`` in fp32 or bf16
+    (rows may be further apart). Writes ``num_accepted`` int32 ``[S]``, ``accepted``
+    int32 ``[rows]`` (the path's rows, -1 behind it) and ``next_tokens`` int64 ``[S]``."""
+    torch = _torch()
+    i32, i64 = torch.int32, torch.int64
+    dev = _cuda_device(target_probs, "target_probs")
+    S = q_offsets.shape[0] - 1
+    if q_offsets.dim() != 1 or S < 0 or target_probs.dim() != 2:
+        raise ValueError("q_offsets must be [num_seqs + 1] and target_probs [rows, vocab]")
+    R, V = target_probs.shape
+    if num_accepted.shape != (S,) or next_tokens.shape != (S,):
+        raise ValueError("num_accepted and next_tokens must be [num_seqs]")
+    for t, name in ((accepted, "accepted"), (tokens, "tokens"), (uniforms, "uniforms"), (parents, "parents")):
+        if t is not None and t.shape != (R,):
+            raise ValueError(f"{name} must be [rows]")
+    probs = []
+    for t, name in ((target_probs, "target_probs"), (draft_probs, "draft_probs")):
+        if t is None:
+            probs += [None, 0]
+            continue
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on device {dev}, with the call's other tensors")
+        if t.shape != (R, V) or t.dtype != target_probs.dtype:
+            raise ValueError("target_probs and draft_probs must have one shape and type")
+        if V > 1 and t.stride(1) != 1:
+            raise ValueError(f"the rows of {name} must be contiguous")
+        probs += [t.data_ptr(), t.stride(0) if R > 1 else V]
+    _launch(torch, "pk_verify_drafts", dev, stream, _at(num_accepted, "num_accepted", dev, i32),
+            _at(accepted, "accepted", dev, i32), _at(next_tokens, "next_tokens", dev, i64), *probs,
+            _io_code(torch, target_probs, "target_probs"), _at(tokens, "tokens", dev, i64),
+            _at(uniforms, "uniforms", dev, torch.float32), _at(q_offsets, "q_offsets", dev, i32),
+            None if parents is None else _at(parents, "parents", dev, i32), S, R, int(max_rows), V)
+
+
+def pk_compact_drafts(k_cache, v_cache, block_tables, context_lens, q_offsets, accepted, num_accepted, max_rows: int,
+                      context_lens_out=None, stream=None):
+    """Moves the cached K and V of the kept rows of each sequence together (see the
+    header): the token at ``base + accepted[q_offsets[s] + k]`` to ``base + k``, ``base``
+    being ``context_lens[s]`` without the sequence's rows. ``context_lens_out`` receives
+    the lengths that are left (``BlockManager.truncate`` cuts the host's to them)."""
+    torch = _torch()
+    i32 = torch.int32
+    dev = _cuda_device(k_cache, "k_cache")
+    _, ref, _ = _desc_of(k_cache)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have one shape")
+    if block_tables.dim() != 2 or accepted.dim() != 1:
+        raise ValueError("block_tables must be [num_seqs, max_blocks] and accepted [rows]")
+    S = block_tables.shape[0]
+    if q_offsets.shape != (S + 1,) or context_lens.shape != (S,) or num_accepted.shape != (S,) or (
+            context_lens_out is not None and context_lens_out.shape != (S,)):
+        raise ValueError("q_offsets must be [num_seqs + 1], context_lens, num_accepted and context_lens_out [num_seqs]")
+    _launch(torch, "pk_compact_drafts", dev, stream, _at(k_cache, "k_cache", dev),
+            _at(v_cache, "v_cache", dev, k_cache.dtype), _at(block_tables, "block_tables", dev, i32),
+            block_tables.shape[1], _at(context_lens, "context_lens", dev, i32),
+            _at(q_offsets, "q_offsets", dev, i32), _at(accepted, "accepted", dev, i32),
+            _at(num_accepted, "num_accepted", dev, i32),
+            None if context_lens_out is None else _at(context_lens_out, "context_lens_out", dev, i32), S,
+            accepted.shape[0], int(max_rows), ref)
+
+
 def pk_get_device_error(stream=None) -> Tuple[int, int]:
     """Synchronises the stream, reads and clears the device error word.
 
@@ -908,6 +1061,10 @@ class BlockManager:
 
     def free_seq(self, seq: int):
         _check(self._L.pk_bm_free_seq(self._h, int(seq)), "pk_bm_free_seq")
+
+    def truncate(self, seq: int, new_len: int):
+        """Cuts a sequence to its first ``new_len`` tokens; blocks behind them lose a reference."""
+        _check(self._L.pk_bm_truncate(self._h, int(seq), int(new_len)), "pk_bm_truncate")
 
     def seq_len(self, seq: int) -> int:
         n = ctypes.c_int64(0)

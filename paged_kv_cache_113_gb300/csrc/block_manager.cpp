@@ -13,6 +13,9 @@
 //     contents with pk_copy_blocks) and the shared block loses one
 //     reference. The slot is table[L / B] * B + L % B.
 //   * Fork: the child names the parent's blocks; each count goes up by one.
+//   * Cut (after refused drafts): the blocks behind the new end lose one reference
+//     each, last first. A cut inside a block that the prefix cache knows leaves it
+//     as it is; the next append copies it like a shared one.
 //   * Retire: each block of the table loses one reference; those reaching
 //     zero go back to the free list, in table order.
 //   * The free list is a stack whose first pop is alloc_order[0].
@@ -167,6 +170,10 @@ struct pk_bm {
     return -1;
   }
 
+  // Whether a partly filled tail block must not be written: another table names it, or
+  // the prefix cache knows its content (a sequence that was cut inside a cached block).
+  bool tail_taken(int32_t b) const { return refs[b] > 1 || entry[b].cached; }
+
   // Appends one token (the caller has checked that a block is available if
   // one is needed). A new block or a CoW copy comes from take_block.
   int64_t append_one(Sequence &s, int64_t *cow_src, int64_t *cow_dst) {
@@ -177,10 +184,10 @@ struct pk_bm {
       s.table.push_back(b);
     } else {
       const int32_t tail = s.table.back();
-      if (refs[tail] > 1) {
+      if (tail_taken(tail)) {
         const int32_t b = take_block();
         refs[b] = 1;
-        refs[tail] -= 1;
+        release(tail);
         s.table.back() = b;
         ++cow_copies;
         if (cow_src) *cow_src = tail;
@@ -251,7 +258,7 @@ pk_status pk_bm_append_slots(pk_bm *bm, int64_t seq_id, int32_t n, int64_t *slot
   // Blocks needed: one per block boundary crossed, plus a CoW copy when the
   // first token lands in a shared, partly filled tail.
   const int64_t fresh = bm->blocks_for(s.len + n) - bm->blocks_for(s.len);
-  const int64_t cow = (s.len % bm->block_size != 0 && bm->refs[s.table.back()] > 1) ? 1 : 0;
+  const int64_t cow = (s.len % bm->block_size != 0 && bm->tail_taken(s.table.back())) ? 1 : 0;
   if (fresh + cow > bm->available()) return PK_ERR_OUT_OF_BLOCKS;
   try {
     reserve_table(s.table, bm->blocks_for(s.len + n));
@@ -303,7 +310,7 @@ pk_status pk_bm_append_batch(pk_bm *bm, const int64_t *seq_ids, int32_t n, int64
           bm->given_up_mark[tail] = ep;
           bm->given_up[tail] = 0;
         }
-        if (bm->refs[tail] - bm->given_up[tail] > 1) {
+        if (bm->refs[tail] - bm->given_up[tail] > 1 || bm->entry[tail].cached) {
           ++need;
           ++bm->given_up[tail];
         }
@@ -359,6 +366,19 @@ pk_status pk_bm_free_seq(pk_bm *bm, int64_t seq_id) {
       bm->release(b);
   }
   bm->seqs.erase(it);
+  return PK_OK;
+}
+
+pk_status pk_bm_truncate(pk_bm *bm, int64_t seq_id, int64_t new_len) {
+  if (!bm || new_len < 0) return PK_ERR_INVALID_ARG;
+  auto it = bm->seqs.find(seq_id);
+  if (it == bm->seqs.end()) return PK_ERR_UNKNOWN_SEQ;
+  Sequence &s = it->second;
+  if (s.swapped || new_len > s.len) return PK_ERR_INVALID_ARG;
+  ++bm->clock;
+  for (const int64_t keep = bm->blocks_for(new_len); int64_t(s.table.size()) > keep; s.table.pop_back())
+    bm->release(s.table.back());
+  s.len = new_len;
   return PK_OK;
 }
 

@@ -159,7 +159,7 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 int64_t elem_size(pk_dtype t) { return t == PK_F32 ? 4 : (t == PK_BF16 ? 2 : 0); }
 
 // The device error words of all files, in the order in which they are reported.
-constexpr int kErrorWords = 6;
+constexpr int kErrorWords = 8;
 struct ErrorWords {
   int *at[kErrorWords];
 };
@@ -193,6 +193,8 @@ extern "C" int *pkx_qk_norm_rope_error_word();
 extern "C" int *pkx_cache_e4m3_error_word();
 extern "C" int *pkx_attention_e4m3_error_word();
 extern "C" int *pkx_tree_attention_error_word();
+extern "C" int *pkx_extend_attention_error_word();
+extern "C" int *pkx_draft_ops_error_word();
 
 extern "C" {
 
@@ -346,7 +348,8 @@ pk_status pk_get_device_error(int32_t *code_out, void *stream) {
   int i = 0;
   for (int *word : {pk::error_word(g_cache_ops_error), pkx_attention_error_word(), pkx_qk_norm_rope_error_word(),
                     pkx_cache_e4m3_error_word(), pkx_attention_e4m3_error_word(),
-                    pkx_tree_attention_error_word()}) {
+                    pkx_tree_attention_error_word(), pkx_extend_attention_error_word(),
+                    pkx_draft_ops_error_word()}) {
     if (!word) return PK_ERR_CUDA;
     words.at[i++] = word;
   }

@@ -1,0 +1,495 @@
+// What follows the attention of drafted tokens: which drafts are kept, by the target's
+// probabilities and given random numbers (pk_verify_drafts), and their keys and values
+// moved together in the cache (pk_compact_drafts).
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "pagedkv.h"
+#include "pk_device.cuh"
+
+namespace pk {
+
+__device__ int g_draft_ops_error;
+
+extern "C" int *pkx_draft_ops_error_word() { return error_word(g_draft_ops_error); }
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kVerifyThreads = 512;
+constexpr int kMaxCluster = 8;
+
+struct VerifyParams {
+  int32_t *num_accepted;   // [S]
+  int32_t *accepted;       // [num_rows]
+  int64_t *next_tokens;    // [S]
+  const void *p, *q;       // [num_rows] rows of V probabilities, q or null
+  int64_t p_stride, q_stride;
+  const int64_t *tokens;   // [num_rows]
+  const float *uniforms;   // [num_rows]
+  const int32_t *q_offsets;
+  const int32_t *parents;  // [num_rows] or null: a chain
+  int32_t num_rows, max_rows, vocab;
+};
+
+// A probability as it counts: what is not a positive finite number is 0.
+__device__ __forceinline__ float weight(float x) { return x > 0.0f && x <= 3.402823466e38f ? x : 0.0f; }
+
+// A sum in two floats: hi + lo, the error of each addition kept (Knuth's two-sum), so
+// that a row's sum is exact to 2^-45 or so without 64-bit additions, of which this
+// chip does two a clock and SM.
+struct Sum2 {
+  float hi = 0.0f, lo = 0.0f;
+  __device__ __forceinline__ void add(float x, float err) {
+    const float t = __fadd_rn(hi, x), b = __fsub_rn(t, hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(x, b)), err));
+    hi = t;
+  }
+  __device__ __forceinline__ double value() const { return double(hi) + double(lo); }
+};
+
+// The weights that the next token is drawn by, element by element.
+template <typename T>
+struct Weights {
+  const T *p, *q;           // q: the refused draft's distribution, or null
+  int vocab, shift;         // elements of p before a multiple of four
+  bool aligned_q;           // q's multiples of four are p's
+  const int64_t *refused;   // tokens that do not count
+  uint64_t mine;            // those that are this thread's
+
+  static __device__ __forceinline__ float4 four(const T *at) { return widen4(raw4(at)); }
+  // Elements 4 g - shift ..  + 3, as x + err (err: of the difference from q).
+  __device__ __forceinline__ void load(int g, float (&x)[4], float (&err)[4]) const {
+    const int e0 = 4 * g - shift;
+    const bool whole = e0 >= 0 && e0 + 4 <= vocab;
+    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (whole) {
+      const float4 v = four(p + e0);
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = e0 + i >= 0 && e0 + i < vocab ? load_elem(p + e0 + i) : 0.0f;
+    }
+    if (q) {
+      if (whole && aligned_q) {
+        const float4 v = four(q + e0);
+        y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = e0 + i >= 0 && e0 + i < vocab ? load_elem(q + e0 + i) : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = weight(x[i]);
+      err[i] = 0.0f;
+      x[i] = a;
+      if (q) {
+        const float b = -weight(y[i]), t = __fadd_rn(a, b), c = __fsub_rn(t, a);
+        const float e = __fadd_rn(__fsub_rn(a, __fsub_rn(t, c)), __fsub_rn(b, c));
+        x[i] = t > 0.0f ? t : 0.0f;
+        err[i] = t > 0.0f ? e : 0.0f;
+      }
+    }
+    for (uint64_t m = mine; m; m &= m - 1) {
+      const int64_t k = refused[__ffsll(m) - 1] - e0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (k == i) x[i] = 0.0f;
+    }
+  }
+};
+
+// A cluster has a sequence: every CTA walks down from its root (a few loads, all nodes'
+// at once), then sums its share of the weights of the row where the walk ended; the
+// totals go round, and the CTA that the drawn number falls into finds the token. Only
+// that row (and with q the refused draft's) is read whole.
+template <typename T>
+__global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(VerifyParams a) {
+  constexpr int NT = kVerifyThreads, NW = NT / 32;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
+  const int s = blockIdx.x / C, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ double totals[2][kMaxCluster], warp_sum[NW];
+  __shared__ float pc[PK_MAX_DRAFT], lim[PK_MAX_DRAFT], un[PK_MAX_DRAFT];
+  __shared__ int parent[PK_MAX_DRAFT];
+  __shared__ int64_t token[PK_MAX_DRAFT];
+  __shared__ uint64_t sh_refused;
+  __shared__ int sh_cur, sh_found;
+
+  const int r0 = __ldg(a.q_offsets + s), r1 = __ldg(a.q_offsets + s + 1);
+  const int64_t len = int64_t(r1) - r0;
+  if (r0 < 0 || len <= 0 || r1 > a.num_rows || len > a.max_rows) {
+    if (rank == 0 && threadIdx.x == 0) {
+      if (len != 0 || r0 < 0 || r1 > a.num_rows) record_error(&g_draft_ops_error, PK_DEVERR_OFFSETS, s);
+      a.num_accepted[s] = 0;
+      a.next_tokens[s] = -1;
+    }
+    return;  // the whole cluster does
+  }
+  const int n = int(len);
+  const T *const p = static_cast<const T *>(a.p), *const q = static_cast<const T *>(a.q);
+  if (warp == 0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = lane + 32 * h;
+      if (i >= n) continue;
+      int up = i == 0 ? -1 : (a.parents ? __ldg(a.parents + r0 + i) : i - 1);
+      int64_t t = i == 0 ? 0 : __ldg(reinterpret_cast<const long long *>(a.tokens) + r0 + i);
+      if (i > 0 && (up < 0 || up >= i || t < 0 || t >= a.vocab)) {  // never reached
+        if (rank == 0) record_error(&g_draft_ops_error, PK_DEVERR_DRAFT, s);
+        up = -1, t = 0;
+      }
+      parent[i] = up;
+      token[i] = t;
+      un[i] = __ldg(a.uniforms + r0 + i);
+      pc[i] = up >= 0 ? weight(load_elem(p + (r0 + up) * a.p_stride + t)) : 0.0f;
+      lim[i] = up >= 0 && q ? weight(load_elem(q + (r0 + i) * a.q_stride + t)) : 0.0f;
+    }
+    __syncwarp();
+    // A node comes after its parent, so one pass over the nodes is the walk. A double
+    // holds the products of two floats exactly.
+    int cur = 0;
+    uint64_t refused = 0, path = 1;
+    double mass = 1.0;  // what the refused siblings leave
+    for (int j = 1; j < n; ++j) {
+      if (parent[j] != cur) continue;
+      double pj = pc[j];
+      if (!q && refused) {  // the same token again has nothing left
+        const int64_t t = token[j];
+        const bool again = (((refused >> lane) & 1) && token[lane] == t) ||
+                           (((refused >> (lane + 32)) & 1) && token[lane + 32] == t);
+        if (__any_sync(0xffffffffu, again)) pj = 0.0;
+      }
+      if (double(un[j]) * (q ? double(lim[j]) : mass) < pj) {
+        cur = j;
+        path |= 1ull << j;
+        refused = 0;
+        mass = 1.0;
+      } else {
+        refused |= 1ull << j;
+        mass -= pj;
+      }
+    }
+    if (lane == 0) sh_cur = cur, sh_refused = refused;
+    if (rank == 0) {
+      const int count = __popcll(path);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = lane + 32 * h;
+        if (i < n && ((path >> i) & 1)) a.accepted[r0 + __popcll(path & ((1ull << i) - 1))] = i;
+        if (i < n && i >= count) a.accepted[r0 + i] = -1;
+      }
+      if (lane == 0) a.num_accepted[s] = count - 1;
+    }
+  }
+  __syncthreads();
+  const uint64_t refused = sh_refused;
+  Weights<T> w;
+  w.p = p + (r0 + sh_cur) * a.p_stride;
+  w.vocab = a.vocab;
+  w.shift = int(reinterpret_cast<uintptr_t>(w.p) / sizeof(T) & 3);
+  w.refused = token;
+  // This CTA's groups of four elements.
+  const int groups = (a.vocab + w.shift + 3) / 4, share = (groups + C - 1) / C;
+  const int g0 = min(groups, rank * share), g1 = min(groups, g0 + share);
+  const int span = (g1 - g0 + NT - 1) / NT;  // of a thread, when the token is looked for
+  const float u = fminf(fmaxf(un[0], 0.0f), 1.0f - 5.9604645e-8f);
+  // Which of the refused tokens are in groups that `have` holds of.
+  auto own = [&](auto have) {
+    uint64_t m = 0;
+    for (uint64_t left = refused; left; left &= left - 1) {
+      const int i = __ffsll(left) - 1, g = int(token[i] + w.shift) / 4;
+      if (have(g)) m |= 1ull << i;
+    }
+    return m;
+  };
+  double total = 0.0, before = 0.0;
+  int plain = 0;  // 1: the refused drafts leave nothing, so the row itself counts
+  for (;; ++plain) {
+    w.q = !plain && q && refused ? q + (r0 + __ffsll(refused) - 1) * a.q_stride : nullptr;
+    w.aligned_q = w.q && int(reinterpret_cast<uintptr_t>(w.q) / sizeof(T) & 3) == w.shift;
+    w.mine = plain || q ? 0 : own([&](int g) { return g >= g0 && g < g1 && (g - g0) % NT == int(threadIdx.x); });
+    Sum2 sum;
+#pragma unroll 4
+    for (int g = g0 + int(threadIdx.x); g < g1; g += NT) {
+      float x[4], err[4];
+      w.load(g, x, err);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum.add(x[i], err[i]);
+    }
+    double mine = sum.value();
+#pragma unroll
+    for (int off = 16; off; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
+    if (lane == 0) warp_sum[warp] = mine;
+    __syncthreads();
+    if (warp == 0) {
+      double x = lane < NW ? warp_sum[lane] : 0.0;
+#pragma unroll
+      for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+      if (lane < C) *cluster.map_shared_rank(&totals[plain][rank], lane) = x;
+    }
+    cluster.sync();
+    total = before = 0.0;
+    for (int c = 0; c < C; ++c) {
+      if (c == rank) before = total;
+      total += totals[plain][c];
+    }
+    if (total > 0.0 || !refused || plain) break;
+  }
+  if (!(total > 0.0)) {
+    if (rank == 0 && threadIdx.x == 0) a.next_tokens[s] = -1;
+    return;
+  }
+  const double target = double(u) * total;
+  // The CTA whose share ends past the target first; the last with anything, should
+  // rounding leave none.
+  int owner = -1, last = 0;
+  {
+    double sum = 0.0;
+    for (int c = 0; c < C; ++c) {
+      const double x = totals[plain][c];
+      sum += x;
+      if (x > 0.0) last = c;
+      if (owner < 0 && sum > target) owner = c;
+    }
+    if (owner < 0) owner = last;
+  }
+  if (rank != owner) return;
+  const double local = target - before;
+  const int b0 = min(g1, g0 + int(threadIdx.x) * span), b1 = min(g1, b0 + span);
+  w.mine = plain || q ? 0 : own([&](int g) { return g >= b0 && g < b1; });
+  Sum2 sum;
+  for (int g = b0; g < b1; ++g) {
+    float x[4], err[4];
+    w.load(g, x, err);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum.add(x[i], err[i]);
+  }
+  const double mine = sum.value();
+  double incl = mine;  // of the threads up to this one
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const double x = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += x;
+  }
+  if (threadIdx.x == 0) sh_found = NT;
+  __syncthreads();
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  double base = 0.0;
+  for (int k = 0; k < warp; ++k) base += warp_sum[k];
+  incl += base;
+  if (mine > 0.0 && incl > local) atomicMin(&sh_found, int(threadIdx.x));
+  __syncthreads();
+  int found = sh_found;
+  if (found == NT) {  // rounding: the last thread with anything
+    __syncthreads();
+    if (threadIdx.x == 0) sh_found = -1;
+    __syncthreads();
+    if (mine > 0.0) atomicMax(&sh_found, int(threadIdx.x));
+    __syncthreads();
+    found = sh_found;
+  }
+  if (int(threadIdx.x) != found) return;
+  double run = incl - mine;
+  int64_t at = -1;
+  for (int g = b0; g < b1; ++g) {
+    float x[4], err[4];
+    w.load(g, x, err);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!(x[i] > 0.0f)) continue;
+      run += double(x[i]) + double(err[i]);
+      at = 4 * int64_t(g) - w.shift + i;
+      if (run > local) {
+        a.next_tokens[s] = at;
+        return;
+      }
+    }
+  }
+  a.next_tokens[s] = at;  // rounding: the thread's last
+}
+
+// A sequence's kept rows to the places behind one another: thread = 16 bytes of a
+// token's row, which it moves for all of the kept ones, first to last. A row never
+// comes from before the place it goes to, and places are filled in order, so no
+// source is overwritten before it is read.
+__global__ void __launch_bounds__(128)
+    compact_drafts_kernel(uint4 *k_cache, uint4 *v_cache, const int32_t *__restrict__ tables, int32_t max_blocks,
+                          const int32_t *__restrict__ lens, const int32_t *__restrict__ q_offsets,
+                          const int32_t *__restrict__ accepted, const int32_t *__restrict__ num_accepted,
+                          int32_t *lens_out, int32_t num_rows, int32_t max_rows, int32_t block_size,
+                          int32_t num_blocks, int32_t row_vecs) {
+  constexpr int U = 8;
+  const int s = blockIdx.y, side = blockIdx.z;
+  const bool record = blockIdx.x == 0 && side == 0;
+  __shared__ int from[PK_MAX_DRAFT], to[PK_MAX_DRAFT];  // slots
+  __shared__ int sh_moves;
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    const int r0 = __ldg(q_offsets + s), r1 = __ldg(q_offsets + s + 1);
+    const int64_t n64 = int64_t(r1) - r0;
+    const int ctx = __ldg(lens + s);
+    int moves = 0, len = ctx;
+    if (r0 < 0 || n64 < 0 || r1 > num_rows || n64 > max_rows) {
+      if (record && lane == 0) record_error(&g_draft_ops_error, PK_DEVERR_OFFSETS, s);
+    } else if (n64 > 0) {
+      const int n = int(n64), last = __ldg(num_accepted + s);
+      const bool fits = ctx >= n && ctx <= int64_t(max_blocks) * block_size;
+      int kept[2];
+      bool good = last >= 0 && last < n;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = lane + 32 * h;
+        kept[h] = k < n ? __ldg(accepted + r0 + k) : 0;
+        if (k < n && k <= last) {  // ascending, within the rows
+          const int prev = k > 0 ? __ldg(accepted + r0 + k - 1) : -1;
+          good = good && kept[h] > prev && kept[h] < n && kept[h] >= k;
+        }
+      }
+      good = __all_sync(0xffffffffu, good);
+      if (!good || !fits) {
+        if (record && lane == 0) record_error(&g_draft_ops_error, fits ? PK_DEVERR_DRAFT : PK_DEVERR_CONTEXT, s);
+      } else {
+        const int base = ctx - n;
+        len = base + last + 1;
+        const int32_t *row = tables + size_t(s) * max_blocks;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k = lane + 32 * h;
+          bool move = k <= last && kept[h] != k;
+          int f = 0, t = 0;
+          if (move) {
+            const int a = base + kept[h], b = base + k;
+            const int pa = __ldg(row + a / block_size), pb = __ldg(row + b / block_size);
+            if (pa < 0 || pa >= num_blocks || pb < 0 || pb >= num_blocks) {
+              if (record) record_error(&g_draft_ops_error, PK_DEVERR_BLOCK_ID, s);
+              move = false;
+            } else {
+              f = pa * block_size + a % block_size;
+              t = pb * block_size + b % block_size;
+            }
+          }
+          const uint32_t all = __ballot_sync(0xffffffffu, move);
+          const int at = moves + __popc(all & ((1u << lane) - 1));
+          if (move) from[at] = f, to[at] = t;
+          moves += __popc(all);
+        }
+      }
+    }
+    if (lane == 0) {
+      sh_moves = moves;
+      if (record && lens_out) lens_out[s] = len;
+    }
+  }
+  __syncthreads();
+  const int moves = sh_moves, j = blockIdx.x * 128 + threadIdx.x;
+  if (j >= row_vecs) return;
+  uint4 *const pool = (side ? v_cache : k_cache) + j;
+  for (int k0 = 0; k0 < moves; k0 += U) {
+    uint4 x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k0 + u < moves) x[u] = pool[size_t(from[k0 + u]) * row_vecs];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k0 + u < moves) pool[size_t(to[k0 + u]) * row_vecs] = x[u];
+  }
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess &&
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0)
+    return n;
+  cudaGetLastError();
+  return 152;
+}
+
+template <typename T>
+pk_status launch_verify(const VerifyParams &a, int32_t num_seqs, cudaStream_t stream) {
+  // CTAs a sequence: until every SM has two, of 2048 elements or more each.
+  const int sms = sm_count();
+  int C = 1;
+  while (C < kMaxCluster && int64_t(num_seqs) * C < 2 * sms && a.vocab / C >= 4096) C *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(num_seqs * C));
+  cfg.blockDim = dim3(kVerifyThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(C);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, verify_drafts_kernel<T>, a) == cudaSuccess ? PK_OK : PK_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+pk_status pk_verify_drafts(int32_t *num_accepted, int32_t *accepted, int64_t *next_tokens,
+                           const void *target_probs, int64_t target_stride, const void *draft_probs,
+                           int64_t draft_stride, pk_dtype probs_dtype, const int64_t *tokens,
+                           const float *uniforms, const int32_t *q_offsets, const int32_t *parents,
+                           int32_t num_seqs, int32_t num_rows, int32_t max_rows, int32_t vocab, void *stream) {
+  if (num_seqs < 0 || num_rows < 0 || max_rows < 0 || vocab <= 0) return PK_ERR_INVALID_ARG;
+  if (probs_dtype != PK_F32 && probs_dtype != PK_BF16) return PK_ERR_UNSUPPORTED;
+  if (max_rows > PK_MAX_DRAFT || vocab > (1 << 24)) return PK_ERR_UNSUPPORTED;
+  if (draft_probs && parents) return PK_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PK_OK;
+  if (num_seqs > (1 << 24)) return PK_ERR_UNSUPPORTED;
+  if (!num_accepted || !next_tokens || !q_offsets) return PK_ERR_INVALID_ARG;
+  if (num_rows > 0 && (!accepted || !target_probs || !tokens || !uniforms)) return PK_ERR_INVALID_ARG;
+  if (target_stride < vocab || (draft_probs && draft_stride < vocab)) return PK_ERR_INVALID_ARG;
+  const uintptr_t mask = probs_dtype == PK_F32 ? 3u : 1u;
+  if (((reinterpret_cast<uintptr_t>(target_probs) | reinterpret_cast<uintptr_t>(draft_probs)) & mask) ||
+      (reinterpret_cast<uintptr_t>(tokens) & 7u) || (reinterpret_cast<uintptr_t>(next_tokens) & 7u))
+    return PK_ERR_INVALID_ARG;
+  VerifyParams a{num_accepted, accepted, next_tokens, target_probs, draft_probs, target_stride, draft_stride,
+                 tokens,       uniforms, q_offsets,   parents,      num_rows,    max_rows,      vocab};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return probs_dtype == PK_F32 ? launch_verify<float>(a, num_seqs, st)
+                               : launch_verify<__nv_bfloat16>(a, num_seqs, st);
+}
+
+pk_status pk_compact_drafts(void *k_cache, void *v_cache, const int32_t *block_tables,
+                            int32_t max_blocks_per_seq, const int32_t *context_lens, const int32_t *q_offsets,
+                            const int32_t *accepted, const int32_t *num_accepted, int32_t *context_lens_out,
+                            int32_t num_seqs, int32_t num_rows, int32_t max_rows, const pk_cache_desc *desc,
+                            void *stream) {
+  if (!desc || desc->num_blocks <= 0 || desc->block_size <= 0 || desc->num_kv_heads <= 0 || desc->head_dim <= 0 ||
+      num_seqs < 0 || num_rows < 0 || max_rows < 0)
+    return PK_ERR_INVALID_ARG;
+  if (desc->dtype != PK_F32 && desc->dtype != PK_BF16) return PK_ERR_UNSUPPORTED;
+  const int64_t bytes = int64_t(desc->num_kv_heads) * desc->head_dim * (desc->dtype == PK_F32 ? 4 : 2);
+  if (bytes % 16 != 0) return PK_ERR_INVALID_ARG;
+  if (max_rows > PK_MAX_DRAFT || num_seqs > 65535 || int64_t(desc->num_blocks) * desc->block_size > INT32_MAX ||
+      bytes / 16 > 1 << 24)
+    return PK_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PK_OK;
+  if (!k_cache || !v_cache || !block_tables || max_blocks_per_seq <= 0 || !context_lens || !q_offsets ||
+      !num_accepted || (num_rows > 0 && !accepted) || context_lens_out == context_lens)
+    return PK_ERR_INVALID_ARG;
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return PK_ERR_INVALID_ARG;
+  const int32_t vecs = int32_t(bytes / 16);
+  compact_drafts_kernel<<<dim3(unsigned((vecs + 127) / 128), unsigned(num_seqs), 2), 128, 0,
+                          static_cast<cudaStream_t>(stream)>>>(
+      static_cast<uint4 *>(k_cache), static_cast<uint4 *>(v_cache), block_tables, max_blocks_per_seq, context_lens,
+      q_offsets, accepted, num_accepted, context_lens_out, num_rows, max_rows, desc->block_size, desc->num_blocks,
+      vecs);
+  return cudaGetLastError() == cudaSuccess ? PK_OK : PK_ERR_CUDA;
+}
+
+}  // extern "C"
+
+}  // namespace pk
