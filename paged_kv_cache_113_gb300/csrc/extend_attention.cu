@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "attn_extend.cuh"
+#include "extend_prompt.cuh"
 #include "pagedkv.h"
 
 namespace pk {
@@ -26,8 +27,14 @@ int sm_count() {
   return 152;
 }
 
+// Whether sequences of at most `rows` rows go to attn_prompt_kernel.
+bool prompt_path(const pk_cache_desc &d, int64_t rows) {
+  return d.dtype == PK_BF16 && rows > 8 && (d.block_size == 8 || d.block_size == 16 || d.block_size == 32);
+}
 // Rows of a unit, for sequences of at most `rows` rows.
-int unit_rows(const pk_cache_desc &, int64_t rows) { return split_rows(int(std::min<int64_t>(rows, 64))); }
+int unit_rows(const pk_cache_desc &d, int64_t rows) {
+  return prompt_path(d, rows) ? kPromptRows : split_rows(int(std::min<int64_t>(rows, 64)));
+}
 
 template <typename T, int D>
 pk_status launch_extend_merge(const ExtendParams &p, cudaStream_t stream) {
@@ -57,10 +64,14 @@ pk_status run(ExtendParams p, const pk_cache_desc &d, cudaStream_t stream) {
   p.tiles = int32_t(tiles);
   const dim3 grid = dim3(unsigned(units));
   pk_status st;
-  switch (R) {
-    case 8: st = launch_split<T, D, 1, ExtendView>(p, grid, stream); break;
-    case 16: st = launch_split<T, D, 2, ExtendView>(p, grid, stream); break;
-    default: st = launch_split<T, D, 4, ExtendView>(p, grid, stream);
+  if (prompt_path(d, rows)) {
+    st = launch_prompt<D>(p, d, unsigned(units), stream);
+  } else {
+    switch (R) {
+      case 8: st = launch_split<T, D, 1, ExtendView>(p, grid, stream); break;
+      case 16: st = launch_split<T, D, 2, ExtendView>(p, grid, stream); break;
+      default: st = launch_split<T, D, 4, ExtendView>(p, grid, stream);
+    }
   }
   if (st != PK_OK || p.num_partitions == 1) return st;
   return launch_extend_merge<T, D>(p, stream);
