@@ -13,7 +13,8 @@ namespace {
 
 constexpr int kPromptRows = 256;     // of a unit: two halves of 128, one lane of tensor memory each
 constexpr int kPromptTile = 128;     // tokens
-constexpr int kPromptThreads = 384;  // two warpgroups of softmax; the producer, the products' warp, two idle
+constexpr int kPromptThreads = 384;  // two warpgroups of softmax; the producer, products, units and queries
+constexpr int kPromptUnits = 4;      // units known at a time
 // 384 threads of 168 registers at launch: 2 x 216 + 72 = 3 x 168.
 constexpr int kPromptSoftmaxRegs = 216, kPromptOtherRegs = 72;
 constexpr float kPromptSlack = 8.0f;  // log2 of how far a maximum may outgrow the reference
@@ -44,6 +45,33 @@ __device__ __forceinline__ uint64_t tanh2(uint64_t x, uint64_t k) {
   b = reciprocal(1.0f + exp2_ftz(b));
   return fma2(pack2(a, b), pack2(-2.0f, -2.0f), pack2(1.0f, 1.0f));
 }
+// The same of f x where |f x| <= kTanhSmall: an odd polynomial of degree 9, the one of least
+// largest error (by linear programming over 2000 points), 2^-22 with its roundings. No
+// exponential and no reciprocal, whose unit the softmax's own exponentials keep busy.
+constexpr float kTanhSmall = 0.75f;
+__device__ __forceinline__ uint64_t tanh2_small(uint64_t x, uint64_t f) {
+  const uint64_t y = mul2(x, f), z = mul2(y, y);
+  uint64_t r = fma2(z, pack2(0.012308921664953232f, 0.012308921664953232f), pack2(-0.049270521849393845f, -0.049270521849393845f));
+  r = fma2(r, z, pack2(0.13225862383842468f, 0.13225862383842468f));
+  r = fma2(r, z, pack2(-0.33323100209236145f, -0.33323100209236145f));
+  r = fma2(r, z, pack2(0.9999973177909851f, 0.9999973177909851f));
+  return mul2(r, y);
+}
+
+// A unit of work: up to 256 rows of one (sequence, KV head) over one partition.
+struct PromptUnit {
+  int s, kvh, part;
+  SeqRows sr;
+  int r0, rows;
+  int start, end, nt;         // its tokens and tiles; s < 0: no more units
+  int all_from, all_to;       // the tokens that every row sees
+  // Whether some row does not see some token of tile j.
+  __device__ __forceinline__ bool careful(int j) const {
+    const int t0 = start + j * kPromptTile;
+    return t0 < all_from || t0 + kPromptTile > all_to;
+  }
+  __device__ __forceinline__ int halves() const { return rows > 128 ? 2 : 1; }
+};
 
 template <int D, bool CAP, bool SLOPES>
 __global__ void __launch_bounds__(kPromptThreads, 1)
@@ -52,90 +80,69 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   using S = PromptShape<D>;
   constexpr int ST = S::STAGES;
   launch_dependents();  // the merge may be scheduled as this grid drains
-  SplitUnit u;
-  if (!extend_unit(p, blockIdx.x, kPromptRows, threadIdx.x == 0, u)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = p.group;
-  auto q_row = [&](int r) {  // element offset of row r0 + r in q and out
-    return (size_t(u.sr.q0 + (u.r0 + r) / G) * p.num_q_heads + u.kvh * G + (u.r0 + r) % G) * D;
-  };
-  auto zero_rows = [&] {
-    for (int i = tid; i < u.rows * (D / 8); i += kPromptThreads)
-      *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + q_row(i / (D / 8)) + i % (D / 8) * 8) =
-          make_uint4(0, 0, 0, 0);
-  };
-  if (u.void_rows) return zero_rows();
-
-  const int halves = u.rows > 128 ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t q_sm = (smem_addr(smem_raw) + 1023u) & ~1023u, kv_sm = q_sm + 2 * S::Q_HALF;
-  __shared__ __align__(8) uint64_t bars[2 * ST + 8];
+  __shared__ __align__(8) uint64_t bars[2 * ST + 2 * kPromptUnits + 11];
+  __shared__ uint4 answer;
+  __shared__ PromptUnit units[kPromptUnits];
   __shared__ uint32_t tmem_slot;
-  __shared__ int lim[4], poisoned;
+  // The unit, plus one, whose values were not all finite where some rows do not see them.
+  // Nothing is cleared: a unit's mark is written by its own softmax warps and read before
+  // they give its entry back, which comes before the next unit of the same word.
+  __shared__ int poisoned[kPromptUnits];
+  // Units i, tiles of K and V k, tiles of a half, careful tiles and so on are counted over
+  // the life of the CTA; a barrier's phase is the count of what uses it. Every wait names a
+  // phase of which the one before has ended for certain and the one after cannot have: a
+  // wait by parity tells neighbouring phases apart, not more.
   auto bar = [&](int i) { return smem_addr(bars + i); };
-  auto kv_full = [&](int i) { return bar(i % ST); };          // tile i: K of tiles 0, 2, .., V of 1, 3, ..
-  auto kv_empty = [&](int i) { return bar(ST + i % ST); };
-  auto kv_phase = [](int i) { return uint32_t(i / ST) & 1u; };
-  const uint32_t q_full = bar(2 * ST), v_clean = bar(2 * ST + 1);
-  auto s_full = [&](int h) { return bar(2 * ST + 2 + h); };   // of a half, by tile
-  auto p_full = [&](int h) { return bar(2 * ST + 4 + h); };
-  auto o_done = [&](int h) { return bar(2 * ST + 6 + h); };   // once
+  auto kv_full = [&](int k) { return bar(k % ST); };
+  auto kv_empty = [&](int k) { return bar(ST + k % ST); };
+  auto kv_phase = [](int k) { return uint32_t(k / ST) & 1u; };
+  auto u_full = [&](int i) { return bar(2 * ST + i % kPromptUnits); };
+  auto u_empty = [&](int i) { return bar(2 * ST + kPromptUnits + i % kPromptUnits); };
+  auto u_phase = [](int i) { return uint32_t(i / kPromptUnits) & 1u; };
+  constexpr int B0 = 2 * ST + 2 * kPromptUnits;
+  const uint32_t q_full = bar(B0), q_empty = bar(B0 + 1), v_clean = bar(B0 + 2), u_want = bar(B0 + 3),
+                 u_answer = bar(B0 + 4);
+  auto s_full = [&](int h) { return bar(B0 + 5 + h); };  // of a half, by tile
+  auto p_full = [&](int h) { return bar(B0 + 7 + h); };
+  auto o_done = [&](int h) { return bar(B0 + 9 + h); };  // of a half, by unit
   if (tid == 0) {
-    lim[0] = INT32_MAX, lim[1] = 0, lim[2] = 0, lim[3] = INT32_MAX;
-    poisoned = 0;
     for (int i = 0; i < ST; ++i) mbar_init(kv_full(i), 1), mbar_init(kv_empty(i), 1);
-    mbar_init(q_full, 256);
-    mbar_init(v_clean, 4 * halves);
+    for (int i = 0; i < kPromptUnits; ++i) {
+      mbar_init(u_full(i), 1);
+      mbar_init(u_empty(i), 11);  // every warp but the one that fills them
+      poisoned[i] = 0;
+    }
+    mbar_init(q_full, 32);
+    mbar_init(q_empty, 1);
+    mbar_init(v_clean, 8);
+    mbar_init(u_want, 1);
+    mbar_init(u_answer, 1);
     for (int h = 0; h < 2; ++h) mbar_init(s_full(h), 1), mbar_init(p_full(h), 4), mbar_init(o_done(h), 1);
     fence_barrier_init();
   }
-  __syncthreads();
-  // A softmax thread has row `tid`; what the unit's rows see between them, and all see.
-  RowSpan x{0, 0, 0};
-  if (warp < 8) {
-    const bool mine = tid < u.rows;
-    if (mine) x = row_span(p, u.sr, u.s, (u.r0 + tid) / G);
-    const bool some = x.lo < x.hi;
-    const int from = __reduce_min_sync(0xffffffffu, some ? x.lo : INT32_MAX);
-    const int to = __reduce_max_sync(0xffffffffu, some ? x.hi : 0);
-    const int af = __reduce_max_sync(0xffffffffu, !mine ? 0 : (some ? x.lo : INT32_MAX));
-    const int at = __reduce_min_sync(0xffffffffu, !mine ? INT32_MAX : (some ? x.hi : 0));
-    if (lane == 0) {
-      atomicMin(&lim[0], from), atomicMax(&lim[1], to);
-      atomicMax(&lim[2], af), atomicMin(&lim[3], at);
-    }
-  }
-  __syncthreads();
-  if (!extend_tokens(p, u, lim[0], lim[1])) {
-    if (p.num_partitions == 1) zero_rows();
-    return;
-  }
-  const int start = u.start, end = u.end, nt = (end - start + kPromptTile - 1) / kPromptTile;
-  const int all_from = lim[2], all_to = min(lim[3], end);
-  // Whether some row does not see some token of tile j.
-  auto is_careful = [&](int j) {
-    const int t0 = start + j * kPromptTile;
-    return t0 < all_from || t0 + kPromptTile > all_to;
-  };
   if (warp == 9) tmem_alloc(smem_addr(&tmem_slot), 512);
-  if (warp < 8) {  // queries; rows past the last keep what is there: no row's result depends on another's
-    constexpr int CH = D / 8, STEP = 256 / CH;  // chunks of a row, rows at once
-    const int ch = tid % CH;
-    for (int row = tid / CH; row < u.rows; row += STEP)
-      cp_async16(q_sm + (row >> 7) * S::Q_HALF + (ch >> 3) * S::SLAB + (row & 127) * 128 +
-                     (((ch & 7) ^ (row & 7)) << 4),
-                 static_cast<const __nv_bfloat16 *>(p.q) + q_row(row) + ch * 8, 16);
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   auto t_s = [&](int h) { return tmem + 128u * h; };                // scores, then weights (64 columns)
   auto t_o = [&](int h) { return tmem + 256u + uint32_t(D) * h; };  // O
+  // A wait of the whole warp, which converges on it; once one has failed, so do all.
   auto warp_wait = [](uint32_t b, uint32_t parity, bool &ok) {
     ok = ok && __all_sync(0xffffffffu, mbar_wait(b, parity));
     return ok;
   };
+  auto release = [&](int i) {  // this warp is done with the unit's entry
+    __syncwarp();
+    if (lane == 0) mbar_arrive(u_empty(i));
+  };
   auto timeout = [&] { record_error(&g_rows_error, PK_DEVERR_TIMEOUT, blockIdx.x); };
+  auto q_row = [&](const SeqRows &sr, int kvh, int row) {  // element offset of a row of q and out
+    return (size_t(sr.q0 + row / G) * p.num_q_heads + kvh * G + row % G) * D;
+  };
 
   if (warp >= 8) {
     setmaxnreg_dec<kPromptOtherRegs>();
@@ -145,266 +152,399 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
       }
-      const int BS = p.block_size, per = kPromptTile / BS, nb = (end - start + BS - 1) / BS;
-      const int32_t *row = p.tables + size_t(u.s) * p.max_blocks + start / BS;
-      auto entry = [&](int j) {  // the lane's block of tile j
-        const int b = j * per + lane;
-        int phys = lane < per && b < nb ? __ldg(row + b) : 0;
-        if (phys < 0 || phys >= p.num_blocks) {
-          record_error(&g_rows_error, PK_DEVERR_BLOCK_ID, u.s);
-          phys = 0;  // stay in bounds and keep the byte count; the result is flagged
-        }
-        return phys;
-      };
+      const int BS = p.block_size, per = kPromptTile / BS;
       bool ok = true;
-      int i = 0, next = entry(0);
-      for (int j = 0; ok && j < nt; ++j) {
-        const int phys = next, nblk = min(per, nb - j * per);
-        next = entry(j + 1);
-        for (int side = 0; side < 2; ++side, ++i) {
-          if (i >= ST && !warp_wait(kv_empty(i), kv_phase(i - ST), ok)) break;
-          if (lane == 0) mbar_arrive_expect_tx(kv_full(i), uint32_t(nblk * S::SLABS * BS * 128));
-          __syncwarp();
-          if (lane < nblk) {
-            const uint32_t dst = kv_sm + i % ST * S::TILE + lane * BS * 128;
+      int k = 0;  // tiles of K and V
+      for (int i = 0; warp_wait(u_full(i), u_phase(i), ok); ++i) {
+        const PromptUnit &c = units[i % kPromptUnits];
+        const int s = c.s, kvh = c.kvh, nt = c.nt, nb = (c.end - c.start + BS - 1) / BS;
+        const int32_t *row = p.tables + size_t(max(s, 0)) * p.max_blocks + c.start / BS;
+        release(i);
+        if (s < 0) break;
+        auto entry = [&](int j) {  // the lane's block of tile j
+          const int b = j * per + lane;
+          int phys = lane < per && b < nb ? __ldg(row + b) : 0;
+          if (phys < 0 || phys >= p.num_blocks) {
+            record_error(&g_rows_error, PK_DEVERR_BLOCK_ID, s);
+            phys = 0;  // stay in bounds and keep the byte count; the result is flagged
+          }
+          return phys;
+        };
+        int next = entry(0);
+        for (int j = 0; ok && j < nt; ++j) {
+          // The unit after this one is asked for three tiles before the end: early enough
+          // to be here in time, late enough to go to the CTA that is free first.
+          if (j == max(0, nt - 3) && lane == 0) mbar_arrive(u_want);
+          const int phys = next, nblk = min(per, nb - j * per);
+          next = entry(j + 1);
+          for (int side = 0; side < 2; ++side, ++k) {
+            if (k >= ST && !warp_wait(kv_empty(k), kv_phase(k - ST), ok)) break;
+            if (lane == 0) mbar_arrive_expect_tx(kv_full(k), uint32_t(nblk * S::SLABS * BS * 128));
+            __syncwarp();
+            if (lane < nblk) {
+              const uint32_t dst = kv_sm + k % ST * S::TILE + lane * BS * 128;
 #pragma unroll
-            for (int c = 0; c < S::SLABS; ++c)
-              tma_load_3d(dst + c * S::SLAB, side ? &vmap : &kmap, kv_full(i), c * 64, u.kvh, phys * BS);
+              for (int x = 0; x < S::SLABS; ++x)
+                tma_load_3d(dst + x * S::SLAB, side ? &vmap : &kmap, kv_full(k), x * 64, kvh, phys * BS);
+            }
           }
         }
       }
       if (!ok && lane == 0) timeout();
       // Let every issued copy land before the warp leaves.
-      for (int k = max(0, i - ST); k < i; ++k) mbar_wait(kv_full(k), kv_phase(k));
+      for (int x = max(0, k - ST); x < k; ++x) mbar_wait(kv_full(x), kv_phase(x));
     } else if (warp == 9) {
       // ---------------- products ----------------
       // S of both halves, then in turn a half's O += P V and its next S: while one half's
       // softmax runs, the tensor cores have the other's products.
       constexpr uint32_t O_DESC = mma_desc(128, D, true);
       const uint32_t s_desc = mma_desc(128, kPromptTile, false) | (p.factor < 0.0f ? 1u << 13 : 0u);  // -Q
-      auto scores = [&](int h, int j) {
-        if (elect_one()) {
-          const uint64_t a = smem_desc(q_sm + h * S::Q_HALF, 16, 1024);
-          const uint64_t b = smem_desc(kv_sm + 2 * j % ST * S::TILE, 16, 1024);
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)  // a descriptor's address counts 16 bytes
-            tc_mma_ss(t_s(h), a + (ks / 4) * (S::SLAB / 16) + (ks % 4) * 2, b + (ks / 4) * (S::SLAB / 16) + (ks % 4) * 2,
-                      s_desc, ks > 0);
-          tc_commit(s_full(h));
-          if (h + 1 == halves) tc_commit(kv_empty(2 * j));
-        }
-        __syncwarp();
-      };
       bool ok = true;
-      if (warp_wait(q_full, 0, ok) && warp_wait(kv_full(0), 0, ok)) {
-        tc_fence_after();
-        for (int h = 0; h < halves; ++h) scores(h, 0);
-      }
-      int c = 0;  // careful tiles so far
-      for (int j = 0; ok && j < nt; ++j) {
-        const int iv = 2 * j + 1, ik = 2 * j + 2;
-        if (!warp_wait(kv_full(iv), kv_phase(iv), ok)) break;
-        if (is_careful(j) && !warp_wait(v_clean, c++ & 1, ok)) break;
-        for (int h = 0; h < halves; ++h) {
-          if (!warp_wait(p_full(h), j & 1, ok)) break;
-          tc_fence_after();
+      int k0 = 0, c = 0, n[2] = {0, 0}, done[2] = {0, 0};  // tiles before the unit, careful ones, of a half, its units
+      for (int i = 0; warp_wait(u_full(i), u_phase(i), ok); ++i) {
+        const PromptUnit unit = units[i % kPromptUnits];
+        const int nt = unit.nt, halves = unit.halves();
+        release(i);
+        if (unit.s < 0) break;
+        auto scores = [&](int h, int j) {
           if (elect_one()) {
-            const uint64_t b = smem_desc(kv_sm + iv % ST * S::TILE, S::SLAB, 1024);
+            const uint64_t a = smem_desc(q_sm + h * S::Q_HALF, 16, 1024);
+            const uint64_t b = smem_desc(kv_sm + (k0 + 2 * j) % ST * S::TILE, 16, 1024);
 #pragma unroll
-            for (int ks = 0; ks < kPromptTile / 16; ++ks)
-              tc_mma_ts(t_o(h), t_s(h) + 8 * ks, b + ks * 128, O_DESC, j > 0 || ks > 0);
-            if (h + 1 == halves) tc_commit(kv_empty(iv));
-            if (j + 1 == nt) tc_commit(o_done(h));
+            for (int ks = 0; ks < D / 16; ++ks)  // a descriptor's address counts 16 bytes
+              tc_mma_ss(t_s(h), a + (ks / 4) * (S::SLAB / 16) + (ks % 4) * 2,
+                        b + (ks / 4) * (S::SLAB / 16) + (ks % 4) * 2, s_desc, ks > 0);
+            tc_commit(s_full(h));
+            if (h + 1 == halves) {
+              tc_commit(kv_empty(k0 + 2 * j));
+              if (j + 1 == nt) tc_commit(q_empty);
+            }
           }
           __syncwarp();
-          if (j + 1 < nt) {
-            if (h == 0 && !warp_wait(kv_full(ik), kv_phase(ik), ok)) break;
-            scores(h, j + 1);
+        };
+        if (!warp_wait(q_full, i & 1, ok) || !warp_wait(kv_full(k0), kv_phase(k0), ok)) break;
+        tc_fence_after();
+        for (int h = 0; h < halves; ++h) scores(h, 0);
+        for (int j = 0; ok && j < nt; ++j) {
+          const int iv = k0 + 2 * j + 1, ik = iv + 1;
+          if (!warp_wait(kv_full(iv), kv_phase(iv), ok)) break;
+          if (unit.careful(j) && !warp_wait(v_clean, c++ & 1, ok)) break;
+          for (int h = 0; h < halves; ++h) {
+            if (!warp_wait(p_full(h), n[h]++ & 1, ok)) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t b = smem_desc(kv_sm + iv % ST * S::TILE, S::SLAB, 1024);
+#pragma unroll
+              for (int ks = 0; ks < kPromptTile / 16; ++ks)
+                tc_mma_ts(t_o(h), t_s(h) + 8 * ks, b + ks * 128, O_DESC, j > 0 || ks > 0);
+              if (h + 1 == halves) tc_commit(kv_empty(iv));
+              if (j + 1 == nt) tc_commit(o_done(h));
+            }
+            __syncwarp();
+            if (j + 1 < nt) {
+              if (h == 0 && !warp_wait(kv_full(ik), kv_phase(ik), ok)) break;
+              scores(h, j + 1);
+            }
           }
         }
+        if (!ok) break;
+        k0 += 2 * nt;
+        for (int h = 0; h < halves; ++h) ++done[h];
       }
       if (!ok && lane == 0) timeout();
       // Nothing of this warp's products is under way when tensor memory is freed.
-      if (!ok && elect_one()) tc_commit(o_done(0));
+      if (!ok) {
+        if (elect_one()) tc_commit(q_empty);
+        __syncwarp();
+        mbar_wait(q_empty, 0, 1u << 10);
+        mbar_wait(q_empty, 1, 1u << 10);
+      }
+      for (int h = 0; h < 2; ++h)
+        if (done[h] > 0) mbar_wait(o_done(h), (done[h] - 1) & 1);
       __syncwarp();
-      mbar_wait(o_done(0), 0);
-      if (ok && halves == 2) mbar_wait(o_done(1), 0);
-      __syncwarp();
+    } else if (warp == 10) {
+      // ---------------- units ----------------
+      // The grid has a CTA per unit; those that find no room are taken over, one at a time,
+      // by whichever CTA needs work next (the list is longest first).
+      bool ok = true;
+      int published = 0;
+      auto publish = [&](const PromptUnit &c) {
+        const int i = published;
+        if (i >= kPromptUnits && !warp_wait(u_empty(i), u_phase(i - kPromptUnits), ok)) return;
+        if (lane == 0) {
+          units[i % kPromptUnits] = c;
+          mbar_arrive(u_full(i));
+        }
+        ++published;
+      };
+      for (int cta = blockIdx.x, asked = 0; cta >= 0;) {
+        SplitUnit u;
+        bool work = extend_unit(p, cta, kPromptRows, lane == 0, u), zero = work && u.void_rows;
+        PromptUnit c;
+        if (work && !zero) {
+          // What the unit's rows see between them, and what all see.
+          int from = INT32_MAX, to = 0, af = 0, at = INT32_MAX;
+          for (int r = lane; r < u.rows; r += 32) {
+            const RowSpan x = row_span(p, u.sr, u.s, (u.r0 + r) / G);
+            const bool some = x.lo < x.hi;
+            if (some) from = min(from, x.lo), to = max(to, x.hi);
+            af = max(af, some ? x.lo : INT32_MAX), at = min(at, some ? x.hi : 0);
+          }
+          from = __reduce_min_sync(0xffffffffu, from), to = __reduce_max_sync(0xffffffffu, to);
+          af = __reduce_max_sync(0xffffffffu, af), at = __reduce_min_sync(0xffffffffu, at);
+          if (!extend_tokens(p, u, from, to)) work = false, zero = p.num_partitions == 1;
+          c.all_from = af, c.all_to = min(at, u.end);
+        }
+        if (zero) {
+          for (int k = lane; k < u.rows * (D / 8); k += 32)
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + q_row(u.sr, u.kvh, u.r0 + k / (D / 8)) +
+                                       k % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
+        } else if (work) {
+          c.s = u.s, c.kvh = u.kvh, c.part = u.part, c.sr = u.sr, c.r0 = u.r0, c.rows = u.rows;
+          c.start = u.start, c.end = u.end, c.nt = (u.end - u.start + kPromptTile - 1) / kPromptTile;
+          publish(c);
+          if (!ok || !warp_wait(u_want, (published - 1) & 1, ok)) break;
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(u_answer, 16);
+          try_cancel(smem_addr(&answer), u_answer);
+        }
+        if (!warp_wait(u_answer, asked & 1, ok)) break;
+        ++asked;
+        cta = cancelled_cta(smem_addr(&answer));
+        fence_answer_read();
+        __syncwarp();
+      }
+      PromptUnit end{};
+      end.s = -1;
+      if (ok) publish(end);
+      if (!ok && lane == 0) timeout();
+    } else {
+      // ---------------- queries ----------------
+      bool ok = true;
+      for (int i = 0; warp_wait(u_full(i), u_phase(i), ok); ++i) {
+        const PromptUnit &c = units[i % kPromptUnits];
+        const int s = c.s, kvh = c.kvh, r0 = c.r0, rows = c.rows;
+        const SeqRows sr = c.sr;
+        release(i);
+        if (s < 0 || (i > 0 && !warp_wait(q_empty, (i - 1) & 1, ok))) break;
+        // Rows past the last keep what is there: no row's result depends on another's query.
+        constexpr int CH = D / 8, STEP = 32 / CH;  // chunks of a row, rows at once
+        const int ch = lane % CH;
+        int tok = (r0 + lane / CH) / G, g = (r0 + lane / CH) % G;
+        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) +
+                                   (size_t(sr.q0) * p.num_q_heads + kvh * G) * D + ch * 8;
+        const uint32_t dst = q_sm + (ch >> 3) * S::SLAB;
+#pragma unroll 4
+        for (int row = lane / CH; row < rows; row += STEP) {
+          cp_async16(dst + (row >> 7) * S::Q_HALF + (row & 127) * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                     src + (size_t(tok) * p.num_q_heads + g) * D, 16);
+          for (g += STEP; g >= G; g -= G) ++tok;
+        }
+        cp_async_wait();
+        fence_proxy_async_shared();
+        mbar_arrive(q_full);
+      }
+      if (!ok && lane == 0) timeout();
     }
   } else {
     // ---------------- softmax: a thread is a row ----------------
     setmaxnreg_inc<kPromptSoftmaxRegs>();
-    cp_async_wait();
-    fence_proxy_async_shared();
-    mbar_arrive(q_full);
     const int h = warp >> 2;
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
-    const bool busy = warp * 32 < u.rows;
     // In the exponent's scale. At least the smallest normal number: a scale of 0 must not
     // turn the -inf of what is masked into NaN.
     const float fac = fmaxf(fabsf(p.factor), 1.17549435e-38f);
     const float sl = SLOPES ? 1.0f : (CAP ? p.cap_log2 : fac);
-    const float slope =
-        SLOPES && tid < u.rows ? __ldg(p.slopes + u.kvh * G + (u.r0 + tid) % G) * 1.44269504f : 0.0f;
     bool ok = true;
-    int c = 0;  // careful tiles so far
-    float ref = -INFINITY, l = 0.0f;  // the exponent's reference (scaled scores), the sum
-    for (int j = 0; h < halves && j < nt; ++j) {
-      const int t0 = start + j * kPromptTile;
-      const bool careful = is_careful(j);
-      uint32_t s[4][32];
-      if (!warp_wait(s_full(h), j & 1, ok)) break;
-      tc_fence_after();
-      if (busy)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) tmem_load32(t_s(h) + lane_base + 32 * e, s[e]);
-      if (careful) {
-        // Values past the end are zeroed, and so is what is not finite in values that some
-        // rows do not see, which would reach those too (0 * NaN); the rows that do see it
-        // get it at the end. The warpgroups share the tokens.
-        const int iv = 2 * j + 1, valid = min(kPromptTile, end - t0);
-        if (!warp_wait(kv_full(iv), kv_phase(iv), ok)) break;
-        constexpr int CH = D / 8, STEP = 128 / CH;
-        const int r = tid & 127, ch = r % CH;
-        const uint32_t at = kv_sm + iv % ST * S::TILE + (ch >> 3) * S::SLAB + (ch & 7) * 16;
-        bool wrote = false;
-#pragma unroll 4
-        for (int k = h * 64 + r / CH; k < (h + 1 == halves ? kPromptTile : 64); k += STEP) {
-          const int t = t0 + k;
-          if (t >= all_from && t < all_to) continue;
-          uint32_t w[4];
-          const uint32_t a = at + k * 128;
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                       : "r"(a));
-          // A carry into a half's sign shows an exponent of all ones.
-          uint32_t odd = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) odd |= (w[e] & 0x7f807f80u) + 0x00800080u;
-          if (k < valid && !(odd & 0x80008000u)) continue;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (k >= valid || (w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
-            if (k >= valid || (w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu;
-          }
-          if (k < valid) poisoned = 1;
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                       "r"(w[3])
-                       : "memory");
-          wrote = true;
-        }
-        if (__any_sync(0xffffffffu, wrote)) fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(v_clean);
-        ++c;
+    int k0 = 0, n = 0, done = 0;  // tiles of K and V before the unit, the half's tiles and units
+    for (int i = 0; warp_wait(u_full(i), u_phase(i), ok); ++i) {
+      const PromptUnit &unit = units[i % kPromptUnits];
+      if (unit.s < 0) break;
+      const int nt = unit.nt, start = unit.start, end = unit.end, halves = unit.halves(), rows = unit.rows;
+      if (h >= halves) {  // the other half has it alone
+        k0 += 2 * nt;
+        release(i);
+        continue;
       }
-      if (busy) {
+      const bool busy = warp * 32 < rows;  // this warp has rows
+      RowSpan x{0, 0, 0};
+      float slope = 0.0f;
+      if (tid < rows) {
+        x = row_span(p, unit.sr, unit.s, (unit.r0 + tid) / G);
+        if (SLOPES) slope = __ldg(p.slopes + unit.kvh * G + (unit.r0 + tid) % G) * 1.44269504f;
+      }
+      float ref = -INFINITY, l = 0.0f;  // the exponent's reference (scaled scores), the sum
+      for (int j = 0; j < nt; ++j, ++n) {
+        const int t0 = start + j * kPromptTile;
+        const bool careful = unit.careful(j);
+        uint32_t s[4][32];
+        if (!warp_wait(s_full(h), n & 1, ok)) break;
+        tc_fence_after();
+        if (busy)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) tmem_wait_load(s[e]);
-        if (CAP) {
-          const uint64_t k = pack2(2.0f * 1.44269504f * fac, 2.0f * 1.44269504f * fac);
-#pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            float a, b;
-            unpack2(tanh2(pack2(__uint_as_float(s[i / 16][2 * (i % 16)]), __uint_as_float(s[i / 16][2 * (i % 16) + 1])), k),
-                    a, b);
-            s[i / 16][2 * (i % 16)] = __float_as_uint(a), s[i / 16][2 * (i % 16) + 1] = __float_as_uint(b);
-          }
-        }
-        if (SLOPES) {
-          const float d0 = float(t0 - x.pos), f = CAP ? p.cap_log2 : fac;
-          const uint64_t f2 = pack2(f, f), m2 = pack2(-slope, -slope);
-#pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            const uint64_t away = add2(pack2(d0, d0), pack2(float(2 * i), float(2 * i + 1))) & 0x7fffffff7fffffffull;
-            float a, b;
-            unpack2(fma2(away, m2, mul2(pack2(__uint_as_float(s[i / 16][2 * (i % 16)]),
-                                              __uint_as_float(s[i / 16][2 * (i % 16) + 1])), f2)),
-                    a, b);
-            s[i / 16][2 * (i % 16)] = __float_as_uint(a), s[i / 16][2 * (i % 16) + 1] = __float_as_uint(b);
-          }
-        }
+          for (int e = 0; e < 4; ++e) tmem_load32(t_s(h) + lane_base + 32 * e, s[e]);
         if (careful) {
-          const int lo = max(0, x.lo - t0), hi = min(x.hi, end) - t0;
+          // Values past the end are zeroed, and so is what is not finite in values that some
+          // rows do not see, which would reach those too (0 * NaN); the rows that do see it
+          // get it at the end. The warpgroups share the tokens.
+          const int iv = k0 + 2 * j + 1, valid = min(kPromptTile, end - t0);
+          const int all_from = unit.all_from, all_to = unit.all_to;
+          if (!warp_wait(kv_full(iv), kv_phase(iv), ok)) break;
+          constexpr int CH = D / 8, STEP = 128 / CH;
+          const int r = tid & 127, ch = r % CH;
+          const uint32_t at = kv_sm + iv % ST * S::TILE + (ch >> 3) * S::SLAB + (ch & 7) * 16;
+          bool wrote = false;
+#pragma unroll 4
+          for (int k = h * 64 + r / CH; k < (h + 1 == halves ? kPromptTile : 64); k += STEP) {
+            const int t = t0 + k;
+            if (t >= all_from && t < all_to) continue;
+            uint32_t w[4];
+            const uint32_t a = at + k * 128;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(a));
+            // A carry into a half's sign shows an exponent of all ones.
+            uint32_t odd = 0;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int a = min(max(lo - 32 * e, 0), 32), b = min(max(hi - 32 * e, 0), 32);  // columns a .. b - 1 seen
-            const uint32_t see = (b == 32 ? ~0u : (1u << b) - 1) & (a == 32 ? 0u : ~0u << a);
+            for (int e = 0; e < 4; ++e) odd |= (w[e] & 0x7f807f80u) + 0x00800080u;
+            if (k < valid && !(odd & 0x80008000u)) continue;
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (!(see & (1u << k))) s[e][k] = 0xff800000u;  // -inf
+            for (int e = 0; e < 4; ++e) {
+              if (k >= valid || (w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
+              if (k >= valid || (w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu;
+            }
+            if (k < valid) poisoned[i % kPromptUnits] = i + 1;
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                         "r"(w[3])
+                         : "memory");
+            wrote = true;
+          }
+          if (__any_sync(0xffffffffu, wrote)) fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(v_clean);
+            if (halves == 1) mbar_arrive(v_clean);  // for the other half's warp
           }
         }
-        float mx;
-        {
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (busy) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
-            top[i & 3] = max3(top[i & 3], __uint_as_float(s[i / 16][2 * (i % 16)]),
-                              __uint_as_float(s[i / 16][2 * (i % 16) + 1]));
-          mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-          mx = mx == -INFINITY ? mx : mx * sl;
-        }
-        const bool move = mx > ref + kPromptSlack;
-        if (__any_sync(0xffffffffu, move)) {
-          const float f = move ? exp2_ftz(ref - mx) : 1.0f;
-          if (move) ref = mx;
-          l *= f;
-          if (j > 0) {  // these scores came after the products of the tile before
-            const uint64_t f2 = pack2(f, f);
-#pragma unroll 1
-            for (int ch = 0; ch < D / 32; ++ch) {
-              uint32_t o[32];
-              tmem_load32(t_o(h) + lane_base + 32 * ch, o);
-              tmem_wait_load(o);
+          for (int e = 0; e < 4; ++e) tmem_wait_load(s[e]);
+          auto pair = [&](int i) {
+            return pack2(__uint_as_float(s[i / 16][2 * (i % 16)]), __uint_as_float(s[i / 16][2 * (i % 16) + 1]));
+          };
+          auto set_pair = [&](int i, uint64_t v) {
+            float a, b;
+            unpack2(v, a, b);
+            s[i / 16][2 * (i % 16)] = __float_as_uint(a), s[i / 16][2 * (i % 16) + 1] = __float_as_uint(b);
+          };
+          auto largest = [&](auto of) {
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                float a, b;
-                unpack2(mul2(pack2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])), f2), a, b);
-                o[2 * k] = __float_as_uint(a);
-                o[2 * k + 1] = __float_as_uint(b);
-              }
-              tmem_store32(t_o(h) + lane_base + 32 * ch, o);
+            for (int i = 0; i < 64; ++i)
+              top[i & 3] = max3(top[i & 3], of(__uint_as_float(s[i / 16][2 * (i % 16)])),
+                                of(__uint_as_float(s[i / 16][2 * (i % 16) + 1])));
+            return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+          };
+          if (CAP) {
+            const bool small = largest([](float v) { return fabsf(v); }) * fac <= kTanhSmall;
+            if (__all_sync(0xffffffffu, small)) {
+              const uint64_t f2 = pack2(fac, fac);
+#pragma unroll
+              for (int i = 0; i < 64; ++i) set_pair(i, tanh2_small(pair(i), f2));
+            } else {
+              const uint64_t k2 = pack2(2.0f * 1.44269504f * fac, 2.0f * 1.44269504f * fac);
+#pragma unroll
+              for (int i = 0; i < 64; ++i) set_pair(i, tanh2(pair(i), k2));
             }
           }
-        }
-        const float m = ref == -INFINITY ? 0.0f : ref;  // nothing seen so far: every weight is 0
-        const uint64_t sl2 = pack2(sl, sl), m2 = pack2(-m, -m);
-        uint64_t sum2[2] = {0, 0};
+          if (SLOPES) {
+            const float d0 = float(t0 - x.pos), f = CAP ? p.cap_log2 : fac;
+            const uint64_t f2 = pack2(f, f), m2 = pack2(-slope, -slope);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t w[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float a, b;
-            unpack2(fma2(pack2(__uint_as_float(s[e][2 * k]), __uint_as_float(s[e][2 * k + 1])), sl2, m2), a, b);
-            // The weights enter the product as one bf16 each and are summed as they enter,
-            // so that a row's weights add up to 1: an average of values, each weight off by
-            // 2^-8 at most. A second half of each would cost half as many products again.
-            w[k] = pack_bf16x2(exp2_ftz(a), exp2_ftz(b));
-            sum2[k & 1] = add2(sum2[k & 1], pack2(bf16_lo(w[k]), bf16_hi(w[k])));
+            for (int i = 0; i < 64; ++i) {
+              const uint64_t away =
+                  add2(pack2(d0, d0), pack2(float(2 * i), float(2 * i + 1))) & 0x7fffffff7fffffffull;
+              set_pair(i, fma2(away, m2, mul2(pair(i), f2)));
+            }
           }
-          tmem_store16(t_s(h) + lane_base + 16 * e, w);
+          if (careful) {
+            const int lo = max(0, x.lo - t0), hi = min(x.hi, end) - t0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int a = min(max(lo - 32 * e, 0), 32), b = min(max(hi - 32 * e, 0), 32);  // columns a .. b - 1 seen
+              const uint32_t see = (b == 32 ? ~0u : (1u << b) - 1) & (a == 32 ? 0u : ~0u << a);
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!(see & (1u << k))) s[e][k] = 0xff800000u;  // -inf
+            }
+          }
+          float mx = largest([](float v) { return v; });
+          mx = mx == -INFINITY ? mx : mx * sl;
+          const bool move = mx > ref + kPromptSlack;
+          if (__any_sync(0xffffffffu, move)) {
+            const float f = move ? exp2_ftz(ref - mx) : 1.0f;
+            if (move) ref = mx;
+            l *= f;
+            if (j > 0) {  // these scores came after the products of the tile before
+              const uint64_t f2 = pack2(f, f);
+#pragma unroll 1
+              for (int ch = 0; ch < D / 32; ++ch) {
+                uint32_t o[32];
+                tmem_load32(t_o(h) + lane_base + 32 * ch, o);
+                tmem_wait_load(o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  float a, b;
+                  unpack2(mul2(pack2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])), f2), a, b);
+                  o[2 * k] = __float_as_uint(a);
+                  o[2 * k + 1] = __float_as_uint(b);
+                }
+                tmem_store32(t_o(h) + lane_base + 32 * ch, o);
+              }
+            }
+          }
+          const float m = ref == -INFINITY ? 0.0f : ref;  // nothing seen so far: every weight is 0
+          const uint64_t sl2 = pack2(sl, sl), m2 = pack2(-m, -m);
+          uint64_t sum2[2] = {0, 0};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float a, b;
+              unpack2(fma2(pair(16 * e + k), sl2, m2), a, b);
+              // The weights enter the product as one bf16 each and are summed as they enter,
+              // so that a row's weights add up to 1: an average of values, each weight off by
+              // 2^-8 at most. A second half of each would cost half as many products again.
+              w[k] = pack_bf16x2(exp2_ftz(a), exp2_ftz(b));
+              sum2[k & 1] = add2(sum2[k & 1], pack2(bf16_lo(w[k]), bf16_hi(w[k])));
+            }
+            tmem_store16(t_s(h) + lane_base + 16 * e, w);
+          }
+          {
+            float a, b;
+            unpack2(add2(sum2[0], sum2[1]), a, b);
+            l += a + b;
+          }
+          tmem_wait_store();
         }
-        {
-          float a, b;
-          unpack2(add2(sum2[0], sum2[1]), a, b);
-          l += a + b;
-        }
-        tmem_wait_store();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(h));
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(h));
-    }
-    // The marks of all warps are in.
-    if (ok && c > 0) warp_wait(v_clean, (c - 1) & 1, ok);
-    if (ok && busy && warp_wait(o_done(h), 0, ok)) {
+      k0 += 2 * nt;
+      // (The products came after every warp had cleared its values, so the marks are in.)
+      if (!ok || !warp_wait(o_done(h), done++ & 1, ok)) break;
+      if (!busy) {
+        release(i);
+        continue;
+      }
       tc_fence_after();
-      const bool mine = tid < u.rows;
-      const Place place = mine ? row_place(p, x.lo, x.hi, u.part) : Place::kNowhere;
+      const bool mine = tid < rows;
+      const Place place = mine ? row_place(p, x.lo, x.hi, unit.part) : Place::kNowhere;
       const float inv = 1.0f / denominator(l, false);
-      const size_t at = mine ? q_row(tid) : 0, slot = at / D * p.num_partitions + u.part;
+      const size_t at = mine ? q_row(unit.sr, unit.kvh, unit.r0 + tid) : 0, slot = at / D * p.num_partitions + unit.part;
       // A lane has a row, but rows are 64 bytes or more apart in memory: 64 bytes of each go
       // through shared memory, so that four lanes write a row's together.
       const uint32_t stage = kv_sm + ST * S::TILE + warp * S::OUT_BYTES;
@@ -423,8 +563,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                        : "r"(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4)));
-          char *dst = reinterpret_cast<char *>(
-              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), r));
+          char *dst = reinterpret_cast<char *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), r));
           if (dst) *reinterpret_cast<uint4 *>(dst + (lane & 3) * 16) = v;
         }
         __syncwarp();
@@ -456,18 +595,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         p.ws_m[slot] = merge_max(ref, l);
         p.ws_l[slot] = l;
       }
-      if (poisoned && place != Place::kNowhere) {
+      if (poisoned[i % kPromptUnits] == i + 1 && place != Place::kNowhere) {
         // What is not finite in the values that the row sees, of the tiles that were cleared.
         for (int j = 0; j < nt; ++j) {
-          if (!is_careful(j)) continue;
+          if (!unit.careful(j)) continue;
           const int t0 = start + j * kPromptTile;
           for (int t = max(x.lo, t0); t < min(min(x.hi, end), t0 + kPromptTile); ++t) {
-            if (t >= all_from && t < all_to) continue;
-            const int phys = __ldg(p.tables + size_t(u.s) * p.max_blocks + t / p.block_size);
+            if (t >= unit.all_from && t < unit.all_to) continue;
+            const int phys = __ldg(p.tables + size_t(unit.s) * p.max_blocks + t / p.block_size);
             if (phys < 0 || phys >= p.num_blocks) continue;
             const __nv_bfloat16 *v =
                 static_cast<const __nv_bfloat16 *>(p.v_cache) +
-                ((size_t(phys) * p.block_size + t % p.block_size) * p.num_kv_heads + u.kvh) * D;
+                ((size_t(phys) * p.block_size + t % p.block_size) * p.num_kv_heads + unit.kvh) * D;
             for (int e = 0; e < D; ++e) {
               const float y = __bfloat162float(v[e]);
               if (fabsf(y) <= 3.402823466e38f) continue;
@@ -481,6 +620,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
         }
       }
+      release(i);
+      tc_fence_before();  // O may be overwritten once the next unit's weights are there
     }
     if (!ok && lane == 0) timeout();
   }
