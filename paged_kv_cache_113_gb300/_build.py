@@ -20,10 +20,12 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libpagedkv.so")
-SOURCES = ["attention.cu", "attention_e4m3.cu", "tree_attention.cu", "extend_attention.cu", "draft_ops.cu", "cache_ops.cu", "cache_e4m3.cu",
+SOURCES = ["attention.cu", "attention_e4m3.cu", "tree_attention.cu", "extend_attention.cu", "draft_ops.cu",
+           "cache_ops.cu", "cache_e4m3.cu",
            "qk_norm_rope.cu", "block_manager.cpp", "decode_step.cpp", "allocator_sim.cpp"]
 HEADERS = [os.path.join(CSRC, "pk_device.cuh"), os.path.join(CSRC, "attn_rows.cuh"),
            os.path.join(CSRC, "attn_split.cuh"), os.path.join(CSRC, "attn_extend.cuh"), os.path.join(CSRC, "extend_prompt.cuh"),
+           os.path.join(CSRC, "extend_few.cuh"), os.path.join(CSRC, "attn_tile.cuh"),
            os.path.join(CSRC, "pk_tma_host.h"), os.path.join(CSRC, "pk_tcgen05.cuh"),
            os.path.join(INCLUDE, "pagedkv.h")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"

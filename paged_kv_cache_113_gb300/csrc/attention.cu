@@ -58,6 +58,7 @@
 #include <new>
 #include <vector>
 
+#include "attn_tile.cuh"
 #include "pagedkv.h"
 #include "pk_device.cuh"
 #include "pk_tma_host.h"
@@ -404,7 +405,6 @@ __device__ __forceinline__ void attn_tile(uint32_t kbase, uint32_t vbase, int sl
                                           float &l1, float sl, int lane) {
   constexpr int HALVES = KSTEPS / 4;
   const int rw = lane >> 2;
-  const int mi = lane >> 3, r8 = lane & 7;
   if (nvalid < 16) {
     const int nz = (16 - nvalid) * HALVES * 8;
     for (int idx = lane; idx < nz; idx += 32) {
@@ -415,18 +415,8 @@ __device__ __forceinline__ void attn_tile(uint32_t kbase, uint32_t vbase, int sl
     }
     __syncwarp();
   }
-  // S^T = K_tile (16 x D) * Q^T (D x 8), as two independent accumulation
-  // chains (even and odd k-steps).
-  float sacc[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-#pragma unroll
-  for (int ks = 0; ks < KSTEPS; ++ks) {
-    const int r = row0 + (mi & 1) * 8 + r8;
-    const int chunk = ks * 2 + (mi >> 1);
-    const uint32_t a = kbase + (chunk >> 3) * slab + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
-    uint32_t a0, a1, a2, a3;
-    pk::ldmatrix_x4(a, a0, a1, a2, a3);
-    pk::mma_bf16_16816(sacc[ks & 1], a0, a1, a2, a3, qb[ks][0], qb[ks][1]);
-  }
+  float sacc[2][4];
+  pk::tile_scores<KSTEPS>(kbase, slab, row0, qb, sacc, lane);
   float x0 = (sacc[0][0] + sacc[1][0]) * sl, x1 = (sacc[0][1] + sacc[1][1]) * sl;
   float x2 = (sacc[0][2] + sacc[1][2]) * sl, x3 = (sacc[0][3] + sacc[1][3]) * sl;
   if (rw >= nvalid) x0 = x1 = -INFINITY;
@@ -458,27 +448,7 @@ __device__ __forceinline__ void attn_tile(uint32_t kbase, uint32_t vbase, int sl
     o[mt][2] *= c0;
     o[mt][3] *= c1;
   }
-  // P^T (16 tokens x 8 heads) as the B operand: transpose the C fragments.
-  const uint32_t b0 = pk::movmatrix_trans(w01);
-  const uint32_t b1 = pk::movmatrix_trans(w23);
-  const uint32_t e0 = pk::movmatrix_trans(r01);
-  const uint32_t e1 = pk::movmatrix_trans(r23);
-  // O^T (D x 8) += V^T (D x 16 tokens) * P^T: all hi products first, then
-  // all lo products, so consecutive MMAs never share an accumulator.
-  uint32_t va[KSTEPS][4];
-#pragma unroll
-  for (int mt = 0; mt < KSTEPS; ++mt) {
-    const int r = row0 + (mi >> 1) * 8 + r8;
-    const int chunk = mt * 2 + (mi & 1);
-    const uint32_t a = vbase + (chunk >> 3) * slab + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
-    pk::ldmatrix_x4_trans(a, va[mt][0], va[mt][1], va[mt][2], va[mt][3]);
-  }
-#pragma unroll
-  for (int mt = 0; mt < KSTEPS; ++mt)
-    pk::mma_bf16_16816(o[mt], va[mt][0], va[mt][1], va[mt][2], va[mt][3], b0, b1);
-#pragma unroll
-  for (int mt = 0; mt < KSTEPS; ++mt)
-    pk::mma_bf16_16816(o[mt], va[mt][0], va[mt][1], va[mt][2], va[mt][3], e0, e1);
+  pk::tile_values<KSTEPS>(vbase, slab, row0, w01, w23, r01, r23, o, lane);
 }
 
 // The work of one attn_mma_kernel CTA at grid coordinate c.

@@ -10,6 +10,7 @@
 
 #include "attn_extend.cuh"
 #include "extend_prompt.cuh"
+#include "extend_few.cuh"
 #include "pagedkv.h"
 
 namespace pk {
@@ -27,13 +28,18 @@ int sm_count() {
   return 152;
 }
 
-// Whether sequences of at most `rows` rows go to attn_prompt_kernel.
-bool prompt_path(const pk_cache_desc &d, int64_t rows) {
-  return d.dtype == PK_BF16 && rows > 8 && (d.block_size == 8 || d.block_size == 16 || d.block_size == 32);
+// The kernel of sequences of at most `rows` rows, and the rows of its units.
+enum class Path { kFew, kPrompt, kSplit };
+Path path_of(const pk_cache_desc &d, int64_t rows) {
+  if (d.dtype != PK_BF16 || (d.block_size != 8 && d.block_size != 16 && d.block_size != 32)) return Path::kSplit;
+  return rows <= kFewRows ? Path::kFew : Path::kPrompt;
 }
-// Rows of a unit, for sequences of at most `rows` rows.
 int unit_rows(const pk_cache_desc &d, int64_t rows) {
-  return prompt_path(d, rows) ? kPromptRows : split_rows(int(std::min<int64_t>(rows, 64)));
+  switch (path_of(d, rows)) {
+    case Path::kFew: return kFewRows;
+    case Path::kPrompt: return kPromptRows;
+    default: return split_rows(int(std::min<int64_t>(rows, 64)));
+  }
 }
 
 template <typename T, int D>
@@ -64,8 +70,11 @@ pk_status run(ExtendParams p, const pk_cache_desc &d, cudaStream_t stream) {
   p.tiles = int32_t(tiles);
   const dim3 grid = dim3(unsigned(units));
   pk_status st;
-  if (prompt_path(d, rows)) {
+  const Path path = path_of(d, rows);
+  if (path == Path::kPrompt) {
     st = launch_prompt<D>(p, d, unsigned(units), stream);
+  } else if (path == Path::kFew) {
+    st = launch_few<D>(p, d, unsigned(units), stream);
   } else {
     switch (R) {
       case 8: st = launch_split<T, D, 1, ExtendView>(p, grid, stream); break;
@@ -111,29 +120,34 @@ void tiles_of(const int32_t *lens, const int32_t *query_lens, int32_t num_seqs, 
 
 // The partition size that the planner chooses (0: none). Units go longest first to
 // the CTA that is free first, so a launch lasts about as long as its longest unit or
-// as the mean share of a CTA, whichever is more; each unit costs some 128 tokens more
-// than its own, and each part of a row that is split d + 2 floats, written and read.
-int32_t choose_partition(const std::vector<Tile> &tiles, const pk_cache_desc &d) {
+// as the mean share of a CTA, whichever is more, plus what the last round leaves idle; a
+// unit costs `extra` tokens more than its own, each part of a row that is split d + 2
+// floats, written and read, and the merge a launch.
+int32_t choose_partition(const std::vector<Tile> &tiles, const pk_cache_desc &d, Path path) {
   int64_t longest = 0;
   for (const Tile &t : tiles) longest = std::max<int64_t>(longest, t.hi - t.lo);
   if (longest <= 1024) return 0;
-  const double slots = 2.0 * sm_count();
-  const double token = 22e-9;  // of a CTA
+  // CTAs at once, the time of a token of one, and a unit's own cost in tokens.
+  const double slots = double(sm_count()) * (path == Path::kPrompt ? 1 : (path == Path::kFew ? 3 : 2));
+  const double token = path == Path::kPrompt ? 10e-9 : (path == Path::kFew ? 35e-9 : 22e-9);
+  const double extra = path == Path::kPrompt ? 400 : 128;
   int32_t best = 0;
   double least = 0;
   for (int c = 1; c <= 32; ++c) {
     int64_t n = ((longest + c - 1) / c + 127) / 128 * 128;
     n = (n + d.block_size - 1) / d.block_size * d.block_size;
     if (c > 1 && n < 512) break;
-    double work = 0, partials = 0;
+    double work = 0, partials = 0, units = 0;
     for (const Tile &t : tiles) {
       const int64_t len = t.hi - t.lo, parts = c == 1 ? 1 : (t.hi - 1) / n - t.lo / n + 1;
-      work += double(len) + 128.0 * double(parts);
+      work += double(len) + extra * double(parts);
+      units += double(parts) * d.num_kv_heads;
       if (parts > 1) partials += double(parts) * t.rows;
     }
     const double merge = partials * d.num_kv_heads * (d.head_dim + 2) * 8 / 6e12 / token;
     const double cost = merge + (c > 1 ? 3e-6 / token : 0) +
-                        std::max(double(std::min(n, longest)), work * d.num_kv_heads / slots);
+                        std::max(double(std::min(n, longest)) + extra,
+                                 work * d.num_kv_heads / slots + 0.5 * work * d.num_kv_heads / units);
     if (c == 1 || cost < 0.97 * least) least = cost, best = c == 1 ? 0 : int32_t(n);
   }
   return best;
@@ -176,7 +190,7 @@ pk_status pk_extend_plan(const int32_t *context_lens, const int32_t *query_lens,
     std::vector<Tile> tiles;
     tiles_of(context_lens, query_lens, num_seqs, group, window, R, tiles);
     int32_t part = partition_size > 0 && partition_size < longest ? partition_size : 0;
-    if (partition_size == -1) part = choose_partition(tiles, *desc);
+    if (partition_size == -1) part = choose_partition(tiles, *desc, path_of(*desc, int64_t(max_query_len) * group));
     // Every partition that a row of the unit may see: a prefix lets it see all of the
     // context. Those of expected work first, longest first.
     std::vector<std::tuple<int64_t, int64_t, int32_t, int32_t>> order;  // -length, -context, tile, partition

@@ -13,10 +13,12 @@ namespace {
 
 constexpr int kPromptRows = 256;     // of a unit: two halves of 128, one lane of tensor memory each
 constexpr int kPromptTile = 128;     // tokens
-constexpr int kPromptThreads = 384;  // two warpgroups of softmax; the producer, products, units and queries
+// Two warpgroups of softmax; the producer, a half's products, units, the other half's
+// products; four warps that bring queries and look after values.
+constexpr int kPromptThreads = 512;
 constexpr int kPromptUnits = 4;      // units known at a time
-// 384 threads of 168 registers at launch: 2 x 216 + 72 = 3 x 168.
-constexpr int kPromptSoftmaxRegs = 216, kPromptOtherRegs = 72;
+// 512 threads of 128 registers at launch: 2 x 200 + 2 x 56 = 4 x 128.
+constexpr int kPromptSoftmaxRegs = 200, kPromptOtherRegs = 56;
 constexpr float kPromptSlack = 8.0f;  // log2 of how far a maximum may outgrow the reference
 
 template <int D>
@@ -25,16 +27,9 @@ struct PromptShape {
   static constexpr int SLAB = 128 * 128;                 // of 128 rows
   static constexpr int Q_HALF = SLABS * SLAB, TILE = SLABS * SLAB;
   static constexpr int STAGES = D == 128 ? 4 : 8;        // tiles of K and V in flight
-  static constexpr int OUT_BYTES = 2048;                 // per softmax warp: 64 bytes of each of its rows
+  static constexpr int OUT_BYTES = 4096;                 // per softmax warp: 128 bytes of each of its rows
   static constexpr int SMEM_BYTES = 1024 + 2 * Q_HALF + STAGES * TILE + 8 * OUT_BYTES;
 };
-
-// 1 / x, maximum error 1 ulp; 0 for infinity.
-__device__ __forceinline__ float reciprocal(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // tanh of two values times `k` / (2 log2(e)): 1 - 2 / (1 + 2^(k x)). The error is absolute,
 // 2^-21 or so, which is what a score that it is multiplied into needs.
@@ -45,18 +40,12 @@ __device__ __forceinline__ uint64_t tanh2(uint64_t x, uint64_t k) {
   b = reciprocal(1.0f + exp2_ftz(b));
   return fma2(pack2(a, b), pack2(-2.0f, -2.0f), pack2(1.0f, 1.0f));
 }
-// The same of f x where |f x| <= kTanhSmall: an odd polynomial of degree 9, the one of least
-// largest error (by linear programming over 2000 points), 2^-22 with its roundings. No
-// exponential and no reciprocal, whose unit the softmax's own exponentials keep busy.
+// For |y| <= kTanhSmall tanh(y) = y (c0 + c1 y^2 + .. + c4 y^8) to 2^-20.6 of itself: the
+// polynomial of least largest relative error, by linear programming over 2000 points. It needs
+// no exponential and no reciprocal, whose unit the softmax's own exponentials keep busy.
 constexpr float kTanhSmall = 0.75f;
-__device__ __forceinline__ uint64_t tanh2_small(uint64_t x, uint64_t f) {
-  const uint64_t y = mul2(x, f), z = mul2(y, y);
-  uint64_t r = fma2(z, pack2(0.012308921664953232f, 0.012308921664953232f), pack2(-0.049270521849393845f, -0.049270521849393845f));
-  r = fma2(r, z, pack2(0.13225862383842468f, 0.13225862383842468f));
-  r = fma2(r, z, pack2(-0.33323100209236145f, -0.33323100209236145f));
-  r = fma2(r, z, pack2(0.9999973177909851f, 0.9999973177909851f));
-  return mul2(r, y);
-}
+constexpr float kTanh0 = 0.999999463558197f, kTanh1 = -0.3332850933074951f, kTanh2 = 0.13261185586452484f,
+                kTanh3 = -0.05011745169758797f, kTanh4 = 0.012983138673007488f;
 
 // A unit of work: up to 256 rows of one (sequence, KV head) over one partition.
 struct PromptUnit {
@@ -83,44 +72,57 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = p.group;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t q_sm = (smem_addr(smem_raw) + 1023u) & ~1023u, kv_sm = q_sm + 2 * S::Q_HALF;
-  __shared__ __align__(8) uint64_t bars[2 * ST + 2 * kPromptUnits + 11];
+  constexpr int NB = 3 * ST + 2 * kPromptUnits;
+  __shared__ __align__(8) uint64_t bars[NB + 16];
   __shared__ uint4 answer;
   __shared__ PromptUnit units[kPromptUnits];
   __shared__ uint32_t tmem_slot;
   // The unit, plus one, whose values were not all finite where some rows do not see them.
-  // Nothing is cleared: a unit's mark is written by its own softmax warps and read before
-  // they give its entry back, which comes before the next unit of the same word.
+  // Nothing is cleared: a unit's mark is written before its products and read before its
+  // softmax warps give its entry back, which comes before the next unit of the same word.
   __shared__ int poisoned[kPromptUnits];
-  // Units i, tiles of K and V k, tiles of a half, careful tiles and so on are counted over
-  // the life of the CTA; a barrier's phase is the count of what uses it. Every wait names a
-  // phase of which the one before has ended for certain and the one after cannot have: a
-  // wait by parity tells neighbouring phases apart, not more.
+  // Units i, tiles of K and V k, tiles and units of a half are counted over the life of the
+  // CTA; a barrier's phase is the count of what uses it. Every wait names a phase of which the
+  // one before has ended for certain and the one after cannot have: a wait by parity tells
+  // neighbouring phases apart, not more.
   auto bar = [&](int i) { return smem_addr(bars + i); };
-  auto kv_full = [&](int k) { return bar(k % ST); };
-  auto kv_empty = [&](int k) { return bar(ST + k % ST); };
+  auto kv_full = [&](int k) { return bar(k % ST); };           // the copy has landed
+  auto v_ready = [&](int k) { return bar(ST + k % ST); };      // and its values are fit for the product
+  auto kv_empty = [&](int k) { return bar(2 * ST + k % ST); };
   auto kv_phase = [](int k) { return uint32_t(k / ST) & 1u; };
-  auto u_full = [&](int i) { return bar(2 * ST + i % kPromptUnits); };
-  auto u_empty = [&](int i) { return bar(2 * ST + kPromptUnits + i % kPromptUnits); };
+  auto u_full = [&](int i) { return bar(3 * ST + i % kPromptUnits); };
+  auto u_empty = [&](int i) { return bar(3 * ST + kPromptUnits + i % kPromptUnits); };
   auto u_phase = [](int i) { return uint32_t(i / kPromptUnits) & 1u; };
-  constexpr int B0 = 2 * ST + 2 * kPromptUnits;
-  const uint32_t q_full = bar(B0), q_empty = bar(B0 + 1), v_clean = bar(B0 + 2), u_want = bar(B0 + 3),
-                 u_answer = bar(B0 + 4);
-  auto s_full = [&](int h) { return bar(B0 + 5 + h); };  // of a half, by tile
-  auto p_full = [&](int h) { return bar(B0 + 7 + h); };
-  auto o_done = [&](int h) { return bar(B0 + 9 + h); };  // of a half, by unit
+  auto q_full = [&](int h) { return bar(NB + h); };       // of a half, by unit
+  auto q_empty = [&](int h) { return bar(NB + 2 + h); };
+  auto o_done = [&](int h) { return bar(NB + 4 + h); };
+  auto s_full = [&](int h) { return bar(NB + 6 + h); };   // of a half, by tile
+  auto p_full = [&](int h) { return bar(NB + 8 + h); };
+  auto turn = [&](int h) { return bar(NB + 10 + h); };    // the other half's products are issued
+  auto drained = [&](int h) { return bar(NB + 12 + h); };
+  const uint32_t u_want = bar(NB + 14), u_answer = bar(NB + 15);
   if (tid == 0) {
-    for (int i = 0; i < ST; ++i) mbar_init(kv_full(i), 1), mbar_init(kv_empty(i), 1);
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(kv_full(i), 1);
+      mbar_init(v_ready(i), 4);
+      mbar_init(kv_empty(i), 2);
+    }
     for (int i = 0; i < kPromptUnits; ++i) {
       mbar_init(u_full(i), 1);
-      mbar_init(u_empty(i), 11);  // every warp but the one that fills them
+      mbar_init(u_empty(i), 15);  // every warp but the one that fills them
       poisoned[i] = 0;
     }
-    mbar_init(q_full, 32);
-    mbar_init(q_empty, 1);
-    mbar_init(v_clean, 8);
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(q_full(h), 128);
+      mbar_init(q_empty(h), 1);
+      mbar_init(o_done(h), 1);
+      mbar_init(s_full(h), 1);
+      mbar_init(p_full(h), 4);
+      mbar_init(turn(h), 1);
+      mbar_init(drained(h), 1);
+    }
     mbar_init(u_want, 1);
     mbar_init(u_answer, 1);
-    for (int h = 0; h < 2; ++h) mbar_init(s_full(h), 1), mbar_init(p_full(h), 4), mbar_init(o_done(h), 1);
     fence_barrier_init();
   }
   if (warp == 9) tmem_alloc(smem_addr(&tmem_slot), 512);
@@ -193,74 +195,81 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (!ok && lane == 0) timeout();
       // Let every issued copy land before the warp leaves.
       for (int x = max(0, k - ST); x < k; ++x) mbar_wait(kv_full(x), kv_phase(x));
-    } else if (warp == 9) {
-      // ---------------- products ----------------
-      // S of both halves, then in turn a half's O += P V and its next S: while one half's
-      // softmax runs, the tensor cores have the other's products.
+    } else if (warp == 9 || warp == 11) {
+      // ---------------- products of a half ----------------
+      // S of the first tile, then in turn O += P V and the next tile's S: while one half's
+      // softmax runs, the tensor cores have the other's products. A warp for each, as a wait
+      // costs some 200 cycles even where its phase has ended, and in one warp the waits and
+      // issues of both took longer than the products (3550 cycles a tile). The two take turns:
+      // products of both that are issued together end together, and then both halves are in
+      // their softmax at once and the tensor cores idle (3400 cycles; now 3200). Heads of 64 have
+      // half the products, and turns only hold them up (1140 us for 1030).
+      constexpr bool TURNS = D == 128;
       constexpr uint32_t O_DESC = mma_desc(128, D, true);
       const uint32_t s_desc = mma_desc(128, kPromptTile, false) | (p.factor < 0.0f ? 1u << 13 : 0u);  // -Q
+      const int h = (warp - 9) / 2;
+      const uint64_t q_d = smem_desc(q_sm + h * S::Q_HALF, 16, 1024);
       bool ok = true;
-      int k0 = 0, c = 0, n[2] = {0, 0}, done[2] = {0, 0};  // tiles before the unit, careful ones, of a half, its units
+      int k0 = 0, n = 0, done = 0, m = 0;  // tiles of K and V before the unit, tiles of the half, its units, turns
       for (int i = 0; warp_wait(u_full(i), u_phase(i), ok); ++i) {
-        const PromptUnit unit = units[i % kPromptUnits];
-        const int nt = unit.nt, halves = unit.halves();
+        const PromptUnit &unit = units[i % kPromptUnits];
+        const int s = unit.s, nt = unit.nt, halves = unit.halves();
         release(i);
-        if (unit.s < 0) break;
-        auto scores = [&](int h, int j) {
+        if (s < 0) break;
+        if (h >= halves) {  // the other half has it alone
+          k0 += 2 * nt;
+          continue;
+        }
+        auto my_turn = [&] { return !TURNS || halves == 1 || (h == 0 && m == 0) || warp_wait(turn(h), (m - (h == 0)) & 1, ok); };
+        // O += P V of tile j and S of the next (j < 0: only that).
+        auto products = [&](int j) {
           if (elect_one()) {
-            const uint64_t a = smem_desc(q_sm + h * S::Q_HALF, 16, 1024);
-            const uint64_t b = smem_desc(kv_sm + (k0 + 2 * j) % ST * S::TILE, 16, 1024);
+            if (j >= 0) {
+              const int k = k0 + 2 * j + 1;
+              const uint64_t b = smem_desc(kv_sm + k % ST * S::TILE, S::SLAB, 1024);
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)  // a descriptor's address counts 16 bytes
-              tc_mma_ss(t_s(h), a + (ks / 4) * (S::SLAB / 16) + (ks % 4) * 2,
-                        b + (ks / 4) * (S::SLAB / 16) + (ks % 4) * 2, s_desc, ks > 0);
-            tc_commit(s_full(h));
-            if (h + 1 == halves) {
-              tc_commit(kv_empty(k0 + 2 * j));
-              if (j + 1 == nt) tc_commit(q_empty);
-            }
-          }
-          __syncwarp();
-        };
-        if (!warp_wait(q_full, i & 1, ok) || !warp_wait(kv_full(k0), kv_phase(k0), ok)) break;
-        tc_fence_after();
-        for (int h = 0; h < halves; ++h) scores(h, 0);
-        for (int j = 0; ok && j < nt; ++j) {
-          const int iv = k0 + 2 * j + 1, ik = iv + 1;
-          if (!warp_wait(kv_full(iv), kv_phase(iv), ok)) break;
-          if (unit.careful(j) && !warp_wait(v_clean, c++ & 1, ok)) break;
-          for (int h = 0; h < halves; ++h) {
-            if (!warp_wait(p_full(h), n[h]++ & 1, ok)) break;
-            tc_fence_after();
-            if (elect_one()) {
-              const uint64_t b = smem_desc(kv_sm + iv % ST * S::TILE, S::SLAB, 1024);
-#pragma unroll
-              for (int ks = 0; ks < kPromptTile / 16; ++ks)
+              for (int ks = 0; ks < kPromptTile / 16; ++ks)  // a descriptor's address counts 16 bytes
                 tc_mma_ts(t_o(h), t_s(h) + 8 * ks, b + ks * 128, O_DESC, j > 0 || ks > 0);
-              if (h + 1 == halves) tc_commit(kv_empty(iv));
+              tc_commit(kv_empty(k));
+              if (halves == 1) tc_commit(kv_empty(k));  // for the other half
               if (j + 1 == nt) tc_commit(o_done(h));
             }
-            __syncwarp();
             if (j + 1 < nt) {
-              if (h == 0 && !warp_wait(kv_full(ik), kv_phase(ik), ok)) break;
-              scores(h, j + 1);
+              const int k = k0 + 2 * j + 2;
+              const uint64_t b = smem_desc(kv_sm + k % ST * S::TILE, 16, 1024);
+#pragma unroll
+              for (int ks = 0; ks < D / 16; ++ks)
+                tc_mma_ss(t_s(h), q_d + (ks / 4) * (S::SLAB / 16) + (ks % 4) * 2,
+                          b + (ks / 4) * (S::SLAB / 16) + (ks % 4) * 2, s_desc, ks > 0);
+              tc_commit(s_full(h));
+              tc_commit(kv_empty(k));
+              if (halves == 1) tc_commit(kv_empty(k));
+              if (j + 2 == nt) tc_commit(q_empty(h));
             }
+            if (TURNS && halves == 2) mbar_arrive(turn(1 - h));
           }
+          __syncwarp();
+          m += halves == 2;
+        };
+        if (!warp_wait(q_full(h), done++ & 1, ok) || !warp_wait(kv_full(k0), kv_phase(k0), ok) || !my_turn()) break;
+        tc_fence_after();
+        products(-1);
+        for (int j = 0; j < nt; ++j, ++n) {
+          const int iv = k0 + 2 * j + 1, ik = iv + 1;
+          if (!warp_wait(v_ready(iv), kv_phase(iv), ok) || (j + 1 < nt && !warp_wait(kv_full(ik), kv_phase(ik), ok)) ||
+              !warp_wait(p_full(h), n & 1, ok) || !my_turn())
+            break;
+          tc_fence_after();
+          products(j);
         }
         if (!ok) break;
         k0 += 2 * nt;
-        for (int h = 0; h < halves; ++h) ++done[h];
       }
       if (!ok && lane == 0) timeout();
       // Nothing of this warp's products is under way when tensor memory is freed.
-      if (!ok) {
-        if (elect_one()) tc_commit(q_empty);
-        __syncwarp();
-        mbar_wait(q_empty, 0, 1u << 10);
-        mbar_wait(q_empty, 1, 1u << 10);
-      }
-      for (int h = 0; h < 2; ++h)
-        if (done[h] > 0) mbar_wait(o_done(h), (done[h] - 1) & 1);
+      if (elect_one()) tc_commit(drained(h));
+      __syncwarp();
+      mbar_wait(drained(h), 0);
       __syncwarp();
     } else if (warp == 10) {
       // ---------------- units ----------------
@@ -320,30 +329,90 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (ok) publish(end);
       if (!ok && lane == 0) timeout();
     } else {
-      // ---------------- queries ----------------
+      // ---------------- queries and values ----------------
+      // These warps bring a half's queries once the scores of the unit before are done with the
+      // last ones, and look at each tile of values that has landed: rows past the end are
+      // zeroed, and so is what is not finite in values that some rows do not see, which would
+      // reach those too (0 * NaN); the rows that do see it get it at the end. A half's queries
+      // are there when all four warps are past the unit before, so that no wait for values
+      // can be a phase early.
+      const int w = warp - 12;
+      constexpr int CH = D / 8;  // chunks of a row
+      const uint32_t inv_g = (65536 + G - 1) / G;  // x / G = x inv_g >> 16 for x < 512
       bool ok = true;
+      int k0 = 0, done[2] = {0, 0};
       for (int i = 0; warp_wait(u_full(i), u_phase(i), ok); ++i) {
         const PromptUnit &c = units[i % kPromptUnits];
-        const int s = c.s, kvh = c.kvh, r0 = c.r0, rows = c.rows;
-        const SeqRows sr = c.sr;
-        release(i);
-        if (s < 0 || (i > 0 && !warp_wait(q_empty, (i - 1) & 1, ok))) break;
-        // Rows past the last keep what is there: no row's result depends on another's query.
-        constexpr int CH = D / 8, STEP = 32 / CH;  // chunks of a row, rows at once
-        const int ch = lane % CH;
-        int tok = (r0 + lane / CH) / G, g = (r0 + lane / CH) % G;
-        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) +
-                                   (size_t(sr.q0) * p.num_q_heads + kvh * G) * D + ch * 8;
-        const uint32_t dst = q_sm + (ch >> 3) * S::SLAB;
+        if (c.s < 0) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h >= c.halves() || (done[h] > 0 && !warp_wait(q_empty(h), (done[h] - 1) & 1, ok))) break;
+          ++done[h];
+          // Rows past the last keep what is there: no row's result depends on another's query.
+          constexpr int STEP = 128 / CH;  // rows at once
+          const int t = tid & 127, ch = t % CH, tok0 = c.r0 / G, rows = min(128, c.rows - 128 * h);
+          const uint32_t x0 = c.r0 % G + 128 * h;
+          const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) +
+                                     (size_t(c.sr.q0 + tok0) * p.num_q_heads + c.kvh * G) * D + ch * 8;
+          const uint32_t dst = q_sm + h * S::Q_HALF + (ch >> 3) * S::SLAB;
 #pragma unroll 4
-        for (int row = lane / CH; row < rows; row += STEP) {
-          cp_async16(dst + (row >> 7) * S::Q_HALF + (row & 127) * 128 + (((ch & 7) ^ (row & 7)) << 4),
-                     src + (size_t(tok) * p.num_q_heads + g) * D, 16);
-          for (g += STEP; g >= G; g -= G) ++tok;
+          for (int row = t / CH; row < rows; row += STEP) {
+            const uint32_t x = x0 + row, tok = x * inv_g >> 16;
+            cp_async16(dst + row * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                       src + (size_t(tok) * (p.num_q_heads - G) + x) * D, 16);
+          }
+          cp_async_wait();
+          fence_proxy_async_shared();
+          mbar_arrive(q_full(h));
         }
-        cp_async_wait();
-        fence_proxy_async_shared();
-        mbar_arrive(q_full);
+        const int nt = c.nt;
+        for (int j = 0; ok && j < nt; ++j) {
+          const int iv = k0 + 2 * j + 1;
+          if (!warp_wait(kv_full(iv), kv_phase(iv), ok)) break;
+          if (c.careful(j)) {
+            const int t0 = c.start + j * kPromptTile, valid = min(kPromptTile, c.end - t0);
+            const int all_from = c.all_from - t0, all_to = c.all_to - t0;
+            const int ch = lane % CH;
+            const uint32_t at = kv_sm + iv % ST * S::TILE + (ch >> 3) * S::SLAB + (ch & 7) * 16;
+            bool wrote = false;
+            constexpr int STEP = 32 / CH, U = 4;  // rows at once, and loads under way
+#pragma unroll 1
+            for (int k0 = 32 * w + lane / CH; k0 < 32 * w + 32; k0 += U * STEP) {
+              uint32_t v[U][4];
+#pragma unroll
+              for (int u = 0; u < U; ++u)
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v[u][0]), "=r"(v[u][1]), "=r"(v[u][2]), "=r"(v[u][3])
+                             : "r"(at + (k0 + u * STEP) * 128));
+#pragma unroll
+              for (int u = 0; u < U; ++u) {
+                const int k = k0 + u * STEP;
+                if (k >= all_from && k < all_to) continue;
+                // A carry into a half's sign shows an exponent of all ones.
+                uint32_t odd = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) odd |= (v[u][e] & 0x7f807f80u) + 0x00800080u;
+                if (k < valid && !(odd & 0x80008000u)) continue;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if (k >= valid || (v[u][e] & 0x7f80u) == 0x7f80u) v[u][e] &= 0xffff0000u;
+                  if (k >= valid || (v[u][e] & 0x7f800000u) == 0x7f800000u) v[u][e] &= 0xffffu;
+                }
+                if (k < valid) poisoned[i % kPromptUnits] = i + 1;
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + k * 128), "r"(v[u][0]),
+                             "r"(v[u][1]), "r"(v[u][2]), "r"(v[u][3])
+                             : "memory");
+                wrote = true;
+              }
+            }
+            if (__any_sync(0xffffffffu, wrote)) fence_proxy_async_shared();
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive(v_ready(iv));
+        }
+        if (!ok) break;
+        k0 += 2 * nt;
+        release(i);
       }
       if (!ok && lane == 0) timeout();
     }
@@ -356,14 +425,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // turn the -inf of what is masked into NaN.
     const float fac = fmaxf(fabsf(p.factor), 1.17549435e-38f);
     const float sl = SLOPES ? 1.0f : (CAP ? p.cap_log2 : fac);
+    // The polynomial of a product, in the exponent's scale.
+    const float f1 = p.cap_log2 * fac, ff = fac * fac;
+    const float tc[5] = {kTanh0 * f1, kTanh1 * f1 * ff, kTanh2 * f1 * ff * ff, kTanh3 * f1 * ff * ff * ff,
+                         kTanh4 * f1 * ff * ff * ff * ff};
     bool ok = true;
-    int k0 = 0, n = 0, done = 0;  // tiles of K and V before the unit, the half's tiles and units
+    int n = 0, done = 0;  // the half's tiles and units
     for (int i = 0; warp_wait(u_full(i), u_phase(i), ok); ++i) {
       const PromptUnit &unit = units[i % kPromptUnits];
       if (unit.s < 0) break;
       const int nt = unit.nt, start = unit.start, end = unit.end, halves = unit.halves(), rows = unit.rows;
       if (h >= halves) {  // the other half has it alone
-        k0 += 2 * nt;
         release(i);
         continue;
       }
@@ -381,53 +453,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         uint32_t s[4][32];
         if (!warp_wait(s_full(h), n & 1, ok)) break;
         tc_fence_after();
-        if (busy)
+        if (busy) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) tmem_load32(t_s(h) + lane_base + 32 * e, s[e]);
-        if (careful) {
-          // Values past the end are zeroed, and so is what is not finite in values that some
-          // rows do not see, which would reach those too (0 * NaN); the rows that do see it
-          // get it at the end. The warpgroups share the tokens.
-          const int iv = k0 + 2 * j + 1, valid = min(kPromptTile, end - t0);
-          const int all_from = unit.all_from, all_to = unit.all_to;
-          if (!warp_wait(kv_full(iv), kv_phase(iv), ok)) break;
-          constexpr int CH = D / 8, STEP = 128 / CH;
-          const int r = tid & 127, ch = r % CH;
-          const uint32_t at = kv_sm + iv % ST * S::TILE + (ch >> 3) * S::SLAB + (ch & 7) * 16;
-          bool wrote = false;
-#pragma unroll 4
-          for (int k = h * 64 + r / CH; k < (h + 1 == halves ? kPromptTile : 64); k += STEP) {
-            const int t = t0 + k;
-            if (t >= all_from && t < all_to) continue;
-            uint32_t w[4];
-            const uint32_t a = at + k * 128;
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(a));
-            // A carry into a half's sign shows an exponent of all ones.
-            uint32_t odd = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) odd |= (w[e] & 0x7f807f80u) + 0x00800080u;
-            if (k < valid && !(odd & 0x80008000u)) continue;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (k >= valid || (w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
-              if (k >= valid || (w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu;
-            }
-            if (k < valid) poisoned[i % kPromptUnits] = i + 1;
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                         "r"(w[3])
-                         : "memory");
-            wrote = true;
-          }
-          if (__any_sync(0xffffffffu, wrote)) fence_proxy_async_shared();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(v_clean);
-            if (halves == 1) mbar_arrive(v_clean);  // for the other half's warp
-          }
-        }
-        if (busy) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) tmem_wait_load(s[e]);
           auto pair = [&](int i) {
@@ -446,18 +474,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                                 of(__uint_as_float(s[i / 16][2 * (i % 16) + 1])));
             return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
           };
+          // Small scores are capped by the polynomial, together with the subtraction of the
+          // maximum where no bias comes between; others by exponentials, in place.
+          bool poly = false;
           if (CAP) {
-            const bool small = largest([](float v) { return fabsf(v); }) * fac <= kTanhSmall;
-            if (__all_sync(0xffffffffu, small)) {
-              const uint64_t f2 = pack2(fac, fac);
-#pragma unroll
-              for (int i = 0; i < 64; ++i) set_pair(i, tanh2_small(pair(i), f2));
-            } else {
+            poly = __all_sync(0xffffffffu, largest([](float v) { return fabsf(v); }) * fac <= kTanhSmall);
+            if (!poly) {
               const uint64_t k2 = pack2(2.0f * 1.44269504f * fac, 2.0f * 1.44269504f * fac);
 #pragma unroll
               for (int i = 0; i < 64; ++i) set_pair(i, tanh2(pair(i), k2));
             }
           }
+          auto capped = [&](int i) {  // the polynomial's sum without the last factor
+            const uint64_t x = pair(i), z = mul2(x, x);
+            uint64_t r = fma2(z, pack2(tc[4], tc[4]), pack2(tc[3], tc[3]));
+            r = fma2(r, z, pack2(tc[2], tc[2]));
+            r = fma2(r, z, pack2(tc[1], tc[1]));
+            return fma2(r, z, pack2(tc[0], tc[0]));
+          };
           if (SLOPES) {
             const float d0 = float(t0 - x.pos), f = CAP ? p.cap_log2 : fac;
             const uint64_t f2 = pack2(f, f), m2 = pack2(-slope, -slope);
@@ -465,8 +499,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             for (int i = 0; i < 64; ++i) {
               const uint64_t away =
                   add2(pack2(d0, d0), pack2(float(2 * i), float(2 * i + 1))) & 0x7fffffff7fffffffull;
-              set_pair(i, fma2(away, m2, mul2(pair(i), f2)));
+              set_pair(i, fma2(away, m2, CAP && poly ? mul2(capped(i), pair(i)) : mul2(pair(i), f2)));
             }
+          }
+          float sl_now = sl;
+          if (CAP && !SLOPES && poly && careful) {  // ahead of the mask, whose -inf is no factor of a polynomial
+#pragma unroll
+            for (int i = 0; i < 64; ++i) set_pair(i, mul2(capped(i), pair(i)));
+            sl_now = 1.0f;
+            poly = false;
           }
           if (careful) {
             const int lo = max(0, x.lo - t0), hi = min(x.hi, end) - t0;
@@ -480,7 +521,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
           }
           float mx = largest([](float v) { return v; });
-          mx = mx == -INFINITY ? mx : mx * sl;
+          if (CAP && !SLOPES && poly) {
+            const float z = mx * mx;
+            mx = mx == -INFINITY ? mx : mx * fmaf(fmaf(fmaf(fmaf(tc[4], z, tc[3]), z, tc[2]), z, tc[1]), z, tc[0]);
+          } else {
+            mx = mx == -INFINITY ? mx : mx * sl_now;
+          }
           const bool move = mx > ref + kPromptSlack;
           if (__any_sync(0xffffffffu, move)) {
             const float f = move ? exp2_ftz(ref - mx) : 1.0f;
@@ -505,23 +551,30 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
           }
           const float m = ref == -INFINITY ? 0.0f : ref;  // nothing seen so far: every weight is 0
-          const uint64_t sl2 = pack2(sl, sl), m2 = pack2(-m, -m);
+          const uint64_t sl2 = pack2(sl_now, sl_now), m2 = pack2(-m, -m);
           uint64_t sum2[2] = {0, 0};
+          auto weights = [&](auto of) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t w[16];
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float a, b;
-              unpack2(fma2(pair(16 * e + k), sl2, m2), a, b);
-              // The weights enter the product as one bf16 each and are summed as they enter,
-              // so that a row's weights add up to 1: an average of values, each weight off by
-              // 2^-8 at most. A second half of each would cost half as many products again.
-              w[k] = pack_bf16x2(exp2_ftz(a), exp2_ftz(b));
-              sum2[k & 1] = add2(sum2[k & 1], pack2(bf16_lo(w[k]), bf16_hi(w[k])));
+              for (int k = 0; k < 16; ++k) {
+                float a, b;
+                unpack2(of(16 * e + k), a, b);
+                // The weights enter the product as one bf16 each: an average of values, each weight
+                // off by 2^-8 at most. A second half of each would cost half as many products
+                // again; to sum them as they enter, two more operations a weight (1494 us for 1413).
+                a = exp2_ftz(a), b = exp2_ftz(b);
+                w[k] = pack_bf16x2(a, b);
+                sum2[k & 1] = add2(sum2[k & 1], pack2(a, b));
+              }
+              tmem_store16(t_s(h) + lane_base + 16 * e, w);
             }
-            tmem_store16(t_s(h) + lane_base + 16 * e, w);
-          }
+          };
+          if (CAP && !SLOPES && poly)
+            weights([&](int i) { return fma2(capped(i), pair(i), m2); });
+          else
+            weights([&](int i) { return fma2(pair(i), sl2, m2); });
           {
             float a, b;
             unpack2(add2(sum2[0], sum2[1]), a, b);
@@ -533,8 +586,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full(h));
       }
-      k0 += 2 * nt;
-      // (The products came after every warp had cleared its values, so the marks are in.)
+      // (The products came after the values were looked at, so the marks are in.)
       if (!ok || !warp_wait(o_done(h), done++ & 1, ok)) break;
       if (!busy) {
         release(i);
@@ -545,26 +597,30 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const Place place = mine ? row_place(p, x.lo, x.hi, unit.part) : Place::kNowhere;
       const float inv = 1.0f / denominator(l, false);
       const size_t at = mine ? q_row(unit.sr, unit.kvh, unit.r0 + tid) : 0, slot = at / D * p.num_partitions + unit.part;
-      // A lane has a row, but rows are 64 bytes or more apart in memory: 64 bytes of each go
-      // through shared memory, so that four lanes write a row's together.
+      // A lane has a row, but rows are 128 bytes or more apart in memory: 128 bytes of each go
+      // through shared memory, so that eight lanes write a row's together (written by its own
+      // lane, 32 bytes at a time, a unit's rows took 4600 cycles).
       const uint32_t stage = kv_sm + ST * S::TILE + warp * S::OUT_BYTES;
-      auto put = [&](const uint32_t (&w)[16], char *row) {  // row: where the lane's goes, or null
+      auto put = [&](const uint32_t (&w)[32], char *row) {  // row: where the lane's goes, or null
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 64 +
-                                                                       ((e ^ ((lane >> 1) & 3)) << 4)),
+        for (int e = 0; e < 8; ++e)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + ((e ^ (lane & 7)) << 4)),
                        "r"(w[4 * e]), "r"(w[4 * e + 1]), "r"(w[4 * e + 2]), "r"(w[4 * e + 3])
                        : "memory");
         __syncwarp();
+        uint4 v[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = 8 * e + lane / 4;
-          uint4 v;
+        for (int e = 0; e < 8; ++e) {
+          const int r = 4 * e + lane / 8;
           asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                       : "r"(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4)));
-          char *dst = reinterpret_cast<char *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), r));
-          if (dst) *reinterpret_cast<uint4 *>(dst + (lane & 3) * 16) = v;
+                       : "=r"(v[e].x), "=r"(v[e].y), "=r"(v[e].z), "=r"(v[e].w)
+                       : "r"(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4)));
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          char *dst = reinterpret_cast<char *>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), 4 * e + lane / 8));
+          if (dst) *reinterpret_cast<uint4 *>(dst + (lane & 7) * 16) = v[e];
         }
         __syncwarp();
       };
@@ -572,23 +628,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       char *const acc = place == Place::kWorkspace ? reinterpret_cast<char *>(p.ws_acc + slot * D) : nullptr;
       const bool some_out = __any_sync(0xffffffffu, res != nullptr), some_acc = __any_sync(0xffffffffu, acc != nullptr);
 #pragma unroll 1
-      for (int ch = 0; ch < D / 32; ++ch) {
-        uint32_t o[32], w[16];
-        tmem_load32(t_o(h) + lane_base + 32 * ch, o);
-        tmem_wait_load(o);
+      for (int ch = 0; ch < D / 64; ++ch) {
+        uint32_t o[2][32];
+        tmem_load32(t_o(h) + lane_base + 64 * ch, o[0]);
+        tmem_load32(t_o(h) + lane_base + 64 * ch + 32, o[1]);
+        tmem_wait_load(o[0]);
+        tmem_wait_load(o[1]);
         if (some_out) {
+          uint32_t w[32];
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            w[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-          put(w, res ? res + 64 * ch : nullptr);
+          for (int e = 0; e < 32; ++e)
+            w[e] = pack_bf16x2(__uint_as_float(o[e / 16][2 * (e % 16)]) * inv,
+                               __uint_as_float(o[e / 16][2 * (e % 16) + 1]) * inv);
+          put(w, res ? res + 128 * ch : nullptr);
         }
         if (some_acc) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = o[16 * half + e];
-            put(w, acc ? acc + 128 * ch + 64 * half : nullptr);
-          }
+          put(o[0], acc ? acc + 256 * ch : nullptr);
+          put(o[1], acc ? acc + 256 * ch + 128 : nullptr);
         }
       }
       if (acc) {

@@ -289,6 +289,13 @@ __device__ __forceinline__ float exp2_ftz(float x) {
   return y;
 }
 
+// 1 / x, maximum error 1 ulp; 0 for infinity.
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Pairs of fp32 values in one 64-bit register: a * b + c and a + b, each of
 // both halves, in one instruction.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
