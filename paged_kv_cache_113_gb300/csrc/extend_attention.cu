@@ -118,37 +118,52 @@ void tiles_of(const int32_t *lens, const int32_t *query_lens, int32_t num_seqs, 
   }
 }
 
-// The partition size that the planner chooses (0: none). Units go longest first to
-// the CTA that is free first, so a launch lasts about as long as its longest unit or
-// as the mean share of a CTA, whichever is more, plus what the last round leaves idle; a
-// unit costs `extra` tokens more than its own, each part of a row that is split d + 2
-// floats, written and read, and the merge a launch.
+// The partition size that the planner chooses (0: none). Units go longest first to the CTA
+// that is free first, so a launch lasts about as long as its longest unit or as the mean
+// share of a CTA with what the last round leaves idle (of the shortest units' length),
+// whichever is more; a unit costs `extra` tokens more than its own, each part of a row that
+// is split d + 2 floats, written and read, and the merge a launch.
 int32_t choose_partition(const std::vector<Tile> &tiles, const pk_cache_desc &d, Path path) {
   int64_t longest = 0;
   for (const Tile &t : tiles) longest = std::max<int64_t>(longest, t.hi - t.lo);
   if (longest <= 1024) return 0;
   // CTAs at once, the time of a token of one, and a unit's own cost in tokens.
-  const double slots = double(sm_count()) * (path == Path::kPrompt ? 1 : (path == Path::kFew ? 3 : 2));
+  const int64_t slots = int64_t(sm_count()) * (path == Path::kPrompt ? 1 : (path == Path::kFew ? 3 : 2));
   const double token = path == Path::kPrompt ? 10e-9 : (path == Path::kFew ? 35e-9 : 22e-9);
   const double extra = path == Path::kPrompt ? 400 : 128;
+  constexpr int64_t kBin = 128;
+  std::vector<int64_t> count;  // parts by length
   int32_t best = 0;
   double least = 0;
   for (int c = 1; c <= 32; ++c) {
-    int64_t n = ((longest + c - 1) / c + 127) / 128 * 128;
+    int64_t n = ((longest + c - 1) / c + kBin - 1) / kBin * kBin;
     n = (n + d.block_size - 1) / d.block_size * d.block_size;
     if (c > 1 && n < 512) break;
-    double work = 0, partials = 0, units = 0;
+    count.assign(size_t(std::max(n, longest) / kBin + 2), 0);
+    double work = 0, partials = 0;
+    int64_t units = 0, most = 0;
     for (const Tile &t : tiles) {
-      const int64_t len = t.hi - t.lo, parts = c == 1 ? 1 : (t.hi - 1) / n - t.lo / n + 1;
-      work += double(len) + extra * double(parts);
-      units += double(parts) * d.num_kv_heads;
-      if (parts > 1) partials += double(parts) * t.rows;
+      const int64_t first = c == 1 ? 0 : t.lo / n, last = c == 1 ? 0 : (t.hi - 1) / n;
+      for (int64_t q = first; q <= last; ++q) {
+        const int64_t len = c == 1 ? t.hi - t.lo
+                                   : std::min<int64_t>(t.hi, (q + 1) * n) - std::max<int64_t>(t.lo, q * n);
+        ++count[size_t((len + kBin - 1) / kBin)];
+        work += double(len) + extra;
+        most = std::max(most, len);
+      }
+      units += last - first + 1;
+      if (last > first) partials += double(last - first + 1) * t.rows;
     }
+    units *= d.num_kv_heads;
+    work *= d.num_kv_heads;
+    int64_t tail = 0;  // the longest of the last `slots` units
+    for (int64_t left = std::min(units, slots); left > 0 && tail + 1 < int64_t(count.size()); ++tail)
+      left -= count[size_t(tail)] * d.num_kv_heads;
+    const double idle = double((slots - units % slots) % slots) / double(slots) * (double(tail * kBin) + extra);
     const double merge = partials * d.num_kv_heads * (d.head_dim + 2) * 8 / 6e12 / token;
-    const double cost = merge + (c > 1 ? 3e-6 / token : 0) +
-                        std::max(double(std::min(n, longest)) + extra,
-                                 work * d.num_kv_heads / slots + 0.5 * work * d.num_kv_heads / units);
-    if (c == 1 || cost < 0.97 * least) least = cost, best = c == 1 ? 0 : int32_t(n);
+    const double cost = merge + (c > 1 ? 5e-6 / token : 0) +
+                        std::max(double(most) + extra, work / double(slots) + idle);
+    if (c == 1 || cost < (best ? 0.97 : 0.92) * least) least = cost, best = c == 1 ? 0 : int32_t(n);
   }
   return best;
 }
