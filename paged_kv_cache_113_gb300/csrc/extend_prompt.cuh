@@ -40,12 +40,15 @@ __device__ __forceinline__ uint64_t tanh2(uint64_t x, uint64_t k) {
   b = reciprocal(1.0f + exp2_ftz(b));
   return fma2(pack2(a, b), pack2(-2.0f, -2.0f), pack2(1.0f, 1.0f));
 }
-// For |y| <= kTanhSmall tanh(y) = y (c0 + c1 y^2 + .. + c4 y^8) to 2^-20.6 of itself: the
-// polynomial of least largest relative error, by linear programming over 2000 points. It needs
-// no exponential and no reciprocal, whose unit the softmax's own exponentials keep busy.
+// For |y| <= kTanhSmall tanh(y) = y (c0 + c1 y^2 + .. + c4 y^8) to 2^-20.6 of itself, for |y| <=
+// kTanhTiny y (t0 + t1 y^2 + t2 y^4) to 2^-17.3: the polynomials of least largest relative error,
+// by linear programming over 2000 points. They need no exponential and no reciprocal, whose unit
+// the softmax's own exponentials keep busy.
 constexpr float kTanhSmall = 0.75f;
 constexpr float kTanh0 = 0.999999463558197f, kTanh1 = -0.3332850933074951f, kTanh2 = 0.13261185586452484f,
                 kTanh3 = -0.05011745169758797f, kTanh4 = 0.012983138673007488f;
+constexpr float kTanhTiny = 0.4f;
+constexpr float kTiny0 = 0.9999939203262329f, kTiny1 = -0.3326335847377777f, kTiny2 = 0.12132595479488373f;
 
 // A unit of work: up to 256 rows of one (sequence, KV head) over one partition.
 struct PromptUnit {
@@ -429,6 +432,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const float f1 = p.cap_log2 * fac, ff = fac * fac;
     const float tc[5] = {kTanh0 * f1, kTanh1 * f1 * ff, kTanh2 * f1 * ff * ff, kTanh3 * f1 * ff * ff * ff,
                          kTanh4 * f1 * ff * ff * ff * ff};
+    const float tt[3] = {kTiny0 * f1, kTiny1 * f1 * ff, kTiny2 * f1 * ff * ff};
     bool ok = true;
     int n = 0, done = 0;  // the half's tiles and units
     for (int i = 0; warp_wait(u_full(i), u_phase(i), ok); ++i) {
@@ -474,23 +478,31 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                                 of(__uint_as_float(s[i / 16][2 * (i % 16) + 1])));
             return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
           };
-          // Small scores are capped by the polynomial, together with the subtraction of the
-          // maximum where no bias comes between; others by exponentials, in place.
-          bool poly = false;
+          // Small scores are capped by a polynomial, together with the subtraction of the
+          // reference where no bias comes between; others by exponentials, in place.
+          float most = 0.0f;  // the largest magnitude
+          bool poly = false, tiny = false;
           if (CAP) {
-            poly = __all_sync(0xffffffffu, largest([](float v) { return fabsf(v); }) * fac <= kTanhSmall);
+            most = largest([](float v) { return fabsf(v); });
+            poly = __all_sync(0xffffffffu, most * fac <= kTanhSmall);
+            tiny = !SLOPES && __all_sync(0xffffffffu, most * fac <= kTanhTiny);
             if (!poly) {
               const uint64_t k2 = pack2(2.0f * 1.44269504f * fac, 2.0f * 1.44269504f * fac);
 #pragma unroll
               for (int i = 0; i < 64; ++i) set_pair(i, tanh2(pair(i), k2));
             }
           }
-          auto capped = [&](int i) {  // the polynomial's sum without the last factor
+          // The polynomials' sums without the last factor.
+          auto capped = [&](int i) {
             const uint64_t x = pair(i), z = mul2(x, x);
             uint64_t r = fma2(z, pack2(tc[4], tc[4]), pack2(tc[3], tc[3]));
             r = fma2(r, z, pack2(tc[2], tc[2]));
             r = fma2(r, z, pack2(tc[1], tc[1]));
             return fma2(r, z, pack2(tc[0], tc[0]));
+          };
+          auto capped_tiny = [&](int i) {
+            const uint64_t x = pair(i), z = mul2(x, x);
+            return fma2(fma2(z, pack2(tt[2], tt[2]), pack2(tt[1], tt[1])), z, pack2(tt[0], tt[0]));
           };
           if (SLOPES) {
             const float d0 = float(t0 - x.pos), f = CAP ? p.cap_log2 : fac;
@@ -507,7 +519,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
             for (int i = 0; i < 64; ++i) set_pair(i, mul2(capped(i), pair(i)));
             sl_now = 1.0f;
-            poly = false;
+            poly = tiny = false;
           }
           if (careful) {
             const int lo = max(0, x.lo - t0), hi = min(x.hi, end) - t0;
@@ -520,12 +532,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 if (!(see & (1u << k))) s[e][k] = 0xff800000u;  // -inf
             }
           }
-          float mx = largest([](float v) { return v; });
-          if (CAP && !SLOPES && poly) {
-            const float z = mx * mx;
-            mx = mx == -INFINITY ? mx : mx * fmaf(fmaf(fmaf(fmaf(tc[4], z, tc[3]), z, tc[2]), z, tc[1]), z, tc[0]);
+          float mx;
+          if (CAP && !SLOPES && poly && __all_sync(0xffffffffu, most * f1 <= 30.0f)) {
+            // Every score is seen and between -30 and 30 in the exponent, so the largest magnitude
+            // serves as a reference: no weight that counts is below 2^-60, and a search for
+            // the maximum is saved.
+            mx = most * f1;
           } else {
-            mx = mx == -INFINITY ? mx : mx * sl_now;
+            mx = largest([](float v) { return v; });
+            if (CAP && !SLOPES && poly) {
+              const float z = mx * mx;
+              mx = mx == -INFINITY ? mx : mx * fmaf(fmaf(fmaf(fmaf(tc[4], z, tc[3]), z, tc[2]), z, tc[1]), z, tc[0]);
+            } else {
+              mx = mx == -INFINITY ? mx : mx * sl_now;
+            }
           }
           const bool move = mx > ref + kPromptSlack;
           if (__any_sync(0xffffffffu, move)) {
@@ -571,7 +591,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               tmem_store16(t_s(h) + lane_base + 16 * e, w);
             }
           };
-          if (CAP && !SLOPES && poly)
+          if (CAP && !SLOPES && tiny)
+            weights([&](int i) { return fma2(capped_tiny(i), pair(i), m2); });
+          else if (CAP && !SLOPES && poly)
             weights([&](int i) { return fma2(capped(i), pair(i), m2); });
           else
             weights([&](int i) { return fma2(pair(i), sl2, m2); });
