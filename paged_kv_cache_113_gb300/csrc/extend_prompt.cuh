@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         for (int j = 0; j < nt; ++j, ++n) {
           const int iv = k0 + 2 * j + 1, ik = iv + 1;
           if (!warp_wait(v_ready(iv), kv_phase(iv), ok) || (j + 1 < nt && !warp_wait(kv_full(ik), kv_phase(ik), ok)) ||
-              !warp_wait(p_full(h), n & 1, ok) || !my_turn())
+              !my_turn() || !warp_wait(p_full(h), n & 1, ok))
             break;
           tc_fence_after();
           products(j);
@@ -378,34 +378,49 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             const int ch = lane % CH;
             const uint32_t at = kv_sm + iv % ST * S::TILE + (ch >> 3) * S::SLAB + (ch & 7) * 16;
             bool wrote = false;
-            constexpr int STEP = 32 / CH, U = 4;  // rows at once, and loads under way
-#pragma unroll 1
-            for (int k0 = 32 * w + lane / CH; k0 < 32 * w + 32; k0 += U * STEP) {
-              uint32_t v[U][4];
-#pragma unroll
-              for (int u = 0; u < U; ++u)
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(v[u][0]), "=r"(v[u][1]), "=r"(v[u][2]), "=r"(v[u][3])
-                             : "r"(at + (k0 + u * STEP) * 128));
-#pragma unroll
-              for (int u = 0; u < U; ++u) {
-                const int k = k0 + u * STEP;
-                if (k >= all_from && k < all_to) continue;
-                // A carry into a half's sign shows an exponent of all ones.
-                uint32_t odd = 0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) odd |= (v[u][e] & 0x7f807f80u) + 0x00800080u;
-                if (k < valid && !(odd & 0x80008000u)) continue;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  if (k >= valid || (v[u][e] & 0x7f80u) == 0x7f80u) v[u][e] &= 0xffff0000u;
-                  if (k >= valid || (v[u][e] & 0x7f800000u) == 0x7f800000u) v[u][e] &= 0xffffu;
-                }
-                if (k < valid) poisoned[i % kPromptUnits] = i + 1;
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + k * 128), "r"(v[u][0]),
-                             "r"(v[u][1]), "r"(v[u][2]), "r"(v[u][3])
-                             : "memory");
+            constexpr int STEP = 32 / CH;  // rows at once
+            const int first = 32 * w + lane / CH, last = 32 * w + 32;
+            for (int k = first; k < last; k += STEP)
+              if (k >= valid) {
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + k * 128), "r"(0) : "memory");
                 wrote = true;
+              }
+            if (32 * w < all_from || 32 * w + 32 > all_to) {  // some of the warp's rows are hidden from some
+              // Four rows' chunks at once; they are looked at one by one only if a carry into a
+              // half's sign shows an exponent of all ones.
+#pragma unroll 1
+              for (int k0 = first; k0 < min(last, valid); k0 += 4 * STEP) {
+                uint32_t v[4][4], odd = 0;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  const int k = k0 + u * STEP;
+                  v[u][0] = v[u][1] = v[u][2] = v[u][3] = 0;
+                  if (k < valid && (k < all_from || k >= all_to))
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v[u][0]), "=r"(v[u][1]), "=r"(v[u][2]), "=r"(v[u][3])
+                                 : "r"(at + k * 128));
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) odd |= (v[u][e] & 0x7f807f80u) + 0x00800080u;
+                if (!(odd & 0x80008000u)) continue;
+                poisoned[i % kPromptUnits] = i + 1;
+                wrote = true;
+#pragma unroll 1
+                for (int u = 0; u < 4; ++u) {
+                  const int k = k0 + u * STEP;
+                  if (k >= valid || (k >= all_from && k < all_to)) continue;
+#pragma unroll 1
+                  for (int e = 0; e < 4; ++e) {
+                    const uint32_t a = at + k * 128 + 4 * e;
+                    uint32_t x;
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(a));
+                    if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+                    if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
+                  }
+                }
               }
             }
             if (__any_sync(0xffffffffu, wrote)) fence_proxy_async_shared();
