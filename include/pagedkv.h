@@ -585,8 +585,9 @@ typedef struct {
  * see, NaN included, does not reach it; a value that is not finite where it is seen
  * makes its element not finite, a NaN query, key or score the row.
  * Precision: of an fp32 pool, factors of 24 bits and fp32 sums; of a bf16 pool,
- * weights of 16 bits (of 8 bits, divided by the sum of the same, where a sequence has
- * more than 8 rows, new tokens times Hq / Hk), fp32 sums of the tensor cores.
+ * weights of 16 bits (of 8 bits where a sequence may have more than 8 rows, new tokens
+ * times Hq / Hk, and B is 8, 16 or 32), fp32 sums of the tensor cores; the cap of small
+ * scores by a polynomial, 2^-17 of itself.
  *   out, q        [num_q_tokens, Hq, d], dtype of the pool; rows of no sequence are
  *                 neither read nor written.
  *   q_offsets     int32 [S + 1], ascending, or NULL: row s is sequence s's only new

@@ -304,6 +304,84 @@ def test_extend_scores_of_minus_infinity(dtype, counts):
                     assert (np.abs(got[ofs[s] + i, h] - w @ vs[:, h]) <= tol).all()
 
 
+def dense(q, k, v, tables, lens, counts, ofs, scale, sc):
+    """extend_attention and check_extend's bound for long prompts: fp64 matrices on the GPU, a sequence
+    and head at a time."""
+    R, hq, d = q.shape
+    B, hk = k.shape[1], k.shape[2]
+    out, tol = torch.zeros((R, hq, d), dtype=torch.float64, device=DEV), torch.zeros((R, hq, d), dtype=torch.float64, device=DEV)
+    D, T, rho, cap = (d + 8) * 2 * U, 2.0 ** -17, 2.0 ** -8, sc["softcap"]
+    log2e = 1 / LN2
+    for s, (n, c) in enumerate(zip(lens, counts)):
+        blocks = i64(tables[s][: -(-n // B)])
+        kk, vv = (x[blocks].reshape(-1, hk, d)[:n].double() for x in (k, v))
+        pos, t = torch.arange(n - c, n, device=DEV)[:, None], torch.arange(n, device=DEV)[None]
+        see = t <= pos
+        if "prefix_lens" in sc:
+            see = see | (t < int(sc["prefix_lens"][s]))
+        if sc["window"]:
+            see = see & (t > pos - sc["window"])
+        if "first_tokens" in sc:
+            see = see & (t >= i32(sc["first_tokens"])[ofs[s]: ofs[s + 1], None])
+        for h in range(hq):
+            qh, kh, vh = q[ofs[s]: ofs[s + 1], h].double(), kk[:, h * hk // hq], vv[:, h * hk // hq]
+            x, m = qh @ kh.T * scale, qh.abs() @ kh.abs().T * abs(scale) * log2e
+            if cap:
+                x = torch.tanh(x / cap) * cap
+            a = x.abs() + cap
+            if "slopes" in sc:
+                far = (pos - t).abs() * float(sc["slopes"][h])
+                x, a = x - far, a + far
+            w = torch.softmax(x.masked_fill(~see, -float("inf")), 1).nan_to_num(0.0)
+            o, e = w @ vh, w * (D * m + (T + 4 * U) * a * log2e)
+            out[ofs[s]: ofs[s + 1], h] = o
+            tol[ofs[s]: ofs[s + 1], h] = 2 * LN2 * (e @ vh.abs() + o.abs() * e.sum(1, keepdim=True)) + (
+                16 * U + 2 * rho + 4 * U * n) * (w @ vh.abs()) + 2.0 ** -8 * o.abs() + 1e-30
+    return out, tol
+
+
+@pytest.mark.parametrize("kind,cap", [("plain", 0.0), ("cap", 50.0), ("cap", 3.0), ("all", 20.0), ("documents", 0.0),
+                                      ("prefix", 30.0), ("slopes", 0.0)])
+@pytest.mark.parametrize("hq,hk,d", [(32, 8, 128), (24, 8, 64)])
+def test_extend_more_units_than_fit_at_once(kind, cap, hq, hk, d):
+    """CTAs go on to units of other lengths, halves, heads and sequences; capped scores of every size."""
+    rng = np.random.default_rng(hq + d + int(cap))
+    counts, lens, B = [1500, 700, 40, 300, 1], [1500, 2100, 3100, 300, 1700], 16
+    tables, k, v, ofs, q, sc = make_case(rng, counts, lens, B, hq, hk, d, torch.bfloat16, kind, pad=2)
+    sc["softcap"] = cap
+    if cap == 50.0:  # rows of large scores among small ones
+        q[::97] *= 8
+    want, tol = dense(q, k, v, tables, lens, counts, ofs, d ** -0.5, sc)
+    for part in (0, 1024):
+        out = run_extend((tables, k, v, ofs, q, sc), lens, counts, d ** -0.5, part)
+        bad = (out.double() - want).abs() > tol
+        bad[int(ofs[-1]):] = out[int(ofs[-1]):] != 7
+        assert not bool(bad.any()), (int(bad.sum()), torch.nonzero(bad)[:5].tolist())
+        assert torch.equal(run_extend((tables, k, v, ofs, q, sc), lens, counts, d ** -0.5, part), out)
+
+
+def test_extend_hidden_nan_in_every_unit():
+    """A NaN value behind every document's end: rows of other documents are as without."""
+    rng = np.random.default_rng(77)
+    n, B, hq, hk, d = 2600, 16, 16, 4, 128
+    tables, k, v, ofs, q, sc = make_case(rng, [n], [n], B, hq, hk, d, torch.bfloat16, "plain")
+    cuts = np.arange(0, n, 130)
+    first = cuts[np.searchsorted(cuts, np.arange(n), side="right") - 1]
+    sc["first_tokens"] = np.concatenate([first, np.zeros(3)]).astype(np.int32)
+    clean = run_extend((tables, k, v, ofs, q, sc), [n], [n], 0.1)
+    vv = v.clone()
+    last = np.append(cuts[1:], n) - 1  # the last token of each document: seen by itself alone
+    vv[i64(tables[0][last // B]), i64(last % B)] = float("nan")
+    for part in (0, 512):
+        out = run_extend((tables, k, vv, ofs, q, sc), [n], [n], 0.1, part)
+        hit = torch.zeros(len(q), dtype=torch.bool, device=DEV)
+        hit[i64(last)] = True
+        assert bool(out[hit].isnan().all())
+        want = run_extend((tables, k, v, ofs, q, sc), [n], [n], 0.1, part)
+        assert torch.equal(out[~hit], want[~hit])
+    assert bool(torch.isfinite(clean).all())
+
+
 def test_extend_long_context_in_parts_and_offsets_past_32_bits():
     """A pool of more than 2^31 elements, its last blocks in use, and a plan that splits."""
     B, hk, hq, d = 16, 8, 16, 128
