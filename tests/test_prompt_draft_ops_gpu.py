@@ -382,6 +382,34 @@ def test_extend_hidden_nan_in_every_unit():
     assert bool(torch.isfinite(clean).all())
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_extend_many_sequences(dtype):
+    """More sequences than a warp's lanes, many without rows, with a list and without; windows and first
+    tokens beyond everything; and on a stream of its own."""
+    dt = DTYPES[dtype]
+    rng = np.random.default_rng(123)
+    S, B, hq, hk, d = 150, 8, 4, 2, 64
+    lens = rng.integers(1, 120, S).tolist()
+    counts = [int(rng.integers(0, min(n, 40) + 1)) if rng.random() < 0.7 else 0 for n in lens]
+    case = make_case(rng, counts, lens, B, hq, hk, d, dt, "plain")
+    tables, k, v, ofs, q, sc = case
+    for window, first in ((0, None), (2 ** 31 - 1, None), (3, None), (0, 2 ** 31 - 1)):
+        sc["window"] = window
+        sc.pop("first_tokens", None)
+        if first is not None:
+            sc["first_tokens"] = np.where(rng.random(len(q)) < 0.5, first, 0).astype(np.int32)
+        for part, listed in ((0, True), (0, False), (64, True), (64, False)):
+            out = run_extend(case, lens, counts, 0.125, part, listed)
+            check_extend(out, q, k, v, tables, lens, 0.125, ofs, sc)
+    st = torch.cuda.Stream()
+    want = run_extend(case, lens, counts, 0.125)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        got = run_extend(case, lens, counts, 0.125)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
 def test_extend_long_context_in_parts_and_offsets_past_32_bits():
     """A pool of more than 2^31 elements, its last blocks in use, and a plan that splits."""
     B, hk, hq, d = 16, 8, 16, 128
@@ -760,6 +788,42 @@ def test_compact_bad_inputs_are_recorded():
     kk, lo, err = call(tb=bad)
     assert err == (2, 1) and lo == [27, 38, 18]
     others(kk, 1)
+
+
+def test_verification_and_compaction_in_a_replayed_graph():
+    """The two captured one after the other and replayed with other numbers, drafts and lengths."""
+    rng = np.random.default_rng(50)
+    B, hk, d, V, counts, lens = 8, 2, 64, 2000, [6, 9, 1, 4], [30, 40, 20, 55]
+    tables, k, v, ofs, q, _ = make_case(rng, counts, lens, B, hk, hk, d, torch.bfloat16, "plain", pad=0)
+    _, target, tokens, u, parents, _ = make_drafts(rng, counts, V, torch.float32, "tree", pad=0)
+    dev = dict(tokens=i64(tokens), u=torch.from_numpy(u).to(DEV), parents=i32(parents), lens=i32(lens), ofs=i32(ofs),
+               tables=i32(tables), na=i32([0] * 4), ac=i32([0] * 20), nt=i64([0] * 4), left=i32([0] * 4))
+
+    def run():
+        pk.pk_verify_drafts(dev["na"], dev["ac"], dev["nt"], target, dev["tokens"], dev["u"], dev["ofs"], 9,
+                            parents=dev["parents"])
+        pk.pk_compact_drafts(k, v, dev["tables"], dev["lens"], dev["ofs"], dev["ac"], dev["na"], 9,
+                             context_lens_out=dev["left"])
+
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for trial in range(3):
+        _, t2, tokens, u, parents, _ = make_drafts(rng, counts, V, torch.float32, "tree", pad=0)
+        target.copy_(t2)
+        lens = [int(n - rng.integers(0, 10)) for n in (30, 40, 20, 55)]
+        for name, x in (("tokens", i64(tokens)), ("u", torch.from_numpy(u).to(DEV)), ("parents", i32(parents)), ("lens", i32(lens))):
+            dev[name].copy_(x)
+        wk, wv = f64(k), f64(v)
+        g.replay()
+        torch.cuda.synchronize()
+        check_verify((dev["na"], dev["ac"], dev["nt"]), ofs, target, tokens, u, parents, None)
+        _, paths, _ = plain.verify_drafts(f64(target), tokens, u, ofs, parents)
+        left = plain.compact_drafts(wk, tables, lens, ofs, paths)
+        plain.compact_drafts(wv, tables, lens, ofs, paths)
+        assert dev["left"].tolist() == left and (f64(k) == wk).all() and (f64(v) == wv).all()
 
 
 # ---------------------------------------------------------------------------
