@@ -736,10 +736,15 @@ pk_status pk_bm_add_seq(pk_bm *bm, int64_t seq_id);
 
 /* Appends n >= 0 tokens to seq_id. slots_out[i] (int64, n entries) receives
  * token i's slot. When the sequence's first new token falls into a partly
- * filled tail block shared with another table, the block is copied first:
+ * filled tail block shared with another table (or known to the prefix cache,
+ * after pk_bm_truncate), the block is copied first:
  * the (src, dst) pair goes to cow_pairs_out[0..1] and *n_cow_out = 1 (else
  * 0); the caller must run pk_copy_blocks on it before the scatter. All or
- * nothing: PK_ERR_OUT_OF_BLOCKS leaves the manager unchanged. */
+ * nothing: PK_ERR_OUT_OF_BLOCKS leaves the manager unchanged. The pairs of
+ * one call (of this or of pk_bm_append_batch) may be copied in any order and
+ * at once: no block is a source and a destination. Those of several calls are
+ * copied call by call, in the order of the calls (one pk_copy_blocks each): a
+ * later call may write over a block that an earlier one copied from. */
 pk_status pk_bm_append_slots(pk_bm *bm, int64_t seq_id, int32_t n, int64_t *slots_out,
                              int64_t *cow_pairs_out, int32_t *n_cow_out);
 

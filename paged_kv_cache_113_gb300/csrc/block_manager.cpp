@@ -15,7 +15,9 @@
 //   * Fork: the child names the parent's blocks; each count goes up by one.
 //   * Cut (after refused drafts): the blocks behind the new end lose one reference
 //     each, last first. A cut inside a block that the prefix cache knows leaves it
-//     as it is; the next append copies it like a shared one.
+//     as it is; the next append copies it like a shared one. The blocks that a call's
+//     appends copied from go back after its last allocation, so that no block is one
+//     copy's source and another's destination: the call's copies run side by side.
 //   * Retire: each block of the table loses one reference; those reaching
 //     zero go back to the free list, in table order.
 //   * The free list is a stack whose first pop is alloc_order[0].
@@ -110,6 +112,7 @@ struct pk_bm {
   std::vector<uint64_t> given_up_mark;   // per block: call that last counted a CoW of it
   std::vector<int32_t> given_up;         // CoW copies of the block that call counted
   std::vector<Sequence *> batch_seqs;    // scratch of pk_bm_append_batch
+  std::vector<int32_t> copied;           // cached tails that no table names since this call's copies
 
   int64_t blocks_for(int64_t len) const { return (len + block_size - 1) / block_size; }
 
@@ -175,7 +178,8 @@ struct pk_bm {
   bool tail_taken(int32_t b) const { return refs[b] > 1 || entry[b].cached; }
 
   // Appends one token (the caller has checked that a block is available if
-  // one is needed). A new block or a CoW copy comes from take_block.
+  // one is needed). A new block or a CoW copy comes from take_block. The caller gives the
+  // copied tails back when it has taken its last block.
   int64_t append_one(Sequence &s, int64_t *cow_src, int64_t *cow_dst) {
     const int64_t off = s.len % block_size;
     if (off == 0) {
@@ -187,7 +191,7 @@ struct pk_bm {
       if (tail_taken(tail)) {
         const int32_t b = take_block();
         refs[b] = 1;
-        release(tail);
+        if (--refs[tail] == 0) copied.push_back(tail);  // a cached one; room was reserved
         s.table.back() = b;
         ++cow_copies;
         if (cow_src) *cow_src = tail;
@@ -197,6 +201,17 @@ struct pk_bm {
     const int64_t slot = int64_t(s.table[s.len / block_size]) * block_size + off;
     s.len += 1;
     return slot;
+  }
+
+  // The copied tails become the youngest unreferenced cached blocks.
+  void give_copied_back() {
+    if (copied.empty()) return;
+    ++clock;
+    for (int32_t b : copied) {
+      entry[b].released = clock;
+      idle.insert(idle_key(b));
+    }
+    copied.clear();
   }
 };
 
@@ -215,6 +230,7 @@ pk_status pk_bm_create(int32_t num_blocks, int32_t block_size, const int32_t *al
     bm->entry.resize(num_blocks);
     bm->given_up_mark.assign(num_blocks, 0);
     bm->given_up.assign(num_blocks, 0);
+    bm->copied.reserve(num_blocks);
     bm->free_stack.resize(num_blocks);
     std::vector<char> seen(num_blocks, 0);
     for (int32_t i = 0; i < num_blocks; ++i) {
@@ -267,6 +283,7 @@ pk_status pk_bm_append_slots(pk_bm *bm, int64_t seq_id, int32_t n, int64_t *slot
   }
   int64_t src = -1, dst = -1;
   for (int32_t i = 0; i < n; ++i) slots_out[i] = bm->append_one(s, &src, &dst);
+  bm->give_copied_back();
   if (src >= 0) {
     if (cow_pairs_out) {
       cow_pairs_out[0] = src;
@@ -334,6 +351,7 @@ pk_status pk_bm_append_batch(pk_bm *bm, const int64_t *seq_ids, int32_t n, int64
       ++ncow;
     }
   }
+  bm->give_copied_back();
   if (n_cow_out) *n_cow_out = ncow;
   return PK_OK;
 }
