@@ -200,8 +200,8 @@ __global__ void __launch_bounds__(256) extend_merge_kernel(ExtendParams p) {
   constexpr int EPL = D / 32, U = 8;
   const int lane = threadIdx.x & 31;
   const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (row >= int64_t(p.num_rows) * p.num_q_heads) return;
-  const int tok = int(row / p.num_q_heads);
+  const bool some = row < int64_t(p.num_rows) * p.num_q_heads;
+  const int tok = some ? int(row / p.num_q_heads) : 0;
   int s = tok;
   if (p.q_offsets) {  // the last sequence that begins at or before the row
     int a = 0, b = p.num_seqs;
@@ -211,19 +211,24 @@ __global__ void __launch_bounds__(256) extend_merge_kernel(ExtendParams p) {
       else b = mid;
     }
     s = a;
-  } else if (s >= p.num_seqs) {
-    return;
   }
-  const SeqRows sr = seq_rows(p, s, false);
-  if (tok < sr.q0 || tok >= sr.q0 + sr.n) return;
   RowSpan x{0, 0, 0};
-  if (sr.ctx > 0) x = row_span(p, sr, s, tok - sr.q0);
   int first = 0, last = -1;
-  if (x.lo < x.hi) {
-    first = x.lo / p.partition, last = (x.hi - 1) / p.partition;
-    if (first == last) return;
+  bool mine = some && s < p.num_seqs;
+  if (mine) {
+    const SeqRows sr = seq_rows(p, s, false);
+    mine = tok >= sr.q0 && tok < sr.q0 + sr.n;
+    if (mine && sr.ctx > 0) x = row_span(p, sr, s, tok - sr.q0);
+    if (x.lo < x.hi) {
+      first = x.lo / p.partition, last = (x.hi - 1) / p.partition;
+      mine = first != last;
+    }
   }
+  // Every warp waits for the attention, those with nothing to do too: what comes after this
+  // grid on the stream or in a graph waits for it alone, and the attention has written the rows
+  // that lie in one partition to `out` itself.
   wait_prerequisites();
+  if (!mine) return;
   float M = -INFINITY, L = 0.0f, acc[EPL];
 #pragma unroll
   for (int e = 0; e < EPL; ++e) acc[e] = 0.0f;

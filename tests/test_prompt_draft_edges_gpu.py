@@ -1,0 +1,68 @@
+"""Edges of prompt attention, draft verification and cache compaction on the GPU: what the calls are
+followed by, sizes and values at the ends of their ranges, and bounds tighter than those of the general tests."""
+import numpy as np
+import pytest
+
+import paged_kv_cache_113_gb300 as pk
+
+torch = pytest.importorskip("torch")
+import test_prompt_draft_ops_gpu as ops  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+DEV, U = ops.DEV, ops.U
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    pk.build()
+
+
+@pytest.fixture(autouse=True)
+def _no_device_error():
+    pk.pk_get_device_error()
+    yield
+    assert pk.pk_get_device_error() == (0, 0)
+
+
+# ---------------------------------------------------------------------------
+# Attention
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,counts", [("bf16", [600, 150, 1, 40]), ("bf16", [1, 1, 1, 1]), ("f32", [60, 15, 1, 4])])
+def test_extend_split_call_is_over_when_what_follows_it_starts(dtype, counts):
+    """A split call of which no row lies in two partitions, so that the merge has no row to write, then a copy of
+    the result: captured together and replayed, the copy is the result every time."""
+    rng = np.random.default_rng(60)
+    B, hq, hk, d, dt = 16, 8, 2, 128, ops.DTYPES[dtype]
+    lens, part = [2040, 900, 700, 1500], 512
+    tables, k, v, ofs, q, sc = ops.make_case(rng, counts, lens, B, hq, hk, d, dt, "plain")
+    # Documents that end where partitions do, a new one at every multiple of 128 within them.
+    sc["first_tokens"] = np.zeros(len(q), np.int32)
+    for s, (c, n) in enumerate(zip(counts, lens)):
+        pos = np.arange(n - c, n)
+        sc["first_tokens"][ofs[s]: ofs[s + 1]] = pos // 128 * 128
+    want = ops.run_extend((tables, k, v, ofs, q, sc), lens, counts, d ** -0.5)
+    ops.check_extend(want, q, k, v, tables, lens, d ** -0.5, ofs, sc)
+    desc = pk.cache_desc(k)
+    part, items = pk.pk_extend_plan(lens, counts, hq, desc, part)
+    assert part == 512
+    ws = torch.zeros(pk.pk_extend_workspace_size(len(q), hq, max(lens), part, desc), dtype=torch.uint8, device=DEV)
+    out, copy = torch.full_like(q, 7.0), torch.empty_like(q)
+    args = (out, q, k, v, ops.i32(tables), ops.i32(lens), ops.i32(ofs), d ** -0.5, max(counts), max(lens))
+    kw = dict(ops.on_device(sc), partition_size=part, workspace=ws, work_items=torch.from_numpy(items).to(DEV))
+    pk.pk_paged_attention_extend(*args, **kw)
+    torch.cuda.synchronize()
+    split = out.clone()  # (of other tiles than the whole call, so not its bits)
+    ops.check_extend(split, q, k, v, tables, lens, d ** -0.5, ofs, sc)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out.fill_(7.0)
+        pk.pk_paged_attention_extend(*args, **kw)
+        copy.copy_(out)
+        out.fill_(-3.0)
+    for _ in range(200):
+        copy.zero_()
+        g.replay()
+        assert torch.equal(copy, split)
+    assert bool((out == -3.0).all())
