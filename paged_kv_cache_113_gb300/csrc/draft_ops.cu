@@ -156,6 +156,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_drafts_kernel(Verify
     }
     return;  // the whole cluster does
   }
+  // Another CTA's shared memory is written only once that CTA is known to run: all say so here,
+  // and are waited for ahead of the first totals.
+  cluster.barrier_arrive();
   const int n = int(len);
   const T *const p = static_cast<const T *>(a.p), *const q = static_cast<const T *>(a.q);
   if (warp == 0) {
@@ -253,6 +256,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_drafts_kernel(Verify
     const Pair sum = sum_of(from, min(g1, from + per));
     if (lane == 0) warp_sum[warp] = sum;
     __syncthreads();
+    if (!plain) cluster.barrier_wait();
     if (warp == 0) {
       Pair x = lane < NW ? warp_sum[lane] : Pair{};
 #pragma unroll

@@ -66,3 +66,35 @@ def test_extend_split_call_is_over_when_what_follows_it_starts(dtype, counts):
         g.replay()
         assert torch.equal(copy, split)
     assert bool((out == -3.0).all())
+
+
+# ---------------------------------------------------------------------------
+# Verification
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("mask,V", [("chain", 50257), ("greedy", 50257), ("tree", 32000), ("chain", 9000)])
+def test_verify_by_several_ctas_a_sequence_again_and_again(mask, V):
+    """Few sequences, so that eight (of 9000 values two) CTAs share one, with roots alone, sequences without rows
+    and bad ranges between them (whose CTAs leave before they meet): the same result every time."""
+    rng = np.random.default_rng(V)
+    counts = [1, 1, 6, 0, 3, 1, 2]
+    ofs, target, tokens, u, parents, draft = ops.make_drafts(rng, counts, V, torch.float32, mask)
+    case = (ofs, target, tokens, u, parents, draft)
+    first = ops.run_verify(*case)
+    ops.check_verify(first, *case)
+    bad = ofs.copy()
+    bad[4] = 99  # sequences 3 and 4 have no range
+    args = [ops.i64(tokens), torch.from_numpy(u).to(DEV)]
+    S, R = len(counts), len(tokens)
+    for of in (ofs, bad):
+        na, ac, nt = (torch.zeros(n, dtype=t, device=DEV) for n, t in ((S, torch.int32), (R, torch.int32), (S, torch.int64)))
+        offsets, par = ops.i32(of), None if parents is None else ops.i32(parents)
+        for _ in range(300):
+            nt.fill_(-9)
+            pk.pk_verify_drafts(na, ac, nt, target, *args, offsets, 64, parents=par, draft_probs=draft)
+            good = [0, 1, 2, 5, 6] if of is bad else list(range(S))
+            assert torch.equal(nt[good], first[2][good]) and torch.equal(na[good], first[0][good])
+            if of is bad:
+                assert nt[[3, 4]].tolist() == [-1, -1] and na[[3, 4]].tolist() == [0, 0]
+        if of is bad:
+            assert pk.pk_get_device_error()[0] == 8
+            pk.pk_get_device_error()
