@@ -153,6 +153,7 @@ __global__ void __launch_bounds__((kFewWarps + 1) * 32, 3)
       if (careful) {
         // Values past the end are zeroed, and so is what is not finite in values that some rows
         // do not see, which would reach those too (0 * NaN); the rows that do get it at the end.
+        bool wrote = false;
         for (int i = lane; i < 16 * S::SLABS * 8; i += 32) {
           const int r = i / (S::SLABS * 8), c = i % (S::SLABS * 8), t = t0 + r;
           if (t >= view.all_from && t < view.all_to) continue;
@@ -168,11 +169,14 @@ __global__ void __launch_bounds__((kFewWarps + 1) * 32, 3)
             if (r >= nvalid || (w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu, odd = true;
           }
           if (!odd) continue;
+          wrote = true;
           if (r < nvalid) poisoned = 1;
           asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                        "r"(w[3])
                        : "memory");
         }
+        // A later tile's copies go to the same bytes by the other proxy.
+        if (__any_sync(0xffffffffu, wrote)) fence_proxy_async_shared();
         __syncwarp();
       }
       float sacc[2][4];

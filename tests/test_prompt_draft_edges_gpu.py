@@ -68,6 +68,31 @@ def test_extend_split_call_is_over_when_what_follows_it_starts(dtype, counts):
     assert bool((out == -3.0).all())
 
 
+@pytest.mark.parametrize("hq,hk,d,B", [(8, 2, 128, 16), (4, 1, 64, 8), (3, 1, 128, 32)])
+def test_extend_few_rows_clear_hidden_values_in_places_that_are_filled_again(hq, hk, d, B):
+    """Two new tokens, the first of which sees what the second does not, NaN and infinities in all of it: many
+    tiles in turn are cleared and their places filled again. The second one's rows are bit for bit as without."""
+    rng = np.random.default_rng(d + B)
+    lens, counts = [2500, 1300, 700, 1999], [2, 2, 2, 2]
+    tables, k, v, ofs, q, sc = ops.make_case(rng, counts, lens, B, hq, hk, d, torch.bfloat16, "plain", pad=0)
+    sc["first_tokens"] = np.stack([np.zeros(4), np.array(lens) - 300], 1).astype(np.int32).reshape(-1)
+    bad = v.clone()
+    for s, n in enumerate(lens):
+        t = np.arange(n - 300)
+        at = ops.i64(tables[s][t // B]), ops.i64(t % B)
+        x = bad[at]
+        x[torch.rand(x.shape, device=DEV) < 0.3] = float("nan")
+        x[torch.rand(x.shape, device=DEV) < 0.3] = float("-inf")
+        bad[at] = x
+    for part in (0, 512):
+        want = ops.run_extend((tables, k, v, ofs, q, sc), lens, counts, d ** -0.5, part)
+        ops.check_extend(want, q, k, v, tables, lens, d ** -0.5, ofs, sc)
+        for _ in range(20):
+            out = ops.run_extend((tables, k, bad, ofs, q, sc), lens, counts, d ** -0.5, part)
+            assert torch.equal(out[1::2], want[1::2])
+            assert not bool(torch.isfinite(out[::2]).any())
+
+
 # ---------------------------------------------------------------------------
 # Verification
 # ---------------------------------------------------------------------------
