@@ -42,6 +42,7 @@ constexpr int kPromptThreads = 512;
 constexpr int kPromptUnits = 4;      // units known at a time
 // 512 threads of 128 registers at launch: 2 x 200 + 2 x 56 = 4 x 128.
 constexpr int kPromptSoftmaxRegs = 200, kPromptOtherRegs = 56;
+constexpr float kPromptExact = 1048576.0f;  // scores up to it are scaled in one operation with the subtraction
 constexpr float kPromptSlack = 8.0f;  // log2 of how far a maximum may outgrow the reference
 
 template <int D>
@@ -588,6 +589,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             } else {
               mx = mx == -INFINITY ? mx : mx * sl_now;
             }
+          }
+          if (!SLOPES && !poly && __any_sync(0xffffffffu, tid < rows && fabsf(mx) > kPromptExact && mx > -INFINITY)) {
+            // The weights' multiply-add takes the reference, a rounded product, from exact ones: of scores
+            // of 2^31 the difference of a score from itself would be some 2^7 and its weight infinite.
+#pragma unroll
+            for (int i = 0; i < 64; ++i) set_pair(i, mul2(pair(i), pack2(sl_now, sl_now)));
+            sl_now = 1.0f;
           }
           const bool move = mx > ref + kPromptSlack;
           if (__any_sync(0xffffffffu, move)) {

@@ -93,6 +93,80 @@ def test_extend_few_rows_clear_hidden_values_in_places_that_are_filled_again(hq,
             assert not bool(torch.isfinite(out[::2]).any())
 
 
+def dense(q, k, v, tables, lens, counts, ofs, scale, sc, rho, T):
+    """The definition in fp64 on the GPU, a sequence and head at a time, and its bound: the general tests'
+    with the cap's error relative to the capped score, not to the cap,
+    e_t = D m_t + (T + 6 u) (|x_t| + |capped x_t| + |bias_t|) log2(e),
+    T being tanh's own relative error: 2^-22 of tanhf, 2^-17 of bf16's (2^-17.3 of the shortest polynomial,
+    2^-20.6 of the longer one; an exponential and a reciprocal are off by 2^-21 where tanh is above 0.6);
+    six roundings: the product by its factor, the tanh's argument, by the cap, bias twice, the maximum's.
+    Where e_t is above 1/2 for a token seen, exp is no longer close to linear and the bound is the values' range."""
+    R, hq, d = q.shape
+    B, hk = k.shape[1], k.shape[2]
+    out, tol = (torch.zeros((R, hq, d), dtype=torch.float64, device=DEV) for _ in range(2))
+    D, cap, log2e, eta = (d + 8) * 2 * U, sc.get("softcap", 0.0), 1 / ops.LN2, ops.ETA[q.dtype]
+    for s, (n, c) in enumerate(zip(lens, counts)):
+        blocks = ops.i64(tables[s][: -(-n // B)])
+        kk, vv = (x[blocks].reshape(-1, hk, d)[:n].double() for x in (k, v))
+        pos, t = torch.arange(n - c, n, device=DEV)[:, None], torch.arange(n, device=DEV)[None]
+        see = t <= pos
+        if sc.get("window"):
+            see = see & (t > pos - sc["window"])
+        for h in range(hq):
+            qh, kh, vh = q[ofs[s]: ofs[s + 1], h].double(), kk[:, h * hk // hq], vv[:, h * hk // hq]
+            x, m = qh @ kh.T * scale, qh.abs() @ kh.abs().T * abs(scale) * log2e
+            a = x.abs()
+            if cap:
+                x = torch.tanh(x / cap) * cap
+                a = a + x.abs()
+            if "slopes" in sc:
+                far = (pos - t).abs() * float(sc["slopes"][h])
+                x, a = x - far, a + far
+            w = torch.softmax(x.masked_fill(~see, -float("inf")), 1).nan_to_num(0.0)
+            e = D * m + (T + 6 * U) * a * log2e
+            o, we = w @ vh, w * e
+            x = 2 * ops.LN2 * (we @ vh.abs() + o.abs() * we.sum(1, keepdim=True)) + (
+                16 * U + 2 * rho + 4 * U * n) * (w @ vh.abs()) + eta * o.abs() + 1e-30
+            wild = (e.masked_fill(~see, 0.0).amax(1) > 0.5)[:, None]
+            out[ofs[s]: ofs[s + 1], h] = o
+            tol[ofs[s]: ofs[s + 1], h] = torch.where(wild, 2.1 * vh.abs().amax(), x)
+    return out, tol
+
+
+def check_dense(out, *args):
+    want, tol = dense(*args)
+    ofs = args[6]
+    bad = ~((out.double() - want).abs() <= tol)
+    bad[int(ofs[-1]):] = False
+    assert not bool(bad.any()), (int(bad.sum()), torch.nonzero(bad)[:4].tolist(), out[bad][:4], want[bad][:4], tol[bad][:4])
+
+
+PATHS = {  # type, block size, new tokens, context lengths
+    "few": ("bf16", 16, [1, 1, 2], [300, 1000, 77]),
+    "prompt": ("bf16", 16, [300, 40, 1], [300, 700, 90]),
+    "other blocks": ("bf16", 12, [60, 3], [60, 200]),
+    "f32": ("f32", 16, [60, 1], [60, 300]),
+    "f32 few": ("f32", 16, [1, 1], [100, 300]),
+}
+# A weight as the product takes it: a bf16 pair, one bf16, 24 bits.
+RHO = {"few": 2.0 ** -17, "prompt": 2.0 ** -8, "other blocks": 2.0 ** -17, "f32": U, "f32 few": U}
+
+
+@pytest.mark.parametrize("path", sorted(PATHS))
+@pytest.mark.parametrize("scale", [1e7, 1e9, -1e9, 1e12, 1e20, 1e30])
+@pytest.mark.parametrize("kind", ["plain", "slopes", "window"])
+def test_extend_scores_far_above_one(path, scale, kind):
+    """Scores of 10^7 and more, where an fp32 score is known to hundreds or worse: finite results within the
+    values' range, and of rows that see one token that token's value."""
+    dtype, B, counts, lens = PATHS[path]
+    rng = np.random.default_rng(len(path))
+    hq, hk, d = 4, 2, 128
+    tables, k, v, ofs, q, sc = ops.make_case(rng, counts, lens, B, hq, hk, d, ops.DTYPES[dtype], kind)
+    for part in (0, 4 * B):
+        out = ops.run_extend((tables, k, v, ofs, q, sc), lens, counts, scale, part)
+        check_dense(out, q, k, v, tables, lens, counts, ofs, scale, sc, RHO[path], 2.0 ** -17)
+
+
 # ---------------------------------------------------------------------------
 # Verification
 # ---------------------------------------------------------------------------
