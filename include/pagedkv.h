@@ -563,7 +563,8 @@ size_t pk_tree_workspace_size(int32_t num_q_tokens, int32_t num_q_heads, int32_t
 /* What is done to the scores of pk_paged_attention_extend, and what a row sees.
  * Arrays are device memory. All zero: plain causal attention. */
 typedef struct {
-    float softcap;                /* c > 0: x becomes c tanh(x / c); 0: not capped       */
+    float softcap;                /* c > 0: x becomes c tanh(x / c); 0: not capped.
+                                     2^-100 <= c <= 2^100, and scale / c as well or 0    */
     int32_t window;               /* w > 0: a row sees no token before position - w + 1  */
     const float *slopes;          /* [Hq] or NULL: x -= slope |position - t|             */
     const int32_t *prefix_lens;   /* [S] or NULL: every row sees the tokens before it    */
@@ -586,8 +587,9 @@ typedef struct {
  * makes its element not finite, a NaN query, key or score the row.
  * Precision: of an fp32 pool, factors of 24 bits and fp32 sums; of a bf16 pool,
  * weights of 16 bits (of 8 bits where a sequence may have more than 8 rows, new tokens
- * times Hq / Hk, and B is 8, 16 or 32), fp32 sums of the tensor cores; the cap of small
- * scores by a polynomial, 2^-17 of itself.
+ * times Hq / Hk, and B is 8, 16 or 32), fp32 sums of the tensor cores; a capped score
+ * to 2^-17 of itself (fp32 2^-22; of those more than 8 rows, with a cap of at most 88,
+ * 2^-21 of the cap where others of the tile reach 3/4 of it).
  *   out, q        [num_q_tokens, Hq, d], dtype of the pool; rows of no sequence are
  *                 neither read nor written.
  *   q_offsets     int32 [S + 1], ascending, or NULL: row s is sequence s's only new
@@ -597,7 +599,7 @@ typedef struct {
  *   context_lens  int32 [S], new tokens included: n <= length <=
  *                 min(max_context_len, max_blocks_per_seq * B), clamped and recorded
  *                 otherwise (PK_DEVERR_CONTEXT; a length below n gives zero rows).
- *   scores        NULL: plain causal attention. softcap finite and not negative.
+ *   scores        NULL: plain causal attention. softcap: 0 or within its bounds.
  *   partition_size, work_items  0 and NULL: each context whole; otherwise
  *                 pk_extend_plan's for the same max_query_len (work_items NULL: all
  *                 units and partitions). An item that is no unit of the call's is

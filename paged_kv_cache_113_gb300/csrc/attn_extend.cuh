@@ -28,6 +28,13 @@ struct ExtendParams : RowsParams {
   int32_t tiles;                // units of a KV head and partition without a list
 };
 
+// For |y| <= kTanhSmall tanh(y) = y (c0 + c1 y^2 + .. + c4 y^8) to 2^-20.6 of itself: like
+// extend_prompt.cuh's shorter one, the polynomial of least largest relative error, by linear
+// programming over 2000 points.
+constexpr float kTanhSmall = 0.75f;
+constexpr float kTanh0 = 0.999999463558197f, kTanh1 = -0.3332850933074951f, kTanh2 = 0.13261185586452484f,
+                kTanh3 = -0.05011745169758797f, kTanh4 = 0.012983138673007488f;
+
 struct RowSpan {
   int pos, lo, hi;  // position, and the tokens that the row sees (lo >= hi: none)
 };

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
 #include <new>
 #include <tuple>
 #include <vector>
@@ -98,6 +99,15 @@ pk_status check_extend(const pk_cache_desc *d, int32_t num_q_heads, int32_t max_
     return PK_ERR_UNSUPPORTED;
   if (int64_t(d->num_blocks) * d->block_size > INT32_MAX) return PK_ERR_UNSUPPORTED;
   return PK_OK;
+}
+
+// Whether a cap and what it makes of the scale are numbers that the kernels can work with: far
+// enough from fp32's ends that their products with queries, in parts too, are normal numbers.
+bool cap_fits(float softcap, float scale) {
+  if (softcap == 0.0f) return true;
+  constexpr double least = 0x1p-100, most = 0x1p100;
+  const double c = softcap, f = std::fabs(double(scale)) / c;
+  return c >= least && c <= most && (f == 0.0 || (f >= least && f <= most));
 }
 
 // Units of work without a split: the tokens that a unit's rows see between them (a
@@ -245,8 +255,7 @@ pk_status pk_paged_attention_extend(void *out, const void *q, const void *k_cach
   pk_status st = check_extend(desc, num_q_heads, max_context_len, partition_size);
   if (st != PK_OK) return st;
   if (num_seqs < 0 || num_q_tokens < 0 || max_query_len < 0 || num_items < 0) return PK_ERR_INVALID_ARG;
-  if (scores && (!(scores->softcap >= 0.0f) || scores->softcap > 3.0e38f || scores->window < 0))
-    return PK_ERR_INVALID_ARG;
+  if (scores && (!cap_fits(scores->softcap, scale) || scores->window < 0)) return PK_ERR_INVALID_ARG;
   if (num_seqs == 0 || num_q_tokens == 0 || max_query_len == 0) return PK_OK;
   if (!q_offsets && (num_q_tokens < num_seqs || max_query_len != 1)) return PK_ERR_INVALID_ARG;
   if (work_items ? (num_items == 0 || !aligned16(work_items)) : num_items != 0) return PK_ERR_INVALID_ARG;

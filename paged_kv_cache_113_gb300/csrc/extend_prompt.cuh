@@ -42,7 +42,8 @@ constexpr int kPromptThreads = 512;
 constexpr int kPromptUnits = 4;      // units known at a time
 // 512 threads of 128 registers at launch: 2 x 200 + 2 x 56 = 4 x 128.
 constexpr int kPromptSoftmaxRegs = 200, kPromptOtherRegs = 56;
-constexpr float kPromptExact = 1048576.0f;  // scores up to it are scaled in one operation with the subtraction
+// Scores (of which the reference) up to which they are scaled in one operation with the subtraction.
+constexpr float kPromptExact = 1048576.0f;
 constexpr float kPromptSlack = 8.0f;  // log2 of how far a maximum may outgrow the reference
 
 template <int D>
@@ -55,8 +56,8 @@ struct PromptShape {
   static constexpr int SMEM_BYTES = 1024 + 2 * Q_HALF + STAGES * TILE + 8 * OUT_BYTES;
 };
 
-// tanh of two values times `k` / (2 log2(e)): 1 - 2 / (1 + 2^(k x)). The error is absolute,
-// 2^-21 or so, which is what a score that it is multiplied into needs.
+// tanh of two values times `k` / (2 log2(e)): 1 - 2 / (1 + 2^(k x)). The error is absolute, 2^-21
+// or so, whatever the value.
 __device__ __forceinline__ uint64_t tanh2(uint64_t x, uint64_t k) {
   float a, b;
   unpack2(mul2(x, k), a, b);
@@ -64,15 +65,33 @@ __device__ __forceinline__ uint64_t tanh2(uint64_t x, uint64_t k) {
   b = reciprocal(1.0f + exp2_ftz(b));
   return fma2(pack2(a, b), pack2(-2.0f, -2.0f), pack2(1.0f, 1.0f));
 }
-// For |y| <= kTanhSmall tanh(y) = y (c0 + c1 y^2 + .. + c4 y^8) to 2^-20.6 of itself, for |y| <=
-// kTanhTiny y (t0 + t1 y^2 + t2 y^4) to 2^-17.3: the polynomials of least largest relative error,
-// by linear programming over 2000 points. They need no exponential and no reciprocal, whose unit
-// the softmax's own exponentials keep busy.
-constexpr float kTanhSmall = 0.75f;
-constexpr float kTanh0 = 0.999999463558197f, kTanh1 = -0.3332850933074951f, kTanh2 = 0.13261185586452484f,
-                kTanh3 = -0.05011745169758797f, kTanh4 = 0.012983138673007488f;
+// tanh of two values to 2^-20 of itself: by the polynomial up to kTanhSmall, and as above beyond.
+__device__ __forceinline__ uint64_t tanh2_relative(uint64_t y) {
+  const uint64_t z = mul2(y, y), t = tanh2(y, pack2(2.0f * 1.44269504f, 2.0f * 1.44269504f));
+  uint64_t r = fma2(z, pack2(kTanh4, kTanh4), pack2(kTanh3, kTanh3));
+  r = fma2(r, z, pack2(kTanh2, kTanh2));
+  r = fma2(r, z, pack2(kTanh1, kTanh1));
+  r = mul2(fma2(r, z, pack2(kTanh0, kTanh0)), y);
+  float ya, yb, ta, tb, ra, rb;
+  unpack2(y, ya, yb);
+  unpack2(t, ta, tb);
+  unpack2(r, ra, rb);
+  return pack2(fabsf(ya) <= kTanhSmall ? ra : ta, fabsf(yb) <= kTanhSmall ? rb : tb);
+}
+// For |y| <= kTanhTiny tanh(y) = y (t0 + t1 y^2 + t2 y^4) to 2^-17.3 of itself. This polynomial and
+// the longer one need no exponential and no reciprocal, whose unit the softmax's own exponentials
+// keep busy.
 constexpr float kTanhTiny = 0.4f;
 constexpr float kTiny0 = 0.9999939203262329f, kTiny1 = -0.3326335847377777f, kTiny2 = 0.12132595479488373f;
+// How scores are capped. kNear: the polynomials are of products as they come, their coefficients
+// holding up to the eighth power of scale / cap, which has to be a normal number; scores of which
+// some reach the cap go through tanh2, whose 2^-21 of the cap is 2^-14 of the exponent at most.
+// kWide, any cap: products are scaled first, and such scores go through tanh2_relative, as 2^-21
+// of a large cap would be more than the scores far below it (0.7 at 10^6). A prompt of 16 384 tokens
+// (32 / 8 heads of 128): 1700 us near and 1890 wide, and where scores reach the cap 2740 and 3500.
+enum class Cap { kNone, kNear, kWide };
+constexpr float kNearFrom = 6.103515625e-5f, kNearTo = 16384.0f;  // scale / cap
+constexpr float kNearCap = 128.0f;                                // cap log2(e)
 
 // A unit of work: up to 256 rows of one (sequence, KV head) over one partition.
 struct PromptUnit {
@@ -89,12 +108,14 @@ struct PromptUnit {
   __device__ __forceinline__ int halves() const { return rows > 128 ? 2 : 1; }
 };
 
-template <int D, bool CAP, bool SLOPES>
+template <int D, Cap CAP, bool SLOPES>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     attn_prompt_kernel(ExtendParams p, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap) {
   using S = PromptShape<D>;
   constexpr int ST = S::STAGES;
+  constexpr bool CAPPED = CAP != Cap::kNone;
+  constexpr bool EXACT = CAP != Cap::kNear && !SLOPES;  // scores may be too large for the shorter way
   launch_dependents();  // the merge may be scheduled as this grid drains
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = p.group;
   extern __shared__ uint8_t smem_raw[];
@@ -465,8 +486,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
     // In the exponent's scale. At least the smallest normal number: a scale of 0 must not
     // turn the -inf of what is masked into NaN.
-    const float fac = fmaxf(fabsf(p.factor), 1.17549435e-38f);
-    const float sl = SLOPES ? 1.0f : (CAP ? p.cap_log2 : fac);
+    const float fac0 = fmaxf(fabsf(p.factor), 1.17549435e-38f), fac = CAP == Cap::kWide ? 1.0f : fac0;
+    const float sl = SLOPES ? 1.0f : (CAPPED ? p.cap_log2 : fac);
     // The polynomial of a product, in the exponent's scale.
     const float f1 = p.cap_log2 * fac, ff = fac * fac;
     const float tc[5] = {kTanh0 * f1, kTanh1 * f1 * ff, kTanh2 * f1 * ff * ff, kTanh3 * f1 * ff * ff * ff,
@@ -490,6 +511,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (SLOPES) slope = __ldg(p.slopes + unit.kvh * G + (unit.r0 + tid) % G) * 1.44269504f;
       }
       float ref = -INFINITY, l = 0.0f;  // the exponent's reference (scaled scores), the sum
+      bool exact = false;               // a reference of the warp's is above kPromptExact
       for (int j = 0; j < nt; ++j, ++n) {
         const int t0 = start + j * kPromptTile;
         const bool careful = unit.careful(j);
@@ -532,17 +554,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           // reference where no bias comes between; others by exponentials, in place.
           float most = 0.0f;  // the largest magnitude
           bool poly = false, tiny = false;
-          if (CAP) {
+          if (CAPPED) {
             // Of what is seen, by rows that there are: the others hold what units before have left,
             // which differs from call to call, and must not choose the way of a result.
+            if (CAP == Cap::kWide)
+#pragma unroll
+              for (int i = 0; i < 64; ++i) set_pair(i, mul2(pair(i), pack2(fac0, fac0)));
             if (careful) hide(0);
             most = tid < rows ? largest([](float v) { return fabsf(v); }) : 0.0f;
-            poly = __all_sync(0xffffffffu, most * fac <= kTanhSmall);
-            tiny = !SLOPES && __all_sync(0xffffffffu, most * fac <= kTanhTiny);
+            poly = __all_sync(0xffffffffu, most * fac <= kTanhSmall && (CAP == Cap::kNear || most * f1 <= kPromptExact));
+            tiny = !SLOPES && __all_sync(0xffffffffu, most * fac <= kTanhTiny) && poly;
             if (!poly) {
               const uint64_t k2 = pack2(2.0f * 1.44269504f * fac, 2.0f * 1.44269504f * fac);
 #pragma unroll
-              for (int i = 0; i < 64; ++i) set_pair(i, tanh2(pair(i), k2));
+              for (int i = 0; i < 64; ++i) set_pair(i, CAP == Cap::kNear ? tanh2(pair(i), k2) : tanh2_relative(pair(i)));
             }
           }
           // The polynomials' sums without the last factor.
@@ -558,17 +583,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             return fma2(fma2(z, pack2(tt[2], tt[2]), pack2(tt[1], tt[1])), z, pack2(tt[0], tt[0]));
           };
           if (SLOPES) {
-            const float d0 = float(t0 - x.pos), f = CAP ? p.cap_log2 : fac;
+            const float d0 = float(t0 - x.pos), f = CAPPED ? p.cap_log2 : fac;
             const uint64_t f2 = pack2(f, f), m2 = pack2(-slope, -slope);
 #pragma unroll
             for (int i = 0; i < 64; ++i) {
               const uint64_t away =
                   add2(pack2(d0, d0), pack2(float(2 * i), float(2 * i + 1))) & 0x7fffffff7fffffffull;
-              set_pair(i, fma2(away, m2, CAP && poly ? mul2(capped(i), pair(i)) : mul2(pair(i), f2)));
+              set_pair(i, fma2(away, m2, CAPPED && poly ? mul2(capped(i), pair(i)) : mul2(pair(i), f2)));
             }
           }
           float sl_now = sl;
-          if (CAP && !SLOPES && poly && careful) {  // ahead of the mask, whose -inf is no factor of a polynomial
+          if (CAPPED && !SLOPES && poly && careful) {  // ahead of the mask, whose -inf is no factor of a polynomial
 #pragma unroll
             for (int i = 0; i < 64; ++i) set_pair(i, mul2(capped(i), pair(i)));
             sl_now = 1.0f;
@@ -576,31 +601,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
           if (careful) hide(0xff800000u);  // -inf
           float mx;
-          if (CAP && !SLOPES && poly && __all_sync(0xffffffffu, most * f1 <= 30.0f)) {
+          if (CAPPED && !SLOPES && poly && __all_sync(0xffffffffu, most * f1 <= 30.0f)) {
             // Every score is seen and between -30 and 30 in the exponent, so the largest magnitude
             // serves as a reference: no weight that counts is below 2^-60, and a search for
             // the maximum is saved.
             mx = most * f1;
           } else {
             mx = largest([](float v) { return v; });
-            if (CAP && !SLOPES && poly) {
+            if (CAPPED && !SLOPES && poly) {
               const float z = mx * mx;
               mx = mx == -INFINITY ? mx : mx * fmaf(fmaf(fmaf(fmaf(tc[4], z, tc[3]), z, tc[2]), z, tc[1]), z, tc[0]);
             } else {
               mx = mx == -INFINITY ? mx : mx * sl_now;
             }
           }
-          if (!SLOPES && !poly && __any_sync(0xffffffffu, tid < rows && fabsf(mx) > kPromptExact && mx > -INFINITY)) {
-            // The weights' multiply-add takes the reference, a rounded product, from exact ones: of scores
-            // of 2^31 the difference of a score from itself would be some 2^7 and its weight infinite.
-#pragma unroll
-            for (int i = 0; i < 64; ++i) set_pair(i, mul2(pair(i), pack2(sl_now, sl_now)));
-            sl_now = 1.0f;
-          }
           const bool move = mx > ref + kPromptSlack;
           if (__any_sync(0xffffffffu, move)) {
             const float f = move ? exp2_ftz(ref - mx) : 1.0f;
             if (move) ref = mx;
+            if (EXACT) exact = exact || __any_sync(0xffffffffu, tid < rows && move && fabsf(mx) > kPromptExact);
             l *= f;
             if (j > 0) {  // these scores came after the products of the tile before
               const uint64_t f2 = pack2(f, f);
@@ -619,6 +638,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 tmem_store32(t_o(h) + lane_base + 32 * ch, o);
               }
             }
+          }
+          if (EXACT && !poly && __builtin_expect(exact, 0)) {
+            // The weights' multiply-add takes the reference, a rounded product, from exact ones: of scores
+            // of 2^31 the difference of a score from itself would be some 2^7 and its weight infinite.
+#pragma unroll
+            for (int i = 0; i < 64; ++i) set_pair(i, mul2(pair(i), pack2(sl_now, sl_now)));
+            sl_now = 1.0f;
           }
           const float m = ref == -INFINITY ? 0.0f : ref;  // nothing seen so far: every weight is 0
           const uint64_t sl2 = pack2(sl_now, sl_now), m2 = pack2(-m, -m);
@@ -641,9 +667,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               tmem_store16(t_s(h) + lane_base + 16 * e, w);
             }
           };
-          if (CAP && !SLOPES && tiny)
+          if (CAPPED && !SLOPES && tiny)
             weights([&](int i) { return fma2(capped_tiny(i), pair(i), m2); });
-          else if (CAP && !SLOPES && poly)
+          else if (CAPPED && !SLOPES && poly)
             weights([&](int i) { return fma2(capped(i), pair(i), m2); });
           else
             weights([&](int i) { return fma2(pair(i), sl2, m2); });
@@ -761,7 +787,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
 }
 
-template <int D, bool CAP, bool SLOPES>
+template <int D, Cap CAP, bool SLOPES>
 pk_status launch_prompt_as(const ExtendParams &p, const pk_cache_desc &d, unsigned units, cudaStream_t stream) {
   CUtensorMap kmap, vmap;
   if (!encode_bf16_pool(&kmap, p.k_cache, d) || !encode_bf16_pool(&vmap, p.v_cache, d)) return PK_ERR_CUDA;
@@ -772,13 +798,19 @@ pk_status launch_prompt_as(const ExtendParams &p, const pk_cache_desc &d, unsign
   return cudaGetLastError() == cudaSuccess ? PK_OK : PK_ERR_CUDA;
 }
 
+template <int D, Cap CAP>
+pk_status launch_prompt_as(const ExtendParams &p, const pk_cache_desc &d, unsigned units, cudaStream_t stream) {
+  return p.slopes ? launch_prompt_as<D, CAP, true>(p, d, units, stream)
+                  : launch_prompt_as<D, CAP, false>(p, d, units, stream);
+}
+
 template <int D>
 pk_status launch_prompt(const ExtendParams &p, const pk_cache_desc &d, unsigned units, cudaStream_t stream) {
-  if (p.cap_log2 != 0.0f)
-    return p.slopes ? launch_prompt_as<D, true, true>(p, d, units, stream)
-                    : launch_prompt_as<D, true, false>(p, d, units, stream);
-  return p.slopes ? launch_prompt_as<D, false, true>(p, d, units, stream)
-                  : launch_prompt_as<D, false, false>(p, d, units, stream);
+  if (p.cap_log2 == 0.0f) return launch_prompt_as<D, Cap::kNone>(p, d, units, stream);
+  const float f = fabsf(p.factor);
+  return f >= kNearFrom && f <= kNearTo && p.cap_log2 <= kNearCap
+             ? launch_prompt_as<D, Cap::kNear>(p, d, units, stream)
+             : launch_prompt_as<D, Cap::kWide>(p, d, units, stream);
 }
 
 }  // namespace

@@ -1,4 +1,7 @@
-"""Edges of the block manager's cut on the CPU: batches of appends after cuts and commits."""
+"""Edges of the block manager's cut on the CPU (batches of appends after cuts and commits), and refusals
+before a launch."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -135,3 +138,24 @@ def test_batches_among_cuts_and_commits_in_a_pool_that_evicts(seed):
             table = bm.table(s)
             assert [cells[table[i // B] * B + i % B] for i in range(len(toks))] == toks
     assert copied > 50
+
+
+def test_extend_refuses_caps_beyond_what_fp32_can_hold():
+    L = pk.lib()
+    buf = np.zeros(1 << 16, np.uint8)
+    p = (buf.ctypes.data + 255) // 256 * 256
+    desc = pk.CacheDesc(64, 16, 2, 128, pk.PK_BF16)
+
+    def call(cap, scale=0.1, R=0):
+        sc = pk.ScoreDesc(cap, 0, None, None, None)
+        return L.pk_paged_attention_extend(p, p, p, p, p, p, p, scale, ctypes.byref(sc), 2, R, 3, 8, 4, 64, 0, None, 0,
+                                           None, 0, ctypes.byref(desc), None)
+
+    for cap, scale in ((2.0 ** 99, 1.0), (2.0 ** 100, 1.0), (2.0 ** -100, 1.0), (1e6, 0.0), (30.0, -0.1), (2.0 ** -50, 2.0 ** 50),
+                       (0.0, 1e-38), (-0.0, 0.1)):
+        assert call(cap, scale) == pk.PK_OK, (cap, scale)  # (no rows, so nothing is launched)
+    for cap, scale in ((2.0 ** 101, 1.0), (3.4e38, 0.1), (2.0 ** -101, 2.0 ** -101), (2.0 ** 60, 2.0 ** -41),
+                       (2.0 ** -60, 2.0 ** 41), (1e30, 0.1), (1e-40, 0.1), (-1.0, 0.1), (float("nan"), 0.1),
+                       (float("inf"), 0.1), (1.0, float("inf"))):
+        for R in (0, 4):
+            assert call(cap, scale, R) == pk.PK_ERR_INVALID_ARG, (cap, scale)

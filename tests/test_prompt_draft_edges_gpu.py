@@ -93,12 +93,13 @@ def test_extend_few_rows_clear_hidden_values_in_places_that_are_filled_again(hq,
             assert not bool(torch.isfinite(out[::2]).any())
 
 
-def dense(q, k, v, tables, lens, counts, ofs, scale, sc, rho, T):
+def dense(q, k, v, tables, lens, counts, ofs, scale, sc, rho, T, A=0.0):
     """The definition in fp64 on the GPU, a sequence and head at a time, and its bound: the general tests'
     with the cap's error relative to the capped score, not to the cap,
-    e_t = D m_t + (T + 6 u) (|x_t| + |capped x_t| + |bias_t|) log2(e),
+    e_t = D m_t + (T + 6 u) (|x_t| + |capped x_t| + |bias_t|) log2(e) + A cap log2(e),
     T being tanh's own relative error: 2^-22 of tanhf, 2^-17 of bf16's (2^-17.3 of the shortest polynomial,
-    2^-20.6 of the longer one; an exponential and a reciprocal are off by 2^-21 where tanh is above 0.6);
+    2^-20.6 of the longer one; an exponential and a reciprocal are off by 2^-21 where tanh is above 0.6),
+    A that of prompts of bf16 with caps of at most 88, 2^-21 (the exponential alone);
     six roundings: the product by its factor, the tanh's argument, by the cap, bias twice, the maximum's.
     Where e_t is above 1/2 for a token seen, exp is no longer close to linear and the bound is the values' range."""
     R, hq, d = q.shape
@@ -123,7 +124,7 @@ def dense(q, k, v, tables, lens, counts, ofs, scale, sc, rho, T):
                 far = (pos - t).abs() * float(sc["slopes"][h])
                 x, a = x - far, a + far
             w = torch.softmax(x.masked_fill(~see, -float("inf")), 1).nan_to_num(0.0)
-            e = D * m + (T + 6 * U) * a * log2e
+            e = D * m + ((T + 6 * U) * a + A * cap) * log2e
             o, we = w @ vh, w * e
             x = 2 * ops.LN2 * (we @ vh.abs() + o.abs() * we.sum(1, keepdim=True)) + (
                 16 * U + 2 * rho + 4 * U * n) * (w @ vh.abs()) + eta * o.abs() + 1e-30
@@ -165,6 +166,26 @@ def test_extend_scores_far_above_one(path, scale, kind):
     for part in (0, 4 * B):
         out = ops.run_extend((tables, k, v, ofs, q, sc), lens, counts, scale, part)
         check_dense(out, q, k, v, tables, lens, counts, ofs, scale, sc, RHO[path], 2.0 ** -17)
+
+
+@pytest.mark.parametrize("path", sorted(PATHS))
+@pytest.mark.parametrize("cap", [2.0 ** -90, 1e-8, 1e-4, 0.5, 20.0, 80.0, 100.0, 1e3, 1e4, 1e6, 1e20])
+@pytest.mark.parametrize("kind", ["plain", "slopes", "window"])
+def test_extend_cap_of_every_size(path, cap, kind):
+    """A cap far above the scores changes nothing, whatever its size, in rows whose neighbours' scores reach it
+    too; one far below them leaves nearly equal weights."""
+    dtype, B, counts, lens = PATHS[path]
+    hq, hk, d = 4, 2, 128
+    rng = np.random.default_rng(len(path) + len(kind))
+    tables, k, v, ofs, q, sc = ops.make_case(rng, counts, lens, B, hq, hk, d, ops.DTYPES[dtype], kind)
+    sc["softcap"] = cap
+    T = 2.0 ** -22 if dtype == "f32" else 2.0 ** -17
+    for big in (1.0, max(1.0, cap / 2)):
+        x = q.clone()
+        x[1::7, 1] *= big  # scores of some rows of a head beyond the cap, among others
+        out = ops.run_extend((tables, k, v, ofs, x, sc), lens, counts, d ** -0.5)
+        check_dense(out, x, k, v, tables, lens, counts, ofs, d ** -0.5, sc, RHO[path], T,
+                    2.0 ** -21 if path == "prompt" and cap <= 88 else 0.0)
 
 
 # ---------------------------------------------------------------------------
