@@ -651,8 +651,9 @@ size_t pk_extend_workspace_size(int32_t num_q_tokens, int32_t num_q_heads, int32
  * tokens, or from max(p - draft_probs[i], 0) of the refused draft i, or from p if none
  * was refused or those weights are all 0. It is the lowest k whose weights up to and
  * including k are more than r times all of them, r = uniforms[the root's row]. Sums and
- * products are exact to 2^-45; probabilities that are not positive and finite count
- * as 0.
+ * products are off by less than 2^-43 of the row's whole weight (2^-47 as a rule), which
+ * has to lie between 2^-90 and 2^127; probabilities that are not positive and finite
+ * count as 0.
  *   num_accepted  int32 [S], accepted drafts (without the root).
  *   accepted      int32 [num_rows]: at q_offsets[s] + k the k-th row of the path,
  *                 counted from the sequence's first (0 is the root), -1 behind it.

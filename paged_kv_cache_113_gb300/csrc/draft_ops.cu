@@ -40,10 +40,12 @@ struct VerifyParams {
 // A probability as it counts: what is not a positive finite number is 0.
 __device__ __forceinline__ float weight(float x) { return x > 0.0f && x <= 3.402823466e38f ? x : 0.0f; }
 
-// A number in two floats, hi + lo, exact to 2^-45 or so of itself: the error of each addition
-// is kept (Knuth's two-sum). Sums, products and comparisons go this way because of 64-bit
-// operations this chip does two a clock and SM (with those, and sums in one pass over each
-// thread's part, 256 chains of 8 drafts took 59 us; now 29).
+// A number in two floats, hi + lo: the error of each addition is kept (Knuth's two-sum). The sum
+// of the errors is rounded itself, by more the longer it is not brought in order: of 32 768 values
+// 2^-34 of their sum in bad cases. So a thread sums 64 values at a time and adds those sums, in
+// order each time: 2^-44 at worst, 2^-47 as a rule. Sums, products and comparisons go this way
+// because of 64-bit operations this chip does two a clock and SM (with those, and sums in one
+// pass over each thread's part, 256 chains of 8 drafts took 59 us; now 29).
 struct Pair {
   float hi = 0.0f, lo = 0.0f;
   __device__ __forceinline__ void add(float x, float err) {
@@ -52,6 +54,12 @@ struct Pair {
     hi = t;
   }
   __device__ __forceinline__ void add(const Pair &x) { add(x.hi, x.lo); }
+  // In order: lo is at most half a unit in hi's last place.
+  __device__ __forceinline__ void settle() {
+    const float t = __fadd_rn(hi, lo);
+    lo = __fsub_rn(lo, __fsub_rn(t, hi));
+    hi = t;
+  }
   __device__ __forceinline__ void sub(const Pair &x) { add(-x.hi, -x.lo); }
   __device__ __forceinline__ Pair times(float f) const {
     const float h = __fmul_rn(hi, f);
@@ -240,12 +248,18 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_drafts_kernel(Verify
   auto sum_of = [&](int from, int to) {
     own(from, to);
     Pair sum;
-    w.each(from + lane, to, 32, [&](int, float x, float err) {
-      sum.add(x, err);
-      return true;
-    });
+    for (int g = from; g < to; g += 32 * 16) {  // 64 values a lane
+      Pair part;
+      w.each(g + lane, min(g + 32 * 16, to), 32, [&](int, float x, float err) {
+        part.add(x, err);
+        return true;
+      });
+      sum.add(part);
+      sum.settle();
+    }
 #pragma unroll
     for (int off = 16; off; off >>= 1) sum.add(sum.shuffled_xor(off));
+    sum.settle();
     return sum;
   };
   Pair total;
@@ -334,6 +348,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_drafts_kernel(Verify
     }
     if (some) at = __shfl_sync(0xffffffffu, last, 31 - __clz(some));
     run = Pair{__shfl_sync(0xffffffffu, incl.hi, 31), __shfl_sync(0xffffffffu, incl.lo, 31)};
+    run.settle();
   }
   if (lane == 0) a.next_tokens[s] = at;  // (the last with anything, should rounding leave none)
 }

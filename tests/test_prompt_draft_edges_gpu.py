@@ -1,5 +1,7 @@
 """Edges of prompt attention, draft verification and cache compaction on the GPU: what the calls are
 followed by, sizes and values at the ends of their ranges, and bounds tighter than those of the general tests."""
+import math
+
 import numpy as np
 import pytest
 
@@ -218,3 +220,41 @@ def test_verify_by_several_ctas_a_sequence_again_and_again(mask, V):
         if of is bad:
             assert pk.pk_get_device_error()[0] == 8
             pk.pk_get_device_error()
+
+
+def test_verify_draws_by_sums_of_long_rows():
+    """Rows of 2^24 values, which a CTA sums alone (of 160 sequences): 32 768 values a thread. The first half are
+    2^-24 each, whose sums are exact; in the second half all threads have the same values, of which float pairs
+    that are not brought in order as they grow lose 2^-34. The whole is 1 + 2^-39, or 1 - 2^-39, so r times
+    the whole lies just above a border of the first half, or below: next to none with an error above 2^-39."""
+    V, S, n = 1 << 24, 160, 1 << 15
+    y = np.random.default_rng(76).random(n)
+    y = y * y
+    y = y * y
+    x = (y / (math.fsum(y.tolist()) * 512)).astype(np.float32)
+    # A thread's values: four neighbours of every 128, of its warp's sixteenth.
+    second = torch.from_numpy(x).to(DEV).view(1, n // 4, 1, 4).expand(8, n // 4, 32, 4).reshape(-1)
+    first = torch.full((V // 2,), 2.0 ** -24, device=DEV)
+    rest = 256 * math.fsum(x.tolist()) - 0.5
+    k = np.random.default_rng(1).integers(V // 10, V // 2 - V // 16, S)  # r = k 2^-24
+    u = (k * 2.0 ** -24).astype(np.float32)
+    ofs, tokens = np.arange(S + 1, dtype=np.int32), np.zeros(S, np.int64)
+    target = torch.empty((S, V), device=DEV)
+    for more in (2.0 ** -39, -(2.0 ** -39)):
+        first[-1] = 2.0 ** -24 - rest + more
+        assert abs(math.fsum(x.tolist()) * 256 + (V // 2 - 1) * 2.0 ** -24 + float(first[-1]) - 1 - more) < 2.0 ** -46
+        target.copy_(torch.cat([first, second]))
+        na, ac, nt = ops.run_verify(ofs, target, tokens, u, None, None, most=1)
+        # The tokens up to k - 1 weigh r: more than r times the whole, or the next is needed.
+        assert nt.tolist() == (k if more > 0 else k - 1).tolist()
+        assert na.tolist() == [0] * S and ac.tolist() == [0] * S
+
+
+@pytest.mark.parametrize("shift", [-88, -40, 40, 126])
+def test_verify_draws_by_weights_of_any_whole(shift):
+    """The next token goes by shares: rows scaled by a power of two draw the same ones."""
+    rng = np.random.default_rng(shift + 100)
+    ofs, target, tokens, u, _, _ = ops.make_drafts(rng, [1] * 40, 5000, torch.float32, "greedy", pad=0)
+    want = ops.run_verify(ofs, target, tokens, u, None, None, most=1)[2]
+    assert int(want.min()) >= 0
+    assert torch.equal(ops.run_verify(ofs, target * 2.0 ** shift, tokens, u, None, None, most=1)[2], want)
