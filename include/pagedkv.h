@@ -602,8 +602,9 @@ typedef struct {
  *   scores        NULL: plain causal attention. softcap: 0 or within its bounds.
  *   partition_size, work_items  0 and NULL: each context whole; otherwise
  *                 pk_extend_plan's for the same max_query_len (work_items NULL: all
- *                 units and partitions). An item that is no unit of the call's is
- *                 skipped and recorded (PK_DEVERR_ORDER).
+ *                 units and partitions). An item that is no unit of the call's, one
+ *                 behind its sequence's rows too, is skipped and recorded
+ *                 (PK_DEVERR_ORDER); a partition behind the end of a context has nothing to do.
  *   workspace     pk_extend_workspace_size bytes when the contexts are split.
  * dtype PK_F32 or PK_BF16, head_dim 64 or 128, Hq / Hk at most 8. Bad table entries
  * are recorded (PK_DEVERR_BLOCK_ID). */

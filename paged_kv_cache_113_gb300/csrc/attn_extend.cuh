@@ -119,7 +119,12 @@ __device__ __forceinline__ bool extend_unit(const ExtendParams &p, int cta, int 
   }
   u.sr = seq_rows(p, u.s, record);
   u.rows = int(min(int64_t(u.rows), int64_t(u.sr.n) * p.group - u.r0));
-  if (u.rows <= 0) return false;
+  if (u.rows <= 0) {
+    // An item behind its sequence's rows (of a sequence whose offsets are bad that is recorded).
+    if (p.items && record && (u.sr.n > 0 || __ldg(p.q_offsets + u.s) == __ldg(p.q_offsets + u.s + 1)))
+      record_error(&g_rows_error, PK_DEVERR_ORDER, y);
+    return false;
+  }
   u.void_rows = u.sr.ctx == 0;  // of a split call, the merge writes them
   if (u.void_rows) return p.num_partitions == 1;
   return true;

@@ -190,6 +190,33 @@ def test_extend_cap_of_every_size(path, cap, kind):
                     2.0 ** -21 if path == "prompt" and cap <= 88 else 0.0)
 
 
+@pytest.mark.parametrize("dtype,counts", [("bf16", [20, 3, 0, 9]), ("f32", [20, 3, 0, 9]), ("bf16", [1, 1, 0, 1])])
+def test_extend_items_behind_their_sequences_rows_are_recorded(dtype, counts):
+    """A first row at or past the sequence's rows, or any of a sequence without rows; the others are done."""
+    rng = np.random.default_rng(70)
+    lens, B, hq = [50, 33, 12, 40], 16, 4
+    tables, k, v, ofs, q, sc = ops.make_case(rng, counts, lens, B, hq, 2, 64, ops.DTYPES[dtype], "plain")
+    want = ops.run_extend((tables, k, v, ofs, q, sc), lens, counts, 0.125)
+    part, items = pk.pk_extend_plan(lens, counts, hq, pk.cache_desc(k), 0)
+
+    def call(extra, ofs=ofs):
+        out = torch.full_like(q, 7.0)
+        it = np.concatenate([items, np.array(extra, np.int32).reshape(-1, 4)])
+        pk.pk_paged_attention_extend(out, q, k, v, ops.i32(tables), ops.i32(lens), ops.i32(ofs), 0.125, max(counts), 50,
+                                     work_items=torch.from_numpy(it).to(DEV))
+        return out, pk.pk_get_device_error()
+
+    out, err = call([])
+    assert err == (0, 0) and torch.equal(out, want)
+    for s, r0 in ((0, 2 * counts[0]), (1, 2 * counts[1] + 5), (3, 2 ** 31 - 1), (2, 0), (2, 4)):
+        out, err = call([s, r0, 2, 0])
+        assert err == (6, len(items)) and torch.equal(out, want), (s, r0)
+    # Bad offsets stay what is recorded.
+    bad = ofs.copy()
+    bad[1] = 1000
+    assert call([], bad)[1][0] == 8
+
+
 # ---------------------------------------------------------------------------
 # Verification
 # ---------------------------------------------------------------------------
