@@ -217,6 +217,48 @@ def test_extend_items_behind_their_sequences_rows_are_recorded(dtype, counts):
     assert call([], bad)[1][0] == 8
 
 
+@pytest.mark.parametrize("path", ["few", "few of two tokens", "other blocks", "prompt", "f32"])
+@pytest.mark.parametrize("part", [0, 96])
+def test_extend_weights_have_the_bits_that_are_promised(path, part):
+    """Weights whose roundings to one bf16 are as large as they get and of opposite sign, under values that nearly
+    cancel: every 16 tokens hold two of score 0 and value 0, the others in turn weights a little above 0.501953,
+    the middle of two bf16 (value 1, rounded up by 2^-8.1), and a little below (value -1, rounded down as much).
+    |error| <= (2 rho + 16 u + 4 u T) W + 4 ln2 e + eta |out| as in the general tests, W = sum w |v| / sum w < 1,
+    with scores that are exact but for factor and exponential: e <= 6 u |x|, |x| <= 1. One bf16 is off by
+    2^-9, a pair must be by less than 2^-12; of prompts of bf16 one bf16 is promised."""
+    dtype, B, n = {"few": ("bf16", 16, 1), "few of two tokens": ("bf16", 8, 2), "other blocks": ("bf16", 12, 30),
+                   "prompt": ("bf16", 16, 60), "f32": ("f32", 16, 3)}[path]
+    rho = {"prompt": 2.0 ** -8, "f32": U}.get(path, 2.0 ** -17)
+    dt, d, T = ops.DTYPES[dtype], 64, 480
+    x = np.where(np.arange(T) % 2 == 0, -1000.0, -1001.0)
+    x[::16] = x[1::16] = 0.0
+    scale = 0.9939 * math.log(2.0) / 1000
+    keys, vals = np.zeros((T, 1, d)), np.zeros((T, 1, d))
+    keys[:, 0, :4], keys[:, 0, 4] = (np.trunc(x / 8) * 2)[:, None], x - np.trunc(x / 8) * 8
+    vals[:, 0] = np.where(x == 0.0, 0.0, np.where(x == -1000.0, 1.0, -1.0))[:, None]
+    assert (torch.from_numpy(keys).to(dt).double().numpy() == keys).all() and (keys.sum(2)[:, 0] == x).all()
+    N = -(-T // B)
+    pools = []
+    for y in (keys, vals):
+        pool = np.zeros((N * B, 1, d))
+        pool[:T] = y
+        pools.append(torch.from_numpy(pool.reshape(N, B, 1, d)).to(DEV).to(dt))
+    q = torch.ones((n, 2, d), dtype=dt, device=DEV)
+    tables, ofs = np.arange(N, dtype=np.int32)[None], np.array([0, n], np.int32)
+    out = ops.run_extend((tables, *pools, ofs, q, {"softcap": 0.0, "window": 0}), [T], [n], scale, part)
+    for i in range(n):
+        see = np.arange(T - n + i + 1)
+        w = np.exp(x[see] * scale)
+        want = w @ vals[see, 0, 0] / w.sum()
+        W = w @ np.abs(vals[see, 0, 0]) / w.sum()
+        tol = (2 * rho + 16 * U + 4 * U * T) * W + 4 * ops.LN2 * 6 * U + ops.ETA[dt] * abs(want)
+        got = ops.f64(out[i])
+        assert (np.abs(got - want) <= tol).all(), (i, got[0, 0], want, tol)
+        if rho == 2.0 ** -17:  # (weights of one bf16 would not pass)
+            short = torch.from_numpy(w).bfloat16().double().numpy()
+            assert abs(short @ vals[see, 0, 0] / w.sum() - want) > 4 * tol
+
+
 # ---------------------------------------------------------------------------
 # Verification
 # ---------------------------------------------------------------------------
@@ -285,3 +327,38 @@ def test_verify_draws_by_weights_of_any_whole(shift):
     want = ops.run_verify(ofs, target, tokens, u, None, None, most=1)[2]
     assert int(want.min()) >= 0
     assert torch.equal(ops.run_verify(ofs, target * 2.0 ** shift, tokens, u, None, None, most=1)[2], want)
+
+
+@pytest.mark.parametrize("kind", ["siblings", "siblings of one token", "two levels", "chain"])
+def test_verify_distribution_of_trees(kind):
+    """Over many draws what greedy drafts and the drawn token come to is distributed as the target's samples: the
+    first new token, and of those that went on the second, within five standard deviations."""
+    rng = np.random.default_rng(len(kind))
+    V, S = 6, 30000
+    p0, p1, p2 = rng.dirichlet(np.ones(V), 3)
+    a, b, c = np.argsort(-p0)[:3]
+    # Rows: the root and its nodes; each row's target is the distribution after its token.
+    parents, toks, rows = {
+        "siblings": ([0, 0, 0, 0], [0, a, b, c], [p0, p1, p2, p1]),
+        "siblings of one token": ([0, 0, 0, 0], [0, a, a, b], [p0, p1, p1, p2]),
+        "two levels": ([0, 0, 0, 1, 1, 2], [0, a, b, 0, 1, 2], [p0, p1, p2, p1, p2, p0]),
+        "chain": (None, [0, a, 3], [p0, p1, p2]),
+    }[kind]
+    n = len(toks)
+    target = torch.from_numpy(np.tile(np.array(rows), (S, 1)).astype(np.float32)).to(DEV)
+    u = np.minimum(rng.random(n * S).astype(np.float32), np.float32(1 - 2.0 ** -24))
+    ofs = np.arange(0, n * S + 1, n).astype(np.int32)
+    na, ac, nt = (x.cpu().numpy() for x in ops.run_verify(ofs, target, np.tile(toks, S).astype(np.int64), u, None if parents is None else np.tile(
+        parents, S).astype(np.int32), None, most=n))
+    ac = ac.reshape(S, n)
+    toks = np.array(toks)
+
+    def close(drawn, p):
+        f = np.bincount(drawn, minlength=V) / len(drawn)
+        assert (np.abs(f - p) <= 5 * np.sqrt(p * (1 - p) / len(drawn)) + 1e-6).all(), (f, p)
+
+    close(np.where(na >= 1, toks[ac[:, 1]], nt), p0)
+    for node in range(1, n):  # behind a kept node
+        on = (na >= 1) & (ac[:, 1] == node)
+        if on.sum() > 1000:
+            close(np.where(na[on] >= 2, toks[ac[on, 2 % n]], nt[on]), rows[node])
