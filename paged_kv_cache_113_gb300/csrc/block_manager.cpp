@@ -149,15 +149,24 @@ struct pk_bm {
     return b;
   }
 
-  // A table stops naming block b.
-  void release(int32_t b) {
-    if (--refs[b] != 0) return;
+  // Block b, which no table names any more, can be taken again. Where there is no memory to keep
+  // it by, a cached block leaves the cache (the free list has room for every block).
+  void retire(int32_t b) {
     if (entry[b].cached) {
       entry[b].released = clock;
-      idle.insert(idle_key(b));
-    } else {
-      free_stack.push_back(b);
+      try {
+        idle.insert(idle_key(b));
+        return;
+      } catch (const std::bad_alloc &) {
+        uncache(b);
+      }
     }
+    free_stack.push_back(b);
+  }
+
+  // A table stops naming block b.
+  void release(int32_t b) {
+    if (--refs[b] == 0) retire(b);
   }
 
   // The cached block holding the prefix whose last block is tok[0, B) at
@@ -207,10 +216,7 @@ struct pk_bm {
   void give_copied_back() {
     if (copied.empty()) return;
     ++clock;
-    for (int32_t b : copied) {
-      entry[b].released = clock;
-      idle.insert(idle_key(b));
-    }
+    for (int32_t b : copied) retire(b);
     copied.clear();
   }
 };

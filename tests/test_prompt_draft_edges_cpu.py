@@ -1,6 +1,9 @@
 """Edges of the block manager's cut on the CPU (batches of appends after cuts and commits), and refusals
 before a launch."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -159,3 +162,67 @@ def test_extend_refuses_caps_beyond_what_fp32_can_hold():
                        (float("inf"), 0.1), (1.0, float("inf"))):
         for R in (0, 4):
             assert call(cap, scale, R) == pk.PK_ERR_INVALID_ARG, (cap, scale)
+
+
+NO_MEMORY = r"""
+// The block manager where allocations fail on request: no exception leaves an entry point, and
+// what a call that needs no memory of its own does is done.
+#include <cstdio>
+#include <cstdlib>
+#include <new>
+#include "block_manager.cpp"
+
+static long left = -1;  // allocations that succeed; -1: all
+static long refused = 0;
+void *operator new(std::size_t n) {
+  if (left == 0) { ++refused; throw std::bad_alloc(); }
+  if (left > 0) --left;
+  if (void *p = std::malloc(n)) return p;
+  throw std::bad_alloc();
+}
+void *operator new(std::size_t n, const std::nothrow_t &) noexcept { return std::malloc(n); }
+void operator delete(void *p) noexcept { std::free(p); }
+void operator delete(void *p, std::size_t) noexcept { std::free(p); }
+
+#define CHECK(x) do { if (!(x)) { std::printf("line %d: %s\n", __LINE__, #x); return 1; } } while (0)
+
+int main() {
+  pk_bm *bm;
+  int64_t slots[64], pairs[8];
+  int32_t n, tokens[64];
+  for (int i = 0; i < 64; ++i) tokens[i] = i;
+  for (long allow = 0; allow < 4; ++allow) {
+    CHECK(pk_bm_create(16, 4, nullptr, &bm) == PK_OK);
+    CHECK(pk_bm_add_seq(bm, 1) == PK_OK && pk_bm_append_slots(bm, 1, 24, slots, pairs, &n) == PK_OK);
+    CHECK(pk_bm_commit(bm, 1, tokens, 24) == PK_OK);
+    left = allow;
+    CHECK(pk_bm_truncate(bm, 1, 6) == PK_OK);             // four cached blocks without a table
+    const pk_status st = pk_bm_append_slots(bm, 1, 1, slots, pairs, &n);  // a copied tail
+    CHECK(st == PK_OK && n == 1);
+    left = -1;
+    CHECK(refused > 0 && pk_bm_check_invariants(bm) == PK_OK && pk_bm_num_free(bm) == 14);
+    left = 0;
+    CHECK(pk_bm_free_seq(bm, 1) == PK_OK);
+    left = -1;
+    CHECK(pk_bm_check_invariants(bm) == PK_OK && pk_bm_num_free(bm) == 16);
+    pk_bm_destroy(bm);
+    refused = 0;
+  }
+  std::puts("ok");
+  return 0;
+}
+"""
+
+
+def test_cuts_and_copies_without_memory_for_the_cache(tmp_path):
+    """A block that no table names any more and for which the cache has no memory leaves the cache instead."""
+    cxx = shutil.which("g++")
+    if not cxx:
+        pytest.skip("no g++")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    (tmp_path / "main.cpp").write_text(NO_MEMORY)
+    exe = str(tmp_path / "main")
+    subprocess.run([cxx, "-std=c++17", "-O1", "-w", "-I", os.path.join(root, "include"), "-I",
+                    os.path.join(root, "paged_kv_cache_113_gb300", "csrc"), str(tmp_path / "main.cpp"), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and r.stdout == "ok\n", (r.returncode, r.stdout, r.stderr)
