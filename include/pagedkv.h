@@ -507,7 +507,8 @@ pk_status pk_paged_attention_decode_e4m3(
  * reaches its element.
  * Precision: of an fp32 pool, factors of 24 bits and fp32 sums; of a bf16 pool,
  * weights of 16 bits, and sums that the tensor cores cut off toward zero, up to
- * some 10^-4 after 32 768 tokens of one partition (results round to 2^-9).
+ * some 10^-4 after 32 768 tokens of one partition (results round to 2^-9). Scores of a
+ * bf16 pool whose magnitude passes 2^30 may make a row NaN.
  *   out, q        [num_q_tokens, Hq, d], dtype of the pool; sequence s's rows
  *                 are q_offsets[s] .. q_offsets[s + 1] - 1, and rows of no
  *                 sequence are neither read nor written.

@@ -88,7 +88,7 @@ constexpr float kTiny0 = 0.9999939203262329f, kTiny1 = -0.3326335847377777f, kTi
 // some reach the cap go through tanh2, whose 2^-21 of the cap is 2^-14 of the exponent at most.
 // kWide, any cap: products are scaled first, and such scores go through tanh2_relative, as 2^-21
 // of a large cap would be more than the scores far below it (0.7 at 10^6). A prompt of 16 384 tokens
-// (32 / 8 heads of 128): 1700 us near and 1890 wide, and where scores reach the cap 2740 and 3500.
+// (32 / 8 heads of 128): 1690 us near and 1800 wide, and where scores reach the cap 2740 and 3500.
 enum class Cap { kNone, kNear, kWide };
 constexpr float kNearFrom = 6.103515625e-5f, kNearTo = 16384.0f;  // scale / cap
 constexpr float kNearCap = 128.0f;                                // cap log2(e)
@@ -616,11 +616,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
           }
           const bool move = mx > ref + kPromptSlack;
-          if (__any_sync(0xffffffffu, move)) {
+          if (__any_sync(0xffffffffu, move || (EXACT && exact))) {
             const float f = move ? exp2_ftz(ref - mx) : 1.0f;
             if (move) ref = mx;
-            if (EXACT) exact = exact || __any_sync(0xffffffffu, tid < rows && move && fabsf(mx) > kPromptExact);
             l *= f;
+            if (EXACT) exact = exact || __any_sync(0xffffffffu, tid < rows && move && fabsf(mx) > kPromptExact);
+            if (EXACT && exact && !poly) {
+              // The weights' multiply-add takes the reference, a rounded product, from exact ones: of scores
+              // of 2^31 the difference of a score from itself would be some 2^7 and its weight infinite.
+#pragma unroll
+              for (int i = 0; i < 64; ++i) set_pair(i, mul2(pair(i), pack2(sl_now, sl_now)));
+              sl_now = 1.0f;
+            }
             if (j > 0) {  // these scores came after the products of the tile before
               const uint64_t f2 = pack2(f, f);
 #pragma unroll 1
@@ -638,13 +645,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 tmem_store32(t_o(h) + lane_base + 32 * ch, o);
               }
             }
-          }
-          if (EXACT && !poly && __builtin_expect(exact, 0)) {
-            // The weights' multiply-add takes the reference, a rounded product, from exact ones: of scores
-            // of 2^31 the difference of a score from itself would be some 2^7 and its weight infinite.
-#pragma unroll
-            for (int i = 0; i < 64; ++i) set_pair(i, mul2(pair(i), pack2(sl_now, sl_now)));
-            sl_now = 1.0f;
           }
           const float m = ref == -INFINITY ? 0.0f : ref;  // nothing seen so far: every weight is 0
           const uint64_t sl2 = pack2(sl_now, sl_now), m2 = pack2(-m, -m);
