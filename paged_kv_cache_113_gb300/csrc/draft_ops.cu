@@ -45,7 +45,7 @@ __device__ __forceinline__ float weight(float x) { return x > 0.0f && x <= 3.402
 // 2^-34 of their sum in bad cases. So a thread sums 64 values at a time and adds those sums, in
 // order each time: 2^-44 at worst, 2^-47 as a rule. Sums, products and comparisons go this way
 // because of 64-bit operations this chip does two a clock and SM (with those, and sums in one
-// pass over each thread's part, 256 chains of 8 drafts took 59 us; now 29).
+// pass over each thread's part, 256 chains of 8 drafts took 59 us; now 30).
 struct Pair {
   float hi = 0.0f, lo = 0.0f;
   __device__ __forceinline__ void add(float x, float err) {
@@ -136,11 +136,12 @@ struct Weights {
 // totals go round, and the CTA that the drawn number falls into finds the token: which
 // warp's part, which of sixteen parts of that, and there 128 elements at a time. Only that
 // row (and with q the refused draft's) is read whole: a vocabulary of V values a sequence,
-// two with q, which memory bounds once there are enough of them.
+// two with q.
 //
 // Measured: 256 chains of 8 drafts, 2 x 32 000 fp32 values each (66 MB, 9.7 us at the rate of a
-// copy) 29 us; 64 trees of 16, 128 000 values (33 MB) 29 us; 4 x 4 drafts 12 us, of which the
-// three reads that the walk waits for, one after the other, are the most.
+// copy) 30 us; 64 trees of 16, 128 000 values (33 MB) 30 us; 4 x 4 drafts 13 us, of which the
+// three reads that the walk waits for, one after the other, are the most. Beyond those an
+// element's eight operations and the two passes behind the first bound it, not memory (23% busy).
 template <typename T>
 __global__ void __launch_bounds__(kVerifyThreads, 2) verify_drafts_kernel(VerifyParams a) {
   constexpr int NT = kVerifyThreads, NW = NT / 32;

@@ -10,9 +10,9 @@
 // copies.
 //
 // Measured (heads of 128, blocks of 16): 8 sequences of 32 768 tokens, 64 / 8 heads, biased, 160 to
-// 164 us, 6.6 TB/s (98% of a copy; 200 on attn_split_kernel); 64 of 1000 to 4000 tokens of which
-// the last 1024 are seen, 32 / 32 heads, 163 to 167 us, 6.5 TB/s (180); 256 of some 500 tokens,
-// 32 / 8 heads, capped, 84 to 87 us, 5.8 TB/s (106): there the launch's first loads and uneven ends.
+// 162 us, 6.6 TB/s (98% of a copy; 200 on attn_split_kernel); 64 of 1000 to 4000 tokens of which
+// the last 1024 are seen, 32 / 32 heads, 163 to 168 us, 6.5 TB/s (180); 256 of some 500 tokens,
+// 32 / 8 heads, capped, 84 to 88 us, 5.8 TB/s (106): there the launch's first loads and uneven ends.
 #pragma once
 
 #include "attn_extend.cuh"

@@ -17,8 +17,8 @@
 // Only tiles that some row does not see as a whole are masked.
 //
 // Measured (32 / 8 heads of 128): one prompt of 16 384 tokens 1.42 ms, 1.55 PFLOP/s of the
-// formula's work (scores capped 1.64 ms, biased 1.91; heads of 64 1.06); eight of 2000 258 us;
-// the last 512 tokens of two contexts of 32 768, 64 / 8 heads, capped, 950 us, 1.15 PFLOP/s.
+// formula's work (scores capped 1.70 ms, biased 1.91; heads of 64 1.05); eight of 2000 261 us;
+// the last 512 tokens of two contexts of 32 768, 64 / 8 heads, capped, 953 us, 1.14 PFLOP/s.
 // What bounds it now: long, a tile's chain in a half (1370 cycles of softmax, 1140 of products,
 // 680 of waits between them) with two halves to overlap it: a tile takes 3200 cycles, 2050 of
 // them products; capped, the softmax's operations; short, a unit's beginning and end, some
@@ -88,7 +88,7 @@ constexpr float kTiny0 = 0.9999939203262329f, kTiny1 = -0.3326335847377777f, kTi
 // some reach the cap go through tanh2, whose 2^-21 of the cap is 2^-14 of the exponent at most.
 // kWide, any cap: products are scaled first, and such scores go through tanh2_relative, as 2^-21
 // of a large cap would be more than the scores far below it (0.7 at 10^6). A prompt of 16 384 tokens
-// (32 / 8 heads of 128): 1690 us near and 1800 wide, and where scores reach the cap 2740 and 3500.
+// (32 / 8 heads of 128): 1700 us near and 1800 wide, and where scores reach the cap 2740 and 3570.
 enum class Cap { kNone, kNear, kWide };
 constexpr float kNearFrom = 6.103515625e-5f, kNearTo = 16384.0f;  // scale / cap
 constexpr float kNearCap = 128.0f;                                // cap log2(e)
