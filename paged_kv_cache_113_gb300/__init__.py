@@ -869,7 +869,7 @@ def pk_paged_attention_extend(out, q, k_cache, v_cache, block_tables, context_le
     """Attention of each sequence's new tokens over its paged context (see the
     header): rows ``q_offsets[s] .. q_offsets[s + 1]`` (int32 ``[S + 1]``; None: one
     row each) of ``q`` and ``out`` ``[rows, Hq, d]`` are the last tokens of its
-    ``context_lens[s]``. Scores are capped by ``softcap``, biased by ``slopes`` (fp32
+    ``context_lens[s]``. Scores are capped by ``softcap`` (0, or within 2^-100 .. 2^100), biased by ``slopes`` (fp32
     ``[Hq]``) times the distance, and limited by ``window``, ``prefix_lens`` (int32
     ``[S]``, seen by every row) and ``first_tokens`` (int32 ``[rows]``, the first
     token that a row sees). ``partition_size`` and ``work_items`` from
@@ -1037,7 +1037,8 @@ class BlockManager:
         _check(self._L.pk_bm_add_seq(self._h, int(seq)), "pk_bm_add_seq")
 
     def append(self, seq: int, n: int):
-        """Appends n tokens; returns (slots int64[n], (src, dst) CoW pair or None)."""
+        """Appends n tokens; returns (slots int64[n], (src, dst) CoW pair or None). The pairs of
+        several calls are copied call by call, in the calls' order."""
         slots = np.empty(max(int(n), 1), np.int64)
         pair = np.zeros(2, np.int64)
         ncow = ctypes.c_int32(0)
@@ -1046,7 +1047,8 @@ class BlockManager:
         return slots[: int(n)], ((int(pair[0]), int(pair[1])) if ncow.value else None)
 
     def append_batch(self, seqs: Sequence[int]):
-        """One token for each sequence in order; returns (slots [n], pairs [k, 2])."""
+        """One token for each sequence in order; returns (slots [n], pairs [k, 2]), the pairs to be
+        copied at once."""
         ids = np.ascontiguousarray(seqs, dtype=np.int64)
         n = len(ids)
         slots = np.empty(max(n, 1), np.int64)
